@@ -86,8 +86,11 @@ typedef enum {
     IQ4XS_ERR_DEVICE = 4,  /* no CUDA device, or the current device is not sm_103 */
     IQ4XS_ERR_CUDA = 5,    /* a CUDA runtime/driver call or a launch failed */
     IQ4XS_ERR_TIMEOUT = 6, /* a bounded device wait ran out (iq4xs_last_device_error) */
-    IQ4XS_ERR_BOUNDS = 7   /* bounds-checked build only: a checked device access
+    IQ4XS_ERR_BOUNDS = 7,  /* bounds-checked build only: a checked device access
                               missed its buffer (iq4xs_last_device_error) */
+    IQ4XS_ERR_DATA = 8     /* a value that a kernel read from device memory (a page
+                              id, length, offset, position, path) was out of
+                              range and was skipped (iq4xs_last_device_error) */
 } iq4xs_status;
 
 typedef enum {
@@ -538,6 +541,184 @@ int iq4xs_set_mma_launch_table(const int64_t* entries, int count);
  * 512 == 0 and the sizes are in range; IQ4XS_ERR_ARG for null outputs.
  */
 int iq4xs_mma_launch_config(int64_t M, int64_t N, int64_t K, int* rows_per_cta, int* k_splits, int* ctas_per_sm);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The attention side of a decode or verify step: a paged key/value cache, the
+ * operator that fills it from the projections, the attention that reads it,
+ * and the operations on its pages.
+ *
+ * Cache.  Element i of (layer, page, head, slot) of K or V is at
+ *   layer*layer_stride + page*page_stride + head*head_stride + slot*slot_stride + i
+ * (strides in elements, any order of the four axes that does not overlap; i
+ * is contiguous).  K and V share the geometry.  k, v 16-byte aligned, every
+ * stride a multiple of 8; page_size a power of two, 16..256; head_dim 64, 128
+ * or 256; at most 2^31 - 1 pages.
+ *
+ * Batch.  Sequence s holds lens[s] cached tokens (positions 0..lens[s]-1) and
+ * owns rows [row_offsets[s], row_offsets[s+1]) of the step's new tokens, which
+ * take the positions behind them: row row_offsets[s] + t has position
+ * lens[s] + t.  Position p lies in slot p % page_size of page
+ * page_table[s*table_stride + p / page_size]; the first held[s] entries of a
+ * table row are valid, the others are not read (a table row is at most 2^20
+ * entries wide).  All four arrays are device
+ * memory, read when the kernels run (so that a captured graph follows them).
+ * A value out of range is recorded in the device error word (code 0x300 + what;
+ * status IQ4XS_ERR_DATA) and what it addresses is skipped: no access leaves
+ * the buffers.
+ *
+ * A page is free when refs[page] == 0; an allocation takes the free pages of
+ * lowest index, sequence after sequence, so that every result is the same
+ * from run to run.
+ */
+typedef enum { IQ4XS_KV_F16 = 0, IQ4XS_KV_BF16 = 1 } iq4xs_kv_dtype;
+
+typedef struct {
+    void* k;
+    void* v;
+    int64_t dtype; /* iq4xs_kv_dtype */
+    int64_t layers, pages, heads, page_size, head_dim;
+    int64_t layer_stride, page_stride, head_stride, slot_stride;
+} iq4xs_kv_cache;
+
+typedef struct {
+    int64_t sequences;          /* 0..65535 */
+    const int32_t* row_offsets; /* [sequences + 1], non-decreasing */
+    int32_t* lens;              /* [sequences] */
+    int32_t* held;              /* [sequences] */
+    int32_t* page_table;        /* [sequences][table_stride] */
+    int64_t table_width, table_stride;
+} iq4xs_kv_batch;
+
+/*
+ * From the projections' fp32 output to attention's input, one launch: per
+ * head RMS norm of q and k, rotation of the first rot_dim channels, rounding
+ * to the cache's type; q goes to q_out, k and v into the cache at their
+ * rows' positions.
+ *   y_i = x_i / sqrt(mean(x^2) + eps) * weight_i; a pair (a, b) of channels
+ *   (i, i + rot_dim/2), or (2i, 2i + 1) with `interleaved`, becomes
+ *   (a cos - b sin, a sin + b cos), (cos, sin) = rope[positions[row]][i].
+ * Norm and rotation are computed in fp32 and rounded once.  v is rounded only.
+ *   q, k, v     fp32 [rows][heads][head_dim], rows and heads at the given
+ *               strides (elements, multiples of 4), 16-byte aligned: the
+ *               column blocks of one fused projection will do.
+ *   q_weight, k_weight  fp32 [head_dim], 16-byte aligned; NULL: no norm.
+ *   rope        fp32 [rope_positions][rot_dim/2][2], 16-byte aligned; NULL
+ *               (with rot_dim 0): no rotation.  rot_dim a multiple of 8, at
+ *               most head_dim.
+ *   positions   int32 [rows], or NULL: lens[s] + t (a drafted tree's tokens
+ *               of one depth share a position, not a cache slot).
+ *   q_out       [rows][q_heads][head_dim] in the cache's type, rows
+ *               q_out_row_stride elements apart (a multiple of 8), 16-byte
+ *               aligned.
+ * Rows outside [row_offsets[0], row_offsets[sequences]) are left alone.
+ * 1 <= rows <= 32768.
+ */
+typedef struct {
+    const float* q;
+    const float* k;
+    const float* v;
+    int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+    const float* q_weight;
+    const float* k_weight;
+    double eps;
+    const float* rope;
+    int64_t rope_positions, rot_dim, interleaved;
+    const int32_t* positions;
+    void* q_out;
+    int64_t q_out_row_stride;
+    int64_t rows, q_heads, layer;
+} iq4xs_qk_norm_rope_args;
+int iq4xs_qk_norm_rope(const iq4xs_qk_norm_rope_args* args, const iq4xs_kv_cache* cache,
+                       const iq4xs_kv_batch* batch, int64_t stream);
+
+/*
+ * Attention of every sequence's new tokens over its cache (whose last
+ * positions hold the new tokens' own K and V): row t of sequence s sees
+ * positions 0..lens[s]-1 and, of the new ones lens[s] + j, those with bit j
+ * of its mask row set -- or j <= t when tree_mask is NULL (a chain, a prompt
+ * chunk, a single token).
+ *   out[row][h] = sum_p w_p v_p / sum_p w_p, w_p = exp(scale * q[row][h].k_p),
+ * query head h reading key/value head h / (q_heads / heads).  A row that sees
+ * nothing gets zeros.  A position that a row does not see has no influence on
+ * it, whatever its K and V hold (NaN and infinities included); slots behind a
+ * sequence's end are never used.
+ *   q          [rows][q_heads][head_dim] in the cache's type, rows
+ *              q_row_stride elements apart (a multiple of 8), 16-byte aligned.
+ *   out        fp32 [rows][out_row_stride >= q_heads*head_dim], 16-byte
+ *              aligned, out_row_stride a multiple of 4: what iq4xs_linear
+ *              takes.  Rows of no sequence are not written.
+ *   tree_mask  uint64 [rows][mask_words], or NULL; a new token j >=
+ *              64*mask_words is seen by no row.
+ *   workspace  iq4xs_tree_attention_workspace_bytes(...) bytes, 16-byte
+ *              aligned, of any content; one per stream.
+ * Scores and softmax statistics are fp32 and weights keep at least 16
+ * significant bits; results are the same from run to run.
+ * 1 <= rows <= 32768; q_heads a multiple of the cache's heads.
+ */
+typedef struct {
+    const void* q;
+    int64_t q_row_stride;
+    float* out;
+    int64_t out_row_stride;
+    int64_t rows, q_heads, layer;
+    double scale;
+    const uint64_t* tree_mask;
+    int64_t mask_words;
+    void* workspace;
+    int64_t workspace_bytes;
+} iq4xs_tree_attention_args;
+int iq4xs_tree_attention(const iq4xs_tree_attention_args* args, const iq4xs_kv_cache* cache,
+                         const iq4xs_kv_batch* batch, int64_t stream);
+
+/* Workspace bytes of iq4xs_tree_attention for a batch of up to `rows` rows
+ * and `sequences` sequences; 0 if invalid (needs a GPU: it depends on the SMs). */
+int64_t iq4xs_tree_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                             int64_t sequences);
+
+/*
+ * Pages for the new tokens of a step: every sequence gets the pages it lacks
+ * for lens[s] + (row_offsets[s+1] - row_offsets[s]) tokens (table and held
+ * grow, refs become 1).  status[s] = 0, or 1 where the free pages (taken in
+ * order of sequences) or the table's width do not suffice: that sequence gets
+ * none.
+ *   refs  int32 [pages], 16-byte aligned; status  int32 [sequences].
+ */
+int iq4xs_cache_reserve(const iq4xs_kv_batch* batch, int64_t page_size, int32_t* refs, int64_t pages,
+                        int32_t* status, int64_t stream);
+
+/*
+ * After verification: sequence s keeps the new tokens paths[s][0..accepted[s])
+ * (indices among its new tokens, strictly rising).  Their K and V move, in
+ * every layer, to positions lens[s], lens[s]+1, ...; new_lens[s] = lens[s] +
+ * accepted[s]; pages behind the new end are dropped (held shrinks, refs fall).
+ *   paths  int32 [sequences][path_width]; accepted  int32 [sequences],
+ *   0..path_width; new_lens  int32 [sequences], may be lens itself.
+ */
+int iq4xs_cache_commit(const iq4xs_kv_cache* cache, const iq4xs_kv_batch* batch, int32_t* refs,
+                       const int32_t* paths, int64_t path_width, const int32_t* accepted, int32_t* new_lens,
+                       int64_t stream);
+
+/*
+ * Sequence children[i] becomes a copy of parents[i]: it shares the full pages
+ * (refs grow) and gets a page of its own with a copy of the last, partly
+ * filled one in every layer; lens and held are set.  Children are distinct,
+ * hold nothing and are not parents in the same call.  status[i] = 0; 1 where
+ * the free pages (taken in order) do not suffice, 2 where an index or a held
+ * count is out of order: that child stays empty.
+ */
+int iq4xs_cache_fork(const iq4xs_kv_cache* cache, const iq4xs_kv_batch* batch, int32_t* refs,
+                     const int32_t* parents, const int32_t* children, int64_t count, int32_t* status,
+                     int64_t stream);
+
+/* Sequences rows[0..count) end: their pages' refs fall, lens and held become 0. */
+int iq4xs_cache_release(const iq4xs_kv_batch* batch, int32_t* refs, int64_t pages, const int32_t* rows,
+                        int64_t count, int64_t stream);
+
+/* Pages dst[i] become copies of pages src[i] in every layer (device int32
+ * [count]); no dst is another's src or dst. */
+int iq4xs_cache_copy_pages(const iq4xs_kv_cache* cache, const int32_t* src, const int32_t* dst, int64_t count,
+                           int64_t stream);
 
 /* Static string for a status code. */
 const char* iq4xs_status_string(int status);

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 
 import torch
@@ -19,10 +20,12 @@ LIB_PATH = os.path.join(_HERE, "libiq4xs.so")
 BOUNDS_LIB_PATH = os.path.join(_HERE, "libiq4xs_bounds.so")  # the bounds-checked debug build
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "iq4xs.h")
 
-OK, ERR_ARG, ERR_ALIGN, ERR_SHAPE, ERR_DEVICE, ERR_CUDA, ERR_TIMEOUT, ERR_BOUNDS = range(8)
+OK, ERR_ARG, ERR_ALIGN, ERR_SHAPE, ERR_DEVICE, ERR_CUDA, ERR_TIMEOUT, ERR_BOUNDS, ERR_DATA = range(9)
 PATH_AUTO, PATH_DP4A, PATH_TC, PATH_BASELINE, PATH_MMA = 0, 1, 2, 3, 4
 PATHS = {"auto": PATH_AUTO, "dp4a": PATH_DP4A, "tc": PATH_TC, "mma": PATH_MMA}
 WTYPE_IQ4_XS, WTYPE_Q4_0, WTYPE_IQ4_NL = 0, 1, 2
+KV_F16, KV_BF16 = 0, 1
+KV_DTYPES = {torch.float16: KV_F16, torch.bfloat16: KV_BF16}
 WTYPES = {"iq4_xs": WTYPE_IQ4_XS, "q4_0": WTYPE_Q4_0, "iq4_nl": WTYPE_IQ4_NL}
 
 _lock = threading.Lock()
@@ -94,6 +97,17 @@ def load(path: str | None = None):
                                                 ctypes.POINTER(ci)]
         lib.iq4xs_set_mma_launch_table.argtypes = [ctypes.POINTER(i64), ci]
         lib.iq4xs_test_bounds_margin.argtypes = [i64]
+        # The attention side takes its argument structs as packed bytes.
+        cp = ctypes.c_char_p
+        lib.iq4xs_qk_norm_rope.argtypes = [cp, cp, cp, i64]
+        lib.iq4xs_tree_attention.argtypes = [cp, cp, cp, i64]
+        lib.iq4xs_tree_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+        lib.iq4xs_tree_attention_workspace_bytes.restype = i64
+        lib.iq4xs_cache_reserve.argtypes = [cp, i64, i64, i64, i64, i64]
+        lib.iq4xs_cache_commit.argtypes = [cp, cp, i64, i64, i64, i64, i64, i64]
+        lib.iq4xs_cache_fork.argtypes = [cp, cp, i64, i64, i64, i64, i64, i64]
+        lib.iq4xs_cache_release.argtypes = [cp, i64, i64, i64, i64, i64]
+        lib.iq4xs_cache_copy_pages.argtypes = [cp, i64, i64, i64, i64]
         lib.iq4xs_status_string.argtypes = [ci]
         lib.iq4xs_status_string.restype = ctypes.c_char_p
         for name in ("iq4xs_quantize_q8_1", "iq4xs_matmul", "iq4xs_matmul_grouped", "iq4xs_matmul_grouped_path",
@@ -106,7 +120,9 @@ def load(path: str | None = None):
                      "iq4xs_test_mma_config",
                      "iq4xs_quantize_q8_1_tc", "iq4xs_matmul_tc_operand",
                      "iq4xs_last_device_error", "iq4xs_bounds_checked", "iq4xs_test_bounds_margin",
-                     "iq4xs_mma_launch_config", "iq4xs_set_mma_launch_table"):
+                     "iq4xs_mma_launch_config", "iq4xs_set_mma_launch_table",
+                     "iq4xs_qk_norm_rope", "iq4xs_tree_attention", "iq4xs_cache_reserve", "iq4xs_cache_commit",
+                     "iq4xs_cache_fork", "iq4xs_cache_release", "iq4xs_cache_copy_pages"):
             getattr(lib, name).restype = ci
         if path is None:
             _lib = lib
@@ -372,12 +388,12 @@ def iq4xs_set_pdl(enable: bool) -> None:
 
 
 def iq4xs_last_device_error() -> int:
-    """The device error word (0 = clean), read and cleared; a timeout or
-    bounds code (status IQ4XS_ERR_TIMEOUT / IQ4XS_ERR_BOUNDS) is returned,
-    not raised."""
+    """The device error word (0 = clean), read and cleared; a timeout, bounds
+    or data code (status IQ4XS_ERR_TIMEOUT / IQ4XS_ERR_BOUNDS /
+    IQ4XS_ERR_DATA) is returned, not raised."""
     out = ctypes.c_int(-1)
     rc = load().iq4xs_last_device_error(ctypes.byref(out))
-    if rc not in (ERR_TIMEOUT, ERR_BOUNDS):
+    if rc not in (ERR_TIMEOUT, ERR_BOUNDS, ERR_DATA):
         _check("iq4xs_last_device_error", rc)
     return out.value
 
@@ -398,6 +414,208 @@ def iq4xs_test_skip_w_stage(stage: int) -> None:
 
 def iq4xs_status_string(status: int) -> str:
     return load().iq4xs_status_string(status).decode()
+
+
+# --------------------------------------------------------------------------
+# The attention side: the paged cache, its batch, and the calls on them.
+# --------------------------------------------------------------------------
+def _need(ok, fn: str, what: str, err=ValueError):
+    if not ok:
+        raise err(f"{fn}: {what}")
+
+
+def _need_i32(fn: str, **tensors):
+    for name, t in tensors.items():
+        _need(t.dtype == torch.int32, fn, f"{name} must be int32", TypeError)
+        _need(t.is_contiguous(), fn, f"{name} must be contiguous")
+
+
+class KVCache:
+    """A paged key/value cache over two tensors of the caller's:
+    k, v [layers, pages, heads, page_size, head_dim], float16 or bfloat16,
+    head_dim contiguous, the other axes at any strides (multiples of 8) that
+    both share: a [..., page_size, heads, head_dim] buffer does, transposed."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        _need(k.dtype in KV_DTYPES, "KVCache", "k must be float16 or bfloat16", TypeError)
+        _need(v.dtype == k.dtype, "KVCache", "v must have k's type", TypeError)
+        _need(k.dim() == 5 and v.shape == k.shape, "KVCache",
+              "k and v are [layers, pages, heads, page_size, head_dim]")
+        _need(v.stride() == k.stride() and k.stride(4) == 1, "KVCache", "k and v share their strides, the last is 1")
+        self.k, self.v, self.dtype = k, v, k.dtype
+        self.layers, self.pages, self.heads, self.page_size, self.head_dim = k.shape
+        self.desc = struct.pack("<12q", k.data_ptr(), v.data_ptr(), KV_DTYPES[k.dtype], *k.shape, *k.stride()[:4])
+
+
+def alloc_kv_cache(layers: int, pages: int, page_size: int, heads: int, head_dim: int, dtype=torch.float16,
+                   device="cuda") -> KVCache:
+    """A KVCache over fresh tensors (contents undefined: nothing behind a sequence's end is used)."""
+    shape = (layers, pages, heads, page_size, head_dim)
+    return KVCache(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
+
+
+class KVBatch:
+    """The sequences of a step, as int32 device tensors of the caller's:
+    row_offsets [B + 1] (sequence s owns the new rows row_offsets[s] ..
+    row_offsets[s+1] - 1), lens [B] cached tokens, held [B] pages held,
+    page_table [B, width] (rows at any stride).  The kernels read and update
+    the tensors in place."""
+
+    def __init__(self, row_offsets: torch.Tensor, lens: torch.Tensor, held: torch.Tensor, page_table: torch.Tensor):
+        _need_i32("KVBatch", row_offsets=row_offsets, lens=lens, held=held)
+        _need(page_table.dtype == torch.int32, "KVBatch", "page_table must be int32", TypeError)
+        b = lens.numel()
+        _need(row_offsets.numel() == b + 1 and held.numel() == b and page_table.dim() == 2 and
+              page_table.shape[0] == b and page_table.stride(1) == 1, "KVBatch",
+              "row_offsets [B + 1], lens [B], held [B], page_table [B, width]")
+        self.row_offsets, self.lens, self.held, self.page_table = row_offsets, lens, held, page_table
+        self.sequences = b
+        width = page_table.shape[1]
+        stride = page_table.stride(0) if b > 1 else width
+        self.desc = struct.pack("<7q", b, row_offsets.data_ptr(), lens.data_ptr(), held.data_ptr(),
+                                page_table.data_ptr(), width, stride)
+
+
+_QK_ARGS = struct.Struct("<11qd10q").pack
+_ATTN_ARGS = struct.Struct("<7qd4q").pack
+assert struct.calcsize("<11qd10q") == 22 * 8 and struct.calcsize("<7qd4q") == 12 * 8
+
+
+def _addr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def iq4xs_qk_norm_rope(q, k, v, q_weight, k_weight, eps: float, rope, positions, q_out, cache: KVCache, layer: int,
+                       batch: KVBatch, interleaved: bool = False, stream=None) -> None:
+    """The projections' fp32 q [M, Hq, D], k, v [M, Hkv, D] (any row and head
+    strides) -> q_out [M, Hq, D] in the cache's type, and k, v into the
+    cache's layer at their rows' positions: RMS norm per head (weights fp32
+    [D], or None), rotation of the first rot channels by rope fp32 [P, rot/2,
+    2] = (cos, sin) at positions int32 [M] (None: the rows' own positions)."""
+    fn = "iq4xs_qk_norm_rope"
+    M, hq, D = q.shape
+    _need(q.dtype == torch.float32 and k.dtype == torch.float32 and v.dtype == torch.float32, fn,
+          "q, k and v must be float32", TypeError)
+    _need(q_out.dtype == cache.dtype, fn, "q_out must have the cache's type", TypeError)
+    _need(D == cache.head_dim and k.shape == (M, cache.heads, D) and v.shape == k.shape and q_out.shape == q.shape,
+          fn, "q [M, Hq, D], k and v [M, Hkv, D], q_out as q")
+    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), q_out.stride()
+    _need(qs[2] == 1 and ks[2] == 1 and vs[2] == 1 and os_[2] == 1 and (os_[1] == D or hq == 1), fn,
+          "channels must be contiguous (heads too in q_out)")
+    for w in (q_weight, k_weight):
+        _need(w is None or (w.dtype == torch.float32 and w.numel() == D and w.is_contiguous()), fn,
+              "weights are float32 [D]")
+    n_pos = rot = 0
+    if rope is not None:
+        _need(rope.dtype == torch.float32 and rope.dim() == 3 and rope.shape[2] == 2 and rope.is_contiguous(), fn,
+              "rope is float32 [positions, rot / 2, 2]")
+        n_pos, rot = rope.shape[0], 2 * rope.shape[1]
+    if positions is not None:
+        _need(positions.dtype == torch.int32 and positions.numel() == M and positions.is_contiguous(), fn,
+              "positions is int32 [M]")
+    args = _QK_ARGS(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
+                    _addr(q_weight), _addr(k_weight), eps, _addr(rope), n_pos, rot, 1 if interleaved else 0,
+                    _addr(positions), q_out.data_ptr(), os_[0] if M > 1 else hq * D, M, hq, layer)
+    rc = load().iq4xs_qk_norm_rope(args, cache.desc, batch.desc, _stream(stream))
+    if rc:
+        _check(fn, rc)
+
+
+def iq4xs_tree_attention_workspace_bytes(rows: int, q_heads: int, cache: KVCache, batch: KVBatch) -> int:
+    """Workspace of iq4xs_tree_attention for up to ``rows`` rows of the batch."""
+    return int(load().iq4xs_tree_attention_workspace_bytes(rows, q_heads, cache.heads, cache.head_dim,
+                                                           batch.sequences))
+
+
+def iq4xs_tree_attention(q, cache: KVCache, layer: int, batch: KVBatch, scale: float, out, workspace, tree_mask=None,
+                         stream=None) -> None:
+    """Attention of the batch's new rows q [M, Hq, D] (the cache's type) over
+    the cache's layer -> out fp32 [M, Hq * D].  tree_mask int64 [M, W]: bit j
+    of a row's words = it sees its sequence's new token j (None: tokens 0..t,
+    a chain).  workspace: uint8, iq4xs_tree_attention_workspace_bytes(...)."""
+    fn = "iq4xs_tree_attention"
+    M, hq, D = q.shape
+    _need(q.dtype == cache.dtype, fn, "q must have the cache's type", TypeError)
+    _need(out.dtype == torch.float32, fn, "out must be float32", TypeError)
+    qs, os_ = q.stride(), out.stride()
+    _need(D == cache.head_dim and qs[2] == 1 and (qs[1] == D or hq == 1), fn,
+          "q is [M, Hq, D], heads and channels contiguous")
+    _need(out.shape == (M, hq * D) and os_[1] == 1, fn, "out is [M, Hq * D]")
+    words = 0
+    if tree_mask is not None:
+        _need(tree_mask.dtype in (torch.int64, torch.uint64), fn, "tree_mask must be int64", TypeError)
+        _need(tree_mask.dim() == 2 and tree_mask.shape[0] == M and tree_mask.is_contiguous(), fn,
+              "tree_mask is [M, words]")
+        words = tree_mask.shape[1]
+    args = _ATTN_ARGS(q.data_ptr(), qs[0] if M > 1 else hq * D, out.data_ptr(), os_[0] if M > 1 else hq * D, M, hq,
+                      layer, scale, _addr(tree_mask), words, workspace.data_ptr(),
+                      workspace.numel() * workspace.element_size())
+    rc = load().iq4xs_tree_attention(args, cache.desc, batch.desc, _stream(stream))
+    if rc:
+        _check(fn, rc)
+
+
+def iq4xs_cache_reserve(batch: KVBatch, page_size: int, refs, status, stream=None) -> None:
+    """Pages for the batch's new tokens, the lowest free ones (refs int32
+    [pages] == 0) in order of sequences; status int32 [B]: 1 = none given,
+    too few are free (or the table is too narrow)."""
+    fn = "iq4xs_cache_reserve"
+    _need_i32(fn, refs=refs, status=status)
+    _need(status.numel() == batch.sequences, fn, "status is int32 [B]")
+    rc = load().iq4xs_cache_reserve(batch.desc, page_size, refs.data_ptr(), refs.numel(), status.data_ptr(),
+                                    _stream(stream))
+    if rc:
+        _check(fn, rc)
+
+
+def iq4xs_cache_commit(cache: KVCache, batch: KVBatch, refs, paths, accepted, new_lens, stream=None) -> None:
+    """Keep the new tokens paths[s, :accepted[s]] (strictly rising) of every
+    sequence: their K and V move up behind the context in every layer,
+    new_lens[s] = lens[s] + accepted[s] (new_lens may be batch.lens), pages
+    behind the new end are dropped."""
+    fn = "iq4xs_cache_commit"
+    _need_i32(fn, refs=refs, paths=paths, accepted=accepted, new_lens=new_lens)
+    _need(refs.numel() == cache.pages, fn, "refs is int32 [pages]")
+    _need(paths.dim() == 2 and paths.shape[0] == batch.sequences and accepted.numel() == batch.sequences and
+          new_lens.numel() == batch.sequences, fn, "paths [B, width], accepted [B], new_lens [B]")
+    rc = load().iq4xs_cache_commit(cache.desc, batch.desc, refs.data_ptr(), paths.data_ptr(), paths.shape[1],
+                                   accepted.data_ptr(), new_lens.data_ptr(), _stream(stream))
+    if rc:
+        _check(fn, rc)
+
+
+def iq4xs_cache_fork(cache: KVCache, batch: KVBatch, refs, parents, children, status, stream=None) -> None:
+    """Sequences children[i] (empty, distinct) become copies of parents[i]:
+    full pages shared, the last partly filled one copied in every layer."""
+    fn = "iq4xs_cache_fork"
+    _need_i32(fn, refs=refs, parents=parents, children=children, status=status)
+    n = parents.numel()
+    _need(refs.numel() == cache.pages, fn, "refs is int32 [pages]")
+    _need(children.numel() == n and status.numel() == n, fn, "parents, children and status are of one length")
+    rc = load().iq4xs_cache_fork(cache.desc, batch.desc, refs.data_ptr(), parents.data_ptr(), children.data_ptr(), n,
+                                 status.data_ptr(), _stream(stream))
+    if rc:
+        _check(fn, rc)
+
+
+def iq4xs_cache_release(batch: KVBatch, refs, rows, stream=None) -> None:
+    """Sequences ``rows`` end: their pages' references fall, lens and held become 0."""
+    fn = "iq4xs_cache_release"
+    _need_i32(fn, refs=refs, rows=rows)
+    rc = load().iq4xs_cache_release(batch.desc, refs.data_ptr(), refs.numel(), rows.data_ptr(), rows.numel(),
+                                    _stream(stream))
+    if rc:
+        _check(fn, rc)
+
+
+def iq4xs_cache_copy_pages(cache: KVCache, src, dst, stream=None) -> None:
+    """Pages dst[i] become copies of pages src[i] in every layer."""
+    fn = "iq4xs_cache_copy_pages"
+    _need_i32(fn, src=src, dst=dst)
+    _need(src.numel() == dst.numel(), fn, "src and dst are of one length")
+    rc = load().iq4xs_cache_copy_pages(cache.desc, src.data_ptr(), dst.data_ptr(), src.numel(), _stream(stream))
+    if rc:
+        _check(fn, rc)
 
 
 # --------------------------------------------------------------------------

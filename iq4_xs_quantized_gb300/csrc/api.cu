@@ -158,6 +158,16 @@ int select_path_impl(int64_t M, int64_t N, int64_t K) {
 
 bool pdl_enabled() { return g_pdl.load() != 0; }
 
+int device_context(int** err, int* num_sms, void** encode) {
+    DevState* st;
+    const int rc = device_state(&st);
+    if (rc) return rc;
+    *err = st->err;
+    *num_sms = st->num_sms;
+    *encode = st->encode;
+    return IQ4XS_OK;
+}
+
 }  // namespace iq4xs
 
 using namespace iq4xs;
@@ -433,8 +443,9 @@ int iq4xs_last_device_error(int* code_out) {
         return IQ4XS_ERR_CUDA;
     const int c = *code_out;
     if (c >= kDevErrBounds && c < kDevErrBounds + 0x100) return IQ4XS_ERR_BOUNDS;
+    if (c >= kDevErrData && c < kDevErrData + 0x100) return IQ4XS_ERR_DATA;
     return ((c >= kDevErrTimeoutW && c <= kDevErrTimeoutX) || c == kDevErrTimeoutMmaStage ||
-            c == kDevErrTimeoutMmaSlot)
+            (c >= kDevErrTimeoutMmaSlot && c <= kDevErrTimeoutScore))
                ? IQ4XS_ERR_TIMEOUT
                : IQ4XS_OK;
 }
@@ -498,6 +509,7 @@ const char* iq4xs_status_string(int status) {
         case IQ4XS_ERR_CUDA: return "CUDA error";
         case IQ4XS_ERR_TIMEOUT: return "device wait timed out";
         case IQ4XS_ERR_BOUNDS: return "checked device access out of bounds";
+        case IQ4XS_ERR_DATA: return "value in device memory out of range";
         default: return "unknown status";
     }
 }

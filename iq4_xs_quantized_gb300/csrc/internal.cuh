@@ -210,7 +210,17 @@ enum DeviceError : int {
     kDevErrLayout = 0x10A,  // dynamic shared memory not 1024-byte aligned
     kDevErrTimeoutMmaStage = 0x10B,  // warp-MMA matmul: a stage (W and codes) never landed
     kDevErrTimeoutMmaSlot = 0x10C,   // warp-MMA matmul: a stage slot was never freed
+    kDevErrTimeoutKv = 0x10D,        // attention: a stage of keys or values never landed
+    kDevErrTimeoutKvSlot = 0x10E,    // attention: a stage slot was never freed
+    kDevErrTimeoutScore = 0x10F,     // attention: a score or output product never completed
     kDevErrBounds = 0x200,           // + BoundsSite: a checked access missed its buffer
+    kDevErrData = 0x300,             // + DataSite: a value read from device memory was out of range
+};
+
+// What was out of range among the values that the cache's kernels read from
+// device memory (every build checks them; the access they lead to is skipped).
+enum DataSite : int {
+    kDataOffsets = 1, kDataLens, kDataHeld, kDataPage, kDataPosition, kDataPath, kDataRow, kDataRefs,
 };
 
 // ---------------------------------------------------------------------------
@@ -237,6 +247,9 @@ enum BoundsSite : int {
     kBcMmaRows, kBcMmaSmem, kBcMmaSplit,
     kBcTcW = 0x40, kBcTcWAlign, kBcTcQ, kBcTcQAlign, kBcTcOp, kBcTcDs, kBcTcY, kBcTcSpan,
     kBcTcSmem, kBcTcRecv, kBcTcRows,
+    kBcAppX = 0x60, kBcAppW, kBcAppRope, kBcAppQ, kBcAppKv,
+    kBcPagesKv = 0x70, kBcPagesTable, kBcPagesRefs,
+    kBcAttnQ = 0x80, kBcAttnOut, kBcAttnMask, kBcAttnWork, kBcAttnKv, kBcAttnSmem,
 };
 #ifdef IQ4XS_BOUNDS_CHECK
 constexpr bool kBoundsCheck = true;
@@ -1026,6 +1039,9 @@ cudaError_t launch_matmul_dp4a_grouped(const void* w, int wt, int64_t expert_str
                                        int64_t ldy, int* err, cudaStream_t stream);
 // Programmatic dependent launch on (default) or off for every launch.
 bool pdl_enabled();
+// The current device's error word, SM count and tensor-map encoder after its
+// one-time set-up; an iq4xs_status.
+int device_context(int** err, int* num_sms, void** encode);
 // `encode` is the driver's cuTensorMapEncodeTiled; `err` the device error word.
 // Activations: the Q8_1 arrays (qs 16-byte aligned: its rows are staged by
 // TMA) when tc_operand is NULL, else the prepared operand alone (qs, ds
