@@ -158,6 +158,8 @@ int select_path_impl(int64_t M, int64_t N, int64_t K) {
 
 bool pdl_enabled() { return g_pdl.load() != 0; }
 
+int take_skip_stage() { return g_skip_w_stage.exchange(-1); }
+
 int device_context(int** err, int* num_sms, void** encode) {
     DevState* st;
     const int rc = device_state(&st);

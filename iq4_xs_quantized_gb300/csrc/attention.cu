@@ -1,26 +1,54 @@
-// attention.cu -- attention of new tokens over the paged cache under a tree
-// mask, in its simplest form: a CTA per (row, query head), a warp per key.
-//
-//   o = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale q.k_p - m)
-//
-// one pass with a running maximum m and sum; the warps' partial results are
-// joined at the end.
-#include "cache.cuh"
+// attention.cu -- tree attention over the paged cache: tensor maps, the
+// choice of the form, and the join of items that the split cut.
+#include "attention.cuh"
 
 namespace iq4xs {
 namespace {
 
-constexpr int kThreads = 128;
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-template <int D, class T>
-__global__ void __launch_bounds__(kThreads)
-    attention_kernel(const iq4xs_tree_attention_args a, const CacheView c, const BatchView b, int* err) {
-    constexpr int kPer = D / 32;  // channels of a lane, 2 adjacent ones 64 apart
-    __shared__ float part[kThreads / 32][D + 2];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int row = blockIdx.x, h = blockIdx.y, kvh = h / (int)(a.q_heads / c.heads);
+constexpr int kMmaRows = 16;         // row tile of the warp-level form
+constexpr int64_t kWholeTokens = 512;
+
+int mma_ctas(int64_t head_dim, int num_sms) { return head_dim == 256 ? num_sms : 2 * num_sms; }
+
+// One map over K or V of a layer: channels, then slot and head by rising
+// stride, then pages; boxes of 64 channels x the slots of a key tile in a page.
+bool encode_kv(EncodeTiledFn enc, uint16_t* base, const CacheView& c, bool bf16, int* slot_axis, CUtensorMap* map) {
+    const bool slot_first = c.slot_stride <= c.head_stride;
+    *slot_axis = slot_first ? 1 : 2;
+    const cuuint64_t slots = (cuuint64_t)c.page_size, heads = (cuuint64_t)c.heads;
+    const cuuint64_t slot_b = (cuuint64_t)c.slot_stride * 2, head_b = (cuuint64_t)c.head_stride * 2;
+    const cuuint64_t gdim[4] = {(cuuint64_t)c.head_dim, slot_first ? slots : heads, slot_first ? heads : slots,
+                                (cuuint64_t)c.pages};
+    const cuuint64_t gstride[3] = {slot_first ? slot_b : head_b, slot_first ? head_b : slot_b,
+                                   (cuuint64_t)c.page_stride * 2};
+    const cuuint32_t box_slots = (cuuint32_t)(c.page_size < kKeyTile ? c.page_size : kKeyTile);
+    const cuuint32_t box[4] = {64, slot_first ? box_slots : 1, slot_first ? 1 : box_slots, 1};
+    const cuuint32_t estride[4] = {1, 1, 1, 1};
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, gdim, gstride,
+               box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ------------------------------------------------------------------- join
+// A CTA per (row, query head) whose item was cut: the partial results of the
+// CTAs that share it, weighted by exp2(m_i - m), over the joined sum.  Warps
+// take every fourth part and add up in shared memory, in a fixed order.
+constexpr int kJoinWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    attention_join_kernel(const AttnParams p, const BatchView b, int row_tile, int* err) {
+    constexpr int kPer = D / 32;
+    __shared__ float acc_s[kJoinWarps][D];
+    // The attention kernel lets this grid start only behind its own wait for
+    // what came before, so lengths and offsets are final: only the partial
+    // results have to be waited for.
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x, head = blockIdx.y;
     int s = 0;
     for (int s0 = 0; s0 < b.sequences; s0 += 32) {
         const unsigned done =
@@ -28,91 +56,122 @@ __global__ void __launch_bounds__(kThreads)
         s += __popc(done);
         if (done != 0xffffffffu) break;
     }
-    if (s >= b.sequences || row < b.row_offsets[0]) return;
-    int first;
-    const int n = batch_rows(b, s, a.rows, &first, err), len = batch_len(b, s, err), t = row - first;
-    if (n == 0 || len < 0 || t < 0 || len > INT32_MAX - n) return;
+    bool cut = s < b.sequences && row >= b.row_offsets[0];
+    int first = 0, last = 0, r = 0;
+    if (cut) {
+        const SeqWork w = seq_work(p, b, s, row_tile, err);
+        const int64_t work = work_before(p, b, b.sequences, row_tile, err);
+        cut = w.work > 0 && row >= w.row0;
+        if (cut) {
+            const int ctas = working_ctas(p, work);
+            r = (row - w.row0) * p.group + head % p.group;
+            const int64_t x = work_before(p, b, s, row_tile, err) +
+                              ((int64_t)(head / p.group) * w.row_tiles + r / row_tile) * w.key_tiles;
+            r %= row_tile;
+            first = range_owner(work, ctas, x);
+            last = range_owner(work, ctas, x + w.key_tiles - 1);
+            cut = first != last;
+        }
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    if (!cut) return;
 
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + row * a.q_row_stride + (int64_t)h * D;
-    float qv[kPer], o[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; i += 2) {
-        const float2 f = T::unpack(*reinterpret_cast<const uint32_t*>(q + 32 * i + 2 * lane));
-        qv[i] = f.x * (float)a.scale;
-        qv[i + 1] = f.y * (float)a.scale;
-        o[i] = o[i + 1] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int p = w; p < len + n; p += kThreads / 32) {
-        const int j = p - len;
-        if (j >= 0) {
-            const bool seen = a.tree_mask == nullptr ? j <= t
-                              : j < 64 * a.mask_words && (a.tree_mask[row * a.mask_words + (j >> 6)] >> (j & 63) & 1);
-            if (!seen) continue;
-        }
-        const int page = page_of(c, b, s, p, err);
-        if (page < 0) continue;
-        const int64_t at = a.layer * c.layer_stride + page * c.page_stride + kvh * c.head_stride +
-                           (p & (c.page_size - 1)) * c.slot_stride;
-        float x = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPer; i += 2) {
-            const float2 f = T::unpack(*reinterpret_cast<const uint32_t*>(c.k + at + 32 * i + 2 * lane));
-            x = fmaf(qv[i], f.x, fmaf(qv[i + 1], f.y, x));
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        const float m2 = fmaxf(m, x);
-        const float old = m2 == -INFINITY ? 1.f : expf(m - m2), e = m2 == -INFINITY ? 0.f : expf(x - m2);
-        l = l * old + e;
-#pragma unroll
-        for (int i = 0; i < kPer; i += 2) {
-            const float2 f = T::unpack(*reinterpret_cast<const uint32_t*>(c.v + at + 32 * i + 2 * lane));
-            o[i] = o[i] * old + e * f.x;
-            o[i + 1] = o[i + 1] * old + e * f.y;
-        }
-        m = m2;
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; i += 2) {
-        part[w][32 * i + 2 * lane] = o[i];
-        part[w][32 * i + 2 * lane + 1] = o[i + 1];
-    }
-    if (lane == 0) {
-        part[w][D] = m;
-        part[w][D + 1] = l;
-    }
-    __syncthreads();
     float top = -INFINITY, sum = 0.f;
-    for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, part[i][D]);
-    for (int i = 0; i < kThreads / 32; ++i) sum += top == -INFINITY ? 0.f : part[i][D + 1] * expf(part[i][D] - top);
-    for (int d = threadIdx.x; d < D; d += kThreads) {
+    for (int i = first + lane; i <= last; i += 32)
+        top = fmaxf(top, p.part_ml[(int64_t)(2 * i + (i == first)) * p.slot_rows + r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int i = first + lane; i <= last; i += 32) {
+        const float2 t = p.part_ml[(int64_t)(2 * i + (i == first)) * p.slot_rows + r];
+        sum += t.x == -INFINITY ? t.y : t.y * fast_exp2(t.x - top);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+
+    float acc[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+#pragma unroll 4
+    for (int i = first + warp; i <= last; i += kJoinWarps) {
+        const int64_t at = (int64_t)(2 * i + (i == first)) * p.slot_rows + r;
+        const float2 t = p.part_ml[at];
+        const float f = t.x == -INFINITY ? t.y : fast_exp2(t.x - top);
+        const float* v = p.part_o + at * D + kPer * lane;
+#pragma unroll
+        for (int k = 0; k < kPer; k += 2) {
+            const float2 u = *reinterpret_cast<const float2*>(v + k);
+            acc[k] = fmaf(u.x, f, acc[k]);
+            acc[k + 1] = fmaf(u.y, f, acc[k + 1]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc_s[warp][kPer * lane + k] = acc[k];
+    __syncthreads();
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
         float v = 0.f;
-        for (int i = 0; i < kThreads / 32; ++i)
-            v += top == -INFINITY || part[i][D + 1] == 0.f ? 0.f : part[i][d] * expf(part[i][D] - top);
-        a.out[row * a.out_row_stride + (int64_t)h * D + d] = sum == 0.f ? 0.f : v / sum;
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) v += acc_s[i][d];
+        p.out[row * p.out_row_stride + (int64_t)head * D + d] = v * inv;
     }
 }
 
-template <class T>
-cudaError_t launch_type(const iq4xs_tree_attention_args& a, const CacheView& c, const BatchView& b, int* err,
+cudaError_t launch_join(const AttnParams& p, const BatchView& b, int row_tile, int q_heads, int* err,
                         cudaStream_t stream) {
-    const dim3 grid((unsigned)a.rows, (unsigned)a.q_heads);
-    switch (c.head_dim) {
-        case 64: return launch_chained(attention_kernel<64, T>, grid, dim3(kThreads), 0, stream, a, c, b, err);
-        case 128: return launch_chained(attention_kernel<128, T>, grid, dim3(kThreads), 0, stream, a, c, b, err);
-        case 256: return launch_chained(attention_kernel<256, T>, grid, dim3(kThreads), 0, stream, a, c, b, err);
+    const dim3 grid((unsigned)p.rows, (unsigned)q_heads), block(32 * kJoinWarps);
+    switch (p.head_dim) {
+        case 64: return launch_chained(attention_join_kernel<64>, grid, block, 0, stream, p, b, row_tile, err);
+        case 128: return launch_chained(attention_join_kernel<128>, grid, block, 0, stream, p, b, row_tile, err);
+        case 256: return launch_chained(attention_join_kernel<256>, grid, block, 0, stream, p, b, row_tile, err);
         default: return cudaErrorInvalidValue;
     }
 }
 
+inline int64_t slot_rows(int64_t row_tile, int64_t rows, int64_t group) {
+    return rows * group < row_tile ? rows * group : row_tile;
+}
+inline int64_t align16(int64_t v) { return (v + 15) / 16 * 16; }
+
 }  // namespace
 
-int64_t tree_attention_workspace(int64_t, int64_t, int64_t, int64_t, int64_t, int) { return 16; }
+int64_t tree_attention_workspace(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t,
+                                 int num_sms) {
+    const int64_t n = 2 * (int64_t)mma_ctas(head_dim, num_sms) * slot_rows(kMmaRows, rows, q_heads / kv_heads);
+    return align16(n * 8) + n * head_dim * 4;
+}
 
 cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const CacheView& c, const BatchView& b, bool bf16,
-                                  void*, int* err, int, cudaStream_t stream) {
-    return bf16 ? launch_type<KvBf16>(a, c, b, err, stream) : launch_type<KvF16>(a, c, b, err, stream);
+                                  void* encode, int* err, int num_sms, int skip_stage, cudaStream_t stream) {
+    AttnParams p;
+    const int group = (int)(a.q_heads / c.heads);
+    p.q = static_cast<const uint16_t*>(a.q);
+    p.out = a.out;
+    p.mask = a.tree_mask;
+    p.q_row_stride = a.q_row_stride;
+    p.out_row_stride = a.out_row_stride;
+    p.rows = a.rows;
+    p.scale_log2 = (float)(a.scale * 1.4426950408889634);
+    p.group = group;
+    p.kv_heads = c.heads;
+    p.mask_words = (int)a.mask_words;
+    p.head_dim = c.head_dim;
+    p.skip_stage = skip_stage;
+    p.ctas = mma_ctas(c.head_dim, num_sms);
+    p.whole_items = (int64_t)b.table_width * c.page_size <= kWholeTokens;
+    p.slot_rows = (int)slot_rows(kMmaRows, a.rows, group);
+    p.part_ml = static_cast<float2*>(a.workspace);
+    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
+                                        align16(2 * (int64_t)p.ctas * p.slot_rows * 8));
+    CUtensorMap tk, tv;
+    const EncodeTiledFn enc = reinterpret_cast<EncodeTiledFn>(encode);
+    const int64_t layer = a.layer * c.layer_stride;
+    if (!encode_kv(enc, c.k + layer, c, bf16, &p.slot_axis, &tk) ||
+        !encode_kv(enc, c.v + layer, c, bf16, &p.slot_axis, &tv))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = launch_attention_mma(p, &tk, &tv, c, b, bf16, err, stream);
+    if (e != cudaSuccess || p.whole_items) return e;
+    return launch_join(p, b, kMmaRows, (int)a.q_heads, err, stream);
 }
 
 }  // namespace iq4xs

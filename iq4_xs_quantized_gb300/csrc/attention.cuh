@@ -1,0 +1,183 @@
+// attention.cuh -- what the attention kernels share: the split of a batch's
+// work over the CTAs, the partial results of work that was cut, and the
+// masks.
+//
+// Work.  An item is (sequence, row tile, key/value head): the rows are the
+// sequence's new tokens times the query heads that share the key/value head
+// (row r: token r / group, query head head * group + r % group), tiled by the
+// kernel's row tile; its keys come in tiles of kKeyTile positions.  The
+// (item, key tile) pairs of the whole batch lie on one line, and CTA g of G
+// takes [g W / G, (g + 1) W / G): every CTA the same number of key tiles,
+// whatever the lengths.  An item that a boundary cuts is joined afterwards:
+// each CTA leaves at most two partial results, slot 2 g for the item whose
+// start lies before its range, 2 g + 1 for the one that it begins and does
+// not finish.  Where no sequence can be long (the table's width says so),
+// items are not cut and nothing is joined.  Lengths live on the device, so
+// every warp works the split out for itself, from the same numbers.
+#pragma once
+
+#include <cuda.h>
+
+#include "cache.cuh"
+
+namespace iq4xs {
+
+constexpr int kKeyTile = 64;
+
+struct AttnParams {
+    const uint16_t* q;
+    float* out;
+    const uint64_t* mask;
+    float* part_o;     // [2 G slots][slot_rows][D]
+    float2* part_ml;   // [2 G slots][slot_rows] {max (log2 units), sum}
+    int64_t q_row_stride, out_row_stride, rows;
+    float scale_log2;  // scale * log2(e): scores are kept in log2 units
+    int group, kv_heads, mask_words, head_dim;
+    int ctas;          // CTAs the work is split over, at most
+    int whole_items;   // 1: items are not cut
+    int slot_rows;     // rows of a partial result: the row tile, or all rows if fewer
+    int slot_axis;     // tensor-map axis of the slot (1 or 2; the head has the other)
+    int skip_stage;    // test hook: this stage of every CTA is left unissued
+};
+
+// One sequence as the split sees it.
+struct SeqWork {
+    int64_t work;  // (item, key tile) pairs, or items
+    int row0, tokens, len, row_tiles, key_tiles;
+    int unit;      // places an item takes on the line: key_tiles, or 1
+};
+
+__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, const BatchView& b, int s, int row_tile, int* err) {
+    SeqWork w;
+    w.tokens = batch_rows(b, s, p.rows, &w.row0, err);
+    w.len = batch_len(b, s, err);
+    if (w.len < 0 || w.len > (INT32_MAX >> 1)) w.tokens = 0;
+    w.row_tiles = (w.tokens * p.group + row_tile - 1) / row_tile;
+    w.key_tiles = (w.len + w.tokens + kKeyTile - 1) / kKeyTile;
+    w.unit = p.whole_items ? 1 : w.key_tiles;
+    w.work = w.tokens > 0 ? (int64_t)w.row_tiles * p.kv_heads * w.unit : 0;
+    return w;
+}
+
+// The batch's work up to (not including) sequence n: 32 sequences a step, one
+// a lane; the result is the same in every lane.
+__device__ __forceinline__ int64_t work_before(const AttnParams& p, const BatchView& b, int n, int row_tile,
+                                               int* err) {
+    const int lane = threadIdx.x & 31;
+    int64_t sum = 0;
+    for (int s0 = 0; s0 < n; s0 += 32)
+        if (s0 + lane < n) sum += seq_work(p, b, s0 + lane, row_tile, err).work;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
+// CTAs that get work: no more than places, so that no range is empty.
+__device__ __forceinline__ int working_ctas(const AttnParams& p, int64_t work) {
+    return (int)min((int64_t)p.ctas, work);
+}
+__device__ __forceinline__ int64_t range_start(int64_t work, int ctas, int g) { return work * g / ctas; }
+// The CTA whose range holds place x.
+__device__ __forceinline__ int range_owner(int64_t work, int ctas, int64_t x) {
+    return (int)(((x + 1) * ctas - 1) / work);
+}
+
+// A CTA's walk over its range, item by item.
+struct WorkWalk {
+    int64_t x, end;      // place on the line, end of the range
+    int64_t seq_x;       // place at which sequence s starts
+    SeqWork w;
+    int s;
+    // the current item's part
+    int head, row_tile, tile0, tile1;
+    bool whole;          // this CTA has all of the item's key tiles
+    int slot;            // of its partial result, if not
+
+    __device__ __forceinline__ void start(const AttnParams& p, const BatchView& b, int g, int rt, int* err) {
+        const int64_t work = work_before(p, b, b.sequences, rt, err);
+        const int ctas = working_ctas(p, work);
+        s = -1;
+        x = end = 0;
+        if (g >= ctas) return;
+        x = range_start(work, ctas, g);
+        end = range_start(work, ctas, g + 1);
+        // the sequence that holds x: the last one that starts at or before it
+        const int lane = threadIdx.x & 31;
+        int64_t before = 0;
+        for (int s0 = 0; s0 < b.sequences; s0 += 32) {
+            int64_t v = s0 + lane < b.sequences ? seq_work(p, b, s0 + lane, rt, err).work : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += y;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, before + v > x);
+            if (past != 0) {
+                const int k = __ffs(past) - 1;
+                const int64_t up = __shfl_sync(0xffffffffu, v, k > 0 ? k - 1 : 0);
+                s = s0 + k;
+                seq_x = before + (k > 0 ? up : 0);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, v, 31);
+        }
+        w = seq_work(p, b, s, rt, err);
+        set(p, g);
+    }
+    __device__ __forceinline__ void set(const AttnParams& p, int g) {
+        const int64_t o = x - seq_x;
+        const int item = (int)(o / w.unit);
+        tile0 = (int)(o - (int64_t)item * w.unit);
+        tile1 = p.whole_items ? w.key_tiles : (int)min((int64_t)w.key_tiles, tile0 + (end - x));
+        head = item / w.row_tiles;
+        row_tile = item - head * w.row_tiles;
+        whole = tile0 == 0 && tile1 == w.key_tiles;
+        slot = 2 * g + (tile0 == 0 ? 1 : 0);
+    }
+    __device__ __forceinline__ bool valid() const { return x < end; }
+    __device__ __forceinline__ void next(const AttnParams& p, const BatchView& b, int g, int rt, int* err) {
+        x += p.whole_items ? 1 : tile1 - tile0;
+        if (x >= end) return;
+        while (x - seq_x >= w.work) {  // (sequences without work are passed over)
+            seq_x += w.work;
+            w = seq_work(p, b, ++s, rt, err);
+        }
+        set(p, g);
+    }
+    // Key tiles that a row of this item can see: without a mask (a chain) the
+    // row tile's last token ends them.
+    __device__ __forceinline__ int seen_tiles(const AttnParams& p, int rt) const {
+        int keys = w.len + w.tokens;
+        if (p.mask == nullptr) {
+            const int last = min(w.tokens - 1, ((row_tile + 1) * rt - 1) / p.group);
+            keys = w.len + last + 1;
+        }
+        return min(tile1, (keys + kKeyTile - 1) / kKeyTile);
+    }
+};
+
+// Whether token t (row `row` of the batch) sees its sequence's new token j >= 0.
+__device__ __forceinline__ bool sees_new(const AttnParams& p, int row, int t, int j) {
+    if (p.mask == nullptr) return j <= t;
+    const int word = j >> 6;
+    return word < p.mask_words && (p.mask[(int64_t)row * p.mask_words + word] >> (j & 63) & 1) != 0;
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Softmax weights are exp2(score - m + kWeightBits) with m the running
+// maximum, or up to kLazy below it: O and the sum are rescaled only when a
+// maximum rises by more than kLazy.  kWeightBits keeps small weights out of
+// the fp16 subnormals: 2^(6 + 8) is the largest, 2^-24 the smallest part.
+constexpr float kWeightBits = 6.0f;
+constexpr float kLazy = 8.0f;
+
+// Launchers of the two forms (csrc/attention_mma.cu, csrc/attention_tc.cu).
+cudaError_t launch_attention_mma(const AttnParams& p, const void* tk, const void* tv, const CacheView& c,
+                                 const BatchView& b, bool bf16, int* err, cudaStream_t stream);
+
+}  // namespace iq4xs

@@ -5,6 +5,8 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "../../include/iq4xs.h"
 #include "internal.cuh"
 
@@ -94,9 +96,23 @@ cudaError_t launch_cache_release(const BatchView& b, int32_t* refs, int pages, c
 cudaError_t launch_cache_copy_pages(const CacheView& c, const int32_t* src, const int32_t* dst, int count, int* err,
                                     cudaStream_t stream);
 cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const CacheView& c, const BatchView& b, bool bf16,
-                                  void* encode, int* err, int num_sms, cudaStream_t stream);
+                                  void* encode, int* err, int num_sms, int skip_stage, cudaStream_t stream);
 int64_t tree_attention_workspace(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t sequences,
                                  int num_sms);
+
+// Dynamic shared memory of a kernel, once per device.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // One launch with the library's programmatic dependent launch setting.
 template <typename... KArgs, typename... Args>

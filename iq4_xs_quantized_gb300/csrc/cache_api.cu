@@ -131,7 +131,7 @@ int iq4xs_tree_attention(const iq4xs_tree_attention_args* a, const iq4xs_kv_cach
         return IQ4XS_ERR_ARG;
     if (b.sequences == 0) return IQ4XS_OK;
     return from_cuda(launch_tree_attention(*a, c, b, cache->dtype == IQ4XS_KV_BF16, encode, err, sms,
-                                           reinterpret_cast<cudaStream_t>(stream)));
+                                           take_skip_stage(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int iq4xs_cache_reserve(const iq4xs_kv_batch* batch, int64_t page_size, int32_t* refs, int64_t pages, int32_t* status,

@@ -1039,6 +1039,8 @@ cudaError_t launch_matmul_dp4a_grouped(const void* w, int wt, int64_t expert_str
                                        int64_t ldy, int* err, cudaStream_t stream);
 // Programmatic dependent launch on (default) or off for every launch.
 bool pdl_enabled();
+// The stage armed by iq4xs_test_skip_w_stage, disarming it; -1 if none.
+int take_skip_stage();
 // The current device's error word, SM count and tensor-map encoder after its
 // one-time set-up; an iq4xs_status.
 int device_context(int** err, int* num_sms, void** encode);
