@@ -2,6 +2,8 @@
 // choice of the form, and the join of items that the split cut.
 #include "attention.cuh"
 
+#include <math.h>
+
 namespace iq4xs {
 namespace {
 
@@ -9,7 +11,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-constexpr int kMmaRows = 16;         // row tile of the warp-level form
+constexpr int kMmaRows = 16, kTcRows = 128;  // row tiles of the two forms
 constexpr int64_t kWholeTokens = 512;
 
 int mma_ctas(int64_t head_dim, int num_sms) { return head_dim == 256 ? num_sms : 2 * num_sms; }
@@ -137,7 +139,11 @@ inline int64_t align16(int64_t v) { return (v + 15) / 16 * 16; }
 
 int64_t tree_attention_workspace(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t,
                                  int num_sms) {
-    const int64_t n = 2 * (int64_t)mma_ctas(head_dim, num_sms) * slot_rows(kMmaRows, rows, q_heads / kv_heads);
+    // the larger of the two forms' (a call's own lengths choose the form)
+    const int64_t group = q_heads / kv_heads;
+    const int64_t mma = 2 * (int64_t)mma_ctas(head_dim, num_sms) * slot_rows(kMmaRows, rows, group);
+    const int64_t tc = 2 * (int64_t)num_sms * slot_rows(kTcRows, rows, group);
+    const int64_t n = mma > tc ? mma : tc;
     return align16(n * 8) + n * head_dim * 4;
 }
 
@@ -151,27 +157,34 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     p.q_row_stride = a.q_row_stride;
     p.out_row_stride = a.out_row_stride;
     p.rows = a.rows;
-    p.scale_log2 = (float)(a.scale * 1.4426950408889634);
+    p.layer_offset = a.layer * c.layer_stride;
+    p.scale_log2 = a.scale == 0 ? 1.f : (float)(fabs(a.scale) * 1.4426950408889634);
+    p.q_and = a.scale == 0 ? 0u : 0xffffffffu;
+    p.q_xor = a.scale < 0 ? 0x80008000u : 0u;
     p.group = group;
     p.kv_heads = c.heads;
     p.mask_words = (int)a.mask_words;
     p.head_dim = c.head_dim;
     p.skip_stage = skip_stage;
-    p.ctas = mma_ctas(c.head_dim, num_sms);
+    // Row tiles of 16 while a sequence's rows a key/value head fit one, of 128 beyond.
+    const int64_t mean_rows = (a.rows + b.sequences - 1) / b.sequences * group;
+    const bool tc = mean_rows > kMmaRows;
+    const int row_tile = tc ? kTcRows : kMmaRows;
+    p.ctas = tc ? num_sms : mma_ctas(c.head_dim, num_sms);
     p.whole_items = (int64_t)b.table_width * c.page_size <= kWholeTokens;
-    p.slot_rows = (int)slot_rows(kMmaRows, a.rows, group);
+    p.slot_rows = (int)slot_rows(row_tile, a.rows, group);
     p.part_ml = static_cast<float2*>(a.workspace);
     p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
                                         align16(2 * (int64_t)p.ctas * p.slot_rows * 8));
     CUtensorMap tk, tv;
     const EncodeTiledFn enc = reinterpret_cast<EncodeTiledFn>(encode);
-    const int64_t layer = a.layer * c.layer_stride;
-    if (!encode_kv(enc, c.k + layer, c, bf16, &p.slot_axis, &tk) ||
-        !encode_kv(enc, c.v + layer, c, bf16, &p.slot_axis, &tv))
+    if (!encode_kv(enc, c.k + p.layer_offset, c, bf16, &p.slot_axis, &tk) ||
+        !encode_kv(enc, c.v + p.layer_offset, c, bf16, &p.slot_axis, &tv))
         return cudaErrorInvalidValue;
-    const cudaError_t e = launch_attention_mma(p, &tk, &tv, c, b, bf16, err, stream);
+    const cudaError_t e = tc ? launch_attention_tc(p, &tk, &tv, c, b, bf16, err, stream)
+                             : launch_attention_mma(p, &tk, &tv, c, b, bf16, err, stream);
     if (e != cudaSuccess || p.whole_items) return e;
-    return launch_join(p, b, kMmaRows, (int)a.q_heads, err, stream);
+    return launch_join(p, b, row_tile, (int)a.q_heads, err, stream);
 }
 
 }  // namespace iq4xs

@@ -31,7 +31,9 @@ struct AttnParams {
     float* part_o;     // [2 G slots][slot_rows][D]
     float2* part_ml;   // [2 G slots][slot_rows] {max (log2 units), sum}
     int64_t q_row_stride, out_row_stride, rows;
-    float scale_log2;  // scale * log2(e): scores are kept in log2 units
+    int64_t layer_offset;  // elements of K and V
+    float scale_log2;  // |scale| log2(e): scores are kept in log2 units
+    uint32_t q_and, q_xor;  // the scale's sign (or zero), put on q: scores may be masked with -inf before scaling
     int group, kv_heads, mask_words, head_dim;
     int ctas;          // CTAs the work is split over, at most
     int whole_items;   // 1: items are not cut
@@ -163,6 +165,23 @@ __device__ __forceinline__ bool sees_new(const AttnParams& p, int row, int t, in
     return word < p.mask_words && (p.mask[(int64_t)row * p.mask_words + word] >> (j & 63) & 1) != 0;
 }
 
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+// Bit k: token t sees the position k behind one whose place among the new
+// tokens is j0 (negative: context); `have` positions lie before the end.
+__device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, int row, int t, int j0, int have) {
+    uint32_t fresh;
+    if (p.mask == nullptr) {
+        fresh = low_bits(t - j0 + 1);
+    } else {
+        const int lo = max(j0, 0), word = lo >> 6, sh = lo & 63;
+        const uint64_t* m = p.mask + (int64_t)row * p.mask_words;
+        uint64_t v = word < p.mask_words ? m[word] >> sh : 0;
+        if (sh > 32 && word + 1 < p.mask_words) v |= m[word + 1] << (64 - sh);
+        fresh = lo - j0 >= 32 ? 0u : (uint32_t)v << (lo - j0);
+    }
+    return (low_bits(-j0) | fresh) & low_bits(have);
+}
+
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -176,8 +195,40 @@ __device__ __forceinline__ float fast_exp2(float x) {
 constexpr float kWeightBits = 6.0f;
 constexpr float kLazy = 8.0f;
 
+// Eight values of q, with the scale's sign.
+__device__ __forceinline__ uint4 load_q(const AttnParams& p, const uint16_t* src) {
+    uint4 v = *reinterpret_cast<const uint4*>(src);
+    v.x = (v.x & p.q_and) ^ p.q_xor;
+    v.y = (v.y & p.q_and) ^ p.q_xor;
+    v.z = (v.z & p.q_and) ^ p.q_xor;
+    v.w = (v.w & p.q_and) ^ p.q_xor;
+    return v;
+}
+
+// Tiles of 16-bit rows in shared memory: [64-channel chunk][row][128 bytes],
+// 16-byte units swizzled within each 8-row atom as TMA's 128-byte swizzle
+// does.  Offset of unit u (8 channels) of row r.
+constexpr int kChunkBytes = 128;
+__device__ __forceinline__ uint32_t unit_at(int r, int u, int rows) {
+    return (uint32_t)((u >> 3) * rows * kChunkBytes + r * kChunkBytes + (((u & 7) ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+// mbar_wait by a whole warp, with one answer for all of its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                          int code) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code)) != 0;
+}
+
 // Launchers of the two forms (csrc/attention_mma.cu, csrc/attention_tc.cu).
 cudaError_t launch_attention_mma(const AttnParams& p, const void* tk, const void* tv, const CacheView& c,
                                  const BatchView& b, bool bf16, int* err, cudaStream_t stream);
+cudaError_t launch_attention_tc(const AttnParams& p, const void* tk, const void* tv, const CacheView& c,
+                                const BatchView& b, bool bf16, int* err, cudaStream_t stream);
 
 }  // namespace iq4xs

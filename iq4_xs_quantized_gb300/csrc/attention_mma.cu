@@ -23,7 +23,6 @@ constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kWarpKeys = kKeyTile / kConsumers;
 static_assert(kWarpKeys == 16, "a warp's keys are one k16 step of the second product");
-constexpr int kChunkBytes = 128;  // one swizzle row: 64 channels
 
 template <int D>
 struct MmaAttn {
@@ -78,19 +77,8 @@ struct Parts<KvBf16> {
     static constexpr int kN = 3;
 };
 
-// Byte offset of the 16-byte unit u (8 channels) of row r in a [chunk][rows][128 B] swizzled tile.
-__device__ __forceinline__ uint32_t unit_at(int r, int u, int rows) {
-    return (uint32_t)((u >> 3) * rows * kChunkBytes + r * kChunkBytes + (((u & 7) ^ (r & 7)) << 4));
-}
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 static_assert(kConsumers * 32 == 128, "the consumers' barrier");
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-        : "memory");
-}
 
 template <int D, class T>
 __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
@@ -144,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
             int ids2 = page0 + 32 + lane < held ? table[page0 + 32 + lane] : -1;
             for (int tile = w.tile0; tile < end; ++tile, ++it) {
                 const int st = it % C::kStages, pos0 = tile * kKeyTile;
-                if (it >= C::kStages && !mbar_wait(slot_free + st, ((it / C::kStages) - 1) & 1, abort_flag, err,
+                if (it >= C::kStages && !warp_wait(slot_free + st, ((it / C::kStages) - 1) & 1, abort_flag, err,
                                                    kDevErrTimeoutKvSlot)) {
                     live = false;
                     break;
@@ -216,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
                                       ((int64_t)w.head * p.group + row % p.group) * D + col * 8;
                 if (bc_global(bc, src, 16, p.q,
                               2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D), kBcAttnQ))
-                    v = *reinterpret_cast<const uint4*>(src);
+                    v = load_q(p, src);
             }
             sts_u128(q_s + unit_at(r, col, kRowTile), v);
         }

@@ -1,0 +1,536 @@
+// attention_tc.cu -- tree attention for many rows a key/value head (drafted
+// trees, prompt chunks): tcgen05 on tiles of 128 rows x 64 keys.
+//
+// One pass, as in the warp-level form; here a row is a lane of tensor memory:
+//
+//   S = Q K^T      128 x 64, Q and K from shared memory (K-major)
+//   P = exp2(S - m) split into 16-bit parts, back into tensor memory over S
+//   T = P V        128 x D, P from tensor memory, V from shared memory (as it
+//                  lies: channels contiguous)
+//   O = O f + T    in fp32 registers of the threads that own the row
+//
+// T starts from zero for every key tile and is added to O by rounded fp32
+// arithmetic: the tensor core cuts its sums off, and thousands of tiles on
+// one accumulator would add those cuts up.
+//
+// Roles: a producer warp (TMA), a warp whose first lane issues the MMAs, and
+// eight softmax warps, two per 32-lane quadrant: one takes keys 0-31 of a
+// tile and channels 0..D/2-1 of O, the other the rest; they share a row's
+// maximum through shared memory.  The MMAs of tile j + 1's scores are issued
+// before tile j's output product, so the tensor core works while the softmax
+// runs.  K and V tiles go through one ring in the order the MMAs take them:
+// K0 K1 V0 K2 V1 ... V(n-1).
+//
+// Up to about 48 rows HBM bounds it (4 D bytes a key), above that the tensor
+// core (1 + parts products of 128 x 64 x D a tile).
+#include "attention.cuh"
+
+namespace iq4xs {
+namespace {
+
+constexpr int kRowTile = 128;
+constexpr int kSoftWarps = 8;
+constexpr int kFirstSoft = 4;  // warps 4-11: two whole warpgroups
+constexpr int kThreads = 32 * (kFirstSoft + kSoftWarps);
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr int kHalfKeys = kKeyTile / 2;
+constexpr int kTmemCols = 512;
+
+template <class T>
+struct TcParts {
+    static constexpr int kN = 2;
+};
+template <>
+struct TcParts<KvBf16> {
+    static constexpr int kN = 3;
+};
+
+template <int D>
+struct TcAttn {
+    static constexpr int kChunks = D / 64;
+    static constexpr int kTileBytes = kKeyTile * D * 2;
+    static constexpr int kSlots = 160 * 1024 / kTileBytes;   // 5, 10, 20
+    static constexpr int kQBytes = kRowTile * D * 2;
+    static constexpr int kQ = kSlots * kTileBytes;
+    static constexpr int kMax = kQ + kQBytes;                // [2][2 halves][128] row maxima
+    static constexpr int kBars = kMax + 2 * 2 * kRowTile * 4;
+    static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 1;
+    static constexpr int kMisc = kBars + kNumBars * 8;       // tensor memory address, abort, odd values
+    static constexpr int kSmem = kMisc + 16;
+    static constexpr int kTBufs = D == 256 ? 1 : 2;          // output products in flight
+    // tensor memory: T, then per score buffer 96 columns: S (64), overlaid by up to three parts of P (32 each)
+    static constexpr int kScoreCols = 96;
+    static constexpr int kScores = kTBufs * D;
+    static constexpr int kHalfD = D / 2;
+    static_assert(kScores + 2 * kScoreCols <= kTmemCols, "tensor memory");
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+// D = 256 keeps 128 output channels a softmax thread: the producer's and the
+// issuer's warpgroup gives up registers (80 + 2 * 208 <= 3 * 168, the launch's).
+constexpr int kSoftRegs = 208, kOtherRegs = 80;
+static_assert(kOtherRegs + 2 * kSoftRegs <= 3 * 168, "register split within the launch's");
+
+// Shared-memory matrix descriptor, 128-byte swizzle.  K-major: sbo between
+// 8-row groups.  MN-major: lbo between 64-element chunks of the M/N axis, sbo
+// between 8-row groups of the K axis.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor, kind::f16, D fp32, M = 128; type 0 fp16, 1 bf16;
+// b_mn: B is N-major.
+constexpr uint32_t idesc_kv(int n, uint32_t type, bool b_mn) {
+    return (1u << 4) | (type << 7) | (type << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(kRowTile >> 4) << 24);
+}
+__device__ __forceinline__ void pair_sync(int quadrant) {
+    asm volatile("bar.sync %0, 64;" ::"r"(quadrant + 1) : "memory");
+}
+// o = o * f + t on two floats at a time.
+__device__ __forceinline__ void fma2(float2& o, float2 f, float2 t) {
+    uint64_t a, b, c;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(o.x), "f"(o.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(f.x), "f"(f.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(t.x), "f"(t.y));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a) : "l"(b), "l"(c));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(a));
+}
+// Places in the ring of tile j's K and V, an item of n tiles starting at place 0.
+__device__ __forceinline__ int place_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int place_v(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+
+template <int D, class T>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                        const AttnParams p, const CacheView c, const BatchView b, int* err) {
+    using C = TcAttn<D>;
+    constexpr int kParts = TcParts<T>::kN;
+    constexpr uint32_t kType = kParts == 3 ? 1u : 0u;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    if ((base & 1023) != 0) {  // (no static shared memory: the swizzle atoms' alignment)
+        if (threadIdx.x == 0) atomicCAS(err, 0, kDevErrLayout);
+        return;
+    }
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);
+    uint64_t* slot_free = full + C::kSlots;
+    uint64_t* s_full = slot_free + C::kSlots;
+    uint64_t* p_full = s_full + 2;
+    uint64_t* t_full = p_full + 2;
+    uint64_t* t_free = t_full + 2;
+    uint64_t* q_full = t_free + 2;
+    uint64_t* drained = q_full + 1;
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::kMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_at + 1);
+    volatile int* odd_flag = abort_flag + 1;  // this item met NaN or infinities among the new tokens' values
+    float* maxima = reinterpret_cast<float*>(smem + C::kMax);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.x;
+    const Bc bc = bc_open(err);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(slot_free + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, kSoftWarps);
+            mbar_init(t_full + i, 1);
+            mbar_init(t_free + i, kSoftWarps);
+        }
+        mbar_init(q_full, kSoftWarps);
+        mbar_init(drained, 1);
+        *abort_flag = 0;
+        *odd_flag = 0;
+        fence_barrier_init();
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+    }
+    if (warp == 1) tmem_alloc(tmem_at, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_at);
+    griddep_wait();
+    griddep_launch_dependents();
+    WorkWalk w;
+    w.start(p, b, g, kRowTile, err);
+
+    if (warp < kFirstSoft) {
+        if constexpr (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 0) {
+            // ------------------------------------------------------ producer
+            const int box_slots = min(c.page_size, kKeyTile);
+            const int boxes = kKeyTile / box_slots * C::kChunks;  // at most 16: one a lane
+            const uint32_t box_bytes = box_slots * kChunkBytes;
+            const int sub = lane / C::kChunks, chunk = lane % C::kChunks;
+            const uint32_t dst0 = base + chunk * kKeyTile * kChunkBytes + sub * box_bytes;
+            int place = 0;  // in the ring, over all items
+            bool live = true;
+            auto load = [&](const void* map, int page, int slot, int used) {
+                const int st = place % C::kSlots;
+                if (place >= C::kSlots && !warp_wait(slot_free + st, ((place / C::kSlots) - 1) & 1, abort_flag, err,
+                                                     kDevErrTimeoutKvSlot)) {
+                    live = false;
+                    return;
+                }
+                const bool skip = place == p.skip_stage;
+                if (lane == 0 && !skip) mbar_arrive_expect_tx(full + st, used * box_bytes);
+                __syncwarp();
+                if (lane < used && !skip) {
+                    const int y = p.slot_axis == 1 ? slot : w.head, z = p.slot_axis == 1 ? w.head : slot;
+                    bc_tma(bc, chunk * 64, 2, 64, D, slot, c.page_size, kBcAttnKv, kBcAttnKv);
+                    tma_load_4d(dst0 + st * C::kTileBytes, map, chunk * 64, y, z, page, full + st);
+                }
+                __syncwarp();
+                ++place;
+            };
+            for (; live && w.valid(); w.next(p, b, g, kRowTile, err)) {
+                const int end = w.seen_tiles(p, kRowTile);
+                const int keys = w.w.len + w.w.tokens;
+                const int held = min(b.held[w.s], b.table_width);
+                const int32_t* table = b.page_table + w.s * b.table_stride;
+                int page0 = (w.tile0 * kKeyTile) >> c.page_shift;
+                int ids = page0 + lane < held ? table[page0 + lane] : -1;
+                int ids2 = page0 + 32 + lane < held ? table[page0 + 32 + lane] : -1;
+                int page_v = 0, slot_v = 0, used_v = 0;  // the previous tile's boxes, for its V
+                for (int tile = w.tile0; live && tile < end; ++tile) {
+                    const int pos0 = tile * kKeyTile, pos = pos0 + sub * box_slots;
+                    while ((pos0 >> c.page_shift) >= page0 + 32) {
+                        page0 += 32;
+                        ids = ids2;
+                        ids2 = page0 + 32 + lane < held ? table[page0 + 32 + lane] : -1;
+                    }
+                    const int used =
+                        min(boxes, (min(kKeyTile, keys - pos0) + box_slots - 1) / box_slots * C::kChunks);
+                    int page = __shfl_sync(0xffffffffu, ids, ((pos >> c.page_shift) - page0) & 31);
+                    if (lane < used && (page < 0 || page >= c.pages)) {
+                        data_error(err, kDataPage);
+                        page = c.pages;  // outside the map: zeros
+                    }
+                    const int slot = pos & (c.page_size - 1);
+                    load(&tk, page, slot, used);
+                    if (live && tile > w.tile0) load(&tv, page_v, slot_v, used_v);
+                    page_v = page;
+                    slot_v = slot;
+                    used_v = used;
+                }
+                if (live && end > w.tile0) load(&tv, page_v, slot_v, used_v);
+            }
+            // No copy may be in flight when the CTA ends.
+            if (*abort_flag)
+                for (int i = max(0, place - C::kSlots); i < place; ++i)
+                    if (i != p.skip_stage) {
+                        int no_abort = 0;
+                        mbar_wait(full + i % C::kSlots, (i / C::kSlots) & 1, &no_abort, err, kDevErrTimeoutKv);
+                    }
+        } else if (warp == 1) {
+            // -------------------------------------------------------- issuer
+            constexpr uint32_t kIdS = idesc_kv(kKeyTile, kType, false), kIdT = idesc_kv(D, kType, true);
+            const uint64_t q_desc = desc_sw128(base + C::kQ, 16, 1024);
+            int place0 = 0, it = 0, items = 0;  // ring place and tile number at the item's start
+            bool live = true;
+            auto scores = [&](int j) {
+                const int place = place0 + place_k(j), st = place % C::kSlots, buf = (it + j) & 1;
+                live = live && warp_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
+                if (live && lane == 0) {
+                    tc_fence_after();
+                    const uint64_t k_desc = desc_sw128(base + st * C::kTileBytes, 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        tc_mma_f16(tmem + C::kScores + buf * C::kScoreCols,
+                                   q_desc + (((k / 4) * kRowTile * kChunkBytes + (k % 4) * 32) >> 4),
+                                   k_desc + (((k / 4) * kKeyTile * kChunkBytes + (k % 4) * 32) >> 4), kIdS, k > 0);
+                    tc_commit(s_full + buf);
+                    tc_commit(slot_free + st);
+                }
+                __syncwarp();
+            };
+            for (; live && w.valid(); w.next(p, b, g, kRowTile, err)) {
+                const int n = w.seen_tiles(p, kRowTile) - w.tile0;
+                if (n <= 0) continue;
+                live = warp_wait(q_full, items & 1, abort_flag, err, kDevErrTimeoutScore);
+                if (!live) break;
+                scores(0);
+                for (int j = 0; live && j < n; ++j) {
+                    if (j + 1 < n) scores(j + 1);
+                    const int place = place0 + place_v(j, n), st = place % C::kSlots;
+                    const int i = it + j, buf = i & 1, tb = i % C::kTBufs;
+                    live = live && warp_wait(p_full + buf, (i >> 1) & 1, abort_flag, err, kDevErrTimeoutScore);
+                    live = live && warp_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
+                    if (i >= C::kTBufs)
+                        live = live && warp_wait(t_free + tb, (i / C::kTBufs - 1) & 1, abort_flag, err,
+                                                 kDevErrTimeoutScore);
+                    if (live && lane == 0) {
+                        tc_fence_after();
+                        const uint64_t v_desc = desc_sw128(base + st * C::kTileBytes, kKeyTile * kChunkBytes, 1024);
+#pragma unroll
+                        for (int n2 = kParts - 1; n2 >= 0; --n2)  // the smallest parts first
+#pragma unroll
+                            for (int k = 0; k < kKeyTile / 16; ++k)
+                                tc_mma_f16_ta(tmem + tb * D,
+                                              tmem + C::kScores + buf * C::kScoreCols + n2 * (kKeyTile / 2) + k * 8,
+                                              v_desc + ((k * 16 * kChunkBytes) >> 4), kIdT, n2 < kParts - 1 || k > 0);
+                        tc_commit(t_full + tb);
+                        tc_commit(slot_free + st);
+                    }
+                    __syncwarp();
+                }
+                place0 += 2 * n;
+                it += n;
+                ++items;
+            }
+            // Tensor memory is given back only when every product is done.
+            if (*abort_flag) {
+                if (lane == 0) tc_commit(drained);
+                int no_abort = 0;
+                mbar_wait(drained, 0, &no_abort, err, kDevErrTimeoutScore);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        if constexpr (D == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        const int quad = warp & 3, half = (warp - kFirstSoft) >> 2;
+        const int r = quad * 32 + lane;               // the thread's row of the tile
+        const int st_id = threadIdx.x - 32 * kFirstSoft;
+        const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
+        int place0 = 0, it = 0;
+        for (; w.valid(); w.next(p, b, g, kRowTile, err)) {
+            const int n = max(0, w.seen_tiles(p, kRowTile) - w.tile0);
+            const int rows = min(kRowTile, w.w.tokens * p.group - w.row_tile * kRowTile);
+            const int keys = w.w.len + w.w.tokens;
+            const bool busy = quad * 32 < rows;       // the warp has rows
+            const int my_row = w.row_tile * kRowTile + min(r, rows - 1);
+            const int tok = my_row / p.group;
+            float2 o[C::kHalfD / 2];
+#pragma unroll
+            for (int i = 0; i < C::kHalfD / 2; ++i) o[i] = make_float2(0.f, 0.f);
+            float m = -INFINITY, l = 0.f, f_last = 1.f;
+            if (n > 0) {
+                // q of the item's rows, all 256 threads; rows behind the last are zero
+                for (int u = st_id; u < kRowTile * (D / 8); u += kSoftThreads) {
+                    const int qr = u / (D / 8), col = u % (D / 8), row = w.row_tile * kRowTile + qr;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (qr < rows) {
+                        const uint16_t* src = p.q + (w.w.row0 + row / p.group) * p.q_row_stride +
+                                              ((int64_t)w.head * p.group + row % p.group) * D + col * 8;
+                        if (bc_global(bc, src, 16, p.q,
+                                      2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D), kBcAttnQ))
+                            v = load_q(p, src);
+                    }
+                    sts_u128(base + C::kQ + unit_at(qr, col, kRowTile), v);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
+            }
+            // O takes tile j's product while tile j + 1's is under way
+            auto accumulate = [&](int i, float f) {
+                const int tb = i % C::kTBufs;
+                mbar_wait(t_full + tb, (i / C::kTBufs) & 1, abort_flag, err, kDevErrTimeoutScore);
+                if (busy) {
+                    tc_fence_after();
+                    const float2 f2 = make_float2(f, f);
+#pragma unroll
+                    for (int k = 0; k < C::kHalfD / 32; ++k) {
+                        uint32_t t[32];
+                        tmem_ld32_wait(tmem + lane_at + tb * D + half * C::kHalfD + 32 * k, t);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            fma2(o[16 * k + x], f2,
+                                 make_float2(__uint_as_float(t[2 * x]), __uint_as_float(t[2 * x + 1])));
+                    }
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(t_free + tb);
+            };
+            for (int j = 0; j < n; ++j) {
+                const int i = it + j, buf = i & 1;
+                const int pos0 = (w.tile0 + j) * kKeyTile, key0 = pos0 + half * kHalfKeys;
+                mbar_wait(s_full + buf, (i >> 1) & 1, abort_flag, err, kDevErrTimeoutScore);
+                float f = 1.f;
+                if (busy) {
+                    tc_fence_after();
+                    const uint32_t s_at = tmem + lane_at + C::kScores + buf * C::kScoreCols;
+                    uint32_t x[32];
+                    tmem_ld32_wait(s_at + half * kHalfKeys, x);
+                    tc_fence_before();
+                    const int have = keys - key0;  // positions before the end
+                    if (key0 + kHalfKeys > w.w.len || have < kHalfKeys) {
+                        const uint32_t seen = seen_bits(p, w.w.row0 + tok, tok, key0 - w.w.len, have);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (!(seen >> k & 1)) x[k] = 0xff800000u;  // -inf
+                    }
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2)
+                        mx = fmaxf(mx, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+                    float* mine = maxima + buf * 2 * kRowTile;
+                    mine[half * kRowTile + r] = mx;
+                    pair_sync(quad);  // also: both halves have read S, which P is about to overwrite
+                    mx = fmaxf(mx, mine[(half ^ 1) * kRowTile + r]);
+                    mx *= p.scale_log2;  // (the scale is positive)
+                    if (mx > m + kLazy) {
+                        f = fast_exp2(m - mx);
+                        m = mx;
+                        l *= f;
+                    }
+                    const float shift = m == -INFINITY ? 0.f : kWeightBits - m;
+                    float l2 = 0.f;
+#pragma unroll
+                    for (int h2 = 0; h2 < 2; ++h2) {  // 16 keys at a time: 8 columns a part
+                        uint32_t part[kParts][8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float a0 = fast_exp2(fmaf(__uint_as_float(x[16 * h2 + 2 * k]), p.scale_log2, shift));
+                            float a1 = fast_exp2(fmaf(__uint_as_float(x[16 * h2 + 2 * k + 1]), p.scale_log2, shift));
+                            l2 += a0 + a1;
+#pragma unroll
+                            for (int n2 = 0; n2 < kParts; ++n2) {
+                                part[n2][k] = T::pack(a0, a1);
+                                const float2 t = T::unpack(part[n2][k]);
+                                a0 -= t.x;
+                                a1 -= t.y;
+                            }
+                        }
+#pragma unroll
+                        for (int n2 = 0; n2 < kParts; ++n2)
+                            asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                                             s_at + n2 * (kKeyTile / 2) + half * (kHalfKeys / 2) + 8 * h2),
+                                         "r"(part[n2][0]), "r"(part[n2][1]), "r"(part[n2][2]), "r"(part[n2][3]),
+                                         "r"(part[n2][4]), "r"(part[n2][5]), "r"(part[n2][6]), "r"(part[n2][7])
+                                         : "memory");
+                    }
+                    l += l2;
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                if (pos0 + kKeyTile > w.w.len && (keys - pos0 < kKeyTile || w.w.tokens > 1)) {
+                    // Slots behind the end may hold anything, and so may tokens
+                    // that some row does not see: a zero weight would carry their
+                    // NaN and infinities into its sum.  Such values leave the
+                    // tile; rows that do see them get them at the item's end.
+                    const int place = place0 + place_v(j, n), st = place % C::kSlots;
+                    mbar_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
+                    const int first_new = max(0, w.w.len - pos0), have = min(kKeyTile, keys - pos0);
+                    bool odd = false;
+                    for (int u = first_new * (D / 8) + st_id; u < kKeyTile * (D / 8); u += kSoftThreads) {
+                        const int key = u / (D / 8);
+                        const uint32_t at = base + st * C::kTileBytes + unit_at(key, u % (D / 8), kKeyTile);
+                        uint32_t v[4] = {0, 0, 0, 0};
+                        bool bad = key >= have;
+                        if (!bad) {
+                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                         : "r"(at));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 t = T::unpack(v[k]);
+                                const bool b0 = !isfinite(t.x), b1 = !isfinite(t.y);
+                                v[k] &= (b0 ? 0u : 0xffffu) | (b1 ? 0u : 0xffff0000u);
+                                bad |= b0 || b1;
+                            }
+                            odd |= bad;
+                        }
+                        if (bad) sts_u128(at, make_uint4(v[0], v[1], v[2], v[3]));
+                    }
+                    if (odd) *odd_flag = 1;
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + buf);
+                if (j > 0) accumulate(i - 1, f_last);
+                f_last = f;
+            }
+            if (n > 0) accumulate(it + n - 1, f_last);
+            place0 += 2 * n;
+            it += n;
+
+            // Join the halves' sums and write the row.
+            float* mine = maxima + (it & 1) * 2 * kRowTile;  // (the buffer the last tile did not use)
+            if (busy) {
+                mine[half * kRowTile + r] = l;
+                pair_sync(quad);
+                l += mine[(half ^ 1) * kRowTile + r];
+            }
+            asm volatile("bar.sync 5, 256;" ::: "memory");  // every thread's odd_flag is in
+            if (*odd_flag && busy && r < rows) {
+                for (int t = 0; t < w.w.tokens; ++t) {
+                    const int pos = w.w.len + t;
+                    if (pos < w.tile0 * kKeyTile || pos >= w.tile1 * kKeyTile ||
+                        !sees_new(p, w.w.row0 + tok, tok, t))
+                        continue;
+                    const int page = page_of(c, b, w.s, pos, err);
+                    if (page < 0) continue;
+                    const uint16_t* src = c.v + p.layer_offset + page * c.page_stride + w.head * c.head_stride +
+                                          (pos & (c.page_size - 1)) * c.slot_stride + half * C::kHalfD;
+#pragma unroll
+                    for (int i = 0; i < C::kHalfD / 2; ++i) {
+                        const float2 v = T::unpack(*reinterpret_cast<const uint32_t*>(src + 2 * i));
+                        if (!isfinite(v.x)) o[i].x += v.x;
+                        if (!isfinite(v.y)) o[i].y += v.y;
+                    }
+                }
+            }
+            asm volatile("bar.sync 5, 256;" ::: "memory");
+            if (st_id == 0) *odd_flag = 0;
+            if (r < rows) {
+                float* dst;
+                float inv = 1.f;
+                if (w.whole) {
+                    inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing: zeros
+                    dst = p.out + (w.w.row0 + tok) * p.out_row_stride +
+                          ((int64_t)w.head * p.group + my_row % p.group) * D + half * C::kHalfD;
+                } else {
+                    dst = p.part_o + ((int64_t)w.slot * p.slot_rows + r) * D + half * C::kHalfD;
+                    if (half == 0) p.part_ml[(int64_t)w.slot * p.slot_rows + r] = make_float2(m, l);
+                }
+                const bool ok = !w.whole || bc_global(bc, dst, 4 * C::kHalfD, p.out,
+                                                      4 * ((p.rows - 1) * p.out_row_stride +
+                                                           (int64_t)p.group * p.kv_heads * D), kBcAttnOut);
+                if (ok)
+#pragma unroll
+                    for (int i = 0; i < C::kHalfD / 4; ++i)
+                        *reinterpret_cast<float4*>(dst + 4 * i) =
+                            make_float4(o[2 * i].x * inv, o[2 * i].y * inv, o[2 * i + 1].x * inv, o[2 * i + 1].y * inv);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D, class T>
+cudaError_t launch_one(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const CacheView& c,
+                       const BatchView& b, int* err, cudaStream_t stream) {
+    const cudaError_t e = allow_smem<attention_tc_kernel<D, T>>(TcAttn<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_chained(attention_tc_kernel<D, T>, dim3((unsigned)p.ctas), dim3(kThreads), TcAttn<D>::kSmem, stream,
+                          tk, tv, p, c, b, err);
+}
+
+template <class T>
+cudaError_t launch_type(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const CacheView& c,
+                        const BatchView& b, int* err, cudaStream_t stream) {
+    switch (c.head_dim) {
+        case 64: return launch_one<64, T>(p, tk, tv, c, b, err, stream);
+        case 128: return launch_one<128, T>(p, tk, tv, c, b, err, stream);
+        case 256: return launch_one<256, T>(p, tk, tv, c, b, err, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tc(const AttnParams& p, const void* tk, const void* tv, const CacheView& c,
+                                const BatchView& b, bool bf16, int* err, cudaStream_t stream) {
+    const CUtensorMap& mk = *static_cast<const CUtensorMap*>(tk);
+    const CUtensorMap& mv = *static_cast<const CUtensorMap*>(tv);
+    return bf16 ? launch_type<KvBf16>(p, mk, mv, c, b, err, stream) : launch_type<KvF16>(p, mk, mv, c, b, err, stream);
+}
+
+}  // namespace iq4xs

@@ -332,7 +332,9 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s: waits for a 
 // 2 s, a hand-off from another role 4 s, the final drains and the split-K
 // slices 6 s.
 __host__ __device__ constexpr unsigned long long wait_limit_ns(int code) {
-    return (code == kDevErrTimeoutW || code == kDevErrTimeoutQ || code == kDevErrTimeoutMmaStage) ? kWaitLimitNs
+    return (code == kDevErrTimeoutW || code == kDevErrTimeoutQ || code == kDevErrTimeoutMmaStage ||
+            code == kDevErrTimeoutKv)
+               ? kWaitLimitNs
            : (code == kDevErrTimeoutDrain || code == kDevErrTimeoutRecv) ? 3 * kWaitLimitNs
                                                                           : 2 * kWaitLimitNs;
 }
