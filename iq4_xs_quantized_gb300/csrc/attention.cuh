@@ -195,6 +195,57 @@ __device__ __forceinline__ float fast_exp2(float x) {
 constexpr float kWeightBits = 6.0f;
 constexpr float kLazy = 8.0f;
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t x, y, z;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x) : "l"(y), "l"(z));
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t x, y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(y));
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ float2 mask2(float2 a, uint32_t mask) {
+    return make_float2(__uint_as_float(__float_as_uint(a.x) & mask), __uint_as_float(__float_as_uint(a.y) & mask));
+}
+// Two weights as the sum of kN packed 16-bit parts, largest first.  All but
+// the last part cut the fp32 value off after the type's significant bits
+// (what is left is exact).  fp16: 11 + 11 bits, of 24 (weights below 2^-14
+// keep 2^-25 of the largest).  bf16: 8 + 8 + 8, the whole value.
+template <class T>
+struct Parts;
+template <>
+struct Parts<KvF16> {
+    static constexpr int kN = 2;
+    static __device__ __forceinline__ void split(float2 a, uint32_t* out) {
+        const float2 h = mask2(a, 0xffffe000u);
+        out[0] = KvF16::pack(h.x, h.y);
+        const float2 r = fma2(h, make_float2(-1.f, -1.f), a);
+        out[1] = KvF16::pack(r.x, r.y);
+    }
+};
+template <>
+struct Parts<KvBf16> {
+    static constexpr int kN = 3;
+    static __device__ __forceinline__ void split(float2 a, uint32_t* out) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            out[i] = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x7632u);
+            if (i < 2) a = fma2(mask2(a, 0xffff0000u), make_float2(-1.f, -1.f), a);
+        }
+    }
+};
+
 // Eight values of q, with the scale's sign.
 __device__ __forceinline__ uint4 load_q(const AttnParams& p, const uint16_t* src) {
     uint4 v = *reinterpret_cast<const uint4*>(src);

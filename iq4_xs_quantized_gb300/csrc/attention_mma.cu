@@ -68,15 +68,6 @@ __device__ __forceinline__ void mma16816<KvBf16>(float* c, const uint32_t* a, ui
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <class T>
-struct Parts {
-    static constexpr int kN = 2;
-};
-template <>
-struct Parts<KvBf16> {
-    static constexpr int kN = 3;
-};
-
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 static_assert(kConsumers * 32 == 128, "the consumers' barrier");
 
@@ -196,17 +187,25 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
         const int rows = min(kRowTile, w.w.tokens * p.group - w.row_tile * kRowTile);
         const int keys = w.w.len + w.w.tokens;
         // q of the item's rows; rows behind the last are zero
-        for (int u = threadIdx.x; u < kRowTile * (D / 8); u += 32 * kConsumers) {
+        constexpr int kQUnits = kRowTile * (D / 8) / (32 * kConsumers);
+        uint4 qv[kQUnits];
+#pragma unroll
+        for (int i = 0; i < kQUnits; ++i) {
+            const int u = threadIdx.x + i * 32 * kConsumers;
             const int r = u / (D / 8), col = u % (D / 8), row = w.row_tile * kRowTile + r;
-            uint4 v = make_uint4(0, 0, 0, 0);
+            qv[i] = make_uint4(0, 0, 0, 0);
             if (r < rows) {
                 const uint16_t* src = p.q + (w.w.row0 + row / p.group) * p.q_row_stride +
                                       ((int64_t)w.head * p.group + row % p.group) * D + col * 8;
                 if (bc_global(bc, src, 16, p.q,
                               2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D), kBcAttnQ))
-                    v = load_q(p, src);
+                    qv[i] = load_q(p, src);
             }
-            sts_u128(q_s + unit_at(r, col, kRowTile), v);
+        }
+#pragma unroll
+        for (int i = 0; i < kQUnits; ++i) {
+            const int u = threadIdx.x + i * 32 * kConsumers;
+            sts_u128(q_s + unit_at(u / (D / 8), u % (D / 8), kRowTile), qv[i]);
         }
         consumer_sync();
         uint32_t qf[C::kQInRegs ? D / 16 : 1][4];
@@ -361,18 +360,13 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
                     __syncwarp();
                     fence_proxy_async_smem();  // these writes come before the slot's next copy
                 }
-                uint32_t pf[Parts<T>::kN][4];
+                uint32_t pf[4][Parts<T>::kN], pn[Parts<T>::kN][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = i & 1, k = (i >> 1) * 2;
-                    float a0 = e[r][k], a1 = e[r][k + 1];
+                    Parts<T>::split(make_float2(e[r][k], e[r][k + 1]), pf[i]);
 #pragma unroll
-                    for (int n = 0; n < Parts<T>::kN; ++n) {
-                        pf[n][i] = T::pack(a0, a1);
-                        const float2 f = T::unpack(pf[n][i]);
-                        a0 -= f.x;
-                        a1 -= f.y;
-                    }
+                    for (int n = 0; n < Parts<T>::kN; ++n) pn[n][i] = pf[i][n];
                 }
                 const int vr = warp * kWarpKeys + (lane & 15);
 #pragma unroll
@@ -388,8 +382,8 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
                     for (int n = 0; n < 8; ++n) (&t[0][0])[n] = 0.f;
 #pragma unroll
                     for (int n = Parts<T>::kN - 1; n >= 0; --n) {
-                        mma16816<T>(t[0], pf[n], vf[0], vf[1]);
-                        mma16816<T>(t[1], pf[n], vf[2], vf[3]);
+                        mma16816<T>(t[0], pn[n], vf[0], vf[1]);
+                        mma16816<T>(t[1], pn[n], vf[2], vf[3]);
                     }
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {

@@ -3,7 +3,7 @@
 //
 // One pass, as in the warp-level form; here a row is a lane of tensor memory:
 //
-//   S = Q K^T      128 x 64, Q and K from shared memory (K-major)
+//   S = Q K^T      128 x 64, Q from tensor memory, K from shared memory
 //   P = exp2(S - m) split into 16-bit parts, back into tensor memory over S
 //   T = P V        128 x D, P from tensor memory, V from shared memory (as it
 //                  lies: channels contiguous)
@@ -36,34 +36,35 @@ constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kHalfKeys = kKeyTile / 2;
 constexpr int kTmemCols = 512;
 
-template <class T>
-struct TcParts {
-    static constexpr int kN = 2;
-};
-template <>
-struct TcParts<KvBf16> {
-    static constexpr int kN = 3;
-};
-
-template <int D>
+template <int D, class T>
 struct TcAttn {
+    static constexpr int kParts = Parts<T>::kN;
     static constexpr int kChunks = D / 64;
     static constexpr int kTileBytes = kKeyTile * D * 2;
-    static constexpr int kSlots = 160 * 1024 / kTileBytes;   // 5, 10, 20
-    static constexpr int kQBytes = kRowTile * D * 2;
+    static constexpr int kTBufs = D == 256 ? 1 : 2;          // output products in flight
+    // Tensor memory: T; Q (16-bit pairs), except where 512 columns do not
+    // hold it; two score buffers: S (64 columns), overlaid in place by P: the
+    // first two parts of 16 keys take the keys' own 16 columns, a third 8 more.
+    static constexpr int kScoreCols = kParts == 3 ? 96 : 64;
+    static constexpr bool kQInTmem = kTBufs * D + D / 2 + 2 * kScoreCols <= kTmemCols;
+    static constexpr int kQCol = kTBufs * D;
+    static constexpr int kScores = kQCol + (kQInTmem ? D / 2 : 0);
+    static_assert(kScores + 2 * kScoreCols <= kTmemCols, "tensor memory");
+    // shared memory
+    static constexpr int kQBytes = kQInTmem ? 0 : kRowTile * D * 2;
+    static constexpr int kSlots = (224 * 1024 - kQBytes) / kTileBytes;  // 7 (5 with Q), 14, 28
     static constexpr int kQ = kSlots * kTileBytes;
     static constexpr int kMax = kQ + kQBytes;                // [2][2 halves][128] row maxima
     static constexpr int kBars = kMax + 2 * 2 * kRowTile * 4;
     static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 1;
     static constexpr int kMisc = kBars + kNumBars * 8;       // tensor memory address, abort, odd values
     static constexpr int kSmem = kMisc + 16;
-    static constexpr int kTBufs = D == 256 ? 1 : 2;          // output products in flight
-    // tensor memory: T, then per score buffer 96 columns: S (64), overlaid by up to three parts of P (32 each)
-    static constexpr int kScoreCols = 96;
-    static constexpr int kScores = kTBufs * D;
-    static constexpr int kHalfD = D / 2;
-    static_assert(kScores + 2 * kScoreCols <= kTmemCols, "tensor memory");
     static_assert(kSmem <= 227 * 1024, "shared memory");
+    static constexpr int kHalfD = D / 2;
+    static constexpr int kHold = D == 256 ? 16 : 32;         // scores a thread holds at a time
+    static __device__ __forceinline__ uint32_t p_col(int key16, int part) {  // from the buffer's first column
+        return part < 2 ? 16 * key16 + 8 * part : kKeyTile + 8 * key16;
+    }
 };
 // D = 256 keeps 128 output channels a softmax thread: the producer's and the
 // issuer's warpgroup gives up registers (80 + 2 * 208 <= 3 * 168, the launch's).
@@ -86,14 +87,23 @@ constexpr uint32_t idesc_kv(int n, uint32_t type, bool b_mn) {
 __device__ __forceinline__ void pair_sync(int quadrant) {
     asm volatile("bar.sync %0, 64;" ::"r"(quadrant + 1) : "memory");
 }
-// o = o * f + t on two floats at a time.
-__device__ __forceinline__ void fma2(float2& o, float2 f, float2 t) {
-    uint64_t a, b, c;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(o.x), "f"(o.y));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(f.x), "f"(f.y));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(t.x), "f"(t.y));
-    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a) : "l"(b), "l"(c));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(a));
+// Largest of n values.
+template <int n>
+__device__ __forceinline__ float max_of(const uint32_t* x, float top) {
+#pragma unroll
+    for (int k = 0; k < n; k += 2)
+        asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(__uint_as_float(x[k])), "f"(__uint_as_float(x[k + 1])));
+    return top;
+}
+template <int n>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t at, uint32_t* x) {
+    if constexpr (n == 16) tmem_ld16_wait(at, x);
+    else tmem_ld32_wait(at, x);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 // Places in the ring of tile j's K and V, an item of n tiles starting at place 0.
 __device__ __forceinline__ int place_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
@@ -103,8 +113,8 @@ template <int D, class T>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                         const AttnParams p, const CacheView c, const BatchView b, int* err) {
-    using C = TcAttn<D>;
-    constexpr int kParts = TcParts<T>::kN;
+    using C = TcAttn<D, T>;
+    constexpr int kParts = C::kParts;
     constexpr uint32_t kType = kParts == 3 ? 1u : 0u;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
@@ -224,57 +234,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                         int no_abort = 0;
                         mbar_wait(full + i % C::kSlots, (i / C::kSlots) & 1, &no_abort, err, kDevErrTimeoutKv);
                     }
-        } else if (warp == 1) {
-            // -------------------------------------------------------- issuer
+        } else if (warp == 1 && elect_one()) {
+            // -------------------------------------------- issuer: one thread
             constexpr uint32_t kIdS = idesc_kv(kKeyTile, kType, false), kIdT = idesc_kv(D, kType, true);
-            const uint64_t q_desc = desc_sw128(base + C::kQ, 16, 1024);
             int place0 = 0, it = 0, items = 0;  // ring place and tile number at the item's start
             bool live = true;
             auto scores = [&](int j) {
                 const int place = place0 + place_k(j), st = place % C::kSlots, buf = (it + j) & 1;
-                live = live && warp_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
-                if (live && lane == 0) {
-                    tc_fence_after();
-                    const uint64_t k_desc = desc_sw128(base + st * C::kTileBytes, 16, 1024);
+                live = live && mbar_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
+                if (!live) return;
+                tc_fence_after();
+                const uint64_t k_desc = desc_sw128(base + st * C::kTileBytes, 16, 1024);
+                const uint32_t s_at = tmem + C::kScores + buf * C::kScoreCols;
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc_mma_f16(tmem + C::kScores + buf * C::kScoreCols,
-                                   q_desc + (((k / 4) * kRowTile * kChunkBytes + (k % 4) * 32) >> 4),
-                                   k_desc + (((k / 4) * kKeyTile * kChunkBytes + (k % 4) * 32) >> 4), kIdS, k > 0);
-                    tc_commit(s_full + buf);
-                    tc_commit(slot_free + st);
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t kd = k_desc + (((k / 4) * kKeyTile * kChunkBytes + (k % 4) * 32) >> 4);
+                    if constexpr (C::kQInTmem)
+                        tc_mma_f16_ta(s_at, tmem + C::kQCol + 8 * k, kd, kIdS, k > 0);
+                    else
+                        tc_mma_f16(s_at,
+                                   desc_sw128(base + C::kQ, 16, 1024) +
+                                       (((k / 4) * kRowTile * kChunkBytes + (k % 4) * 32) >> 4),
+                                   kd, kIdS, k > 0);
                 }
-                __syncwarp();
+                tc_commit(s_full + buf);
+                tc_commit(slot_free + st);
             };
             for (; live && w.valid(); w.next(p, b, g, kRowTile, err)) {
                 const int n = w.seen_tiles(p, kRowTile) - w.tile0;
                 if (n <= 0) continue;
-                live = warp_wait(q_full, items & 1, abort_flag, err, kDevErrTimeoutScore);
-                if (!live) break;
+                live = mbar_wait(q_full, items & 1, abort_flag, err, kDevErrTimeoutScore);
                 scores(0);
                 for (int j = 0; live && j < n; ++j) {
                     if (j + 1 < n) scores(j + 1);
                     const int place = place0 + place_v(j, n), st = place % C::kSlots;
                     const int i = it + j, buf = i & 1, tb = i % C::kTBufs;
-                    live = live && warp_wait(p_full + buf, (i >> 1) & 1, abort_flag, err, kDevErrTimeoutScore);
-                    live = live && warp_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
+                    live = live && mbar_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
                     if (i >= C::kTBufs)
-                        live = live && warp_wait(t_free + tb, (i / C::kTBufs - 1) & 1, abort_flag, err,
+                        live = live && mbar_wait(t_free + tb, (i / C::kTBufs - 1) & 1, abort_flag, err,
                                                  kDevErrTimeoutScore);
-                    if (live && lane == 0) {
-                        tc_fence_after();
-                        const uint64_t v_desc = desc_sw128(base + st * C::kTileBytes, kKeyTile * kChunkBytes, 1024);
+                    live = live && mbar_wait(p_full + buf, (i >> 1) & 1, abort_flag, err, kDevErrTimeoutScore);
+                    if (!live) break;
+                    tc_fence_after();
+                    const uint64_t v_desc = desc_sw128(base + st * C::kTileBytes, kKeyTile * kChunkBytes, 1024);
+                    const uint32_t p_at = tmem + C::kScores + buf * C::kScoreCols, t_at = tmem + tb * D;
 #pragma unroll
-                        for (int n2 = kParts - 1; n2 >= 0; --n2)  // the smallest parts first
+                    for (int part = kParts - 1; part >= 0; --part)  // the smallest parts first
 #pragma unroll
-                            for (int k = 0; k < kKeyTile / 16; ++k)
-                                tc_mma_f16_ta(tmem + tb * D,
-                                              tmem + C::kScores + buf * C::kScoreCols + n2 * (kKeyTile / 2) + k * 8,
-                                              v_desc + ((k * 16 * kChunkBytes) >> 4), kIdT, n2 < kParts - 1 || k > 0);
-                        tc_commit(t_full + tb);
-                        tc_commit(slot_free + st);
-                    }
-                    __syncwarp();
+                        for (int k = 0; k < kKeyTile / 16; ++k)
+                            tc_mma_f16_ta(t_at, p_at + C::p_col(k, part), v_desc + ((k * 16 * kChunkBytes) >> 4), kIdT,
+                                          part < kParts - 1 || k > 0);
+                    tc_commit(t_full + tb);
+                    tc_commit(slot_free + st);
                 }
                 place0 += 2 * n;
                 it += n;
@@ -282,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // Tensor memory is given back only when every product is done.
             if (*abort_flag) {
-                if (lane == 0) tc_commit(drained);
+                tc_commit(drained);
                 int no_abort = 0;
                 mbar_wait(drained, 0, &no_abort, err, kDevErrTimeoutScore);
             }
@@ -307,20 +318,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < C::kHalfD / 2; ++i) o[i] = make_float2(0.f, 0.f);
             float m = -INFINITY, l = 0.f, f_last = 1.f;
             if (n > 0) {
-                // q of the item's rows, all 256 threads; rows behind the last are zero
-                for (int u = st_id; u < kRowTile * (D / 8); u += kSoftThreads) {
-                    const int qr = u / (D / 8), col = u % (D / 8), row = w.row_tile * kRowTile + qr;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (qr < rows) {
-                        const uint16_t* src = p.q + (w.w.row0 + row / p.group) * p.q_row_stride +
-                                              ((int64_t)w.head * p.group + row % p.group) * D + col * 8;
-                        if (bc_global(bc, src, 16, p.q,
-                                      2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D), kBcAttnQ))
-                            v = load_q(p, src);
+                // Q of the item's rows: each thread its row's half of the
+                // channels.  Rows behind the last are zero.
+                const uint16_t* src = p.q + (w.w.row0 + tok) * p.q_row_stride +
+                                      ((int64_t)w.head * p.group + my_row % p.group) * D + half * C::kHalfD;
+                const bool ok = r < rows &&
+                                bc_global(bc, src, 2 * C::kHalfD, p.q,
+                                          2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D),
+                                          kBcAttnQ);
+                uint4 v[C::kHalfD / 8];
+#pragma unroll
+                for (int i = 0; i < C::kHalfD / 8; ++i)
+                    v[i] = ok ? load_q(p, src + 8 * i) : make_uint4(0, 0, 0, 0);
+                if constexpr (C::kQInTmem) {
+                    if (busy) {
+#pragma unroll
+                        for (int i = 0; i < C::kHalfD / 32; ++i)
+                            tmem_st16(tmem + lane_at + C::kQCol + half * (C::kHalfD / 2) + 16 * i,
+                                      reinterpret_cast<const uint32_t*>(v + 4 * i));
+                        tmem_wait_st();
+                        tc_fence_before();
                     }
-                    sts_u128(base + C::kQ + unit_at(qr, col, kRowTile), v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < C::kHalfD / 8; ++i)
+                        sts_u128(base + C::kQ + unit_at(r, half * (C::kHalfD / 8) + i, kRowTile), v[i]);
+                    fence_proxy_async_smem();
                 }
-                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full);
             }
@@ -337,8 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld32_wait(tmem + lane_at + tb * D + half * C::kHalfD + 32 * k, t);
 #pragma unroll
                         for (int x = 0; x < 16; ++x)
-                            fma2(o[16 * k + x], f2,
-                                 make_float2(__uint_as_float(t[2 * x]), __uint_as_float(t[2 * x + 1])));
+                            o[16 * k + x] = fma2(o[16 * k + x], f2,
+                                                 make_float2(__uint_as_float(t[2 * x]), __uint_as_float(t[2 * x + 1])));
                     }
                     tc_fence_before();
                 }
@@ -353,57 +377,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (busy) {
                     tc_fence_after();
                     const uint32_t s_at = tmem + lane_at + C::kScores + buf * C::kScoreCols;
-                    uint32_t x[32];
-                    tmem_ld32_wait(s_at + half * kHalfKeys, x);
-                    tc_fence_before();
+                    const uint32_t my_s = s_at + half * kHalfKeys;
+                    constexpr int kHold = C::kHold;
+                    uint32_t x[kHold];
+                    uint32_t seen = 0xffffffffu;  // bit k: the row sees key0 + k
                     const int have = keys - key0;  // positions before the end
-                    if (key0 + kHalfKeys > w.w.len || have < kHalfKeys) {
-                        const uint32_t seen = seen_bits(p, w.w.row0 + tok, tok, key0 - w.w.len, have);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (!(seen >> k & 1)) x[k] = 0xff800000u;  // -inf
-                    }
+                    if (key0 + kHalfKeys > w.w.len || have < kHalfKeys)
+                        seen = seen_bits(p, w.w.row0 + tok, tok, key0 - w.w.len, have);
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2)
-                        mx = fmaxf(mx, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+                    for (int h = 0; h < kHalfKeys; h += kHold) {
+                        tmem_ld_wait<kHold>(my_s + h, x);
+                        if (seen != 0xffffffffu) {
+#pragma unroll
+                            for (int k = 0; k < kHold; ++k)
+                                if (!(seen >> (h + k) & 1)) x[k] = 0xff800000u;  // -inf
+                        }
+                        mx = max_of<kHold>(x, mx);
+                    }
                     float* mine = maxima + buf * 2 * kRowTile;
                     mine[half * kRowTile + r] = mx;
-                    pair_sync(quad);  // also: both halves have read S, which P is about to overwrite
-                    mx = fmaxf(mx, mine[(half ^ 1) * kRowTile + r]);
-                    mx *= p.scale_log2;  // (the scale is positive)
+                    pair_sync(quad);
+                    mx = fmaxf(mx, mine[(half ^ 1) * kRowTile + r]) * p.scale_log2;  // (the scale is positive)
                     if (mx > m + kLazy) {
                         f = fast_exp2(m - mx);
                         m = mx;
                         l *= f;
                     }
                     const float shift = m == -INFINITY ? 0.f : kWeightBits - m;
-                    float l2 = 0.f;
+                    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), shift2 = make_float2(shift, shift);
+                    float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int h2 = 0; h2 < 2; ++h2) {  // 16 keys at a time: 8 columns a part
+                    for (int h = 0; h < kHalfKeys; h += 16) {  // 16 keys at a time, over their own columns
+                        if constexpr (kHold == 16) {
+                            tmem_ld_wait<16>(my_s + h, x);
+                            if (seen != 0xffffffffu) {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    if (!(seen >> (h + k) & 1)) x[k] = 0xff800000u;
+                            }
+                        }
                         uint32_t part[kParts][8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            float a0 = fast_exp2(fmaf(__uint_as_float(x[16 * h2 + 2 * k]), p.scale_log2, shift));
-                            float a1 = fast_exp2(fmaf(__uint_as_float(x[16 * h2 + 2 * k + 1]), p.scale_log2, shift));
-                            l2 += a0 + a1;
+                            const uint32_t* xk = x + (kHold == 16 ? 0 : h) + 2 * k;
+                            float2 a = fma2(make_float2(__uint_as_float(xk[0]), __uint_as_float(xk[1])), scale2, shift2);
+                            a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+                            l2 = add2(l2, a);
+                            uint32_t out[kParts];
+                            Parts<T>::split(a, out);
 #pragma unroll
-                            for (int n2 = 0; n2 < kParts; ++n2) {
-                                part[n2][k] = T::pack(a0, a1);
-                                const float2 t = T::unpack(part[n2][k]);
-                                a0 -= t.x;
-                                a1 -= t.y;
-                            }
+                            for (int n2 = 0; n2 < kParts; ++n2) part[n2][k] = out[n2];
                         }
 #pragma unroll
                         for (int n2 = 0; n2 < kParts; ++n2)
-                            asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
-                                             s_at + n2 * (kKeyTile / 2) + half * (kHalfKeys / 2) + 8 * h2),
-                                         "r"(part[n2][0]), "r"(part[n2][1]), "r"(part[n2][2]), "r"(part[n2][3]),
-                                         "r"(part[n2][4]), "r"(part[n2][5]), "r"(part[n2][6]), "r"(part[n2][7])
-                                         : "memory");
+                            tmem_st8(s_at + C::p_col(half * (kHalfKeys / 16) + h / 16, n2), part[n2]);
                     }
-                    l += l2;
+                    l += l2.x + l2.y;
                     tmem_wait_st();
                     tc_fence_before();
                 }
@@ -507,9 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, class T>
 cudaError_t launch_one(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const CacheView& c,
                        const BatchView& b, int* err, cudaStream_t stream) {
-    const cudaError_t e = allow_smem<attention_tc_kernel<D, T>>(TcAttn<D>::kSmem);
+    const cudaError_t e = allow_smem<attention_tc_kernel<D, T>>(TcAttn<D, T>::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_chained(attention_tc_kernel<D, T>, dim3((unsigned)p.ctas), dim3(kThreads), TcAttn<D>::kSmem, stream,
+    return launch_chained(attention_tc_kernel<D, T>, dim3((unsigned)p.ctas), dim3(kThreads), TcAttn<D, T>::kSmem, stream,
                           tk, tv, p, c, b, err);
 }
 
