@@ -202,9 +202,18 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without building a Stream object (2.9 us a call
+# on a GB300's host, against 0.2 us); CUDA is up by then: the caller holds
+# device tensors.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None or _raw_device is None or not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_raw_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -426,8 +435,10 @@ def _need(ok, fn: str, what: str, err=ValueError):
 
 def _need_i32(fn: str, **tensors):
     for name, t in tensors.items():
-        _need(t.dtype == torch.int32, fn, f"{name} must be int32", TypeError)
-        _need(t.is_contiguous(), fn, f"{name} must be contiguous")
+        if t.dtype is not torch.int32:
+            raise TypeError(f"{fn}: {name} must be int32")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous")
 
 
 class KVCache:
@@ -494,29 +505,30 @@ def iq4xs_qk_norm_rope(q, k, v, q_weight, k_weight, eps: float, rope, positions,
     2] = (cos, sin) at positions int32 [M] (None: the rows' own positions)."""
     fn = "iq4xs_qk_norm_rope"
     M, hq, D = q.shape
-    _need(q.dtype == torch.float32 and k.dtype == torch.float32 and v.dtype == torch.float32, fn,
-          "q, k and v must be float32", TypeError)
-    _need(q_out.dtype == cache.dtype, fn, "q_out must have the cache's type", TypeError)
-    _need(D == cache.head_dim and k.shape == (M, cache.heads, D) and v.shape == k.shape and q_out.shape == q.shape,
-          fn, "q [M, Hq, D], k and v [M, Hkv, D], q_out as q")
-    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), q_out.stride()
-    _need(qs[2] == 1 and ks[2] == 1 and vs[2] == 1 and os_[2] == 1 and (os_[1] == D or hq == 1), fn,
-          "channels must be contiguous (heads too in q_out)")
+    hkv, n_pos, rot, f32 = cache.heads, 0, 0, torch.float32
+    if not (q.dtype is f32 and k.dtype is f32 and v.dtype is f32):
+        raise TypeError(f"{fn}: q, k and v must be float32")
+    if q_out.dtype is not cache.dtype:
+        raise TypeError(f"{fn}: q_out must have the cache's type")
+    if not (D == cache.head_dim and k.shape == (M, hkv, D) and v.shape == (M, hkv, D) and q_out.shape == (M, hq, D)):
+        raise ValueError(f"{fn}: q [M, Hq, D], k and v [M, Hkv, D], q_out as q")
+    (qr, qh, qc), (kr, kh, kc), (vr, vh, vc), (outr, outh, outc) = q.stride(), k.stride(), v.stride(), q_out.stride()
+    if not (qc == 1 and kc == 1 and vc == 1 and outc == 1 and (outh == D or hq == 1)):
+        raise ValueError(f"{fn}: channels must be contiguous (heads too in q_out)")
     for w in (q_weight, k_weight):
-        _need(w is None or (w.dtype == torch.float32 and w.numel() == D and w.is_contiguous()), fn,
-              "weights are float32 [D]")
-    n_pos = rot = 0
+        if w is not None and not (w.dtype is f32 and w.shape == (D,) and w.stride() == (1,)):
+            raise ValueError(f"{fn}: weights are float32 [D]")
     if rope is not None:
-        _need(rope.dtype == torch.float32 and rope.dim() == 3 and rope.shape[2] == 2 and rope.is_contiguous(), fn,
-              "rope is float32 [positions, rot / 2, 2]")
+        if not (rope.dtype is f32 and rope.dim() == 3 and rope.shape[2] == 2 and rope.is_contiguous()):
+            raise ValueError(f"{fn}: rope is float32 [positions, rot / 2, 2]")
         n_pos, rot = rope.shape[0], 2 * rope.shape[1]
-    if positions is not None:
-        _need(positions.dtype == torch.int32 and positions.numel() == M and positions.is_contiguous(), fn,
-              "positions is int32 [M]")
-    args = _QK_ARGS(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
-                    _addr(q_weight), _addr(k_weight), eps, _addr(rope), n_pos, rot, 1 if interleaved else 0,
-                    _addr(positions), q_out.data_ptr(), os_[0] if M > 1 else hq * D, M, hq, layer)
-    rc = load().iq4xs_qk_norm_rope(args, cache.desc, batch.desc, _stream(stream))
+    if positions is not None and not (positions.dtype is torch.int32 and positions.shape == (M,) and
+                                      positions.is_contiguous()):
+        raise ValueError(f"{fn}: positions is int32 [M]")
+    args = _QK_ARGS(q.data_ptr(), k.data_ptr(), v.data_ptr(), qr, qh, kr, kh, vr, vh, _addr(q_weight),
+                    _addr(k_weight), eps, _addr(rope), n_pos, rot, 1 if interleaved else 0, _addr(positions),
+                    q_out.data_ptr(), outr if M > 1 else hq * D, M, hq, layer)
+    rc = (_lib or load()).iq4xs_qk_norm_rope(args, cache.desc, batch.desc, _stream(stream))
     if rc:
         _check(fn, rc)
 
@@ -535,22 +547,25 @@ def iq4xs_tree_attention(q, cache: KVCache, layer: int, batch: KVBatch, scale: f
     a chain).  workspace: uint8, iq4xs_tree_attention_workspace_bytes(...)."""
     fn = "iq4xs_tree_attention"
     M, hq, D = q.shape
-    _need(q.dtype == cache.dtype, fn, "q must have the cache's type", TypeError)
-    _need(out.dtype == torch.float32, fn, "out must be float32", TypeError)
-    qs, os_ = q.stride(), out.stride()
-    _need(D == cache.head_dim and qs[2] == 1 and (qs[1] == D or hq == 1), fn,
-          "q is [M, Hq, D], heads and channels contiguous")
-    _need(out.shape == (M, hq * D) and os_[1] == 1, fn, "out is [M, Hq * D]")
+    if q.dtype is not cache.dtype:
+        raise TypeError(f"{fn}: q must have the cache's type")
+    if out.dtype is not torch.float32:
+        raise TypeError(f"{fn}: out must be float32")
+    (qr, qh, qc), (outr, outc) = q.stride(), out.stride()
+    if not (D == cache.head_dim and qc == 1 and (qh == D or hq == 1)):
+        raise ValueError(f"{fn}: q is [M, Hq, D], heads and channels contiguous")
+    if not (out.shape == (M, hq * D) and outc == 1):
+        raise ValueError(f"{fn}: out is [M, Hq * D]")
     words = 0
     if tree_mask is not None:
-        _need(tree_mask.dtype in (torch.int64, torch.uint64), fn, "tree_mask must be int64", TypeError)
-        _need(tree_mask.dim() == 2 and tree_mask.shape[0] == M and tree_mask.is_contiguous(), fn,
-              "tree_mask is [M, words]")
+        if tree_mask.dtype not in (torch.int64, torch.uint64):
+            raise TypeError(f"{fn}: tree_mask must be int64")
+        if not (tree_mask.dim() == 2 and tree_mask.shape[0] == M and tree_mask.is_contiguous()):
+            raise ValueError(f"{fn}: tree_mask is [M, words]")
         words = tree_mask.shape[1]
-    args = _ATTN_ARGS(q.data_ptr(), qs[0] if M > 1 else hq * D, out.data_ptr(), os_[0] if M > 1 else hq * D, M, hq,
-                      layer, scale, _addr(tree_mask), words, workspace.data_ptr(),
-                      workspace.numel() * workspace.element_size())
-    rc = load().iq4xs_tree_attention(args, cache.desc, batch.desc, _stream(stream))
+    args = _ATTN_ARGS(q.data_ptr(), qr if M > 1 else hq * D, out.data_ptr(), outr if M > 1 else hq * D, M, hq, layer,
+                      scale, _addr(tree_mask), words, workspace.data_ptr(), workspace.nbytes)
+    rc = (_lib or load()).iq4xs_tree_attention(args, cache.desc, batch.desc, _stream(stream))
     if rc:
         _check(fn, rc)
 
@@ -562,7 +577,7 @@ def iq4xs_cache_reserve(batch: KVBatch, page_size: int, refs, status, stream=Non
     fn = "iq4xs_cache_reserve"
     _need_i32(fn, refs=refs, status=status)
     _need(status.numel() == batch.sequences, fn, "status is int32 [B]")
-    rc = load().iq4xs_cache_reserve(batch.desc, page_size, refs.data_ptr(), refs.numel(), status.data_ptr(),
+    rc = (_lib or load()).iq4xs_cache_reserve(batch.desc, page_size, refs.data_ptr(), refs.numel(), status.data_ptr(),
                                     _stream(stream))
     if rc:
         _check(fn, rc)
@@ -578,7 +593,7 @@ def iq4xs_cache_commit(cache: KVCache, batch: KVBatch, refs, paths, accepted, ne
     _need(refs.numel() == cache.pages, fn, "refs is int32 [pages]")
     _need(paths.dim() == 2 and paths.shape[0] == batch.sequences and accepted.numel() == batch.sequences and
           new_lens.numel() == batch.sequences, fn, "paths [B, width], accepted [B], new_lens [B]")
-    rc = load().iq4xs_cache_commit(cache.desc, batch.desc, refs.data_ptr(), paths.data_ptr(), paths.shape[1],
+    rc = (_lib or load()).iq4xs_cache_commit(cache.desc, batch.desc, refs.data_ptr(), paths.data_ptr(), paths.shape[1],
                                    accepted.data_ptr(), new_lens.data_ptr(), _stream(stream))
     if rc:
         _check(fn, rc)
@@ -592,7 +607,7 @@ def iq4xs_cache_fork(cache: KVCache, batch: KVBatch, refs, parents, children, st
     n = parents.numel()
     _need(refs.numel() == cache.pages, fn, "refs is int32 [pages]")
     _need(children.numel() == n and status.numel() == n, fn, "parents, children and status are of one length")
-    rc = load().iq4xs_cache_fork(cache.desc, batch.desc, refs.data_ptr(), parents.data_ptr(), children.data_ptr(), n,
+    rc = (_lib or load()).iq4xs_cache_fork(cache.desc, batch.desc, refs.data_ptr(), parents.data_ptr(), children.data_ptr(), n,
                                  status.data_ptr(), _stream(stream))
     if rc:
         _check(fn, rc)
@@ -602,7 +617,7 @@ def iq4xs_cache_release(batch: KVBatch, refs, rows, stream=None) -> None:
     """Sequences ``rows`` end: their pages' references fall, lens and held become 0."""
     fn = "iq4xs_cache_release"
     _need_i32(fn, refs=refs, rows=rows)
-    rc = load().iq4xs_cache_release(batch.desc, refs.data_ptr(), refs.numel(), rows.data_ptr(), rows.numel(),
+    rc = (_lib or load()).iq4xs_cache_release(batch.desc, refs.data_ptr(), refs.numel(), rows.data_ptr(), rows.numel(),
                                     _stream(stream))
     if rc:
         _check(fn, rc)
@@ -613,7 +628,7 @@ def iq4xs_cache_copy_pages(cache: KVCache, src, dst, stream=None) -> None:
     fn = "iq4xs_cache_copy_pages"
     _need_i32(fn, src=src, dst=dst)
     _need(src.numel() == dst.numel(), fn, "src and dst are of one length")
-    rc = load().iq4xs_cache_copy_pages(cache.desc, src.data_ptr(), dst.data_ptr(), src.numel(), _stream(stream))
+    rc = (_lib or load()).iq4xs_cache_copy_pages(cache.desc, src.data_ptr(), dst.data_ptr(), src.numel(), _stream(stream))
     if rc:
         _check(fn, rc)
 

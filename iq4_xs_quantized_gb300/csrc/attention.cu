@@ -41,9 +41,9 @@ bool encode_kv(EncodeTiledFn enc, uint16_t* base, const CacheView& c, bool bf16,
 // take every fourth part and add up in shared memory, in a fixed order.
 constexpr int kJoinWarps = 4;
 
-template <int D>
+template <int D, int kRows>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-    attention_join_kernel(const AttnParams p, const BatchView b, int row_tile, int* err) {
+    attention_join_kernel(const AttnParams p, const BatchView b, int* err) {
     constexpr int kPer = D / 32;
     __shared__ float acc_s[kJoinWarps][D];
     // The attention kernel lets this grid start only behind its own wait for
@@ -61,17 +61,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     bool cut = s < b.sequences && row >= b.row_offsets[0];
     int first = 0, last = 0, r = 0;
     if (cut) {
-        const SeqWork w = seq_work(p, b, s, row_tile, err);
-        const int64_t work = work_before(p, b, b.sequences, row_tile, err);
+        const SeqWork w = seq_work<kRows>(p, b, s, err);
+        const Split split(p, work_before<kRows>(p, b, b.sequences, err));
         cut = w.work > 0 && row >= w.row0;
         if (cut) {
-            const int ctas = working_ctas(p, work);
             r = (row - w.row0) * p.group + head % p.group;
-            const int64_t x = work_before(p, b, s, row_tile, err) +
-                              ((int64_t)(head / p.group) * w.row_tiles + r / row_tile) * w.key_tiles;
-            r %= row_tile;
-            first = range_owner(work, ctas, x);
-            last = range_owner(work, ctas, x + w.key_tiles - 1);
+            const int64_t x = work_before<kRows>(p, b, s, err) +
+                              ((int64_t)(head / p.group) * w.row_tiles + r / kRows) * w.key_tiles;
+            r %= kRows;
+            first = split.owner(x);
+            last = split.owner(x + w.key_tiles - 1);
             cut = first != last;
         }
     }
@@ -119,13 +118,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     }
 }
 
-cudaError_t launch_join(const AttnParams& p, const BatchView& b, int row_tile, int q_heads, int* err,
-                        cudaStream_t stream) {
+template <int kRows>
+cudaError_t launch_join(const AttnParams& p, const BatchView& b, int q_heads, int* err, cudaStream_t stream) {
     const dim3 grid((unsigned)p.rows, (unsigned)q_heads), block(32 * kJoinWarps);
     switch (p.head_dim) {
-        case 64: return launch_chained(attention_join_kernel<64>, grid, block, 0, stream, p, b, row_tile, err);
-        case 128: return launch_chained(attention_join_kernel<128>, grid, block, 0, stream, p, b, row_tile, err);
-        case 256: return launch_chained(attention_join_kernel<256>, grid, block, 0, stream, p, b, row_tile, err);
+        case 64: return launch_chained(attention_join_kernel<64, kRows>, grid, block, 0, stream, p, b, err);
+        case 128: return launch_chained(attention_join_kernel<128, kRows>, grid, block, 0, stream, p, b, err);
+        case 256: return launch_chained(attention_join_kernel<256, kRows>, grid, block, 0, stream, p, b, err);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -184,7 +183,8 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     const cudaError_t e = tc ? launch_attention_tc(p, &tk, &tv, c, b, bf16, err, stream)
                              : launch_attention_mma(p, &tk, &tv, c, b, bf16, err, stream);
     if (e != cudaSuccess || p.whole_items) return e;
-    return launch_join(p, b, row_tile, (int)a.q_heads, err, stream);
+    return tc ? launch_join<kTcRows>(p, b, (int)a.q_heads, err, stream)
+              : launch_join<kMmaRows>(p, b, (int)a.q_heads, err, stream);
 }
 
 }  // namespace iq4xs

@@ -6,9 +6,8 @@
 // sequence's new tokens times the query heads that share the key/value head
 // (row r: token r / group, query head head * group + r % group), tiled by the
 // kernel's row tile; its keys come in tiles of kKeyTile positions.  The
-// (item, key tile) pairs of the whole batch lie on one line, and CTA g of G
-// takes [g W / G, (g + 1) W / G): every CTA the same number of key tiles,
-// whatever the lengths.  An item that a boundary cuts is joined afterwards:
+// (item, key tile) pairs of the whole batch lie on one line, of which every
+// CTA takes the same number of places, whatever the lengths.  An item that a boundary cuts is joined afterwards:
 // each CTA leaves at most two partial results, slot 2 g for the item whose
 // start lies before its range, 2 g + 1 for the one that it begins and does
 // not finish.  Where no sequence can be long (the table's width says so),
@@ -49,65 +48,90 @@ struct SeqWork {
     int unit;      // places an item takes on the line: key_tiles, or 1
 };
 
-__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, const BatchView& b, int s, int row_tile, int* err) {
+// From the sequence's row offsets and length as they were read.
+template <int kRows>
+__device__ __forceinline__ SeqWork seq_of(const AttnParams& p, int first, int last, int len, int* err) {
     SeqWork w;
-    w.tokens = batch_rows(b, s, p.rows, &w.row0, err);
-    w.len = batch_len(b, s, err);
-    if (w.len < 0 || w.len > (INT32_MAX >> 1)) w.tokens = 0;
-    w.row_tiles = (w.tokens * p.group + row_tile - 1) / row_tile;
+    w.row0 = first;
+    w.tokens = last - first;
+    w.len = len;
+    if (first < 0 || last < first || last > p.rows) {
+        data_error(err, kDataOffsets);
+        w.tokens = 0;
+    }
+    if (len < 0 || len > (INT32_MAX >> 1)) {
+        data_error(err, kDataLens);
+        w.tokens = w.len = 0;
+    }
+    w.row_tiles = (w.tokens * p.group + kRows - 1) / kRows;
     w.key_tiles = (w.len + w.tokens + kKeyTile - 1) / kKeyTile;
     w.unit = p.whole_items ? 1 : w.key_tiles;
     w.work = w.tokens > 0 ? (int64_t)w.row_tiles * p.kv_heads * w.unit : 0;
     return w;
 }
+template <int kRows>
+__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, const BatchView& b, int s, int* err) {
+    return seq_of<kRows>(p, b.row_offsets[s], b.row_offsets[s + 1], b.lens[s], err);
+}
 
 // The batch's work up to (not including) sequence n: 32 sequences a step, one
 // a lane; the result is the same in every lane.
-__device__ __forceinline__ int64_t work_before(const AttnParams& p, const BatchView& b, int n, int row_tile,
-                                               int* err) {
+template <int kRows>
+__device__ __forceinline__ int64_t work_before(const AttnParams& p, const BatchView& b, int n, int* err) {
     const int lane = threadIdx.x & 31;
     int64_t sum = 0;
     for (int s0 = 0; s0 < n; s0 += 32)
-        if (s0 + lane < n) sum += seq_work(p, b, s0 + lane, row_tile, err).work;
+        if (s0 + lane < n) sum += seq_work<kRows>(p, b, s0 + lane, err).work;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
 }
 
-// CTAs that get work: no more than places, so that no range is empty.
-__device__ __forceinline__ int working_ctas(const AttnParams& p, int64_t work) {
-    return (int)min((int64_t)p.ctas, work);
+// a / b for a that mostly fits 32 bits (a 64-bit division costs ten times one of 32).
+__device__ __forceinline__ int64_t div_small(int64_t a, int b) {
+    return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
-__device__ __forceinline__ int64_t range_start(int64_t work, int ctas, int g) { return work * g / ctas; }
-// The CTA whose range holds place x.
-__device__ __forceinline__ int range_owner(int64_t work, int ctas, int64_t x) {
-    return (int)(((x + 1) * ctas - 1) / work);
-}
+// The split of W places over G CTAs: every CTA W / G of them, the first W % G
+// one more.  No more CTAs than places, so that no range is empty.
+struct Split {
+    int64_t each, more;  // W / G, W % G
+    int ctas;
+    __device__ __forceinline__ Split(const AttnParams& p, int64_t work) {
+        ctas = (int)min((int64_t)p.ctas, work);
+        each = ctas > 0 ? div_small(work, ctas) : 0;
+        more = work - each * ctas;
+    }
+    __device__ __forceinline__ int64_t start(int g) const { return each * g + min((int64_t)g, more); }
+    __device__ __forceinline__ int owner(int64_t x) const {
+        const int64_t in_more = more * (each + 1);
+        return x < in_more ? (int)(x / (each + 1)) : (int)(more + (x - in_more) / each);
+    }
+};
 
 // A CTA's walk over its range, item by item.
+template <int kRows>
 struct WorkWalk {
-    int64_t x, end;      // place on the line, end of the range
-    int64_t seq_x;       // place at which sequence s starts
+    int64_t left;        // places of the range from the current item's part on
     SeqWork w;
     int s;
+    int row_end, next_end, next_len;  // offsets and length behind the sequence, read ahead
     // the current item's part
     int head, row_tile, tile0, tile1;
     bool whole;          // this CTA has all of the item's key tiles
     int slot;            // of its partial result, if not
 
-    __device__ __forceinline__ void start(const AttnParams& p, const BatchView& b, int g, int rt, int* err) {
-        const int64_t work = work_before(p, b, b.sequences, rt, err);
-        const int ctas = working_ctas(p, work);
-        s = -1;
-        x = end = 0;
-        if (g >= ctas) return;
-        x = range_start(work, ctas, g);
-        end = range_start(work, ctas, g + 1);
-        // the sequence that holds x: the last one that starts at or before it
+    __device__ __forceinline__ void start(const AttnParams& p, const BatchView& b, int g, int* err) {
+        const Split split(p, work_before<kRows>(p, b, b.sequences, err));
+        left = 0;
+        if (g >= split.ctas) return;
+        const int64_t x = split.start(g);
+        left = split.start(g + 1) - x;
+        // the sequence that holds x: the first whose end lies behind it
         const int lane = threadIdx.x & 31;
-        int64_t before = 0;
+        int64_t before = 0, seq_x = 0;
+        s = 0;
         for (int s0 = 0; s0 < b.sequences; s0 += 32) {
-            int64_t v = s0 + lane < b.sequences ? seq_work(p, b, s0 + lane, rt, err).work : 0;
+            int64_t v = s0 + lane < b.sequences ? seq_work<kRows>(p, b, s0 + lane, err).work : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
@@ -123,35 +147,51 @@ struct WorkWalk {
             }
             before += __shfl_sync(0xffffffffu, v, 31);
         }
-        w = seq_work(p, b, s, rt, err);
-        set(p, g);
-    }
-    __device__ __forceinline__ void set(const AttnParams& p, int g) {
-        const int64_t o = x - seq_x;
-        const int item = (int)(o / w.unit);
-        tile0 = (int)(o - (int64_t)item * w.unit);
-        tile1 = p.whole_items ? w.key_tiles : (int)min((int64_t)w.key_tiles, tile0 + (end - x));
+        row_end = b.row_offsets[s + 1];
+        w = seq_of<kRows>(p, b.row_offsets[s], row_end, b.lens[s], err);
+        read_ahead(b);
+        const int item = (int)div_small(x - seq_x, w.unit);
+        tile0 = (int)(x - seq_x - (int64_t)item * w.unit);
         head = item / w.row_tiles;
         row_tile = item - head * w.row_tiles;
+        set(p, g);
+    }
+    __device__ __forceinline__ void read_ahead(const BatchView& b) {
+        if (s + 1 < b.sequences) {
+            next_end = b.row_offsets[s + 2];
+            next_len = b.lens[s + 1];
+        }
+    }
+    __device__ __forceinline__ void set(const AttnParams& p, int g) {
+        tile1 = p.whole_items ? w.key_tiles : (int)min((int64_t)w.key_tiles, tile0 + left);
         whole = tile0 == 0 && tile1 == w.key_tiles;
         slot = 2 * g + (tile0 == 0 ? 1 : 0);
     }
-    __device__ __forceinline__ bool valid() const { return x < end; }
-    __device__ __forceinline__ void next(const AttnParams& p, const BatchView& b, int g, int rt, int* err) {
-        x += p.whole_items ? 1 : tile1 - tile0;
-        if (x >= end) return;
-        while (x - seq_x >= w.work) {  // (sequences without work are passed over)
-            seq_x += w.work;
-            w = seq_work(p, b, ++s, rt, err);
+    __device__ __forceinline__ bool valid() const { return left > 0; }
+    __device__ __forceinline__ void next(const AttnParams& p, const BatchView& b, int g, int* err) {
+        left -= p.whole_items ? 1 : tile1 - tile0;
+        if (left <= 0) return;
+        tile0 = 0;
+        if (++row_tile == w.row_tiles) {
+            row_tile = 0;
+            if (++head == p.kv_heads) {
+                head = 0;
+                do {  // (sequences without work are passed over)
+                    ++s;
+                    w = seq_of<kRows>(p, row_end, next_end, next_len, err);
+                    row_end = next_end;
+                    read_ahead(b);
+                } while (w.work == 0);
+            }
         }
         set(p, g);
     }
     // Key tiles that a row of this item can see: without a mask (a chain) the
     // row tile's last token ends them.
-    __device__ __forceinline__ int seen_tiles(const AttnParams& p, int rt) const {
+    __device__ __forceinline__ int seen_tiles(const AttnParams& p) const {
         int keys = w.len + w.tokens;
         if (p.mask == nullptr) {
-            const int last = min(w.tokens - 1, ((row_tile + 1) * rt - 1) / p.group);
+            const int last = min(w.tokens - 1, ((row_tile + 1) * kRows - 1) / p.group);
             keys = w.len + last + 1;
         }
         return min(tile1, (keys + kKeyTile - 1) / kKeyTile);

@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
     __syncthreads();
     griddep_wait();  // lengths, tables, q and the cache's newest rows come from earlier launches
     griddep_launch_dependents();
-    WorkWalk w;
-    w.start(p, b, g, kRowTile, err);
+    WorkWalk<kRowTile> w;
+    w.start(p, b, g, err);
 
     if (warp == kConsumers) {
         // ---------------------------------------------------------- producer
@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
         const uint32_t box_bytes = box_slots * kChunkBytes;
         int it = 0;
         bool live = true;
-        for (; live && w.valid(); w.next(p, b, g, kRowTile, err)) {
-            const int end = w.seen_tiles(p, kRowTile);
+        for (; live && w.valid(); w.next(p, b, g, err)) {
+            const int end = w.seen_tiles(p);
             const int keys = w.w.len + w.w.tokens;
             const int held = min(b.held[w.s], b.table_width);
             const int32_t* table = b.page_table + w.s * b.table_stride;
@@ -182,8 +182,8 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
     float2* ml = reinterpret_cast<float2*>(smem + C::kMl);
     const int rg = lane >> 2, ct = lane & 3;  // fragment row and column pair
     int it = 0;
-    for (; w.valid(); w.next(p, b, g, kRowTile, err)) {
-        const int end = w.seen_tiles(p, kRowTile);
+    for (; w.valid(); w.next(p, b, g, err)) {
+        const int end = w.seen_tiles(p);
         const int rows = min(kRowTile, w.w.tokens * p.group - w.row_tile * kRowTile);
         const int keys = w.w.len + w.w.tokens;
         // q of the item's rows; rows behind the last are zero

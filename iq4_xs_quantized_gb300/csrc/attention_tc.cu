@@ -35,6 +35,7 @@ constexpr int kThreads = 32 * (kFirstSoft + kSoftWarps);
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kHalfKeys = kKeyTile / 2;
 constexpr int kTmemCols = 512;
+constexpr int kStageCols = 16, kStageRow = kStageCols + 4;  // floats of a row on its way out, and its pitch
 
 template <int D, class T>
 struct TcAttn {
@@ -52,9 +53,11 @@ struct TcAttn {
     static_assert(kScores + 2 * kScoreCols <= kTmemCols, "tensor memory");
     // shared memory
     static constexpr int kQBytes = kQInTmem ? 0 : kRowTile * D * 2;
-    static constexpr int kSlots = (224 * 1024 - kQBytes) / kTileBytes;  // 7 (5 with Q), 14, 28
+    static constexpr int kStageBytes = kSoftWarps * 32 * kStageRow * 4;
+    static constexpr int kSlots = (224 * 1024 - kQBytes - kStageBytes) / kTileBytes;  // 6 (4 with Q), 12, 25
     static constexpr int kQ = kSlots * kTileBytes;
-    static constexpr int kMax = kQ + kQBytes;                // [2][2 halves][128] row maxima
+    static constexpr int kOut = kQ + kQBytes;                // the warps' outputs on their way out
+    static constexpr int kMax = kOut + kStageBytes;          // [2][2 halves][128] row maxima
     static constexpr int kBars = kMax + 2 * 2 * kRowTile * 4;
     static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 1;
     static constexpr int kMisc = kBars + kNumBars * 8;       // tensor memory address, abort, odd values
@@ -62,7 +65,8 @@ struct TcAttn {
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static constexpr int kHalfD = D / 2;
     static constexpr int kHold = D == 256 ? 16 : 32;         // scores a thread holds at a time
-    static __device__ __forceinline__ uint32_t p_col(int key16, int part) {  // from the buffer's first column
+    // Column of a part of the weights of keys 16 key16 .. + 15, from the buffer's first.
+    static __device__ __forceinline__ uint32_t p_col(int key16, int part) {
         return part < 2 ? 16 * key16 + 8 * part : kKeyTile + 8 * key16;
     }
 };
@@ -87,6 +91,8 @@ constexpr uint32_t idesc_kv(int n, uint32_t type, bool b_mn) {
 __device__ __forceinline__ void pair_sync(int quadrant) {
     asm volatile("bar.sync %0, 64;" ::"r"(quadrant + 1) : "memory");
 }
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
+static_assert(kSoftThreads == 256, "the softmax warps' barrier");
 // Largest of n values.
 template <int n>
 __device__ __forceinline__ float max_of(const uint32_t* x, float top) {
@@ -97,13 +103,93 @@ __device__ __forceinline__ float max_of(const uint32_t* x, float top) {
 }
 template <int n>
 __device__ __forceinline__ void tmem_ld_wait(uint32_t at, uint32_t* x) {
-    if constexpr (n == 16) tmem_ld16_wait(at, x);
+    if constexpr (n == 8)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+            : "r"(at)
+            : "memory");
+    else if constexpr (n == 16) tmem_ld16_wait(at, x);
     else tmem_ld32_wait(at, x);
 }
-__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t* v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+template <int n>
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* v) {
+    if constexpr (n == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3])
+                     : "memory");
+    else if constexpr (n == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]),
+                     "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    else tmem_st16(at, v);
+}
+
+// The thread's kKeys scores of a tile -> weights, written over them as parts.
+//   s_at   the score buffer's first column in the thread's lane
+//   key    the thread's first key in the tile
+//   seen   bit k: the row sees key + k
+//   mine, theirs  where the thread and the one that has the row's other half leave their maxima
+// m, l: running maximum (log2 units) and sum.  Returns the factor for what O holds.
+template <int D, class T, int kKeys>
+__device__ __forceinline__ float weigh(const AttnParams& p, uint32_t s_at, int key, uint32_t seen,
+                                       volatile float* mine, volatile float* theirs, int quad, float& m, float& l) {
+    using C = TcAttn<D, T>;
+    constexpr int kHold = kKeys == 32 ? C::kHold : kKeys;  // scores held at a time
+    constexpr int kStep = kKeys < 16 ? kKeys : 16;
+    uint32_t x[kHold];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < kKeys; h += kHold) {
+        tmem_ld_wait<kHold>(s_at + key + h, x);
+        if (seen != 0xffffffffu) {
+#pragma unroll
+            for (int k = 0; k < kHold; ++k)
+                if (!(seen >> (h + k) & 1)) x[k] = 0xff800000u;  // -inf
+        }
+        mx = max_of<kHold>(x, mx);
+    }
+    *mine = mx;
+    pair_sync(quad);  // (also: both have read what the weights overwrite)
+    mx = fmaxf(mx, *theirs) * p.scale_log2;  // (the scale is positive)
+    float f = 1.f;
+    if (mx > m + kLazy) {
+        f = fast_exp2(m - mx);
+        m = mx;
+        l *= f;
+    }
+    const float shift = m == -INFINITY ? 0.f : kWeightBits - m;
+    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), shift2 = make_float2(shift, shift);
+    float2 l2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int h = 0; h < kKeys; h += kStep) {
+        if constexpr (kHold < kKeys) {  // (read again: a thread's weights lie over its own scores only)
+            tmem_ld_wait<kStep>(s_at + key + h, x);
+            if (seen != 0xffffffffu) {
+#pragma unroll
+                for (int k = 0; k < kStep; ++k)
+                    if (!(seen >> (h + k) & 1)) x[k] = 0xff800000u;
+            }
+        }
+        uint32_t part[C::kParts][kStep / 2];
+#pragma unroll
+        for (int k = 0; k < kStep / 2; ++k) {
+            const uint32_t* xk = x + (kHold < kKeys ? 0 : h) + 2 * k;
+            float2 a = fma2(make_float2(__uint_as_float(xk[0]), __uint_as_float(xk[1])), scale2, shift2);
+            a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+            l2 = add2(l2, a);
+            uint32_t out[C::kParts];
+            Parts<T>::split(a, out);
+#pragma unroll
+            for (int i = 0; i < C::kParts; ++i) part[i][k] = out[i];
+        }
+#pragma unroll
+        for (int i = 0; i < C::kParts; ++i)
+            tmem_st<kStep / 2>(s_at + C::p_col((key + h) / 16, i) + (key + h) % 16 / 2, part[i]);
+    }
+    l += l2.x + l2.y;
+    return f;
 }
 // Places in the ring of tile j's K and V, an item of n tiles starting at place 0.
 __device__ __forceinline__ int place_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
@@ -163,8 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_at);
     griddep_wait();
     griddep_launch_dependents();
-    WorkWalk w;
-    w.start(p, b, g, kRowTile, err);
+    WorkWalk<kRowTile> w;
+    w.start(p, b, g, err);
 
     if (warp < kFirstSoft) {
         if constexpr (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -195,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 ++place;
             };
-            for (; live && w.valid(); w.next(p, b, g, kRowTile, err)) {
-                const int end = w.seen_tiles(p, kRowTile);
+            for (; live && w.valid(); w.next(p, b, g, err)) {
+                const int end = w.seen_tiles(p);
                 const int keys = w.w.len + w.w.tokens;
                 const int held = min(b.held[w.s], b.table_width);
                 const int32_t* table = b.page_table + w.s * b.table_stride;
@@ -260,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_commit(s_full + buf);
                 tc_commit(slot_free + st);
             };
-            for (; live && w.valid(); w.next(p, b, g, kRowTile, err)) {
-                const int n = w.seen_tiles(p, kRowTile) - w.tile0;
+            for (; live && w.valid(); w.next(p, b, g, err)) {
+                const int n = w.seen_tiles(p) - w.tile0;
                 if (n <= 0) continue;
                 live = mbar_wait(q_full, items & 1, abort_flag, err, kDevErrTimeoutScore);
                 scores(0);
@@ -302,17 +388,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ softmax
         if constexpr (D == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int quad = warp & 3, half = (warp - kFirstSoft) >> 2;
-        const int r = quad * 32 + lane;               // the thread's row of the tile
         const int st_id = threadIdx.x - 32 * kFirstSoft;
         const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
         int place0 = 0, it = 0;
-        for (; w.valid(); w.next(p, b, g, kRowTile, err)) {
-            const int n = max(0, w.seen_tiles(p, kRowTile) - w.tile0);
+        for (; w.valid(); w.next(p, b, g, err)) {
+            const int n = max(0, w.seen_tiles(p) - w.tile0);
             const int rows = min(kRowTile, w.w.tokens * p.group - w.row_tile * kRowTile);
             const int keys = w.w.len + w.w.tokens;
-            const bool busy = quad * 32 < rows;       // the warp has rows
+            // Up to 32 (64) rows stand in all four quadrants (in two pairs of
+            // them), each with a quarter (half) of every tile's keys: all the
+            // SM's schedulers work on the softmax, and the copies' results
+            // are joined at the item's end.
+            const int copies = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+            const int spread = 4 / copies;            // quadrants of a copy
+            const int copy = quad / spread;
+            const int r = quad % spread * 32 + lane;  // the thread's row of the tile
+            const bool busy = quad % spread * 32 < rows;  // the warp has rows
             const int my_row = w.row_tile * kRowTile + min(r, rows - 1);
             const int tok = my_row / p.group;
+            const int my_keys = kHalfKeys / copies, my_key = (2 * copy + half) * my_keys;
             float2 o[C::kHalfD / 2];
 #pragma unroll
             for (int i = 0; i < C::kHalfD / 2; ++i) o[i] = make_float2(0.f, 0.f);
@@ -342,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
 #pragma unroll
                     for (int i = 0; i < C::kHalfD / 8; ++i)
-                        sts_u128(base + C::kQ + unit_at(r, half * (C::kHalfD / 8) + i, kRowTile), v[i]);
+                        sts_u128(base + C::kQ + unit_at(quad * 32 + lane, half * (C::kHalfD / 8) + i, kRowTile), v[i]);
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
@@ -371,69 +465,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (int j = 0; j < n; ++j) {
                 const int i = it + j, buf = i & 1;
-                const int pos0 = (w.tile0 + j) * kKeyTile, key0 = pos0 + half * kHalfKeys;
+                const int pos0 = (w.tile0 + j) * kKeyTile, key0 = pos0 + my_key;
                 mbar_wait(s_full + buf, (i >> 1) & 1, abort_flag, err, kDevErrTimeoutScore);
                 float f = 1.f;
                 if (busy) {
                     tc_fence_after();
                     const uint32_t s_at = tmem + lane_at + C::kScores + buf * C::kScoreCols;
-                    const uint32_t my_s = s_at + half * kHalfKeys;
-                    constexpr int kHold = C::kHold;
-                    uint32_t x[kHold];
-                    uint32_t seen = 0xffffffffu;  // bit k: the row sees key0 + k
-                    const int have = keys - key0;  // positions before the end
-                    if (key0 + kHalfKeys > w.w.len || have < kHalfKeys)
-                        seen = seen_bits(p, w.w.row0 + tok, tok, key0 - w.w.len, have);
-                    float mx = -INFINITY;
+                    uint32_t seen = 0xffffffffu;
+                    if (key0 + my_keys > w.w.len || key0 + my_keys > keys)
+                        seen = seen_bits(p, w.w.row0 + tok, tok, key0 - w.w.len, keys - key0);
+                    volatile float* mine = maxima + (buf * 2 + half) * kRowTile + quad * 32 + lane;
+                    volatile float* theirs = maxima + (buf * 2 + (half ^ 1)) * kRowTile + quad * 32 + lane;
+                    if (copies == 1) {
+                        f = weigh<D, T, 32>(p, s_at, my_key, seen, mine, theirs, quad, m, l);
+                    } else {
+                        f = copies == 2 ? weigh<D, T, 16>(p, s_at, my_key, seen, mine, theirs, quad, m, l)
+                                        : weigh<D, T, 8>(p, s_at, my_key, seen, mine, theirs, quad, m, l);
+                        // the other copies' keys weigh nothing in these lanes
+                        const uint32_t zero[16] = {};
+                        const int own = 4 / copies;  // 16-key groups of a copy
 #pragma unroll
-                    for (int h = 0; h < kHalfKeys; h += kHold) {
-                        tmem_ld_wait<kHold>(my_s + h, x);
-                        if (seen != 0xffffffffu) {
-#pragma unroll
-                            for (int k = 0; k < kHold; ++k)
-                                if (!(seen >> (h + k) & 1)) x[k] = 0xff800000u;  // -inf
-                        }
-                        mx = max_of<kHold>(x, mx);
-                    }
-                    float* mine = maxima + buf * 2 * kRowTile;
-                    mine[half * kRowTile + r] = mx;
-                    pair_sync(quad);
-                    mx = fmaxf(mx, mine[(half ^ 1) * kRowTile + r]) * p.scale_log2;  // (the scale is positive)
-                    if (mx > m + kLazy) {
-                        f = fast_exp2(m - mx);
-                        m = mx;
-                        l *= f;
-                    }
-                    const float shift = m == -INFINITY ? 0.f : kWeightBits - m;
-                    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), shift2 = make_float2(shift, shift);
-                    float2 l2 = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int h = 0; h < kHalfKeys; h += 16) {  // 16 keys at a time, over their own columns
-                        if constexpr (kHold == 16) {
-                            tmem_ld_wait<16>(my_s + h, x);
-                            if (seen != 0xffffffffu) {
-#pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    if (!(seen >> (h + k) & 1)) x[k] = 0xff800000u;
+                        for (int k = 0; k < kKeyTile / 16; ++k)
+                            if (k / own != copy && (k & 1) == half) {
+                                tmem_st<16>(s_at + 16 * k, zero);
+                                if constexpr (kParts == 3) tmem_st<8>(s_at + C::p_col(k, 2), zero);
                             }
-                        }
-                        uint32_t part[kParts][8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t* xk = x + (kHold == 16 ? 0 : h) + 2 * k;
-                            float2 a = fma2(make_float2(__uint_as_float(xk[0]), __uint_as_float(xk[1])), scale2, shift2);
-                            a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-                            l2 = add2(l2, a);
-                            uint32_t out[kParts];
-                            Parts<T>::split(a, out);
-#pragma unroll
-                            for (int n2 = 0; n2 < kParts; ++n2) part[n2][k] = out[n2];
-                        }
-#pragma unroll
-                        for (int n2 = 0; n2 < kParts; ++n2)
-                            tmem_st8(s_at + C::p_col(half * (kHalfKeys / 16) + h / 16, n2), part[n2]);
                     }
-                    l += l2.x + l2.y;
                     tmem_wait_st();
                     tc_fence_before();
                 }
@@ -478,16 +535,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             place0 += 2 * n;
             it += n;
 
-            // Join the halves' sums and write the row.
-            float* mine = maxima + (it & 1) * 2 * kRowTile;  // (the buffer the last tile did not use)
-            if (busy) {
-                mine[half * kRowTile + r] = l;
-                pair_sync(quad);
-                l += mine[(half ^ 1) * kRowTile + r];
+            // The row's maximum over its copies and sum over copies and
+            // halves.  Buffer it & 1 is the one that the last tile did not
+            // use; the other is free once all threads are past that tile.
+            float* all_m = maxima + (it & 1) * 2 * kRowTile;
+            float* all_l = half == 0 ? all_m + kRowTile : maxima + ((it & 1) ^ 1) * 2 * kRowTile;
+            const int at = quad * 32 + lane;
+            if (busy && half == 0) all_m[at] = m;
+            soft_sync();
+            const bool odd_values = *odd_flag != 0;
+            float top = m, fix = 1.f;
+            if (copies > 1) {
+                for (int i = 0; i < copies; ++i) top = fmaxf(top, all_m[(i * spread + quad % spread) * 32 + lane]);
+                fix = m == -INFINITY ? 0.f : fast_exp2(m - top);
+                if (m != -INFINITY) l *= fix;  // (else nothing was seen: 0, or NaN)
             }
-            asm volatile("bar.sync 5, 256;" ::: "memory");  // every thread's odd_flag is in
-            if (*odd_flag && busy && r < rows) {
-                for (int t = 0; t < w.w.tokens; ++t) {
+            if (busy) all_l[at] = l;
+            soft_sync();
+            if (st_id == 0) *odd_flag = 0;
+            float sum = 0.f;
+            for (int i = 0; i < copies; ++i) {
+                const int from = (i * spread + quad % spread) * 32 + lane;
+                sum += all_m[kRowTile + from] + maxima[((it & 1) ^ 1) * 2 * kRowTile + from];
+            }
+            if (odd_values && busy && r < rows) {
+#pragma unroll
+                for (int i = 0; i < C::kHalfD / 2; ++i) o[i] = make_float2(o[i].x * fix, o[i].y * fix);
+                fix = 1.f;
+                for (int t = 0; copy == 0 && t < w.w.tokens; ++t) {
                     const int pos = w.w.len + t;
                     if (pos < w.tile0 * kKeyTile || pos >= w.tile1 * kKeyTile ||
                         !sees_new(p, w.w.row0 + tok, tok, t))
@@ -504,27 +579,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            asm volatile("bar.sync 5, 256;" ::: "memory");
-            if (st_id == 0) *odd_flag = 0;
-            if (r < rows) {
-                float* dst;
-                float inv = 1.f;
-                if (w.whole) {
-                    inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing: zeros
-                    dst = p.out + (w.w.row0 + tok) * p.out_row_stride +
-                          ((int64_t)w.head * p.group + my_row % p.group) * D + half * C::kHalfD;
-                } else {
-                    dst = p.part_o + ((int64_t)w.slot * p.slot_rows + r) * D + half * C::kHalfD;
-                    if (half == 0) p.part_ml[(int64_t)w.slot * p.slot_rows + r] = make_float2(m, l);
-                }
-                const bool ok = !w.whole || bc_global(bc, dst, 4 * C::kHalfD, p.out,
-                                                      4 * ((p.rows - 1) * p.out_row_stride +
-                                                           (int64_t)p.group * p.kv_heads * D), kBcAttnOut);
-                if (ok)
+            if (!w.whole && half == 0 && copy == 0 && r < rows)
+                p.part_ml[(int64_t)w.slot * p.slot_rows + r] = make_float2(top, sum);
+            // Out through shared memory, 16 channels at a time, so that four
+            // lanes write 64 bytes of a row; the copies' warps share the rows
+            // and add up the copies.
+            const float scale = !w.whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: zeros
+            const int64_t row_at = w.whole ? (w.w.row0 + tok) * p.out_row_stride +
+                                                 ((int64_t)w.head * p.group + my_row % p.group) * D
+                                           : ((int64_t)w.slot * p.slot_rows + r) * D;
+            float* const out = w.whole ? p.out : p.part_o;
+            float* const stage = reinterpret_cast<float*>(smem + C::kOut) + half * 4 * 32 * kStageRow;
 #pragma unroll
-                    for (int i = 0; i < C::kHalfD / 4; ++i)
-                        *reinterpret_cast<float4*>(dst + 4 * i) =
-                            make_float4(o[2 * i].x * inv, o[2 * i].y * inv, o[2 * i + 1].x * inv, o[2 * i + 1].y * inv);
+            for (int ch = 0; ch < C::kHalfD / kStageCols; ++ch) {
+                if (busy) {
+#pragma unroll
+                    for (int i = 0; i < kStageCols / 4; ++i) {
+                        const float2 a = o[ch * (kStageCols / 2) + 2 * i], z = o[ch * (kStageCols / 2) + 2 * i + 1];
+                        *reinterpret_cast<float4*>(stage + at * kStageRow + 4 * i) =
+                            make_float4(a.x * fix, a.y * fix, z.x * fix, z.y * fix);
+                    }
+                }
+                if (copies == 1) __syncwarp();
+                else soft_sync();
+                if (busy) {
+                    const int col = (lane & 3) * 4;
+                    for (int i = copy * spread; i < (copy + 1) * spread; ++i) {
+                        const int rr = i * 8 + (lane >> 2);  // row of the quadrant
+                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int k = 0; k < copies; ++k) {
+                            const float4 t = *reinterpret_cast<const float4*>(
+                                stage + ((k * spread + quad % spread) * 32 + rr) * kStageRow + col);
+                            v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+                        }
+                        const float f = __shfl_sync(0xffffffffu, scale, rr);
+                        float* dst = out + __shfl_sync(0xffffffffu, row_at, rr) + half * C::kHalfD + ch * kStageCols + col;
+                        if (quad % spread * 32 + rr < rows &&
+                            (!w.whole || bc_global(bc, dst, 16, p.out,
+                                                   4 * ((p.rows - 1) * p.out_row_stride +
+                                                        (int64_t)p.group * p.kv_heads * D), kBcAttnOut)))
+                            *reinterpret_cast<float4*>(dst) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+                    }
+                }
+                if (copies == 1) __syncwarp();
+                else soft_sync();
             }
         }
     }

@@ -48,7 +48,7 @@ int view_batch(const iq4xs_kv_batch* b, BatchView* out) {
     if (b->sequences < 0 || b->sequences > kMaxSequences) return IQ4XS_ERR_SHAPE;
     if (b->table_width < 1 || b->table_width > (1 << 20)) return IQ4XS_ERR_SHAPE;
     if (b->table_stride < b->table_width) return IQ4XS_ERR_ARG;
-    if (!b->row_offsets || !b->lens || !b->held || !b->page_table) return IQ4XS_ERR_ARG;
+    if (!b->row_offsets || (b->sequences > 0 && (!b->lens || !b->held || !b->page_table))) return IQ4XS_ERR_ARG;
     if (!aligned(b->row_offsets, 4) || !aligned(b->lens, 4) || !aligned(b->held, 4) || !aligned(b->page_table, 4))
         return IQ4XS_ERR_ALIGN;
     out->row_offsets = b->row_offsets;
@@ -139,7 +139,7 @@ int iq4xs_cache_reserve(const iq4xs_kv_batch* batch, int64_t page_size, int32_t*
     BatchView b;
     int rc = view_batch(batch, &b);
     if (rc) return rc;
-    if (!refs || !status) return IQ4XS_ERR_ARG;
+    if (!refs || (!status && b.sequences > 0)) return IQ4XS_ERR_ARG;
     if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) || pages < 1 || pages > INT32_MAX)
         return IQ4XS_ERR_SHAPE;
     if (!aligned(refs, 16) || !aligned(status, 4)) return IQ4XS_ERR_ALIGN;
@@ -157,7 +157,7 @@ int iq4xs_cache_commit(const iq4xs_kv_cache* cache, const iq4xs_kv_batch* batch,
     BatchView b;
     int rc = view_cache(cache, &c);
     if (rc || (rc = view_batch(batch, &b))) return rc;
-    if (!refs || !paths || !accepted || !new_lens) return IQ4XS_ERR_ARG;
+    if (!refs || (b.sequences > 0 && (!paths || !accepted || !new_lens))) return IQ4XS_ERR_ARG;
     if (path_width < 1 || path_width > kMaxRows) return IQ4XS_ERR_SHAPE;
     if (!aligned(refs, 16) || !aligned(paths, 4) || !aligned(accepted, 4) || !aligned(new_lens, 4))
         return IQ4XS_ERR_ALIGN;
@@ -175,7 +175,7 @@ int iq4xs_cache_fork(const iq4xs_kv_cache* cache, const iq4xs_kv_batch* batch, i
     BatchView b;
     int rc = view_cache(cache, &c);
     if (rc || (rc = view_batch(batch, &b))) return rc;
-    if (!refs || !parents || !children || !status) return IQ4XS_ERR_ARG;
+    if (!refs || (count > 0 && (!parents || !children || !status))) return IQ4XS_ERR_ARG;
     if (count < 0 || count > kMaxSequences) return IQ4XS_ERR_SHAPE;
     if (!aligned(refs, 16) || !aligned(parents, 4) || !aligned(children, 4) || !aligned(status, 4))
         return IQ4XS_ERR_ALIGN;
@@ -192,7 +192,7 @@ int iq4xs_cache_release(const iq4xs_kv_batch* batch, int32_t* refs, int64_t page
     BatchView b;
     int rc = view_batch(batch, &b);
     if (rc) return rc;
-    if (!refs || !rows) return IQ4XS_ERR_ARG;
+    if (!refs || (count > 0 && !rows)) return IQ4XS_ERR_ARG;
     if (pages < 1 || pages > INT32_MAX || count < 0 || count > kMaxSequences) return IQ4XS_ERR_SHAPE;
     if (!aligned(refs, 16) || !aligned(rows, 4)) return IQ4XS_ERR_ALIGN;
     int *err, sms;
@@ -208,7 +208,7 @@ int iq4xs_cache_copy_pages(const iq4xs_kv_cache* cache, const int32_t* src, cons
     CacheView c;
     int rc = view_cache(cache, &c);
     if (rc) return rc;
-    if (!src || !dst) return IQ4XS_ERR_ARG;
+    if (count > 0 && (!src || !dst)) return IQ4XS_ERR_ARG;
     if (count < 0 || count > kMaxSequences) return IQ4XS_ERR_SHAPE;
     if (!aligned(src, 4) || !aligned(dst, 4)) return IQ4XS_ERR_ALIGN;
     int *err, sms;

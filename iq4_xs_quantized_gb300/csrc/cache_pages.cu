@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kBookThreads)
 // overtakes a load that is still to come (those read places >= i + 1).
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBatch = 8;
+constexpr int kMoveRows = 64;  // rows of the path looked up at a time
 
 __device__ bool path_ok(const int32_t* path, int n, int width, int tokens, int len) {
     if (n < 0 || n > width || len < 0 || len > INT32_MAX - tokens) return false;
@@ -184,83 +185,81 @@ __device__ bool path_ok(const int32_t* path, int n, int width, int tokens, int l
     return true;
 }
 
+// A cluster per sequence shares its columns; its first CTA then keeps the
+// books, once every CTA is done with what it rewrites (held, and the length
+// when new_lens is lens): one launch where two would follow each other.
 __global__ void __launch_bounds__(kMoveThreads)
-    move_kernel(const CacheView c, const BatchView b, const int32_t* __restrict__ paths, int width,
-                const int32_t* __restrict__ accepted, int* err) {
+    commit_kernel(const CacheView c, const BatchView b, int32_t* refs, const int32_t* __restrict__ paths, int width,
+                  const int32_t* __restrict__ accepted, int32_t* new_lens, int* err) {
+    __shared__ int64_t from_s[kMoveRows], to_s[kMoveRows];
     griddep_launch_dependents();
     griddep_wait();
     const Bc bc = bc_open(err);
-    const int cols = c.head_dim / 8;  // 16-byte columns of a row
     const int s = blockIdx.y;
-    const int64_t u = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x;
-    const int col = (int)(u % cols);
-    const int64_t seg = u / cols;  // (layer, K or V, head)
-    const int head = (int)(seg % c.heads);
-    const int which = (int)(seg / c.heads % 2);
-    const int64_t layer = seg / c.heads / 2;
-    if (layer >= c.layers) return;
-    int first;
-    const int tokens = batch_rows(b, s, INT32_MAX, &first, err);
-    const int len = batch_len(b, s, err), n = accepted[s];
-    const int32_t* path = paths + (int64_t)s * width;
-    if (!path_ok(path, n, width, tokens, len)) return;  // (bookkeeping records it)
-    uint16_t* base = which ? c.v : c.k;
-    uint16_t* rows = base + layer * c.layer_stride + head * c.head_stride + col * 8;
-    for (int i0 = 0; i0 < n; i0 += kMoveBatch) {
-        uint4 val[kMoveBatch];
-        uint16_t* to[kMoveBatch];
-#pragma unroll
-        for (int k = 0; k < kMoveBatch; ++k) {
-            const int i = i0 + k;
-            to[k] = nullptr;
-            if (i >= n || path[i] == i) continue;
-            const int src = len + path[i], dst = len + i;
-            const int ps = page_of(c, b, s, src, err), pd = page_of(c, b, s, dst, err);
-            if (ps < 0 || pd < 0) continue;
-            const uint16_t* from = rows + ps * c.page_stride + (src & (c.page_size - 1)) * c.slot_stride;
-            uint16_t* t = rows + pd * c.page_stride + (dst & (c.page_size - 1)) * c.slot_stride;
-            if (!bc_global(bc, from, 16, base, c.extent, kBcPagesKv) ||
-                !bc_global(bc, t, 16, base, c.extent, kBcPagesKv))
-                continue;
-            val[k] = *reinterpret_cast<const uint4*>(from);
-            to[k] = t;
-        }
-#pragma unroll
-        for (int k = 0; k < kMoveBatch; ++k)
-            if (to[k] != nullptr) *reinterpret_cast<uint4*>(to[k]) = val[k];
-    }
-}
-
-// Lengths, held pages and references after the move: a warp per sequence.
-__global__ void __launch_bounds__(kMoveThreads)
-    commit_book_kernel(const CacheView c, const BatchView b, int32_t* refs, const int32_t* __restrict__ paths,
-                       int width, const int32_t* __restrict__ accepted, int32_t* new_lens, int* err) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const Bc bc = bc_open(err);
-    const int lane = threadIdx.x & 31;
-    const int s = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5);
-    if (s >= b.sequences) return;
     int first;
     const int tokens = batch_rows(b, s, INT32_MAX, &first, err);
     const int len = b.lens[s], n = accepted[s], held = b.held[s];
-    const bool ok = path_ok(paths + (int64_t)s * width, n, width, tokens, len) && held >= 0 && held <= b.table_width;
-    __syncwarp();
+    const int32_t* path = paths + (int64_t)s * width;
+    const bool ok = path_ok(path, n, width, tokens, len) && held >= 0 && held <= b.table_width;
+    const int cols = c.head_dim / 8;  // 16-byte columns of a row
+    const int64_t units = ok ? (int64_t)c.layers * 2 * c.heads * cols : 0;
+    for (int c0 = 0; ok && c0 < n; c0 += kMoveRows) {
+        // where the next rows of the path lie in a (layer, head), -1: stays or cannot move
+        __syncthreads();
+        if (threadIdx.x < kMoveRows) {
+            const int i = c0 + threadIdx.x;
+            int64_t f = -1, t = -1;
+            if (i < n && path[i] != i) {
+                const int src = len + path[i], dst = len + i;
+                const int ps = page_of(c, b, s, src, err), pd = page_of(c, b, s, dst, err);
+                if (ps >= 0 && pd >= 0) {
+                    f = ps * c.page_stride + (src & (c.page_size - 1)) * c.slot_stride;
+                    t = pd * c.page_stride + (dst & (c.page_size - 1)) * c.slot_stride;
+                }
+            }
+            from_s[threadIdx.x] = f;
+            to_s[threadIdx.x] = t;
+        }
+        __syncthreads();
+        const int rows = min(kMoveRows, n - c0);
+        for (int64_t u = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x; u < units;
+             u += (int64_t)gridDim.x * kMoveThreads) {
+            const int64_t seg = u / cols;  // (layer, K or V, head)
+            uint16_t* base = seg / c.heads % 2 ? c.v : c.k;
+            uint16_t* column = base + (seg / c.heads / 2) * c.layer_stride + seg % c.heads * c.head_stride +
+                               (u - seg * cols) * 8;
+            for (int i0 = 0; i0 < rows; i0 += kMoveBatch) {
+                uint4 val[kMoveBatch];
+#pragma unroll
+                for (int k = 0; k < kMoveBatch; ++k)
+                    if (i0 + k < rows && from_s[i0 + k] >= 0 &&
+                        bc_global(bc, column + from_s[i0 + k], 16, base, c.extent, kBcPagesKv))
+                        val[k] = *reinterpret_cast<const uint4*>(column + from_s[i0 + k]);
+#pragma unroll
+                for (int k = 0; k < kMoveBatch; ++k)
+                    if (i0 + k < rows && to_s[i0 + k] >= 0 &&
+                        bc_global(bc, column + to_s[i0 + k], 16, base, c.extent, kBcPagesKv))
+                        *reinterpret_cast<uint4*>(column + to_s[i0 + k]) = val[k];
+            }
+        }
+    }
+    cluster_arrive_release();
+    cluster_wait();
+    if (blockIdx.x != 0) return;
     if (!ok) {
-        if (lane == 0) {
+        if (threadIdx.x == 0) {
             data_error(err, len < 0 ? kDataLens : held < 0 || held > b.table_width ? kDataHeld : kDataPath);
             new_lens[s] = len;
         }
         return;
     }
     const int keep = min(held, pages_for((int64_t)len + n, c.page_shift));
-    for (int j = keep + lane; j < held; j += 32) {
+    for (int j = keep + threadIdx.x; j < held; j += kMoveThreads) {
         const int page = b.page_table[s * b.table_stride + j];
         if (page < 0 || page >= c.pages) data_error(err, kDataPage);
         else if (bc_global(bc, refs + page, 4, refs, 4 * (int64_t)c.pages, kBcPagesRefs)) atomicSub(refs + page, 1);
     }
-    __syncwarp();
-    if (lane == 0) {
+    if (threadIdx.x == 0) {
         b.held[s] = keep;
         new_lens[s] = len + n;
     }
@@ -446,14 +445,23 @@ cudaError_t launch_cache_reserve(const BatchView& b, int page_size, int32_t* ref
 cudaError_t launch_cache_commit(const CacheView& c, const BatchView& b, int32_t* refs, const int32_t* paths,
                                 int path_width, const int32_t* accepted, int32_t* new_lens, int* err,
                                 cudaStream_t stream) {
+    // One CTA a sequence up to the portable eight: as many as its columns fill.
     const int64_t units = (int64_t)c.layers * 2 * c.heads * (c.head_dim / 8);
-    const dim3 grid((unsigned)((units + kMoveThreads - 1) / kMoveThreads), (unsigned)b.sequences);
-    const cudaError_t e =
-        launch_chained(move_kernel, grid, dim3(kMoveThreads), 0, stream, c, b, paths, path_width, accepted, err);
-    if (e != cudaSuccess) return e;
-    constexpr int kWarps = kMoveThreads / 32;
-    return launch_chained(commit_book_kernel, dim3((unsigned)((b.sequences + kWarps - 1) / kWarps)),
-                          dim3(kMoveThreads), 0, stream, c, b, refs, paths, path_width, accepted, new_lens, err);
+    const int64_t full = (units + kMoveThreads - 1) / kMoveThreads;
+    const unsigned ctas = full >= 8 ? 8 : full >= 4 ? 4 : full >= 2 ? 2 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, (unsigned)b.sequences);
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, commit_kernel, c, b, refs, paths, path_width, accepted, new_lens, err);
 }
 
 cudaError_t launch_cache_fork(const CacheView& c, const BatchView& b, int32_t* refs, const int32_t* parents,
