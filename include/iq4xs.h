@@ -650,7 +650,7 @@ int iq4xs_qk_norm_rope(const iq4xs_qk_norm_rope_args* args, const iq4xs_kv_cache
  *              takes.  Rows of no sequence are not written.
  *   tree_mask  uint64 [rows][mask_words], or NULL; a new token j >=
  *              64*mask_words is seen by no row.
- *   workspace  iq4xs_tree_attention_workspace_bytes(...) bytes, 16-byte
+ *   workspace  iq4xs_tree_attention_workspace_bytes(...) bytes, 32-byte
  *              aligned, of any content; one per stream.
  * Scores and softmax statistics are fp32 and weights keep at least 16
  * significant bits; results are the same from run to run.

@@ -132,7 +132,7 @@ cudaError_t launch_join(const AttnParams& p, const BatchView& b, int q_heads, in
 inline int64_t slot_rows(int64_t row_tile, int64_t rows, int64_t group) {
     return rows * group < row_tile ? rows * group : row_tile;
 }
-inline int64_t align16(int64_t v) { return (v + 15) / 16 * 16; }
+inline int64_t align32(int64_t v) { return (v + 31) / 32 * 32; }
 
 }  // namespace
 
@@ -143,7 +143,7 @@ int64_t tree_attention_workspace(int64_t rows, int64_t q_heads, int64_t kv_heads
     const int64_t mma = 2 * (int64_t)mma_ctas(head_dim, num_sms) * slot_rows(kMmaRows, rows, group);
     const int64_t tc = 2 * (int64_t)num_sms * slot_rows(kTcRows, rows, group);
     const int64_t n = mma > tc ? mma : tc;
-    return align16(n * 8) + n * head_dim * 4;
+    return align32(n * 8) + n * head_dim * 4;
 }
 
 cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const CacheView& c, const BatchView& b, bool bf16,
@@ -161,6 +161,8 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     p.q_and = a.scale == 0 ? 0u : 0xffffffffu;
     p.q_xor = a.scale < 0 ? 0x80008000u : 0u;
     p.group = group;
+    p.group_magic = ((uint64_t(1) << 38) + group - 1) / group;
+    p.wide_out = (reinterpret_cast<uintptr_t>(a.out) % 32 == 0) && a.out_row_stride % 8 == 0;
     p.kv_heads = c.heads;
     p.mask_words = (int)a.mask_words;
     p.head_dim = c.head_dim;
@@ -174,7 +176,7 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     p.slot_rows = (int)slot_rows(row_tile, a.rows, group);
     p.part_ml = static_cast<float2*>(a.workspace);
     p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
-                                        align16(2 * (int64_t)p.ctas * p.slot_rows * 8));
+                                        align32(2 * (int64_t)p.ctas * p.slot_rows * 8));
     CUtensorMap tk, tv;
     const EncodeTiledFn enc = reinterpret_cast<EncodeTiledFn>(encode);
     if (!encode_kv(enc, c.k + p.layer_offset, c, bf16, &p.slot_axis, &tk) ||

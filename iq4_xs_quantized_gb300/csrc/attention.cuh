@@ -34,12 +34,20 @@ struct AttnParams {
     float scale_log2;  // |scale| log2(e): scores are kept in log2 units
     uint32_t q_and, q_xor;  // the scale's sign (or zero), put on q: scores may be masked with -inf before scaling
     int group, kv_heads, mask_words, head_dim;
+    uint64_t group_magic;  // ceil(2^38 / group): row / group by one multiplication
+    int wide_out;          // out and its rows are 32-byte aligned
     int ctas;          // CTAs the work is split over, at most
     int whole_items;   // 1: items are not cut
     int slot_rows;     // rows of a partial result: the row tile, or all rows if fewer
     int slot_axis;     // tensor-map axis of the slot (1 or 2; the head has the other)
     int skip_stage;    // test hook: this stage of every CTA is left unissued
 };
+
+// Row r's token and query head of the group (r < 2^25, group <= 2^10: the
+// magic's excess, below 2^10 / 2^38 of a row, never reaches the next token).
+__device__ __forceinline__ int token_of(const AttnParams& p, int r) {
+    return (int)(((uint64_t)(uint32_t)r * p.group_magic) >> 38);
+}
 
 // One sequence as the split sees it.
 struct SeqWork {
@@ -120,32 +128,38 @@ struct WorkWalk {
     bool whole;          // this CTA has all of the item's key tiles
     int slot;            // of its partial result, if not
 
+    int each;            // places of a CTA (the split's)
+
     __device__ __forceinline__ void start(const AttnParams& p, const BatchView& b, int g, int* err) {
-        const Split split(p, work_before<kRows>(p, b, b.sequences, err));
+        // running sums of 32 sequences at a time; those of the first 32 are kept
+        const int lane = threadIdx.x & 31;
+        int64_t total = 0, sums = 0;
+        for (int s0 = 0; s0 < b.sequences; s0 += 32) {
+            const int64_t v = scan(s0 + lane < b.sequences ? seq_work<kRows>(p, b, s0 + lane, err).work : 0, lane);
+            if (s0 == 0) sums = v;
+            total += __shfl_sync(0xffffffffu, v, 31);
+        }
+        const Split split(p, total);
         left = 0;
+        each = (int)min(split.each, (int64_t)INT32_MAX);
         if (g >= split.ctas) return;
         const int64_t x = split.start(g);
         left = split.start(g + 1) - x;
         // the sequence that holds x: the first whose end lies behind it
-        const int lane = threadIdx.x & 31;
         int64_t before = 0, seq_x = 0;
         s = 0;
         for (int s0 = 0; s0 < b.sequences; s0 += 32) {
-            int64_t v = s0 + lane < b.sequences ? seq_work<kRows>(p, b, s0 + lane, err).work : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += y;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, before + v > x);
+            if (s0 > 0)
+                sums = scan(s0 + lane < b.sequences ? seq_work<kRows>(p, b, s0 + lane, err).work : 0, lane);
+            const unsigned past = __ballot_sync(0xffffffffu, before + sums > x);
             if (past != 0) {
                 const int k = __ffs(past) - 1;
-                const int64_t up = __shfl_sync(0xffffffffu, v, k > 0 ? k - 1 : 0);
+                const int64_t up = __shfl_sync(0xffffffffu, sums, k > 0 ? k - 1 : 0);
                 s = s0 + k;
                 seq_x = before + (k > 0 ? up : 0);
                 break;
             }
-            before += __shfl_sync(0xffffffffu, v, 31);
+            before += __shfl_sync(0xffffffffu, sums, 31);
         }
         row_end = b.row_offsets[s + 1];
         w = seq_of<kRows>(p, b.row_offsets[s], row_end, b.lens[s], err);
@@ -155,6 +169,14 @@ struct WorkWalk {
         head = item / w.row_tiles;
         row_tile = item - head * w.row_tiles;
         set(p, g);
+    }
+    static __device__ __forceinline__ int64_t scan(int64_t v, int lane) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        return v;
     }
     __device__ __forceinline__ void read_ahead(const BatchView& b) {
         if (s + 1 < b.sequences) {
@@ -191,7 +213,7 @@ struct WorkWalk {
     __device__ __forceinline__ int seen_tiles(const AttnParams& p) const {
         int keys = w.len + w.tokens;
         if (p.mask == nullptr) {
-            const int last = min(w.tokens - 1, ((row_tile + 1) * kRows - 1) / p.group);
+            const int last = min(w.tokens - 1, token_of(p, (row_tile + 1) * kRows - 1));
             keys = w.len + last + 1;
         }
         return min(tile1, (keys + kKeyTile - 1) / kKeyTile);
@@ -206,21 +228,33 @@ __device__ __forceinline__ bool sees_new(const AttnParams& p, int row, int t, in
 }
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
-// Bit k: token t sees the position k behind one whose place among the new
-// tokens is j0 (negative: context); `have` positions lie before the end.
-__device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, int row, int t, int j0, int have) {
-    uint32_t fresh;
-    if (p.mask == nullptr) {
-        fresh = low_bits(t - j0 + 1);
-    } else {
-        const int lo = max(j0, 0), word = lo >> 6, sh = lo & 63;
-        const uint64_t* m = p.mask + (int64_t)row * p.mask_words;
-        uint64_t v = word < p.mask_words ? m[word] >> sh : 0;
-        if (sh > 32 && word + 1 < p.mask_words) v |= m[word + 1] << (64 - sh);
-        fresh = lo - j0 >= 32 ? 0u : (uint32_t)v << (lo - j0);
+// A row's view of its sequence's new tokens: the mask's first word, read when
+// the row's item starts, and the row, for masks of more words.
+struct RowSight {
+    uint64_t word;
+    int row, token;
+    __device__ __forceinline__ void open(const AttnParams& p, int row0, int t) {
+        row = row0 + t;
+        token = t;
+        word = p.mask != nullptr ? p.mask[(int64_t)row * p.mask_words] : 0;
     }
-    return (low_bits(-j0) | fresh) & low_bits(have);
-}
+    // Bit k: the row sees the position k behind one whose place among the new
+    // tokens is j0 (negative: context); `have` positions lie before the end.
+    __device__ __forceinline__ uint32_t bits(const AttnParams& p, int j0, int have) const {
+        uint32_t fresh;
+        if (p.mask == nullptr) {
+            fresh = low_bits(token - j0 + 1);
+        } else {
+            const int lo = max(j0, 0), at = lo >> 6, sh = lo & 63;
+            const uint64_t* m = p.mask + (int64_t)row * p.mask_words;
+            uint64_t v = 0;
+            if (at < p.mask_words) v = (at == 0 ? word : m[at]) >> sh;
+            if (sh > 32 && at + 1 < p.mask_words) v |= m[at + 1] << (64 - sh);
+            fresh = lo - j0 >= 32 ? 0u : (uint32_t)v << (lo - j0);
+        }
+        return (low_bits(-j0) | fresh) & low_bits(have);
+    }
+};
 
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;

@@ -195,8 +195,9 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
             const int r = u / (D / 8), col = u % (D / 8), row = w.row_tile * kRowTile + r;
             qv[i] = make_uint4(0, 0, 0, 0);
             if (r < rows) {
-                const uint16_t* src = p.q + (w.w.row0 + row / p.group) * p.q_row_stride +
-                                      ((int64_t)w.head * p.group + row % p.group) * D + col * 8;
+                const int t = token_of(p, row);
+                const uint16_t* src = p.q + (w.w.row0 + t) * p.q_row_stride +
+                                      ((int64_t)w.head * p.group + row - t * p.group) * D + col * 8;
                 if (bc_global(bc, src, 16, p.q,
                               2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D), kBcAttnQ))
                     qv[i] = load_q(p, src);
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
         int tok[2];  // the rows' tokens (rows behind the last: the last token)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            tok[i] = min(w.w.tokens - 1, (w.row_tile * kRowTile + rg + 8 * i) / p.group);
+            tok[i] = min(w.w.tokens - 1, token_of(p, w.row_tile * kRowTile + rg + 8 * i));
 
         for (int tile = w.tile0; tile < end; ++tile, ++it) {
             const int st = it % C::kStages, par = (it / C::kStages) & 1;
@@ -450,9 +451,9 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
                 if (w.whole) {
                     const float sum_r = ml[kConsumers * kRowTile + r].y;
                     const float inv = sum_r == 0.f ? 0.f : 1.f / sum_r;  // a row that sees nothing: zeros
-                    const int row = w.row_tile * kRowTile + r;
-                    float* dst = p.out + (w.w.row0 + row / p.group) * p.out_row_stride +
-                                 ((int64_t)w.head * p.group + row % p.group) * D + ch * kCols + col;
+                    const int row = w.row_tile * kRowTile + r, t = token_of(p, row);
+                    float* dst = p.out + (w.w.row0 + t) * p.out_row_stride +
+                                 ((int64_t)w.head * p.group + row - t * p.group) * D + ch * kCols + col;
                     if (bc_global(bc, dst, 16, p.out,
                                   4 * ((p.rows - 1) * p.out_row_stride + (int64_t)p.group * p.kv_heads * D), kBcAttnOut))
                         *reinterpret_cast<float4*>(dst) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);

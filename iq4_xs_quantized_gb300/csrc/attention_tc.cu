@@ -35,7 +35,19 @@ constexpr int kThreads = 32 * (kFirstSoft + kSoftWarps);
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kHalfKeys = kKeyTile / 2;
 constexpr int kTmemCols = 512;
-constexpr int kStageCols = 16, kStageRow = kStageCols + 4;  // floats of a row on its way out, and its pitch
+constexpr int kItems = 4;  // item descriptors in flight
+
+// One item's part as the producer hands it to the other warps.
+struct Item {
+    int row0, tokens, len;  // the sequence's first row, new tokens and length
+    int seq, head, first;   // first: the row tile's first row (token and query head of the group)
+    int tile0, n, turn;     // key tiles tile0 .. + n - 1, starting at tile0 + turn; n < 0: no more items
+    int tile1;              // end of the part (rows may see fewer tiles)
+    int slot;               // of the partial result; -1: the item is whole
+    int pad;
+    __device__ __forceinline__ int tile(int j) const { return tile0 + (j + turn >= n ? j + turn - n : j + turn); }
+};
+static_assert(sizeof(Item) % 16 == 0, "descriptors stay aligned");
 
 template <int D, class T>
 struct TcAttn {
@@ -53,13 +65,16 @@ struct TcAttn {
     static_assert(kScores + 2 * kScoreCols <= kTmemCols, "tensor memory");
     // shared memory
     static constexpr int kQBytes = kQInTmem ? 0 : kRowTile * D * 2;
-    static constexpr int kStageBytes = kSoftWarps * 32 * kStageRow * 4;
-    static constexpr int kSlots = (224 * 1024 - kQBytes - kStageBytes) / kTileBytes;  // 6 (4 with Q), 12, 25
+    static constexpr int kStageCols = kQInTmem ? 32 : 16;    // channels of a row joined at a time, and their pitch
+    static constexpr int kStageRow = kStageCols + 4;
+    static constexpr int kStageBytes = kSoftThreads * kStageRow * 4;
+    static constexpr int kSlots = (224 * 1024 - kQBytes - kStageBytes) / kTileBytes;  // 5 (4 with Q), 11, 23
     static constexpr int kQ = kSlots * kTileBytes;
-    static constexpr int kOut = kQ + kQBytes;                // the warps' outputs on their way out
+    static constexpr int kOut = kQ + kQBytes;                // the copies' outputs on their way together
     static constexpr int kMax = kOut + kStageBytes;          // [2][2 halves][128] row maxima
-    static constexpr int kBars = kMax + 2 * 2 * kRowTile * 4;
-    static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 1;
+    static constexpr int kDesc = kMax + 2 * 2 * kRowTile * 4;
+    static constexpr int kBars = kDesc + kItems * (int)sizeof(Item);
+    static constexpr int kNumBars = 2 * kSlots + 2 * kItems + 2 + 2 + 2 + 2 + 1 + 1;
     static constexpr int kMisc = kBars + kNumBars * 8;       // tensor memory address, abort, odd values
     static constexpr int kSmem = kMisc + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -93,6 +108,26 @@ __device__ __forceinline__ void pair_sync(int quadrant) {
 }
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
 static_assert(kSoftThreads == 256, "the softmax warps' barrier");
+// Whether x holds for any softmax thread: one answer for all of them.
+__device__ __forceinline__ bool soft_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 5, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+// NaN or infinities among two 16-bit values (exponent bits all set).
+template <class T>
+__device__ __forceinline__ bool any_odd(uint32_t w) {
+    constexpr uint32_t kExp = Parts<T>::kN == 3 ? 0x7f807f80u : 0x7c007c00u;
+    const uint32_t t = (w & kExp) ^ kExp;  // a zero half: odd
+    return ((t - 0x00010001u) & ~t & 0x80008000u) != 0;
+}
 // Largest of n values.
 template <int n>
 __device__ __forceinline__ float max_of(const uint32_t* x, float top) {
@@ -210,7 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);
     uint64_t* slot_free = full + C::kSlots;
-    uint64_t* s_full = slot_free + C::kSlots;
+    uint64_t* item_full = slot_free + C::kSlots;
+    uint64_t* item_free = item_full + kItems;
+    uint64_t* s_full = item_free + kItems;
     uint64_t* p_full = s_full + 2;
     uint64_t* t_full = p_full + 2;
     uint64_t* t_free = t_full + 2;
@@ -218,7 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* drained = q_full + 1;
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_at + 1);
-    volatile int* odd_flag = abort_flag + 1;  // this item met NaN or infinities among the new tokens' values
+    volatile int* odd_flag = abort_flag + 1;  // [2]: an item met NaN or infinities among the new tokens' values
+    Item* items = reinterpret_cast<Item*>(smem + C::kDesc);
     float* maxima = reinterpret_cast<float*>(smem + C::kMax);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.x;
     const Bc bc = bc_open(err);
@@ -228,16 +266,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(full + i, 1);
             mbar_init(slot_free + i, 1);
         }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(item_full + i, 1);
+            mbar_init(item_free + i, kSoftWarps + 1);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, kSoftWarps);
             mbar_init(t_full + i, 1);
             mbar_init(t_free + i, kSoftWarps);
+            odd_flag[i] = 0;
         }
         mbar_init(q_full, kSoftWarps);
         mbar_init(drained, 1);
         *abort_flag = 0;
-        *odd_flag = 0;
         fence_barrier_init();
         prefetch_tmap(&tk);
         prefetch_tmap(&tv);
@@ -249,8 +291,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_at);
     griddep_wait();
     griddep_launch_dependents();
-    WorkWalk<kRowTile> w;
-    w.start(p, b, g, err);
 
     if (warp < kFirstSoft) {
         if constexpr (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -261,7 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t box_bytes = box_slots * kChunkBytes;
             const int sub = lane / C::kChunks, chunk = lane % C::kChunks;
             const uint32_t dst0 = base + chunk * kKeyTile * kChunkBytes + sub * box_bytes;
-            int place = 0;  // in the ring, over all items
+            WorkWalk<kRowTile> w;
+            w.start(p, b, g, err);
+            int place = 0, count = 0;  // in the ring, and items, over all of them
             bool live = true;
             auto load = [&](const void* map, int page, int slot, int used) {
                 const int st = place % C::kSlots;
@@ -281,20 +323,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 ++place;
             };
+            // The next item's descriptor, when a place for it is free.
+            auto publish = [&](const Item& d) {
+                const int at = count % kItems;
+                if (count >= kItems && !warp_wait(item_free + at, (count / kItems - 1) & 1, abort_flag, err,
+                                                  kDevErrTimeoutKvSlot)) {
+                    live = false;
+                    return;
+                }
+                if (lane == 0) {
+                    items[at] = d;
+                    mbar_arrive(item_full + at);
+                }
+                __syncwarp();
+                ++count;
+            };
             for (; live && w.valid(); w.next(p, b, g, err)) {
-                const int end = w.seen_tiles(p);
-                const int keys = w.w.len + w.w.tokens;
+                Item d;
+                d.row0 = w.w.row0;
+                d.tokens = w.w.tokens;
+                d.len = w.w.len;
+                d.seq = w.s;
+                d.head = w.head;
+                d.first = w.row_tile * kRowTile;
+                d.tile0 = w.tile0;
+                d.tile1 = w.tile1;
+                d.n = max(0, w.seen_tiles(p) - w.tile0);
+                // Row tiles of one head read the same keys: each CTA starts
+                // where the tile number is a multiple of the places a CTA
+                // takes, so that they read a key at about the same time and
+                // HBM gives it once (three row tiles over 131k tokens: 1.6 GB
+                // of reads become 0.5).
+                d.turn = 0;
+                if (w.w.row_tiles > 1 && !p.whole_items) {
+                    const int past = w.tile0 % w.each;
+                    if (past != 0 && w.each - past < d.n) d.turn = w.each - past;
+                }
+                d.slot = w.whole ? -1 : w.slot;
+                d.pad = 0;
+                publish(d);
+                const int keys = d.len + d.tokens;
                 const int held = min(b.held[w.s], b.table_width);
                 const int32_t* table = b.page_table + w.s * b.table_stride;
-                int page0 = (w.tile0 * kKeyTile) >> c.page_shift;
+                // Page ids of 32 pages, one a lane, and the 32 behind them on their way.
+                int page0 = (d.tile(0) * kKeyTile) >> c.page_shift;
                 int ids = page0 + lane < held ? table[page0 + lane] : -1;
                 int ids2 = page0 + 32 + lane < held ? table[page0 + 32 + lane] : -1;
                 int page_v = 0, slot_v = 0, used_v = 0;  // the previous tile's boxes, for its V
-                for (int tile = w.tile0; live && tile < end; ++tile) {
-                    const int pos0 = tile * kKeyTile, pos = pos0 + sub * box_slots;
-                    while ((pos0 >> c.page_shift) >= page0 + 32) {
-                        page0 += 32;
-                        ids = ids2;
+                for (int j = 0; live && j < d.n; ++j) {
+                    const int pos0 = d.tile(j) * kKeyTile, pos = pos0 + sub * box_slots;
+                    const int first = pos0 >> c.page_shift;
+                    if (first < page0 || first >= page0 + 32) {
+                        if (first == page0 + 32) {
+                            ids = ids2;
+                        } else {  // (back to the part's first tile)
+                            ids = first + lane < held ? table[first + lane] : -1;
+                        }
+                        page0 = first;
                         ids2 = page0 + 32 + lane < held ? table[page0 + 32 + lane] : -1;
                     }
                     const int used =
@@ -306,12 +391,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const int slot = pos & (c.page_size - 1);
                     load(&tk, page, slot, used);
-                    if (live && tile > w.tile0) load(&tv, page_v, slot_v, used_v);
+                    if (live && j > 0) load(&tv, page_v, slot_v, used_v);
                     page_v = page;
                     slot_v = slot;
                     used_v = used;
                 }
-                if (live && end > w.tile0) load(&tv, page_v, slot_v, used_v);
+                if (live && d.n > 0) load(&tv, page_v, slot_v, used_v);
+            }
+            if (live) {
+                Item d = {};
+                d.n = -1;
+                publish(d);
             }
             // No copy may be in flight when the CTA ends.
             if (*abort_flag)
@@ -323,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 1 && elect_one()) {
             // -------------------------------------------- issuer: one thread
             constexpr uint32_t kIdS = idesc_kv(kKeyTile, kType, false), kIdT = idesc_kv(D, kType, true);
-            int place0 = 0, it = 0, items = 0;  // ring place and tile number at the item's start
+            int place0 = 0, it = 0, with_keys = 0;  // ring place and tile number at the item's start
             bool live = true;
             auto scores = [&](int j) {
                 const int place = place0 + place_k(j), st = place % C::kSlots, buf = (it + j) & 1;
@@ -346,10 +436,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_commit(s_full + buf);
                 tc_commit(slot_free + st);
             };
-            for (; live && w.valid(); w.next(p, b, g, err)) {
-                const int n = w.seen_tiles(p) - w.tile0;
-                if (n <= 0) continue;
-                live = mbar_wait(q_full, items & 1, abort_flag, err, kDevErrTimeoutScore);
+            for (int count = 0; live; ++count) {
+                const int at = count % kItems;
+                live = mbar_wait(item_full + at, (count / kItems) & 1, abort_flag, err, kDevErrTimeoutScore);
+                if (!live) break;
+                const int n = *const_cast<volatile int*>(&items[at].n);
+                if (n < 0) break;
+                mbar_arrive(item_free + at);
+                if (n == 0) continue;
+                live = mbar_wait(q_full, with_keys & 1, abort_flag, err, kDevErrTimeoutScore);
                 scores(0);
                 for (int j = 0; live && j < n; ++j) {
                     if (j + 1 < n) scores(j + 1);
@@ -375,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 place0 += 2 * n;
                 it += n;
-                ++items;
+                ++with_keys;
             }
             // Tensor memory is given back only when every product is done.
             if (*abort_flag) {
@@ -391,10 +486,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int st_id = threadIdx.x - 32 * kFirstSoft;
         const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
         int place0 = 0, it = 0;
-        for (; w.valid(); w.next(p, b, g, err)) {
-            const int n = max(0, w.seen_tiles(p) - w.tile0);
-            const int rows = min(kRowTile, w.w.tokens * p.group - w.row_tile * kRowTile);
-            const int keys = w.w.len + w.w.tokens;
+        for (int count = 0;; ++count) {
+            const int at = count % kItems;
+            const bool got = mbar_wait(item_full + at, (count / kItems) & 1, abort_flag, err, kDevErrTimeoutScore);
+            if (soft_any(!got)) break;  // (all softmax threads leave together)
+            const Item& d = items[at];
+            const int n = d.n;
+            if (n < 0) break;
+            const int len = d.len, keys = len + d.tokens;
+            const int rows = min(kRowTile, d.tokens * p.group - d.first);
             // Up to 32 (64) rows stand in all four quadrants (in two pairs of
             // them), each with a quarter (half) of every tile's keys: all the
             // SM's schedulers work on the softmax, and the copies' results
@@ -404,43 +504,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int copy = quad / spread;
             const int r = quad % spread * 32 + lane;  // the thread's row of the tile
             const bool busy = quad % spread * 32 < rows;  // the warp has rows
-            const int my_row = w.row_tile * kRowTile + min(r, rows - 1);
-            const int tok = my_row / p.group;
             const int my_keys = kHalfKeys / copies, my_key = (2 * copy + half) * my_keys;
+            RowSight sight;
             float2 o[C::kHalfD / 2];
 #pragma unroll
             for (int i = 0; i < C::kHalfD / 2; ++i) o[i] = make_float2(0.f, 0.f);
             float m = -INFINITY, l = 0.f, f_last = 1.f;
-            if (n > 0) {
+            {
                 // Q of the item's rows: each thread its row's half of the
                 // channels.  Rows behind the last are zero.
-                const uint16_t* src = p.q + (w.w.row0 + tok) * p.q_row_stride +
-                                      ((int64_t)w.head * p.group + my_row % p.group) * D + half * C::kHalfD;
-                const bool ok = r < rows &&
-                                bc_global(bc, src, 2 * C::kHalfD, p.q,
-                                          2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D),
-                                          kBcAttnQ);
-                uint4 v[C::kHalfD / 8];
-#pragma unroll
-                for (int i = 0; i < C::kHalfD / 8; ++i)
-                    v[i] = ok ? load_q(p, src + 8 * i) : make_uint4(0, 0, 0, 0);
-                if constexpr (C::kQInTmem) {
-                    if (busy) {
-#pragma unroll
-                        for (int i = 0; i < C::kHalfD / 32; ++i)
-                            tmem_st16(tmem + lane_at + C::kQCol + half * (C::kHalfD / 2) + 16 * i,
-                                      reinterpret_cast<const uint32_t*>(v + 4 * i));
-                        tmem_wait_st();
-                        tc_fence_before();
-                    }
-                } else {
+                const int row = d.first + min(r, rows - 1), tok = token_of(p, row);
+                sight.open(p, d.row0, tok);
+                if (n > 0) {
+                    const uint16_t* src = p.q + (d.row0 + tok) * p.q_row_stride +
+                                          ((int64_t)d.head * p.group + row - tok * p.group) * D + half * C::kHalfD;
+                    const bool ok = r < rows &&
+                                    bc_global(bc, src, 2 * C::kHalfD, p.q,
+                                              2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D),
+                                              kBcAttnQ);
+                    uint4 v[C::kHalfD / 8];
 #pragma unroll
                     for (int i = 0; i < C::kHalfD / 8; ++i)
-                        sts_u128(base + C::kQ + unit_at(quad * 32 + lane, half * (C::kHalfD / 8) + i, kRowTile), v[i]);
-                    fence_proxy_async_smem();
+                        v[i] = ok ? load_q(p, src + 8 * i) : make_uint4(0, 0, 0, 0);
+                    if constexpr (C::kQInTmem) {
+                        if (busy) {
+#pragma unroll
+                            for (int i = 0; i < C::kHalfD / 32; ++i)
+                                tmem_st16(tmem + lane_at + C::kQCol + half * (C::kHalfD / 2) + 16 * i,
+                                          reinterpret_cast<const uint32_t*>(v + 4 * i));
+                            tmem_wait_st();
+                            tc_fence_before();
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < C::kHalfD / 8; ++i)
+                            sts_u128(base + C::kQ + unit_at(quad * 32 + lane, half * (C::kHalfD / 8) + i, kRowTile),
+                                     v[i]);
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_full);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
             }
             // O takes tile j's product while tile j + 1's is under way
             auto accumulate = [&](int i, float f) {
@@ -465,15 +569,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (int j = 0; j < n; ++j) {
                 const int i = it + j, buf = i & 1;
-                const int pos0 = (w.tile0 + j) * kKeyTile, key0 = pos0 + my_key;
+                const int pos0 = d.tile(j) * kKeyTile, key0 = pos0 + my_key;
                 mbar_wait(s_full + buf, (i >> 1) & 1, abort_flag, err, kDevErrTimeoutScore);
                 float f = 1.f;
                 if (busy) {
                     tc_fence_after();
                     const uint32_t s_at = tmem + lane_at + C::kScores + buf * C::kScoreCols;
                     uint32_t seen = 0xffffffffu;
-                    if (key0 + my_keys > w.w.len || key0 + my_keys > keys)
-                        seen = seen_bits(p, w.w.row0 + tok, tok, key0 - w.w.len, keys - key0);
+                    if (pos0 + kKeyTile > len) seen = sight.bits(p, key0 - len, keys - key0);
                     volatile float* mine = maxima + (buf * 2 + half) * kRowTile + quad * 32 + lane;
                     volatile float* theirs = maxima + (buf * 2 + (half ^ 1)) * kRowTile + quad * 32 + lane;
                     if (copies == 1) {
@@ -494,36 +597,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                     tc_fence_before();
                 }
-                if (pos0 + kKeyTile > w.w.len && (keys - pos0 < kKeyTile || w.w.tokens > 1)) {
+                if (pos0 + kKeyTile > len && (keys - pos0 < kKeyTile || keys - len > 1)) {
                     // Slots behind the end may hold anything, and so may tokens
                     // that some row does not see: a zero weight would carry their
                     // NaN and infinities into its sum.  Such values leave the
                     // tile; rows that do see them get them at the item's end.
                     const int place = place0 + place_v(j, n), st = place % C::kSlots;
                     mbar_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
-                    const int first_new = max(0, w.w.len - pos0), have = min(kKeyTile, keys - pos0);
+                    const int first_new = max(0, len - pos0), have = min(kKeyTile, keys - pos0);
                     bool odd = false;
+#pragma unroll 2
                     for (int u = first_new * (D / 8) + st_id; u < kKeyTile * (D / 8); u += kSoftThreads) {
                         const int key = u / (D / 8);
-                        const uint32_t at = base + st * C::kTileBytes + unit_at(key, u % (D / 8), kKeyTile);
-                        uint32_t v[4] = {0, 0, 0, 0};
-                        bool bad = key >= have;
-                        if (!bad) {
-                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                                         : "r"(at));
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 t = T::unpack(v[k]);
-                                const bool b0 = !isfinite(t.x), b1 = !isfinite(t.y);
-                                v[k] &= (b0 ? 0u : 0xffffu) | (b1 ? 0u : 0xffff0000u);
-                                bad |= b0 || b1;
-                            }
-                            odd |= bad;
+                        const uint32_t at_v = base + st * C::kTileBytes + unit_at(key, u % (D / 8), kKeyTile);
+                        if (key >= have) {
+                            sts_u128(at_v, make_uint4(0, 0, 0, 0));
+                            continue;
                         }
-                        if (bad) sts_u128(at, make_uint4(v[0], v[1], v[2], v[3]));
+                        uint32_t v[4];
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                     : "r"(at_v));
+                        if (any_odd<T>(v[0]) || any_odd<T>(v[1]) || any_odd<T>(v[2]) || any_odd<T>(v[3])) {
+                            odd = true;
+                            for (int k = 0; k < 8; ++k) {
+                                const float2 t = T::unpack(k & 1 ? v[k >> 1] >> 16 : v[k >> 1] & 0xffffu);
+                                if (!isfinite(t.x))
+                                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at_v + 2 * k), "h"((unsigned short)0)
+                                                 : "memory");
+                            }
+                        }
                     }
-                    if (odd) *odd_flag = 1;
+                    if (odd) odd_flag[count & 1] = 1;
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
@@ -534,42 +639,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n > 0) accumulate(it + n - 1, f_last);
             place0 += 2 * n;
             it += n;
+            // (Every thread is past the previous item: its flag serves the next.)
+            if (n > 0 && st_id == 0) odd_flag[(count & 1) ^ 1] = 0;
 
             // The row's maximum over its copies and sum over copies and
             // halves.  Buffer it & 1 is the one that the last tile did not
-            // use; the other is free once all threads are past that tile.
+            // use; the other is free once both halves are past that tile.
             float* all_m = maxima + (it & 1) * 2 * kRowTile;
-            float* all_l = half == 0 ? all_m + kRowTile : maxima + ((it & 1) ^ 1) * 2 * kRowTile;
-            const int at = quad * 32 + lane;
-            if (busy && half == 0) all_m[at] = m;
-            soft_sync();
-            const bool odd_values = *odd_flag != 0;
-            float top = m, fix = 1.f;
+            float* last_l = maxima + ((it & 1) ^ 1) * 2 * kRowTile;
+            const int lane_row = quad * 32 + lane;
+            float top = m, fix = 1.f, sum = 0.f;
             if (copies > 1) {
+                if (busy && half == 0) all_m[lane_row] = m;
+                soft_sync();
                 for (int i = 0; i < copies; ++i) top = fmaxf(top, all_m[(i * spread + quad % spread) * 32 + lane]);
                 fix = m == -INFINITY ? 0.f : fast_exp2(m - top);
                 if (m != -INFINITY) l *= fix;  // (else nothing was seen: 0, or NaN)
             }
-            if (busy) all_l[at] = l;
-            soft_sync();
-            if (st_id == 0) *odd_flag = 0;
-            float sum = 0.f;
+            if (busy) (half == 0 ? all_m + kRowTile : last_l)[lane_row] = l;
+            if (copies > 1) soft_sync();
+            else if (busy) pair_sync(quad);
             for (int i = 0; i < copies; ++i) {
                 const int from = (i * spread + quad % spread) * 32 + lane;
-                sum += all_m[kRowTile + from] + maxima[((it & 1) ^ 1) * 2 * kRowTile + from];
+                sum += all_m[kRowTile + from] + last_l[from];
             }
-            if (odd_values && busy && r < rows) {
+            const int row = d.first + min(r, rows - 1);
+            if (odd_flag[count & 1] != 0 && busy && r < rows) {
 #pragma unroll
                 for (int i = 0; i < C::kHalfD / 2; ++i) o[i] = make_float2(o[i].x * fix, o[i].y * fix);
                 fix = 1.f;
-                for (int t = 0; copy == 0 && t < w.w.tokens; ++t) {
-                    const int pos = w.w.len + t;
-                    if (pos < w.tile0 * kKeyTile || pos >= w.tile1 * kKeyTile ||
-                        !sees_new(p, w.w.row0 + tok, tok, t))
+                for (int t = 0; copy == 0 && t < d.tokens; ++t) {
+                    const int pos = len + t;
+                    if (pos < d.tile0 * kKeyTile || pos >= d.tile1 * kKeyTile ||
+                        !sees_new(p, sight.row, sight.token, t))
                         continue;
-                    const int page = page_of(c, b, w.s, pos, err);
+                    const int page = page_of(c, b, d.seq, pos, err);
                     if (page < 0) continue;
-                    const uint16_t* src = c.v + p.layer_offset + page * c.page_stride + w.head * c.head_stride +
+                    const uint16_t* src = c.v + p.layer_offset + page * c.page_stride + d.head * c.head_stride +
                                           (pos & (c.page_size - 1)) * c.slot_stride + half * C::kHalfD;
 #pragma unroll
                     for (int i = 0; i < C::kHalfD / 2; ++i) {
@@ -579,51 +685,76 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!w.whole && half == 0 && copy == 0 && r < rows)
-                p.part_ml[(int64_t)w.slot * p.slot_rows + r] = make_float2(top, sum);
-            // Out through shared memory, 16 channels at a time, so that four
-            // lanes write 64 bytes of a row; the copies' warps share the rows
-            // and add up the copies.
-            const float scale = !w.whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: zeros
-            const int64_t row_at = w.whole ? (w.w.row0 + tok) * p.out_row_stride +
-                                                 ((int64_t)w.head * p.group + my_row % p.group) * D
-                                           : ((int64_t)w.slot * p.slot_rows + r) * D;
-            float* const out = w.whole ? p.out : p.part_o;
-            float* const stage = reinterpret_cast<float*>(smem + C::kOut) + half * 4 * 32 * kStageRow;
+            const bool whole = d.slot < 0;
+            if (!whole && half == 0 && copy == 0 && r < rows)
+                p.part_ml[(int64_t)d.slot * p.slot_rows + r] = make_float2(top, sum);
+            const float scale = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: zeros
+            const int tok = sight.token;
+            const int64_t row_at = (whole ? (d.row0 + tok) * p.out_row_stride +
+                                                ((int64_t)d.head * p.group + row - tok * p.group) * D
+                                          : ((int64_t)d.slot * p.slot_rows + r) * D) + half * C::kHalfD;
+            float* const out = whole ? p.out : p.part_o;
+            const int64_t out_bytes = 4 * ((p.rows - 1) * p.out_row_stride + (int64_t)p.group * p.kv_heads * D);
+            if (copies == 1) {
+                float* dst = out + row_at;
+                if (r < rows && (!whole || bc_global(bc, dst, 4 * C::kHalfD, p.out, out_bytes, kBcAttnOut))) {
+                    if (!whole || p.wide_out) {
 #pragma unroll
-            for (int ch = 0; ch < C::kHalfD / kStageCols; ++ch) {
-                if (busy) {
-#pragma unroll
-                    for (int i = 0; i < kStageCols / 4; ++i) {
-                        const float2 a = o[ch * (kStageCols / 2) + 2 * i], z = o[ch * (kStageCols / 2) + 2 * i + 1];
-                        *reinterpret_cast<float4*>(stage + at * kStageRow + 4 * i) =
-                            make_float4(a.x * fix, a.y * fix, z.x * fix, z.y * fix);
-                    }
-                }
-                if (copies == 1) __syncwarp();
-                else soft_sync();
-                if (busy) {
-                    const int col = (lane & 3) * 4;
-                    for (int i = copy * spread; i < (copy + 1) * spread; ++i) {
-                        const int rr = i * 8 + (lane >> 2);  // row of the quadrant
-                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int k = 0; k < copies; ++k) {
-                            const float4 t = *reinterpret_cast<const float4*>(
-                                stage + ((k * spread + quad % spread) * 32 + rr) * kStageRow + col);
-                            v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+                        for (int i = 0; i < C::kHalfD / 8; ++i) {
+                            const float2* x = o + 4 * i;
+                            asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 8 * i),
+                                         "f"(x[0].x * scale), "f"(x[0].y * scale), "f"(x[1].x * scale),
+                                         "f"(x[1].y * scale), "f"(x[2].x * scale), "f"(x[2].y * scale),
+                                         "f"(x[3].x * scale), "f"(x[3].y * scale)
+                                         : "memory");
                         }
-                        const float f = __shfl_sync(0xffffffffu, scale, rr);
-                        float* dst = out + __shfl_sync(0xffffffffu, row_at, rr) + half * C::kHalfD + ch * kStageCols + col;
-                        if (quad % spread * 32 + rr < rows &&
-                            (!w.whole || bc_global(bc, dst, 16, p.out,
-                                                   4 * ((p.rows - 1) * p.out_row_stride +
-                                                        (int64_t)p.group * p.kv_heads * D), kBcAttnOut)))
-                            *reinterpret_cast<float4*>(dst) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < C::kHalfD / 4; ++i)
+                            *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(
+                                o[2 * i].x * scale, o[2 * i].y * scale, o[2 * i + 1].x * scale, o[2 * i + 1].y * scale);
                     }
                 }
-                if (copies == 1) __syncwarp();
-                else soft_sync();
+            } else {
+                // The copies' outputs meet in shared memory, kStageCols
+                // channels at a time; their warps share the rows.
+                constexpr int kCols = C::kStageCols, kPitch = C::kStageRow, kAcross = kCols / 4;
+                constexpr int kDown = 32 / kAcross;  // rows a warp reads at once
+                float* const stage = reinterpret_cast<float*>(smem + C::kOut) + half * kRowTile * kPitch;
+                const int mine_n = 32 / copies;      // rows of the quadrant that this copy's warp writes
+#pragma unroll
+                for (int ch = 0; ch < C::kHalfD / kCols; ++ch) {
+                    if (ch > 0) soft_sync();
+                    if (busy) {
+#pragma unroll
+                        for (int i = 0; i < kCols / 4; ++i) {
+                            const float2 x = o[ch * (kCols / 2) + 2 * i], y = o[ch * (kCols / 2) + 2 * i + 1];
+                            *reinterpret_cast<float4*>(stage + lane_row * kPitch + 4 * i) =
+                                make_float4(x.x * fix, x.y * fix, y.x * fix, y.y * fix);
+                        }
+                    }
+                    soft_sync();
+                    if (busy) {
+                        const int col = lane % kAcross * 4;
+                        for (int i = 0; i < mine_n; i += kDown) {
+                            const int rr = copy * mine_n + i + lane / kAcross;  // row of the quadrant
+                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                            for (int k = 0; k < copies; ++k) {
+                                const float4 t = *reinterpret_cast<const float4*>(
+                                    stage + ((k * spread + quad % spread) * 32 + rr) * kPitch + col);
+                                v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+                            }
+                            const float f = __shfl_sync(0xffffffffu, scale, rr);
+                            float* dst = out + __shfl_sync(0xffffffffu, row_at, rr) + ch * kCols + col;
+                            if (quad % spread * 32 + rr < rows &&
+                                (!whole || bc_global(bc, dst, 16, p.out, out_bytes, kBcAttnOut)))
+                                *reinterpret_cast<float4*>(dst) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+                        }
+                    }
+                }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(item_free + at);
         }
     }
     tc_fence_before();

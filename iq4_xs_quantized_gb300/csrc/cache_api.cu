@@ -122,7 +122,7 @@ int iq4xs_tree_attention(const iq4xs_tree_attention_args* a, const iq4xs_kv_cach
     if (a->q_row_stride > kMaxStride || a->out_row_stride > kMaxStride) return IQ4XS_ERR_ARG;
     if (!(a->scale > -1e30 && a->scale < 1e30)) return IQ4XS_ERR_ARG;
     if (a->tree_mask ? (a->mask_words < 1 || a->mask_words > 512) : a->mask_words != 0) return IQ4XS_ERR_ARG;
-    if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->tree_mask, 8) || !aligned(a->workspace, 16))
+    if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->tree_mask, 8) || !aligned(a->workspace, 32))
         return IQ4XS_ERR_ALIGN;
     int *err, sms;
     void* encode;
