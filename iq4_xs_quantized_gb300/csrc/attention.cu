@@ -11,13 +11,14 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-constexpr int kMmaRows = 16, kTcRows = 128;  // row tiles of the two forms
 constexpr int64_t kWholeTokens = 512;
+constexpr int kBoxSlots = 64;
+static_assert(sizeof(SplitOut) == 32, "partial results stay aligned");
 
 int mma_ctas(int64_t head_dim, int num_sms) { return head_dim == 256 ? num_sms : 2 * num_sms; }
 
 // One map over K or V of a layer: channels, then slot and head by rising
-// stride, then pages; boxes of 64 channels x the slots of a key tile in a page.
+// stride, then pages; boxes of 64 channels x up to 64 slots of a page.
 bool encode_kv(EncodeTiledFn enc, uint16_t* base, const CacheView& c, bool bf16, int* slot_axis, CUtensorMap* map) {
     const bool slot_first = c.slot_stride <= c.head_stride;
     *slot_axis = slot_first ? 1 : 2;
@@ -27,7 +28,7 @@ bool encode_kv(EncodeTiledFn enc, uint16_t* base, const CacheView& c, bool bf16,
                                 (cuuint64_t)c.pages};
     const cuuint64_t gstride[3] = {slot_first ? slot_b : head_b, slot_first ? head_b : slot_b,
                                    (cuuint64_t)c.page_stride * 2};
-    const cuuint32_t box_slots = (cuuint32_t)(c.page_size < kKeyTile ? c.page_size : kKeyTile);
+    const cuuint32_t box_slots = (cuuint32_t)(c.page_size < kBoxSlots ? c.page_size : kBoxSlots);
     const cuuint32_t box[4] = {64, slot_first ? box_slots : 1, slot_first ? 1 : box_slots, 1};
     const cuuint32_t estride[4] = {1, 1, 1, 1};
     return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, gdim, gstride,
@@ -41,16 +42,15 @@ bool encode_kv(EncodeTiledFn enc, uint16_t* base, const CacheView& c, bool bf16,
 // take every fourth part and add up in shared memory, in a fixed order.
 constexpr int kJoinWarps = 4;
 
-template <int D, int kRows>
+template <int D, class F>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     attention_join_kernel(const AttnParams p, const BatchView b, int* err) {
     constexpr int kPer = D / 32;
     __shared__ float acc_s[kJoinWarps][D];
-    // The attention kernel lets this grid start only behind its own wait for
-    // what came before, so lengths and offsets are final: only the partial
-    // results have to be waited for.
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x, head = blockIdx.y;
+    griddep_wait();
+    griddep_launch_dependents();
     int s = 0;
     for (int s0 = 0; s0 < b.sequences; s0 += 32) {
         const unsigned done =
@@ -58,25 +58,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
         s += __popc(done);
         if (done != 0xffffffffu) break;
     }
-    bool cut = s < b.sequences && row >= b.row_offsets[0];
-    int first = 0, last = 0, r = 0;
-    if (cut) {
-        const SeqWork w = seq_work<kRows>(p, b, s, err);
-        const Split split(p, work_before<kRows>(p, b, b.sequences, err));
-        cut = w.work > 0 && row >= w.row0;
-        if (cut) {
-            r = (row - w.row0) * p.group + head % p.group;
-            const int64_t x = work_before<kRows>(p, b, s, err) +
-                              ((int64_t)(head / p.group) * w.row_tiles + r / kRows) * w.key_tiles;
-            r %= kRows;
-            first = split.owner(x);
-            last = split.owner(x + w.key_tiles - 1);
-            cut = first != last;
-        }
-    }
-    griddep_wait();
-    griddep_launch_dependents();
-    if (!cut) return;
+    if (s >= b.sequences || row < b.row_offsets[0]) return;
+    const SeqWork w = seq_work<F>(p, b, s, err);
+    if (w.tokens == 0 || row < w.row0) return;
+    Split split;
+    static_cast<SplitOut&>(split) = *p.split_out;
+    const int unit = w.unit(split.cut);
+    if (unit == 1) return;
+    int64_t x = 0;
+    for (int s0 = 0; s0 < s; s0 += 32)
+        if (s0 + lane < s) x += seq_work<F>(p, b, s0 + lane, err).places(p, split.cut);
+    x = warp_sum(x);
+    const int kv_head = head / p.group;
+    int r = (row - w.row0) * p.group + head - kv_head * p.group;
+    x += ((int64_t)kv_head * w.row_tiles + r / F::kRows) * unit;
+    r %= F::kRows;
+    const int first = split.owner(x), last = split.owner(x + unit - 1);
+    if (first == last) return;
 
     float top = -INFINITY, sum = 0.f;
     for (int i = first + lane; i <= last; i += 32)
@@ -118,13 +116,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     }
 }
 
-template <int kRows>
-cudaError_t launch_join(const AttnParams& p, const BatchView& b, int q_heads, int* err, cudaStream_t stream) {
-    const dim3 grid((unsigned)p.rows, (unsigned)q_heads), block(32 * kJoinWarps);
+template <int D>
+cudaError_t launch_join_width(bool tc, const AttnParams& p, const BatchView& b, dim3 grid, int* err,
+                              cudaStream_t stream) {
+    const dim3 block(32 * kJoinWarps);
+    return tc ? launch_chained(attention_join_kernel<D, TcForm<D>>, grid, block, 0, stream, p, b, err)
+              : launch_chained(attention_join_kernel<D, MmaForm>, grid, block, 0, stream, p, b, err);
+}
+cudaError_t launch_join(bool tc, const AttnParams& p, const BatchView& b, int q_heads, int* err, cudaStream_t stream) {
+    const dim3 grid((unsigned)p.rows, (unsigned)q_heads);
     switch (p.head_dim) {
-        case 64: return launch_chained(attention_join_kernel<64, kRows>, grid, block, 0, stream, p, b, err);
-        case 128: return launch_chained(attention_join_kernel<128, kRows>, grid, block, 0, stream, p, b, err);
-        case 256: return launch_chained(attention_join_kernel<256, kRows>, grid, block, 0, stream, p, b, err);
+        case 64: return launch_join_width<64>(tc, p, b, grid, err, stream);
+        case 128: return launch_join_width<128>(tc, p, b, grid, err, stream);
+        case 256: return launch_join_width<256>(tc, p, b, grid, err, stream);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -140,10 +144,10 @@ int64_t tree_attention_workspace(int64_t rows, int64_t q_heads, int64_t kv_heads
                                  int num_sms) {
     // the larger of the two forms' (a call's own lengths choose the form)
     const int64_t group = q_heads / kv_heads;
-    const int64_t mma = 2 * (int64_t)mma_ctas(head_dim, num_sms) * slot_rows(kMmaRows, rows, group);
-    const int64_t tc = 2 * (int64_t)num_sms * slot_rows(kTcRows, rows, group);
+    const int64_t mma = 2 * (int64_t)mma_ctas(head_dim, num_sms) * slot_rows(MmaForm::kRows, rows, group);
+    const int64_t tc = 2 * (int64_t)num_sms * slot_rows(TcForm<64>::kRows, rows, group);
     const int64_t n = mma > tc ? mma : tc;
-    return align32(n * 8) + n * head_dim * 4;
+    return (int64_t)sizeof(SplitOut) + align32(n * 8) + n * head_dim * 4;
 }
 
 cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const CacheView& c, const BatchView& b, bool bf16,
@@ -162,21 +166,23 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     p.q_xor = a.scale < 0 ? 0x80008000u : 0u;
     p.group = group;
     p.group_magic = ((uint64_t(1) << 38) + group - 1) / group;
-    p.wide_out = (reinterpret_cast<uintptr_t>(a.out) % 32 == 0) && a.out_row_stride % 8 == 0;
     p.kv_heads = c.heads;
     p.mask_words = (int)a.mask_words;
     p.head_dim = c.head_dim;
     p.skip_stage = skip_stage;
     // Row tiles of 16 while a sequence's rows a key/value head fit one, of 128 beyond.
     const int64_t mean_rows = (a.rows + b.sequences - 1) / b.sequences * group;
-    const bool tc = mean_rows > kMmaRows;
-    const int row_tile = tc ? kTcRows : kMmaRows;
+    const bool tc = mean_rows > MmaForm::kRows;
+    const int row_tile = tc ? TcForm<64>::kRows : MmaForm::kRows;
     p.ctas = tc ? num_sms : mma_ctas(c.head_dim, num_sms);
     p.whole_items = (int64_t)b.table_width * c.page_size <= kWholeTokens;
     p.slot_rows = (int)slot_rows(row_tile, a.rows, group);
-    p.part_ml = static_cast<float2*>(a.workspace);
-    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
-                                        align32(2 * (int64_t)p.ctas * p.slot_rows * 8));
+    // Measured: starting and ending a part costs about 8 key tiles on tcgen05, 3 on the warp-level form.
+    p.part_tiles = tc ? 8 : 3;
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    p.split_out = reinterpret_cast<SplitOut*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(ws + sizeof(SplitOut));
+    p.part_o = reinterpret_cast<float*>(ws + sizeof(SplitOut) + align32(2 * (int64_t)p.ctas * p.slot_rows * 8));
     CUtensorMap tk, tv;
     const EncodeTiledFn enc = reinterpret_cast<EncodeTiledFn>(encode);
     if (!encode_kv(enc, c.k + p.layer_offset, c, bf16, &p.slot_axis, &tk) ||
@@ -185,8 +191,7 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     const cudaError_t e = tc ? launch_attention_tc(p, &tk, &tv, c, b, bf16, err, stream)
                              : launch_attention_mma(p, &tk, &tv, c, b, bf16, err, stream);
     if (e != cudaSuccess || p.whole_items) return e;
-    return tc ? launch_join<kTcRows>(p, b, (int)a.q_heads, err, stream)
-              : launch_join<kMmaRows>(p, b, (int)a.q_heads, err, stream);
+    return launch_join(tc, p, b, (int)a.q_heads, err, stream);
 }
 
 }  // namespace iq4xs

@@ -4,15 +4,21 @@
 //
 // Work.  An item is (sequence, row tile, key/value head): the rows are the
 // sequence's new tokens times the query heads that share the key/value head
-// (row r: token r / group, query head head * group + r % group), tiled by the
-// kernel's row tile; its keys come in tiles of kKeyTile positions.  The
-// (item, key tile) pairs of the whole batch lie on one line, of which every
-// CTA takes the same number of places, whatever the lengths.  An item that a boundary cuts is joined afterwards:
-// each CTA leaves at most two partial results, slot 2 g for the item whose
-// start lies before its range, 2 g + 1 for the one that it begins and does
-// not finish.  Where no sequence can be long (the table's width says so),
-// items are not cut and nothing is joined.  Lengths live on the device, so
-// every warp works the split out for itself, from the same numbers.
+// (row r: token r / group, query head head * group + r % group), in the
+// form's row tiles; its keys come in the form's key tiles.  Items lie on a
+// line in order, each with as many places as it may be cut into, and every
+// CTA takes the same number of places:
+//
+//   cut = 0          a place is a key tile: every CTA gets the same number of
+//                    tiles, whatever the lengths, and may cut two items
+//   cut = L          an item is L tiles at most a place, and there are no
+//                    more places than CTAs: a CTA has one part of one item
+//   cut = kWhole     items are not cut (short contexts)
+//
+// An item that is cut is joined afterwards: a CTA leaves at most two partial
+// results, slot 2 g for a part that does not begin its item, 2 g + 1 for one
+// that does.  Lengths live on the device, so the split is worked out there,
+// by every CTA from the same numbers.
 #pragma once
 
 #include <cuda.h>
@@ -21,12 +27,13 @@
 
 namespace iq4xs {
 
-constexpr int kKeyTile = 64;
+constexpr int kWhole = INT32_MAX;
 
 struct AttnParams {
     const uint16_t* q;
     float* out;
     const uint64_t* mask;
+    struct SplitOut* split_out;  // the split, for the join
     float* part_o;     // [2 G slots][slot_rows][D]
     float2* part_ml;   // [2 G slots][slot_rows] {max (log2 units), sum}
     int64_t q_row_stride, out_row_stride, rows;
@@ -35,9 +42,9 @@ struct AttnParams {
     uint32_t q_and, q_xor;  // the scale's sign (or zero), put on q: scores may be masked with -inf before scaling
     int group, kv_heads, mask_words, head_dim;
     uint64_t group_magic;  // ceil(2^38 / group): row / group by one multiplication
-    int wide_out;          // out and its rows are 32-byte aligned
     int ctas;          // CTAs the work is split over, at most
-    int whole_items;   // 1: items are not cut
+    int whole_items;   // 1: cut = kWhole
+    int part_tiles;    // what starting and ending a part costs, in key tiles
     int slot_rows;     // rows of a partial result: the row tile, or all rows if fewer
     int slot_axis;     // tensor-map axis of the slot (1 or 2; the head has the other)
     int skip_stage;    // test hook: this stage of every CTA is left unissued
@@ -51,13 +58,19 @@ __device__ __forceinline__ int token_of(const AttnParams& p, int r) {
 
 // One sequence as the split sees it.
 struct SeqWork {
-    int64_t work;  // (item, key tile) pairs, or items
     int row0, tokens, len, row_tiles, key_tiles;
-    int unit;      // places an item takes on the line: key_tiles, or 1
+    __device__ __forceinline__ int unit(int cut) const {  // places of an item
+        return cut == 0 ? key_tiles : cut == kWhole ? 1 : (key_tiles + cut - 1) / cut;
+    }
+    __device__ __forceinline__ int64_t items(const AttnParams& p) const {
+        return tokens > 0 ? (int64_t)row_tiles * p.kv_heads : 0;
+    }
+    __device__ __forceinline__ int64_t places(const AttnParams& p, int cut) const { return items(p) * unit(cut); }
 };
 
-// From the sequence's row offsets and length as they were read.
-template <int kRows>
+// F: kRows and kKeys of the form's tiles.  From the sequence's row offsets
+// and length as they were read.
+template <class F>
 __device__ __forceinline__ SeqWork seq_of(const AttnParams& p, int first, int last, int len, int* err) {
     SeqWork w;
     w.row0 = first;
@@ -71,55 +84,83 @@ __device__ __forceinline__ SeqWork seq_of(const AttnParams& p, int first, int la
         data_error(err, kDataLens);
         w.tokens = w.len = 0;
     }
-    w.row_tiles = (w.tokens * p.group + kRows - 1) / kRows;
-    w.key_tiles = (w.len + w.tokens + kKeyTile - 1) / kKeyTile;
-    w.unit = p.whole_items ? 1 : w.key_tiles;
-    w.work = w.tokens > 0 ? (int64_t)w.row_tiles * p.kv_heads * w.unit : 0;
+    w.row_tiles = (w.tokens * p.group + F::kRows - 1) / F::kRows;
+    w.key_tiles = (w.len + w.tokens + F::kKeys - 1) / F::kKeys;
     return w;
 }
-template <int kRows>
+// Sequence s (none behind the last: no tokens).
+template <class F>
 __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, const BatchView& b, int s, int* err) {
-    return seq_of<kRows>(p, b.row_offsets[s], b.row_offsets[s + 1], b.lens[s], err);
+    if (s < b.sequences) return seq_of<F>(p, b.row_offsets[s], b.row_offsets[s + 1], b.lens[s], err);
+    return seq_of<F>(p, 0, 0, 0, err);
 }
-
-// The batch's work up to (not including) sequence n: 32 sequences a step, one
-// a lane; the result is the same in every lane.
-template <int kRows>
-__device__ __forceinline__ int64_t work_before(const AttnParams& p, const BatchView& b, int n, int* err) {
-    const int lane = threadIdx.x & 31;
-    int64_t sum = 0;
-    for (int s0 = 0; s0 < n; s0 += 32)
-        if (s0 + lane < n) sum += seq_work<kRows>(p, b, s0 + lane, err).work;
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
-
 // a / b for a that mostly fits 32 bits (a 64-bit division costs ten times one of 32).
 __device__ __forceinline__ int64_t div_small(int64_t a, int b) {
     return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
-// The split of W places over G CTAs: every CTA W / G of them, the first W % G
-// one more.  No more CTAs than places, so that no range is empty.
-struct Split {
-    int64_t each, more;  // W / G, W % G
-    int ctas;
-    __device__ __forceinline__ Split(const AttnParams& p, int64_t work) {
-        ctas = (int)min((int64_t)p.ctas, work);
-        each = ctas > 0 ? div_small(work, ctas) : 0;
-        more = work - each * ctas;
-    }
+
+// The split: `cut` as above, W places over `ctas` CTAs (no more than places,
+// so that none is empty): each W / ctas of them, the first `more` one more.
+struct SplitOut {
+    int64_t each, more;
+    int cut, ctas;
+    int64_t pad;
+};
+struct Split : SplitOut {
     __device__ __forceinline__ int64_t start(int g) const { return each * g + min((int64_t)g, more); }
     __device__ __forceinline__ int owner(int64_t x) const {
         const int64_t in_more = more * (each + 1);
-        return x < in_more ? (int)(x / (each + 1)) : (int)(more + (x - in_more) / each);
+        return (int)(x < in_more ? x / (each + 1) : more + (x - in_more) / each);
+    }
+    // By a whole warp, 32 sequences a step, one a lane (`mine`: the lane's
+    // among the first 32, read by the caller).
+    template <class F>
+    __device__ __forceinline__ void plan(const AttnParams& p, const BatchView& b, const SeqWork& mine, int* err) {
+        const int lane = threadIdx.x & 31;
+        int64_t tiles = mine.places(p, 0), items = mine.items(p);
+        for (int s0 = 32; s0 < b.sequences; s0 += 32) {
+            const SeqWork w = seq_work<F>(p, b, s0 + lane, err);
+            tiles += w.places(p, 0);
+            items += w.items(p);
+        }
+        tiles = warp_sum(tiles);
+        items = warp_sum(items);
+        cut = p.whole_items ? kWhole : 0;
+        int64_t places = p.whole_items ? items : tiles;
+        // Parts of one item each, if the longest is not behind an even share
+        // by more than the second part costs that a CTA has without them.
+        if (!p.whole_items && items <= p.ctas && items > 0) {
+            const int share = (int)div_small(tiles + p.ctas - 1, p.ctas);
+            const int step = max(1, p.part_tiles / 4);
+            for (int len = share; len <= share + p.part_tiles; len += step) {
+                int64_t n = mine.places(p, len);
+                for (int s0 = 32; s0 < b.sequences; s0 += 32)
+                    n += seq_work<F>(p, b, s0 + lane, err).places(p, len);
+                n = warp_sum(n);
+                if (n <= p.ctas) {
+                    cut = len;
+                    places = n;
+                    break;
+                }
+            }
+        }
+        ctas = (int)min((int64_t)p.ctas, places);
+        each = ctas > 0 ? div_small(places, ctas) : 0;
+        more = places - each * ctas;
+        pad = 0;
     }
 };
 
 // A CTA's walk over its range, item by item.
-template <int kRows>
+template <class F>
 struct WorkWalk {
-    int64_t left;        // places of the range from the current item's part on
+    Split split;
+    int64_t left;        // places of the range from the current part on
     SeqWork w;
     int s;
     int row_end, next_end, next_len;  // offsets and length behind the sequence, read ahead
@@ -128,20 +169,12 @@ struct WorkWalk {
     bool whole;          // this CTA has all of the item's key tiles
     int slot;            // of its partial result, if not
 
-    int each;            // places of a CTA (the split's)
-
     __device__ __forceinline__ void start(const AttnParams& p, const BatchView& b, int g, int* err) {
-        // running sums of 32 sequences at a time; those of the first 32 are kept
         const int lane = threadIdx.x & 31;
-        int64_t total = 0, sums = 0;
-        for (int s0 = 0; s0 < b.sequences; s0 += 32) {
-            const int64_t v = scan(s0 + lane < b.sequences ? seq_work<kRows>(p, b, s0 + lane, err).work : 0, lane);
-            if (s0 == 0) sums = v;
-            total += __shfl_sync(0xffffffffu, v, 31);
-        }
-        const Split split(p, total);
+        const SeqWork mine = seq_work<F>(p, b, lane, err);
+        split.plan<F>(p, b, mine, err);
         left = 0;
-        each = (int)min(split.each, (int64_t)INT32_MAX);
+        if (g == 0 && lane == 0) *p.split_out = split;
         if (g >= split.ctas) return;
         const int64_t x = split.start(g);
         left = split.start(g + 1) - x;
@@ -149,8 +182,12 @@ struct WorkWalk {
         int64_t before = 0, seq_x = 0;
         s = 0;
         for (int s0 = 0; s0 < b.sequences; s0 += 32) {
-            if (s0 > 0)
-                sums = scan(s0 + lane < b.sequences ? seq_work<kRows>(p, b, s0 + lane, err).work : 0, lane);
+            int64_t sums = (s0 == 0 ? mine : seq_work<F>(p, b, s0 + lane, err)).places(p, split.cut);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, sums, o);
+                if (lane >= o) sums += y;
+            }
             const unsigned past = __ballot_sync(0xffffffffu, before + sums > x);
             if (past != 0) {
                 const int k = __ffs(past) - 1;
@@ -162,21 +199,13 @@ struct WorkWalk {
             before += __shfl_sync(0xffffffffu, sums, 31);
         }
         row_end = b.row_offsets[s + 1];
-        w = seq_of<kRows>(p, b.row_offsets[s], row_end, b.lens[s], err);
+        w = seq_of<F>(p, b.row_offsets[s], row_end, b.lens[s], err);
         read_ahead(b);
-        const int item = (int)div_small(x - seq_x, w.unit);
-        tile0 = (int)(x - seq_x - (int64_t)item * w.unit);
+        const int unit = w.unit(split.cut);
+        const int item = (int)div_small(x - seq_x, unit);
         head = item / w.row_tiles;
         row_tile = item - head * w.row_tiles;
-        set(p, g);
-    }
-    static __device__ __forceinline__ int64_t scan(int64_t v, int lane) {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += y;
-        }
-        return v;
+        set((int)(x - seq_x - (int64_t)item * unit), unit, g);
     }
     __device__ __forceinline__ void read_ahead(const BatchView& b) {
         if (s + 1 < b.sequences) {
@@ -184,39 +213,45 @@ struct WorkWalk {
             next_len = b.lens[s + 1];
         }
     }
-    __device__ __forceinline__ void set(const AttnParams& p, int g) {
-        tile1 = p.whole_items ? w.key_tiles : (int)min((int64_t)w.key_tiles, tile0 + left);
+    // The part that begins at the item's place `at` of `unit`.
+    __device__ __forceinline__ void set(int at, int unit, int g) {
+        if (split.cut == 0) {
+            tile0 = at;
+            tile1 = (int)min((int64_t)w.key_tiles, at + left);
+        } else {
+            tile0 = (int)((int64_t)at * w.key_tiles / unit);
+            tile1 = (int)((int64_t)(at + 1) * w.key_tiles / unit);
+        }
         whole = tile0 == 0 && tile1 == w.key_tiles;
         slot = 2 * g + (tile0 == 0 ? 1 : 0);
     }
     __device__ __forceinline__ bool valid() const { return left > 0; }
     __device__ __forceinline__ void next(const AttnParams& p, const BatchView& b, int g, int* err) {
-        left -= p.whole_items ? 1 : tile1 - tile0;
+        left -= split.cut == 0 ? tile1 - tile0 : 1;
         if (left <= 0) return;
-        tile0 = 0;
         if (++row_tile == w.row_tiles) {
             row_tile = 0;
             if (++head == p.kv_heads) {
                 head = 0;
                 do {  // (sequences without work are passed over)
                     ++s;
-                    w = seq_of<kRows>(p, row_end, next_end, next_len, err);
+                    w = seq_of<F>(p, row_end, next_end, next_len, err);
                     row_end = next_end;
                     read_ahead(b);
-                } while (w.work == 0);
+                } while (w.tokens == 0);
             }
         }
-        set(p, g);
+        set(0, split.cut == 0 ? w.key_tiles : 1, g);
     }
     // Key tiles that a row of this item can see: without a mask (a chain) the
     // row tile's last token ends them.
     __device__ __forceinline__ int seen_tiles(const AttnParams& p) const {
         int keys = w.len + w.tokens;
         if (p.mask == nullptr) {
-            const int last = min(w.tokens - 1, token_of(p, (row_tile + 1) * kRows - 1));
+            const int last = min(w.tokens - 1, token_of(p, (row_tile + 1) * F::kRows - 1));
             keys = w.len + last + 1;
         }
-        return min(tile1, (keys + kKeyTile - 1) / kKeyTile);
+        return min(tile1, (keys + F::kKeys - 1) / F::kKeys);
     }
 };
 
@@ -349,6 +384,16 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
                                           int code) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code)) != 0;
 }
+
+// The forms' tiles: row tiles of 16 or 128; 128 keys a tile where two tiles of
+// K, of V and of scores fit the SM, 64 at 256 channels.
+struct MmaForm {
+    static constexpr int kRows = 16, kKeys = 64;
+};
+template <int D>
+struct TcForm {
+    static constexpr int kRows = 128, kKeys = D == 256 ? 64 : 128;
+};
 
 // Launchers of the two forms (csrc/attention_mma.cu, csrc/attention_tc.cu).
 cudaError_t launch_attention_mma(const AttnParams& p, const void* tk, const void* tv, const CacheView& c,

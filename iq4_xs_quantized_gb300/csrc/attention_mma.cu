@@ -18,7 +18,7 @@
 namespace iq4xs {
 namespace {
 
-constexpr int kRowTile = 16;
+constexpr int kRowTile = MmaForm::kRows, kKeyTile = MmaForm::kKeys;
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kWarpKeys = kKeyTile / kConsumers;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
     __syncthreads();
     griddep_wait();  // lengths, tables, q and the cache's newest rows come from earlier launches
     griddep_launch_dependents();
-    WorkWalk<kRowTile> w;
+    WorkWalk<MmaForm> w;
     w.start(p, b, g, err);
 
     if (warp == kConsumers) {

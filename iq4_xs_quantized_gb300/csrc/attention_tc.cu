@@ -1,11 +1,11 @@
 // attention_tc.cu -- tree attention for many rows a key/value head (drafted
-// trees, prompt chunks): tcgen05 on tiles of 128 rows x 64 keys.
+// trees, prompt chunks): tcgen05 on tiles of 128 rows x 128 keys (64 at 256 channels).
 //
 // One pass, as in the warp-level form; here a row is a lane of tensor memory:
 //
-//   S = Q K^T      128 x 64, Q from tensor memory, K from shared memory
+//   S = Q K^T      Q from tensor memory (shared where that is full), K from shared
 //   P = exp2(S - m) split into 16-bit parts, back into tensor memory over S
-//   T = P V        128 x D, P from tensor memory, V from shared memory (as it
+//   T = P V        P from tensor memory, V from shared memory (as it
 //                  lies: channels contiguous)
 //   O = O f + T    in fp32 registers of the threads that own the row
 //
@@ -13,27 +13,26 @@
 // arithmetic: the tensor core cuts its sums off, and thousands of tiles on
 // one accumulator would add those cuts up.
 //
-// Roles: a producer warp (TMA), a warp whose first lane issues the MMAs, and
-// eight softmax warps, two per 32-lane quadrant: one takes keys 0-31 of a
-// tile and channels 0..D/2-1 of O, the other the rest; they share a row's
+// Roles: two producer warps, one thread that issues the MMAs, and eight
+// softmax warps, two per 32-lane quadrant: one takes the first half of a
+// tile's keys and of O's channels, the other the rest; they share a row's
 // maximum through shared memory.  The MMAs of tile j + 1's scores are issued
 // before tile j's output product, so the tensor core works while the softmax
-// runs.  K and V tiles go through one ring in the order the MMAs take them:
-// K0 K1 V0 K2 V1 ... V(n-1).
+// runs.  K and V tiles go through one ring in the order the MMAs take them,
+// K0 K1 V0 K2 V1 ... V(n-1), K by one warp and V by another (TMA).
 //
 // Up to about 48 rows HBM bounds it (4 D bytes a key), above that the tensor
-// core (1 + parts products of 128 x 64 x D a tile).
+// core (1 + parts products of 128 x tile x D) and the softmax.
 #include "attention.cuh"
 
 namespace iq4xs {
 namespace {
 
-constexpr int kRowTile = 128;
+constexpr int kRowTile = TcForm<64>::kRows;
 constexpr int kSoftWarps = 8;
 constexpr int kFirstSoft = 4;  // warps 4-11: two whole warpgroups
 constexpr int kThreads = 32 * (kFirstSoft + kSoftWarps);
 constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kHalfKeys = kKeyTile / 2;
 constexpr int kTmemCols = 512;
 constexpr int kItems = 4;  // item descriptors in flight
 
@@ -51,38 +50,43 @@ static_assert(sizeof(Item) % 16 == 0, "descriptors stay aligned");
 
 template <int D, class T>
 struct TcAttn {
+    static constexpr int kTile = TcForm<D>::kKeys;           // keys a tile
     static constexpr int kParts = Parts<T>::kN;
     static constexpr int kChunks = D / 64;
-    static constexpr int kTileBytes = kKeyTile * D * 2;
-    static constexpr int kTBufs = D == 256 ? 1 : 2;          // output products in flight
-    // Tensor memory: T; Q (16-bit pairs), except where 512 columns do not
-    // hold it; two score buffers: S (64 columns), overlaid in place by P: the
-    // first two parts of 16 keys take the keys' own 16 columns, a third 8 more.
-    static constexpr int kScoreCols = kParts == 3 ? 96 : 64;
+    static constexpr int kChunkStride = kTile * kChunkBytes;
+    static constexpr int kTileBytes = kTile * D * 2;
+    // Tensor memory: T (two of them where 512 columns hold them); Q in 16-bit
+    // pairs, if they hold it; two score buffers: S, overlaid in place by P:
+    // the first two parts of 16 keys take the keys' own 16 columns, a third 8
+    // more behind S.
+    static constexpr int kScoreCols = kParts == 3 ? kTile * 3 / 2 : kTile;
+    static constexpr int kTBufs = 2 * D + 2 * kScoreCols <= kTmemCols ? 2 : 1;
     static constexpr bool kQInTmem = kTBufs * D + D / 2 + 2 * kScoreCols <= kTmemCols;
     static constexpr int kQCol = kTBufs * D;
     static constexpr int kScores = kQCol + (kQInTmem ? D / 2 : 0);
     static_assert(kScores + 2 * kScoreCols <= kTmemCols, "tensor memory");
     // shared memory
     static constexpr int kQBytes = kQInTmem ? 0 : kRowTile * D * 2;
-    static constexpr int kStageCols = kQInTmem ? 32 : 16;    // channels of a row joined at a time, and their pitch
+    static constexpr int kStageCols = kQInTmem ? 32 : 16;    // channels of a row on its way out, and their pitch
     static constexpr int kStageRow = kStageCols + 4;
     static constexpr int kStageBytes = kSoftThreads * kStageRow * 4;
-    static constexpr int kSlots = (224 * 1024 - kQBytes - kStageBytes) / kTileBytes;  // 5 (4 with Q), 11, 23
+    static constexpr int kSlots = (224 * 1024 - kQBytes - kStageBytes) / kTileBytes;
     static constexpr int kQ = kSlots * kTileBytes;
-    static constexpr int kOut = kQ + kQBytes;                // the copies' outputs on their way together
+    static constexpr int kOut = kQ + kQBytes;                // rows on their way out (and Q's into tensor memory)
     static constexpr int kMax = kOut + kStageBytes;          // [2][2 halves][128] row maxima
     static constexpr int kDesc = kMax + 2 * 2 * kRowTile * 4;
     static constexpr int kBars = kDesc + kItems * (int)sizeof(Item);
     static constexpr int kNumBars = 2 * kSlots + 2 * kItems + 2 + 2 + 2 + 2 + 1 + 1;
     static constexpr int kMisc = kBars + kNumBars * 8;       // tensor memory address, abort, odd values
-    static constexpr int kSmem = kMisc + 16;
+    static constexpr int kLast = kMisc + 16;                 // the last place loaded into each slot
+    static constexpr int kSmem = kLast + kSlots * 4;
+    static_assert(kSlots >= 4, "K and V of two tiles");
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static constexpr int kHalfD = D / 2;
     static constexpr int kHold = D == 256 ? 16 : 32;         // scores a thread holds at a time
     // Column of a part of the weights of keys 16 key16 .. + 15, from the buffer's first.
     static __device__ __forceinline__ uint32_t p_col(int key16, int part) {
-        return part < 2 ? 16 * key16 + 8 * part : kKeyTile + 8 * key16;
+        return part < 2 ? 16 * key16 + 8 * part : kTile + 8 * key16;
     }
 };
 // D = 256 keeps 128 output channels a softmax thread: the producer's and the
@@ -164,25 +168,32 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* v) {
 // The thread's kKeys scores of a tile -> weights, written over them as parts.
 //   s_at   the score buffer's first column in the thread's lane
 //   key    the thread's first key in the tile
-//   seen   bit k: the row sees key + k
+//   masked some row of the tile sees less than all of it; then the first
+//          key's place among the new tokens is j0, and `have` keys lie
+//          before the end
 //   mine, theirs  where the thread and the one that has the row's other half leave their maxima
 // m, l: running maximum (log2 units) and sum.  Returns the factor for what O holds.
 template <int D, class T, int kKeys>
-__device__ __forceinline__ float weigh(const AttnParams& p, uint32_t s_at, int key, uint32_t seen,
-                                       volatile float* mine, volatile float* theirs, int quad, float& m, float& l) {
+__device__ __forceinline__ float weigh(const AttnParams& p, const RowSight& sight, bool masked, int j0, int have,
+                                       uint32_t s_at, int key, volatile float* mine, volatile float* theirs, int quad,
+                                       float& m, float& l) {
     using C = TcAttn<D, T>;
-    constexpr int kHold = kKeys == 32 ? C::kHold : kKeys;  // scores held at a time
-    constexpr int kStep = kKeys < 16 ? kKeys : 16;
+    constexpr int kHold = kKeys < C::kHold ? kKeys : C::kHold;  // scores held at a time
+    constexpr int kStep = kHold < 16 ? kHold : 16;
     uint32_t x[kHold];
+    auto read = [&](int h) {
+        tmem_ld_wait<kHold>(s_at + key + h, x);
+        if (masked) {
+            const uint32_t seen = sight.bits(p, j0 + h, have - h);
+#pragma unroll
+            for (int k = 0; k < kHold; ++k)
+                if (!(seen >> k & 1)) x[k] = 0xff800000u;  // -inf
+        }
+    };
     float mx = -INFINITY;
 #pragma unroll
     for (int h = 0; h < kKeys; h += kHold) {
-        tmem_ld_wait<kHold>(s_at + key + h, x);
-        if (seen != 0xffffffffu) {
-#pragma unroll
-            for (int k = 0; k < kHold; ++k)
-                if (!(seen >> (h + k) & 1)) x[k] = 0xff800000u;  // -inf
-        }
+        read(h);
         mx = max_of<kHold>(x, mx);
     }
     *mine = mx;
@@ -198,34 +209,51 @@ __device__ __forceinline__ float weigh(const AttnParams& p, uint32_t s_at, int k
     const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), shift2 = make_float2(shift, shift);
     float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int h = 0; h < kKeys; h += kStep) {
-        if constexpr (kHold < kKeys) {  // (read again: a thread's weights lie over its own scores only)
-            tmem_ld_wait<kStep>(s_at + key + h, x);
-            if (seen != 0xffffffffu) {
+    for (int h = kKeys - kHold; h >= 0; h -= kHold) {  // (the last ones are still here)
+        if (h < kKeys - kHold) read(h);                // (a thread's weights lie over its own scores only)
 #pragma unroll
-                for (int k = 0; k < kStep; ++k)
-                    if (!(seen >> (h + k) & 1)) x[k] = 0xff800000u;
+        for (int h2 = 0; h2 < kHold; h2 += kStep) {
+            uint32_t part[C::kParts][kStep / 2];
+#pragma unroll
+            for (int k = 0; k < kStep / 2; ++k) {
+                const uint32_t* xk = x + h2 + 2 * k;
+                float2 a = fma2(make_float2(__uint_as_float(xk[0]), __uint_as_float(xk[1])), scale2, shift2);
+                a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+                l2 = add2(l2, a);
+                uint32_t out[C::kParts];
+                Parts<T>::split(a, out);
+#pragma unroll
+                for (int i = 0; i < C::kParts; ++i) part[i][k] = out[i];
             }
+            const int at = key + h + h2;
+#pragma unroll
+            for (int i = 0; i < C::kParts; ++i)
+                tmem_st<kStep / 2>(s_at + C::p_col(at / 16, i) + at % 16 / 2, part[i]);
         }
-        uint32_t part[C::kParts][kStep / 2];
-#pragma unroll
-        for (int k = 0; k < kStep / 2; ++k) {
-            const uint32_t* xk = x + (kHold < kKeys ? 0 : h) + 2 * k;
-            float2 a = fma2(make_float2(__uint_as_float(xk[0]), __uint_as_float(xk[1])), scale2, shift2);
-            a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-            l2 = add2(l2, a);
-            uint32_t out[C::kParts];
-            Parts<T>::split(a, out);
-#pragma unroll
-            for (int i = 0; i < C::kParts; ++i) part[i][k] = out[i];
-        }
-#pragma unroll
-        for (int i = 0; i < C::kParts; ++i)
-            tmem_st<kStep / 2>(s_at + C::p_col((key + h) / 16, i) + (key + h) % 16 / 2, part[i]);
     }
     l += l2.x + l2.y;
     return f;
 }
+// Page ids of 32 pages of a sequence, one a lane, and the 32 behind them on their way.
+struct PageWindow {
+    const int32_t* table;
+    int held, first, ids, ids2;
+    __device__ __forceinline__ int read(int page) const { return page < held ? table[page] : -1; }
+    __device__ __forceinline__ void open(const BatchView& b, int s) {
+        table = b.page_table + s * b.table_stride;
+        held = min(b.held[s], b.table_width);
+        first = -64;
+        ids2 = -1;
+    }
+    // Brings the window over `page`, a tile's first; by a whole warp.
+    __device__ __forceinline__ void move(int page, int lane) {
+        if (page >= first && page < first + 32) return;
+        ids = page == first + 32 ? ids2 : read(page + lane);
+        first = page;
+        ids2 = read(page + 32 + lane);
+    }
+    __device__ __forceinline__ int id(int page) const { return __shfl_sync(0xffffffffu, ids, (page - first) & 31); }
+};
 // Places in the ring of tile j's K and V, an item of n tiles starting at place 0.
 __device__ __forceinline__ int place_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int place_v(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
@@ -256,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_at + 1);
     volatile int* odd_flag = abort_flag + 1;  // [2]: an item met NaN or infinities among the new tokens' values
+    volatile int* last_place = reinterpret_cast<volatile int*>(smem + C::kLast);
     Item* items = reinterpret_cast<Item*>(smem + C::kDesc);
     float* maxima = reinterpret_cast<float*>(smem + C::kMax);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.x;
@@ -265,10 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(full + i, 1);
             mbar_init(slot_free + i, 1);
+            last_place[i] = -1;
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(item_full + i, 1);
-            mbar_init(item_free + i, kSoftWarps + 1);
+            mbar_init(item_free + i, kSoftWarps + 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
@@ -294,35 +324,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kFirstSoft) {
         if constexpr (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        // One tile of K or V into its place of the ring, by a whole warp: a
+        // box of up to 64 slots x 64 channels a lane.  False: a wait ran out.
+        const int box_slots = min(c.page_size, 64);
+        const int boxes = C::kTile / box_slots * C::kChunks;  // at most 16
+        const uint32_t box_bytes = box_slots * kChunkBytes;
+        const int sub = lane / C::kChunks, chunk = lane % C::kChunks;
+        const uint32_t dst0 = base + chunk * C::kChunkStride + sub * box_bytes;
+        auto load = [&](const void* map, const Item& d, int tile, int place, PageWindow& pages) {
+            const int st = place % C::kSlots, pos0 = tile * C::kTile, pos = pos0 + sub * box_slots;
+            pages.move(pos0 >> c.page_shift, lane);
+            int page = pages.id(pos >> c.page_shift);
+            const int used = min(
+                boxes, (min(C::kTile, d.len + d.tokens - pos0) + box_slots - 1) / box_slots * C::kChunks);
+            if (place >= C::kSlots &&
+                !warp_wait(slot_free + st, ((place / C::kSlots) - 1) & 1, abort_flag, err, kDevErrTimeoutKvSlot))
+                return false;
+            if (place == p.skip_stage) return true;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(full + st, used * box_bytes);
+                last_place[st] = place;
+            }
+            __syncwarp();
+            if (lane < used) {
+                if (page < 0 || page >= c.pages) {
+                    data_error(err, kDataPage);
+                    page = c.pages;  // outside the map: zeros
+                }
+                const int slot = pos & (c.page_size - 1);
+                bc_tma(bc, chunk * 64, 2, 64, D, slot, c.page_size, kBcAttnKv, kBcAttnKv);
+                tma_load_4d(dst0 + st * C::kTileBytes, map, chunk * 64, p.slot_axis == 1 ? slot : d.head,
+                            p.slot_axis == 1 ? d.head : slot, page, full + st);
+            }
+            __syncwarp();
+            return true;
+        };
         if (warp == 0) {
-            // ------------------------------------------------------ producer
-            const int box_slots = min(c.page_size, kKeyTile);
-            const int boxes = kKeyTile / box_slots * C::kChunks;  // at most 16: one a lane
-            const uint32_t box_bytes = box_slots * kChunkBytes;
-            const int sub = lane / C::kChunks, chunk = lane % C::kChunks;
-            const uint32_t dst0 = base + chunk * kKeyTile * kChunkBytes + sub * box_bytes;
-            WorkWalk<kRowTile> w;
+            // ------------------------------------------ producer: items and K
+            WorkWalk<TcForm<D>> w;
             w.start(p, b, g, err);
-            int place = 0, count = 0;  // in the ring, and items, over all of them
+            int place0 = 0, count = 0;  // ring place at the item's start, items so far
             bool live = true;
-            auto load = [&](const void* map, int page, int slot, int used) {
-                const int st = place % C::kSlots;
-                if (place >= C::kSlots && !warp_wait(slot_free + st, ((place / C::kSlots) - 1) & 1, abort_flag, err,
-                                                     kDevErrTimeoutKvSlot)) {
-                    live = false;
-                    return;
-                }
-                const bool skip = place == p.skip_stage;
-                if (lane == 0 && !skip) mbar_arrive_expect_tx(full + st, used * box_bytes);
-                __syncwarp();
-                if (lane < used && !skip) {
-                    const int y = p.slot_axis == 1 ? slot : w.head, z = p.slot_axis == 1 ? w.head : slot;
-                    bc_tma(bc, chunk * 64, 2, 64, D, slot, c.page_size, kBcAttnKv, kBcAttnKv);
-                    tma_load_4d(dst0 + st * C::kTileBytes, map, chunk * 64, y, z, page, full + st);
-                }
-                __syncwarp();
-                ++place;
-            };
+            PageWindow pages;
             // The next item's descriptor, when a place for it is free.
             auto publish = [&](const Item& d) {
                 const int at = count % kItems;
@@ -350,69 +393,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 d.tile1 = w.tile1;
                 d.n = max(0, w.seen_tiles(p) - w.tile0);
                 // Row tiles of one head read the same keys: each CTA starts
-                // where the tile number is a multiple of the places a CTA
-                // takes, so that they read a key at about the same time and
-                // HBM gives it once (three row tiles over 131k tokens: 1.6 GB
-                // of reads become 0.5).
+                // where the tile number is a multiple of a CTA's share, so
+                // that they read a key at about the same time and HBM gives
+                // it once (three row tiles over 131k tokens: 1.6 GB of reads
+                // become 0.5).
                 d.turn = 0;
-                if (w.w.row_tiles > 1 && !p.whole_items) {
-                    const int past = w.tile0 % w.each;
-                    if (past != 0 && w.each - past < d.n) d.turn = w.each - past;
+                if (w.w.row_tiles > 1 && w.split.cut == 0) {
+                    const int each = (int)min(w.split.each, (int64_t)INT32_MAX), past = w.tile0 % each;
+                    if (past != 0 && each - past < d.n) d.turn = each - past;
                 }
                 d.slot = w.whole ? -1 : w.slot;
                 d.pad = 0;
                 publish(d);
-                const int keys = d.len + d.tokens;
-                const int held = min(b.held[w.s], b.table_width);
-                const int32_t* table = b.page_table + w.s * b.table_stride;
-                // Page ids of 32 pages, one a lane, and the 32 behind them on their way.
-                int page0 = (d.tile(0) * kKeyTile) >> c.page_shift;
-                int ids = page0 + lane < held ? table[page0 + lane] : -1;
-                int ids2 = page0 + 32 + lane < held ? table[page0 + 32 + lane] : -1;
-                int page_v = 0, slot_v = 0, used_v = 0;  // the previous tile's boxes, for its V
-                for (int j = 0; live && j < d.n; ++j) {
-                    const int pos0 = d.tile(j) * kKeyTile, pos = pos0 + sub * box_slots;
-                    const int first = pos0 >> c.page_shift;
-                    if (first < page0 || first >= page0 + 32) {
-                        if (first == page0 + 32) {
-                            ids = ids2;
-                        } else {  // (back to the part's first tile)
-                            ids = first + lane < held ? table[first + lane] : -1;
-                        }
-                        page0 = first;
-                        ids2 = page0 + 32 + lane < held ? table[page0 + 32 + lane] : -1;
-                    }
-                    const int used =
-                        min(boxes, (min(kKeyTile, keys - pos0) + box_slots - 1) / box_slots * C::kChunks);
-                    int page = __shfl_sync(0xffffffffu, ids, ((pos >> c.page_shift) - page0) & 31);
-                    if (lane < used && (page < 0 || page >= c.pages)) {
-                        data_error(err, kDataPage);
-                        page = c.pages;  // outside the map: zeros
-                    }
-                    const int slot = pos & (c.page_size - 1);
-                    load(&tk, page, slot, used);
-                    if (live && j > 0) load(&tv, page_v, slot_v, used_v);
-                    page_v = page;
-                    slot_v = slot;
-                    used_v = used;
-                }
-                if (live && d.n > 0) load(&tv, page_v, slot_v, used_v);
+                pages.open(b, d.seq);
+                for (int j = 0; live && j < d.n; ++j) live = load(&tk, d, d.tile(j), place0 + place_k(j), pages);
+                place0 += 2 * d.n;
             }
             if (live) {
                 Item d = {};
                 d.n = -1;
                 publish(d);
             }
-            // No copy may be in flight when the CTA ends.
-            if (*abort_flag)
-                for (int i = max(0, place - C::kSlots); i < place; ++i)
-                    if (i != p.skip_stage) {
-                        int no_abort = 0;
-                        mbar_wait(full + i % C::kSlots, (i / C::kSlots) & 1, &no_abort, err, kDevErrTimeoutKv);
-                    }
+        } else if (warp == 2) {
+            // ---------------------------------------------------- producer: V
+            int place0 = 0;
+            bool live = true;
+            PageWindow pages;
+            for (int count = 0; live; ++count) {
+                const int at = count % kItems;
+                if (!warp_wait(item_full + at, (count / kItems) & 1, abort_flag, err, kDevErrTimeoutScore)) break;
+                const Item d = items[at];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(item_free + at);
+                if (d.n < 0) break;
+                pages.open(b, d.seq);
+                for (int j = 0; live && j < d.n; ++j) live = load(&tv, d, d.tile(j), place0 + place_v(j, d.n), pages);
+                place0 += 2 * d.n;
+            }
         } else if (warp == 1 && elect_one()) {
             // -------------------------------------------- issuer: one thread
-            constexpr uint32_t kIdS = idesc_kv(kKeyTile, kType, false), kIdT = idesc_kv(D, kType, true);
+            constexpr uint32_t kIdS = idesc_kv(C::kTile, kType, false), kIdT = idesc_kv(D, kType, true);
             int place0 = 0, it = 0, with_keys = 0;  // ring place and tile number at the item's start
             bool live = true;
             auto scores = [&](int j) {
@@ -424,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t s_at = tmem + C::kScores + buf * C::kScoreCols;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t kd = k_desc + (((k / 4) * kKeyTile * kChunkBytes + (k % 4) * 32) >> 4);
+                    const uint64_t kd = k_desc + (((k / 4) * C::kChunkStride + (k % 4) * 32) >> 4);
                     if constexpr (C::kQInTmem)
                         tc_mma_f16_ta(s_at, tmem + C::kQCol + 8 * k, kd, kIdS, k > 0);
                     else
@@ -457,12 +477,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     live = live && mbar_wait(p_full + buf, (i >> 1) & 1, abort_flag, err, kDevErrTimeoutScore);
                     if (!live) break;
                     tc_fence_after();
-                    const uint64_t v_desc = desc_sw128(base + st * C::kTileBytes, kKeyTile * kChunkBytes, 1024);
+                    const uint64_t v_desc = desc_sw128(base + st * C::kTileBytes, C::kChunkStride, 1024);
                     const uint32_t p_at = tmem + C::kScores + buf * C::kScoreCols, t_at = tmem + tb * D;
 #pragma unroll
                     for (int part = kParts - 1; part >= 0; --part)  // the smallest parts first
 #pragma unroll
-                        for (int k = 0; k < kKeyTile / 16; ++k)
+                        for (int k = 0; k < C::kTile / 16; ++k)
                             tc_mma_f16_ta(t_at, p_at + C::p_col(k, part), v_desc + ((k * 16 * kChunkBytes) >> 4), kIdT,
                                           part < kParts - 1 || k > 0);
                     tc_commit(t_full + tb);
@@ -504,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int copy = quad / spread;
             const int r = quad % spread * 32 + lane;  // the thread's row of the tile
             const bool busy = quad % spread * 32 < rows;  // the warp has rows
-            const int my_keys = kHalfKeys / copies, my_key = (2 * copy + half) * my_keys;
+            const int my_keys = C::kTile / 2 / copies, my_key = (2 * copy + half) * my_keys;
             RowSight sight;
             float2 o[C::kHalfD / 2];
 #pragma unroll
@@ -515,31 +535,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // channels.  Rows behind the last are zero.
                 const int row = d.first + min(r, rows - 1), tok = token_of(p, row);
                 sight.open(p, d.row0, tok);
+                // All threads, neighbours on neighbouring 16 bytes of a row.
                 if (n > 0) {
-                    const uint16_t* src = p.q + (d.row0 + tok) * p.q_row_stride +
-                                          ((int64_t)d.head * p.group + row - tok * p.group) * D + half * C::kHalfD;
-                    const bool ok = r < rows &&
-                                    bc_global(bc, src, 2 * C::kHalfD, p.q,
-                                              2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D),
-                                              kBcAttnQ);
-                    uint4 v[C::kHalfD / 8];
+                    constexpr int kUnits = kRowTile * (D / 8) / kSoftThreads;
+                    uint4 v[kUnits];
 #pragma unroll
-                    for (int i = 0; i < C::kHalfD / 8; ++i)
-                        v[i] = ok ? load_q(p, src + 8 * i) : make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < kUnits; ++i) {
+                        const int u = st_id + i * kSoftThreads, at_row = u / (D / 8);
+                        // (into shared memory as the quadrants have them, copies and all)
+                        const int from = C::kQInTmem ? at_row : at_row / 32 % spread * 32 + at_row % 32;
+                        const int q_row = d.first + from, t = token_of(p, q_row);
+                        const uint16_t* src = p.q + (d.row0 + t) * p.q_row_stride +
+                                              ((int64_t)d.head * p.group + q_row - t * p.group) * D + u % (D / 8) * 8;
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (from < rows &&
+                            bc_global(bc, src, 16, p.q,
+                                      2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D), kBcAttnQ))
+                            v[i] = load_q(p, src);
+                    }
                     if constexpr (C::kQInTmem) {
-                        if (busy) {
+                        // through the staging rows, 64 channels of each half (or all) at a time
+                        constexpr int kPitch = C::kStageRow * 4, kPiece = C::kHalfD < 64 ? C::kHalfD : 64;
+                        uint8_t* const stage = smem + C::kOut;
 #pragma unroll
-                            for (int i = 0; i < C::kHalfD / 32; ++i)
-                                tmem_st16(tmem + lane_at + C::kQCol + half * (C::kHalfD / 2) + 16 * i,
-                                          reinterpret_cast<const uint32_t*>(v + 4 * i));
-                            tmem_wait_st();
-                            tc_fence_before();
+                        for (int c0 = 0; c0 < C::kHalfD; c0 += kPiece) {
+                            if (c0 > 0) soft_sync();
+#pragma unroll
+                            for (int i = 0; i < kUnits; ++i) {
+                                const int u = st_id + i * kSoftThreads, at_row = u / (D / 8), col = u % (D / 8) * 8;
+                                const int in_half = col % C::kHalfD - c0;
+                                if (in_half >= 0 && in_half < kPiece)
+                                    *reinterpret_cast<uint4*>(stage + (col / C::kHalfD * kRowTile + at_row) * kPitch +
+                                                              in_half * 2) = v[i];
+                            }
+                            soft_sync();
+                            if (busy) {
+                                uint4 mine[kPiece / 8];
+#pragma unroll
+                                for (int i = 0; i < kPiece / 8; ++i)
+                                    mine[i] = *reinterpret_cast<const uint4*>(stage + (half * kRowTile + r) * kPitch +
+                                                                              16 * i);
+#pragma unroll
+                                for (int i = 0; i < kPiece / 32; ++i)
+                                    tmem_st16(tmem + lane_at + C::kQCol + (half * C::kHalfD + c0) / 2 + 16 * i,
+                                              reinterpret_cast<const uint32_t*>(mine + 4 * i));
+                            }
                         }
+                        if (busy) tmem_wait_st();
+                        tc_fence_before();
                     } else {
 #pragma unroll
-                        for (int i = 0; i < C::kHalfD / 8; ++i)
-                            sts_u128(base + C::kQ + unit_at(quad * 32 + lane, half * (C::kHalfD / 8) + i, kRowTile),
-                                     v[i]);
+                        for (int i = 0; i < kUnits; ++i) {
+                            const int u = st_id + i * kSoftThreads;
+                            sts_u128(base + C::kQ + unit_at(u / (D / 8), u % (D / 8), kRowTile), v[i]);
+                        }
                         fence_proxy_async_smem();
                     }
                     __syncwarp();
@@ -569,26 +618,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (int j = 0; j < n; ++j) {
                 const int i = it + j, buf = i & 1;
-                const int pos0 = d.tile(j) * kKeyTile, key0 = pos0 + my_key;
+                const int pos0 = d.tile(j) * C::kTile, key0 = pos0 + my_key;
                 mbar_wait(s_full + buf, (i >> 1) & 1, abort_flag, err, kDevErrTimeoutScore);
                 float f = 1.f;
                 if (busy) {
                     tc_fence_after();
                     const uint32_t s_at = tmem + lane_at + C::kScores + buf * C::kScoreCols;
-                    uint32_t seen = 0xffffffffu;
-                    if (pos0 + kKeyTile > len) seen = sight.bits(p, key0 - len, keys - key0);
+                    const bool masked = pos0 + C::kTile > len;
                     volatile float* mine = maxima + (buf * 2 + half) * kRowTile + quad * 32 + lane;
                     volatile float* theirs = maxima + (buf * 2 + (half ^ 1)) * kRowTile + quad * 32 + lane;
+                    const int j0 = key0 - len, have = keys - key0;
+                    constexpr int kK = C::kTile / 2;
                     if (copies == 1) {
-                        f = weigh<D, T, 32>(p, s_at, my_key, seen, mine, theirs, quad, m, l);
+                        f = weigh<D, T, kK>(p, sight, masked, j0, have, s_at, my_key, mine, theirs, quad, m, l);
                     } else {
-                        f = copies == 2 ? weigh<D, T, 16>(p, s_at, my_key, seen, mine, theirs, quad, m, l)
-                                        : weigh<D, T, 8>(p, s_at, my_key, seen, mine, theirs, quad, m, l);
+                        f = copies == 2
+                                ? weigh<D, T, kK / 2>(p, sight, masked, j0, have, s_at, my_key, mine, theirs, quad, m, l)
+                                : weigh<D, T, kK / 4>(p, sight, masked, j0, have, s_at, my_key, mine, theirs, quad, m, l);
                         // the other copies' keys weigh nothing in these lanes
                         const uint32_t zero[16] = {};
-                        const int own = 4 / copies;  // 16-key groups of a copy
+                        const int own = C::kTile / 16 / copies;  // 16-key groups of a copy
 #pragma unroll
-                        for (int k = 0; k < kKeyTile / 16; ++k)
+                        for (int k = 0; k < C::kTile / 16; ++k)
                             if (k / own != copy && (k & 1) == half) {
                                 tmem_st<16>(s_at + 16 * k, zero);
                                 if constexpr (kParts == 3) tmem_st<8>(s_at + C::p_col(k, 2), zero);
@@ -597,19 +648,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                     tc_fence_before();
                 }
-                if (pos0 + kKeyTile > len && (keys - pos0 < kKeyTile || keys - len > 1)) {
+                if (pos0 + C::kTile > len && (keys - pos0 < C::kTile || keys - len > 1)) {
                     // Slots behind the end may hold anything, and so may tokens
                     // that some row does not see: a zero weight would carry their
                     // NaN and infinities into its sum.  Such values leave the
                     // tile; rows that do see them get them at the item's end.
                     const int place = place0 + place_v(j, n), st = place % C::kSlots;
                     mbar_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
-                    const int first_new = max(0, len - pos0), have = min(kKeyTile, keys - pos0);
+                    const int first_new = max(0, len - pos0), have = min(C::kTile, keys - pos0);
                     bool odd = false;
 #pragma unroll 2
-                    for (int u = first_new * (D / 8) + st_id; u < kKeyTile * (D / 8); u += kSoftThreads) {
+                    for (int u = first_new * (D / 8) + st_id; u < C::kTile * (D / 8); u += kSoftThreads) {
                         const int key = u / (D / 8);
-                        const uint32_t at_v = base + st * C::kTileBytes + unit_at(key, u % (D / 8), kKeyTile);
+                        const uint32_t at_v = base + st * C::kTileBytes + unit_at(key, u % (D / 8), C::kTile);
                         if (key >= have) {
                             sts_u128(at_v, make_uint4(0, 0, 0, 0));
                             continue;
@@ -670,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fix = 1.f;
                 for (int t = 0; copy == 0 && t < d.tokens; ++t) {
                     const int pos = len + t;
-                    if (pos < d.tile0 * kKeyTile || pos >= d.tile1 * kKeyTile ||
+                    if (pos < d.tile0 * C::kTile || pos >= d.tile1 * C::kTile ||
                         !sees_new(p, sight.row, sight.token, t))
                         continue;
                     const int page = page_of(c, b, d.seq, pos, err);
@@ -695,61 +746,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           : ((int64_t)d.slot * p.slot_rows + r) * D) + half * C::kHalfD;
             float* const out = whole ? p.out : p.part_o;
             const int64_t out_bytes = 4 * ((p.rows - 1) * p.out_row_stride + (int64_t)p.group * p.kv_heads * D);
-            if (copies == 1) {
-                float* dst = out + row_at;
-                if (r < rows && (!whole || bc_global(bc, dst, 4 * C::kHalfD, p.out, out_bytes, kBcAttnOut))) {
-                    if (!whole || p.wide_out) {
+            // Out through shared memory, kStageCols channels at a time, so
+            // that neighbouring lanes write a row's neighbouring bytes; the
+            // copies meet there and their warps share the rows.
+            constexpr int kCols = C::kStageCols, kPitch = C::kStageRow, kAcross = kCols / 4;
+            constexpr int kDown = 32 / kAcross;  // rows a warp writes at once
+            float* const stage = reinterpret_cast<float*>(smem + C::kOut) + half * kRowTile * kPitch;
+            const int share = 32 / copies;       // rows of the quadrant that this copy's warp writes
 #pragma unroll
-                        for (int i = 0; i < C::kHalfD / 8; ++i) {
-                            const float2* x = o + 4 * i;
-                            asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 8 * i),
-                                         "f"(x[0].x * scale), "f"(x[0].y * scale), "f"(x[1].x * scale),
-                                         "f"(x[1].y * scale), "f"(x[2].x * scale), "f"(x[2].y * scale),
-                                         "f"(x[3].x * scale), "f"(x[3].y * scale)
-                                         : "memory");
-                        }
-                    } else {
+            for (int ch = 0; ch < C::kHalfD / kCols; ++ch) {
+                if (copies == 1) __syncwarp();
+                else if (ch > 0) soft_sync();
+                if (busy) {
 #pragma unroll
-                        for (int i = 0; i < C::kHalfD / 4; ++i)
-                            *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(
-                                o[2 * i].x * scale, o[2 * i].y * scale, o[2 * i + 1].x * scale, o[2 * i + 1].y * scale);
+                    for (int i = 0; i < kCols / 4; ++i) {
+                        const float2 x = o[ch * (kCols / 2) + 2 * i], y = o[ch * (kCols / 2) + 2 * i + 1];
+                        *reinterpret_cast<float4*>(stage + lane_row * kPitch + 4 * i) =
+                            make_float4(x.x * fix, x.y * fix, y.x * fix, y.y * fix);
                     }
                 }
-            } else {
-                // The copies' outputs meet in shared memory, kStageCols
-                // channels at a time; their warps share the rows.
-                constexpr int kCols = C::kStageCols, kPitch = C::kStageRow, kAcross = kCols / 4;
-                constexpr int kDown = 32 / kAcross;  // rows a warp reads at once
-                float* const stage = reinterpret_cast<float*>(smem + C::kOut) + half * kRowTile * kPitch;
-                const int mine_n = 32 / copies;      // rows of the quadrant that this copy's warp writes
-#pragma unroll
-                for (int ch = 0; ch < C::kHalfD / kCols; ++ch) {
-                    if (ch > 0) soft_sync();
-                    if (busy) {
-#pragma unroll
-                        for (int i = 0; i < kCols / 4; ++i) {
-                            const float2 x = o[ch * (kCols / 2) + 2 * i], y = o[ch * (kCols / 2) + 2 * i + 1];
-                            *reinterpret_cast<float4*>(stage + lane_row * kPitch + 4 * i) =
-                                make_float4(x.x * fix, x.y * fix, y.x * fix, y.y * fix);
+                if (copies == 1) __syncwarp();
+                else soft_sync();
+                if (busy) {
+                    const int col = lane % kAcross * 4;
+#pragma unroll 2
+                    for (int i = 0; i < share; i += kDown) {
+                        const int rr = copy * share + i + lane / kAcross;  // row of the quadrant
+                        float4 v = *reinterpret_cast<const float4*>(stage + (quad % spread * 32 + rr) * kPitch + col);
+                        for (int k = 1; k < copies; ++k) {
+                            const float4 t = *reinterpret_cast<const float4*>(
+                                stage + ((k * spread + quad % spread) * 32 + rr) * kPitch + col);
+                            v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
                         }
-                    }
-                    soft_sync();
-                    if (busy) {
-                        const int col = lane % kAcross * 4;
-                        for (int i = 0; i < mine_n; i += kDown) {
-                            const int rr = copy * mine_n + i + lane / kAcross;  // row of the quadrant
-                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                            for (int k = 0; k < copies; ++k) {
-                                const float4 t = *reinterpret_cast<const float4*>(
-                                    stage + ((k * spread + quad % spread) * 32 + rr) * kPitch + col);
-                                v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
-                            }
-                            const float f = __shfl_sync(0xffffffffu, scale, rr);
-                            float* dst = out + __shfl_sync(0xffffffffu, row_at, rr) + ch * kCols + col;
-                            if (quad % spread * 32 + rr < rows &&
-                                (!whole || bc_global(bc, dst, 16, p.out, out_bytes, kBcAttnOut)))
-                                *reinterpret_cast<float4*>(dst) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-                        }
+                        const float f = __shfl_sync(0xffffffffu, scale, rr);
+                        float* dst = out + __shfl_sync(0xffffffffu, row_at, rr) + ch * kCols + col;
+                        if (quad % spread * 32 + rr < rows &&
+                            (!whole || bc_global(bc, dst, 16, p.out, out_bytes, kBcAttnOut)))
+                            *reinterpret_cast<float4*>(dst) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
                     }
                 }
             }
@@ -760,6 +793,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // No copy may be in flight when the CTA ends; all were waited for, unless
+    // a wait ran out.
+    if (*abort_flag && warp == 0)
+        for (int i = 0; i < C::kSlots; ++i)
+            if (last_place[i] >= 0) {
+                int no_abort = 0;
+                mbar_wait(full + i, (last_place[i] / C::kSlots) & 1, &no_abort, err, kDevErrTimeoutKv);
+            }
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
