@@ -49,8 +49,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     __shared__ float acc_s[kJoinWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x, head = blockIdx.y;
-    griddep_wait();
-    griddep_launch_dependents();
+    // The attention kernel lets this grid start behind its own wait for what
+    // came before, so offsets and lengths are final; the split and the
+    // partial results are not.
     int s = 0;
     for (int s0 = 0; s0 < b.sequences; s0 += 32) {
         const unsigned done =
@@ -58,20 +59,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
         s += __popc(done);
         if (done != 0xffffffffu) break;
     }
-    if (s >= b.sequences || row < b.row_offsets[0]) return;
-    const SeqWork w = seq_work<F>(p, b, s, err);
-    if (w.tokens == 0 || row < w.row0) return;
+    const bool mine = s < b.sequences && row >= b.row_offsets[0];
+    const SeqWork w = seq_work<F>(p, b, mine ? s : b.sequences, err);
+    const SeqWork lane_w = seq_work<F>(p, b, lane < s ? lane : b.sequences, err);
+    const int kv_head = token_of(p, head);  // (head / group)
+    int r = (row - w.row0) * p.group + head - kv_head * p.group;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (!mine || w.tokens == 0 || row < w.row0) return;
     Split split;
     static_cast<SplitOut&>(split) = *p.split_out;
     const int unit = w.unit(split.cut);
     if (unit == 1) return;
-    int64_t x = 0;
-    for (int s0 = 0; s0 < s; s0 += 32)
+    int64_t x = lane_w.places(p, split.cut);
+    for (int s0 = 32; s0 < s; s0 += 32)
         if (s0 + lane < s) x += seq_work<F>(p, b, s0 + lane, err).places(p, split.cut);
-    x = warp_sum(x);
-    const int kv_head = head / p.group;
-    int r = (row - w.row0) * p.group + head - kv_head * p.group;
-    x += ((int64_t)kv_head * w.row_tiles + r / F::kRows) * unit;
+    x = warp_sum(x) + ((int64_t)kv_head * w.row_tiles + r / F::kRows) * unit;
     r %= F::kRows;
     const int first = split.owner(x), last = split.owner(x + unit - 1);
     if (first == last) return;
@@ -166,6 +169,7 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     p.q_xor = a.scale < 0 ? 0x80008000u : 0u;
     p.group = group;
     p.group_magic = ((uint64_t(1) << 38) + group - 1) / group;
+    p.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_row_stride % 8 == 0;
     p.kv_heads = c.heads;
     p.mask_words = (int)a.mask_words;
     p.head_dim = c.head_dim;

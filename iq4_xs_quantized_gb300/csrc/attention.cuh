@@ -42,6 +42,7 @@ struct AttnParams {
     uint32_t q_and, q_xor;  // the scale's sign (or zero), put on q: scores may be masked with -inf before scaling
     int group, kv_heads, mask_words, head_dim;
     uint64_t group_magic;  // ceil(2^38 / group): row / group by one multiplication
+    int wide_out;      // out and its rows are 32-byte aligned
     int ctas;          // CTAs the work is split over, at most
     int whole_items;   // 1: cut = kWhole
     int part_tiles;    // what starting and ending a part costs, in key tiles
@@ -95,14 +96,17 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, const BatchView
     return seq_of<F>(p, 0, 0, 0, err);
 }
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
+    if (__all_sync(0xffffffffu, v < (int64_t(1) << 26)))  // (one instruction where 32 of them fit 31 bits)
+        return (int64_t)__reduce_add_sync(0xffffffffu, (unsigned)v);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-// a / b for a that mostly fits 32 bits (a 64-bit division costs ten times one of 32).
-__device__ __forceinline__ int64_t div_small(int64_t a, int b) {
-    return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+// a / b, both mostly of 32 bits (a 64-bit division costs ten times one of 32).
+__device__ __forceinline__ int64_t div_long(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
+__device__ __forceinline__ int64_t div_small(int64_t a, int b) { return div_long(a, b); }
 
 // The split: `cut` as above, W places over `ctas` CTAs (no more than places,
 // so that none is empty): each W / ctas of them, the first `more` one more.
@@ -115,7 +119,7 @@ struct Split : SplitOut {
     __device__ __forceinline__ int64_t start(int g) const { return each * g + min((int64_t)g, more); }
     __device__ __forceinline__ int owner(int64_t x) const {
         const int64_t in_more = more * (each + 1);
-        return (int)(x < in_more ? x / (each + 1) : more + (x - in_more) / each);
+        return (int)(x < in_more ? div_long(x, each + 1) : more + div_long(x - in_more, each));
     }
     // By a whole warp, 32 sequences a step, one a lane (`mine`: the lane's
     // among the first 32, read by the caller).
@@ -183,10 +187,20 @@ struct WorkWalk {
         s = 0;
         for (int s0 = 0; s0 < b.sequences; s0 += 32) {
             int64_t sums = (s0 == 0 ? mine : seq_work<F>(p, b, s0 + lane, err)).places(p, split.cut);
+            if (__all_sync(0xffffffffu, sums < (int64_t(1) << 26))) {
+                int v = (int)sums;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, sums, o);
-                if (lane >= o) sums += y;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v += y;
+                }
+                sums = v;
+            } else {
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, sums, o);
+                    if (lane >= o) sums += y;
+                }
             }
             const unsigned past = __ballot_sync(0xffffffffu, before + sums > x);
             if (past != 0) {
@@ -219,8 +233,8 @@ struct WorkWalk {
             tile0 = at;
             tile1 = (int)min((int64_t)w.key_tiles, at + left);
         } else {
-            tile0 = (int)((int64_t)at * w.key_tiles / unit);
-            tile1 = (int)((int64_t)(at + 1) * w.key_tiles / unit);
+            tile0 = (int)div_small((int64_t)at * w.key_tiles, unit);
+            tile1 = (int)div_small((int64_t)(at + 1) * w.key_tiles, unit);
         }
         whole = tile0 == 0 && tile1 == w.key_tiles;
         slot = 2 * g + (tile0 == 0 ? 1 : 0);
@@ -379,10 +393,23 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
         : "memory");
 }
-// mbar_wait by a whole warp, with one answer for all of its lanes.
+// mbar_wait whose first probe does not suspend (most phases are complete when
+// they are asked for).
+__device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0 || mbar_wait(bar, parity, abort_flag, err, code);
+}
+// kv_wait by a whole warp, with one answer for all of its lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
                                           int code) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code)) != 0;
+    return __all_sync(0xffffffffu, kv_wait(bar, parity, abort_flag, err, code)) != 0;
 }
 
 // The forms' tiles: row tiles of 16 or 128; 128 keys a tile where two tiles of

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
                 if (i != p.skip_stage) {
                     int no_abort = 0;
                     mbar_wait(k_full + i % C::kStages, (i / C::kStages) & 1, &no_abort, err, kDevErrTimeoutKv);
-                    mbar_wait(v_full + i % C::kStages, (i / C::kStages) & 1, &no_abort, err, kDevErrTimeoutKv);
+                    kv_wait(v_full + i % C::kStages, (i / C::kStages) & 1, &no_abort, err, kDevErrTimeoutKv);
                 }
         }
         return;
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
             const uint32_t k_s = base + st * C::kStageBytes, v_s = k_s + C::kTileBytes;
             const int key0 = tile * kKeyTile + warp * kWarpKeys;  // the warp's first position
             const int have = min(kWarpKeys, keys - key0);          // its positions before the end
-            mbar_wait(k_full + st, par, abort_flag, err, kDevErrTimeoutKv);
+            kv_wait(k_full + st, par, abort_flag, err, kDevErrTimeoutKv);
             if (have > 0) {
                 float s[2][2][4];  // [even, odd k step][8 keys][fragment]
 #pragma unroll
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
                     l[r] += (e[r][0] + e[r][1]) + (e[r][2] + e[r][3]);
                 }
 
-                mbar_wait(v_full + st, par, abort_flag, err, kDevErrTimeoutKv);
+                kv_wait(v_full + st, par, abort_flag, err, kDevErrTimeoutKv);
                 if (hidden || have < kWarpKeys) {
                     // Slots behind the end may hold anything, and so may tokens
                     // that a row does not see: a zero weight would still carry
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
                     }
                 }
             } else {
-                mbar_wait(v_full + st, par, abort_flag, err, kDevErrTimeoutKv);
+                kv_wait(v_full + st, par, abort_flag, err, kDevErrTimeoutKv);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(slot_free + st);

@@ -254,6 +254,54 @@ struct PageWindow {
     }
     __device__ __forceinline__ int id(int page) const { return __shfl_sync(0xffffffffu, ids, (page - first) & 31); }
 };
+// Takes NaN and infinities out of a V tile's keys first .. have - 1, and
+// everything out of those behind; all softmax threads.  True where a thread
+// found some among the former.
+template <int D, class T>
+__device__ __noinline__ bool scrub_tile(uint32_t tile, int first, int have, int thread) {
+    constexpr int kTile = TcForm<D>::kKeys;
+    bool odd = false;
+    for (int u = first * (D / 8) + thread; u < kTile * (D / 8); u += kSoftThreads) {
+        const int key = u / (D / 8);
+        const uint32_t at = tile + unit_at(key, u % (D / 8), kTile);
+        if (key >= have) {
+            sts_u128(at, make_uint4(0, 0, 0, 0));
+            continue;
+        }
+        uint32_t v[4];
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at));
+        if (any_odd<T>(v[0]) || any_odd<T>(v[1]) || any_odd<T>(v[2]) || any_odd<T>(v[3])) {
+            odd = true;
+            for (int k = 0; k < 8; ++k) {
+                const float2 t = T::unpack(k & 1 ? v[k >> 1] >> 16 : v[k >> 1] & 0xffffu);
+                if (!isfinite(t.x))
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 2 * k), "h"((unsigned short)0) : "memory");
+            }
+        }
+    }
+    return odd;
+}
+// Adds to n channels of a row's output the NaN and infinities of the new
+// tokens in tiles tile0 .. tile1 - 1 that it sees (their finite values are in
+// it already).
+template <int D, class T>
+__device__ __noinline__ void add_odd(const AttnParams& p, const CacheView& c, const BatchView& b, const Item& d,
+                                     int row, int token, float* out, int channel, int n, int* err) {
+    for (int t = 0; t < d.tokens; ++t) {
+        const int pos = d.len + t;
+        if (pos < d.tile0 * TcForm<D>::kKeys || pos >= d.tile1 * TcForm<D>::kKeys ||
+            !sees_new(p, row, token, t))
+            continue;
+        const int page = page_of(c, b, d.seq, pos, err);
+        if (page < 0) continue;
+        const uint16_t* src = c.v + p.layer_offset + page * c.page_stride + d.head * c.head_stride +
+                              (pos & (c.page_size - 1)) * c.slot_stride + channel;
+        for (int i = 0; i < n; ++i) {
+            const float2 v = T::unpack(src[i]);
+            if (!isfinite(v.x)) out[i] += v.x;
+        }
+    }
+}
 // Places in the ring of tile j's K and V, an item of n tiles starting at place 0.
 __device__ __forceinline__ int place_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int place_v(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
@@ -261,7 +309,8 @@ __device__ __forceinline__ int place_v(int j, int n) { return j == n - 1 ? 2 * n
 template <int D, class T>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                        const AttnParams p, const CacheView c, const BatchView b, int* err) {
+                        const __grid_constant__ AttnParams p, const __grid_constant__ CacheView c,
+                        const __grid_constant__ BatchView b, int* err) {
     using C = TcAttn<D, T>;
     constexpr int kParts = C::kParts;
     constexpr uint32_t kType = kParts == 3 ? 1u : 0u;
@@ -437,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool live = true;
             auto scores = [&](int j) {
                 const int place = place0 + place_k(j), st = place % C::kSlots, buf = (it + j) & 1;
-                live = live && mbar_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
+                live = live && kv_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
                 if (!live) return;
                 tc_fence_after();
                 const uint64_t k_desc = desc_sw128(base + st * C::kTileBytes, 16, 1024);
@@ -458,23 +507,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (int count = 0; live; ++count) {
                 const int at = count % kItems;
-                live = mbar_wait(item_full + at, (count / kItems) & 1, abort_flag, err, kDevErrTimeoutScore);
+                live = kv_wait(item_full + at, (count / kItems) & 1, abort_flag, err, kDevErrTimeoutScore);
                 if (!live) break;
                 const int n = *const_cast<volatile int*>(&items[at].n);
                 if (n < 0) break;
                 mbar_arrive(item_free + at);
                 if (n == 0) continue;
-                live = mbar_wait(q_full, with_keys & 1, abort_flag, err, kDevErrTimeoutScore);
+                live = kv_wait(q_full, with_keys & 1, abort_flag, err, kDevErrTimeoutScore);
                 scores(0);
                 for (int j = 0; live && j < n; ++j) {
                     if (j + 1 < n) scores(j + 1);
                     const int place = place0 + place_v(j, n), st = place % C::kSlots;
                     const int i = it + j, buf = i & 1, tb = i % C::kTBufs;
-                    live = live && mbar_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
+                    live = live && kv_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
                     if (i >= C::kTBufs)
-                        live = live && mbar_wait(t_free + tb, (i / C::kTBufs - 1) & 1, abort_flag, err,
+                        live = live && kv_wait(t_free + tb, (i / C::kTBufs - 1) & 1, abort_flag, err,
                                                  kDevErrTimeoutScore);
-                    live = live && mbar_wait(p_full + buf, (i >> 1) & 1, abort_flag, err, kDevErrTimeoutScore);
+                    live = live && kv_wait(p_full + buf, (i >> 1) & 1, abort_flag, err, kDevErrTimeoutScore);
                     if (!live) break;
                     tc_fence_after();
                     const uint64_t v_desc = desc_sw128(base + st * C::kTileBytes, C::kChunkStride, 1024);
@@ -496,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (*abort_flag) {
                 tc_commit(drained);
                 int no_abort = 0;
-                mbar_wait(drained, 0, &no_abort, err, kDevErrTimeoutScore);
+                kv_wait(drained, 0, &no_abort, err, kDevErrTimeoutScore);
             }
         }
     } else {
@@ -508,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int place0 = 0, it = 0;
         for (int count = 0;; ++count) {
             const int at = count % kItems;
-            const bool got = mbar_wait(item_full + at, (count / kItems) & 1, abort_flag, err, kDevErrTimeoutScore);
+            const bool got = kv_wait(item_full + at, (count / kItems) & 1, abort_flag, err, kDevErrTimeoutScore);
             if (soft_any(!got)) break;  // (all softmax threads leave together)
             const Item& d = items[at];
             const int n = d.n;
@@ -535,37 +584,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // channels.  Rows behind the last are zero.
                 const int row = d.first + min(r, rows - 1), tok = token_of(p, row);
                 sight.open(p, d.row0, tok);
-                // All threads, neighbours on neighbouring 16 bytes of a row.
+                // Warps take rows, lanes neighbouring 16 bytes of them (256 /
+                // D * 2 rows at a time).  Rows behind the last keep what is
+                // there: a row's products reach its own lane only.
                 if (n > 0) {
-                    constexpr int kUnits = kRowTile * (D / 8) / kSoftThreads;
-                    uint4 v[kUnits];
+                    constexpr int kAcross = D / 8, kDown = 32 / kAcross;
+                    constexpr int kPitch = C::kStageRow * 4, kPiece = C::kHalfD < 64 ? C::kHalfD : 64;
+                    uint8_t* const stage = smem + C::kOut;
+                    const int soft = warp - kFirstSoft, col = lane % kAcross * 8;
+                    const uint16_t* src = p.q + d.row0 * p.q_row_stride + (int64_t)d.head * p.group * D + col;
+                    constexpr int kMost = kRowTile / (kSoftWarps * kDown);
+                    uint4 v[kMost];
 #pragma unroll
-                    for (int i = 0; i < kUnits; ++i) {
-                        const int u = st_id + i * kSoftThreads, at_row = u / (D / 8);
-                        // (into shared memory as the quadrants have them, copies and all)
-                        const int from = C::kQInTmem ? at_row : at_row / 32 % spread * 32 + at_row % 32;
-                        const int q_row = d.first + from, t = token_of(p, q_row);
-                        const uint16_t* src = p.q + (d.row0 + t) * p.q_row_stride +
-                                              ((int64_t)d.head * p.group + q_row - t * p.group) * D + u % (D / 8) * 8;
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (from < rows &&
-                            bc_global(bc, src, 16, p.q,
-                                      2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D), kBcAttnQ))
-                            v[i] = load_q(p, src);
+                    for (int i = 0; i < kMost; ++i) {
+                        const int from = (i * kSoftWarps + soft) * kDown + lane / kAcross;
+                        if (from < rows) {
+                            const int t = token_of(p, d.first + from);
+                            const uint16_t* at_q =
+                                src + t * p.q_row_stride + (d.first + from - t * p.group) * D;
+                            if (bc_global(bc, at_q, 16, p.q,
+                                          2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D),
+                                          kBcAttnQ))
+                                v[i] = load_q(p, at_q);
+                        }
                     }
                     if constexpr (C::kQInTmem) {
                         // through the staging rows, 64 channels of each half (or all) at a time
-                        constexpr int kPitch = C::kStageRow * 4, kPiece = C::kHalfD < 64 ? C::kHalfD : 64;
-                        uint8_t* const stage = smem + C::kOut;
 #pragma unroll
                         for (int c0 = 0; c0 < C::kHalfD; c0 += kPiece) {
                             if (c0 > 0) soft_sync();
+                            const int in_half = col % C::kHalfD - c0;
 #pragma unroll
-                            for (int i = 0; i < kUnits; ++i) {
-                                const int u = st_id + i * kSoftThreads, at_row = u / (D / 8), col = u % (D / 8) * 8;
-                                const int in_half = col % C::kHalfD - c0;
-                                if (in_half >= 0 && in_half < kPiece)
-                                    *reinterpret_cast<uint4*>(stage + (col / C::kHalfD * kRowTile + at_row) * kPitch +
+                            for (int i = 0; i < kMost; ++i) {
+                                const int from = (i * kSoftWarps + soft) * kDown + lane / kAcross;
+                                if (from < rows && in_half >= 0 && in_half < kPiece)
+                                    *reinterpret_cast<uint4*>(stage + (col / C::kHalfD * kRowTile + from) * kPitch +
                                                               in_half * 2) = v[i];
                             }
                             soft_sync();
@@ -585,9 +638,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_before();
                     } else {
 #pragma unroll
-                        for (int i = 0; i < kUnits; ++i) {
-                            const int u = st_id + i * kSoftThreads;
-                            sts_u128(base + C::kQ + unit_at(u / (D / 8), u % (D / 8), kRowTile), v[i]);
+                        for (int i = 0; i < kMost; ++i) {
+                            const int from = (i * kSoftWarps + soft) * kDown + lane / kAcross;
+                            if (from < rows)  // (row `from` of every copy)
+                                for (int k = 0; k < copies; ++k)
+                                    sts_u128(base + C::kQ + unit_at(k * spread * 32 + from, col / 8, kRowTile), v[i]);
                         }
                         fence_proxy_async_smem();
                     }
@@ -598,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O takes tile j's product while tile j + 1's is under way
             auto accumulate = [&](int i, float f) {
                 const int tb = i % C::kTBufs;
-                mbar_wait(t_full + tb, (i / C::kTBufs) & 1, abort_flag, err, kDevErrTimeoutScore);
+                kv_wait(t_full + tb, (i / C::kTBufs) & 1, abort_flag, err, kDevErrTimeoutScore);
                 if (busy) {
                     tc_fence_after();
                     const float2 f2 = make_float2(f, f);
@@ -619,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < n; ++j) {
                 const int i = it + j, buf = i & 1;
                 const int pos0 = d.tile(j) * C::kTile, key0 = pos0 + my_key;
-                mbar_wait(s_full + buf, (i >> 1) & 1, abort_flag, err, kDevErrTimeoutScore);
+                kv_wait(s_full + buf, (i >> 1) & 1, abort_flag, err, kDevErrTimeoutScore);
                 float f = 1.f;
                 if (busy) {
                     tc_fence_after();
@@ -654,32 +709,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // NaN and infinities into its sum.  Such values leave the
                     // tile; rows that do see them get them at the item's end.
                     const int place = place0 + place_v(j, n), st = place % C::kSlots;
-                    mbar_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
-                    const int first_new = max(0, len - pos0), have = min(C::kTile, keys - pos0);
-                    bool odd = false;
-#pragma unroll 2
-                    for (int u = first_new * (D / 8) + st_id; u < C::kTile * (D / 8); u += kSoftThreads) {
-                        const int key = u / (D / 8);
-                        const uint32_t at_v = base + st * C::kTileBytes + unit_at(key, u % (D / 8), C::kTile);
-                        if (key >= have) {
-                            sts_u128(at_v, make_uint4(0, 0, 0, 0));
-                            continue;
-                        }
-                        uint32_t v[4];
-                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                                     : "r"(at_v));
-                        if (any_odd<T>(v[0]) || any_odd<T>(v[1]) || any_odd<T>(v[2]) || any_odd<T>(v[3])) {
-                            odd = true;
-                            for (int k = 0; k < 8; ++k) {
-                                const float2 t = T::unpack(k & 1 ? v[k >> 1] >> 16 : v[k >> 1] & 0xffffu);
-                                if (!isfinite(t.x))
-                                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at_v + 2 * k), "h"((unsigned short)0)
-                                                 : "memory");
-                            }
-                        }
-                    }
-                    if (odd) odd_flag[count & 1] = 1;
+                    kv_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
+                    if (scrub_tile<D, T>(base + st * C::kTileBytes, max(0, len - pos0), min(C::kTile, keys - pos0), st_id))
+                        odd_flag[count & 1] = 1;
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
@@ -714,76 +746,72 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int from = (i * spread + quad % spread) * 32 + lane;
                 sum += all_m[kRowTile + from] + last_l[from];
             }
-            const int row = d.first + min(r, rows - 1);
-            if (odd_flag[count & 1] != 0 && busy && r < rows) {
-#pragma unroll
-                for (int i = 0; i < C::kHalfD / 2; ++i) o[i] = make_float2(o[i].x * fix, o[i].y * fix);
-                fix = 1.f;
-                for (int t = 0; copy == 0 && t < d.tokens; ++t) {
-                    const int pos = len + t;
-                    if (pos < d.tile0 * C::kTile || pos >= d.tile1 * C::kTile ||
-                        !sees_new(p, sight.row, sight.token, t))
-                        continue;
-                    const int page = page_of(c, b, d.seq, pos, err);
-                    if (page < 0) continue;
-                    const uint16_t* src = c.v + p.layer_offset + page * c.page_stride + d.head * c.head_stride +
-                                          (pos & (c.page_size - 1)) * c.slot_stride + half * C::kHalfD;
-#pragma unroll
-                    for (int i = 0; i < C::kHalfD / 2; ++i) {
-                        const float2 v = T::unpack(*reinterpret_cast<const uint32_t*>(src + 2 * i));
-                        if (!isfinite(v.x)) o[i].x += v.x;
-                        if (!isfinite(v.y)) o[i].y += v.y;
-                    }
-                }
-            }
             const bool whole = d.slot < 0;
             if (!whole && half == 0 && copy == 0 && r < rows)
                 p.part_ml[(int64_t)d.slot * p.slot_rows + r] = make_float2(top, sum);
-            const float scale = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: zeros
-            const int tok = sight.token;
-            const int64_t row_at = (whole ? (d.row0 + tok) * p.out_row_stride +
-                                                ((int64_t)d.head * p.group + row - tok * p.group) * D
-                                          : ((int64_t)d.slot * p.slot_rows + r) * D) + half * C::kHalfD;
-            float* const out = whole ? p.out : p.part_o;
-            const int64_t out_bytes = 4 * ((p.rows - 1) * p.out_row_stride + (int64_t)p.group * p.kv_heads * D);
-            // Out through shared memory, kStageCols channels at a time, so
-            // that neighbouring lanes write a row's neighbouring bytes; the
-            // copies meet there and their warps share the rows.
-            constexpr int kCols = C::kStageCols, kPitch = C::kStageRow, kAcross = kCols / 4;
-            constexpr int kDown = 32 / kAcross;  // rows a warp writes at once
-            float* const stage = reinterpret_cast<float*>(smem + C::kOut) + half * kRowTile * kPitch;
-            const int share = 32 / copies;       // rows of the quadrant that this copy's warp writes
+            if (copies > 1) {
+                // The other copies hand their outputs to the first, kStageCols
+                // channels at a time through shared memory.
+                constexpr int kCols = C::kStageCols, kPitch = C::kStageRow;
+                float* const stage = reinterpret_cast<float*>(smem + C::kOut) + half * kRowTile * kPitch;
 #pragma unroll
-            for (int ch = 0; ch < C::kHalfD / kCols; ++ch) {
-                if (copies == 1) __syncwarp();
-                else if (ch > 0) soft_sync();
-                if (busy) {
+                for (int ch = 0; ch < C::kHalfD / kCols; ++ch) {
+                    if (ch > 0) soft_sync();
+                    if (busy && copy > 0) {
 #pragma unroll
-                    for (int i = 0; i < kCols / 4; ++i) {
-                        const float2 x = o[ch * (kCols / 2) + 2 * i], y = o[ch * (kCols / 2) + 2 * i + 1];
-                        *reinterpret_cast<float4*>(stage + lane_row * kPitch + 4 * i) =
-                            make_float4(x.x * fix, x.y * fix, y.x * fix, y.y * fix);
+                        for (int i = 0; i < kCols / 4; ++i) {
+                            const float2 x = o[ch * (kCols / 2) + 2 * i], y = o[ch * (kCols / 2) + 2 * i + 1];
+                            *reinterpret_cast<float4*>(stage + lane_row * kPitch + 4 * i) =
+                                make_float4(x.x * fix, x.y * fix, y.x * fix, y.y * fix);
+                        }
+                    }
+                    soft_sync();
+                    if (busy && copy == 0) {
+#pragma unroll
+                        for (int i = 0; i < kCols / 2; ++i) {
+                            float2& x = o[ch * (kCols / 2) + i];
+                            x = make_float2(x.x * fix, x.y * fix);
+                        }
+                        for (int k = 1; k < copies; ++k) {
+                            const float* from = stage + (k * spread * 32 + r) * kPitch;
+#pragma unroll
+                            for (int i = 0; i < kCols / 4; ++i) {
+                                const float4 t = *reinterpret_cast<const float4*>(from + 4 * i);
+                                float2 &x = o[ch * (kCols / 2) + 2 * i], &y = o[ch * (kCols / 2) + 2 * i + 1];
+                                x = make_float2(x.x + t.x, x.y + t.y);
+                                y = make_float2(y.x + t.z, y.y + t.w);
+                            }
+                        }
                     }
                 }
-                if (copies == 1) __syncwarp();
-                else soft_sync();
-                if (busy) {
-                    const int col = lane % kAcross * 4;
-#pragma unroll 2
-                    for (int i = 0; i < share; i += kDown) {
-                        const int rr = copy * share + i + lane / kAcross;  // row of the quadrant
-                        float4 v = *reinterpret_cast<const float4*>(stage + (quad % spread * 32 + rr) * kPitch + col);
-                        for (int k = 1; k < copies; ++k) {
-                            const float4 t = *reinterpret_cast<const float4*>(
-                                stage + ((k * spread + quad % spread) * 32 + rr) * kPitch + col);
-                            v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+            }
+            if (copy == 0 && r < rows) {
+                const float scale = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: zeros
+                const int row = d.first + r, tok = sight.token;
+                float* const dst = (whole ? p.out + (d.row0 + tok) * p.out_row_stride +
+                                                ((int64_t)d.head * p.group + row - tok * p.group) * D
+                                          : p.part_o + ((int64_t)d.slot * p.slot_rows + r) * D) + half * C::kHalfD;
+                if (!whole || bc_global(bc, dst, 4 * C::kHalfD, p.out,
+                                        4 * ((p.rows - 1) * p.out_row_stride + (int64_t)p.group * p.kv_heads * D),
+                                        kBcAttnOut)) {
+                    if (!whole || p.wide_out) {
+#pragma unroll
+                        for (int i = 0; i < C::kHalfD / 8; ++i) {
+                            const float2* x = o + 4 * i;
+                            asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 8 * i),
+                                         "f"(x[0].x * scale), "f"(x[0].y * scale), "f"(x[1].x * scale),
+                                         "f"(x[1].y * scale), "f"(x[2].x * scale), "f"(x[2].y * scale),
+                                         "f"(x[3].x * scale), "f"(x[3].y * scale)
+                                         : "memory");
                         }
-                        const float f = __shfl_sync(0xffffffffu, scale, rr);
-                        float* dst = out + __shfl_sync(0xffffffffu, row_at, rr) + ch * kCols + col;
-                        if (quad % spread * 32 + rr < rows &&
-                            (!whole || bc_global(bc, dst, 16, p.out, out_bytes, kBcAttnOut)))
-                            *reinterpret_cast<float4*>(dst) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < C::kHalfD / 4; ++i)
+                            *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(
+                                o[2 * i].x * scale, o[2 * i].y * scale, o[2 * i + 1].x * scale, o[2 * i + 1].y * scale);
                     }
+                    if (odd_flag[count & 1] != 0)
+                        add_odd<D, T>(p, c, b, d, sight.row, tok, dst, half * C::kHalfD, C::kHalfD, err);
                 }
             }
             __syncwarp();
@@ -799,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < C::kSlots; ++i)
             if (last_place[i] >= 0) {
                 int no_abort = 0;
-                mbar_wait(full + i, (last_place[i] / C::kSlots) & 1, &no_abort, err, kDevErrTimeoutKv);
+                kv_wait(full + i, (last_place[i] / C::kSlots) & 1, &no_abort, err, kDevErrTimeoutKv);
             }
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
