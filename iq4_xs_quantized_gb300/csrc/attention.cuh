@@ -370,13 +370,9 @@ struct Parts<KvBf16> {
 };
 
 // Eight values of q, with the scale's sign.
-__device__ __forceinline__ uint4 load_q(const AttnParams& p, const uint16_t* src) {
-    uint4 v = *reinterpret_cast<const uint4*>(src);
-    v.x = (v.x & p.q_and) ^ p.q_xor;
-    v.y = (v.y & p.q_and) ^ p.q_xor;
-    v.z = (v.z & p.q_and) ^ p.q_xor;
-    v.w = (v.w & p.q_and) ^ p.q_xor;
-    return v;
+__device__ __forceinline__ uint4 sign_q(const AttnParams& p, uint4 v) {
+    return make_uint4((v.x & p.q_and) ^ p.q_xor, (v.y & p.q_and) ^ p.q_xor, (v.z & p.q_and) ^ p.q_xor,
+                      (v.w & p.q_and) ^ p.q_xor);
 }
 
 // Tiles of 16-bit rows in shared memory: [64-channel chunk][row][128 bytes],

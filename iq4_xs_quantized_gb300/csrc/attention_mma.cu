@@ -186,27 +186,26 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
         const int end = w.seen_tiles(p);
         const int rows = min(kRowTile, w.w.tokens * p.group - w.row_tile * kRowTile);
         const int keys = w.w.len + w.w.tokens;
-        // q of the item's rows; rows behind the last are zero
+        // q of the item's rows
         constexpr int kQUnits = kRowTile * (D / 8) / (32 * kConsumers);
         uint4 qv[kQUnits];
 #pragma unroll
         for (int i = 0; i < kQUnits; ++i) {
-            const int u = threadIdx.x + i * 32 * kConsumers;
-            const int r = u / (D / 8), col = u % (D / 8), row = w.row_tile * kRowTile + r;
+            // (behind the last row the last one again, instead of a branch:
+            // all loads are in flight together)
+            const int u = threadIdx.x + i * 32 * kConsumers, col = u % (D / 8);
+            const int row = w.row_tile * kRowTile + min(u / (D / 8), rows - 1), t = token_of(p, row);
+            const uint16_t* src = p.q + (w.w.row0 + t) * p.q_row_stride +
+                                  ((int64_t)w.head * p.group + row - t * p.group) * D + col * 8;
             qv[i] = make_uint4(0, 0, 0, 0);
-            if (r < rows) {
-                const int t = token_of(p, row);
-                const uint16_t* src = p.q + (w.w.row0 + t) * p.q_row_stride +
-                                      ((int64_t)w.head * p.group + row - t * p.group) * D + col * 8;
-                if (bc_global(bc, src, 16, p.q,
-                              2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D), kBcAttnQ))
-                    qv[i] = load_q(p, src);
-            }
+            if (bc_global(bc, src, 16, p.q,
+                          2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D), kBcAttnQ))
+                qv[i] = *reinterpret_cast<const uint4*>(src);
         }
 #pragma unroll
         for (int i = 0; i < kQUnits; ++i) {
             const int u = threadIdx.x + i * 32 * kConsumers;
-            sts_u128(q_s + unit_at(u / (D / 8), u % (D / 8), kRowTile), qv[i]);
+            sts_u128(q_s + unit_at(u / (D / 8), u % (D / 8), kRowTile), sign_q(p, qv[i]));
         }
         consumer_sync();
         uint32_t qf[C::kQInRegs ? D / 16 : 1][4];

@@ -597,17 +597,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint4 v[kMost];
 #pragma unroll
                     for (int i = 0; i < kMost; ++i) {
-                        const int from = (i * kSoftWarps + soft) * kDown + lane / kAcross;
-                        if (from < rows) {
-                            const int t = token_of(p, d.first + from);
-                            const uint16_t* at_q =
-                                src + t * p.q_row_stride + (d.first + from - t * p.group) * D;
-                            if (bc_global(bc, at_q, 16, p.q,
-                                          2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D),
-                                          kBcAttnQ))
-                                v[i] = load_q(p, at_q);
-                        }
+                        // (the last row again instead of a branch: all loads are in flight together)
+                        const int from = min((i * kSoftWarps + soft) * kDown + lane / kAcross, rows - 1);
+                        const int t = token_of(p, d.first + from);
+                        const uint16_t* at_q = src + t * p.q_row_stride + (d.first + from - t * p.group) * D;
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (bc_global(bc, at_q, 16, p.q,
+                                      2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D), kBcAttnQ))
+                            v[i] = *reinterpret_cast<const uint4*>(at_q);
                     }
+#pragma unroll
+                    for (int i = 0; i < kMost; ++i) v[i] = sign_q(p, v[i]);
                     if constexpr (C::kQInTmem) {
                         // through the staging rows, 64 channels of each half (or all) at a time
 #pragma unroll
