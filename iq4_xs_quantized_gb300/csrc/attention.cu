@@ -12,26 +12,20 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 constexpr int64_t kWholeTokens = 512;
-constexpr int kBoxSlots = 64;
 static_assert(sizeof(SplitOut) == 32, "partial results stay aligned");
 
-int mma_ctas(int64_t head_dim, int num_sms) { return head_dim == 256 ? num_sms : 2 * num_sms; }
-
-// One map over K or V of a layer: channels, then slot and head by rising
-// stride, then pages; boxes of 64 channels x up to 64 slots of a page.
-bool encode_kv(EncodeTiledFn enc, uint16_t* base, const CacheView& c, bool bf16, int* slot_axis, CUtensorMap* map) {
-    const bool slot_first = c.slot_stride <= c.head_stride;
-    *slot_axis = slot_first ? 1 : 2;
-    const cuuint64_t slots = (cuuint64_t)c.page_size, heads = (cuuint64_t)c.heads;
-    const cuuint64_t slot_b = (cuuint64_t)c.slot_stride * 2, head_b = (cuuint64_t)c.head_stride * 2;
-    const cuuint64_t gdim[4] = {(cuuint64_t)c.head_dim, slot_first ? slots : heads, slot_first ? heads : slots,
+// One map over K or V of a layer: 64 channels, slots, 64-channel chunks, heads,
+// pages.  A box is up to `slots` slots of a page by `chunks` chunks, and lies
+// in shared memory as [chunk][slot][128 bytes].
+bool encode_kv(EncodeTiledFn enc, uint16_t* base, const CacheView& c, bool bf16, int slots, int chunks,
+               CUtensorMap* map) {
+    const cuuint64_t gdim[5] = {64, (cuuint64_t)c.page_size, (cuuint64_t)c.head_dim / 64, (cuuint64_t)c.heads,
                                 (cuuint64_t)c.pages};
-    const cuuint64_t gstride[3] = {slot_first ? slot_b : head_b, slot_first ? head_b : slot_b,
+    const cuuint64_t gstride[4] = {(cuuint64_t)c.slot_stride * 2, 128, (cuuint64_t)c.head_stride * 2,
                                    (cuuint64_t)c.page_stride * 2};
-    const cuuint32_t box_slots = (cuuint32_t)(c.page_size < kBoxSlots ? c.page_size : kBoxSlots);
-    const cuuint32_t box[4] = {64, slot_first ? box_slots : 1, slot_first ? 1 : box_slots, 1};
-    const cuuint32_t estride[4] = {1, 1, 1, 1};
-    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, gdim, gstride,
+    const cuuint32_t box[5] = {64, (cuuint32_t)slots, (cuuint32_t)chunks, 1, 1};
+    const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, base, gdim, gstride,
                box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -120,18 +114,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 }
 
 template <int D>
-cudaError_t launch_join_width(bool tc, const AttnParams& p, const BatchView& b, dim3 grid, int* err,
+cudaError_t launch_join_width(int row_tile, const AttnParams& p, const BatchView& b, dim3 grid, int* err,
                               cudaStream_t stream) {
     const dim3 block(32 * kJoinWarps);
-    return tc ? launch_chained(attention_join_kernel<D, TcForm<D>>, grid, block, 0, stream, p, b, err)
-              : launch_chained(attention_join_kernel<D, MmaForm>, grid, block, 0, stream, p, b, err);
+    switch (row_tile) {
+        case 8: return launch_chained(attention_join_kernel<D, MmaForm<1>>, grid, block, 0, stream, p, b, err);
+        case 16: return launch_chained(attention_join_kernel<D, MmaForm<2>>, grid, block, 0, stream, p, b, err);
+        default: return launch_chained(attention_join_kernel<D, TcForm<D>>, grid, block, 0, stream, p, b, err);
+    }
 }
-cudaError_t launch_join(bool tc, const AttnParams& p, const BatchView& b, int q_heads, int* err, cudaStream_t stream) {
+cudaError_t launch_join(int row_tile, const AttnParams& p, const BatchView& b, int q_heads, int* err,
+                        cudaStream_t stream) {
     const dim3 grid((unsigned)p.rows, (unsigned)q_heads);
     switch (p.head_dim) {
-        case 64: return launch_join_width<64>(tc, p, b, grid, err, stream);
-        case 128: return launch_join_width<128>(tc, p, b, grid, err, stream);
-        case 256: return launch_join_width<256>(tc, p, b, grid, err, stream);
+        case 64: return launch_join_width<64>(row_tile, p, b, grid, err, stream);
+        case 128: return launch_join_width<128>(row_tile, p, b, grid, err, stream);
+        case 256: return launch_join_width<256>(row_tile, p, b, grid, err, stream);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -145,11 +143,8 @@ inline int64_t align32(int64_t v) { return (v + 31) / 32 * 32; }
 
 int64_t tree_attention_workspace(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t,
                                  int num_sms) {
-    // the larger of the two forms' (a call's own lengths choose the form)
-    const int64_t group = q_heads / kv_heads;
-    const int64_t mma = 2 * (int64_t)mma_ctas(head_dim, num_sms) * slot_rows(MmaForm::kRows, rows, group);
-    const int64_t tc = 2 * (int64_t)num_sms * slot_rows(TcForm<64>::kRows, rows, group);
-    const int64_t n = mma > tc ? mma : tc;
+    // that of the largest row tile: a call's own rows choose the form
+    const int64_t n = 2 * (int64_t)num_sms * slot_rows(TcForm<64>::kRows, rows, q_heads / kv_heads);
     return (int64_t)sizeof(SplitOut) + align32(n * 8) + n * head_dim * 4;
 }
 
@@ -174,11 +169,12 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     p.mask_words = (int)a.mask_words;
     p.head_dim = c.head_dim;
     p.skip_stage = skip_stage;
-    // Row tiles of 16 while a sequence's rows a key/value head fit one, of 128 beyond.
+    // The warp-level form while a sequence's rows a key/value head fit its
+    // row tile, tcgen05 with tiles of 128 beyond.
     const int64_t mean_rows = (a.rows + b.sequences - 1) / b.sequences * group;
-    const bool tc = mean_rows > MmaForm::kRows;
-    const int row_tile = tc ? TcForm<64>::kRows : MmaForm::kRows;
-    p.ctas = tc ? num_sms : mma_ctas(c.head_dim, num_sms);
+    const int row_tile = mean_rows <= 8 ? 8 : mean_rows <= 16 ? 16 : 128;
+    const bool tc = row_tile == 128;
+    p.ctas = num_sms;
     p.whole_items = (int64_t)b.table_width * c.page_size <= kWholeTokens;
     p.slot_rows = (int)slot_rows(row_tile, a.rows, group);
     // Measured: starting and ending a part costs about 8 key tiles on tcgen05, 3 on the warp-level form.
@@ -189,13 +185,19 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     p.part_o = reinterpret_cast<float*>(ws + sizeof(SplitOut) + align32(2 * (int64_t)p.ctas * p.slot_rows * 8));
     CUtensorMap tk, tv;
     const EncodeTiledFn enc = reinterpret_cast<EncodeTiledFn>(encode);
-    if (!encode_kv(enc, c.k + p.layer_offset, c, bf16, &p.slot_axis, &tk) ||
-        !encode_kv(enc, c.v + p.layer_offset, c, bf16, &p.slot_axis, &tv))
+    // Boxes of whole pages' rows where the form's tiles can take them (one
+    // copy instead of one a chunk); the tcgen05 tiles cannot where a page is
+    // shorter than a tile, for all of a chunk's keys lie together there.
+    const int tile = !tc ? MmaForm<1>::kKeys : c.head_dim == 256 ? TcForm<256>::kKeys : TcForm<128>::kKeys;
+    p.box_slots = c.page_size < tile ? c.page_size : tile;
+    p.box_chunks = tc && c.page_size < tile ? 1 : c.head_dim / 64;
+    if (!encode_kv(enc, c.k + p.layer_offset, c, bf16, p.box_slots, p.box_chunks, &tk) ||
+        !encode_kv(enc, c.v + p.layer_offset, c, bf16, p.box_slots, p.box_chunks, &tv))
         return cudaErrorInvalidValue;
     const cudaError_t e = tc ? launch_attention_tc(p, &tk, &tv, c, b, bf16, err, stream)
-                             : launch_attention_mma(p, &tk, &tv, c, b, bf16, err, stream);
+                             : launch_attention_mma(row_tile, p, &tk, &tv, c, b, bf16, err, stream);
     if (e != cudaSuccess || p.whole_items) return e;
-    return launch_join(tc, p, b, (int)a.q_heads, err, stream);
+    return launch_join(row_tile, p, b, (int)a.q_heads, err, stream);
 }
 
 }  // namespace iq4xs

@@ -47,7 +47,7 @@ struct AttnParams {
     int whole_items;   // 1: cut = kWhole
     int part_tiles;    // what starting and ending a part costs, in key tiles
     int slot_rows;     // rows of a partial result: the row tile, or all rows if fewer
-    int slot_axis;     // tensor-map axis of the slot (1 or 2; the head has the other)
+    int box_slots, box_chunks;  // of a copy: slots of a page, 64-channel chunks
     int skip_stage;    // test hook: this stage of every CTA is left unissued
 };
 
@@ -212,8 +212,14 @@ struct WorkWalk {
             }
             before += __shfl_sync(0xffffffffu, sums, 31);
         }
-        row_end = b.row_offsets[s + 1];
-        w = seq_of<F>(p, b.row_offsets[s], row_end, b.lens[s], err);
+        if (s < 32) {  // (one of those that the lanes hold)
+            const int first = __shfl_sync(0xffffffffu, mine.row0, s), n = __shfl_sync(0xffffffffu, mine.tokens, s);
+            w = seq_of<F>(p, first, first + n, __shfl_sync(0xffffffffu, mine.len, s), err);
+            row_end = first + n;
+        } else {
+            row_end = b.row_offsets[s + 1];
+            w = seq_of<F>(p, b.row_offsets[s], row_end, b.lens[s], err);
+        }
         read_ahead(b);
         const int unit = w.unit(split.cut);
         const int item = (int)div_small(x - seq_x, unit);
@@ -382,11 +388,13 @@ constexpr int kChunkBytes = 128;
 __device__ __forceinline__ uint32_t unit_at(int r, int u, int rows) {
     return (uint32_t)((u >> 3) * rows * kChunkBytes + r * kChunkBytes + (((u & 7) ^ (r & 7)) << 4));
 }
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint64_t* bar) {
+// A box of K or V: from (chunk, slot) of a page and head on.
+__device__ __forceinline__ void tma_load_kv(uint32_t dst, const void* map, int slot, int chunk, int head, int page,
+                                            uint64_t* bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(slot), "r"(chunk), "r"(head), "r"(page), "r"(smem_u32(bar))
         : "memory");
 }
 // mbar_wait whose first probe does not suspend (most phases are complete when
@@ -408,10 +416,33 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, kv_wait(bar, parity, abort_flag, err, code)) != 0;
 }
 
-// The forms' tiles: row tiles of 16 or 128; 128 keys a tile where two tiles of
-// K, of V and of scores fit the SM, 64 at 256 channels.
+// Page ids of 32 pages of a sequence, one a lane, and the 32 behind them on their way.
+struct PageWindow {
+    const int32_t* table;
+    int held, first, ids, ids2;
+    __device__ __forceinline__ int read(int page) const { return page < held ? table[page] : -1; }
+    __device__ __forceinline__ void open(const BatchView& b, int s) {
+        table = b.page_table + s * b.table_stride;
+        held = min(b.held[s], b.table_width);
+        first = -64;
+        ids2 = -1;
+    }
+    // Brings the window over `page`, a tile's first; by a whole warp.
+    __device__ __forceinline__ void move(int page, int lane) {
+        if (page >= first && page < first + 32) return;
+        ids = page == first + 32 ? ids2 : read(page + lane);
+        first = page;
+        ids2 = read(page + 32 + lane);
+    }
+    __device__ __forceinline__ int id(int page) const { return __shfl_sync(0xffffffffu, ids, (page - first) & 31); }
+};
+
+// The forms' tiles: row tiles of 8 or 16 on the warp-level form, of 128 on
+// tcgen05; there 128 keys a tile where two tiles of K, of V and of scores fit
+// the SM, 64 at 256 channels.
+template <int NT>
 struct MmaForm {
-    static constexpr int kRows = 16, kKeys = 64;
+    static constexpr int kRows = 8 * NT, kKeys = 64;
 };
 template <int D>
 struct TcForm {
@@ -419,7 +450,7 @@ struct TcForm {
 };
 
 // Launchers of the two forms (csrc/attention_mma.cu, csrc/attention_tc.cu).
-cudaError_t launch_attention_mma(const AttnParams& p, const void* tk, const void* tv, const CacheView& c,
+cudaError_t launch_attention_mma(int row_tile, const AttnParams& p, const void* tk, const void* tv, const CacheView& c,
                                  const BatchView& b, bool bf16, int* err, cudaStream_t stream);
 cudaError_t launch_attention_tc(const AttnParams& p, const void* tk, const void* tv, const CacheView& c,
                                 const BatchView& b, bool bf16, int* err, cudaStream_t stream);

@@ -1,45 +1,57 @@
 // attention_mma.cu -- tree attention for few rows a key/value head (single
-// tokens, short drafts): warp-level MMA (m16n8k16) on 16-row tiles.
+// tokens, short drafts): warp-level MMA (m16n8k16) with the keys on the
+// 16-wide side and the rows on the 8-wide one.
+//
+//   S^T = K Q^T      16 keys x 8 rows a product
+//   O^T += V^T P^T   16 channels x 8 rows
 //
 // Few rows make the cache the whole cost: 4 D bytes a key against 4 D flops
 // a row and key, so HBM bounds it and the rest has to stay out of the way.
-// One producer warp streams 64-key tiles of K and V through a ring in shared
-// memory by TMA (boxes of 64 channels x a page's slots, 128-byte swizzle);
-// four consumer warps own 16 keys of every tile each, with a running maximum,
-// sum and 16 x D output of their own, so that no warp waits for another until
-// the item ends: scores stay in the MMA's accumulator layout, which is the
-// next MMA's A operand.
+// That way round a tile of 8 rows costs 8 rows' work (the other way round
+// 16), and its output takes D / 4 registers a thread.
 //
-// Weights go into the second product as the sum of 16-bit parts (two for
-// fp16, three for bf16: hi = round(w), lo = round(w - hi), ...), so that
-// rounding them costs less than fp32 accumulation does.
+// Two producer warps stream 64-key tiles of K and of V into shared memory by
+// TMA (up to 64 slots of a page a copy, 128-byte swizzle).  Two sets of four
+// consumer warps (one where the outputs take more registers) take the tiles
+// in turn, each from a ring of its own, K0 V0 K1 V1 ..., and each warp 16
+// keys of the tile, with a running maximum, sum and output of its own: no
+// warp waits for another until the item ends.  (A ring of its own, because a
+// parity wait cannot tell a phase from the next but one: a set must see every
+// phase of the barriers that it waits on.)  The weights go from the first
+// product's accumulators to the second one's B operand by 8 x 8 transposes in
+// registers, as the sum of 16-bit parts (two for fp16, three for bf16), so
+// that rounding them costs less than fp32 accumulation does.
 #include "attention.cuh"
 
 namespace iq4xs {
 namespace {
 
-constexpr int kRowTile = MmaForm::kRows, kKeyTile = MmaForm::kKeys;
-constexpr int kConsumers = 4;
-constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kWarpKeys = kKeyTile / kConsumers;
+constexpr int kKeyTile = MmaForm<1>::kKeys;
+constexpr int kSetWarps = 4;
+constexpr int kWarpKeys = kKeyTile / kSetWarps;
 static_assert(kWarpKeys == 16, "a warp's keys are one k16 step of the second product");
 
-template <int D>
+template <int D, int NT>
 struct MmaAttn {
+    static constexpr int kRows = MmaForm<NT>::kRows;
     static constexpr int kChunks = D / 64;
     static constexpr int kTileBytes = kKeyTile * D * 2;      // K or V of a tile
-    static constexpr int kStageBytes = 2 * kTileBytes;
-    static constexpr int kCtas = D == 256 ? 1 : 2;           // resident a SM
-    static constexpr int kStages = D == 256 ? 3 : D == 128 ? 3 : 6;
-    static constexpr int kQBytes = kRowTile * D * 2;
-    static constexpr int kJoinCols = 32;                     // channels of the warps' outputs joined at a time
-    static constexpr int kJoinBytes = kConsumers * kRowTile * kJoinCols * 4;
-    static constexpr int kJoin = kStages * kStageBytes + kQBytes;
+    static constexpr int kSets = NT * D <= 256 ? 2 : 1;
+    static constexpr int kConsumers = kSetWarps * kSets;
+    static constexpr int kThreads = 32 * (kConsumers + 2);
+    static constexpr int kSlots = 192 * 1024 / kSets / kTileBytes;  // of a set's ring: 3 (6 in one set), 6, 12
+    static constexpr int kQBytes = kRows * D * 2;
+    static constexpr int kJoinCols = NT == 1 ? 64 : 32;      // channels of the warps' outputs joined at a time
+    static constexpr int kJoinPitch = kJoinCols + 4;         // (conflict-free for the fragments' rows and channels)
+    static constexpr int kJoinBytes = kConsumers * kRows * kJoinPitch * 4;
+    static constexpr int kQ = kSets * kSlots * kTileBytes;
+    static constexpr int kJoin = kQ + kQBytes;
     static constexpr int kMl = kJoin + kJoinBytes;           // per warp and row: max, sum; then joined
-    static constexpr int kBars = kMl + (kConsumers + 1) * kRowTile * 8;
-    static constexpr int kSmem = kBars + 3 * kStages * 8 + 16 + 1024;  // + alignment
-    static constexpr bool kQInRegs = D <= 64;
-    static_assert(kSmem <= (kCtas == 1 ? 227 : 113) * 1024, "shared memory of the resident CTAs");
+    static constexpr int kBars = kMl + (kConsumers + 1) * kRows * 8;
+    static constexpr int kSmem = kBars + 2 * kSets * kSlots * 8 + 16;
+    static constexpr bool kQInRegs = NT == 1;
+    static_assert(kSets * kSlots <= 32, "a lane keeps a slot's last place");
+    static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
@@ -53,6 +65,12 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
+}
+// 8 x 8 transpose of 16-bit values held two a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 template <class T>
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1);
@@ -68,29 +86,102 @@ __device__ __forceinline__ void mma16816<KvBf16>(float* c, const uint32_t* a, ui
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-static_assert(kConsumers * 32 == 128, "the consumers' barrier");
+template <int kConsumers>
+__device__ __forceinline__ void consumers_meet() {
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
+}
 
-template <int D, class T>
-__global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
+// Offset of unit u (8 channels) of row r of a strip (which starts at a
+// multiple of 8 rows of its box, so that r alone gives the swizzle).
+__device__ __forceinline__ uint32_t strip_unit(int r, int u, uint32_t chunk_stride) {
+    return (uint32_t)(u >> 3) * chunk_stride + r * kChunkBytes + (((u & 7) ^ (r & 7)) << 4);
+}
+// Keys `have` .. 15 of a warp's V strip become zero, and so does every key
+// that holds NaN or infinities when `hidden` (some row does not see all of the
+// strip): a zero weight would carry such values into rows that do not see
+// them.  Rows that do see such a key get its share here, from e, the weights
+// (x = -inf: not seen).  A lane has channels ch, ch + 8 and rows 2 ct, 2 ct +
+// 1 of every 16 x 8 output tile.
+template <int D, class T, int NT>
+__device__ __forceinline__ void scrub_strip(uint32_t v_s, uint32_t chunk_stride, int have, bool hidden, const float (*x)[4],
+                                            const float (*e)[4], float (*o)[NT][4]) {
+    const int lane = threadIdx.x & 31, rg = lane >> 2, ct = lane & 3;
+    for (int key = 0; key < kWarpKeys; ++key) {
+        bool odd = key >= have;
+        if (!odd && hidden) {
+            for (int u = lane; u < D / 8; u += 32) {
+                uint32_t v[4];
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                             : "r"(v_s + strip_unit(key, u, chunk_stride)));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = T::unpack(v[i]);
+                    odd |= !isfinite(f.x) || !isfinite(f.y);
+                }
+            }
+            odd = __any_sync(0xffffffffu, odd);
+            if (odd) {
+                const int src = (key & 7) * 4 + ct;
+                float pk[NT][2], xk[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        pk[n][r] = __shfl_sync(0xffffffffu, key < 8 ? e[n][r] : e[n][2 + r], src);
+                        xk[n][r] = __shfl_sync(0xffffffffu, key < 8 ? x[n][r] : x[n][2 + r], src);
+                    }
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    float v[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t w = lds_u32_ordered(v_s + strip_unit(key, 2 * i + k, chunk_stride) + (rg >> 1) * 4);
+                        v[k] = T::unpack(rg & 1 ? w >> 16 : w & 0xffffu).x;
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            if (xk[n][r] != -INFINITY) {
+                                o[i][n][r] = fmaf(pk[n][r], v[0], o[i][n][r]);
+                                o[i][n][2 + r] = fmaf(pk[n][r], v[1], o[i][n][2 + r]);
+                            }
+                }
+            }
+        }
+        __syncwarp();
+        if (odd)
+            for (int u = lane; u < D / 8; u += 32) sts_u128(v_s + strip_unit(key, u, chunk_stride), make_uint4(0, 0, 0, 0));
+    }
+    __syncwarp();
+    fence_proxy_async_smem();  // these writes come before the slot's next copy
+}
+
+template <int D, class T, int NT>
+__global__ void __launch_bounds__(MmaAttn<D, NT>::kThreads, 1)
     attention_mma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                         const AttnParams p, const CacheView c, const BatchView b, int* err) {
-    using C = MmaAttn<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);  // swizzle atoms
+                         const __grid_constant__ AttnParams p, const __grid_constant__ CacheView c,
+                         const __grid_constant__ BatchView b, int* err) {
+    using C = MmaAttn<D, NT>;
+    using F = MmaForm<NT>;
+    constexpr int kConsumers = C::kConsumers;
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
-    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kBars);
-    uint64_t* v_full = k_full + C::kStages;
-    uint64_t* slot_free = v_full + C::kStages;
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(slot_free + C::kStages);
+    if ((base & 1023) != 0) {  // (no static shared memory: the swizzle atoms' alignment)
+        if (threadIdx.x == 0) atomicCAS(err, 0, kDevErrLayout);
+        return;
+    }
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);  // [set][slot]
+    uint64_t* slot_free = full + C::kSets * C::kSlots;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(slot_free + C::kSets * C::kSlots);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.x;
     const Bc bc = bc_open(err);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(k_full + i, 1);
-            mbar_init(v_full + i, 1);
-            mbar_init(slot_free + i, kConsumers);
+        for (int i = 0; i < C::kSets * C::kSlots; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(slot_free + i, kSetWarps);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -102,99 +193,83 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
     __syncthreads();
     griddep_wait();  // lengths, tables, q and the cache's newest rows come from earlier launches
     griddep_launch_dependents();
-    WorkWalk<MmaForm> w;
+    WorkWalk<F> w;
     w.start(p, b, g, err);
 
-    if (warp == kConsumers) {
-        // ---------------------------------------------------------- producer
-        const int box_slots = min(c.page_size, kKeyTile);
-        const int boxes = kKeyTile / box_slots * C::kChunks;  // of K (or V) a full tile
-        const uint32_t box_bytes = box_slots * kChunkBytes;
-        int it = 0;
+    if (warp >= kConsumers) {
+        // ----------------------------------------------- producers: K, then V
+        const int kv = warp - kConsumers;
+        const void* map = kv ? &tv : &tk;
+        const int boxes = kKeyTile / p.box_slots;  // a lane copies one
+        const uint32_t box_bytes = p.box_slots * D * 2;
+        const uint32_t dst0 = base + lane * box_bytes;
+        PageWindow pages;
+        int it = 0, last = -1;  // tiles so far; the last place loaded into slot `lane`
         bool live = true;
         for (; live && w.valid(); w.next(p, b, g, err)) {
             const int end = w.seen_tiles(p);
             const int keys = w.w.len + w.w.tokens;
-            const int held = min(b.held[w.s], b.table_width);
-            const int32_t* table = b.page_table + w.s * b.table_stride;
-            // Page ids of 32 pages from page0 on, one a lane, the next 32 on their way.
-            int page0 = (w.tile0 * kKeyTile) >> c.page_shift;
-            int ids = page0 + lane < held ? table[page0 + lane] : -1;
-            int ids2 = page0 + 32 + lane < held ? table[page0 + 32 + lane] : -1;
-            for (int tile = w.tile0; tile < end; ++tile, ++it) {
-                const int st = it % C::kStages, pos0 = tile * kKeyTile;
-                if (it >= C::kStages && !warp_wait(slot_free + st, ((it / C::kStages) - 1) & 1, abort_flag, err,
-                                                   kDevErrTimeoutKvSlot)) {
-                    live = false;
-                    break;
-                }
-                while ((pos0 >> c.page_shift) >= page0 + 32) {
-                    page0 += 32;
-                    ids = ids2;
-                    ids2 = page0 + 32 + lane < held ? table[page0 + 32 + lane] : -1;
-                }
+            pages.open(b, w.s);
+            for (int tile = w.tile0; live && tile < end; ++tile, ++it) {
+                const int pos0 = tile * kKeyTile, pos = pos0 + lane * p.box_slots;
+                pages.move(pos0 >> c.page_shift, lane);
+                int page = pages.id(pos >> c.page_shift);
                 // boxes that hold a key: those of slots at or behind the end stay out
-                const int used = min(boxes, (min(kKeyTile, keys - pos0) + box_slots - 1) / box_slots * C::kChunks);
-                const bool skip = it == p.skip_stage;
-                if (lane == 0 && !skip) {
-                    mbar_arrive_expect_tx(k_full + st, used * box_bytes);
-                    mbar_arrive_expect_tx(v_full + st, used * box_bytes);
+                const int used = min(boxes, (keys - pos0 + p.box_slots - 1) / p.box_slots);
+                if (lane < used && (page < 0 || page >= c.pages)) {
+                    data_error(err, kDataPage);
+                    page = c.pages;  // outside the map: zeros
                 }
+                const int slot = pos & (c.page_size - 1);
+                bc_tma(bc, 0, 2, 64, 64, slot, c.page_size, kBcAttnKv, kBcAttnKv);
+                const int place = it / C::kSets * 2 + kv, st = it % C::kSets * C::kSlots + place % C::kSlots;
+                live = place < C::kSlots || warp_wait(slot_free + st, (place / C::kSlots - 1) & 1, abort_flag, err,
+                                                      kDevErrTimeoutKvSlot);
+                if (!live || it == p.skip_stage) continue;
+                if (lane == 0) mbar_arrive_expect_tx(full + st, used * box_bytes);
+                if (lane == st) last = place;
                 __syncwarp();
-                for (int i0 = 0; i0 < used; i0 += 32) {
-                    const int i = i0 + lane;
-                    const int sub = i / C::kChunks, chunk = i % C::kChunks;
-                    const int pos = pos0 + sub * box_slots;
-                    int page = __shfl_sync(0xffffffffu, ids, ((pos >> c.page_shift) - page0) & 31);
-                    if (i < used && !skip) {
-                        if (page < 0 || page >= c.pages) {
-                            data_error(err, kDataPage);
-                            page = c.pages;  // outside the map: zeros
-                        }
-                        const int slot = pos & (c.page_size - 1);
-                        const int y = p.slot_axis == 1 ? slot : w.head, z = p.slot_axis == 1 ? w.head : slot;
-                        const uint32_t dst = base + st * C::kStageBytes + chunk * kKeyTile * kChunkBytes +
-                                             sub * box_bytes;
-                        bc_tma(bc, chunk * 64, 2, 64, D, slot, c.page_size, kBcAttnKv, kBcAttnKv);
-                        tma_load_4d(dst, &tk, chunk * 64, y, z, page, k_full + st);
-                        tma_load_4d(dst + C::kTileBytes, &tv, chunk * 64, y, z, page, v_full + st);
-                    }
-                }
+                if (lane < used) tma_load_kv(dst0 + st * C::kTileBytes, map, slot, 0, w.head, page, full + st);
                 __syncwarp();
             }
         }
         // No copy may be in flight when the CTA ends; the consumers wait for
-        // every stage, unless a wait ran out.
-        if (*abort_flag) {
-            for (int i = max(0, it - C::kStages); i < it; ++i)
-                if (i != p.skip_stage) {
-                    int no_abort = 0;
-                    mbar_wait(k_full + i % C::kStages, (i / C::kStages) & 1, &no_abort, err, kDevErrTimeoutKv);
-                    kv_wait(v_full + i % C::kStages, (i / C::kStages) & 1, &no_abort, err, kDevErrTimeoutKv);
-                }
-        }
+        // every one, unless a wait ran out.
+        if (*abort_flag)
+            for (int i = 0; i < C::kSets * C::kSlots; ++i) {
+                const int place = __shfl_sync(0xffffffffu, last, i);
+                int no_abort = 0;
+                if (place >= 0)
+                    mbar_wait(full + i, (place / C::kSlots) & 1, &no_abort, err, kDevErrTimeoutKv);
+            }
         return;
     }
 
     // ------------------------------------------------------------ consumers
-    const uint32_t q_s = base + C::kStages * C::kStageBytes;
+    constexpr int kRows = C::kRows;
+    const uint32_t q_s = base + C::kQ;
     float* join = reinterpret_cast<float*>(smem + C::kJoin);
     float2* ml = reinterpret_cast<float2*>(smem + C::kMl);
-    const int rg = lane >> 2, ct = lane & 3;  // fragment row and column pair
+    const int rg = lane >> 2, ct = lane & 3;           // fragment row (key or channel) and column pair (rows)
+    const int set = warp / kSetWarps, strip = warp % kSetWarps * kWarpKeys;
+    // the strip's rows in a tile of [box][chunk][slot][128 bytes]
+    const uint32_t chunk_stride = p.box_slots * kChunkBytes;
+    const uint32_t strip_at = strip / p.box_slots * p.box_slots * D * 2 + strip % p.box_slots * kChunkBytes;
+    const auto consumer_sync = [] { consumers_meet<kConsumers>(); };
     int it = 0;
+    bool live = true;  // no wait has run out: after that a warp waits for nothing and arrives nowhere
     for (; w.valid(); w.next(p, b, g, err)) {
         const int end = w.seen_tiles(p);
-        const int rows = min(kRowTile, w.w.tokens * p.group - w.row_tile * kRowTile);
+        const int rows = min(kRows, w.w.tokens * p.group - w.row_tile * kRows);
         const int keys = w.w.len + w.w.tokens;
-        // q of the item's rows
-        constexpr int kQUnits = kRowTile * (D / 8) / (32 * kConsumers);
+        // q of the item's rows (behind the last row the last one again,
+        // instead of a branch: all loads are in flight together)
+        constexpr int kQUnits = (kRows * (D / 8) + 32 * kConsumers - 1) / (32 * kConsumers);
         uint4 qv[kQUnits];
 #pragma unroll
         for (int i = 0; i < kQUnits; ++i) {
-            // (behind the last row the last one again, instead of a branch:
-            // all loads are in flight together)
             const int u = threadIdx.x + i * 32 * kConsumers, col = u % (D / 8);
-            const int row = w.row_tile * kRowTile + min(u / (D / 8), rows - 1), t = token_of(p, row);
+            const int row = w.row_tile * kRows + min(u / (D / 8), rows - 1), t = token_of(p, row);
             const uint16_t* src = p.q + (w.w.row0 + t) * p.q_row_stride +
                                   ((int64_t)w.head * p.group + row - t * p.group) * D + col * 8;
             qv[i] = make_uint4(0, 0, 0, 0);
@@ -202,255 +277,237 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
                           2 * ((p.rows - 1) * p.q_row_stride + (int64_t)p.group * p.kv_heads * D), kBcAttnQ))
                 qv[i] = *reinterpret_cast<const uint4*>(src);
         }
+        int tok[NT][2];  // the tokens of the lane's rows 8 n + 2 ct + r (behind the last: the last)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                tok[n][r] = min(w.w.tokens - 1, token_of(p, w.row_tile * kRows + 8 * n + 2 * ct + r));
 #pragma unroll
         for (int i = 0; i < kQUnits; ++i) {
             const int u = threadIdx.x + i * 32 * kConsumers;
-            sts_u128(q_s + unit_at(u / (D / 8), u % (D / 8), kRowTile), sign_q(p, qv[i]));
+            if (u < kRows * (D / 8)) sts_u128(q_s + unit_at(u / (D / 8), u % (D / 8), kRows), sign_q(p, qv[i]));
         }
         consumer_sync();
-        uint32_t qf[C::kQInRegs ? D / 16 : 1][4];
-        const uint32_t q_row = q_s;
+        // B operand of k16 steps 2 k, 2 k + 1 and rows 8 n ..: four 8 x 8 blocks
+        auto q_frag = [&](int k, int n, uint32_t* f) {
+            ldsm4(q_s + unit_at(8 * n + (lane & 7), 4 * k + (lane >> 3), kRows), f);
+        };
+        uint32_t qf[C::kQInRegs ? D / 32 : 1][C::kQInRegs ? NT : 1][4];
         if constexpr (C::kQInRegs) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) ldsm4(q_row + unit_at(lane & 15, 2 * k + (lane >> 4), kRowTile), qf[k]);
+            for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) q_frag(k, n, qf[k][n]);
         }
 
-        float o[D / 8][4];
+        float o[D / 16][NT][4];  // channels 16 i + rg, + 8; rows 8 n + 2 ct, + 1
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows rg, rg + 8
-        int tok[2];  // the rows' tokens (rows behind the last: the last token)
+        for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            tok[i] = min(w.w.tokens - 1, token_of(p, w.row_tile * kRowTile + rg + 8 * i));
+            for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+        }
 
         for (int tile = w.tile0; tile < end; ++tile, ++it) {
-            const int st = it % C::kStages, par = (it / C::kStages) & 1;
-            const uint32_t k_s = base + st * C::kStageBytes, v_s = k_s + C::kTileBytes;
-            const int key0 = tile * kKeyTile + warp * kWarpKeys;  // the warp's first position
-            const int have = min(kWarpKeys, keys - key0);          // its positions before the end
-            kv_wait(k_full + st, par, abort_flag, err, kDevErrTimeoutKv);
+            if (it % C::kSets != set || !live) continue;
+            const int k_place = it / C::kSets * 2, v_place = k_place + 1;
+            const int k_st = set * C::kSlots + k_place % C::kSlots, v_st = set * C::kSlots + v_place % C::kSlots;
+            const uint32_t k_s = base + k_st * C::kTileBytes + strip_at, v_s = base + v_st * C::kTileBytes + strip_at;
+            const auto k_done = [&] {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(slot_free + k_st);
+            };
+            const auto v_wait = [&] {
+                live = warp_wait(full + v_st, (v_place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
+                return live;
+            };
+            const int key0 = tile * kKeyTile + strip;       // the warp's first position
+            const int have = min(kWarpKeys, keys - key0);   // its positions before the end
+            live = warp_wait(full + k_st, (k_place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
+            if (!live) continue;
             if (have > 0) {
-                float s[2][2][4];  // [even, odd k step][8 keys][fragment]
+                float s[2][NT][4];  // [even, odd k step]
 #pragma unroll
-                for (int i = 0; i < 16; ++i) (&s[0][0][0])[i] = 0.f;
-                const int kr = warp * kWarpKeys + (lane & 7) + ((lane >> 4) << 3);
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    uint32_t kf[4];
-                    ldsm4(k_s + unit_at(kr, 2 * k + ((lane >> 3) & 1), kKeyTile), kf);
-                    uint32_t qt[4];
-                    const uint32_t* a = qt;
-                    if constexpr (C::kQInRegs) a = qf[k];
-                    else ldsm4(q_row + unit_at(lane & 15, 2 * k + (lane >> 4), kRowTile), qt);
-                    mma16816<T>(s[k & 1][0], a, kf[0], kf[1]);
-                    mma16816<T>(s[k & 1][1], a, kf[2], kf[3]);
+                    for (int n = 0; n < NT; ++n) s[i][n][0] = s[i][n][1] = s[i][n][2] = s[i][n][3] = 0.f;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    uint32_t kf[2][4];
+                    ldsm4(k_s + strip_unit(lane & 15, 4 * k + (lane >> 4), chunk_stride), kf[0]);
+                    ldsm4(k_s + strip_unit(lane & 15, 4 * k + 2 + (lane >> 4), chunk_stride), kf[1]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        uint32_t qt[4];
+                        const uint32_t* f = qt;
+                        if constexpr (C::kQInRegs) f = qf[k][n];
+                        else q_frag(k, n, qt);
+                        mma16816<T>(s[0][n], kf[0], f[0], f[1]);
+                        mma16816<T>(s[1][n], kf[1], f[2], f[3]);
+                    }
                 }
-                float x[2][4];  // [row][key: 2 ct, 2 ct + 1, 8 + 2 ct, 8 + 2 ct + 1]
+                k_done();
+                float x[NT][4];  // keys rg (rows 2 ct, 2 ct + 1), rg + 8 (the same rows)
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        x[r][k] = (s[0][k >> 1][2 * r + (k & 1)] + s[1][k >> 1][2 * r + (k & 1)]) * p.scale_log2;
+                    for (int i = 0; i < 4; ++i) x[n][i] = (s[0][n][i] + s[1][n][i]) * p.scale_log2;
                 bool hidden = false;  // a new token of this strip that some row does not see
                 if (key0 + kWarpKeys > w.w.len) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int key = (k >> 1) * 8 + 2 * ct + (k & 1), j = key0 + key - w.w.len;
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
+                        for (int i = 0; i < 4; ++i) {
+                            const int key = rg + (i >> 1) * 8, j = key0 + key - w.w.len, t = tok[n][i & 1];
                             const bool inside = key < have;
-                            const bool see = inside && (j < 0 || sees_new(p, w.w.row0 + tok[r], tok[r], j));
+                            const bool see = inside && (j < 0 || sees_new(p, w.w.row0 + t, t, j));
                             hidden |= inside && !see;
-                            if (!see) x[r][k] = -INFINITY;
+                            if (!see) x[n][i] = -INFINITY;
                         }
-                    }
                     hidden = __any_sync(0xffffffffu, hidden);
                 }
                 // running maximum (lazily) and weights
-                float mx[2];
+                float mx[NT][2];
                 bool rise = false;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    mx[r] = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
-                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-                    rise |= mx[r] > m[r] + kLazy;
-                }
-                if (__any_sync(0xffffffffu, rise)) {
-                    float f[2];
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const bool up = mx[r] > m[r] + kLazy;
-                        f[r] = up ? fast_exp2(m[r] - mx[r]) : 1.f;
-                        m[r] = up ? mx[r] : m[r];
-                        l[r] *= f[r];
+                        float t = fmaxf(x[n][r], x[n][2 + r]);
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                        mx[n][r] = t;
+                        rise |= t > m[n][r] + kLazy;
                     }
+                if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        o[i][0] *= f[0];
-                        o[i][1] *= f[0];
-                        o[i][2] *= f[1];
-                        o[i][3] *= f[1];
-                    }
-                }
-                float e[2][4];
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float shift = m[r] == -INFINITY ? 0.f : kWeightBits - m[r];
+                        for (int r = 0; r < 2; ++r) {
+                            const bool up = mx[n][r] > m[n][r] + kLazy;
+                            const float f = up ? fast_exp2(m[n][r] - mx[n][r]) : 1.f;
+                            m[n][r] = up ? mx[n][r] : m[n][r];
+                            l[n][r] *= f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) e[r][k] = fast_exp2(x[r][k] + shift);
-                    l[r] += (e[r][0] + e[r][1]) + (e[r][2] + e[r][3]);
-                }
-
-                kv_wait(v_full + st, par, abort_flag, err, kDevErrTimeoutKv);
-                if (hidden || have < kWarpKeys) {
-                    // Slots behind the end may hold anything, and so may tokens
-                    // that a row does not see: a zero weight would still carry
-                    // their NaN and infinities into the sum.  Such values leave
-                    // the tile; those of tokens that a row does see are added
-                    // to it here.
-                    const uint32_t strip = v_s;
-                    for (int key = 0; key < kWarpKeys; ++key) {
-                        const int vr = warp * kWarpKeys + key;
-                        bool odd = key >= have;
-                        if (!odd && hidden) {
-                            for (int u = lane; u < D / 8; u += 32) {
-                                uint4 v;
-                                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                             : "r"(strip + unit_at(vr, u, kKeyTile)));
-                                const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float2 f = T::unpack(wd[i]);
-                                    odd |= !isfinite(f.x) || !isfinite(f.y);
-                                }
-                            }
-                            odd = __any_sync(0xffffffffu, odd);
-                            if (odd) {
-                                const int src = rg * 4 + ((key & 7) >> 1);
-                                float pk[2], xk[2];
-#pragma unroll
-                                for (int r = 0; r < 2; ++r) {
-                                    const float e0 = __shfl_sync(0xffffffffu, key < 8 ? e[r][0] : e[r][2], src);
-                                    const float e1 = __shfl_sync(0xffffffffu, key < 8 ? e[r][1] : e[r][3], src);
-                                    const float x0 = __shfl_sync(0xffffffffu, key < 8 ? x[r][0] : x[r][2], src);
-                                    const float x1 = __shfl_sync(0xffffffffu, key < 8 ? x[r][1] : x[r][3], src);
-                                    pk[r] = key & 1 ? e1 : e0;
-                                    xk[r] = key & 1 ? x1 : x0;
-                                }
-#pragma unroll
-                                for (int i = 0; i < D / 8; ++i) {
-                                    const float2 f = T::unpack(lds_u32_ordered(strip + unit_at(vr, i, kKeyTile) + 4 * ct));
-#pragma unroll
-                                    for (int r = 0; r < 2; ++r)
-                                        if (xk[r] != -INFINITY) {
-                                            o[i][2 * r] = fmaf(pk[r], f.x, o[i][2 * r]);
-                                            o[i][2 * r + 1] = fmaf(pk[r], f.y, o[i][2 * r + 1]);
-                                        }
-                                }
+                            for (int i = 0; i < D / 16; ++i) {
+                                o[i][n][r] *= f;
+                                o[i][n][2 + r] *= f;
                             }
                         }
-                        __syncwarp();
-                        if (odd)
-                            for (int u = lane; u < D / 8; u += 32)
-                                sts_u128(strip + unit_at(vr, u, kKeyTile), make_uint4(0, 0, 0, 0));
+                }
+                float e[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float shift = m[n][r] == -INFINITY ? 0.f : kWeightBits - m[n][r];
+                        e[n][r] = fast_exp2(x[n][r] + shift);
+                        e[n][2 + r] = fast_exp2(x[n][2 + r] + shift);
+                        l[n][r] += e[n][r] + e[n][2 + r];
                     }
-                    __syncwarp();
-                    fence_proxy_async_smem();  // these writes come before the slot's next copy
-                }
-                uint32_t pf[4][Parts<T>::kN], pn[Parts<T>::kN][4];
+
+                if (!v_wait()) continue;
+                if (hidden || have < kWarpKeys) scrub_strip<D, T, NT>(v_s, chunk_stride, have, hidden, x, e, o);
+                uint32_t pf[Parts<T>::kN][NT][2];  // B operand: keys 2 ct, 2 ct + 1 (+ 8), row rg
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = i & 1, k = (i >> 1) * 2;
-                    Parts<T>::split(make_float2(e[r][k], e[r][k + 1]), pf[i]);
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < Parts<T>::kN; ++n) pn[n][i] = pf[i][n];
-                }
-                const int vr = warp * kWarpKeys + (lane & 15);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t part[Parts<T>::kN];
+                        Parts<T>::split(make_float2(e[n][2 * h], e[n][2 * h + 1]), part);
+#pragma unroll
+                        for (int i = 0; i < Parts<T>::kN; ++i) pf[i][n][h] = transpose8(part[i]);
+                    }
+                const int vr = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     uint32_t vf[4];
-                    ldsm4_t(v_s + unit_at(vr, 2 * i + (lane >> 4), kKeyTile), vf);
+                    ldsm4_t(v_s + strip_unit(vr, 2 * i + ((lane >> 3) & 1), chunk_stride), vf);
                     // A product of its own, smallest parts first, added to o by
                     // rounded fp32 adds: the MMA cuts its sums off instead of
                     // rounding them, which over thousands of tiles would lean
                     // all to one side (4e-5 of the result at 131k tokens).
-                    float t[2][4];
 #pragma unroll
-                    for (int n = 0; n < 8; ++n) (&t[0][0])[n] = 0.f;
+                    for (int n = 0; n < NT; ++n) {
+                        float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int n = Parts<T>::kN - 1; n >= 0; --n) {
-                        mma16816<T>(t[0], pn[n], vf[0], vf[1]);
-                        mma16816<T>(t[1], pn[n], vf[2], vf[3]);
-                    }
+                        for (int k = Parts<T>::kN - 1; k >= 0; --k) mma16816<T>(t, vf, pf[k][n][0], pf[k][n][1]);
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        o[2 * i][n] += t[0][n];
-                        o[2 * i + 1][n] += t[1][n];
+                        for (int k = 0; k < 4; ++k) o[i][n][k] += t[k];
                     }
                 }
             } else {
-                kv_wait(v_full + st, par, abort_flag, err, kDevErrTimeoutKv);
+                k_done();
+                if (!v_wait()) continue;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(slot_free + st);
+            if (lane == 0) mbar_arrive(slot_free + v_st);
         }
 
         // Join the warps' results.
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            if (ct == 0) ml[warp * kRowTile + rg + 8 * r] = make_float2(m[r], l[r]);
-        }
-        consumer_sync();
-        float f[2], top[2], sum[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            top[r] = -INFINITY;
-            sum[r] = 0.f;
-            for (int i = 0; i < kConsumers; ++i) top[r] = fmaxf(top[r], ml[i * kRowTile + rg + 8 * r].x);
-            for (int i = 0; i < kConsumers; ++i) {
-                const float2 t = ml[i * kRowTile + rg + 8 * r];
-                // (a maximum of -inf: the warp saw nothing, sum 0, or only NaN)
-                sum[r] += t.x == -INFINITY ? t.y : t.y * fast_exp2(t.x - top[r]);
-            }
-            f[r] = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - top[r]);
-        }
-        if (warp == 0 && ct == 0) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int row = rg + 8 * r;
-                ml[kConsumers * kRowTile + row] = make_float2(top[r], sum[r]);
-                if (!w.whole && row < rows)
-                    p.part_ml[(int64_t)w.slot * p.slot_rows + row] = make_float2(top[r], sum[r]);
+                float t = l[n][r];
+                t += __shfl_xor_sync(0xffffffffu, t, 4);
+                t += __shfl_xor_sync(0xffffffffu, t, 8);
+                t += __shfl_xor_sync(0xffffffffu, t, 16);
+                if (rg == 0) ml[warp * kRows + 8 * n + 2 * ct + r] = make_float2(m[n][r], t);
             }
-        }
-        constexpr int kCols = C::kJoinCols;
+        consumer_sync();
+        float f[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = 8 * n + 2 * ct + r;
+                float top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < kConsumers; ++i) top = fmaxf(top, ml[i * kRows + row].x);
+#pragma unroll
+                for (int i = 0; i < kConsumers; ++i) {
+                    const float2 t = ml[i * kRows + row];
+                    // (a maximum of -inf: the warp saw nothing, sum 0, or only NaN)
+                    sum += t.x == -INFINITY ? t.y : t.y * fast_exp2(t.x - top);
+                }
+                f[n][r] = m[n][r] == -INFINITY ? 0.f : fast_exp2(m[n][r] - top);
+                if (warp == 0 && rg == 0) {
+                    ml[kConsumers * kRows + row] = make_float2(top, sum);
+                    if (!w.whole && row < rows) p.part_ml[(int64_t)w.slot * p.slot_rows + row] = make_float2(top, sum);
+                }
+            }
+        constexpr int kCols = C::kJoinCols, kPitch = C::kJoinPitch;
 #pragma unroll
         for (int ch = 0; ch < D / kCols; ++ch) {
+            if (ch > 0) consumer_sync();
 #pragma unroll
-            for (int i = 0; i < kCols / 8; ++i) {
-                const float* v = o[ch * (kCols / 8) + i];
-                float* to = join + warp * kRowTile * kCols + i * 8 + 2 * ct;
-                *reinterpret_cast<float2*>(to + rg * kCols) = make_float2(v[0] * f[0], v[1] * f[0]);
-                *reinterpret_cast<float2*>(to + (rg + 8) * kCols) = make_float2(v[2] * f[1], v[3] * f[1]);
-            }
+            for (int i = 0; i < kCols / 16; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        join[(warp * kRows + 8 * n + 2 * ct + (k & 1)) * kPitch + 16 * i + rg + (k >> 1) * 8] =
+                            o[ch * (kCols / 16) + i][n][k] * f[n][k & 1];
             consumer_sync();
             for (int u = threadIdx.x; u < rows * (kCols / 4); u += 32 * kConsumers) {
                 const int r = u / (kCols / 4), col = u % (kCols / 4) * 4;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < kConsumers; ++i) {
-                    const float4 t = *reinterpret_cast<const float4*>(join + (i * kRowTile + r) * kCols + col);
+                    const float4 t = *reinterpret_cast<const float4*>(join + (i * kRows + r) * kPitch + col);
                     v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
                 }
                 if (w.whole) {
-                    const float sum_r = ml[kConsumers * kRowTile + r].y;
-                    const float inv = sum_r == 0.f ? 0.f : 1.f / sum_r;  // a row that sees nothing: zeros
-                    const int row = w.row_tile * kRowTile + r, t = token_of(p, row);
+                    const float sum = ml[kConsumers * kRows + r].y;
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: zeros
+                    const int row = w.row_tile * kRows + r, t = token_of(p, row);
                     float* dst = p.out + (w.w.row0 + t) * p.out_row_stride +
                                  ((int64_t)w.head * p.group + row - t * p.group) * D + ch * kCols + col;
                     if (bc_global(bc, dst, 16, p.out,
@@ -461,38 +518,47 @@ __global__ void __launch_bounds__(kThreads, MmaAttn<D>::kCtas)
                     *reinterpret_cast<float4*>(dst) = v;
                 }
             }
-            consumer_sync();
         }
+        consumer_sync();
     }
 }
 
-template <int D, class T>
+template <int D, class T, int NT>
 cudaError_t launch_one(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const CacheView& c,
                        const BatchView& b, int* err, cudaStream_t stream) {
-    const cudaError_t e = allow_smem<attention_mma_kernel<D, T>>(MmaAttn<D>::kSmem);
+    const cudaError_t e = allow_smem<attention_mma_kernel<D, T, NT>>(MmaAttn<D, NT>::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_chained(attention_mma_kernel<D, T>, dim3((unsigned)p.ctas), dim3(kThreads), MmaAttn<D>::kSmem, stream,
-                          tk, tv, p, c, b, err);
+    return launch_chained(attention_mma_kernel<D, T, NT>, dim3((unsigned)p.ctas), dim3(MmaAttn<D, NT>::kThreads),
+                          MmaAttn<D, NT>::kSmem, stream, tk, tv, p, c, b, err);
+}
+
+template <int D, class T>
+cudaError_t launch_width(int row_tile, const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                         const CacheView& c, const BatchView& b, int* err, cudaStream_t stream) {
+    if (row_tile == 8) return launch_one<D, T, 1>(p, tk, tv, c, b, err, stream);
+    if (row_tile == 16) return launch_one<D, T, 2>(p, tk, tv, c, b, err, stream);
+    return cudaErrorInvalidValue;
 }
 
 template <class T>
-cudaError_t launch_type(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const CacheView& c,
-                        const BatchView& b, int* err, cudaStream_t stream) {
+cudaError_t launch_type(int row_tile, const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                        const CacheView& c, const BatchView& b, int* err, cudaStream_t stream) {
     switch (c.head_dim) {
-        case 64: return launch_one<64, T>(p, tk, tv, c, b, err, stream);
-        case 128: return launch_one<128, T>(p, tk, tv, c, b, err, stream);
-        case 256: return launch_one<256, T>(p, tk, tv, c, b, err, stream);
+        case 64: return launch_width<64, T>(row_tile, p, tk, tv, c, b, err, stream);
+        case 128: return launch_width<128, T>(row_tile, p, tk, tv, c, b, err, stream);
+        case 256: return launch_width<256, T>(row_tile, p, tk, tv, c, b, err, stream);
         default: return cudaErrorInvalidValue;
     }
 }
 
 }  // namespace
 
-cudaError_t launch_attention_mma(const AttnParams& p, const void* tk, const void* tv, const CacheView& c,
+cudaError_t launch_attention_mma(int row_tile, const AttnParams& p, const void* tk, const void* tv, const CacheView& c,
                                  const BatchView& b, bool bf16, int* err, cudaStream_t stream) {
     const CUtensorMap& mk = *static_cast<const CUtensorMap*>(tk);
     const CUtensorMap& mv = *static_cast<const CUtensorMap*>(tv);
-    return bf16 ? launch_type<KvBf16>(p, mk, mv, c, b, err, stream) : launch_type<KvF16>(p, mk, mv, c, b, err, stream);
+    return bf16 ? launch_type<KvBf16>(row_tile, p, mk, mv, c, b, err, stream)
+                : launch_type<KvF16>(row_tile, p, mk, mv, c, b, err, stream);
 }
 
 }  // namespace iq4xs

@@ -234,26 +234,6 @@ __device__ __forceinline__ float weigh(const AttnParams& p, const RowSight& sigh
     l += l2.x + l2.y;
     return f;
 }
-// Page ids of 32 pages of a sequence, one a lane, and the 32 behind them on their way.
-struct PageWindow {
-    const int32_t* table;
-    int held, first, ids, ids2;
-    __device__ __forceinline__ int read(int page) const { return page < held ? table[page] : -1; }
-    __device__ __forceinline__ void open(const BatchView& b, int s) {
-        table = b.page_table + s * b.table_stride;
-        held = min(b.held[s], b.table_width);
-        first = -64;
-        ids2 = -1;
-    }
-    // Brings the window over `page`, a tile's first; by a whole warp.
-    __device__ __forceinline__ void move(int page, int lane) {
-        if (page >= first && page < first + 32) return;
-        ids = page == first + 32 ? ids2 : read(page + lane);
-        first = page;
-        ids2 = read(page + 32 + lane);
-    }
-    __device__ __forceinline__ int id(int page) const { return __shfl_sync(0xffffffffu, ids, (page - first) & 31); }
-};
 // Takes NaN and infinities out of a V tile's keys first .. have - 1, and
 // everything out of those behind; all softmax threads.  True where a thread
 // found some among the former.
@@ -373,19 +353,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kFirstSoft) {
         if constexpr (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        // One tile of K or V into its place of the ring, by a whole warp: a
-        // box of up to 64 slots x 64 channels a lane.  False: a wait ran out.
-        const int box_slots = min(c.page_size, 64);
-        const int boxes = C::kTile / box_slots * C::kChunks;  // at most 16
-        const uint32_t box_bytes = box_slots * kChunkBytes;
-        const int sub = lane / C::kChunks, chunk = lane % C::kChunks;
-        const uint32_t dst0 = base + chunk * C::kChunkStride + sub * box_bytes;
+        // One tile of K or V into its place of the ring, by a whole warp, a
+        // box a lane.  False: a wait ran out.
+        const int boxes_down = C::kTile / p.box_slots, boxes_across = C::kChunks / p.box_chunks;  // together <= 16
+        const int sub = lane / boxes_across, chunk = lane % boxes_across;
+        const uint32_t box_bytes = p.box_slots * p.box_chunks * kChunkBytes;
+        const uint32_t dst0 = base + chunk * C::kChunkStride + sub * p.box_slots * kChunkBytes;
         auto load = [&](const void* map, const Item& d, int tile, int place, PageWindow& pages) {
-            const int st = place % C::kSlots, pos0 = tile * C::kTile, pos = pos0 + sub * box_slots;
+            const int st = place % C::kSlots, pos0 = tile * C::kTile, pos = pos0 + sub * p.box_slots;
             pages.move(pos0 >> c.page_shift, lane);
             int page = pages.id(pos >> c.page_shift);
-            const int used = min(
-                boxes, (min(C::kTile, d.len + d.tokens - pos0) + box_slots - 1) / box_slots * C::kChunks);
+            // boxes that hold a key: those of slots at or behind the end stay out
+            const int used = boxes_across * min(boxes_down, (d.len + d.tokens - pos0 + p.box_slots - 1) / p.box_slots);
             if (place >= C::kSlots &&
                 !warp_wait(slot_free + st, ((place / C::kSlots) - 1) & 1, abort_flag, err, kDevErrTimeoutKvSlot))
                 return false;
@@ -401,9 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     page = c.pages;  // outside the map: zeros
                 }
                 const int slot = pos & (c.page_size - 1);
-                bc_tma(bc, chunk * 64, 2, 64, D, slot, c.page_size, kBcAttnKv, kBcAttnKv);
-                tma_load_4d(dst0 + st * C::kTileBytes, map, chunk * 64, p.slot_axis == 1 ? slot : d.head,
-                            p.slot_axis == 1 ? d.head : slot, page, full + st);
+                bc_tma(bc, 0, 2, 64, 64, slot, c.page_size, kBcAttnKv, kBcAttnKv);
+                tma_load_kv(dst0 + st * C::kTileBytes, map, slot, chunk, d.head, page, full + st);
             }
             __syncwarp();
             return true;

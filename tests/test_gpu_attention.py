@@ -74,6 +74,25 @@ def test_long_context_is_split_and_joined():
     _check(bt, _q(bt, 8))
 
 
+@pytest.mark.parametrize("d,heads,group,rows", [(64, 1, 4, 1), (64, 2, 8, 2), (128, 1, 8, 1), (128, 1, 4, 4),
+                                                (256, 1, 6, 1), (256, 1, 8, 2), (256, 1, 6, 8), (64, 1, 5, 6)])
+def test_rings_go_round_many_times(d, heads, group, rows):
+    """Hundreds of key tiles a CTA, on every form: each slot of the rings is
+    filled and freed many times."""
+    bt = Batch([200011], [rows], heads=heads, d=d, page=256, garbage=None)
+    q = _q(bt, heads * group)
+    out = run_attention(bt, q, d ** -0.5)
+    k, v = bt.gather(0, 200011 + rows)
+    seen = torch.arange(200011 + rows, device="cuda") <= torch.arange(200011, 200011 + rows, device="cuda")[:, None]
+    ref = torch.empty(rows, heads * group, d, dtype=torch.float64, device="cuda")
+    for h in range(heads * group):
+        x = (q[:, h].double() @ k[:, h // group].T * d ** -0.5).masked_fill(~seen, -float("inf"))
+        ref[:, h] = torch.softmax(x, -1) @ v[:, h // group]
+    r = gate_parity(out.cpu().numpy(), ref.flatten(1).cpu().numpy())
+    assert r is None, r
+    assert B.iq4xs_last_device_error() == 0
+
+
 def test_many_short_sequences_and_empty_ones():
     rng = np.random.default_rng(3)
     lens = rng.integers(0, 90, 150).tolist()
