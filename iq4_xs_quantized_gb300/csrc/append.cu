@@ -225,8 +225,8 @@ cudaError_t launch_width(const AppendParams& p, const CacheView& c, const BatchV
     const int heads = p.q_heads + 2 * c.heads;
     const int64_t units = (int64_t)p.rows * ((heads + heads_of<D>() - 1) / heads_of<D>());
     const dim3 grid((unsigned)((units + kAppendThreads / 32 - 1) / (kAppendThreads / 32)));
-    return inter ? launch_chained(qk_norm_rope_kernel<D, T, true>, grid, dim3(kAppendThreads), 0, stream, p, c, b, err)
-                 : launch_chained(qk_norm_rope_kernel<D, T, false>, grid, dim3(kAppendThreads), 0, stream, p, c, b, err);
+    return inter ? launch_chained(qk_norm_rope_kernel<D, T, true>, grid, dim3(kAppendThreads), 0, stream, 1, p, c, b, err)
+                 : launch_chained(qk_norm_rope_kernel<D, T, false>, grid, dim3(kAppendThreads), 0, stream, 1, p, c, b, err);
 }
 
 template <class T>

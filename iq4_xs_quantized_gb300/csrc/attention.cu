@@ -11,7 +11,12 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-constexpr int64_t kWholeTokens = 512;
+// Where no sequence can be longer than this (the table's width), in tokens:
+// items are not cut; or from kAloneTokens on a cluster shares an item, if the
+// SMs hold all items' clusters.  Measured for one token, 24/4 heads of 256, as
+// a cluster / not cut / cut and joined: 100 cached tokens 8.7 / 7.7 us, 517
+// 9.1 / 19.5 / 13.4, 2000 10.4 / 53 / 20.4, 16000 30 / - / 33.
+constexpr int64_t kWholeTokens = 512, kAloneTokens = 128, kClusterTokens = 16384;
 static_assert(sizeof(SplitOut) == 32, "partial results stay aligned");
 
 // One map over K or V of a layer: 64 channels, slots, 64-channel chunks, heads,
@@ -32,16 +37,19 @@ bool encode_kv(EncodeTiledFn enc, uint16_t* base, const CacheView& c, bool bf16,
 
 // ------------------------------------------------------------------- join
 // A CTA per (row, query head) whose item was cut: the partial results of the
-// CTAs that share it, weighted by exp2(m_i - m), over the joined sum.  Warps
-// take every fourth part and add up in shared memory, in a fixed order.
-constexpr int kJoinWarps = 4;
+// CTAs that share it, weighted by exp2(m_i - m), over the joined sum.  Groups
+// of D / 4 threads take parts in turn, kJoinBatch of them in flight, and add
+// up in shared memory in a fixed order.
+constexpr int kJoinThreads = 128, kJoinBatch = 8;
+constexpr int kMaxParts = 256;
 
 template <int D, class F>
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(kJoinThreads)
     attention_join_kernel(const AttnParams p, const BatchView b, int* err) {
-    constexpr int kPer = D / 32;
-    __shared__ float acc_s[kJoinWarps][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kAcross = D / 4, kGroups = kJoinThreads / kAcross;
+    __shared__ float4 acc_s[kJoinThreads];
+    __shared__ float2 ml_s[kMaxParts];
+    const int lane = threadIdx.x & 31;
     const int row = blockIdx.x, head = blockIdx.y;
     // The attention kernel lets this grid start behind its own wait for what
     // came before, so offsets and lengths are final; the split and the
@@ -73,54 +81,70 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     const int first = split.owner(x), last = split.owner(x + unit - 1);
     if (first == last) return;
 
+    const int n = last - first + 1;  // (at most the CTAs, which kMaxParts holds)
+    const int group = threadIdx.x / kAcross, col = threadIdx.x % kAcross * 4;
+    const auto slot_of = [&](int i) { return (int64_t)(2 * (first + i) + (i == 0)) * p.slot_rows + r; };
+    for (int i = threadIdx.x; i < n; i += kJoinThreads) ml_s[i] = p.part_ml[slot_of(i)];
+    float4 v[kJoinBatch];
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k) {  // (the last part again instead of a branch)
+        const int i = min(group + k * kGroups, n - 1);
+        v[k] = *reinterpret_cast<const float4*>(p.part_o + slot_of(i) * D + col);
+    }
+    __syncthreads();
     float top = -INFINITY, sum = 0.f;
-    for (int i = first + lane; i <= last; i += 32)
-        top = fmaxf(top, p.part_ml[(int64_t)(2 * i + (i == first)) * p.slot_rows + r].x);
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, ml_s[i].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int i = first + lane; i <= last; i += 32) {
-        const float2 t = p.part_ml[(int64_t)(2 * i + (i == first)) * p.slot_rows + r];
+    for (int i = lane; i < n; i += 32) {
+        const float2 t = ml_s[i];
         sum += t.x == -INFINITY ? t.y : t.y * fast_exp2(t.x - top);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-
-    float acc[kPer];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = group; i0 < n; i0 += kJoinBatch * kGroups) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-#pragma unroll 4
-    for (int i = first + warp; i <= last; i += kJoinWarps) {
-        const int64_t at = (int64_t)(2 * i + (i == first)) * p.slot_rows + r;
-        const float2 t = p.part_ml[at];
-        const float f = t.x == -INFINITY ? t.y : fast_exp2(t.x - top);
-        const float* v = p.part_o + at * D + kPer * lane;
+        for (int k = 0; k < kJoinBatch; ++k) {
+            const int i = i0 + k * kGroups;
+            if (i < n) {
+                const float2 t = ml_s[i];
+                const float f = t.x == -INFINITY ? t.y : fast_exp2(t.x - top);  // (nothing seen: 0, or NaN)
+                acc.x = fmaf(v[k].x, f, acc.x);
+                acc.y = fmaf(v[k].y, f, acc.y);
+                acc.z = fmaf(v[k].z, f, acc.z);
+                acc.w = fmaf(v[k].w, f, acc.w);
+            }
+        }
+        if (i0 + kJoinBatch * kGroups < n) {
 #pragma unroll
-        for (int k = 0; k < kPer; k += 2) {
-            const float2 u = *reinterpret_cast<const float2*>(v + k);
-            acc[k] = fmaf(u.x, f, acc[k]);
-            acc[k + 1] = fmaf(u.y, f, acc[k + 1]);
+            for (int k = 0; k < kJoinBatch; ++k) {
+                const int i = min(i0 + (kJoinBatch + k) * kGroups, n - 1);
+                v[k] = *reinterpret_cast<const float4*>(p.part_o + slot_of(i) * D + col);
+            }
         }
     }
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) acc_s[warp][kPer * lane + k] = acc[k];
+    acc_s[threadIdx.x] = acc;
     __syncthreads();
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
-        float v = 0.f;
+    if (group != 0) return;
 #pragma unroll
-        for (int i = 0; i < kJoinWarps; ++i) v += acc_s[i][d];
-        p.out[row * p.out_row_stride + (int64_t)head * D + d] = v * inv;
+    for (int i = 1; i < kGroups; ++i) {
+        const float4 t = acc_s[i * kAcross + threadIdx.x];
+        acc.x += t.x; acc.y += t.y; acc.z += t.z; acc.w += t.w;
     }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<float4*>(p.out + row * p.out_row_stride + (int64_t)head * D + col) =
+        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
 }
 
 template <int D>
 cudaError_t launch_join_width(int row_tile, const AttnParams& p, const BatchView& b, dim3 grid, int* err,
                               cudaStream_t stream) {
-    const dim3 block(32 * kJoinWarps);
+    const dim3 block(kJoinThreads);
     switch (row_tile) {
-        case 8: return launch_chained(attention_join_kernel<D, MmaForm<1>>, grid, block, 0, stream, p, b, err);
-        case 16: return launch_chained(attention_join_kernel<D, MmaForm<2>>, grid, block, 0, stream, p, b, err);
-        default: return launch_chained(attention_join_kernel<D, TcForm<D>>, grid, block, 0, stream, p, b, err);
+        case 8: return launch_chained(attention_join_kernel<D, MmaForm<1>>, grid, block, 0, stream, 1, p, b, err);
+        case 16: return launch_chained(attention_join_kernel<D, MmaForm<2>>, grid, block, 0, stream, 1, p, b, err);
+        default: return launch_chained(attention_join_kernel<D, TcForm<D>>, grid, block, 0, stream, 1, p, b, err);
     }
 }
 cudaError_t launch_join(int row_tile, const AttnParams& p, const BatchView& b, int q_heads, int* err,
@@ -174,8 +198,20 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     const int64_t mean_rows = (a.rows + b.sequences - 1) / b.sequences * group;
     const int row_tile = mean_rows <= 8 ? 8 : mean_rows <= 16 ? 16 : 128;
     const bool tc = row_tile == 128;
-    p.ctas = num_sms;
-    p.whole_items = (int64_t)b.table_width * c.page_size <= kWholeTokens;
+    p.ctas = num_sms < kMaxParts ? num_sms : kMaxParts;
+    p.cluster = 1;
+    const int64_t tokens = (int64_t)b.table_width * c.page_size;  // no sequence is longer
+    p.whole_items = tokens <= kWholeTokens;
+    if (!tc && tokens > kAloneTokens && tokens <= kClusterTokens) {
+        // Items there can be at most: a row tile more than whole ones a sequence.
+        const int64_t items =
+            c.heads * ((a.rows < b.sequences ? a.rows : b.sequences) + a.rows * group / row_tile);
+        if (items * (kMaxCluster + 1) <= num_sms) {  // (a GPC's SMs are no multiple of eight)
+            p.cluster = kMaxCluster;
+            p.ctas = (int)items;
+            p.whole_items = 1;
+        }
+    }
     p.slot_rows = (int)slot_rows(row_tile, a.rows, group);
     // Measured: starting and ending a part costs about 8 key tiles on tcgen05, 3 on the warp-level form.
     p.part_tiles = tc ? 8 : 3;

@@ -13,7 +13,8 @@
 //                    tiles, whatever the lengths, and may cut two items
 //   cut = L          an item is L tiles at most a place, and there are no
 //                    more places than CTAs: a CTA has one part of one item
-//   cut = kWhole     items are not cut (short contexts)
+//   cut = kWhole     items are not cut (short contexts), or by a cluster of
+//                    CTAs that join their parts themselves
 //
 // An item that is cut is joined afterwards: a CTA leaves at most two partial
 // results, slot 2 g for a part that does not begin its item, 2 g + 1 for one
@@ -28,6 +29,7 @@
 namespace iq4xs {
 
 constexpr int kWhole = INT32_MAX;
+constexpr int kMaxCluster = 8;
 
 struct AttnParams {
     const uint16_t* q;
@@ -45,6 +47,7 @@ struct AttnParams {
     int wide_out;      // out and its rows are 32-byte aligned
     int ctas;          // CTAs the work is split over, at most
     int whole_items;   // 1: cut = kWhole
+    int cluster;       // CTAs that share an item, meeting in shared memory (1: none); then p.ctas counts clusters
     int part_tiles;    // what starting and ending a part costs, in key tiles
     int slot_rows;     // rows of a partial result: the row tile, or all rows if fewer
     int box_slots, box_chunks;  // of a copy: slots of a page, 64-channel chunks
@@ -172,6 +175,7 @@ struct WorkWalk {
     int head, row_tile, tile0, tile1;
     bool whole;          // this CTA has all of the item's key tiles
     int slot;            // of its partial result, if not
+    static constexpr int kRows = F::kRows;
 
     __device__ __forceinline__ void start(const AttnParams& p, const BatchView& b, int g, int* err) {
         const int lane = threadIdx.x & 31;
@@ -246,6 +250,7 @@ struct WorkWalk {
         slot = 2 * g + (tile0 == 0 ? 1 : 0);
     }
     __device__ __forceinline__ bool valid() const { return left > 0; }
+    __device__ __forceinline__ bool last() const { return left <= (split.cut == 0 ? tile1 - tile0 : 1); }
     __device__ __forceinline__ void next(const AttnParams& p, const BatchView& b, int g, int* err) {
         left -= split.cut == 0 ? tile1 - tile0 : 1;
         if (left <= 0) return;

@@ -44,6 +44,11 @@ struct MmaAttn {
     static constexpr int kJoinCols = NT == 1 ? 64 : 32;      // channels of the warps' outputs joined at a time
     static constexpr int kJoinPitch = kJoinCols + 4;         // (conflict-free for the fragments' rows and channels)
     static constexpr int kJoinBytes = kConsumers * kRows * kJoinPitch * 4;
+    // a CTA's last item joins whole rows in the ring, which nothing fills any
+    // more, and a cluster's parts meet behind them
+    static constexpr int kLastPitch = D + 4;
+    static constexpr int kPart = kConsumers * kRows * kLastPitch * 4;
+    static_assert(kPart + kRows * D * 4 <= kSets * kSlots * kTileBytes, "last join in the ring");
     static constexpr int kQ = kSets * kSlots * kTileBytes;
     static constexpr int kJoin = kQ + kQBytes;
     static constexpr int kMl = kJoin + kJoinBytes;           // per warp and row: max, sum; then joined
@@ -96,6 +101,43 @@ __device__ __forceinline__ void consumers_meet() {
 __device__ __forceinline__ uint32_t strip_unit(int r, int u, uint32_t chunk_stride) {
     return (uint32_t)(u >> 3) * chunk_stride + r * kChunkBytes + (((u & 7) ^ (r & 7)) << 4);
 }
+// All threads of the cluster; what they wrote before is seen after.
+__device__ __forceinline__ void cluster_meet() {
+    __syncwarp();
+    cluster_arrive_release();
+    cluster_wait();
+}
+// What CTA `rank` of the cluster has at the place of `at` in this one.
+__device__ __forceinline__ float2 cluster_read(const float2* at, int rank) {
+    uint32_t a;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 cluster_read(const float4* at, int rank) {
+    uint32_t a;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+// Four channels of an item's row r: the joined sums over the row's total.
+template <class Walk>
+__device__ __forceinline__ void put_row(const AttnParams& p, const CacheView& c, const Walk& w, int r, int channel,
+                                        float4 v, float sum, const Bc& bc) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: zeros
+    const int row = w.row_tile * Walk::kRows + r, t = token_of(p, row), D = c.head_dim;
+    float* dst = p.out + (w.w.row0 + t) * p.out_row_stride + ((int64_t)w.head * p.group + row - t * p.group) * D +
+                 channel;
+    if (bc_global(bc, dst, 16, p.out, 4 * ((p.rows - 1) * p.out_row_stride + (int64_t)p.group * p.kv_heads * D),
+                  kBcAttnOut))
+        *reinterpret_cast<float4*>(dst) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+}
+
 // Keys `have` .. 15 of a warp's V strip become zero, and so does every key
 // that holds NaN or infinities when `hidden` (some row does not see all of the
 // strip): a zero weight would carry such values into rows that do not see
@@ -175,7 +217,7 @@ __global__ void __launch_bounds__(MmaAttn<D, NT>::kThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);  // [set][slot]
     uint64_t* slot_free = full + C::kSets * C::kSlots;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(slot_free + C::kSets * C::kSlots);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.x / p.cluster;
     const Bc bc = bc_open(err);
 
     if (threadIdx.x == 0) {
@@ -195,6 +237,14 @@ __global__ void __launch_bounds__(MmaAttn<D, NT>::kThreads, 1)
     griddep_launch_dependents();
     WorkWalk<F> w;
     w.start(p, b, g, err);
+    // A cluster shares one item, an eighth of its key tiles a CTA.
+    const int rank = p.cluster > 1 ? (int)cluster_ctarank() : 0;
+    if (p.cluster > 1 && w.valid()) {
+        const int tiles = w.w.key_tiles;
+        w.tile0 = rank * tiles / p.cluster;
+        w.tile1 = (rank + 1) * tiles / p.cluster;
+        w.whole = false;
+    }
 
     if (warp >= kConsumers) {
         // ----------------------------------------------- producers: K, then V
@@ -206,6 +256,7 @@ __global__ void __launch_bounds__(MmaAttn<D, NT>::kThreads, 1)
         PageWindow pages;
         int it = 0, last = -1;  // tiles so far; the last place loaded into slot `lane`
         bool live = true;
+        const bool in_cluster = p.cluster > 1 && w.valid();
         for (; live && w.valid(); w.next(p, b, g, err)) {
             const int end = w.seen_tiles(p);
             const int keys = w.w.len + w.w.tokens;
@@ -242,6 +293,10 @@ __global__ void __launch_bounds__(MmaAttn<D, NT>::kThreads, 1)
                 if (place >= 0)
                     mbar_wait(full + i, (place / C::kSlots) & 1, &no_abort, err, kDevErrTimeoutKv);
             }
+        if (in_cluster) {  // (the consumers' two meetings count every thread)
+            cluster_meet();
+            cluster_meet();
+        }
         return;
     }
 
@@ -480,46 +535,87 @@ __global__ void __launch_bounds__(MmaAttn<D, NT>::kThreads, 1)
                 f[n][r] = m[n][r] == -INFINITY ? 0.f : fast_exp2(m[n][r] - top);
                 if (warp == 0 && rg == 0) {
                     ml[kConsumers * kRows + row] = make_float2(top, sum);
-                    if (!w.whole && row < rows) p.part_ml[(int64_t)w.slot * p.slot_rows + row] = make_float2(top, sum);
+                    if (!w.whole && p.cluster == 1 && row < rows)
+                        p.part_ml[(int64_t)w.slot * p.slot_rows + row] = make_float2(top, sum);
                 }
             }
-        constexpr int kCols = C::kJoinCols, kPitch = C::kJoinPitch;
+        const bool last = w.last();
+        constexpr int kCols = C::kJoinCols;
+        float* const buf = last ? reinterpret_cast<float*>(smem) : join;
+        const int pitch = last ? C::kLastPitch : C::kJoinPitch;
+        float* const part = reinterpret_cast<float*>(smem + C::kPart);  // this CTA's part of a cluster's item
+        // Adds up `cols` joined channels from channel c0 on and puts them where they belong.
+        const auto put = [&](int c0, int cols) {
+            for (int u = threadIdx.x; u < rows * (cols / 4); u += 32 * kConsumers) {
+                const int r = u / (cols / 4), col = u % (cols / 4) * 4;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < kConsumers; ++i) {
+                    const float4 t = *reinterpret_cast<const float4*>(buf + (i * kRows + r) * pitch + col);
+                    v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+                }
+                if (p.cluster > 1) {
+                    *reinterpret_cast<float4*>(part + r * D + col) = v;
+                } else if (w.whole) {
+                    put_row(p, c, w, r, c0 + col, v, ml[kConsumers * kRows + r].y, bc);
+                } else {
+                    *reinterpret_cast<float4*>(p.part_o + ((int64_t)w.slot * p.slot_rows + r) * D + c0 + col) = v;
+                }
+            }
+        };
 #pragma unroll
         for (int ch = 0; ch < D / kCols; ++ch) {
-            if (ch > 0) consumer_sync();
+            if (ch > 0 && !last) consumer_sync();
 #pragma unroll
             for (int i = 0; i < kCols / 16; ++i)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        join[(warp * kRows + 8 * n + 2 * ct + (k & 1)) * kPitch + 16 * i + rg + (k >> 1) * 8] =
-                            o[ch * (kCols / 16) + i][n][k] * f[n][k & 1];
-            consumer_sync();
-            for (int u = threadIdx.x; u < rows * (kCols / 4); u += 32 * kConsumers) {
-                const int r = u / (kCols / 4), col = u % (kCols / 4) * 4;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < kConsumers; ++i) {
-                    const float4 t = *reinterpret_cast<const float4*>(join + (i * kRows + r) * kPitch + col);
-                    v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
-                }
-                if (w.whole) {
-                    const float sum = ml[kConsumers * kRows + r].y;
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: zeros
-                    const int row = w.row_tile * kRows + r, t = token_of(p, row);
-                    float* dst = p.out + (w.w.row0 + t) * p.out_row_stride +
-                                 ((int64_t)w.head * p.group + row - t * p.group) * D + ch * kCols + col;
-                    if (bc_global(bc, dst, 16, p.out,
-                                  4 * ((p.rows - 1) * p.out_row_stride + (int64_t)p.group * p.kv_heads * D), kBcAttnOut))
-                        *reinterpret_cast<float4*>(dst) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-                } else {
-                    float* dst = p.part_o + ((int64_t)w.slot * p.slot_rows + r) * D + ch * kCols + col;
-                    *reinterpret_cast<float4*>(dst) = v;
-                }
+                        buf[(warp * kRows + 8 * n + 2 * ct + (k & 1)) * pitch + (last ? ch * kCols : 0) + 16 * i + rg +
+                            (k >> 1) * 8] = o[ch * (kCols / 16) + i][n][k] * f[n][k & 1];
+            if (!last) {
+                consumer_sync();
+                put(ch * kCols, kCols);
             }
         }
         consumer_sync();
+        if (last) put(0, D);
+        if (p.cluster > 1) {
+            cluster_meet();
+            // every CTA joins its share of the item's values from all parts
+            const float2* const my_ml = ml + kConsumers * kRows;
+            for (int u = rank * 32 * kConsumers + threadIdx.x; u < rows * (D / 4); u += p.cluster * 32 * kConsumers) {
+                const int r = u / (D / 4), col = u % (D / 4) * 4;
+                float2 t[kMaxCluster];
+                float4 v[kMaxCluster];
+#pragma unroll
+                for (int i = 0; i < kMaxCluster; ++i) {
+                    t[i] = make_float2(-INFINITY, 0.f);
+                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i < p.cluster) {
+                        t[i] = cluster_read(my_ml + r, i);
+                        v[i] = cluster_read(reinterpret_cast<const float4*>(part + r * D + col), i);
+                    }
+                }
+                float top = -INFINITY, sum = 0.f;
+                float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < kMaxCluster; ++i) top = fmaxf(top, t[i].x);
+#pragma unroll
+                for (int i = 0; i < kMaxCluster; ++i) {
+                    const float a = t[i].x == -INFINITY ? t[i].y : fast_exp2(t[i].x - top);  // (nothing seen: 0, or NaN)
+                    sum += t[i].x == -INFINITY ? t[i].y : t[i].y * a;
+                    all.x = fmaf(v[i].x, a, all.x);
+                    all.y = fmaf(v[i].y, a, all.y);
+                    all.z = fmaf(v[i].z, a, all.z);
+                    all.w = fmaf(v[i].w, a, all.w);
+                }
+                put_row(p, c, w, r, col, all, sum, bc);
+            }
+            cluster_meet();  // no CTA ends while another reads its part
+            return;
+        }
     }
 }
 
@@ -528,8 +624,8 @@ cudaError_t launch_one(const AttnParams& p, const CUtensorMap& tk, const CUtenso
                        const BatchView& b, int* err, cudaStream_t stream) {
     const cudaError_t e = allow_smem<attention_mma_kernel<D, T, NT>>(MmaAttn<D, NT>::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_chained(attention_mma_kernel<D, T, NT>, dim3((unsigned)p.ctas), dim3(MmaAttn<D, NT>::kThreads),
-                          MmaAttn<D, NT>::kSmem, stream, tk, tv, p, c, b, err);
+    return launch_chained(attention_mma_kernel<D, T, NT>, dim3((unsigned)(p.ctas * p.cluster)),
+                          dim3(MmaAttn<D, NT>::kThreads), MmaAttn<D, NT>::kSmem, stream, p.cluster, tk, tv, p, c, b, err);
 }
 
 template <int D, class T>

@@ -815,7 +815,7 @@ cudaError_t launch_one(const AttnParams& p, const CUtensorMap& tk, const CUtenso
                        const BatchView& b, int* err, cudaStream_t stream) {
     const cudaError_t e = allow_smem<attention_tc_kernel<D, T>>(TcAttn<D, T>::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_chained(attention_tc_kernel<D, T>, dim3((unsigned)p.ctas), dim3(kThreads), TcAttn<D, T>::kSmem, stream,
+    return launch_chained(attention_tc_kernel<D, T>, dim3((unsigned)p.ctas), dim3(kThreads), TcAttn<D, T>::kSmem, stream, 1,
                           tk, tv, p, c, b, err);
 }
 

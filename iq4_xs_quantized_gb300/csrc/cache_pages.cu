@@ -439,7 +439,7 @@ cudaError_t launch_cache_reserve(const BatchView& b, int page_size, int32_t* ref
                                  cudaStream_t stream) {
     int shift = 0;
     while ((1 << shift) < page_size) ++shift;
-    return launch_chained(reserve_kernel, dim3(1), dim3(kBookThreads), 0, stream, b, shift, refs, pages, status, err);
+    return launch_chained(reserve_kernel, dim3(1), dim3(kBookThreads), 0, stream, 1, b, shift, refs, pages, status, err);
 }
 
 cudaError_t launch_cache_commit(const CacheView& c, const BatchView& b, int32_t* refs, const int32_t* paths,
@@ -449,40 +449,29 @@ cudaError_t launch_cache_commit(const CacheView& c, const BatchView& b, int32_t*
     const int64_t units = (int64_t)c.layers * 2 * c.heads * (c.head_dim / 8);
     const int64_t full = (units + kMoveThreads - 1) / kMoveThreads;
     const unsigned ctas = full >= 8 ? 8 : full >= 4 ? 4 : full >= 2 ? 2 : 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, (unsigned)b.sequences);
-    cfg.blockDim = dim3(kMoveThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, commit_kernel, c, b, refs, paths, path_width, accepted, new_lens, err);
+    return launch_chained(commit_kernel, dim3(ctas, (unsigned)b.sequences), dim3(kMoveThreads), 0, stream, (int)ctas, c,
+                          b, refs, paths, path_width, accepted, new_lens, err);
 }
 
 cudaError_t launch_cache_fork(const CacheView& c, const BatchView& b, int32_t* refs, const int32_t* parents,
                               const int32_t* children, int count, int32_t* status, int* err, cudaStream_t stream) {
-    const cudaError_t e = launch_chained(fork_book_kernel, dim3(1), dim3(kBookThreads), 0, stream, b, c.page_shift,
+    const cudaError_t e = launch_chained(fork_book_kernel, dim3(1), dim3(kBookThreads), 0, stream, 1, b, c.page_shift,
                                          refs, c.pages, parents, children, count, status, err);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(c.layers * 2 * c.heads), (unsigned)count);
-    return launch_chained(fork_copy_kernel, grid, dim3(kCopyThreads), 0, stream, c, b, parents, children,
+    return launch_chained(fork_copy_kernel, grid, dim3(kCopyThreads), 0, stream, 1, c, b, parents, children,
                           (const int32_t*)status, err);
 }
 
 cudaError_t launch_cache_copy_pages(const CacheView& c, const int32_t* src, const int32_t* dst, int count, int* err,
                                     cudaStream_t stream) {
     const dim3 grid((unsigned)(c.layers * 2 * c.heads), (unsigned)count);
-    return launch_chained(copy_pages_kernel, grid, dim3(kCopyThreads), 0, stream, c, src, dst, err);
+    return launch_chained(copy_pages_kernel, grid, dim3(kCopyThreads), 0, stream, 1, c, src, dst, err);
 }
 
 cudaError_t launch_cache_release(const BatchView& b, int32_t* refs, int pages, const int32_t* rows, int count,
                                  int* err, cudaStream_t stream) {
-    return launch_chained(release_kernel, dim3((unsigned)count), dim3(kMoveThreads), 0, stream, b, refs, pages, rows,
+    return launch_chained(release_kernel, dim3((unsigned)count), dim3(kMoveThreads), 0, stream, 1, b, refs, pages, rows,
                           err);
 }
 

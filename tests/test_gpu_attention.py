@@ -69,6 +69,20 @@ def test_chains_of_new_tokens(t, d, heads, group):
     _check(bt, _q(bt, heads * group))
 
 
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("d,group", [(64, 5), (128, 4), (256, 6)])
+@pytest.mark.parametrize("lens,new", [([600], [1]), ([1000], [2]), ([1, 70], [1, 1]), ([3000], [1]), ([127, 0], [1, 2])])
+def test_few_rows_and_short_contexts(lens, new, d, group, dtype):
+    """What clusters of CTAs share: a part may have no key tile at all."""
+    bt = Batch(lens, new, heads=2, d=d, dtype=dtype, width=1 + 3010 // 16)
+    _check(bt, _q(bt, 2 * group))
+    trees = [random_tree(n, np.random.default_rng(n)) for n in bt.new_n]
+    mask = mask_words([r for tr in trees for r in tr], 1)
+    mask[0] = 0
+    trees[0][0] = set()
+    _check(bt, _q(bt, 2 * group), mask, lambda s, i, j: j in trees[s][i])
+
+
 def test_long_context_is_split_and_joined():
     bt = Batch([20011], [3], heads=1, d=128, page=64, dtype=torch.bfloat16)
     _check(bt, _q(bt, 8))
