@@ -15,9 +15,9 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
 // items are not cut; or from kAloneTokens on a cluster shares an item, if the
 // SMs hold all items' clusters.  Measured for one token, 24/4 heads of 256, as
 // a cluster / not cut / cut and joined: 100 cached tokens 8.7 / 7.7 us, 517
-// 9.1 / 19.5 / 13.4, 2000 10.4 / 53 / 20.4, 16000 30 / - / 33.
-constexpr int64_t kWholeTokens = 512, kAloneTokens = 128, kClusterTokens = 16384;
-static_assert(sizeof(SplitOut) == 32, "partial results stay aligned");
+// 9.0 / 19.5 / 10.4, 2000 10.5 / 53 / 10.8, 8000 19.2 / - / 14.4.
+constexpr int64_t kWholeTokens = 512, kAloneTokens = 128, kClusterTokens = 2048;
+static_assert(sizeof(CutItem) == 32, "partial results stay aligned");
 
 // One map over K or V of a layer: 64 channels, slots, 64-channel chunks, heads,
 // pages.  A box is up to `slots` slots of a page by `chunks` chunks, and lies
@@ -36,124 +36,130 @@ bool encode_kv(EncodeTiledFn enc, uint16_t* base, const CacheView& c, bool bf16,
 }
 
 // ------------------------------------------------------------------- join
-// A CTA per (row, query head) whose item was cut: the partial results of the
-// CTAs that share it, weighted by exp2(m_i - m), over the joined sum.  Groups
-// of D / 4 threads take parts in turn, kJoinBatch of them in flight, and add
-// up in shared memory in a fixed order.
-constexpr int kJoinThreads = 128, kJoinBatch = 8;
+// The partial results of cut items, weighted by exp2(m_i - m), over the joined
+// sum; a CTA per cut item and some of its rows, whose addresses the attention
+// kernel left.  Groups of D / 4 threads own the D channels of a row: with few
+// parts an item (kByRows) the groups take rows, with many they take parts of
+// one row, kJoinBatch in flight each, and add up in shared memory.  Sums have
+// a fixed order.
+constexpr int kJoinThreads = 256, kJoinBatch = 8, kJoinRows = 8;
 constexpr int kMaxParts = 256;
 
-template <int D, class F>
-__global__ void __launch_bounds__(kJoinThreads)
-    attention_join_kernel(const AttnParams p, const BatchView b, int* err) {
+template <int D, bool kByRows>
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p) {
     constexpr int kAcross = D / 4, kGroups = kJoinThreads / kAcross;
-    __shared__ float4 acc_s[kJoinThreads];
-    __shared__ float2 ml_s[kMaxParts];
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x, head = blockIdx.y;
-    // The attention kernel lets this grid start behind its own wait for what
-    // came before, so offsets and lengths are final; the split and the
-    // partial results are not.
-    int s = 0;
-    for (int s0 = 0; s0 < b.sequences; s0 += 32) {
-        const unsigned done =
-            __ballot_sync(0xffffffffu, s0 + lane < b.sequences && b.row_offsets[s0 + lane + 1] <= row);
-        s += __popc(done);
-        if (done != 0xffffffffu) break;
-    }
-    const bool mine = s < b.sequences && row >= b.row_offsets[0];
-    const SeqWork w = seq_work<F>(p, b, mine ? s : b.sequences, err);
-    const SeqWork lane_w = seq_work<F>(p, b, lane < s ? lane : b.sequences, err);
-    const int kv_head = token_of(p, head);  // (head / group)
-    int r = (row - w.row0) * p.group + head - kv_head * p.group;
+    __shared__ float4 acc_s[kByRows ? 1 : kJoinThreads];
+    __shared__ float2 ml_s[kByRows ? 1 : kMaxParts];
     griddep_wait();
     griddep_launch_dependents();
-    if (!mine || w.tokens == 0 || row < w.row0) return;
-    Split split;
-    static_cast<SplitOut&>(split) = *p.split_out;
-    const int unit = w.unit(split.cut);
-    if (unit == 1) return;
-    int64_t x = lane_w.places(p, split.cut);
-    for (int s0 = 32; s0 < s; s0 += 32)
-        if (s0 + lane < s) x += seq_work<F>(p, b, s0 + lane, err).places(p, split.cut);
-    x = warp_sum(x) + ((int64_t)kv_head * w.row_tiles + r / F::kRows) * unit;
-    r %= F::kRows;
-    const int first = split.owner(x), last = split.owner(x + unit - 1);
-    if (first == last) return;
-
-    const int n = last - first + 1;  // (at most the CTAs, which kMaxParts holds)
-    const int group = threadIdx.x / kAcross, col = threadIdx.x % kAcross * 4;
-    const auto slot_of = [&](int i) { return (int64_t)(2 * (first + i) + (i == 0)) * p.slot_rows + r; };
-    for (int i = threadIdx.x; i < n; i += kJoinThreads) ml_s[i] = p.part_ml[slot_of(i)];
-    float4 v[kJoinBatch];
+    const CutItem cut = p.cuts[blockIdx.x];
+    const int row0 = blockIdx.y * (kByRows ? kJoinRows : 1);
+    if (cut.first < 0 || row0 >= cut.rows) return;
+    const int n = (int)blockIdx.x - cut.first + 1;  // (at most the CTAs, which kMaxParts holds)
+    const int lane = threadIdx.x & 31, group = threadIdx.x / kAcross, col = threadIdx.x % kAcross * 4;
+    const auto slot_of = [&](int i, int r) { return (int64_t)(2 * (cut.first + i) + (i == 0)) * p.slot_rows + r; };
+    const auto add = [](float4& a, float4 v, float f) {
+        a.x = fmaf(v.x, f, a.x);
+        a.y = fmaf(v.y, f, a.y);
+        a.z = fmaf(v.z, f, a.z);
+        a.w = fmaf(v.w, f, a.w);
+    };
+    const auto put = [&](int r, float4 a, float sum) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: zeros
+        const int row = cut.first_row + r, t = token_of(p, row);
+        *reinterpret_cast<float4*>(p.out + (cut.row0 + t) * p.out_row_stride +
+                                   ((int64_t)cut.head * p.group + row - t * p.group) * D + col) =
+            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    };
+    if constexpr (kByRows) {
+        for (int r = row0 + group; r < min(row0 + kJoinRows, cut.rows); r += kGroups) {
+            float top = -INFINITY, sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i0 = 0; i0 < n; i0 += kJoinBatch) {
+                float2 ml[kJoinBatch];
+                float4 v[kJoinBatch];
 #pragma unroll
-    for (int k = 0; k < kJoinBatch; ++k) {  // (the last part again instead of a branch)
-        const int i = min(group + k * kGroups, n - 1);
-        v[k] = *reinterpret_cast<const float4*>(p.part_o + slot_of(i) * D + col);
-    }
-    __syncthreads();
-    float top = -INFINITY, sum = 0.f;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, ml_s[i].x);
+                for (int k = 0; k < kJoinBatch; ++k) {  // (the last part again instead of a branch)
+                    const int64_t at = slot_of(min(i0 + k, n - 1), r);
+                    ml[k] = p.part_ml[at];
+                    v[k] = *reinterpret_cast<const float4*>(p.part_o + at * D + col);
+                }
+                float most = top;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int i = lane; i < n; i += 32) {
-        const float2 t = ml_s[i];
-        sum += t.x == -INFINITY ? t.y : t.y * fast_exp2(t.x - top);
-    }
+                for (int k = 0; k < kJoinBatch; ++k) most = fmaxf(most, ml[k].x);
+                if (most > top) {
+                    const float f = fast_exp2(top - most);
+                    sum *= f;
+                    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+                    top = most;
+                }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = group; i0 < n; i0 += kJoinBatch * kGroups) {
+                for (int k = 0; k < kJoinBatch; ++k)
+                    if (i0 + k < n) {
+                        const bool none = ml[k].x == -INFINITY;  // (nothing seen: sum 0, or NaN)
+                        const float f = none ? ml[k].y : fast_exp2(ml[k].x - top);
+                        sum += none ? ml[k].y : ml[k].y * f;
+                        add(acc, v[k], f);
+                    }
+            }
+            put(r, acc, sum);
+        }
+    } else {
+        const int r = row0;
+        for (int i = threadIdx.x; i < n; i += kJoinThreads) ml_s[i] = p.part_ml[slot_of(i, r)];
+        float4 v[kJoinBatch];
 #pragma unroll
-        for (int k = 0; k < kJoinBatch; ++k) {
-            const int i = i0 + k * kGroups;
-            if (i < n) {
-                const float2 t = ml_s[i];
-                const float f = t.x == -INFINITY ? t.y : fast_exp2(t.x - top);  // (nothing seen: 0, or NaN)
-                acc.x = fmaf(v[k].x, f, acc.x);
-                acc.y = fmaf(v[k].y, f, acc.y);
-                acc.z = fmaf(v[k].z, f, acc.z);
-                acc.w = fmaf(v[k].w, f, acc.w);
+        for (int k = 0; k < kJoinBatch; ++k)
+            v[k] = *reinterpret_cast<const float4*>(p.part_o + slot_of(min(group + k * kGroups, n - 1), r) * D + col);
+        __syncthreads();
+        float top = -INFINITY, sum = 0.f;
+        for (int i = lane; i < n; i += 32) top = fmaxf(top, ml_s[i].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int i = lane; i < n; i += 32) {
+            const float2 t = ml_s[i];
+            sum += t.x == -INFINITY ? t.y : t.y * fast_exp2(t.x - top);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = group; i0 < n; i0 += kJoinBatch * kGroups) {
+#pragma unroll
+            for (int k = 0; k < kJoinBatch; ++k)
+                if (i0 + k * kGroups < n) {
+                    const float2 t = ml_s[i0 + k * kGroups];
+                    add(acc, v[k], t.x == -INFINITY ? t.y : fast_exp2(t.x - top));
+                }
+            if (i0 + kJoinBatch * kGroups < n) {
+#pragma unroll
+                for (int k = 0; k < kJoinBatch; ++k)
+                    v[k] = *reinterpret_cast<const float4*>(
+                        p.part_o + slot_of(min(i0 + (kJoinBatch + k) * kGroups, n - 1), r) * D + col);
             }
         }
-        if (i0 + kJoinBatch * kGroups < n) {
+        acc_s[threadIdx.x] = acc;
+        __syncthreads();
+        if (group != 0) return;
 #pragma unroll
-            for (int k = 0; k < kJoinBatch; ++k) {
-                const int i = min(i0 + (kJoinBatch + k) * kGroups, n - 1);
-                v[k] = *reinterpret_cast<const float4*>(p.part_o + slot_of(i) * D + col);
-            }
-        }
+        for (int i = 1; i < kGroups; ++i) add(acc, acc_s[i * kAcross + threadIdx.x], 1.f);
+        put(r, acc, sum);
     }
-    acc_s[threadIdx.x] = acc;
-    __syncthreads();
-    if (group != 0) return;
-#pragma unroll
-    for (int i = 1; i < kGroups; ++i) {
-        const float4 t = acc_s[i * kAcross + threadIdx.x];
-        acc.x += t.x; acc.y += t.y; acc.z += t.z; acc.w += t.w;
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<float4*>(p.out + row * p.out_row_stride + (int64_t)head * D + col) =
-        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
 }
 
+// By rows on tcgen05, whose items have many rows and few parts.
 template <int D>
-cudaError_t launch_join_width(int row_tile, const AttnParams& p, const BatchView& b, dim3 grid, int* err,
-                              cudaStream_t stream) {
-    const dim3 block(kJoinThreads);
-    switch (row_tile) {
-        case 8: return launch_chained(attention_join_kernel<D, MmaForm<1>>, grid, block, 0, stream, 1, p, b, err);
-        case 16: return launch_chained(attention_join_kernel<D, MmaForm<2>>, grid, block, 0, stream, 1, p, b, err);
-        default: return launch_chained(attention_join_kernel<D, TcForm<D>>, grid, block, 0, stream, 1, p, b, err);
-    }
+cudaError_t launch_join_width(bool tc, const AttnParams& p, cudaStream_t stream) {
+    const unsigned rows = (unsigned)p.slot_rows, ctas = (unsigned)p.ctas;
+    if (tc)
+        return launch_chained(attention_join_kernel<D, true>, dim3(ctas, (rows + kJoinRows - 1) / kJoinRows),
+                              dim3(kJoinThreads), 0, stream, 1, p);
+    return launch_chained(attention_join_kernel<D, false>, dim3(ctas, rows), dim3(kJoinThreads), 0, stream, 1, p);
 }
-cudaError_t launch_join(int row_tile, const AttnParams& p, const BatchView& b, int q_heads, int* err,
-                        cudaStream_t stream) {
-    const dim3 grid((unsigned)p.rows, (unsigned)q_heads);
+cudaError_t launch_join(bool tc, const AttnParams& p, cudaStream_t stream) {
     switch (p.head_dim) {
-        case 64: return launch_join_width<64>(row_tile, p, b, grid, err, stream);
-        case 128: return launch_join_width<128>(row_tile, p, b, grid, err, stream);
-        case 256: return launch_join_width<256>(row_tile, p, b, grid, err, stream);
+        case 64: return launch_join_width<64>(tc, p, stream);
+        case 128: return launch_join_width<128>(tc, p, stream);
+        case 256: return launch_join_width<256>(tc, p, stream);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -169,7 +175,7 @@ int64_t tree_attention_workspace(int64_t rows, int64_t q_heads, int64_t kv_heads
                                  int num_sms) {
     // that of the largest row tile: a call's own rows choose the form
     const int64_t n = 2 * (int64_t)num_sms * slot_rows(TcForm<64>::kRows, rows, q_heads / kv_heads);
-    return (int64_t)sizeof(SplitOut) + align32(n * 8) + n * head_dim * 4;
+    return (int64_t)sizeof(CutItem) * num_sms + align32(n * 8) + n * head_dim * 4;
 }
 
 cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const CacheView& c, const BatchView& b, bool bf16,
@@ -216,9 +222,10 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     // Measured: starting and ending a part costs about 8 key tiles on tcgen05, 3 on the warp-level form.
     p.part_tiles = tc ? 8 : 3;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    p.split_out = reinterpret_cast<SplitOut*>(ws);
-    p.part_ml = reinterpret_cast<float2*>(ws + sizeof(SplitOut));
-    p.part_o = reinterpret_cast<float*>(ws + sizeof(SplitOut) + align32(2 * (int64_t)p.ctas * p.slot_rows * 8));
+    p.cuts = reinterpret_cast<CutItem*>(ws);
+    ws += sizeof(CutItem) * num_sms;
+    p.part_ml = reinterpret_cast<float2*>(ws);
+    p.part_o = reinterpret_cast<float*>(ws + align32(2 * (int64_t)p.ctas * p.slot_rows * 8));
     CUtensorMap tk, tv;
     const EncodeTiledFn enc = reinterpret_cast<EncodeTiledFn>(encode);
     // Boxes of whole pages' rows where the form's tiles can take them (one
@@ -233,7 +240,7 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     const cudaError_t e = tc ? launch_attention_tc(p, &tk, &tv, c, b, bf16, err, stream)
                              : launch_attention_mma(row_tile, p, &tk, &tv, c, b, bf16, err, stream);
     if (e != cudaSuccess || p.whole_items) return e;
-    return launch_join(row_tile, p, b, (int)a.q_heads, err, stream);
+    return launch_join(tc, p, stream);
 }
 
 }  // namespace iq4xs

@@ -18,8 +18,9 @@
 //
 // An item that is cut is joined afterwards: a CTA leaves at most two partial
 // results, slot 2 g for a part that does not begin its item, 2 g + 1 for one
-// that does.  Lengths live on the device, so the split is worked out there,
-// by every CTA from the same numbers.
+// that does, and the CTA with the item's last part says where the item's
+// others are (CutItem).  Lengths live on the device, so the split is worked
+// out there, by every CTA from the same numbers.
 #pragma once
 
 #include <cuda.h>
@@ -35,7 +36,7 @@ struct AttnParams {
     const uint16_t* q;
     float* out;
     const uint64_t* mask;
-    struct SplitOut* split_out;  // the split, for the join
+    struct CutItem* cuts;  // [G]
     float* part_o;     // [2 G slots][slot_rows][D]
     float2* part_ml;   // [2 G slots][slot_rows] {max (log2 units), sum}
     int64_t q_row_stride, out_row_stride, rows;
@@ -113,12 +114,9 @@ __device__ __forceinline__ int64_t div_small(int64_t a, int b) { return div_long
 
 // The split: `cut` as above, W places over `ctas` CTAs (no more than places,
 // so that none is empty): each W / ctas of them, the first `more` one more.
-struct SplitOut {
+struct Split {
     int64_t each, more;
     int cut, ctas;
-    int64_t pad;
-};
-struct Split : SplitOut {
     __device__ __forceinline__ int64_t start(int g) const { return each * g + min((int64_t)g, more); }
     __device__ __forceinline__ int owner(int64_t x) const {
         const int64_t in_more = more * (each + 1);
@@ -159,8 +157,14 @@ struct Split : SplitOut {
         ctas = (int)min((int64_t)p.ctas, places);
         each = ctas > 0 ? div_small(places, ctas) : 0;
         more = places - each * ctas;
-        pad = 0;
     }
+};
+
+// The cut item whose last part is CTA g's (entry g): its first part's CTA and
+// its rows.  first < 0: CTA g ends none.
+struct CutItem {
+    int first, rows, row0, head, first_row;
+    int pad[3];
 };
 
 // A CTA's walk over its range, item by item.
@@ -182,7 +186,6 @@ struct WorkWalk {
         const SeqWork mine = seq_work<F>(p, b, lane, err);
         split.plan<F>(p, b, mine, err);
         left = 0;
-        if (g == 0 && lane == 0) *p.split_out = split;
         if (g >= split.ctas) return;
         const int64_t x = split.start(g);
         left = split.start(g + 1) - x;
@@ -236,6 +239,19 @@ struct WorkWalk {
             next_end = b.row_offsets[s + 2];
             next_len = b.lens[s + 1];
         }
+    }
+    // Entry g of the cut items, before the first next().
+    __device__ __forceinline__ void tell_cut(const AttnParams& p, int g) const {
+        CutItem t = {};
+        t.first = -1;
+        if (valid() && tile0 > 0 && tile1 == w.key_tiles) {
+            t.first = split.cut == 0 ? split.owner(split.start(g) - tile0) : g - (w.unit(split.cut) - 1);
+            t.rows = min(F::kRows, w.tokens * p.group - row_tile * F::kRows);
+            t.row0 = w.row0;
+            t.head = head;
+            t.first_row = row_tile * F::kRows;
+        }
+        p.cuts[g] = t;
     }
     // The part that begins at the item's place `at` of `unit`.
     __device__ __forceinline__ void set(int at, int unit, int g) {

@@ -34,7 +34,6 @@ static_assert(kWarpKeys == 16, "a warp's keys are one k16 step of the second pro
 template <int D, int NT>
 struct MmaAttn {
     static constexpr int kRows = MmaForm<NT>::kRows;
-    static constexpr int kChunks = D / 64;
     static constexpr int kTileBytes = kKeyTile * D * 2;      // K or V of a tile
     static constexpr int kSets = NT * D <= 256 ? 2 : 1;
     static constexpr int kConsumers = kSetWarps * kSets;
@@ -239,6 +238,7 @@ __global__ void __launch_bounds__(MmaAttn<D, NT>::kThreads, 1)
     w.start(p, b, g, err);
     // A cluster shares one item, an eighth of its key tiles a CTA.
     const int rank = p.cluster > 1 ? (int)cluster_ctarank() : 0;
+    if (threadIdx.x == 0 && !p.whole_items) w.tell_cut(p, g);
     if (p.cluster > 1 && w.valid()) {
         const int tiles = w.w.key_tiles;
         w.tile0 = rank * tiles / p.cluster;

@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------ producer: items and K
             WorkWalk<TcForm<D>> w;
             w.start(p, b, g, err);
+            if (lane == 0 && !p.whole_items) w.tell_cut(p, g);
             int place0 = 0, count = 0;  // ring place at the item's start, items so far
             bool live = true;
             PageWindow pages;
