@@ -6,16 +6,18 @@
 //   y_i = x_i * w_i / sqrt(mean(x^2) + eps);  (a, b) -> (a cos - b sin, a sin + b cos)
 //
 // Every value is read once (4 bytes) and written once (2 bytes), so HBM
-// bounds it.  A warp owns several heads of one row: their loads are in flight
-// together, the row's sequence, position and rotation are looked up once, a
-// head's values stay in the warp's registers, the mean is five shuffles, and
-// a rotation partner is a shuffle (or the lane's next value) away.
+// bounds it, and the instructions a value takes come next.  D / 8 lanes own a
+// head, eight channels each (four from the head's first half, four from its
+// second), and a warp several heads of one row: their loads are in flight
+// together, the row's sequence, position and rotation are looked up once, the
+// mean is three to five shuffles for all of them, and a rotation partner is
+// the lane's own other half, its next value, or a shuffle away.
 #include "cache.cuh"
 
 namespace iq4xs {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 
 struct AppendParams {
     const float* x[3];        // q, k, v
@@ -32,47 +34,48 @@ struct AppendParams {
     int rot_half, rows, q_heads;
 };
 
-// Heads of a row that a warp takes: 2 KB of fp32 in flight (measured at 12289
-// rows of 48 heads of 128: one head a warp 142 us).
+// A warp's heads: side by side, and one after another (2 KB of fp32 in flight).
 template <int D>
-constexpr int heads_of() { return D == 64 ? 8 : D == 128 ? 4 : 2; }
+struct AppendShape {
+    static constexpr int kLanes = D / 8;          // of a head
+    static constexpr int kAbreast = 32 / kLanes;
+    static constexpr int kDeep = 2;
+    static constexpr int kHeads = kAbreast * kDeep;
+};
 
 template <int D, class T, bool kInter>
 __global__ void __launch_bounds__(kAppendThreads)
     qk_norm_rope_kernel(const AppendParams p, const CacheView c, const BatchView b, int* err) {
-    constexpr int kVec = D >= 128 ? 4 : 2;       // consecutive channels of a lane
-    constexpr int kBlocks = D / (32 * kVec);     // such runs, 32 * kVec channels apart
-    constexpr int kHeads = heads_of<D>();
+    using S = AppendShape<D>;
+    constexpr int kL = S::kLanes, kDeep = S::kDeep;
     griddep_launch_dependents();
     griddep_wait();  // the projections (and lengths, tables) may come from the preceding grid
     const Bc bc = bc_open(err);
-    const int lane = threadIdx.x & 31;
-    const int heads = p.q_heads + 2 * c.heads, groups = (heads + kHeads - 1) / kHeads;
+    const int lane = threadIdx.x & 31, l = lane % kL;
+    const int heads = p.q_heads + 2 * c.heads, groups = (heads + S::kHeads - 1) / S::kHeads;
     const int unit = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
     const int row = unit / groups;
     if (row >= p.rows) return;
-    const int h0 = (unit - row * groups) * kHeads;
+    const int h0 = (unit - row * groups) * S::kHeads;
 
-    float v[kHeads][kBlocks][kVec];
+    // The lane's channels: 4 l + e of the head's first half (block 0) and second.
+    float v[kDeep][2][4];
+    int kind[kDeep], in_kind[kDeep];
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        const int h = h0 + i;
-        const int kind = h < p.q_heads ? 0 : h < p.q_heads + c.heads ? 1 : 2;
-        const int in_kind = h - (kind == 0 ? 0 : kind == 1 ? p.q_heads : p.q_heads + c.heads);
-        const float* x = p.x[kind] + row * p.row_stride[kind] + in_kind * p.head_stride[kind];
-        const int64_t extent = 4 * ((p.rows - 1) * p.row_stride[kind] +
-                                    ((kind == 0 ? p.q_heads : c.heads) - 1) * p.head_stride[kind] + D);
+    for (int i = 0; i < kDeep; ++i) {
+        const int h = min(h0 + i * S::kAbreast + lane / kL, heads - 1);  // (the last again instead of a branch)
+        kind[i] = h < p.q_heads ? 0 : h < p.q_heads + c.heads ? 1 : 2;
+        in_kind[i] = h - (kind[i] == 0 ? 0 : kind[i] == 1 ? p.q_heads : p.q_heads + c.heads);
+        const float* base = kind[i] == 0 ? p.x[0] : kind[i] == 1 ? p.x[1] : p.x[2];
+        const int64_t rs = kind[i] == 0 ? p.row_stride[0] : kind[i] == 1 ? p.row_stride[1] : p.row_stride[2];
+        const int64_t hs = kind[i] == 0 ? p.head_stride[0] : kind[i] == 1 ? p.head_stride[1] : p.head_stride[2];
+        const float* x = base + row * rs + in_kind[i] * hs + 4 * l;
+        const int64_t extent = 4 * ((p.rows - 1) * rs + ((kind[i] == 0 ? p.q_heads : c.heads) - 1) * hs + D);
 #pragma unroll
-        for (int j = 0; j < kBlocks; ++j) {
-            const float* src = x + (j * 32 + lane) * kVec;
-            const bool ok = h < heads && bc_global(bc, src, 4 * kVec, p.x[kind], extent, kBcAppX);
-            if constexpr (kVec == 4) {
-                const float4 f = ok ? __ldcs(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                v[i][j][0] = f.x; v[i][j][1] = f.y; v[i][j][2] = f.z; v[i][j][3] = f.w;
-            } else {
-                const float2 f = ok ? __ldcs(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
-                v[i][j][0] = f.x; v[i][j][1] = f.y;
-            }
+        for (int j = 0; j < 2; ++j) {
+            const bool ok = bc_global(bc, x + j * (D / 2), 16, base, extent, kBcAppX);
+            const float4 f = ok ? __ldcs(reinterpret_cast<const float4*>(x + j * (D / 2))) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[i][j][0] = f.x; v[i][j][1] = f.y; v[i][j][2] = f.z; v[i][j][3] = f.w;
         }
     }
 
@@ -94,8 +97,8 @@ __global__ void __launch_bounds__(kAppendThreads)
     const int at = len + (row - first);
 
     // The rotation of the lane's channels: (cos, sin) of their pairs.
-    constexpr int kPairs = kInter ? kVec / 2 : kVec;
-    float2 turn[kBlocks][kPairs];
+    constexpr int kPairs = kInter ? 2 : 4;
+    float2 turn[2][kPairs];
     const int pos = p.positions != nullptr ? given : at;
     if (p.rot_half > 0 && h0 < p.q_heads + c.heads) {
         if (pos < 0 || pos >= p.rope_positions) {
@@ -104,117 +107,125 @@ __global__ void __launch_bounds__(kAppendThreads)
         }
         const float* cs = p.rope + (int64_t)pos * 2 * p.rot_half;
 #pragma unroll
-        for (int j = 0; j < kBlocks; ++j) {
-            const int i = (j * 32 + lane) * kVec;
-            const int pair = kInter ? i / 2 : i < p.rot_half ? i : i - p.rot_half;
+        for (int j = 0; j < 2; ++j) {
+            const int k = j * (D / 2) + 4 * l;
+            const float* from = cs + (kInter ? k : 2 * (k < p.rot_half ? k : k - p.rot_half));
 #pragma unroll
-            for (int e = 0; e < kPairs; ++e)
-                turn[j][e] = i < 2 * p.rot_half && bc_global(bc, cs + 2 * (pair + e), 8, p.rope,
-                                                             p.rope_positions * 8 * p.rot_half, kBcAppRope)
-                                 ? __ldg(reinterpret_cast<const float2*>(cs + 2 * (pair + e)))
-                                 : make_float2(1.f, 0.f);
+            for (int e = 0; e < kPairs; e += 2) {
+                float4 t = make_float4(1.f, 0.f, 1.f, 0.f);
+                if (k < 2 * p.rot_half &&
+                    bc_global(bc, from + 2 * e, 16, p.rope, p.rope_positions * 8 * p.rot_half, kBcAppRope))
+                    t = __ldg(reinterpret_cast<const float4*>(from + 2 * e));
+                turn[j][e] = make_float2(t.x, t.y);
+                turn[j][e + 1] = make_float2(t.z, t.w);
+            }
         }
     }
     int page = -1;
-    if (h0 + kHeads > p.q_heads) {
+    if (h0 + S::kHeads > p.q_heads) {
         page = page_of(c, b, s, at, err);
         if (page < 0 && h0 >= p.q_heads) return;
     }
 
+    // Step by step over all heads, so that their chains run side by side.
+    float sum[kDeep];
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        const int h = h0 + i;
-        if (h >= heads) break;
-        const int kind = h < p.q_heads ? 0 : h < p.q_heads + c.heads ? 1 : 2;
-        const int in_kind = h - (kind == 0 ? 0 : kind == 1 ? p.q_heads : p.q_heads + c.heads);
-        if (kind < 2) {
-            if (p.weight[kind] != nullptr) {
-                float sum = 0.f;
+    for (int i = 0; i < kDeep; ++i) {
+        sum[i] = 0.f;
 #pragma unroll
-                for (int j = 0; j < kBlocks; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) sum = fmaf(v[i][j][e], v[i][j][e], sum);
+            for (int e = 0; e < 4; ++e) sum[i] = fmaf(v[i][j][e], v[i][j][e], sum[i]);
+    }
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                const float r = 1.0f / sqrtf(sum * (1.0f / D) + p.eps);
+    for (int o = kL / 2; o > 0; o >>= 1)
 #pragma unroll
-                for (int j = 0; j < kBlocks; ++j) {
-                    const float* w = p.weight[kind] + (j * 32 + lane) * kVec;
-                    if (bc_global(bc, w, 4 * kVec, p.weight[kind], 4 * D, kBcAppW)) {
+        for (int i = 0; i < kDeep; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
 #pragma unroll
-                        for (int e = 0; e < kVec; ++e) v[i][j][e] = v[i][j][e] * r * __ldg(w + e);
+    for (int i = 0; i < kDeep; ++i) {
+        const float* weight = kind[i] == 0 ? p.weight[0] : kind[i] == 1 ? p.weight[1] : nullptr;
+        if (weight == nullptr) continue;  // (v, or no norm)
+        const float r = rsqrtf(sum[i] * (1.0f / D) + p.eps);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float* w = weight + j * (D / 2) + 4 * l;
+            if (!bc_global(bc, w, 16, weight, 4 * D, kBcAppW)) continue;
+            const float4 t = __ldg(reinterpret_cast<const float4*>(w));
+            v[i][j][0] *= r * t.x;
+            v[i][j][1] *= r * t.y;
+            v[i][j][2] *= r * t.z;
+            v[i][j][3] *= r * t.w;
+        }
+    }
+    if (p.rot_half > 0) {
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) {
+            const bool turns = kind[i] < 2;
+            if constexpr (kInter) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e) {
+                        const bool here = turns && j * (D / 2) + 4 * l < 2 * p.rot_half;
+                        const float a0 = v[i][j][2 * e], a1 = v[i][j][2 * e + 1];
+                        v[i][j][2 * e] = here ? a0 * turn[j][e].x - a1 * turn[j][e].y : a0;
+                        v[i][j][2 * e + 1] = here ? a0 * turn[j][e].y + a1 * turn[j][e].x : a1;
                     }
-                }
-            }
-            if (p.rot_half > 0) {
-                if constexpr (kInter) {
+            } else {
+                // The partner of channel k is k + half (k < half) or k - half;
+                // half is a multiple of 4, so a lane's four have theirs in one
+                // lane's four: its own other ones where all channels turn.
+                // Channels behind the rotated ones stay as they are.
+                float q[2][4];
+                if (p.rot_half == D / 2) {
 #pragma unroll
-                    for (int j = 0; j < kBlocks; ++j)
-#pragma unroll
-                        for (int e = 0; e < kPairs; ++e) {
-                            const float a0 = v[i][j][2 * e], a1 = v[i][j][2 * e + 1];
-                            v[i][j][2 * e] = a0 * turn[j][e].x - a1 * turn[j][e].y;
-                            v[i][j][2 * e + 1] = a0 * turn[j][e].y + a1 * turn[j][e].x;
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        q[0][e] = v[i][1][e];
+                        q[1][e] = v[i][0][e];
+                    }
                 } else {
-                    // The partner of channel k is k + half (k < half) or k - half:
-                    // rot_half is a multiple of kVec, so a lane's run has its
-                    // partners in one lane's run.  (Channels behind the rotated
-                    // ones meet cos 1, sin 0 and some finite or infinite partner:
-                    // they are left out.)
-                    float q[kBlocks][kVec];
 #pragma unroll
-                    for (int j = 0; j < kBlocks; ++j) {
-                        const int k = (j * 32 + lane) * kVec;
+                    for (int j = 0; j < 2; ++j) {
+                        const int k = j * (D / 2) + 4 * l;
                         const int from = (k < p.rot_half ? k + p.rot_half : k - p.rot_half) & (D - 1);
-                        const int src_lane = (from / kVec) & 31, src_block = from / (32 * kVec);
+                        const int src = lane / kL * kL + from / 4 % kL;
 #pragma unroll
-                        for (int e = 0; e < kVec; ++e) {
-                            float got = __shfl_sync(0xffffffffu, v[i][0][e], src_lane);
-                            if constexpr (kBlocks == 2) {
-                                const float other = __shfl_sync(0xffffffffu, v[i][1][e], src_lane);
-                                got = src_block ? other : got;
-                            }
-                            q[j][e] = got;
+                        for (int e = 0; e < 4; ++e) {
+                            const float a0 = __shfl_sync(0xffffffffu, v[i][0][e], src);
+                            const float a1 = __shfl_sync(0xffffffffu, v[i][1][e], src);
+                            q[j][e] = from >= D / 2 ? a1 : a0;
                         }
                     }
+                }
 #pragma unroll
-                    for (int j = 0; j < kBlocks; ++j) {
-                        const int k = (j * 32 + lane) * kVec;
-                        if (k < 2 * p.rot_half) {
+                for (int j = 0; j < 2; ++j) {
+                    const int k = j * (D / 2) + 4 * l;
+                    const bool first_half = k < p.rot_half, here = turns && k < 2 * p.rot_half;
 #pragma unroll
-                            for (int e = 0; e < kVec; ++e) {
-                                const float2 t = turn[j][e];
-                                v[i][j][e] = k < p.rot_half ? v[i][j][e] * t.x - q[j][e] * t.y
-                                                            : q[j][e] * t.y + v[i][j][e] * t.x;
-                            }
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 t = turn[j][e];
+                        const float x = v[i][j][e] * t.x + (first_half ? -q[j][e] : q[j][e]) * t.y;
+                        v[i][j][e] = here ? x : v[i][j][e];
                     }
                 }
             }
         }
-        uint16_t *dst, *base;
-        int64_t extent;
-        if (kind == 0) {
-            base = p.q_out;
-            dst = base + row * p.q_out_row_stride + (int64_t)in_kind * D;
-            extent = 2 * ((p.rows - 1) * p.q_out_row_stride + (int64_t)p.q_heads * D);
-        } else {
-            if (page < 0) continue;
-            base = kind == 1 ? c.k : c.v;
-            dst = base + p.layer_offset + page * c.page_stride + in_kind * c.head_stride +
-                  (at & (c.page_size - 1)) * c.slot_stride;
-            extent = c.extent;
-        }
+    }
 #pragma unroll
-        for (int j = 0; j < kBlocks; ++j) {
-            uint16_t* to = dst + (j * 32 + lane) * kVec;
-            if (!bc_global(bc, to, 2 * kVec, base, extent, kind == 0 ? kBcAppQ : kBcAppKv)) continue;
-            if constexpr (kVec == 4)
+    for (int i = 0; i < kDeep; ++i) {
+        uint16_t* base = kind[i] == 0 ? p.q_out : kind[i] == 1 ? c.k : c.v;
+        const int64_t offset = kind[i] == 0 ? row * p.q_out_row_stride + in_kind[i] * D
+                                            : p.layer_offset + page * c.page_stride + in_kind[i] * c.head_stride +
+                                                  (at & (c.page_size - 1)) * c.slot_stride;
+        const int64_t extent =
+            kind[i] == 0 ? 2 * ((p.rows - 1) * p.q_out_row_stride + (int64_t)p.q_heads * D) : c.extent;
+        if (h0 + i * S::kAbreast + lane / kL >= heads || (kind[i] > 0 && page < 0)) continue;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint16_t* to = base + offset + j * (D / 2) + 4 * l;
+            if (bc_global(bc, to, 8, base, extent, kind[i] == 0 ? kBcAppQ : kBcAppKv))
                 *reinterpret_cast<uint2*>(to) =
                     make_uint2(T::pack(v[i][j][0], v[i][j][1]), T::pack(v[i][j][2], v[i][j][3]));
-            else
-                *reinterpret_cast<uint32_t*>(to) = T::pack(v[i][j][0], v[i][j][1]);
         }
     }
 }
@@ -223,7 +234,7 @@ template <int D, class T>
 cudaError_t launch_width(const AppendParams& p, const CacheView& c, const BatchView& b, bool inter, int* err,
                          cudaStream_t stream) {
     const int heads = p.q_heads + 2 * c.heads;
-    const int64_t units = (int64_t)p.rows * ((heads + heads_of<D>() - 1) / heads_of<D>());
+    const int64_t units = (int64_t)p.rows * ((heads + AppendShape<D>::kHeads - 1) / AppendShape<D>::kHeads);
     const dim3 grid((unsigned)((units + kAppendThreads / 32 - 1) / (kAppendThreads / 32)));
     return inter ? launch_chained(qk_norm_rope_kernel<D, T, true>, grid, dim3(kAppendThreads), 0, stream, 1, p, c, b, err)
                  : launch_chained(qk_norm_rope_kernel<D, T, false>, grid, dim3(kAppendThreads), 0, stream, 1, p, c, b, err);

@@ -71,19 +71,34 @@ __device__ int count_free(const Bc& bc, const int32_t* refs, int pages, int want
     return found;
 }
 
-// give(rank, page) for the free pages of rank 0..wanted-1 in rising order,
-// each by one thread; a page is taken (refs 1) by whoever it is given to.
-template <class Give>
-__device__ void hand_out(const Bc& bc, int32_t* refs, int pages, int wanted, Give give) {
-    int rank0 = 0;
-    for (int64_t c0 = 0; c0 < pages && rank0 < wanted; c0 += kBookThreads * kPagesPerThread) {
+// give(rank, page) for the free pages of rank 0..fit-1 in rising order, each
+// by one thread, where fit = wanted if that many are free, else what
+// fit_of(free pages) says.  Returns fit.
+template <class Fit, class Give>
+__device__ int hand_out(const Bc& bc, const int32_t* refs, int pages, int wanted, Fit fit_of, Give give) {
+    // Mostly the first pages looked at hold enough: then they need no second look.
+    uint32_t bits = free_bits(bc, refs, (int64_t)threadIdx.x * kPagesPerThread, pages);
+    int total;
+    int rank = block_scan(__popc(bits), &total);
+    const auto give_all = [&](int64_t first, int fit) {
+        for (; bits && rank < fit; bits &= bits - 1, ++rank) give(rank, (int)(first + __ffs(bits) - 1));
+    };
+    int fit = wanted;
+    if (total < wanted) {
+        const int nfree = count_free(bc, refs, pages, wanted);
+        if (nfree < wanted) fit = fit_of(nfree);
+        __syncthreads();  // every count is done before a page changes hands
+    }
+    give_all((int64_t)threadIdx.x * kPagesPerThread, fit);
+    int rank0 = total;
+    for (int64_t c0 = kBookThreads * kPagesPerThread; c0 < pages && rank0 < fit; c0 += kBookThreads * kPagesPerThread) {
         const int64_t first = c0 + (int64_t)threadIdx.x * kPagesPerThread;
-        uint32_t bits = free_bits(bc, refs, first, pages);
-        int total;
-        int rank = rank0 + block_scan(__popc(bits), &total);
-        for (; bits && rank < wanted; bits &= bits - 1, ++rank) give(rank, (int)(first + __ffs(bits) - 1));
+        bits = free_bits(bc, refs, first, pages);
+        rank = rank0 + block_scan(__popc(bits), &total);
+        give_all(first, fit);
         rank0 += total;
     }
+    return fit;
 }
 
 // First i with upto[i] > rank (upto does not fall; upto[n - 1] > rank).
@@ -119,7 +134,10 @@ __global__ void __launch_bounds__(kBookThreads)
     griddep_launch_dependents();
     griddep_wait();
     const Bc bc = bc_open(err);
-    // status holds the running sum of the requests until the end
+    // The running sum of the requests: in shared memory, or where there are
+    // more sequences than it holds in status, until the end.
+    __shared__ int32_t upto_s[kBookThreads];
+    int32_t* const upto = b.sequences <= kBookThreads ? upto_s : status;
     int wanted = 0;
     for (int s0 = 0; s0 < b.sequences; s0 += kBookThreads) {
         const int s = s0 + threadIdx.x;
@@ -128,37 +146,33 @@ __global__ void __launch_bounds__(kBookThreads)
         int total;
         const int before = block_scan(lack, &total);
         // (sums past the number of pages are all alike: nothing fits there)
-        if (s < b.sequences) status[s] = (int)min((int64_t)INT32_MAX, (int64_t)wanted + before + lack);
+        if (s < b.sequences) upto[s] = (int)min((int64_t)INT32_MAX, (int64_t)wanted + before + lack);
         wanted = (int)min((int64_t)INT32_MAX, (int64_t)wanted + total);
     }
     __syncthreads();
     int fit = wanted;  // pages handed out: those of the sequences before the first that does not fit
     if (wanted > 0) {
-        const int nfree = count_free(bc, refs, pages, wanted);
-        if (nfree < wanted) {
-            const int i = find_taker(status, b.sequences, nfree);
-            fit = i > 0 ? status[i - 1] : 0;
-        }
-        __syncthreads();
-        hand_out(bc, refs, pages, fit, [&](int rank, int page) {
-            const int s = find_taker(status, b.sequences, rank);
-            const int at = b.held[s] + rank - (s > 0 ? status[s - 1] : 0);
-            int32_t* to = b.page_table + s * b.table_stride + at;
-            if (bc_range(bc, at, 1, b.table_width, kBcPagesTable)) *to = page;
-            refs[page] = 1;
-        });
+        fit = hand_out(
+            bc, refs, pages, wanted,
+            [&](int nfree) {
+                const int i = find_taker(upto, b.sequences, nfree);
+                return i > 0 ? upto[i - 1] : 0;
+            },
+            [&](int rank, int page) {
+                const int s = find_taker(upto, b.sequences, rank);
+                const int at = b.held[s] + rank - (s > 0 ? upto[s - 1] : 0);
+                int32_t* to = b.page_table + s * b.table_stride + at;
+                if (bc_range(bc, at, 1, b.table_width, kBcPagesTable)) *to = page;
+                refs[page] = 1;
+            });
         __syncthreads();
     }
     for (int s0 = 0; s0 < b.sequences; s0 += kBookThreads) {
         const int s = s0 + threadIdx.x;
-        int lack = 0, held = 0, upto = 0;
         if (s < b.sequences) {
-            lack = pages_lacking(b, s, shift, &held, err);
-            upto = status[s];
-        }
-        __syncthreads();
-        if (s < b.sequences) {
-            const bool ok = lack == 0 || (lack > 0 && upto <= fit);
+            int held;
+            const int lack = pages_lacking(b, s, shift, &held, err);
+            const bool ok = lack == 0 || (lack > 0 && upto[s] <= fit);
             if (ok && lack > 0) b.held[s] = held + lack;
             status[s] = ok ? 0 : 1;
         }
@@ -170,7 +184,7 @@ __global__ void __launch_bounds__(kBookThreads)
 // of its sequence in order, up to kMoveBatch loads in flight before their
 // stores.  Paths rise strictly, so path[i] >= i and a store to place i never
 // overtakes a load that is still to come (those read places >= i + 1).
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 512;
 constexpr int kMoveBatch = 8;
 constexpr int kMoveRows = 64;  // rows of the path looked up at a time
 
@@ -286,29 +300,32 @@ __global__ void __launch_bounds__(kBookThreads)
     griddep_launch_dependents();
     griddep_wait();
     const Bc bc = bc_open(err);
-    int wanted = 0;  // status holds the running sum of the requests until the end
+    // the running sum of the requests, as in reserve_kernel
+    __shared__ int32_t upto_s[kBookThreads];
+    int32_t* const upto_all = count <= kBookThreads ? upto_s : status;
+    int wanted = 0;
     for (int i0 = 0; i0 < count; i0 += kBookThreads) {
         const int i = i0 + threadIdx.x;
         int full, take = 0;
         if (i < count) fork_state(b, parents[i], children[i], shift, &full, &take);
         int total;
         const int before = block_scan(take, &total);
-        if (i < count) status[i] = wanted + before + take;
+        if (i < count) upto_all[i] = wanted + before + take;
         wanted += total;
     }
     __syncthreads();
     int fit = wanted;
     if (wanted > 0) {
-        fit = min(wanted, count_free(bc, refs, pages, wanted));
-        __syncthreads();
-        hand_out(bc, refs, pages, fit, [&](int rank, int page) {
-            const int i = find_taker(status, count, rank);
-            int full, take;
-            fork_state(b, parents[i], children[i], shift, &full, &take);
-            if (bc_range(bc, full, 1, b.table_width, kBcPagesTable))
-                b.page_table[children[i] * b.table_stride + full] = page;
-            refs[page] = 1;
-        });
+        fit = hand_out(
+            bc, refs, pages, wanted, [](int nfree) { return nfree; },
+            [&](int rank, int page) {
+                const int i = find_taker(upto_all, count, rank);
+                int full, take;
+                fork_state(b, parents[i], children[i], shift, &full, &take);
+                if (bc_range(bc, full, 1, b.table_width, kBcPagesTable))
+                    b.page_table[children[i] * b.table_stride + full] = page;
+                refs[page] = 1;
+            });
         __syncthreads();
     }
     // A warp per child: the shared pages' entries and references.
@@ -317,7 +334,7 @@ __global__ void __launch_bounds__(kBookThreads)
         const int i = i0 + (threadIdx.x >> 5);
         int full = 0, take = 0, bad = 0, upto = 0;
         if (i < count) {
-            upto = status[i];
+            upto = upto_all[i];
             bad = fork_state(b, parents[i], children[i], shift, &full, &take);
             if (!bad && take && upto > fit) bad = 1;
             if (!bad) {
@@ -403,7 +420,9 @@ __global__ void __launch_bounds__(kCopyThreads)
     if (a != z) copy_slots(bc, c, blockIdx.x, a, z, c.page_size);
 }
 
-__global__ void __launch_bounds__(kMoveThreads)
+constexpr int kReleaseThreads = 256;
+
+__global__ void __launch_bounds__(kReleaseThreads)
     release_kernel(const BatchView b, int32_t* refs, int pages, const int32_t* __restrict__ rows, int* err) {
     __shared__ int held_s;
     griddep_launch_dependents();
@@ -426,7 +445,7 @@ __global__ void __launch_bounds__(kMoveThreads)
         data_error(err, kDataHeld);
         held = 0;
     }
-    for (int j = threadIdx.x; j < held; j += kMoveThreads) {
+    for (int j = threadIdx.x; j < held; j += kReleaseThreads) {
         const int page = b.page_table[s * b.table_stride + j];
         if (page < 0 || page >= pages) data_error(err, kDataPage);
         else if (bc_global(bc, refs + page, 4, refs, 4 * (int64_t)pages, kBcPagesRefs)) atomicSub(refs + page, 1);
@@ -471,7 +490,7 @@ cudaError_t launch_cache_copy_pages(const CacheView& c, const int32_t* src, cons
 
 cudaError_t launch_cache_release(const BatchView& b, int32_t* refs, int pages, const int32_t* rows, int count,
                                  int* err, cudaStream_t stream) {
-    return launch_chained(release_kernel, dim3((unsigned)count), dim3(kMoveThreads), 0, stream, 1, b, refs, pages, rows,
+    return launch_chained(release_kernel, dim3((unsigned)count), dim3(kReleaseThreads), 0, stream, 1, b, refs, pages, rows,
                           err);
 }
 
