@@ -46,7 +46,7 @@ constexpr int kJoinThreads = 256, kJoinBatch = 8, kJoinRows = 8;
 constexpr int kMaxParts = 256;
 
 template <int D, bool kByRows>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p, int* err) {
     constexpr int kAcross = D / 4, kGroups = kJoinThreads / kAcross;
     __shared__ float4 acc_s[kByRows ? 1 : kJoinThreads];
     __shared__ float2 ml_s[kByRows ? 1 : kMaxParts];
@@ -57,7 +57,16 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     if (cut.first < 0 || row0 >= cut.rows) return;
     const int n = (int)blockIdx.x - cut.first + 1;  // (at most the CTAs, which kMaxParts holds)
     const int lane = threadIdx.x & 31, group = threadIdx.x / kAcross, col = threadIdx.x % kAcross * 4;
-    const auto slot_of = [&](int i, int r) { return (int64_t)(2 * (cut.first + i) + (i == 0)) * p.slot_rows + r; };
+    const Bc bc = bc_open(err);
+    const auto slot_of = [&](int i) { return 2 * (cut.first + i) + (i == 0); };
+    const auto sum_of = [&](int i, int r) {
+        const float2* at = part_sum(p, slot_of(i), r, bc);
+        return at != nullptr ? *at : make_float2(-INFINITY, 0.f);
+    };
+    const auto part_of = [&](int i, int r) {
+        const float* at = part_row(p, slot_of(i), r, col, 4, bc);
+        return at != nullptr ? *reinterpret_cast<const float4*>(at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
     const auto add = [](float4& a, float4 v, float f) {
         a.x = fmaf(v.x, f, a.x);
         a.y = fmaf(v.y, f, a.y);
@@ -67,9 +76,10 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     const auto put = [&](int r, float4 a, float sum) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: zeros
         const int row = cut.first_row + r, t = token_of(p, row);
-        *reinterpret_cast<float4*>(p.out + (cut.row0 + t) * p.out_row_stride +
-                                   ((int64_t)cut.head * p.group + row - t * p.group) * D + col) =
-            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+        float* dst = p.out + (cut.row0 + t) * p.out_row_stride + ((int64_t)cut.head * p.group + row - t * p.group) * D + col;
+        if (bc_global(bc, dst, 16, p.out, 4 * ((p.rows - 1) * p.out_row_stride + (int64_t)p.group * p.kv_heads * D),
+                      kBcAttnOut))
+            *reinterpret_cast<float4*>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     };
     if constexpr (kByRows) {
         for (int r = row0 + group; r < min(row0 + kJoinRows, cut.rows); r += kGroups) {
@@ -80,9 +90,8 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
                 float4 v[kJoinBatch];
 #pragma unroll
                 for (int k = 0; k < kJoinBatch; ++k) {  // (the last part again instead of a branch)
-                    const int64_t at = slot_of(min(i0 + k, n - 1), r);
-                    ml[k] = p.part_ml[at];
-                    v[k] = *reinterpret_cast<const float4*>(p.part_o + at * D + col);
+                    ml[k] = sum_of(min(i0 + k, n - 1), r);
+                    v[k] = part_of(min(i0 + k, n - 1), r);
                 }
                 float most = top;
 #pragma unroll
@@ -106,11 +115,11 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
         }
     } else {
         const int r = row0;
-        for (int i = threadIdx.x; i < n; i += kJoinThreads) ml_s[i] = p.part_ml[slot_of(i, r)];
+        for (int i = threadIdx.x; i < n; i += kJoinThreads) ml_s[i] = sum_of(i, r);
         float4 v[kJoinBatch];
 #pragma unroll
         for (int k = 0; k < kJoinBatch; ++k)
-            v[k] = *reinterpret_cast<const float4*>(p.part_o + slot_of(min(group + k * kGroups, n - 1), r) * D + col);
+            v[k] = part_of(min(group + k * kGroups, n - 1), r);
         __syncthreads();
         float top = -INFINITY, sum = 0.f;
         for (int i = lane; i < n; i += 32) top = fmaxf(top, ml_s[i].x);
@@ -133,8 +142,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
             if (i0 + kJoinBatch * kGroups < n) {
 #pragma unroll
                 for (int k = 0; k < kJoinBatch; ++k)
-                    v[k] = *reinterpret_cast<const float4*>(
-                        p.part_o + slot_of(min(i0 + (kJoinBatch + k) * kGroups, n - 1), r) * D + col);
+                    v[k] = part_of(min(i0 + (kJoinBatch + k) * kGroups, n - 1), r);
             }
         }
         acc_s[threadIdx.x] = acc;
@@ -148,18 +156,18 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
 
 // By rows on tcgen05, whose items have many rows and few parts.
 template <int D>
-cudaError_t launch_join_width(bool tc, const AttnParams& p, cudaStream_t stream) {
+cudaError_t launch_join_width(bool tc, const AttnParams& p, int* err, cudaStream_t stream) {
     const unsigned rows = (unsigned)p.slot_rows, ctas = (unsigned)p.ctas;
     if (tc)
         return launch_chained(attention_join_kernel<D, true>, dim3(ctas, (rows + kJoinRows - 1) / kJoinRows),
-                              dim3(kJoinThreads), 0, stream, 1, p);
-    return launch_chained(attention_join_kernel<D, false>, dim3(ctas, rows), dim3(kJoinThreads), 0, stream, 1, p);
+                              dim3(kJoinThreads), 0, stream, 1, p, err);
+    return launch_chained(attention_join_kernel<D, false>, dim3(ctas, rows), dim3(kJoinThreads), 0, stream, 1, p, err);
 }
-cudaError_t launch_join(bool tc, const AttnParams& p, cudaStream_t stream) {
+cudaError_t launch_join(bool tc, const AttnParams& p, int* err, cudaStream_t stream) {
     switch (p.head_dim) {
-        case 64: return launch_join_width<64>(tc, p, stream);
-        case 128: return launch_join_width<128>(tc, p, stream);
-        case 256: return launch_join_width<256>(tc, p, stream);
+        case 64: return launch_join_width<64>(tc, p, err, stream);
+        case 128: return launch_join_width<128>(tc, p, err, stream);
+        case 256: return launch_join_width<256>(tc, p, err, stream);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -240,7 +248,7 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     const cudaError_t e = tc ? launch_attention_tc(p, &tk, &tv, c, b, bf16, err, stream)
                              : launch_attention_mma(row_tile, p, &tk, &tv, c, b, bf16, err, stream);
     if (e != cudaSuccess || p.whole_items) return e;
-    return launch_join(tc, p, stream);
+    return launch_join(tc, p, err, stream);
 }
 
 }  // namespace iq4xs

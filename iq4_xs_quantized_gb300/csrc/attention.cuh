@@ -297,10 +297,24 @@ struct WorkWalk {
 };
 
 // Whether token t (row `row` of the batch) sees its sequence's new token j >= 0.
-__device__ __forceinline__ bool sees_new(const AttnParams& p, int row, int t, int j) {
+__device__ __forceinline__ bool sees_new(const AttnParams& p, int row, int t, int j, const Bc& bc) {
     if (p.mask == nullptr) return j <= t;
     const int word = j >> 6;
-    return word < p.mask_words && (p.mask[(int64_t)row * p.mask_words + word] >> (j & 63) & 1) != 0;
+    const uint64_t* m = p.mask + (int64_t)row * p.mask_words + word;
+    return word < p.mask_words && bc_global(bc, m, 8, p.mask, 8 * p.rows * p.mask_words, kBcAttnMask) &&
+           (*m >> (j & 63) & 1) != 0;
+}
+
+// Row r of a cut item's slot in the workspace: its {max, sum} and, at a
+// channel, its unjoined outputs; nullptr if the bounds-checked build finds
+// them outside (n channels).
+__device__ __forceinline__ float2* part_sum(const AttnParams& p, int64_t slot, int r, const Bc& bc) {
+    float2* at = p.part_ml + slot * p.slot_rows + r;
+    return bc_global(bc, at, 8, p.part_ml, 16 * (int64_t)p.ctas * p.slot_rows, kBcAttnWork) ? at : nullptr;
+}
+__device__ __forceinline__ float* part_row(const AttnParams& p, int64_t slot, int r, int channel, int n, const Bc& bc) {
+    float* at = p.part_o + (slot * p.slot_rows + r) * p.head_dim + channel;
+    return bc_global(bc, at, 4 * n, p.part_o, 8 * (int64_t)p.ctas * p.slot_rows * p.head_dim, kBcAttnWork) ? at : nullptr;
 }
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
@@ -309,10 +323,14 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xfffffff
 struct RowSight {
     uint64_t word;
     int row, token;
-    __device__ __forceinline__ void open(const AttnParams& p, int row0, int t) {
+    __device__ __forceinline__ void open(const AttnParams& p, int row0, int t, const Bc& bc) {
         row = row0 + t;
         token = t;
-        word = p.mask != nullptr ? p.mask[(int64_t)row * p.mask_words] : 0;
+        word = 0;
+        if (p.mask == nullptr) return;
+        const uint64_t* m = p.mask + (int64_t)row * p.mask_words;
+        if (!bc_global(bc, m, 8 * (int64_t)p.mask_words, p.mask, 8 * p.rows * p.mask_words, kBcAttnMask)) row = 0;
+        else word = *m;
     }
     // Bit k: the row sees the position k behind one whose place among the new
     // tokens is j0 (negative: context); `have` positions lie before the end.

@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(MmaAttn<D, NT>::kThreads, 1)
                         for (int i = 0; i < 4; ++i) {
                             const int key = rg + (i >> 1) * 8, j = key0 + key - w.w.len, t = tok[n][i & 1];
                             const bool inside = key < have;
-                            const bool see = inside && (j < 0 || sees_new(p, w.w.row0 + t, t, j));
+                            const bool see = inside && (j < 0 || sees_new(p, w.w.row0 + t, t, j, bc));
                             hidden |= inside && !see;
                             if (!see) x[n][i] = -INFINITY;
                         }
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(MmaAttn<D, NT>::kThreads, 1)
                 if (warp == 0 && rg == 0) {
                     ml[kConsumers * kRows + row] = make_float2(top, sum);
                     if (!w.whole && p.cluster == 1 && row < rows)
-                        p.part_ml[(int64_t)w.slot * p.slot_rows + row] = make_float2(top, sum);
+                        if (float2* to = part_sum(p, w.slot, row, bc)) *to = make_float2(top, sum);
                 }
             }
         const bool last = w.last();
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(MmaAttn<D, NT>::kThreads, 1)
                 } else if (w.whole) {
                     put_row(p, c, w, r, c0 + col, v, ml[kConsumers * kRows + r].y, bc);
                 } else {
-                    *reinterpret_cast<float4*>(p.part_o + ((int64_t)w.slot * p.slot_rows + r) * D + c0 + col) = v;
+                    if (float* to = part_row(p, w.slot, r, c0 + col, 4, bc)) *reinterpret_cast<float4*>(to) = v;
                 }
             }
         };

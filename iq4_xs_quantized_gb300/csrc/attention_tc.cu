@@ -267,15 +267,17 @@ __device__ __noinline__ bool scrub_tile(uint32_t tile, int first, int have, int 
 template <int D, class T>
 __device__ __noinline__ void add_odd(const AttnParams& p, const CacheView& c, const BatchView& b, const Item& d,
                                      int row, int token, float* out, int channel, int n, int* err) {
+    const Bc bc = bc_open(err);
     for (int t = 0; t < d.tokens; ++t) {
         const int pos = d.len + t;
         if (pos < d.tile0 * TcForm<D>::kKeys || pos >= d.tile1 * TcForm<D>::kKeys ||
-            !sees_new(p, row, token, t))
+            !sees_new(p, row, token, t, bc))
             continue;
         const int page = page_of(c, b, d.seq, pos, err);
         if (page < 0) continue;
         const uint16_t* src = c.v + p.layer_offset + page * c.page_stride + d.head * c.head_stride +
                               (pos & (c.page_size - 1)) * c.slot_stride + channel;
+        if (!bc_global(bc, src, 2 * n, c.v, c.extent, kBcAttnKv)) continue;
         for (int i = 0; i < n; ++i) {
             const float2 v = T::unpack(src[i]);
             if (!isfinite(v.x)) out[i] += v.x;
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Q of the item's rows: each thread its row's half of the
                 // channels.  Rows behind the last are zero.
                 const int row = d.first + min(r, rows - 1), tok = token_of(p, row);
-                sight.open(p, d.row0, tok);
+                sight.open(p, d.row0, tok, bc);
                 // Warps take rows, lanes neighbouring 16 bytes of them (256 /
                 // D * 2 rows at a time).  Rows behind the last keep what is
                 // there: a row's products reach its own lane only.
@@ -727,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const bool whole = d.slot < 0;
             if (!whole && half == 0 && copy == 0 && r < rows)
-                p.part_ml[(int64_t)d.slot * p.slot_rows + r] = make_float2(top, sum);
+                if (float2* to = part_sum(p, d.slot, r, bc)) *to = make_float2(top, sum);
             if (copies > 1) {
                 // The other copies hand their outputs to the first, kStageCols
                 // channels at a time through shared memory.
@@ -769,8 +771,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int row = d.first + r, tok = sight.token;
                 float* const dst = (whole ? p.out + (d.row0 + tok) * p.out_row_stride +
                                                 ((int64_t)d.head * p.group + row - tok * p.group) * D
-                                          : p.part_o + ((int64_t)d.slot * p.slot_rows + r) * D) + half * C::kHalfD;
-                if (!whole || bc_global(bc, dst, 4 * C::kHalfD, p.out,
+                                          : part_row(p, d.slot, r, 0, D, bc)) + half * C::kHalfD;
+                if (!whole ? part_row(p, d.slot, r, 0, D, bc) != nullptr : bc_global(bc, dst, 4 * C::kHalfD, p.out,
                                         4 * ((p.rows - 1) * p.out_row_stride + (int64_t)p.group * p.kv_heads * D),
                                         kBcAttnOut)) {
                     if (!whole || p.wide_out) {

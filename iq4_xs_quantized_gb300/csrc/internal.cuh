@@ -249,7 +249,7 @@ enum BoundsSite : int {
     kBcTcSmem, kBcTcRecv, kBcTcRows,
     kBcAppX = 0x60, kBcAppW, kBcAppRope, kBcAppQ, kBcAppKv,
     kBcPagesKv = 0x70, kBcPagesTable, kBcPagesRefs,
-    kBcAttnQ = 0x80, kBcAttnOut, kBcAttnMask, kBcAttnWork, kBcAttnKv, kBcAttnSmem,
+    kBcAttnQ = 0x80, kBcAttnOut, kBcAttnMask, kBcAttnWork, kBcAttnKv,
 };
 #ifdef IQ4XS_BOUNDS_CHECK
 constexpr bool kBoundsCheck = true;
