@@ -394,7 +394,7 @@ __device__ void copy_slots(const Bc& bc, const CacheView& c, int64_t seg, int sr
 
 __global__ void __launch_bounds__(kCopyThreads)
     fork_copy_kernel(const CacheView c, const BatchView b, const int32_t* __restrict__ parents,
-                     const int32_t* __restrict__ children, const int32_t* __restrict__ status, int* err) {
+                     const int32_t* __restrict__ children, const int32_t* status, int* err) {
     griddep_launch_dependents();
     griddep_wait();
     const Bc bc = bc_open(err);

@@ -35,14 +35,15 @@ __global__ void __launch_bounds__(kQuantThreads)
     // launched when each had started).  The matmul's CTAs take SMs as the
     // preceding grid's leave and stream their weights meanwhile.  x may come
     // from the preceding grid, and qs/ds/the operand may still be read by it:
-    // wait for it before reading or writing anything.  x is not even
-    // prefetched before: the L2 of the die that asks keeps what it got, and
-    // the loads below then miss what the preceding grid wrote on the other
-    // die (seen behind a grid that lets this one launch before its stores).
+    // wait for it before reading or writing anything.  Its lines are only
+    // requested into L2 before the wait, and the loads behind it are coherent
+    // ones: loads of the read-only kind found what the request had brought,
+    // not what the preceding grid wrote after it.
     griddep_launch_dependents();
     const int64_t m = blockIdx.y;
     const int64_t e0 = (int64_t)blockIdx.x * kElemsPerCta + threadIdx.x * kElemsPerThread;
     const bool live = e0 < K;  // whole warps (see above)
+    if (live && m < M) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + m * ldx + e0));
     griddep_wait();
     const int lane = threadIdx.x & 31;
     const int l8 = lane & 7;  // position of this thread inside its Q8_1 block
@@ -51,7 +52,10 @@ __global__ void __launch_bounds__(kQuantThreads)
 
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live && m < M && bc_global(bc, x + m * ldx + e0, 16, x, ((M - 1) * ldx + K) * 4, kBcQuantX))
-        v = __ldg(reinterpret_cast<const float4*>(x + m * ldx + e0));
+        asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "l"(x + m * ldx + e0)
+                     : "memory");
 
     float amax = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));

@@ -66,7 +66,7 @@ class Decoder:
         self.batch = B.KVBatch(self.offsets, self.lens, self.held, self.table)
         self.rope = rope_table(width * page_size, head_dim)
         rng = np.random.default_rng(seed)
-        scale = 1.0 / math.sqrt(hidden) / 600  # the blocks' weights have a spread of about 600 d
+        scale = 1.0 / math.sqrt(hidden) / 600  # the blocks' weights spread by about 1300 scale: 2 / sqrt(hidden)
         matrix = lambda n, k: torch.from_numpy(synth.iq4xs_weights(rng, n, k, scale)).cuda()  # noqa: E731
         self.w_qkv = [matrix(self.n_qkv, hidden) for _ in range(layers)]
         self.w_o = [matrix(hidden, q_heads * head_dim) for _ in range(layers)]

@@ -63,3 +63,64 @@ def test_quantizer_behind_matmul(M, path):
     B.iq4xs_quantize_q8_1(x, qs, ds)
     torch.cuda.synchronize()
     _follows(lambda out: B.iq4xs_matmul(w, N, K, qs, ds, M, out, path), M, N)
+
+
+@pytest.mark.parametrize("M", (1, 2, 4, 8, 16, 32, 64, 96, 200))
+def test_projections_that_share_a_workspace(M):
+    """A run of projections on one workspace, each quantizing where the one
+    before it still reads, against the same projections one at a time."""
+    N, K = 4096, 2048
+    rng = np.random.default_rng(M)
+    w = [torch.from_numpy(synth.iq4xs_weights(rng, N, K, 1e-3)).cuda() for _ in range(2)]
+    x = [torch.randn(M, K, device="cuda") * 10.0 ** (i - 4) for i in range(8)]
+    for nbytes in {B.iq4xs_linear_workspace_bytes(M, N, K), B.iq4xs_linear_workspace_min_bytes(M, N, K)}:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        alone = []
+        for i, xi in enumerate(x):
+            alone.append(torch.empty(M, N, device="cuda"))
+            B.iq4xs_linear(w[i % 2], N, K, xi, alone[-1], ws)
+            torch.cuda.synchronize()
+        for _ in range(20):
+            y = [torch.empty(M, N, device="cuda") for _ in x]
+            torch.cuda.synchronize()
+            for i, xi in enumerate(x):
+                B.iq4xs_linear(w[i % 2], N, K, xi, y[i], ws)
+            torch.cuda.synchronize()
+            for got, want in zip(y, alone):
+                assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("d,heads,group,new", [(64, 2, 4, 1), (128, 2, 4, 5), (128, 1, 3, 40)])
+def test_steps_on_one_cache(d, heads, group, new):
+    """Append, attention and commit over and over, nothing waited for, against the same calls one at a time."""
+    def run(wait):
+        bt = Batch([30, 700, 0], [new] * 3, heads=heads, d=d, seed=1, width=(700 + 8 * new) // 16 + 2, spare=90)
+        g = torch.Generator(device="cuda").manual_seed(2)
+        hq, M, outs = heads * group, bt.rows, []
+        x = torch.randn(7, M, hq + 2 * heads, d, generator=g, device="cuda")
+        status = torch.zeros(3, dtype=torch.int32, device="cuda")
+        paths = torch.arange(new, dtype=torch.int32, device="cuda").repeat(3, 1).contiguous()
+        accepted = torch.tensor([new, 1, (new + 1) // 2], dtype=torch.int32, device="cuda")
+        q16 = torch.empty(M, hq, d, dtype=torch.float16, device="cuda")
+        out = [torch.full((M, hq * d), float("nan"), device="cuda") for _ in x]
+        ws = torch.empty(B.iq4xs_tree_attention_workspace_bytes(M, hq, bt.cache, bt.batch), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+
+        def step(f, *a, **k):
+            f(*a, **k)
+            if wait:
+                torch.cuda.synchronize()
+
+        for i in range(len(x)):
+            step(B.iq4xs_cache_reserve, bt.batch, 16, bt.refs, status)
+            step(B.iq4xs_qk_norm_rope, x[i, :, :hq], x[i, :, hq:hq + heads], x[i, :, hq + heads:], None, None, 0.0, None,
+                 None, q16, bt.cache, 0, bt.batch)
+            step(B.iq4xs_tree_attention, q16, bt.cache, 0, bt.batch, d ** -0.5, out[i], ws)
+            step(B.iq4xs_cache_commit, bt.cache, bt.batch, bt.refs, paths, accepted, bt.lens)
+        torch.cuda.synchronize()
+        assert int(status.sum()) == 0 and B.iq4xs_last_device_error() == 0
+        return out + [bt.lens, bt.held, bt.refs]
+
+    want = run(True)
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(run(False), want))
