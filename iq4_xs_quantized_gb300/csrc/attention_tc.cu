@@ -14,9 +14,8 @@
 // one accumulator would add those cuts up.
 //
 // Roles: two producer warps, one thread that issues the MMAs, and eight
-// softmax warps, two per 32-lane quadrant: one takes the first half of a
-// tile's keys and of O's channels, the other the rest; they share a row's
-// maximum through shared memory.  The MMAs of tile j + 1's scores are issued
+// softmax warps, two per 32-lane quadrant, each with half of a tile's keys and
+// of O's channels; they share a row's maximum through shared memory.  The MMAs of tile j + 1's scores are issued
 // before tile j's output product, so the tensor core works while the softmax
 // runs.  K and V tiles go through one ring in the order the MMAs take them,
 // K0 K1 V0 K2 V1 ... V(n-1), K by one warp and V by another (TMA).
@@ -29,12 +28,14 @@ namespace iq4xs {
 namespace {
 
 constexpr int kRowTile = TcForm<64>::kRows;
-constexpr int kSoftWarps = 8;
+constexpr int kShares = 2;     // softmax warps of a quadrant: each has that part of the keys and of the channels
+constexpr int kSoftWarps = 4 * kShares;
 constexpr int kFirstSoft = 4;  // warps 4-11: two whole warpgroups
 constexpr int kThreads = 32 * (kFirstSoft + kSoftWarps);
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kTmemCols = 512;
-constexpr int kItems = 4;  // item descriptors in flight
+constexpr int kItems = 4;     // item descriptors in flight
+constexpr int kAccCols = 16;  // channels of T read at a time
 
 // One item's part as the producer hands it to the other warps.
 struct Item {
@@ -67,14 +68,15 @@ struct TcAttn {
     static_assert(kScores + 2 * kScoreCols <= kTmemCols, "tensor memory");
     // shared memory
     static constexpr int kQBytes = kQInTmem ? 0 : kRowTile * D * 2;
-    static constexpr int kStageCols = kQInTmem ? 32 : 16;    // channels of a row on its way out, and their pitch
+    static constexpr int kStageCols = kQInTmem ? 16 : 8;     // channels of a row on its way out, and their pitch
     static constexpr int kStageRow = kStageCols + 4;
     static constexpr int kStageBytes = kSoftThreads * kStageRow * 4;
     static constexpr int kSlots = (224 * 1024 - kQBytes - kStageBytes) / kTileBytes;
     static constexpr int kQ = kSlots * kTileBytes;
     static constexpr int kOut = kQ + kQBytes;                // rows on their way out (and Q's into tensor memory)
-    static constexpr int kMax = kOut + kStageBytes;          // [2][2 halves][128] row maxima
-    static constexpr int kDesc = kMax + 2 * 2 * kRowTile * 4;
+    static constexpr int kMax = kOut + kStageBytes;          // [2][shares][128] row maxima of a tile
+    static constexpr int kEnd = kMax + 2 * kShares * kRowTile * 4;  // [1 + shares][128] an item's maxima and sums
+    static constexpr int kDesc = kEnd + (1 + kShares) * kRowTile * 4;
     static constexpr int kBars = kDesc + kItems * (int)sizeof(Item);
     static constexpr int kNumBars = 2 * kSlots + 2 * kItems + 2 + 2 + 2 + 2 + 1 + 1;
     static constexpr int kMisc = kBars + kNumBars * 8;       // tensor memory address, abort, odd values
@@ -82,17 +84,18 @@ struct TcAttn {
     static constexpr int kSmem = kLast + kSlots * 4;
     static_assert(kSlots >= 4, "K and V of two tiles");
     static_assert(kSmem <= 227 * 1024, "shared memory");
-    static constexpr int kHalfD = D / 2;
-    static constexpr int kHold = D == 256 ? 16 : 32;         // scores a thread holds at a time
+    static constexpr int kShareD = D / kShares;
+    static constexpr int kHold = D == 256 ? 16 : 32;                         // scores a thread holds at a time
+    static constexpr int kStep = 16;                         // and weights
     // Column of a part of the weights of keys 16 key16 .. + 15, from the buffer's first.
     static __device__ __forceinline__ uint32_t p_col(int key16, int part) {
         return part < 2 ? 16 * key16 + 8 * part : kTile + 8 * key16;
     }
 };
-// D = 256 keeps 128 output channels a softmax thread: the producer's and the
-// issuer's warpgroup gives up registers (80 + 2 * 208 <= 3 * 168, the launch's).
+// The softmax warps keep up to 128 output channels a thread: the producers' and
+// the issuer's warpgroup gives up registers (80 + 2 * 208 <= 3 * 168, the launch's).
 constexpr int kSoftRegs = 208, kOtherRegs = 80;
-static_assert(kOtherRegs + 2 * kSoftRegs <= 3 * 168, "register split within the launch's");
+static_assert(kOtherRegs + kShares * kSoftRegs <= (1 + kShares) * 168, "register split within the launch's");
 
 // Shared-memory matrix descriptor, 128-byte swizzle.  K-major: sbo between
 // 8-row groups.  MN-major: lbo between 64-element chunks of the M/N axis, sbo
@@ -107,21 +110,22 @@ constexpr uint32_t idesc_kv(int n, uint32_t type, bool b_mn) {
     return (1u << 4) | (type << 7) | (type << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(kRowTile >> 4) << 24);
 }
-__device__ __forceinline__ void pair_sync(int quadrant) {
-    asm volatile("bar.sync %0, 64;" ::"r"(quadrant + 1) : "memory");
+__device__ __forceinline__ void quad_sync(int quadrant) {
+    asm volatile("bar.sync %0, %1;" ::"r"(quadrant + 1), "n"(32 * kShares) : "memory");
 }
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
-static_assert(kSoftThreads == 256, "the softmax warps' barrier");
+__device__ __forceinline__ void soft_sync() {
+    asm volatile("bar.sync 5, %0;" ::"n"(kSoftThreads) : "memory");
+}
 // Whether x holds for any softmax thread: one answer for all of them.
 __device__ __forceinline__ bool soft_any(bool x) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 5, 256, p;\n\t"
+        "bar.red.or.pred q, 5, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)x)
+        : "r"((uint32_t)x), "n"(kSoftThreads)
         : "memory");
     return r != 0;
 }
@@ -142,7 +146,14 @@ __device__ __forceinline__ float max_of(const uint32_t* x, float top) {
 }
 template <int n>
 __device__ __forceinline__ void tmem_ld_wait(uint32_t at, uint32_t* x) {
-    if constexpr (n == 8)
+    if constexpr (n == 4)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+            : "r"(at)
+            : "memory");
+    else if constexpr (n == 8)
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
             "tcgen05.wait::ld.sync.aligned;"
@@ -154,7 +165,9 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t at, uint32_t* x) {
 }
 template <int n>
 __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* v) {
-    if constexpr (n == 4)
+    if constexpr (n == 2)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(at), "r"(v[0]), "r"(v[1]) : "memory");
+    else if constexpr (n == 4)
         asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]),
                      "r"(v[2]), "r"(v[3])
                      : "memory");
@@ -171,15 +184,15 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* v) {
 //   masked some row of the tile sees less than all of it; then the first
 //          key's place among the new tokens is j0, and `have` keys lie
 //          before the end
-//   mine, theirs  where the thread and the one that has the row's other half leave their maxima
+//   maxima where the row's shares leave theirs, kRowTile apart; the thread's is `share`
 // m, l: running maximum (log2 units) and sum.  Returns the factor for what O holds.
 template <int D, class T, int kKeys>
 __device__ __forceinline__ float weigh(const AttnParams& p, const RowSight& sight, bool masked, int j0, int have,
-                                       uint32_t s_at, int key, volatile float* mine, volatile float* theirs, int quad,
+                                       uint32_t s_at, int key, volatile float* maxima, int share, int quad,
                                        float& m, float& l) {
     using C = TcAttn<D, T>;
     constexpr int kHold = kKeys < C::kHold ? kKeys : C::kHold;  // scores held at a time
-    constexpr int kStep = kHold < 16 ? kHold : 16;
+    constexpr int kStep = kHold < C::kStep ? kHold : C::kStep;
     uint32_t x[kHold];
     auto read = [&](int h) {
         tmem_ld_wait<kHold>(s_at + key + h, x);
@@ -196,9 +209,11 @@ __device__ __forceinline__ float weigh(const AttnParams& p, const RowSight& sigh
         read(h);
         mx = max_of<kHold>(x, mx);
     }
-    *mine = mx;
-    pair_sync(quad);  // (also: both have read what the weights overwrite)
-    mx = fmaxf(mx, *theirs) * p.scale_log2;  // (the scale is positive)
+    maxima[share * kRowTile] = mx;
+    quad_sync(quad);  // (also: all have read what the weights overwrite)
+#pragma unroll
+    for (int i = 0; i < kShares; ++i) mx = fmaxf(mx, maxima[i * kRowTile]);
+    mx *= p.scale_log2;  // (the scale is positive)
     float f = 1.f;
     if (mx > m + kLazy) {
         f = fast_exp2(m - mx);
@@ -239,7 +254,8 @@ __device__ __forceinline__ float weigh(const AttnParams& p, const RowSight& sigh
 // found some among the former.
 template <int D, class T>
 __device__ __noinline__ bool scrub_tile(uint32_t tile, int first, int have, int thread) {
-    constexpr int kTile = TcForm<D>::kKeys;
+    using C = TcAttn<D, T>;
+    constexpr int kTile = C::kTile;
     bool odd = false;
     for (int u = first * (D / 8) + thread; u < kTile * (D / 8); u += kSoftThreads) {
         const int key = u / (D / 8);
@@ -318,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* last_place = reinterpret_cast<volatile int*>(smem + C::kLast);
     Item* items = reinterpret_cast<Item*>(smem + C::kDesc);
     float* maxima = reinterpret_cast<float*>(smem + C::kMax);
+    float* ends = reinterpret_cast<float*>(smem + C::kEnd);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.x;
     const Bc bc = bc_open(err);
 
@@ -354,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();
 
     if (warp < kFirstSoft) {
-        if constexpr (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // One tile of K or V into its place of the ring, by a whole warp, a
         // box a lane.  False: a wait ran out.
         const int boxes_down = C::kTile / p.box_slots, boxes_across = C::kChunks / p.box_chunks;  // together <= 16
@@ -531,8 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ------------------------------------------------------------ softmax
-        if constexpr (D == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        const int quad = warp & 3, half = (warp - kFirstSoft) >> 2;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        const int quad = warp & 3, share = (warp - kFirstSoft) >> 2;
         const int st_id = threadIdx.x - 32 * kFirstSoft;
         const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
         int place0 = 0, it = 0;
@@ -546,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int len = d.len, keys = len + d.tokens;
             const int rows = min(kRowTile, d.tokens * p.group - d.first);
             // Up to 32 (64) rows stand in all four quadrants (in two pairs of
-            // them), each with a quarter (half) of every tile's keys: all the
+            // them), each with a quarter (a half) of every tile's keys: all the
             // SM's schedulers work on the softmax, and the copies' results
             // are joined at the item's end.
             const int copies = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
@@ -554,14 +571,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int copy = quad / spread;
             const int r = quad % spread * 32 + lane;  // the thread's row of the tile
             const bool busy = quad % spread * 32 < rows;  // the warp has rows
-            const int my_keys = C::kTile / 2 / copies, my_key = (2 * copy + half) * my_keys;
+            const int my_keys = C::kTile / kShares / copies, my_key = (kShares * copy + share) * my_keys;
             RowSight sight;
-            float2 o[C::kHalfD / 2];
+            float2 o[C::kShareD / 2];
 #pragma unroll
-            for (int i = 0; i < C::kHalfD / 2; ++i) o[i] = make_float2(0.f, 0.f);
+            for (int i = 0; i < C::kShareD / 2; ++i) o[i] = make_float2(0.f, 0.f);
             float m = -INFINITY, l = 0.f, f_last = 1.f;
             {
-                // Q of the item's rows: each thread its row's half of the
+                // Q of the item's rows: each thread its share of its row's
                 // channels.  Rows behind the last are zero.
                 const int row = d.first + min(r, rows - 1), tok = token_of(p, row);
                 sight.open(p, d.row0, tok, bc);
@@ -570,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // there: a row's products reach its own lane only.
                 if (n > 0) {
                     constexpr int kAcross = D / 8, kDown = 32 / kAcross;
-                    constexpr int kPitch = C::kStageRow * 4, kPiece = C::kHalfD < 64 ? C::kHalfD : 64;
+                    constexpr int kPitch = C::kStageRow * 4, kPiece = C::kShareD < 32 ? C::kShareD : 32;
                     uint8_t* const stage = smem + C::kOut;
                     const int soft = warp - kFirstSoft, col = lane % kAcross * 8;
                     const uint16_t* src = p.q + d.row0 * p.q_row_stride + (int64_t)d.head * p.group * D + col;
@@ -590,29 +607,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kMost; ++i) v[i] = sign_q(p, v[i]);
                     if constexpr (C::kQInTmem) {
-                        // through the staging rows, 64 channels of each half (or all) at a time
+                        // through the staging rows, 32 channels of each share (or all) at a time
 #pragma unroll
-                        for (int c0 = 0; c0 < C::kHalfD; c0 += kPiece) {
+                        for (int c0 = 0; c0 < C::kShareD; c0 += kPiece) {
                             if (c0 > 0) soft_sync();
-                            const int in_half = col % C::kHalfD - c0;
+                            const int in_share = col % C::kShareD - c0;
 #pragma unroll
                             for (int i = 0; i < kMost; ++i) {
                                 const int from = (i * kSoftWarps + soft) * kDown + lane / kAcross;
-                                if (from < rows && in_half >= 0 && in_half < kPiece)
-                                    *reinterpret_cast<uint4*>(stage + (col / C::kHalfD * kRowTile + from) * kPitch +
-                                                              in_half * 2) = v[i];
+                                if (from < rows && in_share >= 0 && in_share < kPiece)
+                                    *reinterpret_cast<uint4*>(stage + (col / C::kShareD * kRowTile + from) * kPitch +
+                                                              in_share * 2) = v[i];
                             }
                             soft_sync();
                             if (busy) {
                                 uint4 mine[kPiece / 8];
 #pragma unroll
                                 for (int i = 0; i < kPiece / 8; ++i)
-                                    mine[i] = *reinterpret_cast<const uint4*>(stage + (half * kRowTile + r) * kPitch +
+                                    mine[i] = *reinterpret_cast<const uint4*>(stage + (share * kRowTile + r) * kPitch +
                                                                               16 * i);
-#pragma unroll
-                                for (int i = 0; i < kPiece / 32; ++i)
-                                    tmem_st16(tmem + lane_at + C::kQCol + (half * C::kHalfD + c0) / 2 + 16 * i,
-                                              reinterpret_cast<const uint32_t*>(mine + 4 * i));
+                                tmem_st<kPiece / 2>(tmem + lane_at + C::kQCol + (share * C::kShareD + c0) / 2,
+                                                    reinterpret_cast<const uint32_t*>(mine));
                             }
                         }
                         if (busy) tmem_wait_st();
@@ -639,13 +654,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     const float2 f2 = make_float2(f, f);
 #pragma unroll
-                    for (int k = 0; k < C::kHalfD / 32; ++k) {
-                        uint32_t t[32];
-                        tmem_ld32_wait(tmem + lane_at + tb * D + half * C::kHalfD + 32 * k, t);
+                    for (int k = 0; k < C::kShareD; k += kAccCols) {
+                        uint32_t t[kAccCols];
+                        tmem_ld_wait<kAccCols>(tmem + lane_at + tb * D + share * C::kShareD + k, t);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x)
-                            o[16 * k + x] = fma2(o[16 * k + x], f2,
-                                                 make_float2(__uint_as_float(t[2 * x]), __uint_as_float(t[2 * x + 1])));
+                        for (int x = 0; x < kAccCols / 2; ++x)
+                            o[k / 2 + x] = fma2(o[k / 2 + x], f2,
+                                                make_float2(__uint_as_float(t[2 * x]), __uint_as_float(t[2 * x + 1])));
                     }
                     tc_fence_before();
                 }
@@ -661,22 +676,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     const uint32_t s_at = tmem + lane_at + C::kScores + buf * C::kScoreCols;
                     const bool masked = pos0 + C::kTile > len;
-                    volatile float* mine = maxima + (buf * 2 + half) * kRowTile + quad * 32 + lane;
-                    volatile float* theirs = maxima + (buf * 2 + (half ^ 1)) * kRowTile + quad * 32 + lane;
+                    volatile float* most = maxima + buf * kShares * kRowTile + quad * 32 + lane;
                     const int j0 = key0 - len, have = keys - key0;
-                    constexpr int kK = C::kTile / 2;
+                    constexpr int kK = C::kTile / kShares;
                     if (copies == 1) {
-                        f = weigh<D, T, kK>(p, sight, masked, j0, have, s_at, my_key, mine, theirs, quad, m, l);
+                        f = weigh<D, T, kK>(p, sight, masked, j0, have, s_at, my_key, most, share, quad, m, l);
                     } else {
                         f = copies == 2
-                                ? weigh<D, T, kK / 2>(p, sight, masked, j0, have, s_at, my_key, mine, theirs, quad, m, l)
-                                : weigh<D, T, kK / 4>(p, sight, masked, j0, have, s_at, my_key, mine, theirs, quad, m, l);
+                                ? weigh<D, T, kK / 2>(p, sight, masked, j0, have, s_at, my_key, most, share, quad, m, l)
+                                : weigh<D, T, kK / 4>(p, sight, masked, j0, have, s_at, my_key, most, share, quad, m, l);
                         // the other copies' keys weigh nothing in these lanes
                         const uint32_t zero[16] = {};
                         const int own = C::kTile / 16 / copies;  // 16-key groups of a copy
 #pragma unroll
                         for (int k = 0; k < C::kTile / 16; ++k)
-                            if (k / own != copy && (k & 1) == half) {
+                            if (k / own != copy && k % kShares == share) {
                                 tmem_st<16>(s_at + 16 * k, zero);
                                 if constexpr (kParts == 3) tmem_st<8>(s_at + C::p_col(k, 2), zero);
                             }
@@ -707,36 +721,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n > 0 && st_id == 0) odd_flag[(count & 1) ^ 1] = 0;
 
             // The row's maximum over its copies and sum over copies and
-            // halves.  Buffer it & 1 is the one that the last tile did not
-            // use; the other is free once both halves are past that tile.
-            float* all_m = maxima + (it & 1) * 2 * kRowTile;
-            float* last_l = maxima + ((it & 1) ^ 1) * 2 * kRowTile;
+            // shares (all threads have read the last item's by now).
             const int lane_row = quad * 32 + lane;
             float top = m, fix = 1.f, sum = 0.f;
             if (copies > 1) {
-                if (busy && half == 0) all_m[lane_row] = m;
+                if (busy && share == 0) ends[lane_row] = m;
                 soft_sync();
-                for (int i = 0; i < copies; ++i) top = fmaxf(top, all_m[(i * spread + quad % spread) * 32 + lane]);
+                for (int i = 0; i < copies; ++i) top = fmaxf(top, ends[(i * spread + quad % spread) * 32 + lane]);
                 fix = m == -INFINITY ? 0.f : fast_exp2(m - top);
                 if (m != -INFINITY) l *= fix;  // (else nothing was seen: 0, or NaN)
             }
-            if (busy) (half == 0 ? all_m + kRowTile : last_l)[lane_row] = l;
+            if (busy) ends[(1 + share) * kRowTile + lane_row] = l;
             if (copies > 1) soft_sync();
-            else if (busy) pair_sync(quad);
-            for (int i = 0; i < copies; ++i) {
-                const int from = (i * spread + quad % spread) * 32 + lane;
-                sum += all_m[kRowTile + from] + last_l[from];
-            }
+            else if (busy) quad_sync(quad);
+            for (int i = 0; i < copies; ++i)
+#pragma unroll
+                for (int k = 0; k < kShares; ++k)
+                    sum += ends[(1 + k) * kRowTile + (i * spread + quad % spread) * 32 + lane];
             const bool whole = d.slot < 0;
-            if (!whole && half == 0 && copy == 0 && r < rows)
+            if (!whole && share == 0 && copy == 0 && r < rows)
                 if (float2* to = part_sum(p, d.slot, r, bc)) *to = make_float2(top, sum);
             if (copies > 1) {
                 // The other copies hand their outputs to the first, kStageCols
                 // channels at a time through shared memory.
                 constexpr int kCols = C::kStageCols, kPitch = C::kStageRow;
-                float* const stage = reinterpret_cast<float*>(smem + C::kOut) + half * kRowTile * kPitch;
+                float* const stage = reinterpret_cast<float*>(smem + C::kOut) + share * kRowTile * kPitch;
 #pragma unroll
-                for (int ch = 0; ch < C::kHalfD / kCols; ++ch) {
+                for (int ch = 0; ch < C::kShareD / kCols; ++ch) {
                     if (ch > 0) soft_sync();
                     if (busy && copy > 0) {
 #pragma unroll
@@ -771,13 +782,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int row = d.first + r, tok = sight.token;
                 float* const dst = (whole ? p.out + (d.row0 + tok) * p.out_row_stride +
                                                 ((int64_t)d.head * p.group + row - tok * p.group) * D
-                                          : part_row(p, d.slot, r, 0, D, bc)) + half * C::kHalfD;
-                if (!whole ? part_row(p, d.slot, r, 0, D, bc) != nullptr : bc_global(bc, dst, 4 * C::kHalfD, p.out,
+                                          : part_row(p, d.slot, r, 0, D, bc)) + share * C::kShareD;
+                if (!whole ? part_row(p, d.slot, r, 0, D, bc) != nullptr : bc_global(bc, dst, 4 * C::kShareD, p.out,
                                         4 * ((p.rows - 1) * p.out_row_stride + (int64_t)p.group * p.kv_heads * D),
                                         kBcAttnOut)) {
                     if (!whole || p.wide_out) {
 #pragma unroll
-                        for (int i = 0; i < C::kHalfD / 8; ++i) {
+                        for (int i = 0; i < C::kShareD / 8; ++i) {
                             const float2* x = o + 4 * i;
                             asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 8 * i),
                                          "f"(x[0].x * scale), "f"(x[0].y * scale), "f"(x[1].x * scale),
@@ -787,12 +798,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < C::kHalfD / 4; ++i)
+                        for (int i = 0; i < C::kShareD / 4; ++i)
                             *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(
                                 o[2 * i].x * scale, o[2 * i].y * scale, o[2 * i + 1].x * scale, o[2 * i + 1].y * scale);
                     }
                     if (odd_flag[count & 1] != 0)
-                        add_odd<D, T>(p, c, b, d, sight.row, tok, dst, half * C::kHalfD, C::kHalfD, err);
+                        add_odd<D, T>(p, c, b, d, sight.row, tok, dst, share * C::kShareD, C::kShareD, err);
                 }
             }
             __syncwarp();
