@@ -553,7 +553,7 @@ int iq4xs_mma_launch_config(int64_t M, int64_t N, int64_t K, int* rows_per_cta, 
  * (strides in elements, any order of the four axes that does not overlap; i
  * is contiguous).  K and V share the geometry.  k, v 16-byte aligned, every
  * stride a multiple of 8; page_size a power of two, 16..256; head_dim 64, 128
- * or 256; at most 2^31 - 1 pages.
+ * or 256; at most 1024 heads and 2^31 - 1 pages.
  *
  * Batch.  Sequence s holds lens[s] cached tokens (positions 0..lens[s]-1) and
  * owns rows [row_offsets[s], row_offsets[s+1]) of the step's new tokens, which
@@ -565,7 +565,9 @@ int iq4xs_mma_launch_config(int64_t M, int64_t N, int64_t K, int* rows_per_cta, 
  * memory, read when the kernels run (so that a captured graph follows them).
  * A value out of range is recorded in the device error word (code 0x300 + what;
  * status IQ4XS_ERR_DATA) and what it addresses is skipped: no access leaves
- * the buffers.
+ * the buffers.  (Keys of a page out of range read as zeros; what such a
+ * sequence's rows get is of no use.)  What these calls read may come from the
+ * launch before: they wait for it themselves.
  *
  * A page is free when refs[page] == 0; an allocation takes the free pages of
  * lowest index, sequence after sequence, so that every result is the same
@@ -654,7 +656,7 @@ int iq4xs_qk_norm_rope(const iq4xs_qk_norm_rope_args* args, const iq4xs_kv_cache
  *              aligned, of any content; one per stream.
  * Scores and softmax statistics are fp32 and weights keep at least 16
  * significant bits; results are the same from run to run.
- * 1 <= rows <= 32768; q_heads a multiple of the cache's heads.
+ * 1 <= rows <= 32768; q_heads a multiple of the cache's heads, at most 1024.
  */
 typedef struct {
     const void* q;

@@ -11,7 +11,14 @@
 // second), and a warp several heads of one row: their loads are in flight
 // together, the row's sequence, position and rotation are looked up once, the
 // mean is three to five shuffles for all of them, and a rotation partner is
-// the lane's own other half, its next value, or a shuffle away.
+// the lane's own other half, its next value, or a shuffle away.  (A warp a
+// head, each looking its row up, took 142 us where this takes 80; three or
+// four heads after one another instead of two measured the same.)
+//
+// Measured: 12,289 rows of 32 + 2 x 8 heads of 128 channels, all rotated, bf16:
+// 459 MB in 79.7 us, 5.76 TB/s, 85 % of a copy's rate.  One row of 24 + 2 x 4
+// heads of 256: 2.6 us, a launch and three loads that wait for one another.
+// At 256 channels 2.9 of 4 issue slots a cycle are taken, the next bound.
 #include "cache.cuh"
 
 namespace iq4xs {
