@@ -221,8 +221,10 @@ __global__ void __launch_bounds__(kMoveThreads)
     const int len = b.lens[s], n = accepted[s], held = b.held[s];
     const int32_t* path = paths + (int64_t)s * width;
     const bool ok = path_ok(path, n, width, tokens, len) && held >= 0 && held <= b.table_width;
-    const int cols = c.head_dim / 8;  // 16-byte columns of a row
-    const int64_t units = ok ? (int64_t)c.layers * 2 * c.heads * cols : 0;
+    // 16-byte columns of a row, and segments (layer, K or V, head), fewer than
+    // 2^28: 32-bit divisions cost a tenth of 64-bit ones.
+    const int cols = c.head_dim / 8, stride = gridDim.x * kMoveThreads / cols;
+    const uint32_t segs = ok ? (uint32_t)(c.layers * 2 * c.heads) : 0u;
     for (int c0 = 0; ok && c0 < n; c0 += kMoveRows) {
         // where the next rows of the path lie in a (layer, head), -1: stays or cannot move
         __syncthreads();
@@ -242,12 +244,10 @@ __global__ void __launch_bounds__(kMoveThreads)
         }
         __syncthreads();
         const int rows = min(kMoveRows, n - c0);
-        for (int64_t u = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x; u < units;
-             u += (int64_t)gridDim.x * kMoveThreads) {
-            const int64_t seg = u / cols;  // (layer, K or V, head)
-            uint16_t* base = seg / c.heads % 2 ? c.v : c.k;
-            uint16_t* column = base + (seg / c.heads / 2) * c.layer_stride + seg % c.heads * c.head_stride +
-                               (u - seg * cols) * 8;
+        for (uint32_t seg = (blockIdx.x * kMoveThreads + threadIdx.x) / cols; seg < segs; seg += stride) {
+            const uint32_t side = seg / c.heads, head = seg - side * c.heads;
+            uint16_t* base = side % 2 ? c.v : c.k;
+            uint16_t* column = base + (side / 2) * c.layer_stride + head * c.head_stride + threadIdx.x % cols * 8;
             for (int i0 = 0; i0 < rows; i0 += kMoveBatch) {
                 uint4 val[kMoveBatch];
 #pragma unroll
@@ -372,11 +372,11 @@ constexpr int kCopyThreads = 128;
 constexpr int kCopyBatch = 4;
 
 // `slots` slots of one (layer, K or V, head) from page `src` to page `dst`.
-__device__ void copy_slots(const Bc& bc, const CacheView& c, int64_t seg, int src, int dst, int slots) {
+__device__ void copy_slots(const Bc& bc, const CacheView& c, uint32_t seg, int src, int dst, int slots) {
     const int cols = c.head_dim / 8;
-    const int head = (int)(seg % c.heads);
-    uint16_t* base = seg / c.heads % 2 ? c.v : c.k;
-    uint16_t* rows = base + (seg / c.heads / 2) * c.layer_stride + head * c.head_stride;
+    const uint32_t side = seg / c.heads, head = seg - side * c.heads;
+    uint16_t* base = side % 2 ? c.v : c.k;
+    uint16_t* rows = base + (side / 2) * c.layer_stride + head * c.head_stride;
     const uint16_t* from = rows + src * c.page_stride;
     uint16_t* to = rows + dst * c.page_stride;
     const int units = slots * cols;
