@@ -208,24 +208,31 @@ cudaError_t launch_tree_attention(const iq4xs_tree_attention_args& a, const Cach
     p.mask_words = (int)a.mask_words;
     p.head_dim = c.head_dim;
     p.skip_stage = skip_stage;
-    // The warp-level form while a sequence's rows a key/value head fit its
-    // row tile, tcgen05 with tiles of 128 beyond.
+    // The warp-level form up to 8 rows a sequence and key/value head (7
+    // sequences of 9,000 tokens, 8 rows, 128 channels, bf16: 42.7 us, tcgen05
+    // 47.4), and up to 16 at 256 channels (12 rows, fp16: 45.6 and 49.2) or
+    // where the items are few (16 rows of one sequence of 30,000, 128 channels:
+    // 34.3 and 36.1; of 4 sequences 82.6 and 69.3, of 7 of 9,000 57.3 and 47.8);
+    // tcgen05 with tiles of 128 beyond (20 rows of 64 channels: 34.5 us, 45.2 by
+    // warp-level tiles of 24).
     const int64_t mean_rows = (a.rows + b.sequences - 1) / b.sequences * group;
-    const int row_tile = mean_rows <= 8 ? 8 : mean_rows <= 16 ? 16 : 128;
+    // Items there can be at most: a row tile more than whole ones a sequence.
+    const auto items = [&](int rows) {
+        return c.heads * ((a.rows < b.sequences ? a.rows : b.sequences) + a.rows * group / rows);
+    };
+    const auto few = [&](int64_t n) { return n * (kMaxCluster + 1) <= num_sms; };  // a cluster for each fits
+    const int row_tile = mean_rows <= 8                                             ? 8
+                         : mean_rows <= 16 && (c.head_dim == 256 || few(items(16))) ? 16
+                                                                                    : 128;
     const bool tc = row_tile == 128;
     p.ctas = num_sms < kMaxParts ? num_sms : kMaxParts;
     p.cluster = 1;
     const int64_t tokens = (int64_t)b.table_width * c.page_size;  // no sequence is longer
     p.whole_items = tokens <= kWholeTokens;
-    if (!tc && tokens > kAloneTokens && tokens <= kClusterTokens) {
-        // Items there can be at most: a row tile more than whole ones a sequence.
-        const int64_t items =
-            c.heads * ((a.rows < b.sequences ? a.rows : b.sequences) + a.rows * group / row_tile);
-        if (items * (kMaxCluster + 1) <= num_sms) {  // (a GPC's SMs are no multiple of eight)
-            p.cluster = kMaxCluster;
-            p.ctas = (int)items;
-            p.whole_items = 1;
-        }
+    if (!tc && tokens > kAloneTokens && tokens <= kClusterTokens && few(items(row_tile))) {
+        p.cluster = kMaxCluster;  // (one more in `few`: a GPC's SMs are no multiple of eight)
+        p.ctas = (int)items(row_tile);
+        p.whole_items = 1;
     }
     p.slot_rows = (int)slot_rows(row_tile, a.rows, group);
     // Measured: starting and ending a part costs about 8 key tiles on tcgen05, 3 on the warp-level form.
