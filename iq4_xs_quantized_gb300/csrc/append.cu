@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kAppendThreads)
                 float4 t = make_float4(1.f, 0.f, 1.f, 0.f);
                 if (k < 2 * p.rot_half &&
                     bc_global(bc, from + 2 * e, 16, p.rope, p.rope_positions * 8 * p.rot_half, kBcAppRope))
-                    t = __ldg(reinterpret_cast<const float4*>(from + 2 * e));
+                    t = *reinterpret_cast<const float4*>(from + 2 * e);
                 turn[j][e] = make_float2(t.x, t.y);
                 turn[j][e + 1] = make_float2(t.z, t.w);
             }
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kAppendThreads)
         for (int j = 0; j < 2; ++j) {
             const float* w = weight + j * (D / 2) + 4 * l;
             if (!bc_global(bc, w, 16, weight, 4 * D, kBcAppW)) continue;
-            const float4 t = __ldg(reinterpret_cast<const float4*>(w));
+            const float4 t = *reinterpret_cast<const float4*>(w);
             v[i][j][0] *= r * t.x;
             v[i][j][1] *= r * t.y;
             v[i][j][2] *= r * t.z;

@@ -209,8 +209,8 @@ __device__ bool path_ok(const int32_t* path, int n, int width, int tokens, int l
 // books, once every CTA is done with what it rewrites (held, and the length
 // when new_lens is lens): one launch where two would follow each other.
 __global__ void __launch_bounds__(kMoveThreads)
-    commit_kernel(const CacheView c, const BatchView b, int32_t* refs, const int32_t* __restrict__ paths, int width,
-                  const int32_t* __restrict__ accepted, int32_t* new_lens, int* err) {
+    commit_kernel(const CacheView c, const BatchView b, int32_t* refs, const int32_t* paths, int width,
+                  const int32_t* accepted, int32_t* new_lens, int* err) {
     __shared__ int64_t from_s[kMoveRows], to_s[kMoveRows];
     griddep_launch_dependents();
     griddep_wait();
@@ -301,8 +301,8 @@ __device__ int fork_state(const BatchView& b, int parent, int child, int shift, 
 }
 
 __global__ void __launch_bounds__(kBookThreads)
-    fork_book_kernel(const BatchView b, int shift, int32_t* refs, int pages, const int32_t* __restrict__ parents,
-                     const int32_t* __restrict__ children, int count, int32_t* status, int* err) {
+    fork_book_kernel(const BatchView b, int shift, int32_t* refs, int pages, const int32_t* parents,
+                     const int32_t* children, int count, int32_t* status, int* err) {
     griddep_launch_dependents();
     griddep_wait();
     const Bc bc = bc_open(err);
@@ -399,8 +399,8 @@ __device__ void copy_slots(const Bc& bc, const CacheView& c, uint32_t seg, int s
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
-    fork_copy_kernel(const CacheView c, const BatchView b, const int32_t* __restrict__ parents,
-                     const int32_t* __restrict__ children, const int32_t* status, int* err) {
+    fork_copy_kernel(const CacheView c, const BatchView b, const int32_t* parents,
+                     const int32_t* children, const int32_t* status, int* err) {
     griddep_launch_dependents();
     griddep_wait();
     const Bc bc = bc_open(err);
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
-    copy_pages_kernel(const CacheView c, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int* err) {
+    copy_pages_kernel(const CacheView c, const int32_t* src, const int32_t* dst, int* err) {
     griddep_launch_dependents();
     griddep_wait();
     const Bc bc = bc_open(err);
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 constexpr int kReleaseThreads = 256;
 
 __global__ void __launch_bounds__(kReleaseThreads)
-    release_kernel(const BatchView b, int32_t* refs, int pages, const int32_t* __restrict__ rows, int* err) {
+    release_kernel(const BatchView b, int32_t* refs, int pages, const int32_t* rows, int* err) {
     __shared__ int held_s;
     griddep_launch_dependents();
     griddep_wait();
