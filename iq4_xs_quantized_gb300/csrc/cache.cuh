@@ -83,7 +83,7 @@ struct KvBf16 {
 // Host-side launchers (csrc/append.cu, csrc/cache_pages.cu, csrc/attention*.cu);
 // arguments are checked by the callers in csrc/cache_api.cu.
 cudaError_t launch_qk_norm_rope(const iq4xs_qk_norm_rope_args& a, const CacheView& c, const BatchView& b, bool bf16,
-                                int* err, cudaStream_t stream);
+                                int* err, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_reserve(const BatchView& b, int page_size, int32_t* refs, int pages, int32_t* status, int* err,
                                  cudaStream_t stream);
 cudaError_t launch_cache_commit(const CacheView& c, const BatchView& b, int32_t* refs, const int32_t* paths,

@@ -90,7 +90,7 @@ int iq4xs_qk_norm_rope(const iq4xs_qk_norm_rope_args* a, const iq4xs_kv_cache* c
     void* encode;
     if ((rc = device_context(&err, &sms, &encode))) return rc;
     if (b.sequences == 0) return IQ4XS_OK;
-    return from_cuda(launch_qk_norm_rope(*a, c, b, cache->dtype == IQ4XS_KV_BF16, err,
+    return from_cuda(launch_qk_norm_rope(*a, c, b, cache->dtype == IQ4XS_KV_BF16, err, sms,
                                          reinterpret_cast<cudaStream_t>(stream)));
 }
 
