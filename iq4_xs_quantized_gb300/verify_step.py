@@ -9,7 +9,7 @@ forked and released between steps.
     python -m iq4_xs_quantized_gb300.verify_step [--layers L] [--sequences S] [--tree T] [--steps N]
 
 Weights are seeded random IQ4_XS blocks and a token is a seeded random hidden
-state, so a path's acceptance is drawn, not judged; what a run checks is that
+state, so a path's acceptance is drawn at random; what a run checks is that
 a sequence that came by drafted trees ends where one that was decoded token
 by token ends.
 """
