@@ -710,11 +710,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                     tc_fence_before();
                 }
-                if (pos0 + C::kTile > len && (keys - pos0 < C::kTile || keys - len > 1)) {
+                if (pos0 + C::kTile > len && (keys - pos0 < C::kTile || keys - len > 1 || p.mask != nullptr)) {
                     // Slots behind the end may hold anything, and so may tokens
-                    // that some row does not see: a zero weight would carry their
-                    // NaN and infinities into its sum.  Such values leave the
-                    // tile; rows that do see them get them at the item's end.
+                    // that some row does not see (without a mask a single new
+                    // token sees itself): a zero weight would carry their NaN
+                    // and infinities into its sum.  Such values leave the tile;
+                    // rows that do see them get them at the item's end.
                     const int place = place0 + place_v(j, n), st = place % C::kSlots;
                     kv_wait(full + st, (place / C::kSlots) & 1, abort_flag, err, kDevErrTimeoutKv);
                     if (scrub_tile<D, T>(base + st * C::kTileBytes, max(0, len - pos0), min(C::kTile, keys - pos0), st_id))

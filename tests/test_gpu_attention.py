@@ -193,6 +193,28 @@ def test_nan_and_infinities_of_hidden_tokens_stay_out(d, t, dtype):
     assert bool(torch.isnan(out2[3]).all())
 
 
+@pytest.mark.parametrize("value", (float("nan"), float("inf")))
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("d,group", [(64, 20), (128, 20), (256, 20), (64, 2), (128, 8), (256, 12)])
+def test_a_single_hidden_token_on_a_tiles_last_place_stays_out(d, group, dtype, value):
+    """One new token a sequence, hidden by its own mask row, where context and
+    token fill whole key tiles of 64 and of 128: nothing lies behind the end,
+    and no other token is hidden, but its K and V stay out all the same."""
+    lens = [63, 127, 255, 1023, 40]
+    bt = Batch(lens, [1] * 5, heads=2, d=d, dtype=dtype)
+    for s, n in enumerate(lens):
+        page, slot = int(bt.table_n[s][n // 16]), n % 16
+        bt.cache.v[0, page, :, slot] = value
+        bt.cache.k[0, page, :, slot] = value
+    q = _q(bt, 2 * group)
+    out = run_attention(bt, q, d ** -0.5, mask_words([set()] * 5, 1))
+    ref = attention_ref(bt, q, d ** -0.5, lambda s, t, j: False)
+    assert torch.isfinite(ref).all()
+    r = gate_parity(out.cpu().numpy(), ref.cpu().numpy())
+    assert r is None, r
+    assert B.iq4xs_last_device_error() == 0
+
+
 def test_large_scores_and_negative_scale():
     bt = Batch([300, 10], [3, 1], heads=1, d=64)
     _check(bt, _q(bt, 4, mult=8.0), scale=1.0)     # scores of a few hundred: one key carries the row
