@@ -242,7 +242,10 @@ __global__ void __launch_bounds__(MmaAttn<D, NT>::kThreads, 1)
     griddep_launch_dependents();
     WorkWalk<F> w;
     w.start(p, b, g, err);
-    // A cluster shares one item, an eighth of its key tiles a CTA.
+    // A cluster shares one item, an eighth of its key tiles a CTA.  It takes
+    // one alone, and there are as many clusters as items, unless row offsets
+    // fall (recorded), so that sequences overlap: items past the clusters are
+    // left out, for the ring of the first one is where its parts meet.
     const int rank = p.cluster > 1 ? (int)cluster_ctarank() : 0;
     if (threadIdx.x == 0 && !p.whole_items) w.tell_cut(p, g);
     if (p.cluster > 1 && w.valid()) {
@@ -250,6 +253,7 @@ __global__ void __launch_bounds__(MmaAttn<D, NT>::kThreads, 1)
         w.tile0 = rank * tiles / p.cluster;
         w.tile1 = (rank + 1) * tiles / p.cluster;
         w.whole = false;
+        w.left = 1;
     }
 
     if (warp >= kConsumers) {

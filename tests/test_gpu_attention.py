@@ -342,6 +342,28 @@ def test_bad_device_values_are_reported_and_skipped():
     assert torch.equal(run_attention(bt, q, 0.125), good)
 
 
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("d", (64, 128, 256))
+def test_falling_offsets_where_clusters_share_items(d, dtype):
+    """Offsets that fall leave sequences that overlap, and more items than the
+    clusters that one row asks for: it is reported, every cluster takes one
+    item, and the next call gives what it gave before."""
+    bt = Batch([600, 5, 700, 900, 300], [1] * 5, heads=2, d=d, dtype=dtype, width=64)
+    one = Batch([600], [1], heads=2, d=d, dtype=dtype, width=64)
+    q = _q(one, 16)
+    good = run_attention(one, q, d ** -0.5)
+    offsets = torch.tensor([0, 1, 0, 1, 0, 1], dtype=torch.int32, device="cuda")  # two heads of three sequences, 4 clusters
+    batch = B.KVBatch(offsets, bt.lens, bt.held, bt.table)
+    out = torch.full((1, 16 * d), float("nan"), device="cuda")
+    ws = torch.empty(B.iq4xs_tree_attention_workspace_bytes(1, 16, bt.cache, batch), dtype=torch.uint8, device="cuda")
+    code = ctypes.c_int(-1)
+    for _ in range(3):
+        B.iq4xs_tree_attention(q, bt.cache, 0, batch, d ** -0.5, out, ws)
+        torch.cuda.synchronize()
+        assert B.load().iq4xs_last_device_error(ctypes.byref(code)) == B.ERR_DATA and code.value == 0x301, hex(code.value)
+    assert torch.equal(run_attention(one, q, d ** -0.5), good)
+
+
 @pytest.mark.parametrize("stage", (0, 3))
 @pytest.mark.parametrize("rows", (1, 40))
 def test_unissued_stage_times_out_and_context_stays_usable(stage, rows):
