@@ -694,6 +694,8 @@ int iq4xs_cache_reserve(const iq4xs_kv_batch* batch, int64_t page_size, int32_t*
  * (indices among its new tokens, strictly rising).  Their K and V move, in
  * every layer, to positions lens[s], lens[s]+1, ...; new_lens[s] = lens[s] +
  * accepted[s]; pages behind the new end are dropped (held shrinks, refs fall).
+ * A sequence whose path is out of order, or would end behind the pages it
+ * holds, keeps its length and pages (IQ4XS_ERR_DATA).
  *   paths  int32 [sequences][path_width]; accepted  int32 [sequences],
  *   0..path_width; new_lens  int32 [sequences], may be lens itself.
  */

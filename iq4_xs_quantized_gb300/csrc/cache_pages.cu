@@ -220,7 +220,9 @@ __global__ void __launch_bounds__(kMoveThreads)
     const int tokens = batch_rows(b, s, INT32_MAX, &first, err);
     const int len = b.lens[s], n = accepted[s], held = b.held[s];
     const int32_t* path = paths + (int64_t)s * width;
-    const bool ok = path_ok(path, n, width, tokens, len) && held >= 0 && held <= b.table_width;
+    // (rows that stay where they are look no page up: their end is compared with the pages held)
+    const bool held_ok = held >= 0 && held <= b.table_width && (int64_t)len + n <= (int64_t)held << c.page_shift;
+    const bool ok = path_ok(path, n, width, tokens, len) && held_ok;
     // 16-byte columns of a row, and segments (layer, K or V, head), fewer than
     // 2^28: 32-bit divisions cost a tenth of 64-bit ones.
     const int cols = c.head_dim / 8, stride = gridDim.x * kMoveThreads / cols;
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kMoveThreads)
     if (blockIdx.x != 0) return;
     if (!ok) {
         if (threadIdx.x == 0) {
-            data_error(err, len < 0 ? kDataLens : held < 0 || held > b.table_width ? kDataHeld : kDataPath);
+            data_error(err, len < 0 ? kDataLens : held_ok ? kDataPath : kDataHeld);
             new_lens[s] = len;
         }
         return;

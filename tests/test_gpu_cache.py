@@ -256,6 +256,27 @@ def test_commit_refuses_bad_paths_of_a_sequence_alone(path, n):
     assert torch.equal(bt.cache.k[0, page, :, slot], k[0, page, :, 23 % 16])
 
 
+@pytest.mark.parametrize("path", ([0, 1, 2, 3], [1, 2, 3, 4]))
+def test_commit_keeps_a_sequence_within_its_pages(path):
+    """A sequence that reserve gave no page keeps its length: a path that ends
+    behind the pages held is refused, also where no row of it has to move."""
+    bt = Batch([14, 20], [0, 0], d=64, heads=1, spare=0, width=4, garbage=None)
+    batch = B.KVBatch(_i32([0, 5, 8]), bt.lens, bt.held, bt.table)
+    st = _i32([9, 9])
+    B.iq4xs_cache_reserve(batch, 16, bt.refs, st)
+    torch.cuda.synchronize()
+    assert st.tolist() == [1, 0] and bt.held.tolist() == [1, 2]
+    new_lens = _i32([0, 0])
+    B.iq4xs_cache_commit(bt.cache, batch, bt.refs, _i32([path, [0, 1, 2, -7]]), _i32([4, 3]), new_lens)
+    _data_error(3)
+    assert new_lens.tolist() == [14, 23] and bt.held.tolist() == [1, 2]
+    assert bt.refs.tolist() == bt.refs_n.tolist()
+    # up to the last slot of the pages held it is taken
+    B.iq4xs_cache_commit(bt.cache, batch, bt.refs, _i32([[0, 1], [0, 1]]), _i32([2, 0]), new_lens)
+    torch.cuda.synchronize()
+    assert new_lens.tolist() == [16, 20] and B.iq4xs_last_device_error() == 0
+
+
 @pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
 @pytest.mark.parametrize("page,order,d", [(16, "heads slots", 64), (64, "slots heads", 128), (256, "heads slots", 256)])
 def test_fork_shares_copies_and_release_restores(page, order, d, dtype):
