@@ -715,7 +715,8 @@ int iq4xs_cache_fork(const iq4xs_kv_cache* cache, const iq4xs_kv_batch* batch, i
                      const int32_t* parents, const int32_t* children, int64_t count, int32_t* status,
                      int64_t stream);
 
-/* Sequences rows[0..count) end: their pages' refs fall, lens and held become 0. */
+/* Sequences rows[0..count) end: their pages' refs fall (one that is 0 already
+ * stays 0 and is reported, here as in a commit), lens and held become 0. */
 int iq4xs_cache_release(const iq4xs_kv_batch* batch, int32_t* refs, int64_t pages, const int32_t* rows,
                         int64_t count, int64_t stream);
 

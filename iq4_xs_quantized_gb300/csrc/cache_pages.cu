@@ -185,6 +185,19 @@ __global__ void __launch_bounds__(kBookThreads)
     }
 }
 
+// One reference less to `page`.  A count that is zero already stays zero, and
+// is reported: the page would otherwise never be free again.
+__device__ __forceinline__ void drop_page(const Bc& bc, int32_t* refs, int page, int pages, int* err) {
+    if (page < 0 || page >= pages) {
+        data_error(err, kDataPage);
+    } else if (bc_global(bc, refs + page, 4, refs, 4 * (int64_t)pages, kBcPagesRefs)) {
+        if (atomicSub(refs + page, 1) <= 0) {
+            atomicAdd(refs + page, 1);
+            data_error(err, kDataRefs);
+        }
+    }
+}
+
 // ------------------------------------------------------------------ commit
 // One thread per 16-byte column of a head's row: it walks the accepted path
 // of its sequence in order, up to kMoveBatch loads in flight before their
@@ -276,11 +289,8 @@ __global__ void __launch_bounds__(kMoveThreads)
         return;
     }
     const int keep = min(held, pages_for((int64_t)len + n, c.page_shift));
-    for (int j = keep + threadIdx.x; j < held; j += kMoveThreads) {
-        const int page = b.page_table[s * b.table_stride + j];
-        if (page < 0 || page >= c.pages) data_error(err, kDataPage);
-        else if (bc_global(bc, refs + page, 4, refs, 4 * (int64_t)c.pages, kBcPagesRefs)) atomicSub(refs + page, 1);
-    }
+    for (int j = keep + threadIdx.x; j < held; j += kMoveThreads)
+        drop_page(bc, refs, b.page_table[s * b.table_stride + j], c.pages, err);
     if (threadIdx.x == 0) {
         b.held[s] = keep;
         new_lens[s] = len + n;
@@ -453,11 +463,8 @@ __global__ void __launch_bounds__(kReleaseThreads)
         data_error(err, kDataHeld);
         held = 0;
     }
-    for (int j = threadIdx.x; j < held; j += kReleaseThreads) {
-        const int page = b.page_table[s * b.table_stride + j];
-        if (page < 0 || page >= pages) data_error(err, kDataPage);
-        else if (bc_global(bc, refs + page, 4, refs, 4 * (int64_t)pages, kBcPagesRefs)) atomicSub(refs + page, 1);
-    }
+    for (int j = threadIdx.x; j < held; j += kReleaseThreads)
+        drop_page(bc, refs, b.page_table[s * b.table_stride + j], pages, err);
 }
 
 }  // namespace

@@ -323,6 +323,29 @@ def test_fork_without_pages_or_with_bad_rows():
     assert sorted(bt.refs.tolist()) == sorted([2, 2, 1, 1, 1, 1, 1])
 
 
+def test_a_page_dropped_twice_is_reported_and_stays_free():
+    """Two table rows that name the same pages, counted once: what the second
+    one drops is reported, and the pages can be given out again."""
+    bt = Batch([40, 5, 0], [0] * 3, heads=1, d=64, garbage=None)
+    bt.table[2, :3] = bt.table[0, :3]
+    bt.held[2], bt.lens[2] = 3, 40
+    want = bt.refs_n.copy()
+    want[bt.table_n[0][:3]] = 0
+    B.iq4xs_cache_release(bt.batch, bt.refs, _i32([0]))
+    torch.cuda.synchronize()
+    assert B.iq4xs_last_device_error() == 0 and bt.refs.tolist() == want.tolist()
+    B.iq4xs_cache_release(bt.batch, bt.refs, _i32([2]))
+    _data_error(8)
+    assert bt.refs.tolist() == want.tolist() and bt.held.tolist() == [0, 1, 0]
+    # the same by a commit that gives up all of its pages
+    bt.table[2, :3] = bt.table[0, :3]
+    bt.held[2] = 3
+    new_lens = _i32([0, 0, 0])
+    B.iq4xs_cache_commit(bt.cache, bt.batch, bt.refs, _i32([[0]] * 3), _i32([0] * 3), new_lens)
+    _data_error(8)
+    assert bt.refs.tolist() == want.tolist() and bt.held.tolist() == [0, 1, 0]
+
+
 def test_copy_pages_every_layer():
     bt = Batch([200], [0], heads=2, d=128, layers=4, spare=8, garbage=None)
     k, v = bt.cache.k.clone(), bt.cache.v.clone()
