@@ -654,8 +654,9 @@ int iq4xs_qk_norm_rope(const iq4xs_qk_norm_rope_args* args, const iq4xs_kv_cache
  *              64*mask_words is seen by no row.
  *   workspace  iq4xs_tree_attention_workspace_bytes(...) bytes, 32-byte
  *              aligned, of any content; one per stream.
- * Scores and softmax statistics are fp32 and weights keep at least 16
- * significant bits; results are the same from run to run.
+ * Scores and softmax statistics are fp32.  A weight is kept to 2^-22 of itself
+ * or 2^-43 of the row's largest one, whichever is more, rounded to nearest
+ * (fp16 cache), or to 24 bits (bf16).  Results are the same from run to run.
  * 1 <= rows <= 32768; q_heads a multiple of the cache's heads, at most 1024.
  */
 typedef struct {

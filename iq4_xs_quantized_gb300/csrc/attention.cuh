@@ -358,8 +358,8 @@ __device__ __forceinline__ float fast_exp2(float x) {
 
 // Softmax weights are exp2(score - m + kWeightBits) with m the running
 // maximum, or up to kLazy below it: O and the sum are rescaled only when a
-// maximum rises by more than kLazy.  kWeightBits keeps small weights out of
-// the fp16 subnormals: 2^(6 + 8) is the largest, 2^-24 the smallest part.
+// maximum rises by more than kLazy.  kWeightBits uses fp16's range: weights
+// go up to 2^(6 + 8), and the largest of a row is 2^6 at least.
 constexpr float kWeightBits = 6.0f;
 constexpr float kLazy = 8.0f;
 
@@ -386,25 +386,30 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ float2 mask2(float2 a, uint32_t mask) {
     return make_float2(__uint_as_float(__float_as_uint(a.x) & mask), __uint_as_float(__float_as_uint(a.y) & mask));
 }
-// Two weights as the sum of kN packed 16-bit parts, largest first.  All but
-// the last part cut the fp32 value off after the type's significant bits
-// (what is left is exact).  fp16: 11 + 11 bits, of 24 (weights below 2^-14
-// keep 2^-25 of the largest).  bf16: 8 + 8 + 8, the whole value.
+// Two weights as the sum of kN packed 16-bit parts, largest first; the last
+// one is kept times 2^kLastShift, and so is what it makes of V until it meets
+// the others.  fp16: the nearest 11 bits, down to the subnormals' 2^-24, and
+// what is left of them (exact in fp32) times 2^12: 22 bits of every weight from
+// 2^-14 on and 2^-37 of smaller ones, 2^-43 of the row's largest, rounded to
+// nearest both times.  (Without the factor what is left of a weight below 2^-14
+// falls under half of 2^-24 and is lost: beside one key that outweighs the
+// others by 2^20 the result was off by 2e-5, by 2^24 by 7e-4.)  bf16: 8 + 8 +
+// 8 bits cut off, the whole value.
 template <class T>
 struct Parts;
 template <>
 struct Parts<KvF16> {
-    static constexpr int kN = 2;
+    static constexpr int kN = 2, kLastShift = 12;
     static __device__ __forceinline__ void split(float2 a, uint32_t* out) {
-        const float2 h = mask2(a, 0xffffe000u);
-        out[0] = KvF16::pack(h.x, h.y);
-        const float2 r = fma2(h, make_float2(-1.f, -1.f), a);
-        out[1] = KvF16::pack(r.x, r.y);
+        constexpr float kUp = 1 << kLastShift;
+        out[0] = KvF16::pack(a.x, a.y);
+        const float2 r = fma2(KvF16::unpack(out[0]), make_float2(-1.f, -1.f), a);
+        out[1] = KvF16::pack(r.x * kUp, r.y * kUp);
     }
 };
 template <>
 struct Parts<KvBf16> {
-    static constexpr int kN = 3;
+    static constexpr int kN = 3, kLastShift = 0;
     static __device__ __forceinline__ void split(float2 a, uint32_t* out) {
 #pragma unroll
         for (int i = 0; i < 3; ++i) {

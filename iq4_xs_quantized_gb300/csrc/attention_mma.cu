@@ -502,7 +502,13 @@ __global__ void __launch_bounds__(MmaAttn<D, NT>::kThreads, 1)
                     for (int n = 0; n < NT; ++n) {
                         float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int k = Parts<T>::kN - 1; k >= 0; --k) mma16816<T>(t, vf, pf[k][n][0], pf[k][n][1]);
+                        for (int k = Parts<T>::kN - 1; k >= 0; --k) {
+                            mma16816<T>(t, vf, pf[k][n][0], pf[k][n][1]);
+                            if (Parts<T>::kLastShift > 0 && k == Parts<T>::kN - 1) {
+                                constexpr float kDown = 1.0f / (1 << Parts<T>::kLastShift);
+                                t[0] *= kDown; t[1] *= kDown; t[2] *= kDown; t[3] *= kDown;
+                            }
+                        }
 #pragma unroll
                         for (int k = 0; k < 4; ++k) o[i][n][k] += t[k];
                     }

@@ -541,9 +541,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int part = kParts - 1; part >= 0; --part)  // the smallest parts first
 #pragma unroll
-                        for (int k = 0; k < C::kTile / 16; ++k)
-                            tc_mma_f16_ta(t_at, p_at + C::p_col(k, part), v_desc + ((k * 16 * kChunkBytes) >> 4), kIdT,
-                                          part < kParts - 1 || k > 0);
+                        for (int k = 0; k < C::kTile / 16; ++k) {
+                            const uint64_t vd = v_desc + ((k * 16 * kChunkBytes) >> 4);
+                            // (the product that joins the smallest parts brings their sum down to scale)
+                            if (Parts<T>::kLastShift > 0 && part == kParts - 2 && k == 0)
+                                tc_mma_f16_ta_down<Parts<T>::kLastShift>(t_at, p_at + C::p_col(k, part), vd, kIdT);
+                            else
+                                tc_mma_f16_ta(t_at, p_at + C::p_col(k, part), vd, kIdT, part < kParts - 1 || k > 0);
+                        }
                     tc_commit(t_full + tb);
                     tc_commit(slot_free + st);
                 }

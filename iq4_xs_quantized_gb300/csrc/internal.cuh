@@ -684,6 +684,17 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, 
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// The same added to the accumulator times 2^-kShift (0..15).
+template <int kShift>
+__device__ __forceinline__ void tc_mma_f16_ta_down(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc) {
+    static_assert(kShift >= 0 && kShift <= 15, "the instruction's range");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, 1, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p, %4;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "n"(kShift)
+        : "memory");
+}
 // One lane of the (converged) warp returns true.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;

@@ -6,6 +6,7 @@ feeds.  Expected: weights carry the scores' fp32 rounding (~|s| 2^-23 ~ 1e-6
 for |s| <= 10) and 2^-22 from exp2 and their split into parts; sums are fp32.
 """
 import ctypes
+import math
 
 import numpy as np
 import pytest
@@ -232,6 +233,66 @@ def test_rising_maxima_rescale():
     slot = (torch.arange(2000) % 16).cuda()
     bt.cache.k[0][page, :, slot] = k[order].to(bt.cache.dtype)
     _check(bt, q, scale=1.0)
+
+
+def _with_sink(n, above, d, heads, group, rows, dtype, v_sink, v_rest=None, at=0, seed=7):
+    """A sequence of n cached tokens of which one, at `at`, scores about `above`
+    (in log2 units) over the others, whose scores spread by one such unit."""
+    bt = Batch([n], [rows], heads=heads, d=d, page=64, dtype=dtype, garbage=None, seed=seed)
+    q = _q(bt, heads * group, mult=1.0)
+    q[..., 0] = 8.0
+    k, v = bt.cache.k, bt.cache.v
+    k *= math.log(2)  # q.k d^-1/2 spreads by one: log2 units after the factor log2(e)
+    k[..., 0] = 0
+    page, slot = int(bt.table_n[0][at // 64]), at % 64
+    k[0, page, :, slot] = 0
+    k[0, page, :, slot, 0] = above * math.log(2) * d ** 0.5 / 8
+    if v_rest is not None:
+        v.fill_(v_rest)
+    v[0, page, :, slot] = v_sink
+    return bt, q
+
+
+def _all_rows_ref(bt, q):
+    """Chains over one sequence in float64, head by head."""
+    (n,), (rows,) = bt.lens_n, bt.new_n
+    k, v = bt.gather(0, n + rows)
+    seen = torch.arange(n + rows, device="cuda") <= torch.arange(n, n + rows, device="cuda")[:, None]
+    group, ref = q.shape[1] // bt.heads, torch.empty(q.shape, dtype=torch.float64, device="cuda")
+    for h in range(q.shape[1]):
+        x = (q[:, h].double() @ k[:, h // group].T * bt.d ** -0.5).masked_fill(~seen, -float("inf"))
+        ref[:, h] = torch.softmax(x, -1) @ v[:, h // group]
+    return ref.flatten(1)
+
+
+FORMS = [(64, 2, 4, 1), (128, 2, 4, 1), (256, 1, 6, 1), (256, 2, 6, 2), (64, 1, 5, 6), (128, 1, 8, 12), (256, 1, 6, 12),
+         (128, 1, 16, 16)]
+
+
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("above", (16, 20, 24))
+@pytest.mark.parametrize("d,heads,group,rows", FORMS)
+def test_small_weights_beside_a_dominant_key(d, heads, group, rows, above, dtype):
+    """A first key that carries nearly all of the weight and has V = 0: the
+    result is made of weights of 2^-16 .. 2^-24 of the largest.  A weight is
+    kept to 2^-43 of the largest, so these to 2^-19 and, over 3,000 of them
+    with roundings to either side, to 2^-19 / sqrt(3) against their sum;
+    scores of up to 24 log2 units carry 2^-20 each."""
+    for n, at in ((3000, 0), (3000, 1500)):
+        bt, q = _with_sink(n, above, d, heads, group, rows, dtype, 0.0, at=at)
+        out = run_attention(bt, q, d ** -0.5)
+        r = gate_parity(out.cpu().numpy(), _all_rows_ref(bt, q).cpu().numpy())
+        assert r is None, (n, at, r)
+
+
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("d,heads,group,rows", FORMS)
+def test_values_that_are_all_one(d, heads, group, rows, dtype):
+    """Whatever the weights, their mean of ones is one: numerator and sum hold
+    the same weights.  131,000 of 2^-22 of the largest are 4 % of the sum."""
+    bt, q = _with_sink(131000, 22, d, heads, group, rows, dtype, 1.0, v_rest=1.0)
+    out = run_attention(bt, q, d ** -0.5)
+    assert (out - 1).abs().max() <= 4e-6  # fp32 sums of 131,000 weights in a few hundred steps each
 
 
 # --------------------------------------------------------- streams, repeats
