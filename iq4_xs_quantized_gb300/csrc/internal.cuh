@@ -607,6 +607,24 @@ __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wa
 __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// What the preceding grid may have written, read behind griddep_wait: by a
+// coherent load.  That grid ran while this one was resident, so a load of the
+// read-only kind (__ldg, or what the compiler makes of a const __restrict__
+// pointer) may find what a line held before.
+__device__ __forceinline__ uint32_t ld_fresh(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int ld_fresh(const int* p) { return (int)ld_fresh(reinterpret_cast<const uint32_t*>(p)); }
+__device__ __forceinline__ float ld_fresh(const float* p) {
+    return __uint_as_float(ld_fresh(reinterpret_cast<const uint32_t*>(p)));
+}
+__device__ __forceinline__ uint4 ld_fresh(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 __device__ __forceinline__ void prefetch_tmap(const void* tmap) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
 }

@@ -50,8 +50,8 @@ __device__ __forceinline__ int dp4a(uint32_t a, uint32_t b, int c) {
 // extents (checked in the bounds-checked build) follow from N, K, M, ldy.
 template <int MC, int WT, int kIters>
 __device__ __forceinline__ void dp4a_rows(const uint8_t* __restrict__ w, int64_t N, int64_t K,
-                                          const int8_t* __restrict__ qs,
-                                          const __half2* __restrict__ ds, int64_t M,
+                                          const int8_t* qs,
+                                          const __half2* ds, int64_t M,
                                           float* __restrict__ y, int64_t ldy, int64_t n0, int lane,
                                           bool waited, const Bc& bc) {
     const int64_t nsub = K / kSub;
@@ -100,9 +100,10 @@ __device__ __forceinline__ void dp4a_rows(const uint8_t* __restrict__ w, int64_t
                         bc_global(bc, qs + (m0 + mi) * K + s * kSub, kSub, qs, qs_ext, kBcDp4aQs) &&
                         bc_global(bc, ds + (m0 + mi) * nsub + s, 4, ds, ds_ext, kBcDp4aDs)) {
                         const uint4* qp = reinterpret_cast<const uint4*>(qs + (m0 + mi) * K + s * kSub);
-                        qa[mi][0] = __ldg(qp);
-                        qa[mi][1] = __ldg(qp + 1);
-                        dx[mi] = __low2float(__ldg(ds + (m0 + mi) * nsub + s));
+                        qa[mi][0] = ld_fresh(qp);
+                        qa[mi][1] = ld_fresh(qp + 1);
+                        const uint32_t d2 = ld_fresh(reinterpret_cast<const uint32_t*>(ds + (m0 + mi) * nsub + s));
+                        dx[mi] = __half2float(__ushort_as_half((unsigned short)(d2 & 0xFFFFu)));
                     } else {
                         qa[mi][0] = qa[mi][1] = make_uint4(0, 0, 0, 0);
                         dx[mi] = 0.f;
@@ -167,7 +168,7 @@ __device__ __forceinline__ void dp4a_rows(const uint8_t* __restrict__ w, int64_t
 template <int MC, int WT, int S>  // activation rows per pass, weight format, launch shape
 __global__ void __launch_bounds__(kDp4aThreads, ctas_per_sm<MC, S>())
     matmul_dp4a_kernel(const uint8_t* __restrict__ w, int64_t N, int64_t K,
-                       const int8_t* __restrict__ qs, const __half2* __restrict__ ds, int64_t M,
+                       const int8_t* qs, const __half2* ds, int64_t M,
                        float* __restrict__ y, int64_t ldy, int* err) {
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -193,8 +194,8 @@ __global__ void __launch_bounds__(kDp4aThreads, ctas_per_sm<MC, S>())
 template <bool kNarrow, int WT>
 __global__ void __launch_bounds__(kDp4aThreads, kNarrow ? 3 : 2)
     matmul_dp4a_grouped_kernel(const uint8_t* __restrict__ w, int64_t expert_stride, int64_t G,
-                               int64_t N, int64_t K, const int8_t* __restrict__ qs,
-                               const __half2* __restrict__ ds, const int32_t* __restrict__ row_offsets,
+                               int64_t N, int64_t K, const int8_t* qs,
+                               const __half2* ds, const int32_t* row_offsets,
                                int64_t total_rows, float* __restrict__ y, int64_t ldy, int* err) {
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -212,8 +213,8 @@ __global__ void __launch_bounds__(kDp4aThreads, kNarrow ? 3 : 2)
         for (int j = 0; j < 4; ++j) {
             const int64_t e = base + 32 * j + lane;
             const bool in = e < G && bc_global(bc, row_offsets + e, 8, row_offsets, (G + 1) * 4, kBcDp4aOffsets);
-            lo[j] = in ? __ldg(row_offsets + e) : 0;
-            hi[j] = in ? __ldg(row_offsets + e + 1) : 0;
+            lo[j] = in ? ld_fresh(row_offsets + e) : 0;
+            hi[j] = in ? ld_fresh(row_offsets + e + 1) : 0;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

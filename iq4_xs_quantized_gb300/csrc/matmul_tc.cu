@@ -257,10 +257,10 @@ __device__ __forceinline__ void named_barrier_sync(int id, int count) {
 template <int MT, int WT, bool kPrep, bool kGrouped = false>
 __global__ void __launch_bounds__(TcCfg<MT, WT, kPrep>::kThreads, 1)
     matmul_tc_kernel(const __grid_constant__ CUtensorMap tmap_w,
-                     const __grid_constant__ CUtensorMap tmap_q, const __half* __restrict__ ds,
-                     const uint8_t* __restrict__ tc_op, int64_t M, int N, int K,
+                     const __grid_constant__ CUtensorMap tmap_q, const __half* ds,
+                     const uint8_t* tc_op, int64_t M, int N, int K,
                      float* __restrict__ y, int64_t ldy, int* err, int skip_w_stage,
-                     const int32_t* __restrict__ row_offsets, int G) {
+                     const int32_t* row_offsets, int G) {
     using C = TcCfg<MT, WT, kPrep>;
     constexpr int kDecGroups = C::kDecGroups, kDecWarps = C::kDecWarps;
     constexpr int kMmaWarp0 = C::kMmaWarp0, kMmaWarp1 = C::kMmaWarp1;
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(TcCfg<MT, WT, kPrep>::kThreads, 1)
                 const int e = e0 + lane;
                 int tiles = 0;
                 if (e < G && bc_global(bc, row_offsets + e, 8, row_offsets, (int64_t)(G + 1) * 4, kBcTcRows)) {
-                    const int lo = __ldg(row_offsets + e), hi = __ldg(row_offsets + e + 1);
+                    const int lo = ld_fresh(row_offsets + e), hi = ld_fresh(row_offsets + e + 1);
                     tiles = hi > lo ? (hi - lo + MT - 1) / MT : 0;
                 }
                 int incl = tiles;  // inclusive prefix sum over the 32 experts
@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(TcCfg<MT, WT, kPrep>::kThreads, 1)
         __syncthreads();
         gexp = grp[0];
         if (gexp < 0) return;  // past the layer's last tile (whole CTA; no cluster)
-        row_lo = __ldg(row_offsets + gexp) + grp[1] * MT;
-        row_hi = __ldg(row_offsets + gexp + 1);
+        row_lo = ld_fresh(row_offsets + gexp) + grp[1] * MT;
+        row_hi = ld_fresh(row_offsets + gexp + 1);
         if (!bc_range(bc, row_lo, row_hi - row_lo, M, kBcTcRows)) return;  // offsets outside the rows of y
     }
     const int pairs = K / kPairK;
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(TcCfg<MT, WT, kPrep>::kThreads, 1)
                 const int64_t row = row_lo + e / kBStageSubs;
                 const uint32_t* dp = ds32 + row * K32 + sub0 + e % kBStageSubs;
                 dsv[k] = (e < kBStageSubs * MT && row < row_hi && bc_global(bc, dp, 4, ds, M * K32 * 4, kBcTcDs))
-                             ? __ldg(dp)
+                             ? ld_fresh(dp)
                              : 0u;
             }
             if (ok && bs >= C::kNX)
@@ -796,6 +796,8 @@ __global__ void __launch_bounds__(TcCfg<MT, WT, kPrep>::kThreads, 1)
         int nswitch = 0;
         if constexpr (kPrep) {
             griddep_wait();
+            // (plain loads: coherent, as tc_op is not __restrict__; ordered as
+            // ld_fresh orders them they cost 2-3 % at M = 64, 30.4 for 29.5 us)
             span_scale = reinterpret_cast<const float*>(tc_op + tc_qh_bytes(M, K)) +
                          (int64_t)z * tc_num_spans(K) * MT + c0;
             if (t < kMH) {

@@ -199,8 +199,8 @@ __device__ __forceinline__ bool consumers_any(bool v) {
 template <int NT, int T, int kOcc, bool kGrouped, bool kB18 = false>
 __global__ void __launch_bounds__(kMmaThreads, kOcc)
     matmul_mma_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_q,
-                      const __half* __restrict__ ds, int64_t M, int N, int K, float* __restrict__ y, int64_t ldy,
-                      int* err, const int32_t* __restrict__ row_offsets, int G, int wt, int skip_stage) {
+                      const __half* ds, int64_t M, int N, int K, float* __restrict__ y, int64_t ldy,
+                      int* err, const int32_t* row_offsets, int G, int wt, int skip_stage) {
     using C = MmaCfg<NT, T, kOcc, kB18, kGrouped>;
     constexpr int kTMax = T, kMt = C::kMt, kSPW = C::kSPW, kRG = C::kRG, R = C::kR, NS = C::kNS;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(kMmaThreads, kOcc)
                         const int e = e0 + lane;
                         const bool in = e < G && bc_global(bc, row_offsets + e, 8, row_offsets,
                                                            (int64_t)(G + 1) * 4, kBcMmaOffsets);
-                        lo = in ? __ldg(row_offsets + e) : 0;
-                        hi = in ? __ldg(row_offsets + e + 1) : 0;
+                        lo = in ? ld_fresh(row_offsets + e) : 0;
+                        hi = in ? ld_fresh(row_offsets + e + 1) : 0;
                         // offsets outside the rows of y: the expert is skipped
                         if (hi > lo && !bc_range(bc, lo, (int64_t)hi - lo, M, kBcMmaRows)) hi = lo;
                         cnt = hi > lo ? ntx * ((hi - lo + kMt - 1) / kMt) : 0;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kMmaThreads, kOcc)
                 const int64_t sub = (int64_t)pair * kSubPerPair + sub_w + e % kSPW;
                 dxv[k] = (e < C::kDxFloats && m < rhi && sub < K32 &&
                           bc_global(bc, ds32 + m * K32 + sub, 4, ds, M * K32 * 4, kBcMmaDs))
-                             ? __ldg(ds32 + m * K32 + sub)
+                             ? ld_fresh(ds32 + m * K32 + sub)
                              : 0u;
             }
         };

@@ -26,7 +26,7 @@ static_assert(kElemsPerCta == kScaleSpan, "one CTA per activation scale span");
 // are either all inside K or all outside it.
 template <bool kTc>
 __global__ void __launch_bounds__(kQuantThreads)
-    quantize_q8_1_kernel(const float* __restrict__ x, int64_t M, int64_t K, int64_t ldx,
+    quantize_q8_1_kernel(const float* x, int64_t M, int64_t K, int64_t ldx,
                          int8_t* __restrict__ qs, __half2* __restrict__ ds,
                          uint4* __restrict__ qh, float* __restrict__ spanscale, int MT, int* err) {
     // The next grid (the matmul) may launch at once: it reads qs/ds only
