@@ -124,7 +124,7 @@ def run(layers=2, sequences=3, tree=8, steps=4, prompt=37, seed=0, dtype=torch.f
     """Decodes `sequences` sequences by drafted trees and again token by token;
     returns the last token's hidden states of both, [sequences, hidden]."""
     rng = np.random.default_rng(seed)
-    most = prompt + steps * tree + tree
+    most = prompt + 5 * (sequences - 1) + steps * tree + tree  # the last prompt is the longest
     width = -(-most // 16) + 1
     dec = Decoder(layers=layers, slots=sequences + 1, width=width, pages=(sequences + 2) * width, dtype=dtype, seed=seed)
     # prompts, and what each sequence comes to hold

@@ -39,3 +39,15 @@ def test_trees_end_where_single_tokens_end(sequences, tree, steps, dtype):
     # and not because nothing is attended to: another text ends elsewhere
     other, _ = verify_step.run(2, sequences, tree, steps, seed=sequences + tree + 1, dtype=dtype)
     assert float(((by_trees - other).norm(dim=1) / by_tokens.norm(dim=1)).min()) > 0.1
+
+
+@pytest.mark.gpu
+def test_many_sequences_fit_their_tables():
+    """Prompts grow by five tokens a sequence: the table has to hold the last one's."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from iq4_xs_quantized_gb300 import build
+    build.build()
+    by_trees, by_tokens = verify_step.run(1, 16, 3, 1, seed=4)
+    off = (by_trees - by_tokens).norm(dim=1) / by_tokens.norm(dim=1)
+    assert by_trees.shape[0] == 16 and float(off.max()) <= 1e-2, off
