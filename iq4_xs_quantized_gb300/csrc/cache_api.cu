@@ -9,6 +9,7 @@ namespace {
 constexpr int64_t kMaxRows = 32768;
 constexpr int64_t kMaxSequences = 65535;
 constexpr int64_t kMaxStride = int64_t(1) << 44;
+constexpr int64_t kMaxExtent = int64_t(1) << 59;  // elements of an axis
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline int from_cuda(cudaError_t e) { return e == cudaSuccess ? IQ4XS_OK : IQ4XS_ERR_CUDA; }
@@ -24,6 +25,10 @@ int view_cache(const iq4xs_kv_cache* c, CacheView* out) {
     const int64_t strides[4] = {c->layer_stride, c->page_stride, c->head_stride, c->slot_stride};
     for (int64_t s : strides)
         if (s < 0 || s > kMaxStride || s % 8) return IQ4XS_ERR_ARG;
+    // (offsets are 64-bit elements: the last one's may not pass them)
+    const int64_t last[4] = {c->layers - 1, c->pages - 1, c->heads - 1, c->page_size - 1};
+    for (int i = 0; i < 4; ++i)
+        if (last[i] > 0 && strides[i] > kMaxExtent / last[i]) return IQ4XS_ERR_ARG;
     if (!aligned(c->k, 16) || !aligned(c->v, 16)) return IQ4XS_ERR_ALIGN;
     out->k = static_cast<uint16_t*>(c->k);
     out->v = static_cast<uint16_t*>(c->v);
@@ -47,7 +52,7 @@ int view_batch(const iq4xs_kv_batch* b, BatchView* out) {
     if (!b) return IQ4XS_ERR_ARG;
     if (b->sequences < 0 || b->sequences > kMaxSequences) return IQ4XS_ERR_SHAPE;
     if (b->table_width < 1 || b->table_width > (1 << 20)) return IQ4XS_ERR_SHAPE;
-    if (b->table_stride < b->table_width) return IQ4XS_ERR_ARG;
+    if (b->table_stride < b->table_width || b->table_stride > kMaxStride) return IQ4XS_ERR_ARG;
     if (!b->row_offsets || (b->sequences > 0 && (!b->lens || !b->held || !b->page_table))) return IQ4XS_ERR_ARG;
     if (!aligned(b->row_offsets, 4) || !aligned(b->lens, 4) || !aligned(b->held, 4) || !aligned(b->page_table, 4))
         return IQ4XS_ERR_ALIGN;
@@ -79,7 +84,8 @@ int iq4xs_qk_norm_rope(const iq4xs_qk_norm_rope_args* a, const iq4xs_kv_cache* c
                                 a->k_head_stride, a->v_row_stride, a->v_head_stride};
     for (int64_t s : strides)
         if (s < 0 || s > kMaxStride || s % 4) return IQ4XS_ERR_ARG;
-    if (a->q_out_row_stride < a->q_heads * c.head_dim || a->q_out_row_stride % 8) return IQ4XS_ERR_ARG;
+    if (a->q_out_row_stride < a->q_heads * c.head_dim || a->q_out_row_stride > kMaxStride || a->q_out_row_stride % 8)
+        return IQ4XS_ERR_ARG;
     if (a->rope ? (a->rope_positions < 1 || a->rot_dim < 8) : a->rot_dim != 0) return IQ4XS_ERR_ARG;
     if (a->rot_dim % 8 || a->rot_dim > c.head_dim) return IQ4XS_ERR_SHAPE;
     if (a->interleaved != 0 && a->interleaved != 1) return IQ4XS_ERR_ARG;

@@ -99,6 +99,21 @@ def test_bad_attention_arguments(lib, change, want):
     assert lib.iq4xs_tree_attention(pack("<7qd4q", ATTN, **change), cache(), batch(), 0) == want
 
 
+def test_strides_whose_offsets_pass_64_bits(lib):
+    """A stride within its limit times its axis may pass 63 bits, and so may the
+    strides that had no limit."""
+    for change in (dict(pages=1 << 30, page_stride=1 << 43), dict(pages=(1 << 31) - 1, page_stride=1 << 32),
+                   dict(layers=65535, layer_stride=1 << 44), dict(heads=1024, head_stride=1 << 44, pages=1, layers=65535,
+                                                                  layer_stride=(1 << 44) - 8)):
+        for rc in calls(lib, cache(**change), batch()):
+            assert rc == B.ERR_ARG
+    wide = batch(table_stride=(1 << 44) + 1)
+    for rc in calls(lib, cache(), wide):
+        assert rc == B.ERR_ARG
+    assert lib.iq4xs_cache_release(wide, P, 8, P, 1, 0) == B.ERR_ARG
+    assert lib.iq4xs_qk_norm_rope(pack("<11qd10q", QK, q_out_row=(1 << 44) + 8), cache(), batch(), 0) == B.ERR_ARG
+
+
 def test_bad_page_arguments(lib):
     c, b = cache(), batch()
     f = lib.iq4xs_cache_reserve
