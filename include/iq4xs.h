@@ -644,7 +644,8 @@ int iq4xs_qk_norm_rope(const iq4xs_qk_norm_rope_args* args, const iq4xs_kv_cache
  * query head h reading key/value head h / (q_heads / heads).  A row that sees
  * nothing gets zeros.  A position that a row does not see has no influence on
  * it, whatever its K and V hold (NaN and infinities included); slots behind a
- * sequence's end are never used.
+ * sequence's end are never used.  A NaN or an infinity in the V of a position
+ * that it does see makes that channel of it NaN or infinite.
  *   q          [rows][q_heads][head_dim] in the cache's type, rows
  *              q_row_stride elements apart (a multiple of 8), 16-byte aligned.
  *   out        fp32 [rows][out_row_stride >= q_heads*head_dim], 16-byte
@@ -655,8 +656,8 @@ int iq4xs_qk_norm_rope(const iq4xs_qk_norm_rope_args* args, const iq4xs_kv_cache
  *   workspace  iq4xs_tree_attention_workspace_bytes(...) bytes, 32-byte
  *              aligned, of any content; one per stream.
  * Scores and softmax statistics are fp32.  A weight is kept to 2^-22 of itself
- * or 2^-43 of the row's largest one, whichever is more, rounded to nearest
- * (fp16 cache), or to 24 bits (bf16).  Results are the same from run to run.
+ * or 2^-42 of the row's largest one, whichever is more (fp16 cache), or to 24
+ * bits (bf16).  Results are the same from run to run.
  * 1 <= rows <= 32768; q_heads a multiple of the cache's heads, at most 1024.
  */
 typedef struct {

@@ -388,13 +388,14 @@ __device__ __forceinline__ float2 mask2(float2 a, uint32_t mask) {
 }
 // Two weights as the sum of kN packed 16-bit parts, largest first; the last
 // one is kept times 2^kLastShift, and so is what it makes of V until it meets
-// the others.  fp16: the nearest 11 bits, down to the subnormals' 2^-24, and
-// what is left of them (exact in fp32) times 2^12: 22 bits of every weight from
-// 2^-14 on and 2^-37 of smaller ones, 2^-43 of the row's largest, rounded to
-// nearest both times.  (Without the factor what is left of a weight below 2^-14
-// falls under half of 2^-24 and is lost: beside one key that outweighs the
-// others by 2^20 the result was off by 2e-5, by 2^24 by 7e-4.)  bf16: 8 + 8 +
-// 8 bits cut off, the whole value.
+// the others.  fp16: 11 bits cut off, down to the subnormals' 2^-24, and what
+// is left of the stored value (exact in fp32) times 2^12: 22 bits of every
+// weight from 2^-14 on and 2^-36 of smaller ones, 2^-42 of the row's largest.
+// (Without the factor what is left of a weight below 2^-14 falls under half of
+// 2^-24 and is lost: beside one key that outweighs the others by 2^20 the
+// result was off by 2e-5, by 2^24 by 7e-4.)  bf16: 8 + 8 + 8 bits cut off, the
+// whole value.  No part is negative: an infinity among the V that a row sees
+// times a negative part would meet itself with the other sign.
 template <class T>
 struct Parts;
 template <>
@@ -402,7 +403,7 @@ struct Parts<KvF16> {
     static constexpr int kN = 2, kLastShift = 12;
     static __device__ __forceinline__ void split(float2 a, uint32_t* out) {
         constexpr float kUp = 1 << kLastShift;
-        out[0] = KvF16::pack(a.x, a.y);
+        out[0] = KvF16::pack_rz(a.x, a.y);
         const float2 r = fma2(KvF16::unpack(out[0]), make_float2(-1.f, -1.f), a);
         out[1] = KvF16::pack(r.x * kUp, r.y * kUp);
     }

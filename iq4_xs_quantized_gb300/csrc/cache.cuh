@@ -66,6 +66,11 @@ struct KvF16 {
         const __half2 h = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
+    static __device__ __forceinline__ uint32_t pack_rz(float lo, float hi) {  // cut off
+        uint32_t w;
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+        return w;
+    }
     static __device__ __forceinline__ float2 unpack(uint32_t w) {
         return __half22float2(*reinterpret_cast<const __half2*>(&w));
     }

@@ -275,8 +275,8 @@ FORMS = [(64, 2, 4, 1), (128, 2, 4, 1), (256, 1, 6, 1), (256, 2, 6, 2), (64, 1, 
 def test_small_weights_beside_a_dominant_key(d, heads, group, rows, above, dtype):
     """A first key that carries nearly all of the weight and has V = 0: the
     result is made of weights of 2^-16 .. 2^-24 of the largest.  A weight is
-    kept to 2^-43 of the largest, so these to 2^-19 and, over 3,000 of them
-    with roundings to either side, to 2^-19 / sqrt(3) against their sum;
+    kept to 2^-42 of the largest, so these to 2^-18 and, over 3,000 of them
+    with roundings to either side, to 2^-18 / sqrt(3) against their sum;
     scores of up to 24 log2 units carry 2^-20 each."""
     for n, at in ((3000, 0), (3000, 1500)):
         bt, q = _with_sink(n, above, d, heads, group, rows, dtype, 0.0, at=at)
@@ -293,6 +293,35 @@ def test_values_that_are_all_one(d, heads, group, rows, dtype):
     bt, q = _with_sink(131000, 22, d, heads, group, rows, dtype, 1.0, v_rest=1.0)
     out = run_attention(bt, q, d ** -0.5)
     assert (out - 1).abs().max() <= 4e-6  # fp32 sums of 131,000 weights in a few hundred steps each
+
+
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("d,heads,group,rows", FORMS)
+def test_infinities_that_all_rows_see(d, heads, group, rows, dtype):
+    """Infinities in the context's V reach their channels, which are not finite
+    then, and no other one.  fp16: a weight's parts are not negative, so they
+    stay infinities unless a second part is zero (one weight in 2^13; 12 here)
+    or a row is copied, with zero weights for other copies' keys (17-64 rows)."""
+    bt = Batch([900], [rows], heads=heads, d=d, dtype=dtype, garbage=None)
+    q = _q(bt, heads * group)
+    at = [100 + 37 * i for i in range(12)]
+    for i in at:
+        page, slot = int(bt.table_n[0][i // 16]), i % 16
+        bt.cache.k[0, page, :, slot] = 0  # (score 0: no maximum, so that its weight is no power of two)
+        bt.cache.v[0, page, :, slot, 1] = float("inf")
+        bt.cache.v[0, page, :, slot, d - 2] = -float("inf")
+    out = run_attention(bt, q, d ** -0.5).unflatten(1, (heads * group, d))
+    assert not bool(torch.isfinite(out[..., 1]).any()) and not bool(torch.isfinite(out[..., d - 2]).any())
+    if dtype == torch.float16 and not 16 < rows * group <= 64:
+        assert torch.isposinf(out[..., 1]).float().mean() >= 0.9 and torch.isneginf(out[..., d - 2]).float().mean() >= 0.9
+    out[..., 1] = out[..., d - 2] = 0
+    for i in at:
+        page, slot = int(bt.table_n[0][i // 16]), i % 16
+        bt.cache.v[0, page, :, slot, 1] = bt.cache.v[0, page, :, slot, d - 2] = 0
+    ref = _all_rows_ref(bt, q).unflatten(1, (heads * group, d))
+    ref[..., 1] = ref[..., d - 2] = 0
+    r = gate_parity(out.flatten(1).cpu().numpy(), ref.flatten(1).cpu().numpy())
+    assert r is None, r
 
 
 # --------------------------------------------------------- streams, repeats
