@@ -658,6 +658,10 @@ int iq4xs_qk_norm_rope(const iq4xs_qk_norm_rope_args* args, const iq4xs_kv_cache
  * Scores and softmax statistics are fp32.  A weight is kept to 2^-22 of itself
  * or 2^-42 of the row's largest one, whichever is more (fp16 cache), or to 24
  * bits (bf16).  Results are the same from run to run.
+ * Speed: the kernel's form follows rows / sequences, with sequences that have
+ * no new token counted, one form for the whole batch; and a table of at most
+ * 2048 tokens (table_width * page_size) says that no sequence is longer, which
+ * short batches gain from: pass a view of the table's first columns.
  * 1 <= rows <= 32768; q_heads a multiple of the cache's heads, at most 1024.
  */
 typedef struct {

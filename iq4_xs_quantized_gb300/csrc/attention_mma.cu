@@ -27,6 +27,8 @@
 // busy, the warps wait for K and V).  64 channels and pages of 16 slots stop at
 // about 4.2 TB/s: a copy is 2 KB there, and the copy unit's rate binds.  One
 // token over 517 cached, 24 heads over 4 of 256: 9.0 us by clusters, latency.
+// 16 rows at 128 channels, in two sets, do not fit the registers: ptxas spills
+// up to 174 bytes a thread there (the other forms at most 42).
 #include "attention.cuh"
 
 namespace iq4xs {

@@ -11,9 +11,12 @@
 // wait for one another: row, length, page, data.
 //
 // Measured: fork of 4 parents of 700 tokens by 8, 64 layers of 4 heads of 256,
-// 482 MB in 80.8 us, 5.97 TB/s (88 % of a copy's rate); commit of 7 of 16
-// tokens of 32 sequences in the same cache, 42 MB in 19.2 us (2.2 TB/s), of 4
-// tokens of one sequence in 8 layers 5.9 us; fork of one by two there 10.9 us.
+// 482 MB in 80.5 us, 5.99 TB/s (88 % of a copy's rate); commit of 7 of 16
+// tokens of 32 sequences in the same cache, 42 MB in 17.5-19.4 us (2.2-2.4
+// TB/s), of 4 tokens of one sequence in 8 layers 5.6 us; fork of one by two
+// there 10.7 us.  Long ones stay far off: every thread of a commit walks the
+// whole path (a chain of 512 tokens 69 us, of 8,000 1.05 ms), and a fork's books
+// are one CTA's (one child of 100,000 tokens in pages of 16: 42 us).
 #include "cache.cuh"
 
 namespace iq4xs {
@@ -298,8 +301,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 }
 
 // -------------------------------------------------------------------- fork
-// A child's request: 0 or 1 page; status 2 where its indices or counts are
-// out of order, 1 where the table is too narrow for the parent's pages.
+// A child's full pages to share and pages to take, 0 or 1; 2 where its indices
+// or counts are out of order, else 0.
 __device__ int fork_state(const BatchView& b, int parent, int child, int shift, int* full, int* take) {
     *full = *take = 0;
     if (parent < 0 || parent >= b.sequences || child < 0 || child >= b.sequences || parent == child) return 2;

@@ -610,7 +610,8 @@ __device__ __forceinline__ void griddep_launch_dependents() {
 // What the preceding grid may have written, read behind griddep_wait: by a
 // coherent load.  That grid ran while this one was resident, so a load of the
 // read-only kind (__ldg, or what the compiler makes of a const __restrict__
-// pointer) may find what a line held before.
+// pointer) may find what a line held before, and nothing keeps it behind the
+// wait.
 __device__ __forceinline__ uint32_t ld_fresh(const uint32_t* p) {
     uint32_t v;
     asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
