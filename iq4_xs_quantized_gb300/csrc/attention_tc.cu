@@ -24,13 +24,13 @@
 // core (1 + parts products of 128 x tile x D) and the softmax.
 //
 // Measured: a tree of 64 tokens over 131,071, 24 heads over 4 of 256, fp16:
-// 238 us a call in a hundred from idle, 257 in long runs, where the power cap
-// lowers the clock (206 GFLOP counting the output product once, 0.8-0.87
+// 238 us a call in a hundred from idle, 257-268 in long runs, where the power
+// cap lowers the clock (206 GFLOP counting the output product once, 0.8-0.87
 // PFLOP/s); prompt chunks of 2 x 512 over 8,000, 32 heads over 8 of 128, bf16:
 // 182 us.  The tensor pipe is 60 % and 52 % busy; a 64-key tile of the former
-// takes about 2,100 cycles of the softmax warps (scores and maximum 250, the exchange 200,
-// weights 600: exponentials at 16 a cycle and SM and the parts' shuffles; O
-// 600, where tensor memory is read at about 220 bytes a cycle), 1,536 of them
+// takes about 2,100 cycles of the softmax warps (scores and maximum 250, the
+// exchange 200, weights 600: exponentials at 16 a cycle and SM and the parts'
+// shuffles; O 600, where tensor memory is read at about 220 bytes a cycle), 1,536 of them
 // under products.  Measured as well: 16 softmax warps, no faster (tree 250,
 // chunk 188 us, 20 rows over 20k 61 against 54); T over four tiles before O
 // takes it, 224 against 230 us for the tree, 134 against 122 for 64 rows over
