@@ -404,7 +404,7 @@ def _plain_rule(st):
 def _own_rule(st):
     from iq4_xs_quantized_gb300 import binding as B
     B.iq4xs_delta_rule(st["q"], st["k"], st["v"], st["g"], st["beta"], st["scale"], st["out"], st["state"], 0,
-                       st["batch"], u=st["u"], tree_mask=st["mask"])
+                       st["batch"], u=st["u"], tree_mask=st["mask"], max_rows=st["t_max"])
     return {"out": st["out"], "s": st["s"]} if st["u"] is None else {"out": st["out"], "u": st["u"]}
 
 
