@@ -731,6 +731,206 @@ int iq4xs_cache_release(const iq4xs_kv_batch* batch, int32_t* refs, int64_t page
 int iq4xs_cache_copy_pages(const iq4xs_kv_cache* cache, const int32_t* src, const int32_t* dst, int64_t count,
                            int64_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The recurrent layers of the same step: layers whose memory is not a cache of
+ * keys and values but a matrix S of every value head, moved by the gated delta
+ * rule.  The calls mirror the attention side's: one that makes the operands
+ * from the projection (iq4xs_delta_inputs), one that reads the memory
+ * (iq4xs_delta_rule), one that keeps a verified path (iq4xs_delta_commit).
+ *
+ * State.  Element (layer, slot, head, i, j) of S is at
+ *   layer*s_layer_stride + slot*s_slot_stride + (head*key_dim + i)*value_dim + j
+ * in fp32; the last three inputs of the convolution, oldest first, at
+ *   layer*conv_layer_stride + slot*conv_slot_stride + t*channels + c,
+ * channels = 2*key_heads*key_dim + heads*value_dim (conv may be NULL where no
+ * call needs it).  Strides in elements, multiples of 4, no overlap; s, conv
+ * 16-byte aligned.  Value head h goes with key head h / (heads / key_heads).
+ * key_dim and value_dim 64 or 128; heads a multiple of key_heads, at most 1024.
+ * Sequence s of a batch has slot slot_of[s], or s where slot_of is NULL (device
+ * memory; slots of one batch are distinct).  A sequence with lens[s] == 0 has
+ * an empty state, whatever its slot holds.  Of the batch these calls read
+ * row_offsets and lens only.
+ */
+typedef struct {
+    float* s;
+    float* conv;
+    const int32_t* slot_of;
+    int64_t layers, slots, key_heads, heads, key_dim, value_dim;
+    int64_t s_layer_stride, s_slot_stride, conv_layer_stride, conv_slot_stride;
+} iq4xs_delta_state;
+
+/*
+ * From the projection's fp32 output to the rule's input, one launch.
+ *   y[c] = silu(sum_j conv_weight[c][j] x_j[c]), x_3 the row's own input, x_2
+ *   that of its parent, and so on (before the first: the state's inputs);
+ *   q, k  every head of y's first two blocks / sqrt(sum y^2 + eps);  v  the rest;
+ *   g = -exp(a_log) softplus(a + dt_bias);  beta = sigmoid(b).
+ * Computed in fp32, q, k and v rounded once to `dtype` (iq4xs_kv_dtype).
+ *   x           fp32 [rows][channels = q heads, k heads, v heads], 16-byte
+ *               aligned, rows x_row_stride elements apart (a multiple of 4).
+ *   conv_weight fp32 [channels][4], 16-byte aligned.
+ *   a, b        fp32 [rows][heads], rows a_row_stride, b_row_stride apart.
+ *   a_log, dt_bias  fp32 [heads].
+ *   q, k, v     [rows][heads][dim], rows at the given strides (multiples of 8),
+ *               16-byte aligned: views of one buffer will do.
+ *   g, beta     fp32 [rows][heads].
+ *   tree_mask   as in iq4xs_tree_attention, of a tree: row t's parent is the last
+ *               new token before t that it sees; NULL: chains.
+ *   advance     1: the state's inputs become the last three of the sequence's
+ *               rows (chains only).  0: they stay (a later commit moves them).
+ * 1 <= rows <= 32768.
+ */
+typedef struct {
+    const float* x;
+    int64_t x_row_stride;
+    const float* conv_weight;
+    const float* a;
+    const float* b;
+    int64_t a_row_stride, b_row_stride;
+    const float* a_log;
+    const float* dt_bias;
+    double eps;
+    void* q;
+    void* k;
+    void* v;
+    int64_t q_row_stride, k_row_stride, v_row_stride, dtype;
+    float* g;
+    float* beta;
+    const uint64_t* tree_mask;
+    int64_t mask_words, advance;
+    int64_t rows, layer;
+} iq4xs_delta_inputs_args;
+int iq4xs_delta_inputs(const iq4xs_delta_inputs_args* args, const iq4xs_delta_state* state,
+                       const iq4xs_kv_batch* batch, int64_t stream);
+
+/*
+ * The gated delta rule over every sequence's new tokens, from its state S:
+ *   S <- e^g S;  u = beta (v - S^T k);  S <- S + k u^T;  out = scale S^T q.
+ * With u == NULL the rows are chains and the state moves on over all of them.
+ * With u the state stays and every row starts from its parent's (tree_mask as
+ * above; NULL: a chain): what verification needs; u keeps what the commit of an
+ * accepted path adds.  A sequence then has at most 64 rows.
+ *   q, k, v   as iq4xs_delta_inputs writes them.
+ *   g, beta   fp32 [rows][heads]; g, a logarithm, is 0 or below.
+ *   out       fp32 [rows][out_row_stride >= heads*value_dim], 16-byte aligned,
+ *             out_row_stride a multiple of 4: what iq4xs_linear takes.
+ *   u         fp32 [rows][heads][value_dim], 16-byte aligned, or NULL.
+ *   max_rows  no sequence has more rows (one that does is skipped,
+ *             IQ4XS_ERR_DATA); 0: not known.
+ * Rows of no sequence are not written.  A row has no influence on rows that do
+ * not come from it, whatever it holds.  S, sums and products are kept to fp32
+ * (long runs of rows in two fp16 parts with a common exponent a column, 2^-22
+ * of a value or 2^-38 of the column's largest, whichever is more).  Results are
+ * the same from run to run.
+ * 1 <= rows <= 32768.
+ */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_row_stride, k_row_stride, v_row_stride, dtype;
+    const float* g;
+    const float* beta;
+    double scale;
+    float* out;
+    int64_t out_row_stride;
+    float* u;
+    const uint64_t* tree_mask;
+    int64_t mask_words, max_rows;
+    int64_t rows, layer;
+} iq4xs_delta_rule_args;
+int iq4xs_delta_rule(const iq4xs_delta_rule_args* args, const iq4xs_delta_state* state, const iq4xs_kv_batch* batch,
+                     int64_t stream);
+
+/*
+ * After verification, all layers in one launch: sequence s keeps the new tokens
+ * paths[s][0..accepted[s]) (as iq4xs_cache_commit, which comes after: it may
+ * move lens, by which an empty state is known):
+ *   S <- e^{g_n} (... e^{g_1} S + k_1 u_1^T ...) + k_n u_n^T over the path,
+ * and the convolution's inputs become the path's last three.
+ *   k  [layers][rows][key_heads][key_dim] of `dtype`, rows k_row_stride, layers
+ *      k_layer_stride apart (multiples of 8), 16-byte aligned;
+ *   g  fp32 [layers][rows][heads];  u  fp32 [layers][rows][heads][value_dim],
+ *      16-byte aligned; layers g_layer_stride, u_layer_stride apart;
+ *   x  fp32 [layers][rows][channels], rows x_row_stride, layers x_layer_stride
+ *      apart (multiples of 4), 16-byte aligned; NULL where state->conv is.
+ * A path out of order leaves its sequence as it is (IQ4XS_ERR_DATA).
+ */
+typedef struct {
+    const void* k;
+    int64_t k_row_stride, k_layer_stride, dtype;
+    const float* g;
+    int64_t g_layer_stride;
+    const float* u;
+    int64_t u_layer_stride;
+    const float* x;
+    int64_t x_row_stride, x_layer_stride;
+    const int32_t* paths;
+    int64_t path_width;
+    const int32_t* accepted;
+    int64_t rows;
+} iq4xs_delta_commit_args;
+int iq4xs_delta_commit(const iq4xs_delta_commit_args* args, const iq4xs_delta_state* state,
+                       const iq4xs_kv_batch* batch, int64_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The end of a verify step: the target's probabilities, and which drafted
+ * tokens they accept.
+ *
+ * probs[r][i] = e^{(l_i - max l) / T} / sum_j e^{(l_j - max l) / T}, T =
+ * temperature[r] (NULL: 1); T not above 0: 1 at the first of the largest
+ * logits, else 0.  -inf logits get 0; a row of nothing else is all zeros; a row
+ * with a NaN (or, T above 0, with +inf) is all NaN.
+ *   logits, probs  fp32 [rows][vocab], rows logits_stride, probs_stride elements
+ *                  apart, 4-byte aligned (in place will do); rows 1..32768,
+ *                  vocab 1..2^20.
+ */
+int iq4xs_token_probs(const float* logits, int64_t logits_stride, int64_t rows, int64_t vocab,
+                      const float* temperature, float* probs, int64_t probs_stride, int64_t stream);
+
+/*
+ * Speculative acceptance by given random numbers.  Sequence s's rows are a
+ * drafted tree (or a chain, tree_mask NULL; parents as above): row 0 is the
+ * last token kept before, probs[row] the target's distribution of the token
+ * behind a row, tokens[row] the row's token.  From row 0 on, the children of the
+ * row reached, n, are tried in rising order, r = probs[n] and m = 1 at first:
+ *   child c is accepted if accept_u[c] m q(x) < r(x), x = tokens[c], and n = c;
+ *   else r <- max(r - m q, 0), m <- sum r.
+ * q = draft_probs[n], the distribution that n's children were drawn from; or,
+ * with draft_probs NULL (drafts that were not drawn), q(i) = [i = x], where the
+ * sum is 1 less the tokens rejected.  When no child is left, next[s] is the
+ * first i with r_0 + ... + r_i > draw_u[s] sum r (sum r = 0: from probs[n]; that
+ * 0 too: -1); the same when the path is full.  Values are taken as exact and sums kept to 2^-61, so that results
+ * do not depend on timing.  A probability is taken as within 0..1 (NaN: 0).
+ *   probs, draft_probs  fp32 [rows][vocab], rows probs_stride, draft_stride apart
+ *   tokens      int32 [rows]; one outside 0..vocab-1 is never accepted
+ *   accept_u    fp32 [rows];  draw_u  fp32 [sequences], in [0, 1)
+ *   paths       int32 [sequences][path_width]: the rows accepted, row 0 first, as
+ *               iq4xs_cache_commit takes them; zeros behind.  accepted int32
+ *               [sequences] their number, at most path_width.
+ *   next        int32 [sequences]; a sequence without rows: accepted 0, next -1.
+ * rows 1..32768, at most 1024 of a sequence (more: IQ4XS_ERR_DATA, accepted 0).
+ */
+typedef struct {
+    const float* probs;
+    int64_t probs_stride;
+    const float* draft_probs;
+    int64_t draft_stride;
+    const int32_t* tokens;
+    const uint64_t* tree_mask;
+    int64_t mask_words;
+    const float* accept_u;
+    const float* draw_u;
+    int64_t rows, vocab;
+    int32_t* paths;
+    int64_t path_width;
+    int32_t* accepted;
+    int32_t* next;
+} iq4xs_verify_drafts_args;
+int iq4xs_verify_drafts(const iq4xs_verify_drafts_args* args, const iq4xs_kv_batch* batch, int64_t stream);
+
 /* Static string for a status code. */
 const char* iq4xs_status_string(int status);
 

@@ -108,6 +108,11 @@ def load(path: str | None = None):
         lib.iq4xs_cache_fork.argtypes = [cp, cp, i64, i64, i64, i64, i64, i64]
         lib.iq4xs_cache_release.argtypes = [cp, i64, i64, i64, i64, i64]
         lib.iq4xs_cache_copy_pages.argtypes = [cp, i64, i64, i64, i64]
+        lib.iq4xs_delta_inputs.argtypes = [cp, cp, cp, i64]
+        lib.iq4xs_delta_rule.argtypes = [cp, cp, cp, i64]
+        lib.iq4xs_delta_commit.argtypes = [cp, cp, cp, i64]
+        lib.iq4xs_token_probs.argtypes = [i64] * 8
+        lib.iq4xs_verify_drafts.argtypes = [cp, cp, i64]
         lib.iq4xs_status_string.argtypes = [ci]
         lib.iq4xs_status_string.restype = ctypes.c_char_p
         for name in ("iq4xs_quantize_q8_1", "iq4xs_matmul", "iq4xs_matmul_grouped", "iq4xs_matmul_grouped_path",
@@ -122,7 +127,9 @@ def load(path: str | None = None):
                      "iq4xs_last_device_error", "iq4xs_bounds_checked", "iq4xs_test_bounds_margin",
                      "iq4xs_mma_launch_config", "iq4xs_set_mma_launch_table",
                      "iq4xs_qk_norm_rope", "iq4xs_tree_attention", "iq4xs_cache_reserve", "iq4xs_cache_commit",
-                     "iq4xs_cache_fork", "iq4xs_cache_release", "iq4xs_cache_copy_pages"):
+                     "iq4xs_cache_fork", "iq4xs_cache_release", "iq4xs_cache_copy_pages",
+                     "iq4xs_delta_inputs", "iq4xs_delta_rule", "iq4xs_delta_commit", "iq4xs_token_probs",
+                     "iq4xs_verify_drafts"):
             getattr(lib, name).restype = ci
         if path is None:
             _lib = lib
@@ -629,6 +636,237 @@ def iq4xs_cache_copy_pages(cache: KVCache, src, dst, stream=None) -> None:
     _need_i32(fn, src=src, dst=dst)
     _need(src.numel() == dst.numel(), fn, "src and dst are of one length")
     rc = (_lib or load()).iq4xs_cache_copy_pages(cache.desc, src.data_ptr(), dst.data_ptr(), src.numel(), _stream(stream))
+    if rc:
+        _check(fn, rc)
+
+
+# --------------------------------------------------------------------------
+# The recurrent layers of a step, and its verification.
+# --------------------------------------------------------------------------
+def _need_device(fn: str, *tensors):
+    """All of them (None aside) on the current device, the one that a call runs on."""
+    at = {t.get_device() for t in tensors if t is not None}
+    if -1 in at or at != {torch.cuda.current_device() if _raw_device is None else _raw_device()}:
+        raise ValueError(f"{fn}: tensors must be on the current CUDA device")
+
+
+class DeltaState:
+    """The state of a step's recurrent layers over tensors of the caller's: s
+    fp32 [layers, slots, heads, key_dim, value_dim] and conv fp32 [layers,
+    slots, 3, channels] (or None where no call needs it), layers and slots at
+    any strides (multiples of 4), channels = 2 * key_heads * key_dim + heads *
+    value_dim.  Sequence s of a batch has slot s, or slot_of[s] (int32)."""
+
+    def __init__(self, s: torch.Tensor, conv: torch.Tensor | None, key_heads: int, slot_of: torch.Tensor | None = None):
+        _need(s.dtype is torch.float32 and (conv is None or conv.dtype is torch.float32), "DeltaState",
+              "s and conv must be float32", TypeError)
+        _need(s.dim() == 5, "DeltaState", "s is [layers, slots, heads, key_dim, value_dim]")
+        self.layers, self.slots, self.heads, self.key_dim, self.value_dim = s.shape
+        self.key_heads = key_heads
+        self.channels = 2 * key_heads * self.key_dim + self.heads * self.value_dim
+        _need(s.stride()[2:] == (self.key_dim * self.value_dim, self.value_dim, 1), "DeltaState",
+              "a slot's heads must be contiguous")
+        _need(conv is None or (conv.shape == (self.layers, self.slots, 3, self.channels) and
+                               conv.stride()[2:] == (self.channels, 1)), "DeltaState",
+              "conv is [layers, slots, 3, channels], a slot's inputs contiguous")
+        if slot_of is not None:
+            _need_i32("DeltaState", slot_of=slot_of)
+        _need(all(t is None or t.device == s.device for t in (conv, slot_of)), "DeltaState", "tensors of one device")
+        self.s, self.conv, self.slot_of = s, conv, slot_of
+        self.mapped = None if slot_of is None else slot_of.numel()
+        conv_strides = (0, 0) if conv is None else conv.stride()[:2]
+        self.desc = struct.pack("<13q", s.data_ptr(), _addr(conv), _addr(slot_of), self.layers, self.slots, key_heads,
+                                self.heads, self.key_dim, self.value_dim, *s.stride()[:2], *conv_strides)
+
+    def _check_batch(self, fn: str, batch: KVBatch):
+        if self.mapped is not None and self.mapped != batch.sequences:
+            raise ValueError(f"{fn}: slot_of is int32 [B]")
+
+
+def alloc_delta_state(layers: int, slots: int, key_heads: int, heads: int, key_dim: int, value_dim: int,
+                      device="cuda") -> DeltaState:
+    """A DeltaState over fresh tensors (contents undefined: a sequence of length 0 has an empty state)."""
+    channels = 2 * key_heads * key_dim + heads * value_dim
+    return DeltaState(torch.empty((layers, slots, heads, key_dim, value_dim), dtype=torch.float32, device=device),
+                      torch.empty((layers, slots, 3, channels), dtype=torch.float32, device=device), key_heads)
+
+
+_DELTA_INPUTS = struct.Struct("<9qd14q").pack
+_DELTA_RULE = struct.Struct("<9qd8q").pack
+_DELTA_COMMIT = struct.Struct("<15q").pack
+_VERIFY = struct.Struct("<15q").pack
+
+
+def _need_rows16(fn: str, m: int, what: str, t, heads: int, dim: int):
+    """t is 16-bit [m, heads, dim], heads and channels contiguous; its row stride."""
+    if not (t.shape == (m, heads, dim) and t.stride(2) == 1 and (t.stride(1) == dim or heads == 1)):
+        raise ValueError(f"{fn}: {what} is [M, {heads}, {dim}], heads and channels contiguous")
+    return t.stride(0) if m > 1 else heads * dim
+
+
+def _need_f32(fn: str, what: str, t, shape):
+    if not (t.dtype is torch.float32 and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{fn}: {what} is contiguous float32 {list(shape)}")
+
+
+def _need_cols(fn: str, what: str, t, m: int, n: int) -> int:
+    """t is fp32 [m, n], columns contiguous; its row stride."""
+    if not (t.dtype is torch.float32 and t.shape == (m, n) and (t.stride(1) == 1 or n == 1)):
+        raise ValueError(f"{fn}: {what} is float32 [{m}, {n}], columns contiguous")
+    return t.stride(0) if m > 1 else n
+
+
+def _need_mask(fn: str, tree_mask, m: int) -> int:
+    if tree_mask is None:
+        return 0
+    if tree_mask.dtype not in (torch.int64, torch.uint64):
+        raise TypeError(f"{fn}: tree_mask must be int64")
+    if not (tree_mask.dim() == 2 and tree_mask.shape[0] == m and tree_mask.is_contiguous()):
+        raise ValueError(f"{fn}: tree_mask is [M, words]")
+    return tree_mask.shape[1]
+
+
+def _need_16(fn: str, *tensors):
+    dt = tensors[0].dtype
+    if dt not in KV_DTYPES or any(t.dtype is not dt for t in tensors):
+        raise TypeError(f"{fn}: q, k and v must be float16 or bfloat16, all the same")
+    return KV_DTYPES[dt]
+
+
+def iq4xs_delta_inputs(x, conv_weight, a, b, a_log, dt_bias, eps: float, q, k, v, g, beta, state: DeltaState, layer: int,
+                       batch: KVBatch, tree_mask=None, advance: bool = True, stream=None) -> None:
+    """The projection's fp32 x [M, channels] (rows at any stride) -> q, k [M, Hk,
+    Dk], v [M, Hv, Dv] (16 bits) and g, beta fp32 [M, Hv]: causal convolution by
+    conv_weight fp32 [channels, 4] along each row's ancestors (tree_mask as in
+    iq4xs_tree_attention; None: chains) and the state's last inputs, SiLU, unit
+    norm of q and k; g = -exp(a_log) softplus(a + dt_bias), beta = sigmoid(b).
+    advance: the state's inputs move on behind the rows (chains only)."""
+    fn = "iq4xs_delta_inputs"
+    M, c, st = x.shape[0], state.channels, state
+    st._check_batch(fn, batch)
+    dt = _need_16(fn, q, k, v)
+    _need(st.conv is not None, fn, "the state has no inputs (conv)")
+    xs = _need_cols(fn, "x", x, M, c)
+    a_s, b_s = _need_cols(fn, "a", a, M, st.heads), _need_cols(fn, "b", b, M, st.heads)
+    _need_f32(fn, "conv_weight", conv_weight, (c, 4))
+    _need_f32(fn, "a_log", a_log, (st.heads,))
+    _need_f32(fn, "dt_bias", dt_bias, (st.heads,))
+    qs, ks = _need_rows16(fn, M, "q", q, st.key_heads, st.key_dim), _need_rows16(fn, M, "k", k, st.key_heads, st.key_dim)
+    vs = _need_rows16(fn, M, "v", v, st.heads, st.value_dim)
+    _need_f32(fn, "g", g, (M, st.heads))
+    _need_f32(fn, "beta", beta, (M, st.heads))
+    words = _need_mask(fn, tree_mask, M)
+    _need_device(fn, st.s, x, conv_weight, a, b, a_log, dt_bias, q, k, v, g, beta, tree_mask)
+    args = _DELTA_INPUTS(x.data_ptr(), xs, conv_weight.data_ptr(), a.data_ptr(), b.data_ptr(), a_s, b_s, a_log.data_ptr(),
+                         dt_bias.data_ptr(), eps, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, dt, g.data_ptr(),
+                         beta.data_ptr(), _addr(tree_mask), words, 1 if advance else 0, M, layer)
+    rc = (_lib or load()).iq4xs_delta_inputs(args, st.desc, batch.desc, _stream(stream))
+    if rc:
+        _check(fn, rc)
+
+
+def iq4xs_delta_rule(q, k, v, g, beta, scale: float, out, state: DeltaState, layer: int, batch: KVBatch, u=None,
+                     tree_mask=None, max_rows: int | None = None, stream=None) -> None:
+    """The gated delta rule over the batch's new rows -> out fp32 [M, Hv * Dv].
+    Without u the rows are chains and the layer's state moves on over them; with
+    u (fp32 [M, Hv, Dv], written: what iq4xs_delta_commit takes) the state stays
+    and every row starts from its parent's (tree_mask; None: a chain), at most 64
+    rows a sequence.  max_rows: no sequence has more rows (None: not known)."""
+    fn = "iq4xs_delta_rule"
+    M, st = q.shape[0], state
+    st._check_batch(fn, batch)
+    dt = _need_16(fn, q, k, v)
+    qs, ks = _need_rows16(fn, M, "q", q, st.key_heads, st.key_dim), _need_rows16(fn, M, "k", k, st.key_heads, st.key_dim)
+    vs = _need_rows16(fn, M, "v", v, st.heads, st.value_dim)
+    _need_f32(fn, "g", g, (M, st.heads))
+    _need_f32(fn, "beta", beta, (M, st.heads))
+    outs = _need_cols(fn, "out", out, M, st.heads * st.value_dim)
+    if u is not None:
+        _need_f32(fn, "u", u, (M, st.heads, st.value_dim))
+    words = _need_mask(fn, tree_mask, M)
+    _need_device(fn, st.s, q, k, v, g, beta, out, u, tree_mask)
+    args = _DELTA_RULE(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, dt, g.data_ptr(), beta.data_ptr(), scale,
+                       out.data_ptr(), outs, _addr(u), _addr(tree_mask), words, 0 if max_rows is None else max_rows, M, layer)
+    rc = (_lib or load()).iq4xs_delta_rule(args, st.desc, batch.desc, _stream(stream))
+    if rc:
+        _check(fn, rc)
+
+
+def iq4xs_delta_commit(k, g, u, x, state: DeltaState, batch: KVBatch, paths, accepted, stream=None) -> None:
+    """Keep the new tokens paths[s, :accepted[s]] (strictly rising) of every
+    sequence in the states of all layers; before iq4xs_cache_commit, which may
+    move lens.  k [layers, M, Hk, Dk], g fp32 [layers, M, Hv], u fp32 [layers,
+    M, Hv, Dv] and x fp32 [layers, M, channels] (None where the state has no
+    conv) are what the step's calls left."""
+    fn = "iq4xs_delta_commit"
+    st = state
+    st._check_batch(fn, batch)
+    dt = _need_16(fn, k)
+    _need(k.dim() == 4 and k.shape[0] == st.layers, fn, "k is [layers, M, Hk, Dk]")
+    M = k.shape[1]
+    ks = _need_rows16(fn, M, "a layer of k", k[0], st.key_heads, st.key_dim)
+    _need(g.dtype is torch.float32 and g.shape == (st.layers, M, st.heads) and g[0].is_contiguous(), fn,
+          "g is float32 [layers, M, Hv], a layer contiguous")
+    _need(u.dtype is torch.float32 and u.shape == (st.layers, M, st.heads, st.value_dim) and u[0].is_contiguous(), fn,
+          "u is float32 [layers, M, Hv, Dv], a layer contiguous")
+    _need((x is None) == (st.conv is None), fn, "x goes with the state's inputs (conv)")
+    xs = xl = 0
+    if x is not None:
+        _need(x.dim() == 3 and x.shape[0] == st.layers, fn, "x is [layers, M, channels]")
+        xs, xl = _need_cols(fn, "a layer of x", x[0], M, st.channels), x.stride(0)
+    _need_i32(fn, paths=paths, accepted=accepted)
+    _need(paths.dim() == 2 and paths.shape[0] == batch.sequences and accepted.numel() == batch.sequences, fn,
+          "paths [B, width], accepted [B]")
+    _need_device(fn, st.s, k, g, u, x, paths, accepted)
+    args = _DELTA_COMMIT(k.data_ptr(), ks, k.stride(0), dt, g.data_ptr(), g.stride(0), u.data_ptr(), u.stride(0), _addr(x),
+                         xs, xl, paths.data_ptr(), paths.shape[1], accepted.data_ptr(), M)
+    rc = (_lib or load()).iq4xs_delta_commit(args, st.desc, batch.desc, _stream(stream))
+    if rc:
+        _check(fn, rc)
+
+
+def iq4xs_token_probs(logits, probs, temperature=None, stream=None) -> None:
+    """probs fp32 [M, V] = softmax of logits fp32 [M, V] / temperature fp32 [M]
+    (None: 1; not above 0: all on the first of the largest); in place will do."""
+    fn = "iq4xs_token_probs"
+    _need(logits.dim() == 2, fn, "logits is [M, V]")
+    M, V = logits.shape
+    ls, ps = _need_cols(fn, "logits", logits, M, V), _need_cols(fn, "probs", probs, M, V)
+    if temperature is not None:
+        _need_f32(fn, "temperature", temperature, (M,))
+    _need_device(fn, logits, probs, temperature)
+    rc = (_lib or load()).iq4xs_token_probs(logits.data_ptr(), ls, M, V, _addr(temperature), probs.data_ptr(), ps,
+                                            _stream(stream))
+    if rc:
+        _check(fn, rc)
+
+
+def iq4xs_verify_drafts(probs, tokens, accept_u, draw_u, paths, accepted, next_token, batch: KVBatch, draft_probs=None,
+                        tree_mask=None, stream=None) -> None:
+    """Which drafted tokens (int32 [M]; a sequence's row 0 is its last kept one)
+    the target's probabilities probs fp32 [M, V] accept, by accept_u fp32 [M]:
+    paths int32 [B, width] and accepted int32 [B] as iq4xs_cache_commit takes
+    them, and next_token int32 [B], drawn by draw_u fp32 [B] from what is left.
+    draft_probs fp32 [M, V]: row r's distribution that its children were drawn
+    from (None: they were not drawn)."""
+    fn = "iq4xs_verify_drafts"
+    _need(probs.dim() == 2, fn, "probs is [M, V]")
+    M, V = probs.shape
+    ps, ds = _need_cols(fn, "probs", probs, M, V), 0
+    if draft_probs is not None:
+        ds = _need_cols(fn, "draft_probs", draft_probs, M, V)
+    _need_i32(fn, tokens=tokens, paths=paths, accepted=accepted, next_token=next_token)
+    _need_f32(fn, "accept_u", accept_u, (M,))
+    _need_f32(fn, "draw_u", draw_u, (batch.sequences,))
+    _need(tokens.numel() == M and paths.dim() == 2 and paths.shape[0] == batch.sequences and
+          accepted.numel() == batch.sequences and next_token.numel() == batch.sequences, fn,
+          "tokens [M], paths [B, width], accepted [B], next_token [B]")
+    words = _need_mask(fn, tree_mask, M)
+    _need_device(fn, probs, draft_probs, tokens, tree_mask, accept_u, draw_u, paths, accepted, next_token)
+    args = _VERIFY(probs.data_ptr(), ps, _addr(draft_probs), ds, tokens.data_ptr(), _addr(tree_mask), words,
+                   accept_u.data_ptr(), draw_u.data_ptr(), M, V, paths.data_ptr(), paths.shape[1], accepted.data_ptr(),
+                   next_token.data_ptr())
+    rc = (_lib or load()).iq4xs_verify_drafts(args, batch.desc, _stream(stream))
     if rc:
         _check(fn, rc)
 

@@ -85,6 +85,9 @@ struct KvBf16 {
     }
 };
 
+// The host's checks of a batch (csrc/cache_api.cu).
+int view_batch(const iq4xs_kv_batch* b, BatchView* out);
+
 // Host-side launchers (csrc/append.cu, csrc/cache_pages.cu, csrc/attention*.cu);
 // arguments are checked by the callers in csrc/cache_api.cu.
 cudaError_t launch_qk_norm_rope(const iq4xs_qk_norm_rope_args& a, const CacheView& c, const BatchView& b, bool bf16,

@@ -48,7 +48,9 @@ int view_cache(const iq4xs_kv_cache* c, CacheView* out) {
     return IQ4XS_OK;
 }
 
-int view_batch(const iq4xs_kv_batch* b, BatchView* out) {
+}  // namespace
+
+int iq4xs::view_batch(const iq4xs_kv_batch* b, BatchView* out) {
     if (!b) return IQ4XS_ERR_ARG;
     if (b->sequences < 0 || b->sequences > kMaxSequences) return IQ4XS_ERR_SHAPE;
     if (b->table_width < 1 || b->table_width > (1 << 20)) return IQ4XS_ERR_SHAPE;
@@ -65,8 +67,6 @@ int view_batch(const iq4xs_kv_batch* b, BatchView* out) {
     out->sequences = (int)b->sequences;
     return IQ4XS_OK;
 }
-
-}  // namespace
 
 extern "C" {
 

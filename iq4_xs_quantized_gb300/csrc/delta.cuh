@@ -1,0 +1,84 @@
+// delta.cuh -- the recurrent layers' state as kernels see it (layouts:
+// include/iq4xs.h), and what their kernels share.
+#pragma once
+
+#include "cache.cuh"
+
+namespace iq4xs {
+
+struct DeltaView {
+    float* s;
+    float* conv;
+    const int32_t* slot_of;
+    int64_t s_slot_stride, conv_slot_stride;    // elements
+    int64_t s_layer_stride, conv_layer_stride;
+    int64_t s_extent, conv_extent;              // bytes from the first element to behind the last
+    int layers, slots, key_heads, heads, key_dim, value_dim, channels;
+};
+
+constexpr int kConvTaps = 4;
+constexpr int kDeltaTreeRows = 64;  // rows of a sequence whose state stays
+
+// The slot of sequence s; -1 (recorded) where it is out of range.
+__device__ __forceinline__ int delta_slot(const DeltaView& d, int s, int* err) {
+    const int slot = d.slot_of != nullptr ? d.slot_of[s] : s;
+    if (slot >= 0 && slot < d.slots) return slot;
+    data_error(err, kDataSlot);
+    return -1;
+}
+
+// Eight 16-bit values -> fp32.
+template <class T>
+__device__ __forceinline__ void unpack8(const uint4& w, float* x) {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = T::unpack(v[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ void unpack8(bool bf16, const uint4& w, float* x) {
+    if (bf16) unpack8<KvBf16>(w, x);
+    else unpack8<KvF16>(w, x);
+}
+
+struct DeltaRule {  // iq4xs_delta_rule_args as its kernels see them
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t q_row_stride, k_row_stride, v_row_stride;
+    const float* g;
+    const float* beta;
+    float* out;
+    int64_t out_row_stride;
+    float* u;
+    const uint64_t* tree_mask;
+    int64_t s_offset;  // of the layer
+    float scale;
+    int mask_words, max_rows, rows, bf16;
+};
+
+// The new tokens before t that row row0 + t comes from, as bits (of 64).
+__device__ __forceinline__ uint64_t delta_seen(const uint64_t* mask, int words, int rows, int row0, int t,
+                                               const Bc& bc) {
+    const uint64_t before = (1ull << t) - 1;
+    if (mask == nullptr) return before;
+    const uint64_t* at = mask + (int64_t)(row0 + t) * words;
+    if (!bc_global(bc, at, 8, mask, 8 * (int64_t)rows * words, kBcDeltaMask)) return 0;
+    return *at & before;
+}
+
+cudaError_t launch_delta_inputs(const iq4xs_delta_inputs_args& a, const DeltaView& d, const BatchView& b, int* err,
+                                int num_sms, cudaStream_t stream);
+cudaError_t launch_delta_rule(const DeltaRule& p, const DeltaView& d, const BatchView& b, int* err, int num_sms,
+                              cudaStream_t stream);
+cudaError_t launch_delta_commit(const iq4xs_delta_commit_args& a, const DeltaView& d, const BatchView& b, int* err,
+                                cudaStream_t stream);
+cudaError_t launch_token_probs(const float* logits, int64_t logits_stride, int64_t rows, int64_t vocab,
+                               const float* temperature, float* probs, int64_t probs_stride, int* err,
+                               cudaStream_t stream);
+cudaError_t launch_verify_drafts(const iq4xs_verify_drafts_args& a, const BatchView& b, int* err,
+                                 cudaStream_t stream);
+
+}  // namespace iq4xs

@@ -1,0 +1,213 @@
+// delta_inputs.cu -- from the projection's fp32 rows to the delta rule's
+// operands in one pass: causal convolution over four inputs along a row's
+// ancestors, SiLU, unit norm of every query and key head, one rounding to 16
+// bits; decay and step size of every head; the state's last inputs.
+//
+// A thread takes four channels of a run of one sequence's rows and keeps the
+// last three inputs in registers (chains), so that HBM reads each value once
+// (4 bytes) and writes it once (2 bytes), which bounds it.  The first run of a
+// sequence alone reads the state's inputs, and writes them anew: its rows are
+// at least the three that need them.  A drafted tree's rows read their
+// ancestors' inputs instead, out of L1 or L2.
+#include "delta.cuh"
+
+namespace iq4xs {
+namespace {
+
+constexpr int kInputThreads = 128;
+constexpr int kInputCols = 4 * kInputThreads;  // channels of a CTA
+
+struct InputParams {
+    const float* x;
+    const float* weight;
+    const float* a;
+    const float* b;
+    const float* a_log;
+    const float* dt_bias;
+    uint16_t* out[3];          // q, k, v
+    int64_t out_stride[3];
+    float* g;
+    float* beta;
+    const uint64_t* tree_mask;
+    int64_t x_stride, a_stride, b_stride, conv_offset;
+    float eps;
+    int mask_words, advance, rows, run, col_parts, key_lanes;
+};
+
+__device__ __forceinline__ float silu(float y) { return y / (1.f + __expf(-y)); }
+__device__ __forceinline__ void tap(float4& y, const float4 (&w)[4], int j, const float4& x) {
+    const float* w0 = reinterpret_cast<const float*>(w);  // [channel][tap]
+    y.x = fmaf(w0[j], x.x, y.x);
+    y.y = fmaf(w0[4 + j], x.y, y.y);
+    y.z = fmaf(w0[8 + j], x.z, y.z);
+    y.w = fmaf(w0[12 + j], x.w, y.w);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kInputThreads) delta_inputs_kernel(const InputParams p, const DeltaView d,
+                                                                     const BatchView b, int* err) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const Bc bc = bc_open(err);
+    const int lane = threadIdx.x & 31, part = blockIdx.x % p.col_parts, at = blockIdx.x / p.col_parts;
+    // Sequence s's runs begin at place row_offsets[s] / run + s: enough places
+    // for them all, and the last sequence that begins at or before `at` is this one's.
+    int s = -1;
+    for (int s0 = 0; s0 < b.sequences; s0 += 32) {
+        const int i = s0 + lane;
+        const unsigned begun = __ballot_sync(0xffffffffu, i < b.sequences && b.row_offsets[i] / p.run + i <= at);
+        s += __popc(begun);
+        if (begun != 0xffffffffu) break;
+    }
+    if (s < 0) return;
+    int first;
+    const int n = batch_rows(b, s, p.rows, &first, err), len = batch_len(b, s, err), slot = delta_slot(d, s, err);
+    const int t0 = (at - (first / p.run + s)) * p.run, t1 = min(n, t0 + p.run);
+    if (len < 0 || slot < 0 || t0 < 0 || t0 >= n) return;
+
+    if (part == p.col_parts - 1) {  // the gates
+        const int64_t extent = 4 * (int64_t)p.rows * d.heads;
+        for (int i = threadIdx.x; i < (t1 - t0) * d.heads; i += kInputThreads) {
+            const int row = first + t0 + i / d.heads, h = i % d.heads;
+            const float* a = p.a + row * p.a_stride + h;
+            const float* c = p.b + row * p.b_stride + h;
+            if (!bc_global(bc, a, 4, p.a, 4 * ((p.rows - 1) * p.a_stride + d.heads), kBcDeltaGate) ||
+                !bc_global(bc, c, 4, p.b, 4 * ((p.rows - 1) * p.b_stride + d.heads), kBcDeltaGate))
+                continue;
+            const float z = *a + p.dt_bias[h];
+            const float g = -expf(p.a_log[h]) * (fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))));
+            const int64_t to = (int64_t)row * d.heads + h;
+            if (bc_global(bc, p.g + to, 4, p.g, extent, kBcDeltaGate)) p.g[to] = g;
+            if (bc_global(bc, p.beta + to, 4, p.beta, extent, kBcDeltaGate)) p.beta[to] = 1.f / (1.f + expf(-*c));
+        }
+        return;
+    }
+    const int c = part * kInputCols + 4 * threadIdx.x;
+    const bool here = c < d.channels;  // (lanes behind the last channel take part in the shuffles)
+    const int64_t x_extent = 4 * ((p.rows - 1) * p.x_stride + d.channels);
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto input = [&](int row) {
+        const float* from = p.x + row * p.x_stride + c;
+        return here && bc_global(bc, from, 16, p.x, x_extent, kBcDeltaX) ? *reinterpret_cast<const float4*>(from) : zero;
+    };
+    float* const at_conv = d.conv + p.conv_offset + slot * d.conv_slot_stride;
+    auto before = [&](int i) {  // input i of the state's, oldest first
+        const float* from = at_conv + (int64_t)i * d.channels + c;
+        return here && len > 0 && bc_global(bc, from, 16, d.conv, d.conv_extent, kBcDeltaConv)
+                   ? *reinterpret_cast<const float4*>(from) : zero;
+    };
+    float4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float* from = p.weight + 4 * (int64_t)(c + i);
+        w[i] = here && bc_global(bc, from, 16, p.weight, 16 * (int64_t)d.channels, kBcDeltaW)
+                   ? *reinterpret_cast<const float4*>(from) : zero;
+    }
+    const int keys = d.key_heads * d.key_dim, kind = c < keys ? 0 : c < 2 * keys ? 1 : 2;
+    uint16_t* const base = p.out[kind];
+    const int64_t out_stride = p.out_stride[kind];
+    const int64_t out_extent = 2 * ((p.rows - 1) * out_stride + (kind < 2 ? keys : d.heads * d.value_dim));
+    auto finish = [&](int t, float4 y) {
+        y = make_float4(silu(y.x), silu(y.y), silu(y.z), silu(y.w));
+        float sum = fmaf(y.x, y.x, fmaf(y.y, y.y, fmaf(y.z, y.z, y.w * y.w)));
+        for (int o = p.key_lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float r = kind < 2 ? rsqrtf(sum + p.eps) : 1.f;
+        uint16_t* to = base + (first + t) * out_stride + c - kind * keys;
+        if (here && bc_global(bc, to, 8, base, out_extent, kBcDeltaQkv))
+            *reinterpret_cast<uint2*>(to) = make_uint2(T::pack(r * y.x, r * y.y), T::pack(r * y.z, r * y.w));
+    };
+    auto past = [&](int t) { return t >= 0 ? input(first + t) : before(kConvTaps - 1 + t); };
+    if (p.tree_mask == nullptr) {
+        float4 x0 = past(t0 - 3), x1 = past(t0 - 2), x2 = past(t0 - 1);
+        float4 new0 = zero, new1 = zero, new2 = zero;
+        const bool moves = p.advance && t0 == 0;
+        if (moves) {  // (the state's inputs are read before they are written)
+            new0 = past(n - 3);
+            new1 = past(n - 2);
+            new2 = past(n - 1);
+        }
+#pragma unroll 4
+        for (int t = t0; t < t1; ++t) {
+            const float4 x3 = input(first + t);
+            float4 y = zero;
+            tap(y, w, 0, x0);
+            tap(y, w, 1, x1);
+            tap(y, w, 2, x2);
+            tap(y, w, 3, x3);
+            finish(t, y);
+            x0 = x1;
+            x1 = x2;
+            x2 = x3;
+        }
+        if (moves && here && bc_global(bc, at_conv + c, 16, d.conv, d.conv_extent, kBcDeltaConv) &&
+            bc_global(bc, at_conv + 2 * d.channels + c, 16, d.conv, d.conv_extent, kBcDeltaConv)) {
+            *reinterpret_cast<float4*>(at_conv + c) = new0;
+            *reinterpret_cast<float4*>(at_conv + d.channels + c) = new1;
+            *reinterpret_cast<float4*>(at_conv + 2 * (int64_t)d.channels + c) = new2;
+        }
+        return;
+    }
+    // The parent of row t (below 0: an input of the state's).
+    auto parent = [&](int t) {
+        if (t < 0) return t - 1;
+        for (int i = min(p.mask_words - 1, t >> 6); i >= 0; --i) {
+            const uint64_t* from = p.tree_mask + (int64_t)(first + t) * p.mask_words + i;
+            uint64_t bits = bc_global(bc, from, 8, p.tree_mask, 8 * (int64_t)p.rows * p.mask_words, kBcDeltaMask) ? *from : 0;
+            if (i == t >> 6) bits &= (1ull << (t & 63)) - 1;
+            if (bits != 0) return 64 * i + 63 - __clzll(bits);
+        }
+        return -1;
+    };
+    for (int t = t0; t < t1; ++t) {
+        float4 y = zero;
+        int from = t;
+        tap(y, w, 3, input(first + t));
+#pragma unroll
+        for (int j = 2; j >= 0; --j) {
+            from = parent(from);
+            tap(y, w, j, past(from));
+        }
+        finish(t, y);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_delta_inputs(const iq4xs_delta_inputs_args& a, const DeltaView& d, const BatchView& b, int* err,
+                                int num_sms, cudaStream_t stream) {
+    InputParams p;
+    p.x = a.x;
+    p.weight = a.conv_weight;
+    p.a = a.a;
+    p.b = a.b;
+    p.a_log = a.a_log;
+    p.dt_bias = a.dt_bias;
+    p.out[0] = static_cast<uint16_t*>(a.q);
+    p.out[1] = static_cast<uint16_t*>(a.k);
+    p.out[2] = static_cast<uint16_t*>(a.v);
+    p.out_stride[0] = a.q_row_stride;
+    p.out_stride[1] = a.k_row_stride;
+    p.out_stride[2] = a.v_row_stride;
+    p.g = a.g;
+    p.beta = a.beta;
+    p.tree_mask = a.tree_mask;
+    p.x_stride = a.x_row_stride;
+    p.a_stride = a.a_row_stride;
+    p.b_stride = a.b_row_stride;
+    p.conv_offset = a.layer * d.conv_layer_stride;
+    p.eps = (float)a.eps;
+    p.mask_words = (int)a.mask_words;
+    p.advance = (int)a.advance;
+    p.rows = (int)a.rows;
+    p.key_lanes = d.key_dim / 4;
+    p.col_parts = (d.channels + kInputCols - 1) / kInputCols + 1;
+    p.run = 16;  // (at least the three rows that read the state's inputs)
+    const int64_t blocks = (a.rows / p.run + b.sequences) * p.col_parts;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)blocks);
+    return a.dtype == IQ4XS_KV_BF16
+               ? launch_chained(delta_inputs_kernel<KvBf16>, grid, dim3(kInputThreads), 0, stream, 1, p, d, b, err)
+               : launch_chained(delta_inputs_kernel<KvF16>, grid, dim3(kInputThreads), 0, stream, 1, p, d, b, err);
+}
+
+}  // namespace iq4xs

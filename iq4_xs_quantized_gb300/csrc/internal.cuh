@@ -213,6 +213,7 @@ enum DeviceError : int {
     kDevErrTimeoutKv = 0x10D,        // attention: a stage of keys or values never landed
     kDevErrTimeoutKvSlot = 0x10E,    // attention: a stage slot was never freed
     kDevErrTimeoutScore = 0x10F,     // attention: a score or output product never completed
+    kDevErrTimeoutDelta = 0x110,     // delta rule: a product never completed
     kDevErrBounds = 0x200,           // + BoundsSite: a checked access missed its buffer
     kDevErrData = 0x300,             // + DataSite: a value read from device memory was out of range
 };
@@ -221,6 +222,7 @@ enum DeviceError : int {
 // device memory (every build checks them; the access they lead to is skipped).
 enum DataSite : int {
     kDataOffsets = 1, kDataLens, kDataHeld, kDataPage, kDataPosition, kDataPath, kDataRow, kDataRefs,
+    kDataSlot, kDataCount,
 };
 
 // ---------------------------------------------------------------------------
@@ -250,6 +252,9 @@ enum BoundsSite : int {
     kBcAppX = 0x60, kBcAppW, kBcAppRope, kBcAppQ, kBcAppKv,
     kBcPagesKv = 0x70, kBcPagesTable, kBcPagesRefs,
     kBcAttnQ = 0x80, kBcAttnOut, kBcAttnMask, kBcAttnWork, kBcAttnKv,
+    kBcDeltaX = 0x90, kBcDeltaW, kBcDeltaGate, kBcDeltaQkv, kBcDeltaS, kBcDeltaConv, kBcDeltaOut, kBcDeltaU,
+    kBcDeltaMask, kBcDeltaPath,
+    kBcProbs = 0xA0, kBcLogits, kBcTemp, kBcVerifyRow, kBcVerifyProbs, kBcVerifyOut,
 };
 #ifdef IQ4XS_BOUNDS_CHECK
 constexpr bool kBoundsCheck = true;

@@ -1,0 +1,333 @@
+// verify.cu -- which drafted tokens the target's probabilities accept, and the
+// token behind them (include/iq4xs.h).
+//
+// The walk down the tree takes single probabilities: a cluster's first CTA
+// looks them all up at once and walks in shared memory.  Whole rows of the
+// vocabulary are summed where a drafter's distribution is taken off after a
+// rejection, and once for the draw; a cluster shares them.  The sums are of
+// whole numbers (values times 2^61), so that neither the order nor the split
+// changes them: a draw near the border of two tokens always falls alike.
+//
+// Few bytes are read (a row or two of probabilities a sequence): what it takes
+// is the chain of launch, tree, probabilities, sums, and the draw's search.
+#include "delta.cuh"
+
+namespace iq4xs {
+namespace {
+
+constexpr int kVerifyThreads = 512;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyCluster = 8;
+constexpr int kVerifyRows = 1024;
+
+struct VerifyParams {
+    const float* probs;
+    const float* draft;
+    int64_t probs_stride, draft_stride;
+    const int32_t* tokens;
+    const uint64_t* tree_mask;
+    const float* accept_u;
+    const float* draw_u;
+    int32_t* paths;
+    int32_t* accepted;
+    int32_t* next;
+    int mask_words, rows, vocab, path_width, ranks;
+};
+
+// What the first CTA tells the others to do next.
+struct __align__(16) Order {
+    int what;   // kSum, kDraw, kEnd
+    int node;   // row of the batch whose probabilities they are
+    int taken;  // times that the drafter's distribution comes off
+    int gone;   // without one: rejected tokens in the first CTA's list
+};
+enum { kSum, kDraw, kEnd };
+
+struct VerifyShared {
+    int parent[kVerifyRows], token[kVerifyRows];
+    float u[kVerifyRows], p[kVerifyRows], q[kVerifyRows];
+    unsigned char again[kVerifyRows];              // a sibling before has the same token
+    int gone[kVerifyRows];                         // tokens rejected at the row
+    unsigned long long mass[kVerifyRows];          // m before each subtraction
+    unsigned long long parts[kVerifyCluster];      // the CTAs' sums
+    unsigned long long warps[kVerifyWarps];
+    Order order;
+};
+
+// p in 0..1 as a whole number of 2^-61.
+__device__ __forceinline__ unsigned long long whole(float p) {
+    if (!(p > 0.f)) return 0;
+    const uint32_t bits = __float_as_uint(fminf(p, 1.f));
+    const int e = max((int)(bits >> 23), 1);  // value = mantissa * 2^(e - 150)
+    const unsigned long long m = (bits & 0x7fffffu) | (bits >> 23 ? 0x800000u : 0u);
+    const int shift = e - 150 + 61;
+    return shift >= 0 ? m << shift : shift > -32 ? m >> -shift : 0;
+}
+__device__ __forceinline__ double real(unsigned long long w) { return (double)w * 0x1p-61; }
+// max(r - m q, 0)
+__device__ __forceinline__ unsigned long long take_off(unsigned long long r, unsigned long long m, unsigned long long q) {
+    const unsigned long long off = __umul64hi(m << 1, q << 2);
+    return r > off ? r - off : 0;
+}
+__device__ __forceinline__ uint32_t at_rank(const void* p, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void st_rank(const void* p, int rank, unsigned long long v) {
+    asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(at_rank(p, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ int ld_rank(const int* p, int rank) {
+    int v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(at_rank(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive_release();
+    cluster_wait();
+}
+
+__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p, const BatchView b, int* err) {
+    __shared__ VerifyShared sh;
+    cluster_arrive_relaxed();
+    griddep_launch_dependents();
+    griddep_wait();
+    const Bc bc = bc_open(err);
+    const int rank = blockIdx.x % p.ranks, s = blockIdx.x / p.ranks;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t p_extent = 4 * ((p.rows - 1) * p.probs_stride + p.vocab);
+    const int64_t q_extent = 4 * ((p.rows - 1) * p.draft_stride + p.vocab);
+    const int64_t path_extent = 4 * (int64_t)b.sequences * p.path_width;
+    int32_t* const path = p.paths + (int64_t)s * p.path_width;
+    int first = 0, n = 0;
+    if (rank == 0) {
+        n = batch_rows(b, s, p.rows, &first, err);
+        if (n > kVerifyRows) {
+            if (tid == 0) data_error(err, kDataCount);
+            n = 0;
+        }
+        // Every row: parent, token, random number, and its token's probabilities behind its parent.
+        for (int t = tid; t < n; t += kVerifyThreads) {
+            int parent = t - 1;
+            if (p.tree_mask != nullptr) {
+                parent = -1;
+                for (int i = min(p.mask_words - 1, t >> 6); i >= 0 && parent < 0; --i) {
+                    const uint64_t* from = p.tree_mask + (int64_t)(first + t) * p.mask_words + i;
+                    uint64_t bits =
+                        bc_global(bc, from, 8, p.tree_mask, 8 * (int64_t)p.rows * p.mask_words, kBcVerifyRow) ? *from : 0;
+                    if (i == t >> 6) bits &= (1ull << (t & 63)) - 1;
+                    if (bits != 0) parent = 64 * i + 63 - __clzll(bits);
+                }
+            }
+            int token = -1;
+            float u = 0.f, pr = 0.f, qr = 0.f;
+            if (bc_global(bc, p.tokens + first + t, 4, p.tokens, 4 * (int64_t)p.rows, kBcVerifyRow))
+                token = p.tokens[first + t];
+            if (bc_global(bc, p.accept_u + first + t, 4, p.accept_u, 4 * (int64_t)p.rows, kBcVerifyRow))
+                u = p.accept_u[first + t];
+            if (token < 0 || token >= p.vocab) token = -1;
+            if (parent >= 0 && token >= 0) {
+                const float* from = p.probs + (first + parent) * p.probs_stride + token;
+                if (bc_global(bc, from, 4, p.probs, p_extent, kBcVerifyProbs)) pr = *from;
+                if (p.draft != nullptr) {
+                    from = p.draft + (first + parent) * p.draft_stride + token;
+                    if (bc_global(bc, from, 4, p.draft, q_extent, kBcVerifyProbs)) qr = *from;
+                }
+            }
+            sh.parent[t] = parent;
+            sh.token[t] = token;
+            sh.u[t] = u;
+            sh.p[t] = pr;
+            sh.q[t] = qr;
+        }
+        __syncthreads();
+        if (p.draft == nullptr)
+            for (int t = tid; t < n; t += kVerifyThreads) {
+                bool again = false;
+                for (int i = t - 1; i > sh.parent[t] && !again; --i)
+                    again = sh.parent[i] == sh.parent[t] && sh.token[i] == sh.token[t];
+                sh.again[t] = again;
+            }
+        __syncthreads();
+    }
+    // Thread 0 of the first CTA: where the walk stands.
+    constexpr unsigned long long kOne = 1ull << 61;
+    int node = 0, t = 1, count = 1, taken = 0, gone = 0;
+    unsigned long long mass = kOne;
+    auto accept = [&] {
+        node = t;
+        if (bc_global(bc, path + count, 4, p.paths, path_extent, kBcVerifyOut)) path[count] = t;
+        ++count;
+        taken = gone = 0;
+        mass = kOne;
+    };
+    auto walk = [&]() -> int {
+        for (; t < n && count < p.path_width; ++t) {
+            if (sh.parent[t] != node) continue;
+            // (the same comparisons whatever the token: one outside has no chance and nothing to take off)
+            unsigned long long r = whole(sh.p[t]);
+            const double u = (double)sh.u[t];
+            if (p.draft != nullptr) {
+                const unsigned long long q = whole(sh.q[t]);
+                for (int i = 0; i < taken; ++i) r = take_off(r, sh.mass[i], q);
+                if (sh.token[t] >= 0 && u * real(mass) * real(q) < real(r)) {
+                    accept();
+                    continue;
+                }
+                for (int k = 0; k < p.ranks; ++k) st_rank(&sh.mass[taken], k, mass);
+                ++taken;
+                ++t;
+                return kSum;
+            }
+            if (sh.token[t] < 0) continue;
+            if (sh.again[t]) r = 0;
+            if (u * real(mass) < real(r)) {
+                accept();
+                continue;
+            }
+            mass -= min(mass, r);
+            if (!sh.again[t]) sh.gone[gone++] = sh.token[t];
+        }
+        return kDraw;
+    };
+    // The part of a row of the vocabulary that this CTA sums, a run a warp.
+    const int each = (p.vocab + p.ranks - 1) / p.ranks, run = (each + kVerifyWarps - 1) / kVerifyWarps;
+    const int begin = min(p.vocab, rank * each), end = min(p.vocab, begin + each);
+    const int lo = min(end, begin + warp * run), hi = min(end, lo + run);
+    bool plain = false;
+    cluster_wait();  // (every CTA has begun: its shared memory may be written)
+    for (;;) {
+        if (rank == 0 && tid == 0) {
+            Order o = {kEnd, 0, 0, 0};
+            if (n > 0) {
+                o.what = plain ? kDraw : walk();
+                o.node = first + node;
+                o.taken = plain ? 0 : taken;
+                o.gone = plain ? 0 : gone;
+            }
+            const unsigned long long* w = reinterpret_cast<const unsigned long long*>(&o);
+            for (int k = 0; k < p.ranks; ++k) {
+                st_rank(&sh.order, k, w[0]);
+                st_rank(reinterpret_cast<unsigned long long*>(&sh.order) + 1, k, w[1]);
+            }
+        }
+        cluster_sync();
+        const Order o = sh.order;
+        if (o.what == kEnd) break;
+        // Value i of what is left behind the row.
+        auto left_at = [&](int i) -> unsigned long long {
+            const float* from = p.probs + o.node * p.probs_stride + i;
+            if (!bc_global(bc, from, 4, p.probs, p_extent, kBcVerifyProbs)) return 0;
+            unsigned long long r = whole(*from);
+            if (o.taken > 0) {
+                from = p.draft + o.node * p.draft_stride + i;
+                if (!bc_global(bc, from, 4, p.draft, q_extent, kBcVerifyProbs)) return 0;
+                const unsigned long long q = whole(*from);
+                for (int k = 0; k < o.taken; ++k) r = take_off(r, sh.mass[k], q);
+            }
+            return r;
+        };
+        unsigned long long sum = 0;
+        for (int i = lo + lane; i < hi; i += 32) sum += left_at(i);
+        for (int i = tid; i < o.gone; i += kVerifyThreads)
+            if (rank != 0) sh.gone[i] = ld_rank(&sh.gone[i], 0);
+        __syncthreads();
+        for (int i = lane; i < o.gone; i += 32)
+            if (sh.gone[i] >= lo && sh.gone[i] < hi) sum -= left_at(sh.gone[i]);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        if (lane == 0) sh.warps[warp] = sum;
+        __syncthreads();
+        if (tid < p.ranks) {
+            unsigned long long all = 0;
+            for (int w = 0; w < kVerifyWarps; ++w) all += sh.warps[w];
+            st_rank(&sh.parts[rank], tid, all);
+        }
+        cluster_sync();
+        unsigned long long total = 0, before = 0;
+        for (int k = 0; k < p.ranks; ++k) {
+            before += k < rank ? sh.parts[k] : 0;
+            total += sh.parts[k];
+        }
+        if (o.what == kSum) {
+            mass = total;
+            continue;
+        }
+        if (total == 0 && !plain) {  // nothing is left: from the row itself
+            plain = true;
+            continue;
+        }
+        if (total == 0) {
+            if (rank == 0 && tid == 0 && bc_global(bc, p.next + s, 4, p.next, 4 * (int64_t)b.sequences, kBcVerifyOut))
+                p.next[s] = -1;
+            break;
+        }
+        float u = 0.f;
+        if (bc_global(bc, p.draw_u + s, 4, p.draw_u, 4 * (int64_t)b.sequences, kBcVerifyRow)) u = fmaxf(p.draw_u[s], 0.f);
+        const double at = (double)fminf(u, 1.f) * (double)total;
+        unsigned long long wanted = at < (double)total ? (unsigned long long)at : total - 1;
+        wanted = min(wanted, total - 1);  // the first value whose running sum is above it
+        if (wanted < before || wanted - before >= sh.parts[rank]) break;
+        wanted -= before;
+        int w = 0;
+        for (; w < kVerifyWarps - 1 && wanted >= sh.warps[w]; ++w) wanted -= sh.warps[w];
+        if (warp != w) break;
+        for (int i0 = lo; i0 < hi; i0 += 32) {
+            const int i = i0 + lane;
+            unsigned long long x = i < hi ? left_at(i) : 0;
+            for (int k = 0; k < o.gone; ++k) x = sh.gone[k] == i ? 0 : x;
+#pragma unroll
+            for (int k = 1; k < 32; k <<= 1) {
+                const unsigned long long y = __shfl_up_sync(0xffffffffu, x, k);
+                if (lane >= k) x += y;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, x > wanted);
+            if (hit != 0) {
+                if (lane == __ffs(hit) - 1 && bc_global(bc, p.next + s, 4, p.next, 4 * (int64_t)b.sequences, kBcVerifyOut))
+                    p.next[s] = i;
+                break;
+            }
+            wanted -= __shfl_sync(0xffffffffu, x, 31);
+        }
+        break;
+    }
+    if (rank == 0) {
+        if (tid == 0) {
+            sh.order.node = n > 0 ? count : 0;
+            if (bc_global(bc, p.accepted + s, 4, p.accepted, 4 * (int64_t)b.sequences, kBcVerifyOut))
+                p.accepted[s] = n > 0 ? count : 0;
+            if (n > 0 && bc_global(bc, path, 4, p.paths, path_extent, kBcVerifyOut)) path[0] = 0;
+            if (n == 0 && bc_global(bc, p.next + s, 4, p.next, 4 * (int64_t)b.sequences, kBcVerifyOut)) p.next[s] = -1;
+        }
+        __syncthreads();
+        for (int i = sh.order.node + tid; i < p.path_width; i += kVerifyThreads)
+            if (bc_global(bc, path + i, 4, p.paths, path_extent, kBcVerifyOut)) path[i] = 0;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_verify_drafts(const iq4xs_verify_drafts_args& a, const BatchView& b, int* err, cudaStream_t stream) {
+    VerifyParams p;
+    p.probs = a.probs;
+    p.draft = a.draft_probs;
+    p.probs_stride = a.probs_stride;
+    p.draft_stride = a.draft_probs ? a.draft_stride : 0;
+    p.tokens = a.tokens;
+    p.tree_mask = a.tree_mask;
+    p.accept_u = a.accept_u;
+    p.draw_u = a.draw_u;
+    p.paths = a.paths;
+    p.accepted = a.accepted;
+    p.next = a.next;
+    p.mask_words = (int)a.mask_words;
+    p.rows = (int)a.rows;
+    p.vocab = (int)a.vocab;
+    p.path_width = (int)a.path_width;
+    p.ranks = 1;
+    while (p.ranks < kVerifyCluster && p.ranks * 4 * kVerifyThreads < p.vocab) p.ranks *= 2;
+    return launch_chained(verify_kernel, dim3((unsigned)(b.sequences * p.ranks)), dim3(kVerifyThreads), 0, stream, p.ranks,
+                          p, b, err);
+}
+
+}  // namespace iq4xs
