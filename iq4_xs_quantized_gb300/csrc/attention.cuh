@@ -433,6 +433,19 @@ constexpr int kChunkBytes = 128;
 __device__ __forceinline__ uint32_t unit_at(int r, int u, int rows) {
     return (uint32_t)((u >> 3) * rows * kChunkBytes + r * kChunkBytes + (((u & 7) ^ (r & 7)) << 4));
 }
+// Shared-memory matrix descriptor, 128-byte swizzle.  K-major: sbo between
+// 8-row groups.  MN-major: lbo between 64-element chunks of the M/N axis, sbo
+// between 8-row groups of the K axis.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor, kind::f16, D fp32, M = 128; type 0 fp16, 1 bf16;
+// b_mn: B is N-major.
+constexpr uint32_t idesc_kv(int n, uint32_t type, bool b_mn) {
+    return (1u << 4) | (type << 7) | (type << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           (8u << 24);
+}
 // A box of K or V: from (chunk, slot) of a page and head on.
 __device__ __forceinline__ void tma_load_kv(uint32_t dst, const void* map, int slot, int chunk, int head, int page,
                                             uint64_t* bar) {

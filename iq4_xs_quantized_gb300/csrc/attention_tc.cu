@@ -110,19 +110,6 @@ struct TcAttn {
 constexpr int kSoftRegs = 208, kOtherRegs = 80;
 static_assert(kOtherRegs + kShares * kSoftRegs <= (1 + kShares) * 168, "register split within the launch's");
 
-// Shared-memory matrix descriptor, 128-byte swizzle.  K-major: sbo between
-// 8-row groups.  MN-major: lbo between 64-element chunks of the M/N axis, sbo
-// between 8-row groups of the K axis.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-// Instruction descriptor, kind::f16, D fp32, M = 128; type 0 fp16, 1 bf16;
-// b_mn: B is N-major.
-constexpr uint32_t idesc_kv(int n, uint32_t type, bool b_mn) {
-    return (1u << 4) | (type << 7) | (type << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
-           ((uint32_t)(kRowTile >> 4) << 24);
-}
 __device__ __forceinline__ void quad_sync(int quadrant) {
     asm volatile("bar.sync %0, %1;" ::"r"(quadrant + 1), "n"(32 * kShares) : "memory");
 }

@@ -73,6 +73,8 @@ cudaError_t launch_delta_inputs(const iq4xs_delta_inputs_args& a, const DeltaVie
                                 int num_sms, cudaStream_t stream);
 cudaError_t launch_delta_rule(const DeltaRule& p, const DeltaView& d, const BatchView& b, int* err, int num_sms,
                               cudaStream_t stream);
+cudaError_t launch_delta_chunk(const DeltaRule& p, const DeltaView& d, const BatchView& b, int* err,
+                               cudaStream_t stream);
 cudaError_t launch_delta_commit(const iq4xs_delta_commit_args& a, const DeltaView& d, const BatchView& b, int* err,
                                 cudaStream_t stream);
 cudaError_t launch_token_probs(const float* logits, int64_t logits_stride, int64_t rows, int64_t vocab,

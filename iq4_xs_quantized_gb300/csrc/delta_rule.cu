@@ -249,8 +249,7 @@ template <int DK, int VS>
 cudaError_t launch_rows(const DeltaRule& p, const DeltaView& d, const BatchView& b, int* err, cudaStream_t stream) {
     // Blocks of one row where a sequence has one; a tree is one block.
     if (p.max_rows == 1 || (p.u == nullptr && p.rows <= b.sequences)) return launch_step<DK, VS, 1>(p, d, b, err, stream);
-    if (p.u == nullptr || p.max_rows <= 16) return launch_step<DK, VS, 16>(p, d, b, err, stream);
-    return launch_step<DK, VS, 64>(p, d, b, err, stream);
+    return launch_step<DK, VS, 16>(p, d, b, err, stream);
 }
 
 template <int DK>
@@ -265,6 +264,9 @@ cudaError_t launch_keys(const DeltaRule& p, const DeltaView& d, const BatchView&
 
 cudaError_t launch_delta_rule(const DeltaRule& p, const DeltaView& d, const BatchView& b, int* err, int num_sms,
                               cudaStream_t stream) {
+    // A tree is one block; chains of more than 12 rows on average go in blocks of 64.
+    if (p.u != nullptr ? p.max_rows > 16 : p.rows > 12 * (int64_t)b.sequences && p.max_rows > 16)
+        return launch_delta_chunk(p, d, b, err, stream);
     return d.key_dim == 64 ? launch_keys<64>(p, d, b, err, num_sms, stream)
                            : launch_keys<128>(p, d, b, err, num_sms, stream);
 }
