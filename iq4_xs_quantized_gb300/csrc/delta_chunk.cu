@@ -26,6 +26,8 @@
 //
 // A row that holds NaN or infinities (or meets them in S) gives zeros to the
 // products and is marked; u and o of rows that come from it are made NaN after them.
+#include <type_traits>
+
 #include "attention.cuh"
 #include "delta.cuh"
 
@@ -33,19 +35,22 @@ namespace iq4xs {
 namespace {
 
 constexpr int kRows = kDeltaTreeRows;  // of a block
-constexpr int kMainWarps = 8, kPrepWarps = 4;
+constexpr int kMainWarps = 8, kPrepWarps = 8;
 constexpr int kMainThreads = 32 * kMainWarps, kPrepThreads = 32 * kPrepWarps;
 constexpr int kChunkThreads = kMainThreads + kPrepThreads;
 constexpr int kPitch = kRows + 4;      // of A and T in fp32
+// The main warps keep S; the others give up registers (the sum is the launch's).
+constexpr int kMainRegs = 168, kPrepRegs = 88;
+static_assert(kMainWarps * kMainRegs + kPrepWarps * kPrepRegs <= (kMainWarps + kPrepWarps) * 128, "register split");
 static_assert(kRows == 64, "a row of T or P is one swizzle row; the halves of the substitution are 32");
 
 // What a block's rows say, one set a buffer.
-struct Gates {
+struct __align__(16) Gates {
     float beta[kRows];
-    float gk[kRows];    // G_t, less the scale of k_t
+    float bg[kRows];    // -beta G_t, less the scale of k_t
     float gq[kRows];    // scale G_t, less that of q_t
     float left[kRows];  // F_nj, less the scale of k_j
-    float ct[kRows];    // what the rows of T and P were divided by
+    float ct[kRows];    // what the rows of T and P are to be multiplied by
     float cp[kRows];
     unsigned long long seen[kRows];
     unsigned long long odd;  // rows whose k or gates are not finite
@@ -62,14 +67,13 @@ struct ChunkShape {
     static constexpr int kT = kKq + 2 * kKqBytes;         // [buffer][hi, lo]
     static constexpr int kP = kT + 4 * kPartBytes;
     static constexpr int kV = kP + 4 * kPartBytes;
-    static constexpr int kA = kV + 2 * kVBytes;           // fp32
-    static constexpr int kTs = kA + kRows * kPitch * 4;
-    static constexpr int kX = kTs + kRows * kPitch * 4;   // [32][32]
-    static constexpr int kGates = kX + 32 * 32 * 4;
+    static constexpr int kA = kV + 2 * kVBytes;           // A and P in fp32
+    static constexpr int kTs = kA + 2 * kRows * kPitch * 4;
+    static constexpr int kGates = kTs + kRows * kPitch * 4;
     static constexpr int kTops = kGates + 2 * (int)sizeof(Gates);  // [S, r, u, u F][share][128] largest
     static constexpr int kOdd = kTops + 4 * 2 * 128 * 4;           // [r, u][share][128] rows not finite
-    static constexpr int kScales = kOdd + 2 * 2 * 128 * 4;         // [128] of K's and Q's rows; then their g
-    static constexpr int kBars = kScales + 2 * kRows * 4 + kRows * 4;
+    static constexpr int kScales = kOdd + 2 * 2 * 128 * 4;         // [128] of K's and Q's rows; their g; P's largest
+    static constexpr int kBars = kScales + 5 * kRows * 4;
     static constexpr int kMisc = kBars + 16 * 8;
     static constexpr int kSmem = kMisc + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -115,7 +119,70 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
     const float2 r = KvF16::unpack(hi);
     lo = KvF16::pack(a - r.x, b - r.y);
 }
+// Two bf16 values times a power of two in fp16.
+__device__ __forceinline__ uint32_t scaled16(uint32_t w, float f) {
+    const float2 x = KvBf16::unpack(w);
+    return KvF16::pack(x.x * f, x.y * f);
+}
+__device__ __forceinline__ uint4 lds_u128(uint32_t at) {
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+    return w;
+}
 __device__ __forceinline__ bool odd_value(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return fma2(a, b, make_float2(-0.f, -0.f)); }
+__device__ __forceinline__ float max3(float top, float a, float b) {  // of magnitudes
+    asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return top;
+}
+// Values that are not finite become 0; their places as bits, and the largest of
+// the others.  (Out of line, and called on a copy: the values stay in registers.)
+__device__ __noinline__ float take_odd_at(float2* x, uint32_t* places) {
+    float top = 0.f;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (odd_value(x[i].x)) {
+            bits |= 1u << (2 * i);
+            x[i].x = 0.f;
+        }
+        if (odd_value(x[i].y)) {
+            bits |= 2u << (2 * i);
+            x[i].y = 0.f;
+        }
+        top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+    }
+    *places = bits;
+    return top;
+}
+__device__ __forceinline__ float take_odd(float2 (&x)[16], uint32_t& bits) {
+    float2 copy[16];
+    uint32_t places;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) copy[i] = x[i];
+    const float top = take_odd_at(copy, &places);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = copy[i];
+    bits = places;
+    return top;
+}
+// Of rows first .. first + 31 those that come from rows marked in `odd`: zeros, and their places as bits.
+__device__ __noinline__ uint32_t hidden(const Gates& gt, int first, uint64_t odd) {
+    uint32_t bits = 0;
+    for (int i = 0; i < 32; ++i)
+        if ((gt.seen[first + i] | 1ull << (first + i)) & odd) bits |= 1u << i;
+    return bits;
+}
+__device__ __forceinline__ uint32_t hide(float2 (&x)[16], const Gates& gt, int first, uint64_t odd) {
+    const uint32_t bits = hidden(gt, first, odd);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (bits >> (2 * i) & 1) x[i].x = 0.f;
+        if (bits >> (2 * i + 1) & 1) x[i].y = 0.f;
+    }
+    return bits;
+}
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __grid_constant__ DeltaRule p,
@@ -178,96 +245,109 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
 
     if (warp >= kMainWarps) {
         // ------------------------------------------------ the next block's operands
+        // (Loops are kept small: a block's instructions are run through once,
+        // and unrolled they came from beyond the instruction caches.)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrepRegs));
         const int id = tid - kMainThreads;
         constexpr int kUnits = DK / 8, kDown = kPrepThreads / kUnits, kTimes = 2 * kRows / kDown;
         const int unit = id % kUnits;
-        float* const scales = reinterpret_cast<float*>(smem + C::kScales);  // what K's and Q's rows are to be divided by
-        float* const g_at = scales + 2 * kRows;
+        float* const scales = reinterpret_cast<float*>(smem + C::kScales);  // what K's and Q's rows are to be multiplied by
+        float* const g_at = scales + 2 * kRows;                             // in log2
+        float* const maxima = g_at + kRows;  // [half] of P's rows
         float* const A = reinterpret_cast<float*>(smem + C::kA);
         float* const Ts = reinterpret_cast<float*>(smem + C::kTs);
-        float* const X = reinterpret_cast<float*>(smem + C::kX);
-        uint4 raw[kTimes];
-        auto load = [&](int t0) {
-#pragma unroll
+        const int64_t k_extent = 2 * ((p.rows - 1) * p.k_row_stride + keys), q_extent = 2 * ((p.rows - 1) * p.q_row_stride + keys);
+        const int64_t v_extent = 2 * ((p.rows - 1) * p.v_row_stride + values);
+        int staged = -1;  // the last block whose rows this thread has asked for
+        // K, Q and V of a block as they lie, zeros behind the last row
+        auto stage = [&](int c) {
+            const int buf = c & 1, t0 = c * kRows, m = min(kRows, n - t0);
+            staged = c;
+#pragma unroll 4
             for (int i = 0; i < kTimes; ++i) {
                 const int r = id / kUnits + i * kDown, t = r % kRows;
                 const uint16_t* from = r < kRows ? p.k : p.q;
-                const int64_t stride = r < kRows ? p.k_row_stride : p.q_row_stride;
-                const uint16_t* at = from + (row0 + t0 + t) * stride + key_head * DK + 8 * unit;
-                raw[i] = make_uint4(0, 0, 0, 0);
-                if (t0 + t < n && bc_global(bc, at, 16, from, 2 * ((p.rows - 1) * stride + keys), kBcDeltaQkv))
-                    raw[i] = *reinterpret_cast<const uint4*>(at);
+                const uint16_t* at = from + (row0 + t0 + min(t, m - 1)) * (r < kRows ? p.k_row_stride : p.q_row_stride) +
+                                     key_head * DK + 8 * unit;
+                const bool in = t < m && bc_global(bc, at, 16, from, r < kRows ? k_extent : q_extent, kBcDeltaQkv);
+                cp_async16(base + C::kKq + buf * C::kKqBytes + unit_at(r, unit, 2 * kRows), at, in ? 16 : 0);
+            }
+#pragma unroll 2
+            for (int i = id; i < kRows * (DV / 8); i += kPrepThreads) {
+                const int t = i / (DV / 8), u = i % (DV / 8);
+                const uint16_t* at = p.v + (row0 + t0 + min(t, m - 1)) * p.v_row_stride + head * DV + 8 * u;
+                const bool in = t < m && bc_global(bc, at, 16, p.v, v_extent, kBcDeltaQkv);
+                cp_async16(base + C::kV + buf * C::kVBytes + (t * DV + 8 * u) * 2, at, in ? 16 : 0);
             }
         };
-        load(0);
         for (int c = 0; c < blocks; ++c) {
             const int buf = c & 1, t0 = c * kRows, m = min(kRows, n - t0);
             Gates& gt = gates[buf];
             bool lost = c >= 2 && !kv_wait(empty + buf, (c / 2 - 1) & 1, abort_flag, err, kDevErrTimeoutDelta);
             if (any_of<6, kPrepThreads>(lost)) break;  // (all leave together)
-            // V as it lies
-            for (int i = id; i < kRows * (DV / 8); i += kPrepThreads) {
-                const int t = i / (DV / 8), u = i % (DV / 8);
-                const uint16_t* at = p.v + (row0 + t0 + min(t, m - 1)) * p.v_row_stride + head * DV + 8 * u;
-                const bool in = t < m && bc_global(bc, at, 16, p.v, 2 * ((p.rows - 1) * p.v_row_stride + values), kBcDeltaQkv);
-                cp_async16(base + C::kV + buf * C::kVBytes + (t * DV + 8 * u) * 2, at, in ? 16 : 0);
-            }
-            if (id == 0) gt.odd = 0;
-            prep_sync();
+            const uint32_t kq_at = base + C::kKq + buf * C::kKqBytes;
+            if (staged != c) stage(c);
             if (id < kRows) {
                 const int64_t at = (int64_t)(row0 + t0 + id) * d.heads + head, extent = 4 * (int64_t)p.rows * d.heads;
                 float g = 0.f, beta = 0.f;
                 uint64_t seen = 0;
+                bool odd = false;
                 if (id < m) {
                     if (bc_global(bc, p.g + at, 4, p.g, extent, kBcDeltaGate)) g = p.g[at];
                     if (bc_global(bc, p.beta + at, 4, p.beta, extent, kBcDeltaGate)) beta = p.beta[at];
                     seen = delta_seen(p.tree_mask, p.mask_words, p.rows, row0, id, bc);
-                    if (odd_value(beta) || isnan(g) || g == INFINITY) {
-                        g = beta = 0.f;
-                        atomicOr(&gt.odd, 1ull << id);
-                    }
+                    odd = odd_value(beta) || isnan(g) || g == INFINITY;
+                    if (odd) g = beta = 0.f;
                 }
-                g_at[id] = g;
+                g_at[id] = g * 1.44269504088896340736f;
                 gt.beta[id] = beta;
                 gt.seen[id] = seen;
                 gt.left[id] = 0.f;
+                const unsigned bits = __ballot_sync(0xffffffffu, odd);
+                if (lane == 0) reinterpret_cast<unsigned*>(&gt.odd)[id / 32] = bits;
             }
-            // K and Q: fp16 as it is, bf16 with its row's largest at 2^13; a row of K that is not finite: zeros
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            prep_sync();
+            // K and Q for the products: fp16 as it is, bf16 with its row's largest
+            // brought to 2^13; a row of K that is not finite: zeros
+#pragma unroll 1
+            for (int i0 = 0; i0 < kTimes; i0 += 4) {
+                uint4 w[4];
+                uint32_t top[4];
 #pragma unroll
-            for (int i = 0; i < kTimes; ++i) {
-                const int r = id / kUnits + i * kDown;
-                uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-                const uint32_t exp = p.bf16 ? 0x7f80u : 0x7c00u;
-                bool odd = false;
+                for (int i = 0; i < 4; ++i)
+                    w[i] = lds_u128(kq_at + unit_at(id / kUnits + (i0 + i) * kDown, unit, 2 * kRows));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) odd |= (w[e] & exp) == exp || (w[e] >> 16 & exp) == exp;
-                const unsigned odd_lanes = __ballot_sync(0xffffffffu, odd) >> (lane / kUnits * kUnits) &
-                                           (kUnits == 32 ? 0xffffffffu : (1u << kUnits) - 1);
-                float inverse = 1.f;
-                if (p.bf16) {
-                    float x[8], top = 0.f;
-                    unpack8<KvBf16>(raw[i], x);
+                for (int i = 0; i < 4; ++i)
+                    top[i] = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                      __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+                for (int o = kUnits / 2; o > 0; o >>= 1)
 #pragma unroll
-                    for (int o = kUnits / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const float2 f = fit(top);
-                    inverse = f.y;
+                    for (int i = 0; i < 4; ++i) top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = KvF16::pack(x[2 * e] * f.x, x[2 * e + 1] * f.x);
+                for (int i = 0; i < 4; ++i) {
+                    const int r = id / kUnits + (i0 + i) * kDown;
+                    const uint32_t most = max(top[i] & 0xffffu, top[i] >> 16);
+                    const bool odd = most >= (p.bf16 ? 0x7f80u : 0x7c00u);
+                    float2 f = make_float2(1.f, 1.f);
+                    if (p.bf16) {
+                        f = fit(__uint_as_float(most << 16));
+                        w[i] = make_uint4(scaled16(w[i].x, f.x), scaled16(w[i].y, f.x), scaled16(w[i].z, f.x), scaled16(w[i].w, f.x));
+                    }
+                    if (odd && r < kRows) {
+                        w[i] = make_uint4(0, 0, 0, 0);
+                        if (unit == 0) atomicOr(&gt.odd, 1ull << r);
+                    }
+                    if (p.bf16 || odd) sts_u128(kq_at + unit_at(r, unit, 2 * kRows), w[i]);
+                    if (unit == 0) scales[r] = f.y;
                 }
-                if (odd_lanes != 0 && r < kRows) {
-                    w[0] = w[1] = w[2] = w[3] = 0;
-                    if (unit == 0) atomicOr(&gt.odd, 1ull << r);
-                }
-                sts_u128(base + C::kKq + buf * C::kKqBytes + unit_at(r, unit, 2 * kRows), make_uint4(w[0], w[1], w[2], w[3]));
-                if (unit == 0) scales[r] = inverse;
             }
             fence_proxy_async_smem();
             prep_sync();
             if (id == 0) {
                 tc_fence_after();
-                const uint64_t kq = desc_sw128(base + C::kKq + buf * C::kKqBytes, 16, 1024);
+                const uint64_t kq = desc_sw128(kq_at, 16, 1024);
 #pragma unroll
                 for (int k = 0; k < DK / 16; ++k) {
                     const uint64_t at = kq + (((k / 4) * 2 * kRows * kChunkBytes + (k % 4) * 32) >> 4);
@@ -275,67 +355,91 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 }
                 tc_commit(done_pairs);
             }
-            if (c + 1 < blocks) load(t0 + kRows);
-            // Row t of the pairs: A from the rows of K, P from those of Q.
-            const int t = id % kRows;
-            const bool is_q = id >= kRows;
-            lost = !kv_wait(done_pairs, c & 1, abort_flag, err, kDevErrTimeoutDelta);
-            tc_fence_after();
-            {
-                uint32_t x[kRows];
-                const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kPairs;
-                tmem_ld32_wait(at, x);
-                tmem_ld32_wait(at + 32, x + 32);
-                const uint64_t seen = gt.seen[t];
-                const float mine = scales[id];
-                const float factor = (is_q ? p.scale : gt.beta[t]) * mine;
-                float sum = 0.f, before = g_at[t], top = 0.f;
-#pragma unroll
-                for (int j = kRows - 1; j >= 0; --j) {
-                    const bool from = seen >> j & 1, self = j == t;
-                    if (from) {
-                        sum += before;
-                        before = g_at[j];
-                    }
-                    const float far = self ? 1.f : expf(sum);
-                    const float scaled = far * scales[j];
-                    const float y = from || (self && is_q) ? __uint_as_float(x[j]) * (factor * scaled) : 0.f;
-                    x[j] = __float_as_uint(y);
-                    top = fmaxf(top, fabsf(y));
-                    if (!is_q && t == m - 1 && (from || self)) gt.left[j] = scaled;
-                }
-                const float all = expf(sum + before);  // from the block's start
-                if (is_q) {
-                    gt.gq[t] = p.scale * all * mine;
-                    const float2 f = fit(top);
-                    gt.cp[t] = f.y;
-                    const uint32_t to = base + C::kP + buf * 2 * C::kPartBytes;
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            split2(__uint_as_float(x[8 * u + 2 * e]) * f.x, __uint_as_float(x[8 * u + 2 * e + 1]) * f.x, hi[e], lo[e]);
-                        sts_u128(to + unit_at(t, u, kRows), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                        sts_u128(to + C::kPartBytes + unit_at(t, u, kRows), make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                    }
-                } else {
-                    gt.gk[t] = all * mine;
-                    if (t == m - 1) gt.decay = all;
-#pragma unroll
-                    for (int j = 0; j < kRows; j += 4)
-                        *reinterpret_cast<uint4*>(A + t * kPitch + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+            // Half a row of the pairs: A from the rows of K, P from those of Q.
+            const int pair_row = (warp & 3) * 32 + lane, t = pair_row % kRows, half = (warp - kMainWarps) >> 2;
+            const bool is_q = pair_row >= kRows;
+            const uint32_t bits = (uint32_t)(gt.seen[t] >> (32 - 32 * half));  // half 0: columns 32 .. 63, then 0 .. 31
+            const float mine = scales[pair_row], factor = (is_q ? p.scale : gt.beta[t]) * mine;
+            const bool last = !is_q && t == m - 1;
+            float run = g_at[t], top = 0.f;  // the decay's logarithm from behind the column
+            if (half == 1) {
+                const uint32_t above = (uint32_t)(gt.seen[t] >> 32);
+#pragma unroll 2
+                for (int j = kRows - 4; j >= 32; j -= 4) {
+                    const float4 g = *reinterpret_cast<const float4*>(g_at + j);
+                    run += above >> (j - 29) & 1 ? g.w : 0.f;
+                    run += above >> (j - 30) & 1 ? g.z : 0.f;
+                    run += above >> (j - 31) & 1 ? g.y : 0.f;
+                    run += above >> (j - 32) & 1 ? g.x : 0.f;
                 }
             }
-            tc_fence_before();
-            prep_sync();
-            // T's diagonal halves, a column a thread.
-            if (id < kRows) {
-                const float* a = A + (id & 32) * (kPitch + 1);
-                float x[32];
+            float* const my_row = A + pair_row * kPitch;
+            lost = !kv_wait(done_pairs, c & 1, abort_flag, err, kDevErrTimeoutDelta);
+            tc_fence_after();
+#pragma unroll 1
+            for (int j0 = 16; j0 >= 0; j0 -= 16) {
+                const int col = 32 - 32 * half + j0;
+                uint32_t x[16];
+                tmem_ld16_wait(tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kPairs + col, x);
+                const int self = t - col;
+                float f[16], g[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float y[4] = {i == lane ? 1.f : 0.f, 0.f, 0.f, 0.f};
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 a = *reinterpret_cast<const float4*>(scales + col + j), e = *reinterpret_cast<const float4*>(g_at + col + j);
+                    f[j] = a.x; f[j + 1] = a.y; f[j + 2] = a.z; f[j + 3] = a.w;
+                    g[j] = e.x; g[j + 1] = e.y; g[j + 2] = e.z; g[j + 3] = e.w;
+                }
+#pragma unroll
+                for (int j = 15; j >= 0; --j) {
+                    const bool from = bits >> (j0 + j) & 1;
+                    f[j] *= self == j ? 1.f : from ? fast_exp2(run) : 0.f;
+                    run += from ? g[j] : 0.f;
+                    const float y = from || is_q ? __uint_as_float(x[j]) * (factor * f[j]) : 0.f;
+                    x[j] = __float_as_uint(f[j] == 0.f ? 0.f : y);  // (rows behind the last hold no values to scale)
+                    top = fmaxf(top, fabsf(__uint_as_float(x[j])));
+                }
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    *reinterpret_cast<uint4*>(my_row + col + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                    if (last) *reinterpret_cast<float4*>(gt.left + col + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+                }
+            }
+            if (half == 1) {
+                const float all = fast_exp2(run);  // from the block's start
+                if (is_q) gt.gq[t] = p.scale * all * mine;
+                else gt.bg[t] = -gt.beta[t] * all * mine;
+                if (last) gt.decay = all;
+            }
+            if (is_q) maxima[half * kRows + t] = top;
+            tc_fence_before();
+            // Part of a row in fp32 -> its parts
+            auto put_parts = [&](const float* row, int u0, int u1, float scale, uint32_t to, int r) {
+#pragma unroll 1
+                for (int u = u0; u < u1; ++u) {
+                    const float4 a = *reinterpret_cast<const float4*>(row + 8 * u), e = *reinterpret_cast<const float4*>(row + 8 * u + 4);
+                    uint32_t hi[4], lo[4];
+                    split2(a.x * scale, a.y * scale, hi[0], lo[0]);
+                    split2(a.z * scale, a.w * scale, hi[1], lo[1]);
+                    split2(e.x * scale, e.y * scale, hi[2], lo[2]);
+                    split2(e.z * scale, e.w * scale, hi[3], lo[3]);
+                    sts_u128(to + unit_at(r, u, kRows), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                    sts_u128(to + C::kPartBytes + unit_at(r, u, kRows), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                }
+            };
+            prep_sync();
+            // T by halves: its diagonal blocks of 16 by substitution, a column a
+            // thread; then the blocks below, -T22 (A21 T11), of 16 and of 32.
+            if (is_q) {
+                const float2 f = fit(fmaxf(maxima[t], maxima[kRows + t]));
+                gt.cp[t] = f.y;
+                put_parts(my_row, 4 - 4 * half, 8 - 4 * half, f.x, base + C::kP + buf * 2 * C::kPartBytes, t);
+            } else if (half == 0) {
+                const int at = t / 16 * 16, col = t % 16;
+                const float* a = A + at * (kPitch + 1);
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float y[4] = {i == col ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int j = 0; j < i; j += 4) {
                         const float4 w = *reinterpret_cast<const float4*>(a + i * kPitch + j);
@@ -345,70 +449,74 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                         if (j + 3 < i) y[3] = fmaf(-w.w, x[j + 3], y[3]);
                     }
                     x[i] = (y[0] + y[1]) + (y[2] + y[3]);
-                    Ts[((id & 32) + i) * kPitch + id] = x[i];
+                    Ts[(at + i) * kPitch + t] = x[i];
                 }
             }
+            if (c + 1 < blocks && (c < 1 || mbar_try_wait(smem_u32(empty + (buf ^ 1)), ((c + 1) / 2 - 1) & 1))) stage(c + 1);
             prep_sync();
-            // The half below: -T22 (A21 T11), eight rows of a column a thread.
-            auto product = [&](const float* left, int pitch, const float* right, int right_pitch, float (&y)[8]) {
-                float x[32];
+            // N x N blocks, R rows of a column a thread: X = A21 T11 into the
+            // empty block above, then T21 = -T22 X.
+            auto below = [&](auto n_tag, auto r_tag, int at, int col, int rows_at) {
+                constexpr int N = decltype(n_tag)::value, R = decltype(r_tag)::value;
+#pragma unroll 1
+                for (int pass = 0; pass < 2; ++pass) {
+                    const float* left = (pass == 0 ? A + (at + N + rows_at) * kPitch + at : Ts + (at + N + rows_at) * kPitch + at + N);
+                    const float* right = Ts + at * kPitch + at + col + (pass == 0 ? 0 : N);
+                    float z[R][4] = {};
 #pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] = right[j * right_pitch + lane];
+                    for (int j0 = 0; j0 < N; j0 += 16) {
+                        float x[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float z[4] = {0.f, 0.f, 0.f, 0.f};
+                        for (int j = 0; j < 16; ++j) x[j] = right[(j0 + j) * kPitch];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 w = *reinterpret_cast<const float4*>(left + i * pitch + j);
-                        z[0] = fmaf(w.x, x[j], z[0]);
-                        z[1] = fmaf(w.y, x[j + 1], z[1]);
-                        z[2] = fmaf(w.z, x[j + 2], z[2]);
-                        z[3] = fmaf(w.w, x[j + 3], z[3]);
+                        for (int i = 0; i < R; ++i) {
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 w = *reinterpret_cast<const float4*>(left + i * kPitch + j0 + j);
+                                z[i][0] = fmaf(w.x, x[j], z[i][0]);
+                                z[i][1] = fmaf(w.y, x[j + 1], z[i][1]);
+                                z[i][2] = fmaf(w.z, x[j + 2], z[i][2]);
+                                z[i][3] = fmaf(w.w, x[j + 3], z[i][3]);
+                            }
+                        }
                     }
-                    y[i] = (z[0] + z[1]) + (z[2] + z[3]);
+                    float* to = pass == 0 ? Ts + (at + rows_at) * kPitch + at + N + col : Ts + (at + N + rows_at) * kPitch + at + col;
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        const float y = (z[i][0] + z[i][1]) + (z[i][2] + z[i][3]);
+                        to[i * kPitch] = pass == 0 ? y : -y;
+                    }
+                    prep_sync();
+                }
+                if (N == 16) {  // what is above the diagonal is zero to the next level
+#pragma unroll
+                    for (int i = 0; i < R; ++i) Ts[(at + rows_at + i) * kPitch + at + N + col] = 0.f;
+                    prep_sync();
                 }
             };
-            const int r8 = 8 * (warp - kMainWarps);
-            if (m > 32) {  // (else the half below is of empty rows)
-                float y[8];
-                product(A + (32 + r8) * kPitch, kPitch, Ts, kPitch, y);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) X[(r8 + i) * 32 + lane] = y[i];
-                prep_sync();
-                product(Ts + (32 + r8) * kPitch + 32, kPitch, X, 32, y);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) Ts[(32 + r8 + i) * kPitch + lane] = -y[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) Ts[(32 + r8 + i) * kPitch + lane] = 0.f;
-            }
-            prep_sync();
+            below(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{}, id / 128 * 32, id % 16, id % 128 / 16 * 2);
+            below(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{}, 0, lane, (warp - kMainWarps) * 4);
             {
-                const int row = id / 2, half = id % 2;
-                const bool zero = row < 32 && half == 1;
-                float x[32], top = 0.f;
+                // A quarter of a row a thread (above the diagonal lies what was left of X).
+                const int row = id / 4, quarter = id % 4, lim = row - 16 * quarter;
+                float* const mine_at = Ts + row * kPitch + 16 * quarter;
+                float most = 0.f;
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 w = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                          : *reinterpret_cast<const float4*>(Ts + row * kPitch + 32 * half + j);
-                    x[j] = w.x; x[j + 1] = w.y; x[j + 2] = w.z; x[j + 3] = w.w;
+                for (int j = 0; j < 16; j += 4) {
+                    float4 w = *reinterpret_cast<const float4*>(mine_at + j);
+                    w.x = j <= lim ? w.x : 0.f;
+                    w.y = j + 1 <= lim ? w.y : 0.f;
+                    w.z = j + 2 <= lim ? w.z : 0.f;
+                    w.w = j + 3 <= lim ? w.w : 0.f;
+                    most = fmaxf(fmaxf(fmaxf(most, fabsf(w.x)), fmaxf(fabsf(w.y), fabsf(w.z))), fabsf(w.w));
+                    *reinterpret_cast<float4*>(mine_at + j) = w;
                 }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) top = fmaxf(top, fabsf(x[j]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                const float2 f = fit(top);
-                if (half == 0) gt.ct[row] = f.y;
-                const uint32_t to = base + C::kT + buf * 2 * C::kPartBytes;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) split2(x[8 * u + 2 * e] * f.x, x[8 * u + 2 * e + 1] * f.x, hi[e], lo[e]);
-                    sts_u128(to + unit_at(row, 4 * half + u, kRows), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                    sts_u128(to + C::kPartBytes + unit_at(row, 4 * half + u, kRows), make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                }
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                const float2 f = fit(most);
+                if (quarter == 0) gt.ct[row] = f.y;
+                put_parts(Ts + row * kPitch, 2 * quarter, 2 * quarter + 2, f.x, base + C::kT + buf * 2 * C::kPartBytes, row);
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
             if (any_of<6, kPrepThreads>(lost)) break;
             mbar_arrive(full + buf);
@@ -421,6 +529,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         }
     } else {
         // ------------------------------------------------------------ the blocks
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMainRegs));
         const int quad = warp & 3, share = warp >> 2, at_lane = quad * 32 + lane;
         const bool busy = quad < C::kQuads;  // the warp has value channels
         const uint32_t lane_at = tmem + ((uint32_t)(quad * 32) << 16);
@@ -431,35 +540,43 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             tops[(what * 2 + share) * 128 + at_lane] = mine;
         };
         auto largest_of = [&](int what) { return fmaxf(tops[what * 256 + at_lane], tops[what * 256 + 128 + at_lane]); };
-        float S[C::kHalf];
+        float2 S[C::kHalf / 2];
 #pragma unroll
         for (int i = 0; i < C::kHalf; ++i) {
             const float* from = at_s + i * DV;
-            S[i] = busy && len > 0 && bc_global(bc, from, 4, d.s, d.s_extent, kBcDeltaS) ? *from : 0.f;
+            const float x = busy && len > 0 && bc_global(bc, from, 4, d.s, d.s_extent, kBcDeltaS) ? *from : 0.f;
+            (i & 1 ? S[i / 2].y : S[i / 2].x) = x;
         }
         float inverse_s = 1.f;
+        // Two neighbouring values -> their parts.
+        auto split = [&](float2 x, float scale, uint32_t& hi, uint32_t& lo) {
+            x = mul2(x, make_float2(scale, scale));
+            hi = KvF16::pack(x.x, x.y);
+            const float2 r = fma2(KvF16::unpack(hi), make_float2(-1.f, -1.f), x);
+            lo = KvF16::pack(r.x, r.y);
+        };
         // S into its parts.
         auto put_state = [&] {
             float top = 0.f;
 #pragma unroll
-            for (int i = 0; i < C::kHalf; ++i) top = fmaxf(top, fabsf(S[i]));
+            for (int i = 0; i < C::kHalf / 2; ++i) top = max3(top, S[i].x, S[i].y);
             largest(0, top);
             pair_sync(quad);
             const float2 f = fit(largest_of(0));
             inverse_s = f.y;
 #pragma unroll
-            for (int i = 0; i < C::kHalf; i += 32) {
+            for (int i = 0; i < C::kHalf / 2; i += 16) {
                 uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) split2(S[i + 2 * e] * f.x, S[i + 2 * e + 1] * f.x, hi[e], lo[e]);
-                tmem_st16(lane_at + C::kParts + (share * C::kHalf + i) / 2, hi);
-                tmem_st16(lane_at + C::kParts + DK / 2 + (share * C::kHalf + i) / 2, lo);
+                for (int e = 0; e < 16; ++e) split(S[i + e], f.x, hi[e], lo[e]);
+                tmem_st16(lane_at + C::kParts + share * C::kHalf / 2 + i, hi);
+                tmem_st16(lane_at + C::kParts + DK / 2 + share * C::kHalf / 2 + i, lo);
             }
             tmem_wait_st();
         };
         if (busy) put_state();
         bool lost = false;
-        float o[32];
+        float2 o[16];
         int o_rows = 0;          // rows of `o` on their way out
         int64_t o_first = 0;
         auto put_rows = [&] {
@@ -468,7 +585,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
 #pragma unroll
             for (int i = 0; i < 32; ++i, to += p.out_row_stride)
                 if (i < o_rows && bc_global(bc, to, 4, p.out, 4 * ((p.rows - 1) * p.out_row_stride + values), kBcDeltaOut))
-                    *to = o[i];
+                    *to = i & 1 ? o[i / 2].y : o[i / 2].x;
         };
         for (int c = 0; c < blocks; ++c) {
             const int buf = c & 1, t0 = c * kRows, m = min(kRows, n - t0);
@@ -500,17 +617,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 uint32_t x[32];
                 tmem_ld32_wait(lane_at + C::kD + first, x);
                 const uint16_t* v = reinterpret_cast<const uint16_t*>(smem + C::kV + buf * C::kVBytes) + first * DV + at_lane;
+                const float2 inverse2 = make_float2(inverse_s, inverse_s);
+                float2 r[16], zero = make_float2(0.f, 0.f);
                 float top = 0.f;
                 uint32_t bits = 0;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const uint32_t raw = v[i * DV];
-                    const float value = p.bf16 ? __uint_as_float(raw << 16) : KvF16::unpack(raw).x;
-                    const float y = gt.beta[first + i] * (value - gt.gk[first + i] * (inverse_s * __uint_as_float(x[i])));
-                    if (odd_value(y)) bits |= 1u << i;
-                    x[i] = odd_value(y) ? 0 : __float_as_uint(y);
-                    top = fmaxf(top, fabsf(__uint_as_float(x[i])));
+                for (int i = 0; i < 16; i += 2) {
+                    const float4 beta = *reinterpret_cast<const float4*>(gt.beta + first + 2 * i);
+                    const float4 bg = *reinterpret_cast<const float4*>(gt.bg + first + 2 * i);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t both = v[(2 * (i + e)) * DV] | (uint32_t)v[(2 * (i + e) + 1) * DV] << 16;
+                        const float2 value = p.bf16 ? KvBf16::unpack(both) : KvF16::unpack(both);
+                        const float2 xs = make_float2(__uint_as_float(x[2 * (i + e)]), __uint_as_float(x[2 * (i + e) + 1]));
+                        r[i + e] = fma2(mul2(xs, inverse2), e ? make_float2(bg.z, bg.w) : make_float2(bg.x, bg.y),
+                                        mul2(value, e ? make_float2(beta.z, beta.w) : make_float2(beta.x, beta.y)));
+                        zero = fma2(r[i + e], make_float2(0.f, 0.f), zero);
+                        top = max3(top, r[i + e].x, r[i + e].y);
+                    }
                 }
+                if (!(zero.x + zero.y == 0.f)) top = take_odd(r, bits);  // (NaN)
                 largest(1, top);
                 odds[share * 128 + at_lane] = bits;
                 pair_sync(quad);
@@ -519,8 +645,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 inverse_r = f.y;
                 uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    split2(__uint_as_float(x[2 * e]) * f.x, __uint_as_float(x[2 * e + 1]) * f.x, hi[e], lo[e]);
+                for (int e = 0; e < 16; ++e) split(r[e], f.x, hi[e], lo[e]);
                 tmem_st16(lane_at + C::kR + first / 2, hi);
                 tmem_st16(lane_at + C::kR + kRows / 2 + first / 2, lo);
                 tmem_wait_st();
@@ -544,34 +669,38 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 tc_fence_after();
                 uint32_t x[32];
                 tmem_ld32_wait(lane_at + C::kD + first, x);
-                float top = 0.f, top_f = 0.f;
+                float2 u[16], zero = make_float2(0.f, 0.f);
+                const float2 inverse2 = make_float2(inverse_r, inverse_r);
                 uint32_t bits = 0;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float y = __uint_as_float(x[i]) * inverse_r * gt.ct[first + i];
-                    if (odd_value(y)) bits |= 1u << i;
-                    x[i] = odd_value(y) ? 0 : __float_as_uint(y);
+                for (int i = 0; i < 16; i += 2) {
+                    const float4 ct = *reinterpret_cast<const float4*>(gt.ct + first + 2 * i);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 xs = make_float2(__uint_as_float(x[2 * (i + e)]), __uint_as_float(x[2 * (i + e) + 1]));
+                        u[i + e] = mul2(mul2(xs, inverse2), e ? make_float2(ct.z, ct.w) : make_float2(ct.x, ct.y));
+                        zero = fma2(u[i + e], make_float2(0.f, 0.f), zero);
+                    }
                 }
+                if (!(zero.x + zero.y == 0.f)) take_odd(u, bits);
                 odds[256 + share * 128 + at_lane] = bits;
-                if (odd != 0) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if ((gt.seen[first + i] | 1ull << (first + i)) & odd) {
-                            bits |= 1u << i;
-                            x[i] = 0;
-                        }
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    top = fmaxf(top, fabsf(__uint_as_float(x[i])));
-                    top_f = fmaxf(top_f, fabsf(__uint_as_float(x[i]) * gt.left[first + i]));
-                }
+                if (odd != 0) bits |= hide(u, gt, first, odd);
                 if (keep) {
                     float* to = p.u + ((int64_t)(row0 + t0 + first) * d.heads + head) * DV + at_lane;
 #pragma unroll
                     for (int i = 0; i < 32; ++i, to += values)
                         if (first + i < m && bc_global(bc, to, 4, p.u, 4 * p.rows * values, kBcDeltaU))
-                            *to = bits >> i & 1 ? NAN : __uint_as_float(x[i]);
+                            *to = bits >> i & 1 ? NAN : i & 1 ? u[i / 2].y : u[i / 2].x;
+                }
+                float top = 0.f, top_f = 0.f;
+                float2 w[16];
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float4 left = *reinterpret_cast<const float4*>(gt.left + first + 2 * i);
+                    w[i] = mul2(u[i], make_float2(left.x, left.y));
+                    w[i + 1] = mul2(u[i + 1], make_float2(left.z, left.w));
+                    top = max3(max3(top, u[i].x, u[i].y), u[i + 1].x, u[i + 1].y);
+                    top_f = max3(max3(top_f, w[i].x, w[i].y), w[i + 1].x, w[i + 1].y);
                 }
                 largest(2, top);
                 largest(3, top_f);
@@ -581,19 +710,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 inverse_u = f.y;
                 inverse_f = ff.y;
                 uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    split2(__uint_as_float(x[2 * e]) * f.x, __uint_as_float(x[2 * e + 1]) * f.x, hi[e], lo[e]);
-                tmem_st16(lane_at + C::kParts + first / 2, hi);
-                tmem_st16(lane_at + C::kParts + kRows / 2 + first / 2, lo);
                 if (!keep) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        split2(__uint_as_float(x[2 * e]) * gt.left[first + 2 * e] * ff.x,
-                               __uint_as_float(x[2 * e + 1]) * gt.left[first + 2 * e + 1] * ff.x, hi[e], lo[e]);
+                    for (int e = 0; e < 16; ++e) split(w[e], ff.x, hi[e], lo[e]);
                     tmem_st16(lane_at + C::kParts + kRows + first / 2, hi);
                     tmem_st16(lane_at + C::kParts + kRows + kRows / 2 + first / 2, lo);
                 }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) split(u[e], f.x, hi[e], lo[e]);
+                tmem_st16(lane_at + C::kParts + first / 2, hi);
+                tmem_st16(lane_at + C::kParts + kRows / 2 + first / 2, lo);
                 tmem_wait_st();
             }
             tc_fence_before();
@@ -623,17 +749,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 lost |= !kv_wait(done_s, c & 1, abort_flag, err, kDevErrTimeoutDelta);
                 if (busy) {
                     tc_fence_after();
-                    const float decay = gt.decay;
+                    const float2 decay2 = make_float2(gt.decay, gt.decay), inverse2 = make_float2(inverse_f, inverse_f);
 #pragma unroll
                     for (int i = 0; i < C::kHalf; i += 32) {
                         uint32_t x[32];
                         tmem_ld32_wait(lane_at + C::kNew + share * C::kHalf + i, x);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) S[i + e] = fmaf(decay, S[i + e], inverse_f * __uint_as_float(x[e]));
+                        for (int e = 0; e < 16; ++e)
+                            S[i / 2 + e] = fma2(S[i / 2 + e], decay2,
+                                                mul2(inverse2, make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]))));
                     }
                     if (odd != 0) {
 #pragma unroll
-                        for (int i = 0; i < C::kHalf; ++i) S[i] = NAN;
+                        for (int i = 0; i < C::kHalf / 2; ++i) S[i] = make_float2(NAN, NAN);
                     }
                 }
             }
@@ -643,14 +771,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 uint32_t x[32], y[32];
                 tmem_ld32_wait(lane_at + C::kD + first, x);
                 tmem_ld32_wait(lane_at + C::kD + kRows + first, y);
+                const float2 inv_s = make_float2(inverse_s, inverse_s), inv_u = make_float2(inverse_u, inverse_u);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    o[i] = fmaf(gt.gq[first + i] * inverse_s, __uint_as_float(y[i]),
-                                gt.cp[first + i] * inverse_u * __uint_as_float(x[i]));
+                for (int i = 0; i < 16; i += 2) {
+                    const float4 gq = *reinterpret_cast<const float4*>(gt.gq + first + 2 * i);
+                    const float4 cp = *reinterpret_cast<const float4*>(gt.cp + first + 2 * i);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int k = 2 * (i + e);
+                        const float2 xs = make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                        const float2 ys = make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+                        o[i + e] = fma2(mul2(ys, inv_s), e ? make_float2(gq.z, gq.w) : make_float2(gq.x, gq.y),
+                                        mul2(mul2(xs, inv_u), e ? make_float2(cp.z, cp.w) : make_float2(cp.x, cp.y)));
+                    }
+                }
                 if (odd != 0) {
+                    const uint32_t gone = hide(o, gt, first, odd);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if ((gt.seen[first + i] | 1ull << (first + i)) & odd) o[i] = NAN;
+                    for (int i = 0; i < 16; ++i) {
+                        if (gone >> (2 * i) & 1) o[i].x = NAN;
+                        if (gone >> (2 * i + 1) & 1) o[i].y = NAN;
+                    }
                 }
                 o_rows = m - first;
                 o_first = row0 + t0 + first;
@@ -664,7 +805,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         if (!keep && busy && !lost) {
 #pragma unroll
             for (int i = 0; i < C::kHalf; ++i)
-                if (bc_global(bc, at_s + i * DV, 4, d.s, d.s_extent, kBcDeltaS)) at_s[i * DV] = S[i];
+                if (bc_global(bc, at_s + i * DV, 4, d.s, d.s_extent, kBcDeltaS))
+                    at_s[i * DV] = i & 1 ? S[i / 2].y : S[i / 2].x;
         }
         if (*abort_flag && tid == 0) {
             tc_commit(drained);
