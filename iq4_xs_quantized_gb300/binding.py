@@ -643,11 +643,15 @@ def iq4xs_cache_copy_pages(cache: KVCache, src, dst, stream=None) -> None:
 # --------------------------------------------------------------------------
 # The recurrent layers of a step, and its verification.
 # --------------------------------------------------------------------------
-def _need_device(fn: str, *tensors):
-    """All of them (None aside) on the current device, the one that a call runs on."""
-    at = {t.get_device() for t in tensors if t is not None}
-    if -1 in at or at != {torch.cuda.current_device() if _raw_device is None else _raw_device()}:
-        raise ValueError(f"{fn}: tensors must be on the current CUDA device")
+def _wrong_device(fn: str):
+    raise ValueError(f"{fn}: tensors must be on the current CUDA device")
+
+
+def _device() -> int:
+    """The current device, the one that a call runs on (-2 without one)."""
+    if not torch.cuda.is_initialized():
+        return torch.cuda.current_device() if torch.cuda.is_available() else -2
+    return torch.cuda.current_device() if _raw_device is None else _raw_device()
 
 
 class DeltaState:
@@ -672,7 +676,7 @@ class DeltaState:
         if slot_of is not None:
             _need_i32("DeltaState", slot_of=slot_of)
         _need(all(t is None or t.device == s.device for t in (conv, slot_of)), "DeltaState", "tensors of one device")
-        self.s, self.conv, self.slot_of = s, conv, slot_of
+        self.s, self.conv, self.slot_of, self.device = s, conv, slot_of, s.get_device()
         self.mapped = None if slot_of is None else slot_of.numel()
         conv_strides = (0, 0) if conv is None else conv.stride()[:2]
         self.desc = struct.pack("<13q", s.data_ptr(), _addr(conv), _addr(slot_of), self.layers, self.slots, key_heads,
@@ -697,40 +701,34 @@ _DELTA_COMMIT = struct.Struct("<15q").pack
 _VERIFY = struct.Struct("<15q").pack
 
 
-def _need_rows16(fn: str, m: int, what: str, t, heads: int, dim: int):
-    """t is 16-bit [m, heads, dim], heads and channels contiguous; its row stride."""
-    if not (t.shape == (m, heads, dim) and t.stride(2) == 1 and (t.stride(1) == dim or heads == 1)):
-        raise ValueError(f"{fn}: {what} is [M, {heads}, {dim}], heads and channels contiguous")
-    return t.stride(0) if m > 1 else heads * dim
-
-
-def _need_f32(fn: str, what: str, t, shape):
-    if not (t.dtype is torch.float32 and t.shape == shape and t.is_contiguous()):
-        raise ValueError(f"{fn}: {what} is contiguous float32 {list(shape)}")
-
-
-def _need_cols(fn: str, what: str, t, m: int, n: int) -> int:
-    """t is fp32 [m, n], columns contiguous; its row stride."""
-    if not (t.dtype is torch.float32 and t.shape == (m, n) and (t.stride(1) == 1 or n == 1)):
-        raise ValueError(f"{fn}: {what} is float32 [{m}, {n}], columns contiguous")
-    return t.stride(0) if m > 1 else n
-
-
-def _need_mask(fn: str, tree_mask, m: int) -> int:
-    if tree_mask is None:
-        return 0
+# (These checks are most of a small call's time: each property of a tensor is
+# asked for once, and messages are made where a check has failed.)
+def _mask_words(fn: str, tree_mask, m: int) -> int:
     if tree_mask.dtype not in (torch.int64, torch.uint64):
         raise TypeError(f"{fn}: tree_mask must be int64")
-    if not (tree_mask.dim() == 2 and tree_mask.shape[0] == m and tree_mask.is_contiguous()):
+    shape = tree_mask.shape
+    if not (len(shape) == 2 and shape[0] == m and tree_mask.is_contiguous()):
         raise ValueError(f"{fn}: tree_mask is [M, words]")
-    return tree_mask.shape[1]
+    return shape[1]
 
 
-def _need_16(fn: str, *tensors):
-    dt = tensors[0].dtype
-    if dt not in KV_DTYPES or any(t.dtype is not dt for t in tensors):
+def _need_operands(fn: str, M: int, q, k, v, g, beta, st):
+    """q, k, v, g and beta as the delta rule takes them; row strides of the first three and their type."""
+    dt = KV_DTYPES.get(q.dtype)
+    if dt is None or k.dtype is not q.dtype or v.dtype is not q.dtype:
         raise TypeError(f"{fn}: q, k and v must be float16 or bfloat16, all the same")
-    return KV_DTYPES[dt]
+    hk, hv, dk, dv = st.key_heads, st.heads, st.key_dim, st.value_dim
+    keys = (M, hk, dk)
+    if not (q.shape == keys and k.shape == keys and v.shape == (M, hv, dv)):
+        raise ValueError(f"{fn}: q and k are [M, Hk, Dk], v [M, Hv, Dv]")
+    (qr, qh, qc), (kr, kh, kc), (vr, vh, vc) = q.stride(), k.stride(), v.stride()
+    if not (qc == 1 and kc == 1 and vc == 1 and (hk == 1 or (qh == dk and kh == dk)) and (hv == 1 or vh == dv)):
+        raise ValueError(f"{fn}: heads and channels of q, k and v must be contiguous")
+    gates = (M, hv)
+    if not (g.dtype is torch.float32 and beta.dtype is torch.float32 and g.shape == gates and beta.shape == gates and
+            g.is_contiguous() and beta.is_contiguous()):
+        raise ValueError(f"{fn}: g and beta are contiguous float32 [M, Hv]")
+    return (qr, kr, vr, dt) if M > 1 else (hk * dk, hk * dk, hv * dv, dt)
 
 
 def iq4xs_delta_inputs(x, conv_weight, a, b, a_log, dt_bias, eps: float, q, k, v, g, beta, state: DeltaState, layer: int,
@@ -741,25 +739,44 @@ def iq4xs_delta_inputs(x, conv_weight, a, b, a_log, dt_bias, eps: float, q, k, v
     iq4xs_tree_attention; None: chains) and the state's last inputs, SiLU, unit
     norm of q and k; g = -exp(a_log) softplus(a + dt_bias), beta = sigmoid(b).
     advance: the state's inputs move on behind the rows (chains only)."""
-    fn = "iq4xs_delta_inputs"
-    M, c, st = x.shape[0], state.channels, state
-    st._check_batch(fn, batch)
-    dt = _need_16(fn, q, k, v)
-    _need(st.conv is not None, fn, "the state has no inputs (conv)")
-    xs = _need_cols(fn, "x", x, M, c)
-    a_s, b_s = _need_cols(fn, "a", a, M, st.heads), _need_cols(fn, "b", b, M, st.heads)
-    _need_f32(fn, "conv_weight", conv_weight, (c, 4))
-    _need_f32(fn, "a_log", a_log, (st.heads,))
-    _need_f32(fn, "dt_bias", dt_bias, (st.heads,))
-    qs, ks = _need_rows16(fn, M, "q", q, st.key_heads, st.key_dim), _need_rows16(fn, M, "k", k, st.key_heads, st.key_dim)
-    vs = _need_rows16(fn, M, "v", v, st.heads, st.value_dim)
-    _need_f32(fn, "g", g, (M, st.heads))
-    _need_f32(fn, "beta", beta, (M, st.heads))
-    words = _need_mask(fn, tree_mask, M)
-    _need_device(fn, st.s, x, conv_weight, a, b, a_log, dt_bias, q, k, v, g, beta, tree_mask)
-    args = _DELTA_INPUTS(x.data_ptr(), xs, conv_weight.data_ptr(), a.data_ptr(), b.data_ptr(), a_s, b_s, a_log.data_ptr(),
-                         dt_bias.data_ptr(), eps, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, dt, g.data_ptr(),
-                         beta.data_ptr(), _addr(tree_mask), words, 1 if advance else 0, M, layer)
+    fn, f32 = "iq4xs_delta_inputs", torch.float32
+    M, c = x.shape
+    hv, st = state.heads, state
+    if st.mapped is not None:
+        st._check_batch(fn, batch)
+    qr, kr, vr, dt = _need_operands(fn, M, q, k, v, g, beta, st)
+    if st.conv is None:
+        raise ValueError(f"{fn}: the state has no inputs (conv)")
+    if not (x.dtype is f32 and a.dtype is f32 and b.dtype is f32 and conv_weight.dtype is f32 and a_log.dtype is f32 and
+            dt_bias.dtype is f32):
+        raise TypeError(f"{fn}: x, a, b, conv_weight, a_log and dt_bias must be float32")
+    (xr, xc), (ar, ac), (br, bc) = x.stride(), a.stride(), b.stride()
+    if not (c == st.channels and xc == 1):
+        raise ValueError(f"{fn}: x is [M, channels], channels contiguous")
+    gates = (M, hv)
+    if not (a.shape == gates and b.shape == gates and (hv == 1 or (ac == 1 and bc == 1))):
+        raise ValueError(f"{fn}: a and b are [M, Hv], heads contiguous")
+    if not (conv_weight.shape == (c, 4) and conv_weight.is_contiguous()):
+        raise ValueError(f"{fn}: conv_weight is contiguous [channels, 4]")
+    heads = (hv,)
+    if not (a_log.shape == heads and dt_bias.shape == heads and a_log.is_contiguous() and dt_bias.is_contiguous()):
+        raise ValueError(f"{fn}: a_log and dt_bias are contiguous [Hv]")
+    mask, words = 0, 0
+    dev = _device()
+    if tree_mask is not None:
+        words = _mask_words(fn, tree_mask, M)
+        mask = tree_mask.data_ptr()
+        if tree_mask.get_device() != dev:
+            _wrong_device(fn)
+    if not (dev == st.device == x.get_device() == conv_weight.get_device() == a.get_device() == b.get_device() ==
+            a_log.get_device() == dt_bias.get_device() == q.get_device() == k.get_device() == v.get_device() ==
+            g.get_device() == beta.get_device()):
+        _wrong_device(fn)
+    if M == 1:
+        xr, ar, br = c, hv, hv
+    args = _DELTA_INPUTS(x.data_ptr(), xr, conv_weight.data_ptr(), a.data_ptr(), b.data_ptr(), ar, br, a_log.data_ptr(),
+                         dt_bias.data_ptr(), eps, q.data_ptr(), k.data_ptr(), v.data_ptr(), qr, kr, vr, dt, g.data_ptr(),
+                         beta.data_ptr(), mask, words, 1 if advance else 0, M, layer)
     rc = (_lib or load()).iq4xs_delta_inputs(args, st.desc, batch.desc, _stream(stream))
     if rc:
         _check(fn, rc)
@@ -772,21 +789,33 @@ def iq4xs_delta_rule(q, k, v, g, beta, scale: float, out, state: DeltaState, lay
     u (fp32 [M, Hv, Dv], written: what iq4xs_delta_commit takes) the state stays
     and every row starts from its parent's (tree_mask; None: a chain), at most 64
     rows a sequence.  max_rows: no sequence has more rows (None: not known)."""
-    fn = "iq4xs_delta_rule"
-    M, st = q.shape[0], state
-    st._check_batch(fn, batch)
-    dt = _need_16(fn, q, k, v)
-    qs, ks = _need_rows16(fn, M, "q", q, st.key_heads, st.key_dim), _need_rows16(fn, M, "k", k, st.key_heads, st.key_dim)
-    vs = _need_rows16(fn, M, "v", v, st.heads, st.value_dim)
-    _need_f32(fn, "g", g, (M, st.heads))
-    _need_f32(fn, "beta", beta, (M, st.heads))
-    outs = _need_cols(fn, "out", out, M, st.heads * st.value_dim)
+    fn, st = "iq4xs_delta_rule", state
+    M = q.shape[0]
+    if st.mapped is not None:
+        st._check_batch(fn, batch)
+    qr, kr, vr, dt = _need_operands(fn, M, q, k, v, g, beta, st)
+    n = st.heads * st.value_dim
+    outr, outc = out.stride()
+    if not (out.dtype is torch.float32 and out.shape == (M, n) and outc == 1):
+        raise ValueError(f"{fn}: out is float32 [M, Hv * Dv], columns contiguous")
+    dev = _device()
+    at_u = mask = words = 0
     if u is not None:
-        _need_f32(fn, "u", u, (M, st.heads, st.value_dim))
-    words = _need_mask(fn, tree_mask, M)
-    _need_device(fn, st.s, q, k, v, g, beta, out, u, tree_mask)
-    args = _DELTA_RULE(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, dt, g.data_ptr(), beta.data_ptr(), scale,
-                       out.data_ptr(), outs, _addr(u), _addr(tree_mask), words, 0 if max_rows is None else max_rows, M, layer)
+        if not (u.dtype is torch.float32 and u.shape == (M, st.heads, st.value_dim) and u.is_contiguous()):
+            raise ValueError(f"{fn}: u is contiguous float32 [M, Hv, Dv]")
+        at_u = u.data_ptr()
+        if u.get_device() != dev:
+            _wrong_device(fn)
+    if tree_mask is not None:
+        words = _mask_words(fn, tree_mask, M)
+        mask = tree_mask.data_ptr()
+        if tree_mask.get_device() != dev:
+            _wrong_device(fn)
+    if not (dev == st.device == q.get_device() == k.get_device() == v.get_device() == g.get_device() == beta.get_device() ==
+            out.get_device()):
+        _wrong_device(fn)
+    args = _DELTA_RULE(q.data_ptr(), k.data_ptr(), v.data_ptr(), qr, kr, vr, dt, g.data_ptr(), beta.data_ptr(), scale,
+                       out.data_ptr(), outr if M > 1 else n, at_u, mask, words, max_rows or 0, M, layer)
     rc = (_lib or load()).iq4xs_delta_rule(args, st.desc, batch.desc, _stream(stream))
     if rc:
         _check(fn, rc)
@@ -798,28 +827,48 @@ def iq4xs_delta_commit(k, g, u, x, state: DeltaState, batch: KVBatch, paths, acc
     move lens.  k [layers, M, Hk, Dk], g fp32 [layers, M, Hv], u fp32 [layers,
     M, Hv, Dv] and x fp32 [layers, M, channels] (None where the state has no
     conv) are what the step's calls left."""
-    fn = "iq4xs_delta_commit"
-    st = state
-    st._check_batch(fn, batch)
-    dt = _need_16(fn, k)
-    _need(k.dim() == 4 and k.shape[0] == st.layers, fn, "k is [layers, M, Hk, Dk]")
-    M = k.shape[1]
-    ks = _need_rows16(fn, M, "a layer of k", k[0], st.key_heads, st.key_dim)
-    _need(g.dtype is torch.float32 and g.shape == (st.layers, M, st.heads) and g[0].is_contiguous(), fn,
-          "g is float32 [layers, M, Hv], a layer contiguous")
-    _need(u.dtype is torch.float32 and u.shape == (st.layers, M, st.heads, st.value_dim) and u[0].is_contiguous(), fn,
-          "u is float32 [layers, M, Hv, Dv], a layer contiguous")
-    _need((x is None) == (st.conv is None), fn, "x goes with the state's inputs (conv)")
-    xs = xl = 0
-    if x is not None:
-        _need(x.dim() == 3 and x.shape[0] == st.layers, fn, "x is [layers, M, channels]")
-        xs, xl = _need_cols(fn, "a layer of x", x[0], M, st.channels), x.stride(0)
-    _need_i32(fn, paths=paths, accepted=accepted)
-    _need(paths.dim() == 2 and paths.shape[0] == batch.sequences and accepted.numel() == batch.sequences, fn,
-          "paths [B, width], accepted [B]")
-    _need_device(fn, st.s, k, g, u, x, paths, accepted)
-    args = _DELTA_COMMIT(k.data_ptr(), ks, k.stride(0), dt, g.data_ptr(), g.stride(0), u.data_ptr(), u.stride(0), _addr(x),
-                         xs, xl, paths.data_ptr(), paths.shape[1], accepted.data_ptr(), M)
+    fn, st, f32 = "iq4xs_delta_commit", state, torch.float32
+    if st.mapped is not None:
+        st._check_batch(fn, batch)
+    dt, hk, hv, dk, dv = KV_DTYPES.get(k.dtype), st.key_heads, st.heads, st.key_dim, st.value_dim
+    if dt is None:
+        raise TypeError(f"{fn}: k must be float16 or bfloat16")
+    k_shape = k.shape
+    M = k_shape[1]
+    (kl, kr, kh, kc), (gl, gr, gc), (ul, ur, uh, uc) = k.stride(), g.stride(), u.stride()
+    if not (k_shape == (st.layers, M, hk, dk) and kc == 1 and (hk == 1 or kh == dk)):
+        raise ValueError(f"{fn}: k is [layers, M, Hk, Dk], heads and channels contiguous")
+    if not (g.dtype is f32 and g.shape == (st.layers, M, hv) and (hv == 1 or gc == 1) and (M == 1 or gr == hv)):
+        raise ValueError(f"{fn}: g is float32 [layers, M, Hv], a layer contiguous")
+    if not (u.dtype is f32 and u.shape == (st.layers, M, hv, dv) and uc == 1 and (hv == 1 or uh == dv) and
+            (M == 1 or ur == hv * dv)):
+        raise ValueError(f"{fn}: u is float32 [layers, M, Hv, Dv], a layer contiguous")
+    dev = _device()
+    at_x = xr = xl = 0
+    if x is None:
+        if st.conv is not None:
+            raise ValueError(f"{fn}: x goes with the state's inputs (conv)")
+    else:
+        xl, xr, xc = x.stride()
+        if not (st.conv is not None and x.dtype is f32 and x.shape == (st.layers, M, st.channels) and xc == 1):
+            raise ValueError(f"{fn}: x is float32 [layers, M, channels] and goes with the state's inputs (conv)")
+        at_x = x.data_ptr()
+        if x.get_device() != dev:
+            _wrong_device(fn)
+    i32, B = torch.int32, batch.sequences
+    if not (paths.dtype is i32 and accepted.dtype is i32):
+        raise TypeError(f"{fn}: paths and accepted must be int32")
+    p_shape = paths.shape
+    if not (len(p_shape) == 2 and p_shape[0] == B and accepted.numel() == B and paths.is_contiguous() and
+            accepted.is_contiguous()):
+        raise ValueError(f"{fn}: paths [B, width], accepted [B], contiguous")
+    if not (dev == st.device == k.get_device() == g.get_device() == u.get_device() == paths.get_device() ==
+            accepted.get_device()):
+        _wrong_device(fn)
+    if M == 1:
+        kr, xr = hk * dk, st.channels if at_x else 0
+    args = _DELTA_COMMIT(k.data_ptr(), kr, kl, dt, g.data_ptr(), gl, u.data_ptr(), ul, at_x, xr, xl, paths.data_ptr(),
+                         p_shape[1], accepted.data_ptr(), M)
     rc = (_lib or load()).iq4xs_delta_commit(args, st.desc, batch.desc, _stream(stream))
     if rc:
         _check(fn, rc)
@@ -828,15 +877,24 @@ def iq4xs_delta_commit(k, g, u, x, state: DeltaState, batch: KVBatch, paths, acc
 def iq4xs_token_probs(logits, probs, temperature=None, stream=None) -> None:
     """probs fp32 [M, V] = softmax of logits fp32 [M, V] / temperature fp32 [M]
     (None: 1; not above 0: all on the first of the largest); in place will do."""
-    fn = "iq4xs_token_probs"
-    _need(logits.dim() == 2, fn, "logits is [M, V]")
-    M, V = logits.shape
-    ls, ps = _need_cols(fn, "logits", logits, M, V), _need_cols(fn, "probs", probs, M, V)
+    fn, f32 = "iq4xs_token_probs", torch.float32
+    shape = logits.shape
+    M, V = shape
+    (lr, lc), (pr, pc) = logits.stride(), probs.stride()
+    if not (logits.dtype is f32 and probs.dtype is f32 and probs.shape == shape and (V == 1 or (lc == 1 and pc == 1))):
+        raise ValueError(f"{fn}: logits and probs are float32 [M, V], columns contiguous")
+    dev, at_t = _device(), 0
     if temperature is not None:
-        _need_f32(fn, "temperature", temperature, (M,))
-    _need_device(fn, logits, probs, temperature)
-    rc = (_lib or load()).iq4xs_token_probs(logits.data_ptr(), ls, M, V, _addr(temperature), probs.data_ptr(), ps,
-                                            _stream(stream))
+        if not (temperature.dtype is f32 and temperature.shape == (M,) and temperature.is_contiguous()):
+            raise ValueError(f"{fn}: temperature is contiguous float32 [M]")
+        at_t = temperature.data_ptr()
+        if temperature.get_device() != dev:
+            _wrong_device(fn)
+    if not (dev == logits.get_device() == probs.get_device()):
+        _wrong_device(fn)
+    if M == 1:
+        lr = pr = V
+    rc = (_lib or load()).iq4xs_token_probs(logits.data_ptr(), lr, M, V, at_t, probs.data_ptr(), pr, _stream(stream))
     if rc:
         _check(fn, rc)
 
@@ -849,23 +907,43 @@ def iq4xs_verify_drafts(probs, tokens, accept_u, draw_u, paths, accepted, next_t
     them, and next_token int32 [B], drawn by draw_u fp32 [B] from what is left.
     draft_probs fp32 [M, V]: row r's distribution that its children were drawn
     from (None: they were not drawn)."""
-    fn = "iq4xs_verify_drafts"
-    _need(probs.dim() == 2, fn, "probs is [M, V]")
-    M, V = probs.shape
-    ps, ds = _need_cols(fn, "probs", probs, M, V), 0
+    fn, f32, i32, B = "iq4xs_verify_drafts", torch.float32, torch.int32, batch.sequences
+    shape = probs.shape
+    M, V = shape
+    pr, pc = probs.stride()
+    if not (probs.dtype is f32 and (V == 1 or pc == 1)):
+        raise ValueError(f"{fn}: probs is float32 [M, V], columns contiguous")
+    dev, at_d, dr = _device(), 0, 0
     if draft_probs is not None:
-        ds = _need_cols(fn, "draft_probs", draft_probs, M, V)
-    _need_i32(fn, tokens=tokens, paths=paths, accepted=accepted, next_token=next_token)
-    _need_f32(fn, "accept_u", accept_u, (M,))
-    _need_f32(fn, "draw_u", draw_u, (batch.sequences,))
-    _need(tokens.numel() == M and paths.dim() == 2 and paths.shape[0] == batch.sequences and
-          accepted.numel() == batch.sequences and next_token.numel() == batch.sequences, fn,
-          "tokens [M], paths [B, width], accepted [B], next_token [B]")
-    words = _need_mask(fn, tree_mask, M)
-    _need_device(fn, probs, draft_probs, tokens, tree_mask, accept_u, draw_u, paths, accepted, next_token)
-    args = _VERIFY(probs.data_ptr(), ps, _addr(draft_probs), ds, tokens.data_ptr(), _addr(tree_mask), words,
-                   accept_u.data_ptr(), draw_u.data_ptr(), M, V, paths.data_ptr(), paths.shape[1], accepted.data_ptr(),
-                   next_token.data_ptr())
+        dr, dc = draft_probs.stride()
+        if not (draft_probs.dtype is f32 and draft_probs.shape == shape and (V == 1 or dc == 1)):
+            raise ValueError(f"{fn}: draft_probs is float32 [M, V], columns contiguous")
+        at_d = draft_probs.data_ptr()
+        if draft_probs.get_device() != dev:
+            _wrong_device(fn)
+    if not (tokens.dtype is i32 and paths.dtype is i32 and accepted.dtype is i32 and next_token.dtype is i32):
+        raise TypeError(f"{fn}: tokens, paths, accepted and next_token must be int32")
+    if not (accept_u.dtype is f32 and draw_u.dtype is f32):
+        raise TypeError(f"{fn}: accept_u and draw_u must be float32")
+    p_shape = paths.shape
+    if not (tokens.numel() == M and accept_u.numel() == M and draw_u.numel() == B and accepted.numel() == B and
+            next_token.numel() == B and len(p_shape) == 2 and p_shape[0] == B and tokens.is_contiguous() and
+            accept_u.is_contiguous() and draw_u.is_contiguous() and accepted.is_contiguous() and
+            next_token.is_contiguous() and paths.is_contiguous()):
+        raise ValueError(f"{fn}: tokens and accept_u [M], draw_u, accepted and next_token [B], paths [B, width], contiguous")
+    mask = words = 0
+    if tree_mask is not None:
+        words = _mask_words(fn, tree_mask, M)
+        mask = tree_mask.data_ptr()
+        if tree_mask.get_device() != dev:
+            _wrong_device(fn)
+    if not (dev == probs.get_device() == tokens.get_device() == accept_u.get_device() == draw_u.get_device() ==
+            paths.get_device() == accepted.get_device() == next_token.get_device()):
+        _wrong_device(fn)
+    if M == 1:
+        pr, dr = V, V if at_d else 0
+    args = _VERIFY(probs.data_ptr(), pr, at_d, dr, tokens.data_ptr(), mask, words, accept_u.data_ptr(), draw_u.data_ptr(),
+                   M, V, paths.data_ptr(), p_shape[1], accepted.data_ptr(), next_token.data_ptr())
     rc = (_lib or load()).iq4xs_verify_drafts(args, batch.desc, _stream(stream))
     if rc:
         _check(fn, rc)

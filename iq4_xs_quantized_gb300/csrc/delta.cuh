@@ -78,7 +78,7 @@ cudaError_t launch_delta_chunk(const DeltaRule& p, const DeltaView& d, const Bat
 cudaError_t launch_delta_commit(const iq4xs_delta_commit_args& a, const DeltaView& d, const BatchView& b, int* err,
                                 cudaStream_t stream);
 cudaError_t launch_token_probs(const float* logits, int64_t logits_stride, int64_t rows, int64_t vocab,
-                               const float* temperature, float* probs, int64_t probs_stride, int* err,
+                               const float* temperature, float* probs, int64_t probs_stride, int* err, int num_sms,
                                cudaStream_t stream);
 cudaError_t launch_verify_drafts(const iq4xs_verify_drafts_args& a, const BatchView& b, int* err,
                                  cudaStream_t stream);

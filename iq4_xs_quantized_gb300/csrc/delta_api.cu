@@ -180,7 +180,7 @@ int iq4xs_token_probs(const float* logits, int64_t logits_stride, int64_t rows, 
     void* encode;
     const int rc = device_context(&err, &sms, &encode);
     if (rc) return rc;
-    return from_cuda(launch_token_probs(logits, logits_stride, rows, vocab, temperature, probs, probs_stride, err,
+    return from_cuda(launch_token_probs(logits, logits_stride, rows, vocab, temperature, probs, probs_stride, err, sms,
                                         reinterpret_cast<cudaStream_t>(stream)));
 }
 

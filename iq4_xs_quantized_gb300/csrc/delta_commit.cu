@@ -4,8 +4,8 @@
 //
 // over the path's rows, in every layer; the convolution's inputs become the
 // path's last three.  The rows' k and u are small beside S, which is read once
-// and written once: HBM bounds it.  A CTA takes one head of one sequence and
-// layer, S in registers; paths of more than kPath rows go in runs.
+// and written once: HBM bounds it.  A CTA takes 64 columns of one head of one
+// sequence and layer, S in registers; paths of more than kPath rows go in runs.
 #include "delta.cuh"
 
 namespace iq4xs {
@@ -26,17 +26,18 @@ struct CommitParams {
 };
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(kCommitThreads) delta_commit_kernel(const CommitParams p, const DeltaView d,
+__global__ void __launch_bounds__(kCommitThreads, 4) delta_commit_kernel(const CommitParams p, const DeltaView d,
                                                                       const BatchView b, int* err) {
-    constexpr int kCols = DV / 4, kGroups = kCommitThreads / kCols, kKeys = DK / kGroups;
+    constexpr int VS = 64, kCols = VS / 4, kGroups = kCommitThreads / kCols, kKeys = DK / kGroups;
     __shared__ __align__(16) float k_at[kPath][DK];
-    __shared__ __align__(16) float u_at[kPath][DV];
+    __shared__ __align__(16) float u_at[kPath][VS];
     __shared__ int row_at[kPath];
     __shared__ float g_at[kPath], decay[kPath + 1];
     griddep_launch_dependents();
     griddep_wait();
     const Bc bc = bc_open(err);
-    const int parts = d.heads + p.conv_parts, tid = threadIdx.x;
+    constexpr int kSlices = DV / VS;
+    const int parts = d.heads * kSlices + p.conv_parts, tid = threadIdx.x;
     const int part = blockIdx.x % parts, s = blockIdx.x / parts % b.sequences, layer = blockIdx.x / parts / b.sequences;
     int row0;
     const int n = batch_rows(b, s, p.rows, &row0, err);
@@ -47,6 +48,19 @@ __global__ void __launch_bounds__(kCommitThreads) delta_commit_kernel(const Comm
         return;
     }
     if (count == 0) return;
+    // S is asked for first: what comes behind the path's checks hides under it.
+    const bool moves_s = part < d.heads * kSlices;
+    const int head = part / kSlices, v0 = part % kSlices * VS, key_head = head / (d.heads / d.key_heads);
+    const int col = tid % kCols * 4, group = tid / kCols;
+    float* const at_s = d.s + layer * d.s_layer_stride + slot * d.s_slot_stride +
+                        ((int64_t)head * DK + group * kKeys) * DV + v0 + col;
+    float4 S[kKeys];
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+        S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (moves_s && len > 0 && bc_global(bc, at_s + i * DV, 16, d.s, d.s_extent, kBcDeltaS))
+            S[i] = __ldcs(reinterpret_cast<const float4*>(at_s + i * DV));
+    }
     const int32_t* path = p.paths + (int64_t)s * p.path_width;
     bool bad = false;
     for (int i = tid; i < count; i += kCommitThreads) {
@@ -57,12 +71,12 @@ __global__ void __launch_bounds__(kCommitThreads) delta_commit_kernel(const Comm
         if (tid == 0) data_error(err, kDataPath);
         return;
     }
-    if (part >= d.heads) {
+    if (!moves_s) {
         // The last three inputs: of the path, and before it of the state.
         float* const at = d.conv + layer * d.conv_layer_stride + slot * d.conv_slot_stride;
         const float* x = p.x + layer * p.x_layer_stride;
         const int64_t extent = 4 * ((d.layers - 1) * p.x_layer_stride + (p.rows - 1) * p.x_row_stride + d.channels);
-        const int c = 4 * ((part - d.heads) * kCommitThreads + tid);
+        const int c = 4 * ((part - d.heads * kSlices) * kCommitThreads + tid);
         if (c >= d.channels) return;
         float4 in[kConvTaps - 1];
 #pragma unroll
@@ -84,17 +98,6 @@ __global__ void __launch_bounds__(kCommitThreads) delta_commit_kernel(const Comm
             if (bc_global(bc, to, 16, d.conv, d.conv_extent, kBcDeltaConv)) *reinterpret_cast<float4*>(to) = in[i];
         }
         return;
-    }
-    const int head = part, key_head = head / (d.heads / d.key_heads);
-    const int col = tid % kCols * 4, group = tid / kCols;
-    float* const at_s = d.s + layer * d.s_layer_stride + slot * d.s_slot_stride +
-                        ((int64_t)head * DK + group * kKeys) * DV + col;
-    float4 S[kKeys];
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i) {
-        S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (len > 0 && bc_global(bc, at_s + i * DV, 16, d.s, d.s_extent, kBcDeltaS))
-            S[i] = __ldcs(reinterpret_cast<const float4*>(at_s + i * DV));
     }
     const int64_t k_extent = 2 * ((d.layers - 1) * p.k_layer_stride + (p.rows - 1) * p.k_row_stride +
                                   (int64_t)d.key_heads * DK);
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(kCommitThreads) delta_commit_kernel(const Comm
         }
         for (int i = tid; i < m * kCols; i += kCommitThreads) {
             const int c = i % kCols * 4, t = i / kCols;
-            const float* from = p.u + layer * p.u_layer_stride + ((int64_t)row_at[t] * d.heads + head) * DV + c;
+            const float* from = p.u + layer * p.u_layer_stride + ((int64_t)row_at[t] * d.heads + head) * DV + v0 + c;
             float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
             if (bc_global(bc, from, 16, p.u, u_extent, kBcDeltaU)) w = *reinterpret_cast<const float4*>(from);
             *reinterpret_cast<float4*>(&u_at[t][c]) = w;
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(kCommitThreads) delta_commit_kernel(const Comm
 
 template <int DK, int DV>
 cudaError_t launch(const CommitParams& p, const DeltaView& d, const BatchView& b, int* err, cudaStream_t stream) {
-    const int64_t blocks = (int64_t)d.layers * b.sequences * (d.heads + p.conv_parts);
+    const int64_t blocks = (int64_t)d.layers * b.sequences * (d.heads * (DV / 64) + p.conv_parts);
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     return launch_chained(delta_commit_kernel<DK, DV>, dim3((unsigned)blocks), dim3(kCommitThreads), 0, stream, 1, p, d,
                           b, err);

@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kInputThreads = 128;
 constexpr int kInputCols = 4 * kInputThreads;  // channels of a CTA
+constexpr int kAbreast = 4;                    // rows whose loads are in flight together
 
 struct InputParams {
     const float* x;
@@ -34,7 +35,7 @@ struct InputParams {
     int mask_words, advance, rows, run, col_parts, key_lanes;
 };
 
-__device__ __forceinline__ float silu(float y) { return y / (1.f + __expf(-y)); }
+__device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
 __device__ __forceinline__ void tap(float4& y, const float4 (&w)[4], int j, const float4& x) {
     const float* w0 = reinterpret_cast<const float*>(w);  // [channel][tap]
     y.x = fmaf(w0[j], x.x, y.x);
@@ -104,17 +105,30 @@ __global__ void __launch_bounds__(kInputThreads) delta_inputs_kernel(const Input
                    ? *reinterpret_cast<const float4*>(from) : zero;
     }
     const int keys = d.key_heads * d.key_dim, kind = c < keys ? 0 : c < 2 * keys ? 1 : 2;
+    const bool unit_norm = part * kInputCols + 4 * (threadIdx.x & ~31) < 2 * keys;
     uint16_t* const base = p.out[kind];
     const int64_t out_stride = p.out_stride[kind];
     const int64_t out_extent = 2 * ((p.rows - 1) * out_stride + (kind < 2 ? keys : d.heads * d.value_dim));
-    auto finish = [&](int t, float4 y) {
-        y = make_float4(silu(y.x), silu(y.y), silu(y.z), silu(y.w));
-        float sum = fmaf(y.x, y.x, fmaf(y.y, y.y, fmaf(y.z, y.z, y.w * y.w)));
-        for (int o = p.key_lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float r = kind < 2 ? rsqrtf(sum + p.eps) : 1.f;
+    // Four rows side by side: SiLU, unit norm, rounding (rows t .. t1 - 1).
+    auto finish = [&](int t, float4 (&y)[kAbreast]) {
+        float sum[kAbreast];
+#pragma unroll
+        for (int i = 0; i < kAbreast; ++i) {
+            y[i] = make_float4(silu(y[i].x), silu(y[i].y), silu(y[i].z), silu(y[i].w));
+            sum[i] = fmaf(y[i].x, y[i].x, fmaf(y[i].y, y[i].y, fmaf(y[i].z, y[i].z, y[i].w * y[i].w)));
+        }
+        if (unit_norm)  // (some lane of the warp has a query's or key's channels)
+            for (int o = p.key_lanes / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < kAbreast; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
         uint16_t* to = base + (first + t) * out_stride + c - kind * keys;
-        if (here && bc_global(bc, to, 8, base, out_extent, kBcDeltaQkv))
-            *reinterpret_cast<uint2*>(to) = make_uint2(T::pack(r * y.x, r * y.y), T::pack(r * y.z, r * y.w));
+#pragma unroll
+        for (int i = 0; i < kAbreast; ++i, to += out_stride) {
+            const float r = kind < 2 ? rsqrtf(sum[i] + p.eps) : 1.f;
+            if (here && t + i < t1 && bc_global(bc, to, 8, base, out_extent, kBcDeltaQkv))
+                *reinterpret_cast<uint2*>(to) =
+                    make_uint2(T::pack(r * y[i].x, r * y[i].y), T::pack(r * y[i].z, r * y[i].w));
+        }
     };
     auto past = [&](int t) { return t >= 0 ? input(first + t) : before(kConvTaps - 1 + t); };
     if (p.tree_mask == nullptr) {
@@ -126,18 +140,22 @@ __global__ void __launch_bounds__(kInputThreads) delta_inputs_kernel(const Input
             new1 = past(n - 2);
             new2 = past(n - 1);
         }
-#pragma unroll 4
-        for (int t = t0; t < t1; ++t) {
-            const float4 x3 = input(first + t);
-            float4 y = zero;
-            tap(y, w, 0, x0);
-            tap(y, w, 1, x1);
-            tap(y, w, 2, x2);
-            tap(y, w, 3, x3);
+        for (int t = t0; t < t1; t += kAbreast) {
+            float4 x3[kAbreast], y[kAbreast];
+#pragma unroll
+            for (int i = 0; i < kAbreast; ++i) x3[i] = t + i < t1 ? input(first + t + i) : zero;
+#pragma unroll
+            for (int i = 0; i < kAbreast; ++i) {
+                y[i] = zero;
+                tap(y[i], w, 0, x0);
+                tap(y[i], w, 1, x1);
+                tap(y[i], w, 2, x2);
+                tap(y[i], w, 3, x3[i]);
+                x0 = x1;
+                x1 = x2;
+                x2 = x3[i];
+            }
             finish(t, y);
-            x0 = x1;
-            x1 = x2;
-            x2 = x3;
         }
         if (moves && here && bc_global(bc, at_conv + c, 16, d.conv, d.conv_extent, kBcDeltaConv) &&
             bc_global(bc, at_conv + 2 * d.channels + c, 16, d.conv, d.conv_extent, kBcDeltaConv)) {
@@ -158,15 +176,22 @@ __global__ void __launch_bounds__(kInputThreads) delta_inputs_kernel(const Input
         }
         return -1;
     };
-    for (int t = t0; t < t1; ++t) {
-        float4 y = zero;
-        int from = t;
-        tap(y, w, 3, input(first + t));
+    for (int t = t0; t < t1; t += kAbreast) {
+        float4 y[kAbreast];
+        int from[kAbreast];
 #pragma unroll
-        for (int j = 2; j >= 0; --j) {
-            from = parent(from);
-            tap(y, w, j, past(from));
+        for (int i = 0; i < kAbreast; ++i) {
+            from[i] = min(t + i, t1 - 1);
+            y[i] = zero;
+            tap(y[i], w, 3, input(first + from[i]));
         }
+#pragma unroll
+        for (int j = 2; j >= 0; --j)
+#pragma unroll
+            for (int i = 0; i < kAbreast; ++i) {
+                from[i] = parent(from[i]);
+                tap(y[i], w, j, past(from[i]));
+            }
         finish(t, y);
     }
 }

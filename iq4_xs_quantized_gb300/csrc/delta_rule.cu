@@ -20,26 +20,30 @@
 namespace iq4xs {
 namespace {
 
-constexpr int kStepThreads = 256;
+constexpr int kStepThreads = 256, kStepWarps = kStepThreads / 32;
 
 // DK key channels; VS of the value channels; blocks of TB rows.
 template <int DK, int VS, int TB>
 struct StepShape {
-    static constexpr int kCols = VS / 4;                // threads across the columns
+    static constexpr int kCols = VS / 4;                  // threads across the columns
     static constexpr int kGroups = kStepThreads / kCols;  // and down the key channels
-    static constexpr int kKeys = DK / kGroups;          // key channels a thread
-    static constexpr int kRound = TB < 4 ? TB : 4;      // rows summed over the groups at a time
+    static constexpr int kKeys = DK / kGroups;            // key channels a thread
+    static constexpr int kRound = TB < 4 ? TB : 4;        // rows summed over the warps at a time
+    static constexpr int kPitch = DK + 16;                // (two rows' quarters of 16 channels on all the banks)
     // shared memory, in floats
-    static constexpr int kKq = 0;                            // [TB][k, q][DK]
-    static constexpr int kSums = kKq + TB * 2 * DK;          // [TB][S^T k -> u, S^T q][VS]
-    static constexpr int kRed = kSums + TB * 2 * VS;         // [groups][round][2][VS]
-    static constexpr int kA = kRed + kGroups * kRound * 2 * VS;  // [TB][TB]
+    static constexpr int kK = 0;                          // [TB][pitch]
+    static constexpr int kQ = kK + TB * kPitch;
+    static constexpr int kV = kQ + TB * kPitch;           // [TB][VS]
+    static constexpr int kSums = kV + TB * VS;            // [TB][S^T k -> u, S^T q][VS]
+    static constexpr int kRed = kSums + TB * 2 * VS;      // [warps][round][2][VS]
+    static constexpr int kA = kRed + kStepWarps * kRound * 2 * VS;  // [TB][TB]
     static constexpr int kP = kA + TB * TB;
     static constexpr int kFar = kP + TB * TB;
-    static constexpr int kGates = kFar + TB * TB;            // [TB] g, beta, G
+    static constexpr int kGates = kFar + TB * TB;         // [TB] g, beta, G
     static constexpr int kFloats = kGates + 3 * TB;
     static constexpr int kSmem = (kFloats + (kFloats & 1)) * 4 + TB * 8;  // and the rows seen
     static_assert(kKeys >= 1 && kKeys % 2 == 0, "key channels a thread");
+    static_assert(TB == 1 || ((kA & 3) == 0 && (kP & 3) == 0), "rows of A and P are read as vectors");
 };
 
 __device__ __forceinline__ void axpy(float4& y, float a, const float4& x) {
@@ -50,7 +54,7 @@ __device__ __forceinline__ void axpy(float4& y, float a, const float4& x) {
 }
 
 template <int DK, int VS, int TB>
-__global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaRule p, const DeltaView d,
+__global__ void __launch_bounds__(kStepThreads, TB == 1 ? 4 : 3) delta_step_kernel(const DeltaRule p, const DeltaView d,
                                                                   const BatchView b, int* err) {
     using C = StepShape<DK, VS, TB>;
     extern __shared__ __align__(16) float sm[];
@@ -84,140 +88,177 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaRul
     for (int t0 = 0; t0 < n; t0 += TB) {
         const int m = min(TB, n - t0), first = row0 + t0;
         if (t0 > 0) __syncthreads();  // the last block's rows have been used
+        auto put8 = [&](const uint16_t* base, const uint16_t* from, int64_t extent, float* to) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (bc_global(bc, from, 16, base, extent, kBcDeltaQkv)) w = *reinterpret_cast<const uint4*>(from);
+            float x[8];
+            unpack8(p.bf16, w, x);
+            *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        };
         for (int i = tid; i < m * 2 * (DK / 8); i += kStepThreads) {
             const int c = i % (DK / 8) * 8, which = i / (DK / 8) % 2, t = i / (DK / 8) / 2;
             const uint16_t* base = which ? p.q : p.k;
             const int64_t stride = which ? p.q_row_stride : p.k_row_stride;
-            const uint16_t* from = base + (first + t) * stride + key_head * DK + c;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (bc_global(bc, from, 16, base, 2 * ((p.rows - 1) * stride + keys), kBcDeltaQkv))
-                w = *reinterpret_cast<const uint4*>(from);
-            float x[8];
-            unpack8(p.bf16, w, x);
-            float* to = sm + C::kKq + (2 * t + which) * DK + c;
-            *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4*>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+            put8(base, base + (first + t) * stride + key_head * DK + c, 2 * ((p.rows - 1) * stride + keys),
+                 sm + (which ? C::kQ : C::kK) + t * C::kPitch + c);
         }
-        for (int t = tid; t < m; t += kStepThreads) {
-            const int64_t at = (int64_t)(first + t) * d.heads + head, extent = 4 * (int64_t)p.rows * d.heads;
+        for (int i = kStepThreads - 1 - tid; i < m * (VS / 8); i += kStepThreads) {  // (threads that have no key first)
+            const int c = i % (VS / 8) * 8, t = i / (VS / 8);
+            put8(p.v, p.v + (first + t) * p.v_row_stride + head * d.value_dim + v0 + c,
+                 2 * ((p.rows - 1) * p.v_row_stride + values), sm + C::kV + t * VS + c);
+        }
+        if (tid < m) {
+            const int64_t at = (int64_t)(first + tid) * d.heads + head, extent = 4 * (int64_t)p.rows * d.heads;
             float g = 0.f, beta = 0.f;
             if (bc_global(bc, p.g + at, 4, p.g, extent, kBcDeltaGate)) g = p.g[at];
             if (bc_global(bc, p.beta + at, 4, p.beta, extent, kBcDeltaGate)) beta = p.beta[at];
-            sm[C::kGates + t] = g;
-            sm[C::kGates + TB + t] = beta;
-            seen[t] = p.tree_mask ? delta_seen(p.tree_mask, p.mask_words, p.rows, row0, t, bc) : (1ull << t) - 1;
+            sm[C::kGates + tid] = g;
+            sm[C::kGates + TB + tid] = beta;
+            seen[tid] = p.tree_mask ? delta_seen(p.tree_mask, p.mask_words, p.rows, row0, tid, bc) : (1ull << tid) - 1;
         }
         __syncthreads();
         // Decays by walking back from every row.
         if (tid < m) {
-            float sum = 0.f;
-            int from = tid;
+            float run = sm[C::kGates + tid];
             sm[C::kFar + tid * TB + tid] = 1.f;
-            for (uint64_t left = seen[tid]; left != 0;) {
-                const int j = 63 - __clzll(left);
-                left ^= 1ull << j;
-                sum += sm[C::kGates + from];
-                sm[C::kFar + tid * TB + j] = expf(sum);
-                from = j;
+            for (uint32_t left = (uint32_t)seen[tid]; left != 0;) {
+                const int j = 31 - __clz(left);
+                left ^= 1u << j;
+                sm[C::kFar + tid * TB + j] = expf(run);
+                run += sm[C::kGates + j];
             }
-            sm[C::kGates + 2 * TB + tid] = expf(sum + sm[C::kGates + from]);
+            sm[C::kGates + 2 * TB + tid] = expf(run);
         }
-        __syncthreads();
-        // Products of the rows' keys and queries, a pair a warp.
-        for (int t = 0, pair = 0; t < m; ++t) {
-            const uint64_t with = seen[t] | 1ull << t;
-            for (int j = 0; j <= t; ++j) {
-                if (!(with >> j & 1) || (pair++ & (kStepThreads / 32 - 1)) != warp) continue;
-                const float* kt = sm + C::kKq + 2 * t * DK;
-                const float* kj = sm + C::kKq + 2 * j * DK;
-                float kk = 0.f, qk = 0.f;
+        // Products of the rows' keys and queries, four lanes a pair, a quarter of every 16 channels each.
+        for (int i0 = 0; i0 < m * TB; i0 += kStepThreads / 4) {
+            const int i = i0 + tid / 4, t = i / TB, j = i % TB;
+            float kk = 0.f, qk = 0.f;
+            if (t < m && j <= t) {
+                const float* kt = sm + C::kK + t * C::kPitch + lane % 4 * 4;
+                const float* qt = sm + C::kQ + t * C::kPitch + lane % 4 * 4;
+                const float* kj = sm + C::kK + j * C::kPitch + lane % 4 * 4;
 #pragma unroll
-                for (int i = 0; i < DK / 32; ++i) {
-                    kk = fmaf(kt[lane + 32 * i], kj[lane + 32 * i], kk);
-                    qk = fmaf(kt[DK + lane + 32 * i], kj[lane + 32 * i], qk);
+                for (int c = 0; c < DK; c += 16) {
+                    const float4 a = *reinterpret_cast<const float4*>(kt + c), q = *reinterpret_cast<const float4*>(qt + c);
+                    const float4 e = *reinterpret_cast<const float4*>(kj + c);
+                    kk = fmaf(a.x, e.x, fmaf(a.y, e.y, fmaf(a.z, e.z, fmaf(a.w, e.w, kk))));
+                    qk = fmaf(q.x, e.x, fmaf(q.y, e.y, fmaf(q.z, e.z, fmaf(q.w, e.w, qk))));
                 }
+            }
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    kk += __shfl_xor_sync(0xffffffffu, kk, o);
-                    qk += __shfl_xor_sync(0xffffffffu, qk, o);
-                }
-                if (lane == 0) {
-                    const float far = sm[C::kFar + t * TB + j];
-                    sm[C::kA + t * TB + j] = sm[C::kGates + TB + t] * far * kk;
-                    sm[C::kP + t * TB + j] = p.scale * far * qk;
-                }
+            for (int o = 2; o > 0; o >>= 1) {
+                kk += __shfl_xor_sync(0xffffffffu, kk, o);
+                qk += __shfl_xor_sync(0xffffffffu, qk, o);
+            }
+            if (lane % 4 == 0 && t < m) {
+                sm[C::kA + i] = kk;
+                sm[C::kP + i] = qk;
             }
         }
         // S^T k and S^T q, kRound rows at a time.
+#pragma unroll 1
         for (int r0 = 0; r0 < m; r0 += C::kRound) {
 #pragma unroll
             for (int r = 0; r < C::kRound; ++r) {
                 if (r0 + r >= m) break;
-                const float* kq = sm + C::kKq + 2 * (r0 + r) * DK + group * C::kKeys;
+                const float* kt = sm + C::kK + (r0 + r) * C::kPitch + group * C::kKeys;
+                const float* qt = sm + C::kQ + (r0 + r) * C::kPitch + group * C::kKeys;
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f), c = a;
 #pragma unroll
                 for (int i = 0; i < C::kKeys; i += 2) {
-                    const float2 k2 = *reinterpret_cast<const float2*>(kq + i);
-                    const float2 q2 = *reinterpret_cast<const float2*>(kq + DK + i);
+                    const float2 k2 = *reinterpret_cast<const float2*>(kt + i), q2 = *reinterpret_cast<const float2*>(qt + i);
                     axpy(a, k2.x, S[i]);
                     axpy(c, q2.x, S[i]);
                     axpy(a, k2.y, S[i + 1]);
                     axpy(c, q2.y, S[i + 1]);
                 }
-                float* to = sm + C::kRed + (group * C::kRound + r) * 2 * VS + col;
-                *reinterpret_cast<float4*>(to) = a;
-                *reinterpret_cast<float4*>(to + VS) = c;
+                // over the warp's groups: the lower lanes the keys' sums, the upper the queries'
+                const bool low = lane < 16;
+                float4 mine = low ? a : c, other = low ? c : a;
+                mine.x += __shfl_xor_sync(0xffffffffu, other.x, 16);
+                mine.y += __shfl_xor_sync(0xffffffffu, other.y, 16);
+                mine.z += __shfl_xor_sync(0xffffffffu, other.z, 16);
+                mine.w += __shfl_xor_sync(0xffffffffu, other.w, 16);
+                if (C::kCols == 8) {
+                    mine.x += __shfl_xor_sync(0xffffffffu, mine.x, 8);
+                    mine.y += __shfl_xor_sync(0xffffffffu, mine.y, 8);
+                    mine.z += __shfl_xor_sync(0xffffffffu, mine.z, 8);
+                    mine.w += __shfl_xor_sync(0xffffffffu, mine.w, 8);
+                }
+                if (lane % 16 < C::kCols)
+                    *reinterpret_cast<float4*>(sm + C::kRed + ((warp * C::kRound + r) * 2 + (low ? 0 : 1)) * VS + col) = mine;
             }
             __syncthreads();
-            for (int i = tid; i < C::kRound * 2 * VS; i += kStepThreads) {
-                if (r0 + i / (2 * VS) >= m) break;
+            const int count = min(C::kRound, m - r0) * 2 * VS;
+            for (int i = tid; i < count; i += kStepThreads) {
                 float sum = 0.f;
 #pragma unroll
-                for (int k = 0; k < C::kGroups; ++k) sum += sm[C::kRed + k * C::kRound * 2 * VS + i];
+                for (int k = 0; k < kStepWarps; ++k) sum += sm[C::kRed + k * C::kRound * 2 * VS + i];
                 sm[C::kSums + r0 * 2 * VS + i] = sum;
             }
+            if (r0 == 0)  // (every decay and product is there)
+                for (int i = tid; i < m * TB; i += kStepThreads) {
+                    const int t = i / TB, j = i % TB;
+                    const bool from = seen[t] >> j & 1;
+                    const float far = from || j == t ? sm[C::kFar + i] : 0.f;
+                    sm[C::kA + i] = from ? sm[C::kGates + TB + t] * far * sm[C::kA + i] : 0.f;
+                    sm[C::kP + i] = from || j == t ? p.scale * far * sm[C::kP + i] : 0.f;
+                }
             __syncthreads();
         }
-        // u, a column a thread.
+        // u, a column a thread.  (A row takes the rows that it comes from, and no
+        // others: 0 times NaN is none of its.)
         if (tid < VS) {
-            float* const u = sm + C::kSums + tid;  // [t][2][VS]
-            for (int t = 0; t < m; ++t) {
-                const uint16_t* from = p.v + (first + t) * p.v_row_stride + head * d.value_dim + v0 + tid;
-                float v = 0.f;
-                if (bc_global(bc, from, 2, p.v, 2 * ((p.rows - 1) * p.v_row_stride + values), kBcDeltaQkv))
-                    v = p.bf16 ? KvBf16::unpack(*from).x : KvF16::unpack(*from).x;
-                float x = sm[C::kGates + TB + t] * (v - sm[C::kGates + 2 * TB + t] * u[t * 2 * VS]);
-                for (uint64_t left = seen[t]; left != 0; left &= left - 1) {
-                    const int j = __ffsll(left) - 1;
-                    x = fmaf(-sm[C::kA + t * TB + j], u[j * 2 * VS], x);
+            float u[TB];
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                if (t >= m) break;
+                const float beta = sm[C::kGates + TB + t];
+                float x = beta * (sm[C::kV + t * VS + tid] - sm[C::kGates + 2 * TB + t] * sm[C::kSums + t * 2 * VS + tid]);
+                const uint32_t from = (uint32_t)seen[t];
+#pragma unroll
+                for (int j = 0; j < t; j += 4) {
+                    const float4 a = *reinterpret_cast<const float4*>(sm + C::kA + t * TB + j);
+                    if (from >> j & 1) x = fmaf(-a.x, u[j], x);
+                    if (j + 1 < t && (from >> (j + 1) & 1)) x = fmaf(-a.y, u[j + 1], x);
+                    if (j + 2 < t && (from >> (j + 2) & 1)) x = fmaf(-a.z, u[j + 2], x);
+                    if (j + 3 < t && (from >> (j + 3) & 1)) x = fmaf(-a.w, u[j + 3], x);
                 }
-                u[t * 2 * VS] = x;
-                if (p.u != nullptr) {
-                    float* to = p.u + ((int64_t)(first + t) * d.heads + head) * d.value_dim + v0 + tid;
-                    if (bc_global(bc, to, 4, p.u, 4 * p.rows * values, kBcDeltaU)) *to = x;
-                }
+                u[t] = x;
+                sm[C::kSums + t * 2 * VS + tid] = x;
             }
         }
         __syncthreads();
         for (int i = tid; i < m * VS; i += kStepThreads) {
             const int t = i / VS, c = i % VS;
+            const float u = sm[C::kSums + 2 * t * VS + c];
             float x = p.scale * sm[C::kGates + 2 * TB + t] * sm[C::kSums + (2 * t + 1) * VS + c];
-            for (uint64_t left = seen[t] | 1ull << t; left != 0; left &= left - 1) {
-                const int j = __ffsll(left) - 1;
-                x = fmaf(sm[C::kP + t * TB + j], sm[C::kSums + 2 * j * VS + c], x);
+            const uint32_t from = (uint32_t)seen[t];
+#pragma unroll 4
+            for (int j = 0; j < t; ++j) {
+                const float y = sm[C::kSums + 2 * j * VS + c];
+                if (from >> j & 1) x = fmaf(sm[C::kP + t * TB + j], y, x);
             }
+            x = fmaf(sm[C::kP + t * TB + t], u, x);
             float* to = p.out + (first + t) * p.out_row_stride + head * d.value_dim + v0 + c;
             if (bc_global(bc, to, 4, p.out, 4 * ((p.rows - 1) * p.out_row_stride + values), kBcDeltaOut)) *to = x;
+            if (p.u != nullptr) {
+                to = p.u + ((int64_t)(first + t) * d.heads + head) * d.value_dim + v0 + c;
+                if (bc_global(bc, to, 4, p.u, 4 * p.rows * values, kBcDeltaU)) *to = u;
+            }
         }
         if (p.u == nullptr) {
             const float decay = sm[C::kGates + 2 * TB + m - 1];
 #pragma unroll
-            for (int i = 0; i < C::kKeys; ++i) S[i] = make_float4(decay * S[i].x, decay * S[i].y, decay * S[i].z, decay * S[i].w);
+            for (int i = 0; i < C::kKeys; ++i)
+                S[i] = make_float4(decay * S[i].x, decay * S[i].y, decay * S[i].z, decay * S[i].w);
+#pragma unroll 2
             for (int j = 0; j < m; ++j) {
                 const float far = sm[C::kFar + (m - 1) * TB + j];
                 float4 u = *reinterpret_cast<const float4*>(sm + C::kSums + 2 * j * VS + col);
                 u = make_float4(far * u.x, far * u.y, far * u.z, far * u.w);
-                const float* kj = sm + C::kKq + 2 * j * DK + group * C::kKeys;
+                const float* kj = sm + C::kK + j * C::kPitch + group * C::kKeys;
 #pragma unroll
                 for (int i = 0; i < C::kKeys; i += 2) {
                     const float2 k2 = *reinterpret_cast<const float2*>(kj + i);
@@ -249,7 +290,9 @@ template <int DK, int VS>
 cudaError_t launch_rows(const DeltaRule& p, const DeltaView& d, const BatchView& b, int* err, cudaStream_t stream) {
     // Blocks of one row where a sequence has one; a tree is one block.
     if (p.max_rows == 1 || (p.u == nullptr && p.rows <= b.sequences)) return launch_step<DK, VS, 1>(p, d, b, err, stream);
-    return launch_step<DK, VS, 16>(p, d, b, err, stream);
+    return p.max_rows <= 8 || (p.u == nullptr && p.rows <= 8 * (int64_t)b.sequences)
+               ? launch_step<DK, VS, 8>(p, d, b, err, stream)
+               : launch_step<DK, VS, 16>(p, d, b, err, stream);
 }
 
 template <int DK>

@@ -7,60 +7,46 @@
 // and sum through distributed shared memory, and written once: HBM bounds it.
 // Rows start at any multiple of four bytes; a part's units of four values lie on
 // 16-byte boundaries of the logits, cut at the row's ends.
-#include "cache.cuh"
 #include "delta.cuh"
 
 namespace iq4xs {
 namespace {
 
 constexpr int kProbThreads = 512;
-constexpr int kProbUnits = 8;  // of four logits that a thread keeps
+constexpr int kProbWarps = kProbThreads / 32;
+constexpr int kProbUnits = 9;  // of four logits that a thread keeps
 constexpr int kProbPart = 4 * kProbThreads * kProbUnits;
 constexpr int kProbCluster = 8;
 
-struct Top {
-    float x;   // largest logit
-    int at;    // where it stands first
-    float sum; // of e^((l - x) / T)
-};
 __device__ __forceinline__ uint32_t rank_addr(const void* p, int rank) {
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     return a;
 }
-__device__ __forceinline__ float ld_rank(const float* p, int rank) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(rank_addr(p, rank)) : "memory");
+__device__ __forceinline__ uint4 ld_rank(const uint4* p, int rank) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(rank_addr(p, rank)) : "memory");
     return v;
 }
-__device__ __forceinline__ int ld_rank(const int* p, int rank) {
-    int v;
-    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(rank_addr(p, rank)) : "memory");
-    return v;
+__device__ __forceinline__ float exp2_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-__global__ void __launch_bounds__(kProbThreads) token_probs_kernel(const float* logits, int64_t logits_stride,
-                                                                   int64_t rows, int vocab, const float* temperature,
-                                                                   float* probs, int64_t probs_stride, int ranks,
-                                                                   int* err) {
-    __shared__ float tops[kProbThreads / 32], sums[kProbThreads / 32], mine[2];
-    __shared__ int places[kProbThreads / 32], my_place;
-    griddep_launch_dependents();
-    griddep_wait();
-    const Bc bc = bc_open(err);
-    const int rank = blockIdx.x % ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / ranks;
-    const float* const in = logits + row * logits_stride;
-    float* const out = probs + row * probs_stride;
-    const int64_t in_extent = 4 * ((rows - 1) * logits_stride + vocab), out_extent = 4 * ((rows - 1) * probs_stride + vocab);
+template <bool kGreedy>
+__device__ __forceinline__ void row_probs(const float* logits, const float* in, int64_t in_extent, float* probs, float* out,
+                                          int64_t out_extent, int vocab, float t, int rank, int ranks, const Bc& bc) {
+    __shared__ float tops[kProbWarps], sums[kProbWarps];
+    __shared__ int places[kProbWarps];
+    __shared__ uint4 mine;  // the part's largest, where it stands, its sum
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // unit u holds values 4 u - skew .. + 3
     const int skew = (int)(reinterpret_cast<uintptr_t>(in) >> 2 & 3);
     const bool same = (int)(reinterpret_cast<uintptr_t>(out) >> 2 & 3) == skew;
     const int units = (vocab + skew + 3) / 4, each = (units + ranks - 1) / ranks;
     const int u0 = rank * each, u1 = min(units, u0 + each);
-    float t = 1.f;
-    if (temperature != nullptr && bc_global(bc, temperature + row, 4, temperature, 4 * rows, kBcTemp)) t = temperature[row];
-    const bool greedy = !(t > 0.f);
     auto load = [&](int u, float (&x)[4]) {
         const int i0 = 4 * u - skew;
         if (i0 >= 0 && i0 + 4 <= vocab) {
@@ -77,19 +63,8 @@ __global__ void __launch_bounds__(kProbThreads) token_probs_kernel(const float* 
         }
     };
     float x[kProbUnits][4];
-    float top = -INFINITY;
+    float top = -INFINITY, sum = 0.f;
     int place = INT32_MAX;
-    bool odd = false;  // a NaN
-    auto look = [&](const float (&v)[4], int u) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            odd |= isnan(v[e]);
-            if (v[e] > top) {  // (places rise)
-                top = v[e];
-                place = 4 * u - skew + e;
-            }
-        }
-    };
 #pragma unroll
     for (int k = 0; k < kProbUnits; ++k) {
         const int u = u0 + k * kProbThreads + tid;
@@ -97,6 +72,24 @@ __global__ void __launch_bounds__(kProbThreads) token_probs_kernel(const float* 
         for (int e = 0; e < 4; ++e) x[k][e] = -INFINITY;
         if (u < u1) load(u, x[k]);
     }
+    auto look = [&](const float (&v)[4], int u) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (kGreedy) {
+                if (isnan(v[e])) sum = v[e];
+                if (v[e] > top) {  // (places rise)
+                    top = v[e];
+                    place = 4 * u - skew + e;
+                }
+            } else {
+                top = fmaxf(top, v[e]);
+            }
+        }
+    };
+    auto first_top = [&](float other, int at) {
+        if (kGreedy && (other > top || (other == top && at < place))) place = at;
+        top = fmaxf(top, other);
+    };
 #pragma unroll
     for (int k = 0; k < kProbUnits; ++k) look(x[k], u0 + k * kProbThreads + tid);
     for (int u = u0 + kProbUnits * kProbThreads + tid; u < u1; u += kProbThreads) {  // what registers do not hold
@@ -104,36 +97,36 @@ __global__ void __launch_bounds__(kProbThreads) token_probs_kernel(const float* 
         load(u, v);
         look(v, u);
     }
-    auto first_top = [&](float other, int at) {
-        if (other > top || (other == top && at < place)) {
-            top = other;
-            place = at;
-        }
-    };
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        first_top(__shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, place, o));
+    for (int o = 16; o > 0; o >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, top, o);
+        first_top(other, kGreedy ? __shfl_xor_sync(0xffffffffu, place, o) : 0);
+    }
     if (lane == 0) {
         tops[warp] = top;
         places[warp] = place;
     }
-    odd = __syncthreads_or(odd);
-    for (int w = 0; w < kProbThreads / 32; ++w) first_top(tops[w], places[w]);
-    // The part's sum against its own maximum; the row's is made of the parts'.
-    const float scale = 1.f / t;
-    float sum = 0.f;
-    auto add = [&](const float (&v)[4]) {
+    __syncthreads();
+    for (int w = 0; w < kProbWarps; ++w) first_top(tops[w], places[w]);
+    // e^((l - top) / T) against the part's own maximum, in the logits' place; the
+    // row's is made of the parts'.  (1 / T within fp32's range: equal values
+    // then give 1 at any T.)
+    const float c = fminf(fmaxf(1.44269504088896340736f / t, 1.17549435e-38f), 3.40282347e38f);
+    const float own = top, shift = top == -INFINITY ? 0.f : top;
+    auto weigh = [&](float (&v)[4]) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum += v[e] == -INFINITY ? 0.f : expf((v[e] - top) / t);
+        for (int e = 0; e < 4; ++e) {
+            v[e] = exp2_of((v[e] - shift) * c);
+            sum += v[e];
+        }
     };
-    (void)scale;
-    if (!greedy) {
+    if (!kGreedy) {
 #pragma unroll
-        for (int k = 0; k < kProbUnits; ++k) add(x[k]);
+        for (int k = 0; k < kProbUnits; ++k) weigh(x[k]);
         for (int u = u0 + kProbUnits * kProbThreads + tid; u < u1; u += kProbThreads) {
             float v[4];
             load(u, v);
-            add(v);
+            weigh(v);
         }
     }
 #pragma unroll
@@ -141,36 +134,35 @@ __global__ void __launch_bounds__(kProbThreads) token_probs_kernel(const float* 
     if (lane == 0) sums[warp] = sum;
     __syncthreads();
     sum = 0.f;
-    for (int w = 0; w < kProbThreads / 32; ++w) sum += sums[w];
-    if (odd) sum = NAN;
+    for (int w = 0; w < kProbWarps; ++w) sum += sums[w];
     if (ranks > 1) {
-        if (tid == 0) {
-            mine[0] = top;
-            mine[1] = sum;
-            my_place = place;
-        }
+        if (tid == 0) mine = make_uint4(__float_as_uint(top), (uint32_t)place, __float_as_uint(sum), 0);
         cluster_arrive_release();
         cluster_wait();
-        float all = 0.f;
-        for (int r = 0; r < ranks; ++r) first_top(ld_rank(&mine[0], r), ld_rank(&my_place, r));
-        for (int r = 0; r < ranks; ++r) {
-            const float part_top = ld_rank(&mine[0], r), part = ld_rank(&mine[1], r);
-            all += greedy || part_top == -INFINITY ? (isnan(part) ? part : 0.f) : part * expf((part_top - top) / t);
-        }
-        sum = all;
+        uint4 part[kProbCluster];
+#pragma unroll
+        for (int r = 0; r < kProbCluster; ++r)
+            if (r < ranks) part[r] = ld_rank(&mine, r);
+#pragma unroll
+        for (int r = 0; r < kProbCluster; ++r)
+            if (r < ranks) first_top(__uint_as_float(part[r].x), (int)part[r].y);
+        sum = 0.f;
+#pragma unroll
+        for (int r = 0; r < kProbCluster; ++r)
+            if (r < ranks) {
+                const float of = __uint_as_float(part[r].z), its = __uint_as_float(part[r].x);
+                sum += kGreedy ? of : its == -INFINITY ? of : of * exp2_of((its - top) * c);
+            }
         cluster_arrive_release();  // (no CTA ends while another reads its part)
     }
-    const bool nothing = top == -INFINITY && !isnan(sum), bad = isnan(sum) || (!greedy && top == INFINITY);
-    const float inverse = 1.f / sum;
+    // a weight times this is the probability (a part without any: zeros, unless the row is NaN)
+    const float factor = own == -INFINITY ? sum * 0.f : own == top ? 1.f / sum : exp2_of((own - top) * c) / sum;
     auto put = [&](const float (&v)[4], int u) {
         const int i0 = 4 * u - skew;
         float y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            y[e] = bad ? NAN
-                   : nothing || v[e] == -INFINITY ? 0.f
-                   : greedy ? (i0 + e == place ? 1.f : 0.f)
-                            : expf((v[e] - top) / t) * inverse;
+            y[e] = kGreedy ? (isnan(sum) ? sum : i0 + e == place ? 1.f : 0.f) : v[e] * factor;
         if (same && i0 >= 0 && i0 + 4 <= vocab) {
             if (bc_global(bc, out + i0, 16, probs, out_extent, kBcProbs))
                 *reinterpret_cast<float4*>(out + i0) = make_float4(y[0], y[1], y[2], y[3]);
@@ -181,26 +173,48 @@ __global__ void __launch_bounds__(kProbThreads) token_probs_kernel(const float* 
                     out[i0 + e] = y[e];
         }
     };
+    for (int u = u0 + kProbUnits * kProbThreads + tid; u < u1; u += kProbThreads) {
+        float v[4];
+        load(u, v);
+        if (!kGreedy) weigh(v);
+        put(v, u);
+    }
 #pragma unroll
     for (int k = 0; k < kProbUnits; ++k) {
         const int u = u0 + k * kProbThreads + tid;
         if (u < u1) put(x[k], u);
     }
-    for (int u = u0 + kProbUnits * kProbThreads + tid; u < u1; u += kProbThreads) {
-        float v[4];
-        load(u, v);
-        put(v, u);
-    }
     if (ranks > 1) cluster_wait();
+}
+
+__global__ void __launch_bounds__(kProbThreads, 2) token_probs_kernel(const float* logits, int64_t logits_stride,
+                                                                   int64_t rows, int vocab, const float* temperature,
+                                                                   float* probs, int64_t probs_stride, int ranks,
+                                                                   int* err) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const Bc bc = bc_open(err);
+    const int rank = blockIdx.x % ranks;
+    const int64_t row = blockIdx.x / ranks;
+    const float* const in = logits + row * logits_stride;
+    float* const out = probs + row * probs_stride;
+    const int64_t in_extent = 4 * ((rows - 1) * logits_stride + vocab), out_extent = 4 * ((rows - 1) * probs_stride + vocab);
+    float t = 1.f;
+    if (temperature != nullptr && bc_global(bc, temperature + row, 4, temperature, 4 * rows, kBcTemp)) t = temperature[row];
+    if (t > 0.f) row_probs<false>(logits, in, in_extent, probs, out, out_extent, vocab, t, rank, ranks, bc);
+    else row_probs<true>(logits, in, in_extent, probs, out, out_extent, vocab, 1.f, rank, ranks, bc);
 }
 
 }  // namespace
 
 cudaError_t launch_token_probs(const float* logits, int64_t logits_stride, int64_t rows, int64_t vocab,
-                               const float* temperature, float* probs, int64_t probs_stride, int* err,
+                               const float* temperature, float* probs, int64_t probs_stride, int* err, int num_sms,
                                cudaStream_t stream) {
+    // A row's parts: as many as registers want, and more while SMs are free.
     int ranks = 1;
-    while (ranks < kProbCluster && (int64_t)ranks * kProbPart < vocab + 3) ranks *= 2;
+    while (ranks < kProbCluster && ((int64_t)ranks * kProbPart < vocab + 3 ||
+                                    (2 * ranks * rows <= num_sms && (int64_t)ranks * 4 * kProbThreads < vocab)))
+        ranks *= 2;
     return launch_chained(token_probs_kernel, dim3((unsigned)(rows * ranks)), dim3(kProbThreads), 0, stream, ranks, logits,
                           logits_stride, rows, (int)vocab, temperature, probs, probs_stride, ranks, err);
 }

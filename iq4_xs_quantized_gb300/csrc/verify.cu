@@ -19,6 +19,8 @@ constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyCluster = 8;
 constexpr int kVerifyRows = 1024;
+constexpr int kRun = 256;  // values that a warp sums at a time, eight a lane
+constexpr int kMaxRuns = (1 << 20) / kVerifyCluster / kRun;
 
 struct VerifyParams {
     const float* probs;
@@ -39,7 +41,7 @@ struct __align__(16) Order {
     int what;   // kSum, kDraw, kEnd
     int node;   // row of the batch whose probabilities they are
     int taken;  // times that the drafter's distribution comes off
-    int gone;   // without one: rejected tokens in the first CTA's list
+    int gone;   // without one: rejected tokens in the first CTA's list; -1: the sums of before hold
 };
 enum { kSum, kDraw, kEnd };
 
@@ -50,7 +52,7 @@ struct VerifyShared {
     int gone[kVerifyRows];                         // tokens rejected at the row
     unsigned long long mass[kVerifyRows];          // m before each subtraction
     unsigned long long parts[kVerifyCluster];      // the CTAs' sums
-    unsigned long long warps[kVerifyWarps];
+    unsigned long long runs[kMaxRuns];             // this CTA's, run by run
     Order order;
 };
 
@@ -153,6 +155,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     // Thread 0 of the first CTA: where the walk stands.
     constexpr unsigned long long kOne = 1ull << 61;
     int node = 0, t = 1, count = 1, taken = 0, gone = 0;
+    bool summed = false;  // what is left behind the node has been summed
     unsigned long long mass = kOne;
     auto accept = [&] {
         node = t;
@@ -160,6 +163,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         ++count;
         taken = gone = 0;
         mass = kOne;
+        summed = false;
     };
     auto walk = [&]() -> int {
         for (; t < n && count < p.path_width; ++t) {
@@ -177,6 +181,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
                 for (int k = 0; k < p.ranks; ++k) st_rank(&sh.mass[taken], k, mass);
                 ++taken;
                 ++t;
+                summed = true;
                 return kSum;
             }
             if (sh.token[t] < 0) continue;
@@ -190,10 +195,13 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         }
         return kDraw;
     };
-    // The part of a row of the vocabulary that this CTA sums, a run a warp.
-    const int each = (p.vocab + p.ranks - 1) / p.ranks, run = (each + kVerifyWarps - 1) / kVerifyWarps;
-    const int begin = min(p.vocab, rank * each), end = min(p.vocab, begin + each);
-    const int lo = min(end, begin + warp * run), hi = min(end, lo + run);
+    // The part of a row of the vocabulary that this CTA sums, in runs that go round its warps.
+    const int each = ((p.vocab + p.ranks - 1) / p.ranks + kRun - 1) / kRun * kRun;
+    const int begin = min(p.vocab, rank * each), end = min(p.vocab, begin + each), runs = (end - begin + kRun - 1) / kRun;
+    const int some = (runs + 31) / 32;
+    unsigned long long upto = 0;  // the first warp's sums up to and with a lane's runs
+    float draw = 0.f;
+    if (bc_global(bc, p.draw_u + s, 4, p.draw_u, 4 * (int64_t)b.sequences, kBcVerifyRow)) draw = p.draw_u[s];
     bool plain = false;
     cluster_wait();  // (every CTA has begun: its shared memory may be written)
     for (;;) {
@@ -203,7 +211,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
                 o.what = plain ? kDraw : walk();
                 o.node = first + node;
                 o.taken = plain ? 0 : taken;
-                o.gone = plain ? 0 : gone;
+                o.gone = plain ? 0 : o.what == kDraw && summed ? -1 : gone;
             }
             const unsigned long long* w = reinterpret_cast<const unsigned long long*>(&o);
             for (int k = 0; k < p.ranks; ++k) {
@@ -214,36 +222,65 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         cluster_sync();
         const Order o = sh.order;
         if (o.what == kEnd) break;
-        // Value i of what is left behind the row.
-        auto left_at = [&](int i) -> unsigned long long {
-            const float* from = p.probs + o.node * p.probs_stride + i;
-            if (!bc_global(bc, from, 4, p.probs, p_extent, kBcVerifyProbs)) return 0;
-            unsigned long long r = whole(*from);
-            if (o.taken > 0) {
-                from = p.draft + o.node * p.draft_stride + i;
-                if (!bc_global(bc, from, 4, p.draft, q_extent, kBcVerifyProbs)) return 0;
-                const unsigned long long q = whole(*from);
-                for (int k = 0; k < o.taken; ++k) r = take_off(r, sh.mass[k], q);
-            }
-            return r;
-        };
-        unsigned long long sum = 0;
-        for (int i = lo + lane; i < hi; i += 32) sum += left_at(i);
-        for (int i = tid; i < o.gone; i += kVerifyThreads)
-            if (rank != 0) sh.gone[i] = ld_rank(&sh.gone[i], 0);
-        __syncthreads();
-        for (int i = lane; i < o.gone; i += 32)
-            if (sh.gone[i] >= lo && sh.gone[i] < hi) sum -= left_at(sh.gone[i]);
+        // What is left behind the row of eight values from i0 on, `step` apart (0 behind the part's end).
+        const float* const p_row = p.probs + o.node * p.probs_stride;
+        const float* const q_row = p.draft + o.node * p.draft_stride;
+        auto left_at = [&](int i0, int step, unsigned long long (&r)[8]) {
+            float pr[8], qr[8];
 #pragma unroll
-        for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-        if (lane == 0) sh.warps[warp] = sum;
-        __syncthreads();
-        if (tid < p.ranks) {
-            unsigned long long all = 0;
-            for (int w = 0; w < kVerifyWarps; ++w) all += sh.warps[w];
-            st_rank(&sh.parts[rank], tid, all);
+            for (int k = 0; k < 8; ++k) {
+                const int i = i0 + k * step;
+                pr[k] = i < end && bc_global(bc, p_row + i, 4, p.probs, p_extent, kBcVerifyProbs) ? p_row[i] : 0.f;
+            }
+            if (o.taken > 0) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int i = i0 + k * step;
+                    qr[k] = i < end && bc_global(bc, q_row + i, 4, p.draft, q_extent, kBcVerifyProbs) ? q_row[i] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) r[k] = whole(pr[k]);
+            if (o.taken > 0) {  // (the first m is 1)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const unsigned long long q = whole(qr[k]);
+                    r[k] = r[k] > q ? r[k] - q : 0;
+                    for (int x = 1; x < o.taken; ++x) r[k] = take_off(r[k], sh.mass[x], q);
+                }
+            }
+        };
+        if (o.gone >= 0) {
+            for (int run = warp; run < runs; run += kVerifyWarps) {
+                unsigned long long r[8];
+                left_at(begin + run * kRun + lane, 32, r);
+                unsigned long long sum = ((r[0] + r[1]) + (r[2] + r[3])) + ((r[4] + r[5]) + (r[6] + r[7]));
+#pragma unroll
+                for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+                if (lane == 0) sh.runs[run] = sum;
+            }
+            __syncthreads();
+            for (int i = tid; i < o.gone; i += kVerifyThreads) {
+                const int x = rank != 0 ? ld_rank(&sh.gone[i], 0) : sh.gone[i];
+                if (rank != 0) sh.gone[i] = x;
+                if (x >= begin && x < end && bc_global(bc, p_row + x, 4, p.probs, p_extent, kBcVerifyProbs))
+                    atomicAdd(&sh.runs[(x - begin) / kRun], 0ull - whole(p_row[x]));
+            }
+            __syncthreads();
+            // Lane l of the first warp: runs l * some .. of the part.
+            upto = 0;
+            if (warp == 0) {
+                for (int i = lane * some; i < min(runs, (lane + 1) * some); ++i) upto += sh.runs[i];
+#pragma unroll
+                for (int k = 1; k < 32; k <<= 1) {
+                    const unsigned long long y = __shfl_up_sync(0xffffffffu, upto, k);
+                    if (lane >= k) upto += y;
+                }
+                const unsigned long long all = __shfl_sync(0xffffffffu, upto, 31);
+                if (lane < p.ranks) st_rank(&sh.parts[rank], lane, all);
+            }
+            cluster_sync();
         }
-        cluster_sync();
         unsigned long long total = 0, before = 0;
         for (int k = 0; k < p.ranks; ++k) {
             before += k < rank ? sh.parts[k] : 0;
@@ -262,32 +299,41 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
                 p.next[s] = -1;
             break;
         }
-        float u = 0.f;
-        if (bc_global(bc, p.draw_u + s, 4, p.draw_u, 4 * (int64_t)b.sequences, kBcVerifyRow)) u = fmaxf(p.draw_u[s], 0.f);
-        const double at = (double)fminf(u, 1.f) * (double)total;
+        const double at = (double)fminf(fmaxf(draw, 0.f), 1.f) * (double)total;
         unsigned long long wanted = at < (double)total ? (unsigned long long)at : total - 1;
         wanted = min(wanted, total - 1);  // the first value whose running sum is above it
         if (wanted < before || wanted - before >= sh.parts[rank]) break;
         wanted -= before;
-        int w = 0;
-        for (; w < kVerifyWarps - 1 && wanted >= sh.warps[w]; ++w) wanted -= sh.warps[w];
-        if (warp != w) break;
-        for (int i0 = lo; i0 < hi; i0 += 32) {
-            const int i = i0 + lane;
-            unsigned long long x = i < hi ? left_at(i) : 0;
-            for (int k = 0; k < o.gone; ++k) x = sh.gone[k] == i ? 0 : x;
+        if (warp != 0) break;
+        const int at_lane = __ffs(__ballot_sync(0xffffffffu, upto > wanted)) - 1;
+        const unsigned long long below = __shfl_up_sync(0xffffffffu, upto, 1);
+        if (at_lane > 0) wanted -= __shfl_sync(0xffffffffu, below, at_lane);
+        int run = at_lane * some;
+        for (; run < min(runs, (at_lane + 1) * some) - 1 && wanted >= sh.runs[run]; ++run) wanted -= sh.runs[run];
+        // Eight neighbouring values a lane.
+        const int i0 = begin + run * kRun + 8 * lane;
+        unsigned long long r[8], sum = 0;
+        left_at(i0, 1, r);
+        for (int k = 0; k < o.gone; ++k)
 #pragma unroll
-            for (int k = 1; k < 32; k <<= 1) {
-                const unsigned long long y = __shfl_up_sync(0xffffffffu, x, k);
-                if (lane >= k) x += y;
+            for (int x = 0; x < 8; ++x) r[x] = sh.gone[k] == i0 + x ? 0 : r[x];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) sum += r[x];
+        unsigned long long with = sum;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const unsigned long long y = __shfl_up_sync(0xffffffffu, with, k);
+            if (lane >= k) with += y;
+        }
+        if (lane == __ffs(__ballot_sync(0xffffffffu, with > wanted)) - 1) {
+            unsigned long long so_far = with - sum;
+            int x = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                so_far += r[k];
+                x += so_far <= wanted;
             }
-            const unsigned hit = __ballot_sync(0xffffffffu, x > wanted);
-            if (hit != 0) {
-                if (lane == __ffs(hit) - 1 && bc_global(bc, p.next + s, 4, p.next, 4 * (int64_t)b.sequences, kBcVerifyOut))
-                    p.next[s] = i;
-                break;
-            }
-            wanted -= __shfl_sync(0xffffffffu, x, 31);
+            if (bc_global(bc, p.next + s, 4, p.next, 4 * (int64_t)b.sequences, kBcVerifyOut)) p.next[s] = i0 + x;
         }
         break;
     }
@@ -325,7 +371,7 @@ cudaError_t launch_verify_drafts(const iq4xs_verify_drafts_args& a, const BatchV
     p.vocab = (int)a.vocab;
     p.path_width = (int)a.path_width;
     p.ranks = 1;
-    while (p.ranks < kVerifyCluster && p.ranks * 4 * kVerifyThreads < p.vocab) p.ranks *= 2;
+    while (p.ranks < kVerifyCluster && p.ranks * 8 * kRun < p.vocab) p.ranks *= 2;  // (a run for half of a CTA's warps)
     return launch_chained(verify_kernel, dim3((unsigned)(b.sequences * p.ranks)), dim3(kVerifyThreads), 0, stream, p.ranks,
                           p, b, err);
 }
