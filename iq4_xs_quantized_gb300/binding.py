@@ -766,11 +766,10 @@ def iq4xs_delta_inputs(x, conv_weight, a, b, a_log, dt_bias, eps: float, q, k, v
     if tree_mask is not None:
         words = _mask_words(fn, tree_mask, M)
         mask = tree_mask.data_ptr()
-        if tree_mask.get_device() != dev:
-            _wrong_device(fn)
-    if not (dev == st.device == x.get_device() == conv_weight.get_device() == a.get_device() == b.get_device() ==
+    if (not (dev == st.device == x.get_device() == conv_weight.get_device() == a.get_device() == b.get_device() ==
             a_log.get_device() == dt_bias.get_device() == q.get_device() == k.get_device() == v.get_device() ==
-            g.get_device() == beta.get_device()):
+            g.get_device() == beta.get_device()) or
+            (tree_mask is not None and tree_mask.get_device() != dev)):
         _wrong_device(fn)
     if M == 1:
         xr, ar, br = c, hv, hv
@@ -804,15 +803,13 @@ def iq4xs_delta_rule(q, k, v, g, beta, scale: float, out, state: DeltaState, lay
         if not (u.dtype is torch.float32 and u.shape == (M, st.heads, st.value_dim) and u.is_contiguous()):
             raise ValueError(f"{fn}: u is contiguous float32 [M, Hv, Dv]")
         at_u = u.data_ptr()
-        if u.get_device() != dev:
-            _wrong_device(fn)
     if tree_mask is not None:
         words = _mask_words(fn, tree_mask, M)
         mask = tree_mask.data_ptr()
-        if tree_mask.get_device() != dev:
-            _wrong_device(fn)
-    if not (dev == st.device == q.get_device() == k.get_device() == v.get_device() == g.get_device() == beta.get_device() ==
-            out.get_device()):
+    if (not (dev == st.device == q.get_device() == k.get_device() == v.get_device() == g.get_device() == beta.get_device() ==
+            out.get_device()) or
+            (u is not None and u.get_device() != dev) or
+            (tree_mask is not None and tree_mask.get_device() != dev)):
         _wrong_device(fn)
     args = _DELTA_RULE(q.data_ptr(), k.data_ptr(), v.data_ptr(), qr, kr, vr, dt, g.data_ptr(), beta.data_ptr(), scale,
                        out.data_ptr(), outr if M > 1 else n, at_u, mask, words, max_rows or 0, M, layer)
@@ -853,8 +850,6 @@ def iq4xs_delta_commit(k, g, u, x, state: DeltaState, batch: KVBatch, paths, acc
         if not (st.conv is not None and x.dtype is f32 and x.shape == (st.layers, M, st.channels) and xc == 1):
             raise ValueError(f"{fn}: x is float32 [layers, M, channels] and goes with the state's inputs (conv)")
         at_x = x.data_ptr()
-        if x.get_device() != dev:
-            _wrong_device(fn)
     i32, B = torch.int32, batch.sequences
     if not (paths.dtype is i32 and accepted.dtype is i32):
         raise TypeError(f"{fn}: paths and accepted must be int32")
@@ -862,8 +857,9 @@ def iq4xs_delta_commit(k, g, u, x, state: DeltaState, batch: KVBatch, paths, acc
     if not (len(p_shape) == 2 and p_shape[0] == B and accepted.numel() == B and paths.is_contiguous() and
             accepted.is_contiguous()):
         raise ValueError(f"{fn}: paths [B, width], accepted [B], contiguous")
-    if not (dev == st.device == k.get_device() == g.get_device() == u.get_device() == paths.get_device() ==
-            accepted.get_device()):
+    if (not (dev == st.device == k.get_device() == g.get_device() == u.get_device() == paths.get_device() ==
+            accepted.get_device()) or
+            (x is not None and x.get_device() != dev)):
         _wrong_device(fn)
     if M == 1:
         kr, xr = hk * dk, st.channels if at_x else 0
@@ -888,9 +884,8 @@ def iq4xs_token_probs(logits, probs, temperature=None, stream=None) -> None:
         if not (temperature.dtype is f32 and temperature.shape == (M,) and temperature.is_contiguous()):
             raise ValueError(f"{fn}: temperature is contiguous float32 [M]")
         at_t = temperature.data_ptr()
-        if temperature.get_device() != dev:
-            _wrong_device(fn)
-    if not (dev == logits.get_device() == probs.get_device()):
+    if (not (dev == logits.get_device() == probs.get_device()) or
+            (temperature is not None and temperature.get_device() != dev)):
         _wrong_device(fn)
     if M == 1:
         lr = pr = V
@@ -919,8 +914,6 @@ def iq4xs_verify_drafts(probs, tokens, accept_u, draw_u, paths, accepted, next_t
         if not (draft_probs.dtype is f32 and draft_probs.shape == shape and (V == 1 or dc == 1)):
             raise ValueError(f"{fn}: draft_probs is float32 [M, V], columns contiguous")
         at_d = draft_probs.data_ptr()
-        if draft_probs.get_device() != dev:
-            _wrong_device(fn)
     if not (tokens.dtype is i32 and paths.dtype is i32 and accepted.dtype is i32 and next_token.dtype is i32):
         raise TypeError(f"{fn}: tokens, paths, accepted and next_token must be int32")
     if not (accept_u.dtype is f32 and draw_u.dtype is f32):
@@ -935,10 +928,10 @@ def iq4xs_verify_drafts(probs, tokens, accept_u, draw_u, paths, accepted, next_t
     if tree_mask is not None:
         words = _mask_words(fn, tree_mask, M)
         mask = tree_mask.data_ptr()
-        if tree_mask.get_device() != dev:
-            _wrong_device(fn)
-    if not (dev == probs.get_device() == tokens.get_device() == accept_u.get_device() == draw_u.get_device() ==
-            paths.get_device() == accepted.get_device() == next_token.get_device()):
+    if (not (dev == probs.get_device() == tokens.get_device() == accept_u.get_device() == draw_u.get_device() ==
+            paths.get_device() == accepted.get_device() == next_token.get_device()) or
+            (draft_probs is not None and draft_probs.get_device() != dev) or
+            (tree_mask is not None and tree_mask.get_device() != dev)):
         _wrong_device(fn)
     if M == 1:
         pr, dr = V, V if at_d else 0

@@ -3,15 +3,20 @@ them: for every step the pages a drafted tree needs (iq4xs_cache_reserve),
 for every layer the quantized q, k, v projection (iq4xs_linear), norm,
 rotation and cache append (iq4xs_qk_norm_rope), tree attention over the paged
 cache (iq4xs_tree_attention) and the quantized output projection, and after
-verification the accepted path committed (iq4xs_cache_commit).  Sequences are
-forked and released between steps.
+verification the accepted path committed (iq4xs_cache_commit).  Recurrent layers
+(--recurrent) go with them: the projection's convolution, norm and gates
+(iq4xs_delta_inputs), the gated delta rule over the same drafted tree from a
+state that stays (iq4xs_delta_rule), and the state moved along the accepted path
+(iq4xs_delta_commit).  With a vocabulary (--vocab) an output projection's
+probabilities (iq4xs_token_probs) choose the path and the token behind it
+(iq4xs_verify_drafts).  Sequences are forked and released between steps.
 
-    python -m iq4_xs_quantized_gb300.verify_step [--layers L] [--sequences S] [--tree T] [--steps N]
+    python -m iq4_xs_quantized_gb300.verify_step [--layers L] [--recurrent R] [--vocab V] [--sequences S] [--tree T] [--steps N]
 
 Weights are seeded random IQ4_XS blocks and a token is a seeded random hidden
-state, so a path's acceptance is drawn at random; what a run checks is that
-a sequence that came by drafted trees ends where one that was decoded token
-by token ends.
+state; without a vocabulary a path's acceptance is drawn at random.  What a run
+checks is that a sequence that came by drafted trees ends where one that was
+decoded token by token ends.
 """
 from __future__ import annotations
 
@@ -52,10 +57,12 @@ def rope_table(positions: int, rot_dim: int, base: float = 1e6) -> torch.Tensor:
 
 
 class Decoder:
-    """The attention layers of a decoder over a paged cache; one page table for all layers."""
+    """The layers of a decoder: `recurrent` ones over a state for each slot, then
+    attention layers over a paged cache, one page table for all; an output
+    projection to `vocab` tokens."""
 
     def __init__(self, layers=2, hidden=1024, q_heads=8, kv_heads=2, head_dim=128, page_size=16, pages=256, slots=4,
-                 width=32, dtype=torch.float16, seed=0):
+                 width=32, dtype=torch.float16, seed=0, recurrent=0, vocab=0):
         self.layers, self.hidden, self.hq, self.hkv, self.d = layers, hidden, q_heads, kv_heads, head_dim
         self.page_size, self.slots = page_size, slots
         self.n_qkv = (q_heads + 2 * kv_heads) * head_dim
@@ -71,6 +78,18 @@ class Decoder:
         self.w_qkv = [matrix(self.n_qkv, hidden) for _ in range(layers)]
         self.w_o = [matrix(hidden, q_heads * head_dim) for _ in range(layers)]
         self.norm_q, self.norm_k = (torch.ones(head_dim, device="cuda") for _ in range(2))
+        # recurrent layers: 2 query and key heads, 4 value heads of head_dim; a and b from the same projection
+        self.vocab, self.recurrent, self.rk, self.rv, self.kept = vocab, recurrent, 2, 4, None
+        self.state = None
+        if recurrent:
+            self.state = B.alloc_delta_state(recurrent, slots, self.rk, self.rv, head_dim, head_dim)
+            self.n_in = self.state.channels + 2 * self.rv
+            self.w_in = [matrix(self.n_in, hidden) for _ in range(recurrent)]
+            self.w_out = [matrix(hidden, self.rv * head_dim) for _ in range(recurrent)]
+            normal = lambda *shape: torch.from_numpy(rng.standard_normal(shape, dtype=np.float32)).cuda()  # noqa: E731
+            self.w_conv = [0.5 * normal(self.state.channels, 4) for _ in range(recurrent)]
+            self.a_log, self.dt_bias = normal(recurrent, self.rv), normal(recurrent, self.rv) - 3
+        self.w_vocab = matrix(vocab, hidden) if vocab else None  # (last: the other weights are the same without)
 
     def _buffers(self, m):
         d, ws = self.d, max(B.iq4xs_linear_workspace_bytes(m, self.n_qkv, self.hidden),
@@ -81,14 +100,47 @@ class Decoder:
                 torch.empty(B.iq4xs_tree_attention_workspace_bytes(m, self.hq, self.cache, self.batch),
                             dtype=torch.uint8, device="cuda"))
 
-    def forward(self, x, rows, positions, mask):
+    def _recurrent(self, x, max_rows, mask, keep):
+        """The recurrent layers.  keep: the states stay, and what a commit needs is kept."""
+        st, m, d, c = self.state, x.shape[0], self.d, self.state.channels
+        ws = torch.empty(max(B.iq4xs_linear_workspace_bytes(m, self.n_in, self.hidden),
+                             B.iq4xs_linear_workspace_bytes(m, self.hidden, self.rv * d)), dtype=torch.uint8, device="cuda")
+        f32 = lambda *shape: torch.empty(shape, device="cuda")  # noqa: E731
+        proj, out, y = f32(self.recurrent, m, self.n_in), f32(m, self.rv * d), f32(m, self.hidden)
+        qkv = torch.empty(self.recurrent, m, c, dtype=self.cache.dtype, device="cuda")
+        q, k, v = (t.unflatten(2, (-1, d)) for t in qkv.split((self.rk * d, self.rk * d, self.rv * d), dim=2))
+        g, beta, u = f32(self.recurrent, m, self.rv), f32(m, self.rv), f32(self.recurrent, m, self.rv, d) if keep else None
+        for i in range(self.recurrent):
+            B.iq4xs_linear(self.w_in[i], self.n_in, self.hidden, x, proj[i], ws)
+            B.iq4xs_delta_inputs(proj[i, :, :c], self.w_conv[i], proj[i, :, c:c + self.rv], proj[i, :, c + self.rv:], self.a_log[i],
+                                 self.dt_bias[i], 1e-6, q[i], k[i], v[i], g[i], beta, st, i, self.batch, tree_mask=mask,
+                                 advance=not keep)
+            B.iq4xs_delta_rule(q[i], k[i], v[i], g[i], beta, 1.0, out, st, i, self.batch, u=u[i] if keep else None,
+                               tree_mask=mask, max_rows=max_rows)
+            B.iq4xs_linear(self.w_out[i], self.hidden, self.rv * d, out, y, ws)
+            x = x + y
+        self.kept = (k, g, u, proj[:, :, :c]) if keep else None
+        return x
+
+    def logits(self, x):
+        """fp32 [M, vocab] of hidden states [M, hidden]."""
+        m = x.shape[0]
+        ws = torch.empty(B.iq4xs_linear_workspace_bytes(m, self.vocab, self.hidden), dtype=torch.uint8, device="cuda")
+        out = torch.empty(m, self.vocab, device="cuda")
+        B.iq4xs_linear(self.w_vocab, self.vocab, self.hidden, x.contiguous(), out, ws)
+        return out
+
+    def forward(self, x, rows, positions, mask, keep=False):
         """Hidden states x [M, hidden] of rows[s] new tokens for each sequence
         slot, at `positions`, under `mask` (None: chains) -> hidden states.
-        The new tokens' K and V stay in the cache behind lens, not committed."""
+        The new tokens' K and V stay in the cache behind lens, not committed;
+        recurrent states move on over all of them, or stay with `keep`."""
         self.offsets.copy_(torch.tensor(np.concatenate([[0], np.cumsum(rows)]), dtype=torch.int32))
         B.iq4xs_cache_reserve(self.batch, self.page_size, self.refs, self.status)
         if bool(self.status.any()):
             raise RuntimeError("the cache has too few pages")
+        if self.recurrent:
+            x = self._recurrent(x, max(rows), mask, keep)
         m, d = x.shape[0], self.d
         qkv, q, att, y, ws, aws = self._buffers(m)
         at_k, at_v = self.hq * d, (self.hq + self.hkv) * d
@@ -103,12 +155,18 @@ class Decoder:
         return x
 
     def commit(self, paths, accepted):
+        if self.kept is not None:
+            B.iq4xs_delta_commit(*self.kept, self.state, self.batch, paths, accepted)
+            self.kept = None
         B.iq4xs_cache_commit(self.cache, self.batch, self.refs, paths, accepted, self.lens)
 
     def fork(self, parents, children):
         i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
         status = i32([0] * len(parents))
         B.iq4xs_cache_fork(self.cache, self.batch, self.refs, i32(parents), i32(children), status)
+        if self.state is not None:
+            self.state.s[:, children] = self.state.s[:, parents]
+            self.state.conv[:, children] = self.state.conv[:, parents]
         return status
 
     def release(self, slots):
@@ -120,13 +178,30 @@ def token_states(ids, hidden: int) -> torch.Tensor:
     return torch.stack([torch.randn(hidden, generator=torch.Generator().manual_seed(int(i))) for i in ids]).cuda()
 
 
-def run(layers=2, sequences=3, tree=8, steps=4, prompt=37, seed=0, dtype=torch.float16, verbose=False):
+def verified(dec, hidden, tokens, mask, tree, seed):
+    """The paths that the output projection's probabilities accept, committed;
+    each sequence's accepted tokens (places in its tree) and the token behind them."""
+    slots, m = dec.slots, hidden.shape[0]
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    probs = dec.logits(hidden)
+    B.iq4xs_token_probs(probs, probs)
+    i32 = lambda *shape: torch.empty(shape, dtype=torch.int32, device="cuda")  # noqa: E731
+    paths, accepted, ahead = i32(slots, tree), i32(slots), i32(slots)
+    rand = torch.rand(m + slots, generator=g, device="cuda")
+    B.iq4xs_verify_drafts(probs, tokens, rand[:m], rand[m:], paths, accepted, ahead, dec.batch, tree_mask=mask)
+    dec.commit(paths, accepted)
+    counts = accepted.tolist()
+    return [way[:n] for way, n in zip(paths.tolist(), counts) if n], [t for t, n in zip(ahead.tolist(), counts) if n]
+
+
+def run(layers=2, sequences=3, tree=8, steps=4, prompt=37, seed=0, dtype=torch.float16, verbose=False, recurrent=0, vocab=0):
     """Decodes `sequences` sequences by drafted trees and again token by token;
     returns the last token's hidden states of both, [sequences, hidden]."""
     rng = np.random.default_rng(seed)
     most = prompt + 5 * (sequences - 1) + steps * tree + tree  # the last prompt is the longest
     width = -(-most // 16) + 1
-    dec = Decoder(layers=layers, slots=sequences + 1, width=width, pages=(sequences + 2) * width, dtype=dtype, seed=seed)
+    dec = Decoder(layers=layers, slots=sequences + 1, width=width, pages=(sequences + 2) * width, dtype=dtype, seed=seed,
+                  recurrent=recurrent, vocab=vocab)
     # prompts, and what each sequence comes to hold
     text = [rng.integers(0, 10**6, prompt + 5 * s).tolist() for s in range(sequences)]
     prompts = [list(t) for t in text]
@@ -137,29 +212,34 @@ def run(layers=2, sequences=3, tree=8, steps=4, prompt=37, seed=0, dtype=torch.f
     width_p = max(max(rows), tree)
     chain = np.tile(np.arange(width_p, dtype=np.int32), (sequences + 1, 1))
     dec.commit(i32(chain), i32(rows))
-    last = None
+    last, ahead = None, rng.integers(0, vocab, sequences).tolist() if vocab else None  # the token that a sequence goes on with
     began = time.perf_counter()
     for step in range(steps):
         parents = [[-1] + [int(rng.integers(max(0, i - 3), i)) for i in range(1, tree)] for _ in range(sequences)]
-        ids = [rng.integers(0, 10**6, tree).tolist() for _ in range(sequences)]
+        ids = [rng.integers(0, vocab or 10**6, tree).tolist() for _ in range(sequences)]
+        for s in range(sequences if vocab else 0):
+            ids[s][0] = ahead[s]
         built = [tree_mask(p) for p in parents]
         mask = torch.from_numpy(np.concatenate([b[0] for b in built])).cuda()
         lens = [len(t) for t in text]
         positions = i32(np.concatenate([b[1] + n for b, n in zip(built, lens)]))
-        out = dec.forward(token_states([i for t in ids for i in t], dec.hidden), [tree] * sequences + [0], positions, mask)
-        # "verification": the way from the root to a drawn token
-        paths, accepted, ends = np.zeros((sequences + 1, tree), np.int32), [], []
-        for s in range(sequences):
-            way, at = [], int(rng.integers(0, tree))
-            ends.append(s * tree + at)
-            while at >= 0:
-                way.insert(0, at)
-                at = parents[s][at]
-            paths[s, :len(way)] = way
-            accepted.append(len(way))
+        out = dec.forward(token_states([i for t in ids for i in t], dec.hidden), [tree] * sequences + [0], positions, mask,
+                          keep=True)
+        if vocab:
+            ways, ahead = verified(dec, out, i32([i for t in ids for i in t]), mask, tree, seed + step)
+        else:  # "verification": the way from the root to a drawn token
+            paths, ways = np.zeros((sequences + 1, tree), np.int32), []
+            for s in range(sequences):
+                way, at = [], int(rng.integers(0, tree))
+                while at >= 0:
+                    way.insert(0, at)
+                    at = parents[s][at]
+                paths[s, :len(way)] = way
+                ways.append(way)
+            dec.commit(i32(paths), i32([len(way) for way in ways] + [0]))
+        for s, way in enumerate(ways):
             text[s] += [ids[s][i] for i in way]
-        dec.commit(i32(paths), i32(accepted + [0]))
-        last = out[ends]
+        last = out[[s * tree + way[-1] for s, way in enumerate(ways)]]
         # a second continuation of the first sequence begins and is given up again
         if bool(dec.fork([0], [sequences]).any()):
             raise RuntimeError("the cache has too few pages")
@@ -167,7 +247,8 @@ def run(layers=2, sequences=3, tree=8, steps=4, prompt=37, seed=0, dtype=torch.f
     torch.cuda.synchronize()
     took = time.perf_counter() - began
     # the same texts token by token
-    one = Decoder(layers=layers, slots=sequences, width=width, pages=sequences * width + 1, dtype=dtype, seed=seed)
+    one = Decoder(layers=layers, slots=sequences, width=width, pages=sequences * width + 1, dtype=dtype, seed=seed,
+                  recurrent=recurrent)
     one.forward(token_states([i for t in prompts for i in t], one.hidden), [len(t) for t in prompts], None, None)
     one.commit(i32(chain[:sequences]), i32([len(t) for t in prompts]))
     final = torch.empty(sequences, one.hidden, device="cuda")
@@ -182,7 +263,7 @@ def run(layers=2, sequences=3, tree=8, steps=4, prompt=37, seed=0, dtype=torch.f
                 final[s] = out[k]
     torch.cuda.synchronize()
     if verbose:
-        print(f"{steps} steps of {sequences} trees of {tree} tokens, {layers} layers: {took / steps * 1e3:.2f} ms a step, "
+        print(f"{steps} steps of {sequences} trees of {tree} tokens, {recurrent} + {layers} layers: {took / steps * 1e3:.2f} ms a step, "
               f"{sum(len(t) for t in text)} tokens cached, {int((dec.refs > 0).sum())} pages held")
     assert B.iq4xs_last_device_error() == 0
     return last, final
@@ -191,11 +272,13 @@ def run(layers=2, sequences=3, tree=8, steps=4, prompt=37, seed=0, dtype=torch.f
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--layers", type=int, default=4)
+    ap.add_argument("--recurrent", type=int, default=0, help="recurrent layers ahead of the attention layers")
+    ap.add_argument("--vocab", type=int, default=0, help="tokens of an output projection that verifies the drafts")
     ap.add_argument("--sequences", type=int, default=4)
     ap.add_argument("--tree", type=int, default=16)
     ap.add_argument("--steps", type=int, default=6)
     a = ap.parse_args()
-    by_trees, by_tokens = run(a.layers, a.sequences, a.tree, a.steps, verbose=True)
+    by_trees, by_tokens = run(a.layers, a.sequences, a.tree, a.steps, verbose=True, recurrent=a.recurrent, vocab=a.vocab)
     off = ((by_trees - by_tokens).norm(dim=1) / by_tokens.norm(dim=1)).max().item()
     print(f"by trees against token by token: {off:.2e} of the hidden state")
 
