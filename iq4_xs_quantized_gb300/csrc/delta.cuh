@@ -71,9 +71,9 @@ __device__ __forceinline__ uint64_t delta_seen(const uint64_t* mask, int words, 
 
 cudaError_t launch_delta_inputs(const iq4xs_delta_inputs_args& a, const DeltaView& d, const BatchView& b, int* err,
                                 int num_sms, cudaStream_t stream);
-cudaError_t launch_delta_rule(const DeltaRule& p, const DeltaView& d, const BatchView& b, int* err, int num_sms,
+cudaError_t launch_delta_rule(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err, int num_sms,
                               cudaStream_t stream);
-cudaError_t launch_delta_chunk(const DeltaRule& p, const DeltaView& d, const BatchView& b, int* err,
+cudaError_t launch_delta_chunk(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err,
                                cudaStream_t stream);
 cudaError_t launch_delta_commit(const iq4xs_delta_commit_args& a, const DeltaView& d, const BatchView& b, int* err,
                                 cudaStream_t stream);

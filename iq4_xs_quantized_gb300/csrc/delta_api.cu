@@ -139,7 +139,7 @@ int iq4xs_delta_rule(const iq4xs_delta_rule_args* a, const iq4xs_delta_state* st
     // The most rows that a sequence can have; the kernels skip one with more.
     p.max_rows = (int)(a->max_rows > 0 && a->max_rows < a->rows ? a->max_rows : a->rows);
     if (a->u && p.max_rows > kDeltaTreeRows) p.max_rows = kDeltaTreeRows;
-    return from_cuda(launch_delta_rule(p, d, b, err, sms, reinterpret_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_delta_rule(p, d, b, encode, err, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int iq4xs_delta_commit(const iq4xs_delta_commit_args* a, const iq4xs_delta_state* state, const iq4xs_kv_batch* batch,

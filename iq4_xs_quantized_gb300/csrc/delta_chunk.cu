@@ -103,9 +103,6 @@ __device__ __forceinline__ bool any_of(bool x) {
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {  // the rest of 16: zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 // A power of two that brings `top` to 2^13 .. 2^14, and its inverse; 1 where it is 0 or not finite.
 __device__ __forceinline__ float2 fit(float top) {
     const int e = (int)(__float_as_uint(top) >> 23);
@@ -119,10 +116,17 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
     const float2 r = KvF16::unpack(hi);
     lo = KvF16::pack(a - r.x, b - r.y);
 }
-// Two bf16 values times a power of two in fp16.
-__device__ __forceinline__ uint32_t scaled16(uint32_t w, float f) {
-    const float2 x = KvBf16::unpack(w);
-    return KvF16::pack(x.x * f, x.y * f);
+// Two bf16 values times a power of two (twice, side by side) in fp16.
+__device__ __forceinline__ uint32_t scaled16(uint32_t w, uint32_t f) {
+    uint32_t y;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(w), "r"(f), "r"(0x80008000u));
+    const float2 x = KvBf16::unpack(y);
+    return KvF16::pack(x.x, x.y);
+}
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
 }
 __device__ __forceinline__ uint4 lds_u128(uint32_t at) {
     uint4 w;
@@ -184,8 +188,11 @@ __device__ __forceinline__ uint32_t hide(float2 (&x)[16], const Gates& gt, int f
     return bits;
 }
 
-template <int DK, int DV>
-__global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __grid_constant__ DeltaRule p,
+template <int DK, int DV, bool kBf16>
+__global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __grid_constant__ CUtensorMap map_q,
+                                                                       const __grid_constant__ CUtensorMap map_k,
+                                                                       const __grid_constant__ CUtensorMap map_v,
+                                                                       const __grid_constant__ DeltaRule p,
                                                                        const __grid_constant__ DeltaView d,
                                                                        const __grid_constant__ BatchView b, int* err) {
     using C = ChunkShape<DK, DV>;
@@ -197,7 +204,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     }
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);  // [2] a block is prepared
     uint64_t* empty = full + 2;                                     // [2] and used
-    uint64_t* done1 = empty + 2;
+    uint64_t* landed = empty + 2;                                   // [2] its rows have come
+    uint64_t* done1 = landed + 2;
     uint64_t* done2 = done1 + 1;
     uint64_t* done_s = done2 + 1;
     uint64_t* done_o = done_s + 1;
@@ -225,6 +233,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         for (int i = 0; i < 2; ++i) {
             mbar_init(full + i, kPrepThreads);
             mbar_init(empty + i, kMainWarps);
+            mbar_init(landed + i, 1);
             mbar_init(drained + i, 1);
         }
         mbar_init(done1, 1);
@@ -234,6 +243,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         mbar_init(done_pairs, 1);
         *abort_flag = 0;
         fence_barrier_init();
+        prefetch_tmap(&map_q);
+        prefetch_tmap(&map_k);
+        prefetch_tmap(&map_v);
     }
     if (warp == 0) tmem_alloc(tmem_at, 512);
     tc_fence_before();
@@ -249,98 +261,104 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         // and unrolled they came from beyond the instruction caches.)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrepRegs));
         const int id = tid - kMainThreads;
-        constexpr int kUnits = DK / 8, kDown = kPrepThreads / kUnits, kTimes = 2 * kRows / kDown;
-        const int unit = id % kUnits;
+        constexpr int kLanes = 8, kDown = kPrepThreads / kLanes;  // of a row, one or two of its 16-byte units each
+        constexpr int kTimes = 2 * kRows / kDown, kEach = DK / 64;
+        const int unit = id % kLanes;
         float* const scales = reinterpret_cast<float*>(smem + C::kScales);  // what K's and Q's rows are to be multiplied by
         float* const g_at = scales + 2 * kRows;                             // in log2
         float* const maxima = g_at + kRows;  // [half] of P's rows
         float* const A = reinterpret_cast<float*>(smem + C::kA);
         float* const Ts = reinterpret_cast<float*>(smem + C::kTs);
-        const int64_t k_extent = 2 * ((p.rows - 1) * p.k_row_stride + keys), q_extent = 2 * ((p.rows - 1) * p.q_row_stride + keys);
-        const int64_t v_extent = 2 * ((p.rows - 1) * p.v_row_stride + values);
-        int staged = -1;  // the last block whose rows this thread has asked for
-        // K, Q and V of a block as they lie, zeros behind the last row
+        int staged = -1;  // the last block whose rows the first thread has asked for
+        // K, Q and V of a block as they lie; what comes behind its last row is another's, or zeros
         auto stage = [&](int c) {
-            const int buf = c & 1, t0 = c * kRows, m = min(kRows, n - t0);
+            const int buf = c & 1, row = row0 + c * kRows;
             staged = c;
-#pragma unroll 4
-            for (int i = 0; i < kTimes; ++i) {
-                const int r = id / kUnits + i * kDown, t = r % kRows;
-                const uint16_t* from = r < kRows ? p.k : p.q;
-                const uint16_t* at = from + (row0 + t0 + min(t, m - 1)) * (r < kRows ? p.k_row_stride : p.q_row_stride) +
-                                     key_head * DK + 8 * unit;
-                const bool in = t < m && bc_global(bc, at, 16, from, r < kRows ? k_extent : q_extent, kBcDeltaQkv);
-                cp_async16(base + C::kKq + buf * C::kKqBytes + unit_at(r, unit, 2 * kRows), at, in ? 16 : 0);
+            mbar_arrive_expect_tx(landed + buf, C::kKqBytes + C::kVBytes);
+            uint8_t* const kq = smem + C::kKq + buf * C::kKqBytes;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int x = key_head * DK + 64 * i;
+                bc_tma(bc, x, 2, 64, keys, row, p.rows, kBcDeltaQkv, kBcDeltaQkv);
+                tma_load_2d(kq + i * 2 * kRows * kChunkBytes, &map_k, x, row, landed + buf);
+                tma_load_2d(kq + (i * 2 + 1) * kRows * kChunkBytes, &map_q, x, row, landed + buf);
             }
-#pragma unroll 2
-            for (int i = id; i < kRows * (DV / 8); i += kPrepThreads) {
-                const int t = i / (DV / 8), u = i % (DV / 8);
-                const uint16_t* at = p.v + (row0 + t0 + min(t, m - 1)) * p.v_row_stride + head * DV + 8 * u;
-                const bool in = t < m && bc_global(bc, at, 16, p.v, v_extent, kBcDeltaQkv);
-                cp_async16(base + C::kV + buf * C::kVBytes + (t * DV + 8 * u) * 2, at, in ? 16 : 0);
+            bc_tma(bc, head * DV, 2, DV, values, row, p.rows, kBcDeltaQkv, kBcDeltaQkv);
+            tma_load_2d(smem + C::kV + buf * C::kVBytes, &map_v, head * DV, row, landed + buf);
+        };
+        // The block's gates, asked for ahead of their use.
+        float g_next = 0.f, beta_next = 0.f;
+        auto load_gates = [&](int t0) {
+            g_next = beta_next = 0.f;
+            if (id < kRows && t0 + id < n) {
+                const int64_t at = (int64_t)(row0 + t0 + id) * d.heads + head, extent = 4 * (int64_t)p.rows * d.heads;
+                if (bc_global(bc, p.g + at, 4, p.g, extent, kBcDeltaGate)) g_next = p.g[at];
+                if (bc_global(bc, p.beta + at, 4, p.beta, extent, kBcDeltaGate)) beta_next = p.beta[at];
             }
         };
+        load_gates(0);
         for (int c = 0; c < blocks; ++c) {
             const int buf = c & 1, t0 = c * kRows, m = min(kRows, n - t0);
             Gates& gt = gates[buf];
             bool lost = c >= 2 && !kv_wait(empty + buf, (c / 2 - 1) & 1, abort_flag, err, kDevErrTimeoutDelta);
             if (any_of<6, kPrepThreads>(lost)) break;  // (all leave together)
             const uint32_t kq_at = base + C::kKq + buf * C::kKqBytes;
-            if (staged != c) stage(c);
+            if (id == 0 && staged != c) stage(c);
             if (id < kRows) {
-                const int64_t at = (int64_t)(row0 + t0 + id) * d.heads + head, extent = 4 * (int64_t)p.rows * d.heads;
-                float g = 0.f, beta = 0.f;
-                uint64_t seen = 0;
-                bool odd = false;
-                if (id < m) {
-                    if (bc_global(bc, p.g + at, 4, p.g, extent, kBcDeltaGate)) g = p.g[at];
-                    if (bc_global(bc, p.beta + at, 4, p.beta, extent, kBcDeltaGate)) beta = p.beta[at];
-                    seen = delta_seen(p.tree_mask, p.mask_words, p.rows, row0, id, bc);
-                    odd = odd_value(beta) || isnan(g) || g == INFINITY;
-                    if (odd) g = beta = 0.f;
-                }
+                float g = g_next, beta = beta_next;
+                const bool odd = odd_value(beta) || isnan(g) || g == INFINITY;
+                if (odd) g = beta = 0.f;
                 g_at[id] = g * 1.44269504088896340736f;
                 gt.beta[id] = beta;
-                gt.seen[id] = seen;
+                gt.seen[id] = id < m ? delta_seen(p.tree_mask, p.mask_words, p.rows, row0, id, bc) : 0;
                 gt.left[id] = 0.f;
                 const unsigned bits = __ballot_sync(0xffffffffu, odd);
                 if (lane == 0) reinterpret_cast<unsigned*>(&gt.odd)[id / 32] = bits;
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
+            lost = !kv_wait(landed + buf, (c / 2) & 1, abort_flag, err, kDevErrTimeoutDeltaRows);
             prep_sync();
             // K and Q for the products: fp16 as it is, bf16 with its row's largest
-            // brought to 2^13; a row of K that is not finite: zeros
-#pragma unroll 1
-            for (int i0 = 0; i0 < kTimes; i0 += 4) {
-                uint4 w[4];
-                uint32_t top[4];
+            // brought to 2^13; a row of K that is not finite, or behind the last: zeros
+            {
+                uint4 w[kTimes][kEach];
+                uint32_t top[kTimes];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[i] = lds_u128(kq_at + unit_at(id / kUnits + (i0 + i) * kDown, unit, 2 * kRows));
+                for (int i = 0; i < kTimes; ++i)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    top[i] = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                      __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+                    for (int e = 0; e < kEach; ++e)
+                        w[i][e] = lds_u128(kq_at + unit_at(id / kLanes + i * kDown, unit + 8 * e, 2 * kRows));
 #pragma unroll
-                for (int o = kUnits / 2; o > 0; o >>= 1)
+                for (int i = 0; i < kTimes; ++i) {
+                    top[i] = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+                    for (int e = 0; e < kEach; ++e)
+                        top[i] = max16x2(top[i], max16x2(max16x2(w[i][e].x & 0x7fff7fffu, w[i][e].y & 0x7fff7fffu),
+                                                         max16x2(w[i][e].z & 0x7fff7fffu, w[i][e].w & 0x7fff7fffu)));
+                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = id / kUnits + (i0 + i) * kDown;
+                for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+                    for (int i = 0; i < kTimes; ++i) top[i] = max16x2(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+#pragma unroll
+                for (int i = 0; i < kTimes; ++i) {
+                    const int r = id / kLanes + i * kDown;
                     const uint32_t most = max(top[i] & 0xffffu, top[i] >> 16);
-                    const bool odd = most >= (p.bf16 ? 0x7f80u : 0x7c00u);
+                    const bool odd = most >= (kBf16 ? 0x7f80u : 0x7c00u), gone = r % kRows >= m || (odd && r < kRows);
                     float2 f = make_float2(1.f, 1.f);
-                    if (p.bf16) {
+                    if (kBf16) {
                         f = fit(__uint_as_float(most << 16));
-                        w[i] = make_uint4(scaled16(w[i].x, f.x), scaled16(w[i].y, f.x), scaled16(w[i].z, f.x), scaled16(w[i].w, f.x));
+                        const uint32_t f2 = (__float_as_uint(f.x) >> 16) * 0x10001u;  // (a power of two is a bf16)
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e)
+                            w[i][e] = make_uint4(scaled16(w[i][e].x, f2), scaled16(w[i][e].y, f2), scaled16(w[i][e].z, f2),
+                                                 scaled16(w[i][e].w, f2));
                     }
-                    if (odd && r < kRows) {
-                        w[i] = make_uint4(0, 0, 0, 0);
-                        if (unit == 0) atomicOr(&gt.odd, 1ull << r);
-                    }
-                    if (p.bf16 || odd) sts_u128(kq_at + unit_at(r, unit, 2 * kRows), w[i]);
-                    if (unit == 0) scales[r] = f.y;
+                    if (odd && r < m && unit == 0) atomicOr(&gt.odd, 1ull << r);
+                    if (kBf16 || gone)
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e)
+                            sts_u128(kq_at + unit_at(r, unit + 8 * e, 2 * kRows), gone ? make_uint4(0, 0, 0, 0) : w[i][e]);
+                    if (unit == 0) scales[r] = gone ? 1.f : f.y;
                 }
             }
             fence_proxy_async_smem();
@@ -358,12 +376,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             // Half a row of the pairs: A from the rows of K, P from those of Q.
             const int pair_row = (warp & 3) * 32 + lane, t = pair_row % kRows, half = (warp - kMainWarps) >> 2;
             const bool is_q = pair_row >= kRows;
-            const uint32_t bits = (uint32_t)(gt.seen[t] >> (32 - 32 * half));  // half 0: columns 32 .. 63, then 0 .. 31
+            const uint64_t from = gt.seen[t] | 1ull << t;  // and the row itself
+            const uint32_t bits = (uint32_t)(from >> (32 - 32 * half));  // half 0: columns 32 .. 63, half 1: 0 .. 31
             const float mine = scales[pair_row], factor = (is_q ? p.scale : gt.beta[t]) * mine;
             const bool last = !is_q && t == m - 1;
-            float run = g_at[t], top = 0.f;  // the decay's logarithm from behind the column
+            float run = 0.f, top = 0.f;  // the logarithm of the decay from behind the column
             if (half == 1) {
-                const uint32_t above = (uint32_t)(gt.seen[t] >> 32);
+                const uint32_t above = (uint32_t)(from >> 32);
 #pragma unroll 2
                 for (int j = kRows - 4; j >= 32; j -= 4) {
                     const float4 g = *reinterpret_cast<const float4*>(g_at + j);
@@ -374,14 +393,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 }
             }
             float* const my_row = A + pair_row * kPitch;
-            lost = !kv_wait(done_pairs, c & 1, abort_flag, err, kDevErrTimeoutDelta);
+            lost |= !kv_wait(done_pairs, c & 1, abort_flag, err, kDevErrTimeoutDelta);
             tc_fence_after();
 #pragma unroll 1
             for (int j0 = 16; j0 >= 0; j0 -= 16) {
                 const int col = 32 - 32 * half + j0;
                 uint32_t x[16];
                 tmem_ld16_wait(tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kPairs + col, x);
-                const int self = t - col;
                 float f[16], g[16];
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
@@ -389,14 +407,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                     f[j] = a.x; f[j + 1] = a.y; f[j + 2] = a.z; f[j + 3] = a.w;
                     g[j] = e.x; g[j + 1] = e.y; g[j + 2] = e.z; g[j + 3] = e.w;
                 }
+                const uint32_t here = bits >> j0;
 #pragma unroll
                 for (int j = 15; j >= 0; --j) {
-                    const bool from = bits >> (j0 + j) & 1;
-                    f[j] *= self == j ? 1.f : from ? fast_exp2(run) : 0.f;
-                    run += from ? g[j] : 0.f;
-                    const float y = from || is_q ? __uint_as_float(x[j]) * (factor * f[j]) : 0.f;
-                    x[j] = __float_as_uint(f[j] == 0.f ? 0.f : y);  // (rows behind the last hold no values to scale)
-                    top = fmaxf(top, fabsf(__uint_as_float(x[j])));
+                    const bool with = here >> j & 1;
+                    f[j] = with ? f[j] * fast_exp2(run) : 0.f;
+                    run += with ? g[j] : 0.f;
+                    const float y = __uint_as_float(x[j]) * (factor * f[j]);  // (A's diagonal is not read)
+                    x[j] = __float_as_uint(y);
+                    top = fmaxf(top, fabsf(y));
                 }
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
@@ -452,7 +471,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                     Ts[(at + i) * kPitch + t] = x[i];
                 }
             }
-            if (c + 1 < blocks && (c < 1 || mbar_try_wait(smem_u32(empty + (buf ^ 1)), ((c + 1) / 2 - 1) & 1))) stage(c + 1);
+            load_gates(t0 + kRows);
+            if (id == 0 && c + 1 < blocks && (c < 1 || mbar_try_wait(smem_u32(empty + (buf ^ 1)), ((c + 1) / 2 - 1) & 1)))
+                stage(c + 1);
             prep_sync();
             // N x N blocks, R rows of a column a thread: X = A21 T11 into the
             // empty block above, then T21 = -T22 X.
@@ -522,10 +543,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             mbar_arrive(full + buf);
         }
         // Tensor memory is given back only when every product is done.
+        // And no copy may be in flight when the CTA ends.
         if (*abort_flag && id == 0) {
             tc_commit(drained + 1);
             int no_abort = 0;
             kv_wait(drained + 1, 0, &no_abort, err, kDevErrTimeoutDelta);
+            for (int c = max(0, staged - 1); c <= staged; ++c)
+                kv_wait(landed + (c & 1), (c / 2) & 1, &no_abort, err, kDevErrTimeoutDeltaRows);
         }
     } else {
         // ------------------------------------------------------------ the blocks
@@ -582,6 +606,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         auto put_rows = [&] {
             if (!busy) return;
             float* to = p.out + o_first * p.out_row_stride + head * DV + at_lane;
+            if (o_rows >= 32 && !kBoundsCheck) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i, to += p.out_row_stride) *to = i & 1 ? o[i / 2].y : o[i / 2].x;
+                return;
+            }
 #pragma unroll
             for (int i = 0; i < 32; ++i, to += p.out_row_stride)
                 if (i < o_rows && bc_global(bc, to, 4, p.out, 4 * ((p.rows - 1) * p.out_row_stride + values), kBcDeltaOut))
@@ -612,6 +641,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             lost |= !kv_wait(done1, c & 1, abort_flag, err, kDevErrTimeoutDelta);
             float inverse_r = 1.f;
             uint64_t odd = gt.odd;
+            const uint64_t rows_in = ~0ull >> (kRows - m);  // (V behind them is another's)
             if (busy) {
                 tc_fence_after();
                 uint32_t x[32];
@@ -628,7 +658,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t both = v[(2 * (i + e)) * DV] | (uint32_t)v[(2 * (i + e) + 1) * DV] << 16;
-                        const float2 value = p.bf16 ? KvBf16::unpack(both) : KvF16::unpack(both);
+                        const float2 value = kBf16 ? KvBf16::unpack(both) : KvF16::unpack(both);
                         const float2 xs = make_float2(__uint_as_float(x[2 * (i + e)]), __uint_as_float(x[2 * (i + e) + 1]));
                         r[i + e] = fma2(mul2(xs, inverse2), e ? make_float2(bg.z, bg.w) : make_float2(bg.x, bg.y),
                                         mul2(value, e ? make_float2(beta.z, beta.w) : make_float2(beta.x, beta.y)));
@@ -640,7 +670,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 largest(1, top);
                 odds[share * 128 + at_lane] = bits;
                 pair_sync(quad);
-                odd |= (uint64_t)odds[128 + at_lane] << 32 | odds[at_lane];
+                odd |= ((uint64_t)odds[128 + at_lane] << 32 | odds[at_lane]) & rows_in;
                 const float2 f = fit(largest_of(1));
                 inverse_r = f.y;
                 uint32_t hi[16], lo[16];
@@ -705,7 +735,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 largest(2, top);
                 largest(3, top_f);
                 pair_sync(quad);
-                odd |= (uint64_t)odds[256 + 128 + at_lane] << 32 | odds[256 + at_lane];
+                odd |= ((uint64_t)odds[256 + 128 + at_lane] << 32 | odds[256 + at_lane]) & rows_in;
                 const float2 f = fit(largest_of(2)), ff = fit(largest_of(3));
                 inverse_u = f.y;
                 inverse_f = ff.y;
@@ -820,20 +850,52 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-template <int DK, int DV>
-cudaError_t launch_chunk(const DeltaRule& p, const DeltaView& d, const BatchView& b, int* err, cudaStream_t stream) {
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Rows of `width` 16-bit values, in boxes of kRows rows by `box`.
+bool encode_rows(void* enc, const uint16_t* base, int64_t width, int64_t rows, int64_t stride, int box, CUtensorMapSwizzle swizzle,
+                 CUtensorMap* map) {
+    const cuuint64_t gdim[2] = {(cuuint64_t)width, (cuuint64_t)rows}, gstride[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box_dim[2] = {(cuuint32_t)box, (cuuint32_t)kRows}, estride[2] = {1, 1};
+    return reinterpret_cast<EncodeTiledFn>(enc)(
+               map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<uint16_t*>(base), gdim, gstride, box_dim, estride,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK, int DV, bool kBf16>
+cudaError_t launch_type(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err,
+                        cudaStream_t stream) {
     using C = ChunkShape<DK, DV>;
-    const cudaError_t e = allow_smem<delta_chunk_kernel<DK, DV>>(C::kSmem);
+    CUtensorMap q, k, v;
+    const int64_t keys = (int64_t)d.key_heads * DK, values = (int64_t)d.heads * DV;
+    if (!encode_rows(encode, p.q, keys, p.rows, p.q_row_stride, 64, CU_TENSOR_MAP_SWIZZLE_128B, &q) ||
+        !encode_rows(encode, p.k, keys, p.rows, p.k_row_stride, 64, CU_TENSOR_MAP_SWIZZLE_128B, &k) ||
+        !encode_rows(encode, p.v, values, p.rows, p.v_row_stride, DV, CU_TENSOR_MAP_SWIZZLE_NONE, &v))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = allow_smem<delta_chunk_kernel<DK, DV, kBf16>>(C::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_chained(delta_chunk_kernel<DK, DV>, dim3((unsigned)((int64_t)b.sequences * d.heads)), dim3(kChunkThreads),
-                          C::kSmem, stream, 1, p, d, b, err);
+    return launch_chained(delta_chunk_kernel<DK, DV, kBf16>, dim3((unsigned)((int64_t)b.sequences * d.heads)),
+                          dim3(kChunkThreads), C::kSmem, stream, 1, q, k, v, p, d, b, err);
+}
+template <int DK, int DV>
+cudaError_t launch_chunk(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err,
+                         cudaStream_t stream) {
+    return p.bf16 ? launch_type<DK, DV, true>(p, d, b, encode, err, stream)
+                  : launch_type<DK, DV, false>(p, d, b, encode, err, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_delta_chunk(const DeltaRule& p, const DeltaView& d, const BatchView& b, int* err, cudaStream_t stream) {
-    if (d.key_dim == 64) return d.value_dim == 64 ? launch_chunk<64, 64>(p, d, b, err, stream) : launch_chunk<64, 128>(p, d, b, err, stream);
-    return d.value_dim == 64 ? launch_chunk<128, 64>(p, d, b, err, stream) : launch_chunk<128, 128>(p, d, b, err, stream);
+cudaError_t launch_delta_chunk(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err,
+                               cudaStream_t stream) {
+    if (d.key_dim == 64)
+        return d.value_dim == 64 ? launch_chunk<64, 64>(p, d, b, encode, err, stream)
+                                 : launch_chunk<64, 128>(p, d, b, encode, err, stream);
+    return d.value_dim == 64 ? launch_chunk<128, 64>(p, d, b, encode, err, stream)
+                             : launch_chunk<128, 128>(p, d, b, encode, err, stream);
 }
 
 }  // namespace iq4xs

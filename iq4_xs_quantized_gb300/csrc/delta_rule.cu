@@ -305,11 +305,11 @@ cudaError_t launch_keys(const DeltaRule& p, const DeltaView& d, const BatchView&
 
 }  // namespace
 
-cudaError_t launch_delta_rule(const DeltaRule& p, const DeltaView& d, const BatchView& b, int* err, int num_sms,
+cudaError_t launch_delta_rule(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err, int num_sms,
                               cudaStream_t stream) {
     // A tree is one block; chains of more than 12 rows on average go in blocks of 64.
     if (p.u != nullptr ? p.max_rows > 16 : p.rows > 12 * (int64_t)b.sequences && p.max_rows > 16)
-        return launch_delta_chunk(p, d, b, err, stream);
+        return launch_delta_chunk(p, d, b, encode, err, stream);
     return d.key_dim == 64 ? launch_keys<64>(p, d, b, err, num_sms, stream)
                            : launch_keys<128>(p, d, b, err, num_sms, stream);
 }

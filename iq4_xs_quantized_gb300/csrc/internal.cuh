@@ -213,7 +213,8 @@ enum DeviceError : int {
     kDevErrTimeoutKv = 0x10D,        // attention: a stage of keys or values never landed
     kDevErrTimeoutKvSlot = 0x10E,    // attention: a stage slot was never freed
     kDevErrTimeoutScore = 0x10F,     // attention: a score or output product never completed
-    kDevErrTimeoutDelta = 0x110,     // delta rule: a product never completed
+    kDevErrTimeoutDelta = 0x110,     // delta rule: a product or a block's operands never came
+    kDevErrTimeoutDeltaRows = 0x111, // delta rule: a block's rows never landed
     kDevErrBounds = 0x200,           // + BoundsSite: a checked access missed its buffer
     kDevErrData = 0x300,             // + DataSite: a value read from device memory was out of range
 };
@@ -338,7 +339,7 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s: waits for a 
 // slices 6 s.
 __host__ __device__ constexpr unsigned long long wait_limit_ns(int code) {
     return (code == kDevErrTimeoutW || code == kDevErrTimeoutQ || code == kDevErrTimeoutMmaStage ||
-            code == kDevErrTimeoutKv)
+            code == kDevErrTimeoutKv || code == kDevErrTimeoutDeltaRows)
                ? kWaitLimitNs
            : (code == kDevErrTimeoutDrain || code == kDevErrTimeoutRecv) ? 3 * kWaitLimitNs
                                                                           : 2 * kWaitLimitNs;
