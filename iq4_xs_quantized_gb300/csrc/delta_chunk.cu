@@ -72,8 +72,9 @@ struct ChunkShape {
     static constexpr int kGates = kTs + kRows * kPitch * 4;
     static constexpr int kTops = kGates + 2 * (int)sizeof(Gates);  // [S, r, u, u F][share][128] largest
     static constexpr int kOdd = kTops + 4 * 2 * 128 * 4;           // [r, u][share][128] rows not finite
-    static constexpr int kScales = kOdd + 2 * 2 * 128 * 4;         // [128] of K's and Q's rows; their g; P's largest
-    static constexpr int kBars = kScales + 5 * kRows * 4;
+    static constexpr int kScales = kOdd + 2 * 2 * 128 * 4;         // [128] of K's and Q's rows; their g and beta; P's largest
+    static constexpr int kSeen = kScales + 6 * kRows * 4;           // [64] 64-bit, and the rows that are not finite
+    static constexpr int kBars = kSeen + kRows * 8 + 8;
     static constexpr int kMisc = kBars + 16 * 8;
     static constexpr int kSmem = kMisc + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -132,6 +133,34 @@ __device__ __forceinline__ uint4 lds_u128(uint32_t at) {
     uint4 w;
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
     return w;
+}
+// Products issued by a whole warp, of which one lane (`one`) counts: descriptors
+// and columns then stay in uniform registers.
+__device__ __forceinline__ void mma_ta(bool one, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n\t}" ::"r"((uint32_t)one),
+        "r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ss(bool one, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n\t}" ::"r"((uint32_t)one),
+        "r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void commit_one(bool one, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"((uint32_t)one),
+        "r"(smem_u32(bar))
+        : "memory");
 }
 __device__ __forceinline__ bool odd_value(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
 
@@ -205,7 +234,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);  // [2] a block is prepared
     uint64_t* empty = full + 2;                                     // [2] and used
     uint64_t* landed = empty + 2;                                   // [2] its rows have come
-    uint64_t* done1 = landed + 2;
+    uint64_t* unread = landed + 2;                                  // [2] and are not needed any more
+    uint64_t* done1 = unread + 2;
     uint64_t* done2 = done1 + 1;
     uint64_t* done_s = done2 + 1;
     uint64_t* done_o = done_s + 1;
@@ -234,6 +264,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             mbar_init(full + i, kPrepThreads);
             mbar_init(empty + i, kMainWarps);
             mbar_init(landed + i, 1);
+            mbar_init(unread + i, 1);
             mbar_init(drained + i, 1);
         }
         mbar_init(done1, 1);
@@ -266,9 +297,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         const int unit = id % kLanes;
         float* const scales = reinterpret_cast<float*>(smem + C::kScales);  // what K's and Q's rows are to be multiplied by
         float* const g_at = scales + 2 * kRows;                             // in log2
-        float* const maxima = g_at + kRows;  // [half] of P's rows
+        float* const beta_at = g_at + kRows;
+        float* const maxima = beta_at + kRows;  // [half] of P's rows
+        unsigned long long* const seen_at = reinterpret_cast<unsigned long long*>(smem + C::kSeen);
+        unsigned long long* const odd_at = seen_at + kRows;
         float* const A = reinterpret_cast<float*>(smem + C::kA);
         float* const Ts = reinterpret_cast<float*>(smem + C::kTs);
+        float* const X = A + 32;  // (A's rows 0 .. 31 have no columns there)
+        for (int i = id; i < kRows * kPitch; i += kPrepThreads) Ts[i] = 0.f;  // (above the diagonal nothing is written)
+        const bool one = elect_one();
         int staged = -1;  // the last block whose rows the first thread has asked for
         // K, Q and V of a block as they lie; what comes behind its last row is another's, or zeros
         auto stage = [&](int c) {
@@ -300,20 +337,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         for (int c = 0; c < blocks; ++c) {
             const int buf = c & 1, t0 = c * kRows, m = min(kRows, n - t0);
             Gates& gt = gates[buf];
-            bool lost = c >= 2 && !kv_wait(empty + buf, (c / 2 - 1) & 1, abort_flag, err, kDevErrTimeoutDelta);
-            if (any_of<6, kPrepThreads>(lost)) break;  // (all leave together)
             const uint32_t kq_at = base + C::kKq + buf * C::kKqBytes;
-            if (id == 0 && staged != c) stage(c);
+            bool lost = false;
+            if (id == 0 && staged != c) {
+                lost = c >= 2 && !kv_wait(unread + buf, (c / 2 - 1) & 1, abort_flag, err, kDevErrTimeoutDelta);
+                if (!lost) stage(c);
+            }
+            if (any_of<6, kPrepThreads>(lost)) break;  // (all leave together)
             if (id < kRows) {
                 float g = g_next, beta = beta_next;
                 const bool odd = odd_value(beta) || isnan(g) || g == INFINITY;
                 if (odd) g = beta = 0.f;
                 g_at[id] = g * 1.44269504088896340736f;
-                gt.beta[id] = beta;
-                gt.seen[id] = id < m ? delta_seen(p.tree_mask, p.mask_words, p.rows, row0, id, bc) : 0;
-                gt.left[id] = 0.f;
+                beta_at[id] = beta;
+                seen_at[id] = id < m ? delta_seen(p.tree_mask, p.mask_words, p.rows, row0, id, bc) : 0;
                 const unsigned bits = __ballot_sync(0xffffffffu, odd);
-                if (lane == 0) reinterpret_cast<unsigned*>(&gt.odd)[id / 32] = bits;
+                if (lane == 0) reinterpret_cast<unsigned*>(odd_at)[id / 32] = bits;
             }
             lost = !kv_wait(landed + buf, (c / 2) & 1, abort_flag, err, kDevErrTimeoutDeltaRows);
             prep_sync();
@@ -353,7 +392,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                             w[i][e] = make_uint4(scaled16(w[i][e].x, f2), scaled16(w[i][e].y, f2), scaled16(w[i][e].z, f2),
                                                  scaled16(w[i][e].w, f2));
                     }
-                    if (odd && r < m && unit == 0) atomicOr(&gt.odd, 1ull << r);
+                    if (odd && r < m && unit == 0) atomicOr(odd_at, 1ull << r);
                     if (kBf16 || gone)
 #pragma unroll
                         for (int e = 0; e < kEach; ++e)
@@ -363,22 +402,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             }
             fence_proxy_async_smem();
             prep_sync();
-            if (id == 0) {
+            if (warp == kMainWarps) {
                 tc_fence_after();
                 const uint64_t kq = desc_sw128(kq_at, 16, 1024);
 #pragma unroll
                 for (int k = 0; k < DK / 16; ++k) {
                     const uint64_t at = kq + (((k / 4) * 2 * kRows * kChunkBytes + (k % 4) * 32) >> 4);
-                    tc_mma_f16(tmem + C::kPairs, at, at, idesc_kv(kRows, 0, false), k > 0);
+                    mma_ss(one, tmem + C::kPairs, at, at, idesc_kv(kRows, 0, false), k > 0);
                 }
-                tc_commit(done_pairs);
+                commit_one(one, done_pairs);
             }
             // Half a row of the pairs: A from the rows of K, P from those of Q.
             const int pair_row = (warp & 3) * 32 + lane, t = pair_row % kRows, half = (warp - kMainWarps) >> 2;
             const bool is_q = pair_row >= kRows;
-            const uint64_t from = gt.seen[t] | 1ull << t;  // and the row itself
+            const uint64_t from = seen_at[t] | 1ull << t;  // and the row itself
             const uint32_t bits = (uint32_t)(from >> (32 - 32 * half));  // half 0: columns 32 .. 63, half 1: 0 .. 31
-            const float mine = scales[pair_row], factor = (is_q ? p.scale : gt.beta[t]) * mine;
+            const float mine = scales[pair_row], factor = (is_q ? p.scale : beta_at[t]) * mine;
             const bool last = !is_q && t == m - 1;
             float run = 0.f, top = 0.f;  // the logarithm of the decay from behind the column
             if (half == 1) {
@@ -394,6 +433,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             }
             float* const my_row = A + pair_row * kPitch;
             lost |= !kv_wait(done_pairs, c & 1, abort_flag, err, kDevErrTimeoutDelta);
+            // (the block before the last has been used, its gates too)
+            lost |= c >= 2 && !kv_wait(empty + buf, (c / 2 - 1) & 1, abort_flag, err, kDevErrTimeoutDelta);
             tc_fence_after();
 #pragma unroll 1
             for (int j0 = 16; j0 >= 0; j0 -= 16) {
@@ -426,10 +467,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             if (half == 1) {
                 const float all = fast_exp2(run);  // from the block's start
                 if (is_q) gt.gq[t] = p.scale * all * mine;
-                else gt.bg[t] = -gt.beta[t] * all * mine;
+                else gt.bg[t] = -beta_at[t] * all * mine;
                 if (last) gt.decay = all;
             }
-            if (is_q) maxima[half * kRows + t] = top;
+            if (is_q) {
+                maxima[half * kRows + t] = top;
+            } else if (half == 0) {
+                gt.beta[t] = beta_at[t];
+                gt.seen[t] = seen_at[t];
+                if (t == 0) gt.odd = *odd_at;
+            }
             tc_fence_before();
             // Part of a row in fp32 -> its parts
             auto put_parts = [&](const float* row, int u0, int u1, float scale, uint32_t to, int r) {
@@ -472,17 +519,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 }
             }
             load_gates(t0 + kRows);
-            if (id == 0 && c + 1 < blocks && (c < 1 || mbar_try_wait(smem_u32(empty + (buf ^ 1)), ((c + 1) / 2 - 1) & 1)))
+            if (id == 0 && c + 1 < blocks && (c < 1 || mbar_try_wait(smem_u32(unread + (buf ^ 1)), ((c + 1) / 2 - 1) & 1)))
                 stage(c + 1);
             prep_sync();
-            // N x N blocks, R rows of a column a thread: X = A21 T11 into the
-            // empty block above, then T21 = -T22 X.
-            auto below = [&](auto n_tag, auto r_tag, int at, int col, int rows_at) {
+            // N x N blocks, R rows of a column a thread: X = A21 T11, then T21 = -T22 X.
+            auto below = [&](auto n_tag, auto r_tag, int at, float* x_at, int col, int rows_at) {
                 constexpr int N = decltype(n_tag)::value, R = decltype(r_tag)::value;
 #pragma unroll 1
                 for (int pass = 0; pass < 2; ++pass) {
                     const float* left = (pass == 0 ? A + (at + N + rows_at) * kPitch + at : Ts + (at + N + rows_at) * kPitch + at + N);
-                    const float* right = Ts + at * kPitch + at + col + (pass == 0 ? 0 : N);
+                    const float* right = pass == 0 ? Ts + at * kPitch + at + col : x_at + col;
                     float z[R][4] = {};
 #pragma unroll
                     for (int j0 = 0; j0 < N; j0 += 16) {
@@ -501,7 +547,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                             }
                         }
                     }
-                    float* to = pass == 0 ? Ts + (at + rows_at) * kPitch + at + N + col : Ts + (at + N + rows_at) * kPitch + at + col;
+                    float* to = pass == 0 ? x_at + rows_at * kPitch + col : Ts + (at + N + rows_at) * kPitch + at + col;
 #pragma unroll
                     for (int i = 0; i < R; ++i) {
                         const float y = (z[i][0] + z[i][1]) + (z[i][2] + z[i][3]);
@@ -509,28 +555,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                     }
                     prep_sync();
                 }
-                if (N == 16) {  // what is above the diagonal is zero to the next level
-#pragma unroll
-                    for (int i = 0; i < R; ++i) Ts[(at + rows_at + i) * kPitch + at + N + col] = 0.f;
-                    prep_sync();
-                }
             };
-            below(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{}, id / 128 * 32, id % 16, id % 128 / 16 * 2);
-            below(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{}, 0, lane, (warp - kMainWarps) * 4);
+            below(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{}, id / 128 * 32, X + id / 128 * 16, id % 16,
+                  id % 128 / 16 * 2);
+            below(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{}, 0, X, lane, (warp - kMainWarps) * 4);
             {
-                // A quarter of a row a thread (above the diagonal lies what was left of X).
-                const int row = id / 4, quarter = id % 4, lim = row - 16 * quarter;
-                float* const mine_at = Ts + row * kPitch + 16 * quarter;
+                // A quarter of a row a thread.
+                const int row = id / 4, quarter = id % 4;
                 float most = 0.f;
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
-                    float4 w = *reinterpret_cast<const float4*>(mine_at + j);
-                    w.x = j <= lim ? w.x : 0.f;
-                    w.y = j + 1 <= lim ? w.y : 0.f;
-                    w.z = j + 2 <= lim ? w.z : 0.f;
-                    w.w = j + 3 <= lim ? w.w : 0.f;
-                    most = fmaxf(fmaxf(fmaxf(most, fabsf(w.x)), fmaxf(fabsf(w.y), fabsf(w.z))), fabsf(w.w));
-                    *reinterpret_cast<float4*>(mine_at + j) = w;
+                    const float4 w = *reinterpret_cast<const float4*>(Ts + row * kPitch + 16 * quarter + j);
+                    most = max3(max3(most, w.x, w.y), w.z, w.w);
                 }
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
@@ -544,10 +580,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         }
         // Tensor memory is given back only when every product is done.
         // And no copy may be in flight when the CTA ends.
-        if (*abort_flag && id == 0) {
+        if (*abort_flag && warp == kMainWarps && one) {
             tc_commit(drained + 1);
             int no_abort = 0;
             kv_wait(drained + 1, 0, &no_abort, err, kDevErrTimeoutDelta);
+        }
+        if (*abort_flag && id == 0) {
+            int no_abort = 0;
             for (int c = max(0, staged - 1); c <= staged; ++c)
                 kv_wait(landed + (c & 1), (c / 2) & 1, &no_abort, err, kDevErrTimeoutDeltaRows);
         }
@@ -599,25 +638,64 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             tmem_wait_st();
         };
         if (busy) put_state();
+        const bool one = elect_one();
         bool lost = false;
-        float2 o[16];
-        int o_rows = 0;          // rows of `o` on their way out
-        int64_t o_first = 0;
-        auto put_rows = [&] {
+        // o of the last block: S^T q's and U's parts lie in its columns until the block after next writes there.
+        auto take_rows = [&](int c, uint64_t odd, float scale_s, float scale_u) {
+            const int buf = c & 1, m = min(kRows, n - c * kRows), first = 32 * share;
+            const uint32_t at_d = buf ? C::kNew : C::kD;
+            const Gates& gt = gates[buf];
+            float2 o[16];
+            if (busy) {
+                tc_fence_after();
+                const float2 inv_s = make_float2(scale_s, scale_s), inv_u = make_float2(scale_u, scale_u);
+#pragma unroll
+                for (int h = 0; h < 32; h += 16) {
+                    uint32_t x[16], y[16];
+                    tmem_ld16_wait(lane_at + at_d + first + h, x);
+                    tmem_ld16_wait(lane_at + at_d + kRows + first + h, y);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 gq = *reinterpret_cast<const float4*>(gt.gq + first + h + i);
+                        const float4 cp = *reinterpret_cast<const float4*>(gt.cp + first + h + i);
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const float2 xs = make_float2(__uint_as_float(x[i + e]), __uint_as_float(x[i + e + 1]));
+                            const float2 ys = make_float2(__uint_as_float(y[i + e]), __uint_as_float(y[i + e + 1]));
+                            o[(h + i + e) / 2] = fma2(mul2(ys, inv_s), e ? make_float2(gq.z, gq.w) : make_float2(gq.x, gq.y),
+                                                      mul2(mul2(xs, inv_u), e ? make_float2(cp.z, cp.w) : make_float2(cp.x, cp.y)));
+                        }
+                    }
+                }
+                if (odd != 0) {
+                    const uint32_t gone = hide(o, gt, first, odd);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (gone >> (2 * i) & 1) o[i].x = NAN;
+                        if (gone >> (2 * i + 1) & 1) o[i].y = NAN;
+                    }
+                }
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + buf);
             if (!busy) return;
-            float* to = p.out + o_first * p.out_row_stride + head * DV + at_lane;
-            if (o_rows >= 32 && !kBoundsCheck) {
+            float* to = p.out + (row0 + c * kRows + first) * p.out_row_stride + head * DV + at_lane;
+            if (m - first >= 32 && !kBoundsCheck) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i, to += p.out_row_stride) *to = i & 1 ? o[i / 2].y : o[i / 2].x;
                 return;
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i, to += p.out_row_stride)
-                if (i < o_rows && bc_global(bc, to, 4, p.out, 4 * ((p.rows - 1) * p.out_row_stride + values), kBcDeltaOut))
+                if (first + i < m && bc_global(bc, to, 4, p.out, 4 * ((p.rows - 1) * p.out_row_stride + values), kBcDeltaOut))
                     *to = i & 1 ? o[i / 2].y : o[i / 2].x;
         };
+        uint64_t odd_last = 0;
+        float scale_s = 1.f, scale_u = 1.f;
         for (int c = 0; c < blocks; ++c) {
             const int buf = c & 1, t0 = c * kRows, m = min(kRows, n - t0);
+            const uint32_t at_d = buf ? C::kNew : C::kD, at_new = buf ? C::kD : C::kNew;  // (in turn)
             const Gates& gt = gates[buf];
             lost |= !kv_wait(full + buf, (c / 2) & 1, abort_flag, err, kDevErrTimeoutDelta);
             tc_fence_before();
@@ -625,18 +703,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             const uint64_t kq = desc_sw128(base + C::kKq + buf * C::kKqBytes, 16, 1024);
             const uint64_t td = desc_sw128(base + C::kT + buf * 2 * C::kPartBytes, 16, 1024);
             const uint64_t pd = desc_sw128(base + C::kP + buf * 2 * C::kPartBytes, 16, 1024);
-            if (tid == 0) {
+            if (warp == 0) {
                 tc_fence_after();
 #pragma unroll
                 for (int part = 1; part >= 0; --part)  // the smaller parts first
 #pragma unroll
                     for (int k = 0; k < DK / 16; ++k)
-                        tc_mma_f16_ta(tmem + C::kD, tmem + C::kParts + part * DK / 2 + 8 * k,
+                        mma_ta(one, tmem + at_d, tmem + C::kParts + part * DK / 2 + 8 * k,
                                       kq + (((k / 4) * 2 * kRows * kChunkBytes + (k % 4) * 32) >> 4),
                                       idesc_kv(2 * kRows, 0, false), part == 0 || k > 0);
-                tc_commit(done1);
+                commit_one(one, done1);
             }
-            put_rows();  // (the last block's)
+            if (c > 0) take_rows(c - 1, odd_last, scale_s, scale_u);  // (under the product)
             const int first = 32 * share;  // the thread's rows of the block
             lost |= !kv_wait(done1, c & 1, abort_flag, err, kDevErrTimeoutDelta);
             float inverse_r = 1.f;
@@ -645,7 +723,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             if (busy) {
                 tc_fence_after();
                 uint32_t x[32];
-                tmem_ld32_wait(lane_at + C::kD + first, x);
+                tmem_ld32_wait(lane_at + at_d + first, x);
                 const uint16_t* v = reinterpret_cast<const uint16_t*>(smem + C::kV + buf * C::kVBytes) + first * DV + at_lane;
                 const float2 inverse2 = make_float2(inverse_s, inverse_s);
                 float2 r[16], zero = make_float2(0.f, 0.f);
@@ -682,23 +760,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             }
             tc_fence_before();
             main_sync();
-            if (tid == 0) {
+            if (warp == 0) {
                 tc_fence_after();
                 constexpr uint32_t kId = idesc_kv(kRows, 0, false);
 #pragma unroll
                 for (int pass = 0; pass < 3; ++pass)  // remainder by value, value by remainder, value by value
 #pragma unroll
                     for (int k = 0; k < kRows / 16; ++k)
-                        tc_mma_f16_ta(tmem + C::kD, tmem + C::kR + (pass == 0 ? kRows / 2 : 0) + 8 * k,
+                        mma_ta(one, tmem + at_d, tmem + C::kR + (pass == 0 ? kRows / 2 : 0) + 8 * k,
                                       td + (((pass == 1 ? C::kPartBytes : 0) + k * 32) >> 4), kId, pass > 0 || k > 0);
-                tc_commit(done2);
+                commit_one(one, done2);
             }
             lost |= !kv_wait(done2, c & 1, abort_flag, err, kDevErrTimeoutDelta);
             float inverse_u = 1.f, inverse_f = 1.f;
             if (busy) {
                 tc_fence_after();
                 uint32_t x[32];
-                tmem_ld32_wait(lane_at + C::kD + first, x);
+                tmem_ld32_wait(lane_at + at_d + first, x);
                 float2 u[16], zero = make_float2(0.f, 0.f);
                 const float2 inverse2 = make_float2(inverse_r, inverse_r);
                 uint32_t bits = 0;
@@ -754,7 +832,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             }
             tc_fence_before();
             main_sync();
-            if (tid == 0) {
+            if (warp == 0) {
                 tc_fence_after();
                 if (!keep) {
                     const uint64_t kn = desc_sw128(base + C::kKq + buf * C::kKqBytes, 2 * kRows * kChunkBytes, 1024);
@@ -762,18 +840,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                     for (int part = 1; part >= 0; --part)
 #pragma unroll
                         for (int k = 0; k < kRows / 16; ++k)
-                            tc_mma_f16_ta(tmem + C::kNew, tmem + C::kParts + kRows + part * kRows / 2 + 8 * k,
+                            mma_ta(one, tmem + at_new, tmem + C::kParts + kRows + part * kRows / 2 + 8 * k,
                                           kn + ((k * 16 * kChunkBytes) >> 4), idesc_kv(DK, 0, true), part == 0 || k > 0);
-                    tc_commit(done_s);
+                    commit_one(one, done_s);
                 }
                 constexpr uint32_t kId = idesc_kv(kRows, 0, false);
 #pragma unroll
                 for (int pass = 0; pass < 3; ++pass)
 #pragma unroll
                     for (int k = 0; k < kRows / 16; ++k)
-                        tc_mma_f16_ta(tmem + C::kD, tmem + C::kParts + (pass == 0 ? kRows / 2 : 0) + 8 * k,
+                        mma_ta(one, tmem + at_d, tmem + C::kParts + (pass == 0 ? kRows / 2 : 0) + 8 * k,
                                       pd + (((pass == 1 ? C::kPartBytes : 0) + k * 32) >> 4), kId, pass > 0 || k > 0);
-                tc_commit(done_o);
+                commit_one(one, done_o);
+                commit_one(one, unread + buf);
             }
             if (!keep) {
                 lost |= !kv_wait(done_s, c & 1, abort_flag, err, kDevErrTimeoutDelta);
@@ -783,7 +862,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
 #pragma unroll
                     for (int i = 0; i < C::kHalf; i += 32) {
                         uint32_t x[32];
-                        tmem_ld32_wait(lane_at + C::kNew + share * C::kHalf + i, x);
+                        tmem_ld32_wait(lane_at + at_new + share * C::kHalf + i, x);
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             S[i / 2 + e] = fma2(S[i / 2 + e], decay2,
@@ -796,49 +875,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 }
             }
             lost |= !kv_wait(done_o, c & 1, abort_flag, err, kDevErrTimeoutDelta);
-            if (busy) {
+            odd_last = odd;
+            scale_s = inverse_s;
+            scale_u = inverse_u;
+            if (busy && c + 1 < blocks) {
                 tc_fence_after();
-                uint32_t x[32], y[32];
-                tmem_ld32_wait(lane_at + C::kD + first, x);
-                tmem_ld32_wait(lane_at + C::kD + kRows + first, y);
-                const float2 inv_s = make_float2(inverse_s, inverse_s), inv_u = make_float2(inverse_u, inverse_u);
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const float4 gq = *reinterpret_cast<const float4*>(gt.gq + first + 2 * i);
-                    const float4 cp = *reinterpret_cast<const float4*>(gt.cp + first + 2 * i);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int k = 2 * (i + e);
-                        const float2 xs = make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-                        const float2 ys = make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]));
-                        o[i + e] = fma2(mul2(ys, inv_s), e ? make_float2(gq.z, gq.w) : make_float2(gq.x, gq.y),
-                                        mul2(mul2(xs, inv_u), e ? make_float2(cp.z, cp.w) : make_float2(cp.x, cp.y)));
-                    }
-                }
-                if (odd != 0) {
-                    const uint32_t gone = hide(o, gt, first, odd);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (gone >> (2 * i) & 1) o[i].x = NAN;
-                        if (gone >> (2 * i + 1) & 1) o[i].y = NAN;
-                    }
-                }
-                o_rows = m - first;
-                o_first = row0 + t0 + first;
-                if (c + 1 < blocks) put_state();
+                put_state();
             }
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + buf);
         }
-        put_rows();
+        if (!lost) take_rows(blocks - 1, odd_last, scale_s, scale_u);
         if (!keep && busy && !lost) {
 #pragma unroll
             for (int i = 0; i < C::kHalf; ++i)
                 if (bc_global(bc, at_s + i * DV, 4, d.s, d.s_extent, kBcDeltaS))
                     at_s[i * DV] = i & 1 ? S[i / 2].y : S[i / 2].x;
         }
-        if (*abort_flag && tid == 0) {
+        if (*abort_flag && warp == 0 && one) {
             tc_commit(drained);
             int no_abort = 0;
             kv_wait(drained, 0, &no_abort, err, kDevErrTimeoutDelta);
