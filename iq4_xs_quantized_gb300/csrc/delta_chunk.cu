@@ -72,8 +72,8 @@ struct ChunkShape {
     static constexpr int kGates = kTs + kRows * kPitch * 4;
     static constexpr int kTops = kGates + 2 * (int)sizeof(Gates);  // [S, r, u, u F][share][128] largest
     static constexpr int kOdd = kTops + 4 * 2 * 128 * 4;           // [r, u][share][128] rows not finite
-    static constexpr int kScales = kOdd + 2 * 2 * 128 * 4;         // [128] of K's and Q's rows; their g and beta; P's largest
-    static constexpr int kSeen = kScales + 6 * kRows * 4;           // [64] 64-bit, and the rows that are not finite
+    static constexpr int kScales = kOdd + 2 * 2 * 128 * 4;         // [128] of K's and Q's rows; their g and beta; P's largest; g summed up
+    static constexpr int kSeen = kScales + 7 * kRows * 4;           // [64] 64-bit, and the rows that are not finite
     static constexpr int kBars = kSeen + kRows * 8 + 8;
     static constexpr int kMisc = kBars + 16 * 8;
     static constexpr int kSmem = kMisc + 16;
@@ -103,6 +103,9 @@ __device__ __forceinline__ bool any_of(bool x) {
         : "r"((uint32_t)x), "n"(kBar), "n"(kThreads)
         : "memory");
     return r != 0;
+}
+__device__ __forceinline__ void prefetch_2d(const void* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
 }
 // A power of two that brings `top` to 2^13 .. 2^14, and its inverse; 1 where it is 0 or not finite.
 __device__ __forceinline__ float2 fit(float top) {
@@ -217,6 +220,43 @@ __device__ __forceinline__ uint32_t hide(float2 (&x)[16], const Gates& gt, int f
     return bits;
 }
 
+// D += A B of a 16 x 8 x 8 tile by the warp-level MMA on tf32, both sides in two parts.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// A tile (16 rows from `rows`, 8 columns from `cols`) of an N x N block below T's
+// diagonal at `at`: pass 0, X = A21 T11; pass 1, T21 = -T22 X.
+template <int N>
+__device__ __forceinline__ void below_tile(const float* A, float* T, float* X, int at, int rows, int cols, int lane, int pass) {
+    const int g = lane / 4, t = lane % 4;
+    const float* left = (pass == 0 ? A : T + N) + (at + N + rows + g) * kPitch + at + t;
+    const float* right = (pass == 0 ? T + at * kPitch + at : X) + t * kPitch + cols + g;
+    float d[2][4] = {};
+#pragma unroll
+    for (int k = 0; k < N; k += 8) {
+        uint32_t a[2][4], b[2][2];
+        split_tf32(left[k], a[0][0], a[1][0]);
+        split_tf32(left[k + 8 * kPitch], a[0][1], a[1][1]);
+        split_tf32(left[k + 4], a[0][2], a[1][2]);
+        split_tf32(left[k + 4 + 8 * kPitch], a[0][3], a[1][3]);
+        split_tf32(right[k * kPitch], b[0][0], b[1][0]);
+        split_tf32(right[(k + 4) * kPitch], b[0][1], b[1][1]);
+        mma_tf32(d[1], a[1], b[0]);
+        mma_tf32(d[1], a[0], b[1]);
+        mma_tf32(d[0], a[0], b[0]);
+    }
+    float* to = (pass == 0 ? X + rows * kPitch : T + (at + N + rows) * kPitch + at) + g * kPitch + cols + 2 * t;
+    const float sign = pass == 0 ? 1.f : -1.f;
+    *reinterpret_cast<float2*>(to) = make_float2(sign * (d[0][0] + d[1][0]), sign * (d[0][1] + d[1][1]));
+    *reinterpret_cast<float2*>(to + 8 * kPitch) = make_float2(sign * (d[0][2] + d[1][2]), sign * (d[0][3] + d[1][3]));
+}
+
 template <int DK, int DV, bool kBf16>
 __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __grid_constant__ CUtensorMap map_q,
                                                                        const __grid_constant__ CUtensorMap map_k,
@@ -299,6 +339,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         float* const g_at = scales + 2 * kRows;                             // in log2
         float* const beta_at = g_at + kRows;
         float* const maxima = beta_at + kRows;  // [half] of P's rows
+        float* const scan = maxima + 2 * kRows;
         unsigned long long* const seen_at = reinterpret_cast<unsigned long long*>(smem + C::kSeen);
         unsigned long long* const odd_at = seen_at + kRows;
         float* const A = reinterpret_cast<float*>(smem + C::kA);
@@ -322,6 +363,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             }
             bc_tma(bc, head * DV, 2, DV, values, row, p.rows, kBcDeltaQkv, kBcDeltaQkv);
             tma_load_2d(smem + C::kV + buf * C::kVBytes, &map_v, head * DV, row, landed + buf);
+            if (c + 1 < blocks) {  // the next block's on their way to L2: its copies start late
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    prefetch_2d(&map_k, key_head * DK + 64 * i, row + kRows);
+                    prefetch_2d(&map_q, key_head * DK + 64 * i, row + kRows);
+                }
+                prefetch_2d(&map_v, head * DV, row + kRows);
+            }
         };
         // The block's gates, asked for ahead of their use.
         float g_next = 0.f, beta_next = 0.f;
@@ -353,6 +402,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 seen_at[id] = id < m ? delta_seen(p.tree_mask, p.mask_words, p.rows, row0, id, bc) : 0;
                 const unsigned bits = __ballot_sync(0xffffffffu, odd);
                 if (lane == 0) reinterpret_cast<unsigned*>(odd_at)[id / 32] = bits;
+                float upto = g_at[id];  // of a half's rows, up to and with this one
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float y = __shfl_up_sync(0xffffffffu, upto, o);
+                    upto += lane >= o ? y : 0.f;
+                }
+                scan[id] = upto;
             }
             lost = !kv_wait(landed + buf, (c / 2) & 1, abort_flag, err, kDevErrTimeoutDeltaRows);
             prep_sync();
@@ -420,7 +476,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             const float mine = scales[pair_row], factor = (is_q ? p.scale : beta_at[t]) * mine;
             const bool last = !is_q && t == m - 1;
             float run = 0.f, top = 0.f;  // the logarithm of the decay from behind the column
-            if (half == 1) {
+            if (half == 1 && p.tree_mask == nullptr) {
+                run = t >= 32 ? scan[t] : 0.f;
+            } else if (half == 1) {
                 const uint32_t above = (uint32_t)(from >> 32);
 #pragma unroll 2
                 for (int j = kRows - 4; j >= 32; j -= 4) {
@@ -522,43 +580,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             if (id == 0 && c + 1 < blocks && (c < 1 || mbar_try_wait(smem_u32(unread + (buf ^ 1)), ((c + 1) / 2 - 1) & 1)))
                 stage(c + 1);
             prep_sync();
-            // N x N blocks, R rows of a column a thread: X = A21 T11, then T21 = -T22 X.
-            auto below = [&](auto n_tag, auto r_tag, int at, float* x_at, int col, int rows_at) {
-                constexpr int N = decltype(n_tag)::value, R = decltype(r_tag)::value;
-#pragma unroll 1
-                for (int pass = 0; pass < 2; ++pass) {
-                    const float* left = (pass == 0 ? A + (at + N + rows_at) * kPitch + at : Ts + (at + N + rows_at) * kPitch + at + N);
-                    const float* right = pass == 0 ? Ts + at * kPitch + at + col : x_at + col;
-                    float z[R][4] = {};
-#pragma unroll
-                    for (int j0 = 0; j0 < N; j0 += 16) {
-                        float x[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) x[j] = right[(j0 + j) * kPitch];
-#pragma unroll
-                        for (int i = 0; i < R; ++i) {
-#pragma unroll
-                            for (int j = 0; j < 16; j += 4) {
-                                const float4 w = *reinterpret_cast<const float4*>(left + i * kPitch + j0 + j);
-                                z[i][0] = fmaf(w.x, x[j], z[i][0]);
-                                z[i][1] = fmaf(w.y, x[j + 1], z[i][1]);
-                                z[i][2] = fmaf(w.z, x[j + 2], z[i][2]);
-                                z[i][3] = fmaf(w.w, x[j + 3], z[i][3]);
-                            }
-                        }
-                    }
-                    float* to = pass == 0 ? x_at + rows_at * kPitch + col : Ts + (at + N + rows_at) * kPitch + at + col;
-#pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        const float y = (z[i][0] + z[i][1]) + (z[i][2] + z[i][3]);
-                        to[i * kPitch] = pass == 0 ? y : -y;
-                    }
-                    prep_sync();
-                }
-            };
-            below(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{}, id / 128 * 32, X + id / 128 * 16, id % 16,
-                  id % 128 / 16 * 2);
-            below(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{}, 0, X, lane, (warp - kMainWarps) * 4);
+            // The blocks below, N x N: X = A21 T11, then T21 = -T22 X, a tile of 16 x 8 a warp.
+            const int tile = warp - kMainWarps;
+            if (tile < 4) below_tile<16>(A, Ts, X + tile / 2 * 16, tile / 2 * 32, 0, tile % 2 * 8, lane, 0);
+            prep_sync();
+            if (tile < 4) below_tile<16>(A, Ts, X + tile / 2 * 16, tile / 2 * 32, 0, tile % 2 * 8, lane, 1);
+            prep_sync();
+            below_tile<32>(A, Ts, X, 0, tile / 4 * 16, tile % 4 * 8, lane, 0);
+            prep_sync();
+            below_tile<32>(A, Ts, X, 0, tile / 4 * 16, tile % 4 * 8, lane, 1);
+            prep_sync();
             {
                 // A quarter of a row a thread.
                 const int row = id / 4, quarter = id % 4;
