@@ -8,7 +8,7 @@ using namespace iq4xs;
 namespace {
 
 constexpr int64_t kMaxRows = 32768;
-constexpr int64_t kMaxStride = int64_t(1) << 44;
+constexpr int64_t kMaxStride = int64_t(1) << 37;  // elements (tensor maps hold strides of up to 2^40 bytes)
 constexpr int64_t kMaxExtent = int64_t(1) << 59;  // elements of an axis
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -169,6 +169,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) delta_row_kernel(const DeltaRu
 // it stays where it is.  K and Q of 16 bits are exact in tf32; S and u go in two
 // parts, a value without its last 13 bits and the remainder (22 bits together);
 // sums are joined, and S moved on, by fp32 arithmetic that rounds.
+//
+// CTAs stay for several items (a head's columns of a sequence): S comes to shared
+// memory by TMA, goes to registers, and the next item's is on its way meanwhile.
+// (CTAs of one item each load together and then compute together: 16.3 us where
+// this takes @@ for 12 trees of 8.)
 constexpr int kFewPad = 8;  // floats behind a row in shared memory: rows an operand reads together on all banks
 
 template <int DK, int kWarps, int TB>
@@ -176,7 +181,9 @@ struct FewShape {
     static constexpr int kThreads = 32 * kWarps, VS = 16 * kWarps;
     static constexpr int kPitch = DK + kFewPad, kVPitch = VS + kFewPad;
     // shared memory, in floats
-    static constexpr int kK = 0;                       // [TB][pitch]
+    static constexpr int kBoxes = VS / 32;             // of 32 columns, 128 bytes a key channel, swizzled
+    static constexpr int kS = 0;
+    static constexpr int kK = kS + DK * VS;            // [TB][pitch]
     static constexpr int kQ = kK + TB * kPitch;
     static constexpr int kU = kQ + TB * kPitch;        // [TB] S^T k, then u
     static constexpr int kO = kU + TB * kVPitch;       // [TB] S^T q
@@ -184,8 +191,10 @@ struct FewShape {
     static constexpr int kP = kA + TB * TB;
     static constexpr int kGates = kP + TB * TB;        // [TB] g, beta, G, F of the last row
     static constexpr int kSeen = kGates + 4 * TB;      // [TB]
-    static constexpr int kSmem = (kSeen + TB) * 4;
+    static constexpr int kBar = kSeen + TB;            // the barrier S lands on, and whether a wait ran out
+    static constexpr int kSmem = (kBar + 4) * 4;
     static constexpr int kTiles = TB / 8;
+    static_assert(kBar % 2 == 0, "barrier's alignment");
 };
 
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
@@ -198,144 +207,200 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
 }
 
+struct FewItem {
+    int row0, n, len, slot, head, v0;  // n = 0: nothing to do
+};
+
 template <int DK, int kWarps, int TB>
 __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarps)
-    delta_few_kernel(const DeltaRule p, const DeltaView d, const BatchView b, int* err) {
+    delta_few_kernel(const __grid_constant__ CUtensorMap map_s, const __grid_constant__ DeltaRule p,
+                     const __grid_constant__ DeltaView d, const __grid_constant__ BatchView b, int items, int* err) {
     using C = FewShape<DK, kWarps, TB>;
     constexpr int kSteps = DK / 8, VS = C::VS, kTiles = C::kTiles;
-    extern __shared__ __align__(16) float sm[];
+    extern __shared__ __align__(1024) float sm[];
     uint32_t* const seen = reinterpret_cast<uint32_t*>(sm + C::kSeen);
+    uint64_t* const landed = reinterpret_cast<uint64_t*>(sm + C::kBar);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(landed + 1);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane / 4, t4 = lane % 4;
+    if ((smem_u32(sm) & 1023) != 0) {  // (no static shared memory: the swizzle atoms' alignment)
+        if (tid == 0) atomicCAS(err, 0, kDevErrLayout);
+        return;
+    }
+    if (tid == 0) {
+        mbar_init(landed, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tmap(&map_s);
+    }
+    __syncthreads();
     griddep_launch_dependents();
     griddep_wait();
     const Bc bc = bc_open(err);
     const int slices = d.value_dim / VS;
-    const int slice = blockIdx.x % slices, head = blockIdx.x / slices % d.heads, s = blockIdx.x / slices / d.heads;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane / 4, t4 = lane % 4;
-    int row0;
-    const int n = batch_rows(b, s, p.rows, &row0, err);
-    const int len = batch_len(b, s, err), slot = delta_slot(d, s, err);
-    if (n == 0 || len < 0 || slot < 0) return;
-    if (n > p.max_rows) {
-        if (tid == 0) data_error(err, kDataCount);
-        return;
-    }
-    const int key_head = head / (d.heads / d.key_heads), v0 = slice * VS;
     const int64_t keys = (int64_t)d.key_heads * DK, values = (int64_t)d.heads * d.value_dim;
-    // Element e of step i: key channel 8 i + 2 t4 + (e & 1), column 16 warp + g + 8 (e >> 1).
-    float* const at_s = d.s + p.s_offset + slot * d.s_slot_stride + ((int64_t)head * DK + 2 * t4) * d.value_dim + v0 + 16 * warp + g;
-    float S[kSteps][4];
+    auto look = [&](int item) {
+        FewItem it = {};
+        if (item >= items) return it;
+        const int s = item / slices / d.heads;
+        it.head = item / slices % d.heads;
+        it.v0 = item % slices * VS;
+        const int n = batch_rows(b, s, p.rows, &it.row0, err);
+        it.len = batch_len(b, s, err);
+        it.slot = delta_slot(d, s, err);
+        if (n > p.max_rows && tid == 0) data_error(err, kDataCount);
+        it.n = it.len < 0 || it.slot < 0 || n > p.max_rows ? 0 : n;
+        return it;
+    };
+    auto fetch = [&](const FewItem& it) {  // by one thread
+        if (it.n == 0 || it.len == 0) return;
+        mbar_arrive_expect_tx(landed, DK * VS * 4);
+        bc_tma(bc, it.v0, 4, VS, d.value_dim, it.head * DK, (int64_t)d.heads * DK, kBcDeltaS, kBcDeltaS);
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
+        for (int i = 0; i < C::kBoxes; ++i)
+            tma_load_3d(sm + C::kS + i * DK * 32, &map_s, it.v0 + 32 * i, it.head * DK, it.slot, landed);
+    };
+    FewItem now = look(blockIdx.x);
+    if (tid == 0) fetch(now);
+    uint32_t phase = 0;
+    bool lost = false;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const FewItem next = look(item + gridDim.x);
+        const int n = now.n, row0 = now.row0, len = now.len, slot = now.slot, head = now.head, v0 = now.v0;
+        const int key_head = head / (d.heads / d.key_heads);
+        // Element e of step i: key channel 8 i + 2 t4 + (e & 1), column 16 warp + g + 8 (e >> 1).
+        float S[kSteps][4];
+        if (n > 0 && len > 0) {
+            lost = !kv_wait(landed, phase & 1, abort_flag, err, kDevErrTimeoutDeltaRows);
+            ++phase;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float* from = at_s + (8 * i + (e & 1)) * d.value_dim + 8 * (e >> 1);
-            S[i][e] = len > 0 && bc_global(bc, from, 4, d.s, d.s_extent, kBcDeltaS) ? *from : 0.f;
-        }
-    for (int t0 = 0; t0 < n; t0 += TB) {
-        const int m = min(TB, n - t0), first = row0 + t0;
-        if (t0 > 0) __syncthreads();  // the last block's rows have been used
-        for (int i = tid; i < TB * 2 * (DK / 8); i += C::kThreads) {  // (rows behind the last: zeros)
-            const int c = i % (DK / 8) * 8, which = i / (DK / 8) % 2, t = i / (DK / 8) / 2;
-            const uint16_t* base = which ? p.q : p.k;
-            const int64_t stride = which ? p.q_row_stride : p.k_row_stride;
-            const uint16_t* from = base + (first + t) * stride + key_head * DK + c;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (t < m && bc_global(bc, from, 16, base, 2 * ((p.rows - 1) * stride + keys), kBcDeltaQkv))
-                w = *reinterpret_cast<const uint4*>(from);
-            float x[8];
-            unpack8(p.bf16, w, x);
-            float* const to = sm + (which ? C::kQ : C::kK) + t * C::kPitch + c;
-            *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4*>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
-        }
-        float v[TB];  // of a column, where the thread has one
+            for (int e = 0; e < 4; ++e) {
+                const int r = 2 * t4 + (e & 1), c = 16 * (warp & 1) + g + 8 * (e >> 1);
+                const float* from = sm + C::kS + (warp >> 1) * DK * 32 + r * 32 + ((c >> 2) ^ r) * 4 + (c & 3);
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            const uint16_t* from = p.v + (first + t) * p.v_row_stride + head * d.value_dim + v0 + tid;
-            v[t] = 0.f;
-            if (tid < VS && t < m && bc_global(bc, from, 2, p.v, 2 * ((p.rows - 1) * p.v_row_stride + values), kBcDeltaQkv))
-                v[t] = p.bf16 ? KvBf16::unpack(*from).x : KvF16::unpack(*from).x;
-        }
-        if (tid < TB) {
-            const int64_t at = (int64_t)(first + tid) * d.heads + head, extent = 4 * (int64_t)p.rows * d.heads;
-            float gate = 0.f, beta = 0.f;
-            if (tid < m && bc_global(bc, p.g + at, 4, p.g, extent, kBcDeltaGate)) gate = p.g[at];
-            if (tid < m && bc_global(bc, p.beta + at, 4, p.beta, extent, kBcDeltaGate)) beta = p.beta[at];
-            sm[C::kGates + tid] = gate;
-            sm[C::kGates + TB + tid] = beta;
-            seen[tid] = tid >= m ? 0 : p.tree_mask ? (uint32_t)delta_seen(p.tree_mask, p.mask_words, p.rows, row0, tid, bc)
-                                                   : (1u << tid) - 1;
-        }
-        __syncthreads();
-        // S^T [K; Q]: columns by rows.  The last warps also [K; Q] K^T: rows by rows,
-        // tile y of rows with tile x before or at it.
-        {
-            float sk[kTiles][2][4] = {}, sq[kTiles][2][4] = {}, pairs[2][4] = {};
-            const int pair = kWarps - 1 - warp;  // tiles (0, 0), (1, 0), (1, 1)
-            const int ty = pair > 0 ? 1 : 0, tx = pair > 1 ? 1 : 0;
-            const bool has_pair = pair < (kTiles == 2 ? 3 : 1);
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                uint32_t hi[4], lo[4];
-                split_tf32(S[i][0], hi[0], lo[0]);
-                split_tf32(S[i][2], hi[1], lo[1]);
-                split_tf32(S[i][1], hi[2], lo[2]);
-                split_tf32(S[i][3], hi[3], lo[3]);
-#pragma unroll
-                for (int x = 0; x < kTiles; ++x) {
-                    const uint2 k = *reinterpret_cast<const uint2*>(sm + C::kK + (8 * x + g) * C::kPitch + 8 * i + 2 * t4);
-                    const uint2 q = *reinterpret_cast<const uint2*>(sm + C::kQ + (8 * x + g) * C::kPitch + 8 * i + 2 * t4);
-                    mma_tf32(sk[x][1], lo, k);
-                    mma_tf32(sq[x][1], lo, q);
-                    mma_tf32(sk[x][0], hi, k);
-                    mma_tf32(sq[x][0], hi, q);
-                }
-                if (has_pair) {
-                    const uint2 k = *reinterpret_cast<const uint2*>(sm + C::kK + (8 * ty + g) * C::kPitch + 8 * i + 2 * t4);
-                    const uint2 q = *reinterpret_cast<const uint2*>(sm + C::kQ + (8 * ty + g) * C::kPitch + 8 * i + 2 * t4);
-                    const uint32_t a[4] = {k.x, q.x, k.y, q.y};
-                    mma_tf32(pairs[i & 1], a, *reinterpret_cast<const uint2*>(sm + C::kK + (8 * tx + g) * C::kPitch + 8 * i + 2 * t4));
-                }
+                for (int i = 0; i < kSteps; ++i) S[i][e] = from[i * 8 * 32];
             }
+        } else {
 #pragma unroll
-            for (int x = 0; x < kTiles; ++x)
+            for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int to = (8 * x + 2 * t4 + (e & 1)) * C::kVPitch + 16 * warp + g + 8 * (e >> 1);
-                    sm[C::kU + to] = sk[x][0][e] + sk[x][1][e];
-                    sm[C::kO + to] = sq[x][0][e] + sq[x][1][e];
-                }
-            if (has_pair) {
-                const int t = 8 * ty + g;
-                const uint32_t with = seen[t] | 1u << t;
-                auto decay_over = [&](uint32_t rows) {
-                    float sum = 0.f;
-#pragma unroll
-                    for (int k = TB - 1; k >= 0; --k) sum += rows >> k & 1 ? sm[C::kGates + k] : 0.f;
-                    return expf(sum);
-                };
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int j = 8 * tx + 2 * t4 + e;
-                    const bool from = with >> j & 1;
-                    const float far = decay_over(with & ~((2u << j) - 1));
-                    sm[C::kA + t * TB + j] = from ? sm[C::kGates + TB + t] * far * (pairs[0][e] + pairs[1][e]) : 0.f;
-                    sm[C::kP + t * TB + j] = from ? p.scale * far * (pairs[0][2 + e] + pairs[1][2 + e]) : 0.f;
-                    if (t == m - 1) sm[C::kGates + 3 * TB + j] = from ? far : 0.f;
-                }
-                if (tx == ty && t4 == 0) sm[C::kGates + 2 * TB + t] = decay_over(with);
-                if (kTiles == 2 && m <= 8 && tx == 0 && t4 == 0) sm[C::kGates + 3 * TB + 8 + g] = 0.f;
+                for (int e = 0; e < 4; ++e) S[i][e] = 0.f;
+        }
+        if (__syncthreads_or(lost)) break;  // (all leave together; S has been read, the last item is done)
+        if (tid == 0) fetch(next);
+        if (tid < 3 * TB && next.n > 0) {  // the next item's rows on their way to L2
+            const int t = tid / 3, which = tid % 3, nk = next.head / (d.heads / d.key_heads) * DK;
+            if (t < next.n) {
+                const uint16_t* at = which == 0   ? p.k + (next.row0 + t) * p.k_row_stride + nk
+                                     : which == 1 ? p.q + (next.row0 + t) * p.q_row_stride + nk
+                                                  : p.v + (next.row0 + t) * p.v_row_stride + next.head * d.value_dim + next.v0;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+                if (which < 2 ? DK > 64 : VS > 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 64));
             }
         }
-        __syncthreads();
-        // u, a column a thread.  (A row takes the rows that it comes from, and no
-        // others: 0 times NaN is none of its.)
-        if (tid < VS) {
-            float u[TB];
+        now = next;
+        for (int t0 = 0; t0 < n; t0 += TB) {
+            const int m = min(TB, n - t0), first = row0 + t0;
+            if (t0 > 0) __syncthreads();  // the last block's rows have been used
+            for (int i = tid; i < TB * 2 * (DK / 8); i += C::kThreads) {  // (rows behind the last: zeros)
+                const int c = i % (DK / 8) * 8, which = i / (DK / 8) % 2, t = i / (DK / 8) / 2;
+                const uint16_t* base = which ? p.q : p.k;
+                const int64_t stride = which ? p.q_row_stride : p.k_row_stride;
+                const uint16_t* from = base + (first + t) * stride + key_head * DK + c;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (t < m && bc_global(bc, from, 16, base, 2 * ((p.rows - 1) * stride + keys), kBcDeltaQkv))
+                    w = *reinterpret_cast<const uint4*>(from);
+                float x[8];
+                unpack8(p.bf16, w, x);
+                float* const to = sm + (which ? C::kQ : C::kK) + t * C::kPitch + c;
+                *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4*>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+            }
+            float v[TB];  // of a column, where the thread has one
 #pragma unroll
             for (int t = 0; t < TB; ++t) {
-                u[t] = 0.f;
-                if (t < m) {
+                const uint16_t* from = p.v + (first + t) * p.v_row_stride + head * d.value_dim + v0 + tid;
+                v[t] = 0.f;
+                if (tid < VS && t < m && bc_global(bc, from, 2, p.v, 2 * ((p.rows - 1) * p.v_row_stride + values), kBcDeltaQkv))
+                    v[t] = p.bf16 ? KvBf16::unpack(*from).x : KvF16::unpack(*from).x;
+            }
+            if (tid < TB) {
+                const int64_t at = (int64_t)(first + tid) * d.heads + head, extent = 4 * (int64_t)p.rows * d.heads;
+                float gate = 0.f, beta = 0.f;
+                if (tid < m && bc_global(bc, p.g + at, 4, p.g, extent, kBcDeltaGate)) gate = p.g[at];
+                if (tid < m && bc_global(bc, p.beta + at, 4, p.beta, extent, kBcDeltaGate)) beta = p.beta[at];
+                sm[C::kGates + tid] = gate;
+                sm[C::kGates + TB + tid] = beta;
+                seen[tid] = tid >= m ? 0 : p.tree_mask ? (uint32_t)delta_seen(p.tree_mask, p.mask_words, p.rows, row0, tid, bc)
+                                                       : (1u << tid) - 1;
+            }
+            __syncthreads();
+            // S^T [K; Q]: columns by rows.  The last warps also [K; Q] K^T: rows by rows,
+            // tile y of rows with tile x before or at it.
+            {
+                float sk[kTiles][2][4] = {}, sq[kTiles][2][4] = {}, pairs[2][4] = {};
+                const int pair = kWarps - 1 - warp;  // tiles (0, 0), (1, 0), (1, 1)
+                const int ty = pair > 0 ? 1 : 0, tx = pair > 1 ? 1 : 0;
+                const bool has_pair = pair < (kTiles == 2 ? 3 : 1);
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    uint32_t hi[4], lo[4];
+                    split_tf32(S[i][0], hi[0], lo[0]);
+                    split_tf32(S[i][2], hi[1], lo[1]);
+                    split_tf32(S[i][1], hi[2], lo[2]);
+                    split_tf32(S[i][3], hi[3], lo[3]);
+#pragma unroll
+                    for (int x = 0; x < kTiles; ++x) {
+                        const uint2 k = *reinterpret_cast<const uint2*>(sm + C::kK + (8 * x + g) * C::kPitch + 8 * i + 2 * t4);
+                        const uint2 q = *reinterpret_cast<const uint2*>(sm + C::kQ + (8 * x + g) * C::kPitch + 8 * i + 2 * t4);
+                        mma_tf32(sk[x][1], lo, k);
+                        mma_tf32(sq[x][1], lo, q);
+                        mma_tf32(sk[x][0], hi, k);
+                        mma_tf32(sq[x][0], hi, q);
+                    }
+                    if (has_pair) {
+                        const uint2 k = *reinterpret_cast<const uint2*>(sm + C::kK + (8 * ty + g) * C::kPitch + 8 * i + 2 * t4);
+                        const uint2 q = *reinterpret_cast<const uint2*>(sm + C::kQ + (8 * ty + g) * C::kPitch + 8 * i + 2 * t4);
+                        const uint32_t a[4] = {k.x, q.x, k.y, q.y};
+                        mma_tf32(pairs[i & 1], a, *reinterpret_cast<const uint2*>(sm + C::kK + (8 * tx + g) * C::kPitch + 8 * i + 2 * t4));
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < kTiles; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int to = (8 * x + 2 * t4 + (e & 1)) * C::kVPitch + 16 * warp + g + 8 * (e >> 1);
+                        sm[C::kU + to] = sk[x][0][e] + sk[x][1][e];
+                        sm[C::kO + to] = sq[x][0][e] + sq[x][1][e];
+                    }
+                if (has_pair) {
+                    const int t = 8 * ty + g;
+                    const uint32_t with = seen[t] | 1u << t;
+                    auto decay_over = [&](uint32_t rows) {
+                        float sum = 0.f;
+#pragma unroll
+                        for (int k = TB - 1; k >= 0; --k) sum += rows >> k & 1 ? sm[C::kGates + k] : 0.f;
+                        return expf(sum);
+                    };
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = 8 * tx + 2 * t4 + e;
+                        const bool from = with >> j & 1;
+                        const float far = decay_over(with & ~((2u << j) - 1));
+                        sm[C::kA + t * TB + j] = from ? sm[C::kGates + TB + t] * far * (pairs[0][e] + pairs[1][e]) : 0.f;
+                        sm[C::kP + t * TB + j] = from ? p.scale * far * (pairs[0][2 + e] + pairs[1][2 + e]) : 0.f;
+                        if (t == m - 1) sm[C::kGates + 3 * TB + j] = from ? far : 0.f;
+                    }
+                    if (tx == ty && t4 == 0) sm[C::kGates + 2 * TB + t] = decay_over(with);
+                    if (kTiles == 2 && m <= 8 && tx == 0 && t4 == 0) sm[C::kGates + 3 * TB + 8 + g] = 0.f;
+                }
+            }
+            __syncthreads();
+            // u, a column a thread.  (A row takes the rows that it comes from, and no
+            // others: 0 times NaN is none of its.)
+            if (tid < VS) {
+                float u[TB];
+#pragma unroll
+                for (int t = 0; t < TB; ++t) {
                     float x = sm[C::kGates + TB + t] * (v[t] - sm[C::kGates + 2 * TB + t] * sm[C::kU + t * C::kVPitch + tid]);
                     const uint32_t from = seen[t];
 #pragma unroll
@@ -346,75 +411,82 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
                         if (j + 2 < t && (from >> (j + 2) & 1)) x = fmaf(-a.z, u[j + 2], x);
                         if (j + 3 < t && (from >> (j + 3) & 1)) x = fmaf(-a.w, u[j + 3], x);
                     }
-                    u[t] = x;
-                    if (p.u != nullptr) {
-                        float* to = p.u + ((int64_t)(first + t) * d.heads + head) * d.value_dim + v0 + tid;
-                        if (bc_global(bc, to, 4, p.u, 4 * p.rows * values, kBcDeltaU)) *to = x;
-                    }
+                    u[t] = t < m ? x : 0.f;
                 }
-                sm[C::kU + t * C::kVPitch + tid] = u[t];
-            }
-        }
-        __syncthreads();
-        // out: a column and every second row a thread
-        {
-            const int c = tid % VS;
-            float u[TB];
 #pragma unroll
-            for (int t = 0; t < TB; ++t) u[t] = sm[C::kU + t * C::kVPitch + c];
-#pragma unroll
-            for (int t2 = 0; t2 < TB; t2 += 2) {
-                const int t = t2 + tid / VS;
-                if (t < m) {
-                    float x = p.scale * sm[C::kGates + 2 * TB + t] * sm[C::kO + t * C::kVPitch + c];
-                    const uint32_t from = seen[t] | 1u << t;
-#pragma unroll
-                    for (int j = 0; j < t2 + 2; j += 4) {
-                        const float4 a = *reinterpret_cast<const float4*>(sm + C::kP + t * TB + j);
-                        if (from >> j & 1) x = fmaf(a.x, u[j], x);
-                        if (j + 1 < t2 + 2 && (from >> (j + 1) & 1)) x = fmaf(a.y, u[j + 1], x);
-                        if (j + 2 < t2 + 2 && (from >> (j + 2) & 1)) x = fmaf(a.z, u[j + 2], x);
-                        if (j + 3 < t2 + 2 && (from >> (j + 3) & 1)) x = fmaf(a.w, u[j + 3], x);
-                    }
-                    float* to = p.out + (first + t) * p.out_row_stride + head * d.value_dim + v0 + c;
-                    if (bc_global(bc, to, 4, p.out, 4 * ((p.rows - 1) * p.out_row_stride + values), kBcDeltaOut)) *to = x;
+                for (int t = 0; t < TB; ++t) {
+                    sm[C::kU + t * C::kVPitch + tid] = u[t];
+                    float* to = p.u + ((int64_t)(first + t) * d.heads + head) * d.value_dim + v0 + tid;
+                    if (p.u != nullptr && t < m && bc_global(bc, to, 4, p.u, 4 * p.rows * values, kBcDeltaU)) *to = u[t];
                 }
             }
-        }
-        if (p.u == nullptr) {
-            // S: columns by key channels, the rows between
-            uint32_t hi[kTiles][4], lo[kTiles][4];
+            __syncthreads();
+            // out: a column and every second row a thread
+            {
+                const int c = tid % VS;
+                float u[TB];
 #pragma unroll
-            for (int x = 0; x < kTiles; ++x)
+                for (int t = 0; t < TB; ++t) u[t] = sm[C::kU + t * C::kVPitch + c];
+#pragma unroll
+                for (int t2 = 0; t2 < TB; t2 += 2) {
+                    const int t = t2 + tid / VS;
+                    if (t < m) {
+                        float x = p.scale * sm[C::kGates + 2 * TB + t] * sm[C::kO + t * C::kVPitch + c];
+                        const uint32_t from = seen[t] | 1u << t;
+#pragma unroll
+                        for (int j = 0; j < t2 + 2; j += 4) {
+                            const float4 a = *reinterpret_cast<const float4*>(sm + C::kP + t * TB + j);
+                            if (from >> j & 1) x = fmaf(a.x, u[j], x);
+                            if (j + 1 < t2 + 2 && (from >> (j + 1) & 1)) x = fmaf(a.y, u[j + 1], x);
+                            if (j + 2 < t2 + 2 && (from >> (j + 2) & 1)) x = fmaf(a.z, u[j + 2], x);
+                            if (j + 3 < t2 + 2 && (from >> (j + 3) & 1)) x = fmaf(a.w, u[j + 3], x);
+                        }
+                        float* to = p.out + (first + t) * p.out_row_stride + head * d.value_dim + v0 + c;
+                        if (bc_global(bc, to, 4, p.out, 4 * ((p.rows - 1) * p.out_row_stride + values), kBcDeltaOut)) *to = x;
+                    }
+                }
+            }
+            if (p.u == nullptr) {
+                // S: columns by key channels, the rows between
+                uint32_t hi[kTiles][4], lo[kTiles][4];
+#pragma unroll
+                for (int x = 0; x < kTiles; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = 8 * x + t4 + 4 * (e >> 1);
+                        split_tf32(sm[C::kGates + 3 * TB + t] * sm[C::kU + t * C::kVPitch + 16 * warp + g + 8 * (e & 1)], hi[x][e], lo[x][e]);
+                    }
+                const float decay = sm[C::kGates + 2 * TB + m - 1];
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    float add[4] = {};
+#pragma unroll
+                    for (int x = 0; x < kTiles; ++x) {
+                        const float* k = sm + C::kK + (8 * x + t4) * C::kPitch + 8 * i + g;
+                        const uint2 k2 = make_uint2(__float_as_uint(k[0]), __float_as_uint(k[4 * C::kPitch]));
+                        mma_tf32(add, lo[x], k2);
+                        mma_tf32(add, hi[x], k2);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[i][e] = fmaf(decay, S[i][e], add[e]);
+                }
+            }
+        }
+        if (n > 0 && p.u == nullptr) {
+            float* const at_s = d.s + p.s_offset + slot * d.s_slot_stride + ((int64_t)head * DK + 2 * t4) * d.value_dim + v0 + 16 * warp + g;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int t = 8 * x + t4 + 4 * (e >> 1);
-                    split_tf32(sm[C::kGates + 3 * TB + t] * sm[C::kU + t * C::kVPitch + 16 * warp + g + 8 * (e & 1)], hi[x][e], lo[x][e]);
+                    float* to = at_s + (8 * i + (e & 1)) * d.value_dim + 8 * (e >> 1);
+                    if (bc_global(bc, to, 4, d.s, d.s_extent, kBcDeltaS)) *to = S[i][e];
                 }
-            const float decay = sm[C::kGates + 2 * TB + m - 1];
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                float add[4] = {};
-#pragma unroll
-                for (int x = 0; x < kTiles; ++x) {
-                    const float* k = sm + C::kK + (8 * x + t4) * C::kPitch + 8 * i + g;
-                    const uint2 k2 = make_uint2(__float_as_uint(k[0]), __float_as_uint(k[4 * C::kPitch]));
-                    mma_tf32(add, lo[x], k2);
-                    mma_tf32(add, hi[x], k2);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[i][e] = fmaf(decay, S[i][e], add[e]);
-            }
         }
     }
-    if (p.u == nullptr) {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float* to = at_s + (8 * i + (e & 1)) * d.value_dim + 8 * (e >> 1);
-                if (bc_global(bc, to, 4, d.s, d.s_extent, kBcDeltaS)) *to = S[i][e];
-            }
+    // No copy may be in flight when the CTA ends; all were waited for, unless a wait ran out.
+    if (lost && tid == 0) {
+        int no_abort = 0;
+        kv_wait(landed, (phase - 1) & 1, &no_abort, err, kDevErrTimeoutDeltaRows);
     }
 }
 
@@ -423,27 +495,47 @@ cudaError_t launch_row(const DeltaRule& p, const DeltaView& d, const BatchView& 
     const dim3 grid((unsigned)((int64_t)b.sequences * d.heads * (d.value_dim / VS)));
     return launch_chained(delta_row_kernel<DK, VS>, grid, dim3(kRowThreads), 0, stream, 1, p, d, b, err);
 }
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
 template <int DK, int kWarps, int TB>
-cudaError_t launch_few(const DeltaRule& p, const DeltaView& d, const BatchView& b, int* err, cudaStream_t stream) {
+cudaError_t launch_few(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err, int num_sms,
+                       cudaStream_t stream) {
     using C = FewShape<DK, kWarps, TB>;
+    // One map over the layer's states: columns, key channels of all heads, slots.
+    CUtensorMap map;
+    const int64_t size = (int64_t)d.heads * DK * d.value_dim;
+    const cuuint64_t gdim[3] = {(cuuint64_t)d.value_dim, (cuuint64_t)d.heads * DK, (cuuint64_t)d.slots};
+    const cuuint64_t gstride[2] = {(cuuint64_t)d.value_dim * 4, (cuuint64_t)(d.slots > 1 ? d.s_slot_stride : size) * 4};
+    const cuuint32_t box[3] = {32, DK, 1}, estride[3] = {1, 1, 1};
+    if (reinterpret_cast<EncodeTiledFn>(encode)(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, d.s + p.s_offset, gdim, gstride, box,
+                                                estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
     const cudaError_t e = allow_smem<delta_few_kernel<DK, kWarps, TB>>(C::kSmem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((int64_t)b.sequences * d.heads * (d.value_dim / C::VS)));
-    return launch_chained(delta_few_kernel<DK, kWarps, TB>, grid, dim3(C::kThreads), C::kSmem, stream, 1, p, d, b, err);
+    const int64_t items = (int64_t)b.sequences * d.heads * (d.value_dim / C::VS), most = (int64_t)num_sms * (16 / kWarps);
+    return launch_chained(delta_few_kernel<DK, kWarps, TB>, dim3((unsigned)(items < most ? items : most)), dim3(C::kThreads),
+                          C::kSmem, stream, 1, map, p, d, b, (int)items, err);
 }
 
 // Single rows where a sequence has one on average; else blocks of eight, or of
 // 16.  Slices of 32 columns while that many CTAs find an SM of their own.
 template <int DK>
-cudaError_t launch_keys(const DeltaRule& p, const DeltaView& d, const BatchView& b, int* err, int num_sms,
+cudaError_t launch_keys(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err, int num_sms,
                         cudaStream_t stream) {
     const int64_t items = (int64_t)b.sequences * d.heads;
     const bool few = items * (d.value_dim / 32) <= 2 * num_sms;
     if (p.max_rows == 1 || (p.u == nullptr && p.rows <= b.sequences))
         return few ? launch_row<DK, 32>(p, d, b, err, stream) : launch_row<DK, 64>(p, d, b, err, stream);
     if (p.max_rows <= 8 || (p.u == nullptr && p.rows <= 8 * (int64_t)b.sequences))
-        return few ? launch_few<DK, 2, 8>(p, d, b, err, stream) : launch_few<DK, 4, 8>(p, d, b, err, stream);
-    return launch_few<DK, 4, 16>(p, d, b, err, stream);
+        return few                  ? launch_few<DK, 2, 8>(p, d, b, encode, err, num_sms, stream)
+               : d.value_dim == 128 ? launch_few<DK, 8, 8>(p, d, b, encode, err, num_sms, stream)
+                                    : launch_few<DK, 4, 8>(p, d, b, encode, err, num_sms, stream);
+    return d.value_dim == 128 ? launch_few<DK, 8, 16>(p, d, b, encode, err, num_sms, stream)
+                              : launch_few<DK, 4, 16>(p, d, b, encode, err, num_sms, stream);
 }
 
 }  // namespace
@@ -453,8 +545,8 @@ cudaError_t launch_delta_rule(const DeltaRule& p, const DeltaView& d, const Batc
     // A tree is one block; chains of more than 12 rows on average go in blocks of 64.
     if (p.u != nullptr ? p.max_rows > 16 : p.rows > 12 * (int64_t)b.sequences && p.max_rows > 16)
         return launch_delta_chunk(p, d, b, encode, err, stream);
-    return d.key_dim == 64 ? launch_keys<64>(p, d, b, err, num_sms, stream)
-                           : launch_keys<128>(p, d, b, err, num_sms, stream);
+    return d.key_dim == 64 ? launch_keys<64>(p, d, b, encode, err, num_sms, stream)
+                           : launch_keys<128>(p, d, b, encode, err, num_sms, stream);
 }
 
 }  // namespace iq4xs
