@@ -207,6 +207,12 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
 }
 
+// x + a u where `with` holds (a selection, not a branch).
+__device__ __forceinline__ float take(bool with, float a, float u, float x) {
+    const float y = fmaf(a, u, x);
+    return with ? y : x;
+}
+
 struct FewItem {
     int row0, n, len, slot, head, v0;  // n = 0: nothing to do
 };
@@ -267,6 +273,37 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
         const FewItem next = look(item + gridDim.x);
         const int n = now.n, row0 = now.row0, len = now.len, slot = now.slot, head = now.head, v0 = now.v0;
         const int key_head = head / (d.heads / d.key_heads);
+        // A block's rows: asked for before the next item's state, behind which they would wait.
+        constexpr int kAll = TB * 2 * (DK / 8), kUnits = (kAll + C::kThreads - 1) / C::kThreads;
+        uint4 kq[kUnits];
+        uint16_t v[TB];  // of a column, where the thread has one
+        float gate = 0.f, beta = 0.f;
+        auto ask = [&](int t0) {
+            const int m = min(TB, n - t0), first = row0 + t0;
+#pragma unroll
+            for (int x = 0; x < kUnits; ++x) {  // (rows behind the last: zeros)
+                const int i = tid + x * C::kThreads, c = i % (DK / 8) * 8, which = i / (DK / 8) % 2, t = i / (DK / 8) / 2;
+                const uint16_t* base = which ? p.q : p.k;
+                const int64_t stride = which ? p.q_row_stride : p.k_row_stride;
+                const uint16_t* from = base + (first + t) * stride + key_head * DK + c;
+                kq[x] = make_uint4(0, 0, 0, 0);
+                if (t < m && bc_global(bc, from, 16, base, 2 * ((p.rows - 1) * stride + keys), kBcDeltaQkv))
+                    kq[x] = *reinterpret_cast<const uint4*>(from);
+            }
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                const uint16_t* from = p.v + (first + t) * p.v_row_stride + head * d.value_dim + v0 + tid;
+                v[t] = 0;
+                if (tid < VS && t < m && bc_global(bc, from, 2, p.v, 2 * ((p.rows - 1) * p.v_row_stride + values), kBcDeltaQkv))
+                    v[t] = *from;
+            }
+            if (tid < m) {
+                const int64_t at = (int64_t)(first + tid) * d.heads + head, extent = 4 * (int64_t)p.rows * d.heads;
+                if (bc_global(bc, p.g + at, 4, p.g, extent, kBcDeltaGate)) gate = p.g[at];
+                if (bc_global(bc, p.beta + at, 4, p.beta, extent, kBcDeltaGate)) beta = p.beta[at];
+            }
+        };
+        ask(0);
         // Element e of step i: key channel 8 i + 2 t4 + (e & 1), column 16 warp + g + 8 (e >> 1).
         float S[kSteps][4];
         if (n > 0 && len > 0) {
@@ -300,34 +337,22 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
         now = next;
         for (int t0 = 0; t0 < n; t0 += TB) {
             const int m = min(TB, n - t0), first = row0 + t0;
-            if (t0 > 0) __syncthreads();  // the last block's rows have been used
-            for (int i = tid; i < TB * 2 * (DK / 8); i += C::kThreads) {  // (rows behind the last: zeros)
-                const int c = i % (DK / 8) * 8, which = i / (DK / 8) % 2, t = i / (DK / 8) / 2;
-                const uint16_t* base = which ? p.q : p.k;
-                const int64_t stride = which ? p.q_row_stride : p.k_row_stride;
-                const uint16_t* from = base + (first + t) * stride + key_head * DK + c;
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (t < m && bc_global(bc, from, 16, base, 2 * ((p.rows - 1) * stride + keys), kBcDeltaQkv))
-                    w = *reinterpret_cast<const uint4*>(from);
-                float x[8];
-                unpack8(p.bf16, w, x);
-                float* const to = sm + (which ? C::kQ : C::kK) + t * C::kPitch + c;
-                *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<float4*>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+            if (t0 > 0) {
+                gate = beta = 0.f;
+                ask(t0);
+                __syncthreads();  // the last block's rows have been used
             }
-            float v[TB];  // of a column, where the thread has one
 #pragma unroll
-            for (int t = 0; t < TB; ++t) {
-                const uint16_t* from = p.v + (first + t) * p.v_row_stride + head * d.value_dim + v0 + tid;
-                v[t] = 0.f;
-                if (tid < VS && t < m && bc_global(bc, from, 2, p.v, 2 * ((p.rows - 1) * p.v_row_stride + values), kBcDeltaQkv))
-                    v[t] = p.bf16 ? KvBf16::unpack(*from).x : KvF16::unpack(*from).x;
+            for (int x = 0; x < kUnits; ++x) {
+                const int i = tid + x * C::kThreads, c = i % (DK / 8) * 8, which = i / (DK / 8) % 2, t = i / (DK / 8) / 2;
+                if (i >= kAll) break;
+                float y[8];
+                unpack8(p.bf16, kq[x], y);
+                float* const to = sm + (which ? C::kQ : C::kK) + t * C::kPitch + c;
+                *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<float4*>(to + 4) = make_float4(y[4], y[5], y[6], y[7]);
             }
             if (tid < TB) {
-                const int64_t at = (int64_t)(first + tid) * d.heads + head, extent = 4 * (int64_t)p.rows * d.heads;
-                float gate = 0.f, beta = 0.f;
-                if (tid < m && bc_global(bc, p.g + at, 4, p.g, extent, kBcDeltaGate)) gate = p.g[at];
-                if (tid < m && bc_global(bc, p.beta + at, 4, p.beta, extent, kBcDeltaGate)) beta = p.beta[at];
                 sm[C::kGates + tid] = gate;
                 sm[C::kGates + TB + tid] = beta;
                 seen[tid] = tid >= m ? 0 : p.tree_mask ? (uint32_t)delta_seen(p.tree_mask, p.mask_words, p.rows, row0, tid, bc)
@@ -401,15 +426,16 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
                 float u[TB];
 #pragma unroll
                 for (int t = 0; t < TB; ++t) {
-                    float x = sm[C::kGates + TB + t] * (v[t] - sm[C::kGates + 2 * TB + t] * sm[C::kU + t * C::kVPitch + tid]);
+                    float x = sm[C::kGates + TB + t] * ((p.bf16 ? KvBf16::unpack(v[t]).x : KvF16::unpack(v[t]).x) -
+                                                              sm[C::kGates + 2 * TB + t] * sm[C::kU + t * C::kVPitch + tid]);
                     const uint32_t from = seen[t];
 #pragma unroll
                     for (int j = 0; j < t; j += 4) {
                         const float4 a = *reinterpret_cast<const float4*>(sm + C::kA + t * TB + j);
-                        if (from >> j & 1) x = fmaf(-a.x, u[j], x);
-                        if (j + 1 < t && (from >> (j + 1) & 1)) x = fmaf(-a.y, u[j + 1], x);
-                        if (j + 2 < t && (from >> (j + 2) & 1)) x = fmaf(-a.z, u[j + 2], x);
-                        if (j + 3 < t && (from >> (j + 3) & 1)) x = fmaf(-a.w, u[j + 3], x);
+                        x = take(from >> j & 1, -a.x, u[j], x);
+                        if (j + 1 < t) x = take(from >> (j + 1) & 1, -a.y, u[j + 1], x);
+                        if (j + 2 < t) x = take(from >> (j + 2) & 1, -a.z, u[j + 2], x);
+                        if (j + 3 < t) x = take(from >> (j + 3) & 1, -a.w, u[j + 3], x);
                     }
                     u[t] = t < m ? x : 0.f;
                 }
@@ -436,10 +462,10 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
 #pragma unroll
                         for (int j = 0; j < t2 + 2; j += 4) {
                             const float4 a = *reinterpret_cast<const float4*>(sm + C::kP + t * TB + j);
-                            if (from >> j & 1) x = fmaf(a.x, u[j], x);
-                            if (j + 1 < t2 + 2 && (from >> (j + 1) & 1)) x = fmaf(a.y, u[j + 1], x);
-                            if (j + 2 < t2 + 2 && (from >> (j + 2) & 1)) x = fmaf(a.z, u[j + 2], x);
-                            if (j + 3 < t2 + 2 && (from >> (j + 3) & 1)) x = fmaf(a.w, u[j + 3], x);
+                            x = take(from >> j & 1, a.x, u[j], x);
+                            if (j + 1 < t2 + 2) x = take(from >> (j + 1) & 1, a.y, u[j + 1], x);
+                            if (j + 2 < t2 + 2) x = take(from >> (j + 2) & 1, a.z, u[j + 2], x);
+                            if (j + 3 < t2 + 2) x = take(from >> (j + 3) & 1, a.w, u[j + 3], x);
                         }
                         float* to = p.out + (first + t) * p.out_row_stride + head * d.value_dim + v0 + c;
                         if (bc_global(bc, to, 4, p.out, 4 * ((p.rows - 1) * p.out_row_stride + values), kBcDeltaOut)) *to = x;
