@@ -647,11 +647,14 @@ def _wrong_device(fn: str):
     raise ValueError(f"{fn}: tensors must be on the current CUDA device")
 
 
-def _device() -> int:
-    """The current device, the one that a call runs on (-2 without one)."""
-    if not torch.cuda.is_initialized():
-        return torch.cuda.current_device() if torch.cuda.is_available() else -2
-    return torch.cuda.current_device() if _raw_device is None else _raw_device()
+def _device(t) -> int:
+    """t's device, if that is the current one, on which a call runs; else -2."""
+    dev = t.get_device()
+    return dev if dev >= 0 and dev == (torch.cuda.current_device() if _raw_device is None else _raw_device()) else -2
+
+
+def _stream_on(stream, dev: int) -> int:
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 class DeltaState:
@@ -762,11 +765,11 @@ def iq4xs_delta_inputs(x, conv_weight, a, b, a_log, dt_bias, eps: float, q, k, v
     if not (a_log.shape == heads and dt_bias.shape == heads and a_log.is_contiguous() and dt_bias.is_contiguous()):
         raise ValueError(f"{fn}: a_log and dt_bias are contiguous [Hv]")
     mask, words = 0, 0
-    dev = _device()
+    dev = _device(x)
     if tree_mask is not None:
         words = _mask_words(fn, tree_mask, M)
         mask = tree_mask.data_ptr()
-    if (not (dev == st.device == x.get_device() == conv_weight.get_device() == a.get_device() == b.get_device() ==
+    if (not (dev == st.device == conv_weight.get_device() == a.get_device() == b.get_device() ==
             a_log.get_device() == dt_bias.get_device() == q.get_device() == k.get_device() == v.get_device() ==
             g.get_device() == beta.get_device()) or
             (tree_mask is not None and tree_mask.get_device() != dev)):
@@ -776,7 +779,7 @@ def iq4xs_delta_inputs(x, conv_weight, a, b, a_log, dt_bias, eps: float, q, k, v
     args = _DELTA_INPUTS(x.data_ptr(), xr, conv_weight.data_ptr(), a.data_ptr(), b.data_ptr(), ar, br, a_log.data_ptr(),
                          dt_bias.data_ptr(), eps, q.data_ptr(), k.data_ptr(), v.data_ptr(), qr, kr, vr, dt, g.data_ptr(),
                          beta.data_ptr(), mask, words, 1 if advance else 0, M, layer)
-    rc = (_lib or load()).iq4xs_delta_inputs(args, st.desc, batch.desc, _stream(stream))
+    rc = (_lib or load()).iq4xs_delta_inputs(args, st.desc, batch.desc, _stream_on(stream, dev))
     if rc:
         _check(fn, rc)
 
@@ -797,7 +800,7 @@ def iq4xs_delta_rule(q, k, v, g, beta, scale: float, out, state: DeltaState, lay
     outr, outc = out.stride()
     if not (out.dtype is torch.float32 and out.shape == (M, n) and outc == 1):
         raise ValueError(f"{fn}: out is float32 [M, Hv * Dv], columns contiguous")
-    dev = _device()
+    dev = _device(q)
     at_u = mask = words = 0
     if u is not None:
         if not (u.dtype is torch.float32 and u.shape == (M, st.heads, st.value_dim) and u.is_contiguous()):
@@ -806,14 +809,14 @@ def iq4xs_delta_rule(q, k, v, g, beta, scale: float, out, state: DeltaState, lay
     if tree_mask is not None:
         words = _mask_words(fn, tree_mask, M)
         mask = tree_mask.data_ptr()
-    if (not (dev == st.device == q.get_device() == k.get_device() == v.get_device() == g.get_device() == beta.get_device() ==
+    if (not (dev == st.device == k.get_device() == v.get_device() == g.get_device() == beta.get_device() ==
             out.get_device()) or
             (u is not None and u.get_device() != dev) or
             (tree_mask is not None and tree_mask.get_device() != dev)):
         _wrong_device(fn)
     args = _DELTA_RULE(q.data_ptr(), k.data_ptr(), v.data_ptr(), qr, kr, vr, dt, g.data_ptr(), beta.data_ptr(), scale,
                        out.data_ptr(), outr if M > 1 else n, at_u, mask, words, max_rows or 0, M, layer)
-    rc = (_lib or load()).iq4xs_delta_rule(args, st.desc, batch.desc, _stream(stream))
+    rc = (_lib or load()).iq4xs_delta_rule(args, st.desc, batch.desc, _stream_on(stream, dev))
     if rc:
         _check(fn, rc)
 
@@ -840,7 +843,7 @@ def iq4xs_delta_commit(k, g, u, x, state: DeltaState, batch: KVBatch, paths, acc
     if not (u.dtype is f32 and u.shape == (st.layers, M, hv, dv) and uc == 1 and (hv == 1 or uh == dv) and
             (M == 1 or ur == hv * dv)):
         raise ValueError(f"{fn}: u is float32 [layers, M, Hv, Dv], a layer contiguous")
-    dev = _device()
+    dev = _device(k)
     at_x = xr = xl = 0
     if x is None:
         if st.conv is not None:
@@ -857,7 +860,7 @@ def iq4xs_delta_commit(k, g, u, x, state: DeltaState, batch: KVBatch, paths, acc
     if not (len(p_shape) == 2 and p_shape[0] == B and accepted.numel() == B and paths.is_contiguous() and
             accepted.is_contiguous()):
         raise ValueError(f"{fn}: paths [B, width], accepted [B], contiguous")
-    if (not (dev == st.device == k.get_device() == g.get_device() == u.get_device() == paths.get_device() ==
+    if (not (dev == st.device == g.get_device() == u.get_device() == paths.get_device() ==
             accepted.get_device()) or
             (x is not None and x.get_device() != dev)):
         _wrong_device(fn)
@@ -865,7 +868,7 @@ def iq4xs_delta_commit(k, g, u, x, state: DeltaState, batch: KVBatch, paths, acc
         kr, xr = hk * dk, st.channels if at_x else 0
     args = _DELTA_COMMIT(k.data_ptr(), kr, kl, dt, g.data_ptr(), gl, u.data_ptr(), ul, at_x, xr, xl, paths.data_ptr(),
                          p_shape[1], accepted.data_ptr(), M)
-    rc = (_lib or load()).iq4xs_delta_commit(args, st.desc, batch.desc, _stream(stream))
+    rc = (_lib or load()).iq4xs_delta_commit(args, st.desc, batch.desc, _stream_on(stream, dev))
     if rc:
         _check(fn, rc)
 
@@ -879,17 +882,17 @@ def iq4xs_token_probs(logits, probs, temperature=None, stream=None) -> None:
     (lr, lc), (pr, pc) = logits.stride(), probs.stride()
     if not (logits.dtype is f32 and probs.dtype is f32 and probs.shape == shape and (V == 1 or (lc == 1 and pc == 1))):
         raise ValueError(f"{fn}: logits and probs are float32 [M, V], columns contiguous")
-    dev, at_t = _device(), 0
+    dev, at_t = _device(logits), 0
     if temperature is not None:
         if not (temperature.dtype is f32 and temperature.shape == (M,) and temperature.is_contiguous()):
             raise ValueError(f"{fn}: temperature is contiguous float32 [M]")
         at_t = temperature.data_ptr()
-    if (not (dev == logits.get_device() == probs.get_device()) or
+    if (not (dev  == probs.get_device()) or
             (temperature is not None and temperature.get_device() != dev)):
         _wrong_device(fn)
     if M == 1:
         lr = pr = V
-    rc = (_lib or load()).iq4xs_token_probs(logits.data_ptr(), lr, M, V, at_t, probs.data_ptr(), pr, _stream(stream))
+    rc = (_lib or load()).iq4xs_token_probs(logits.data_ptr(), lr, M, V, at_t, probs.data_ptr(), pr, _stream_on(stream, dev))
     if rc:
         _check(fn, rc)
 
@@ -908,7 +911,7 @@ def iq4xs_verify_drafts(probs, tokens, accept_u, draw_u, paths, accepted, next_t
     pr, pc = probs.stride()
     if not (probs.dtype is f32 and (V == 1 or pc == 1)):
         raise ValueError(f"{fn}: probs is float32 [M, V], columns contiguous")
-    dev, at_d, dr = _device(), 0, 0
+    dev, at_d, dr = _device(probs), 0, 0
     if draft_probs is not None:
         dr, dc = draft_probs.stride()
         if not (draft_probs.dtype is f32 and draft_probs.shape == shape and (V == 1 or dc == 1)):
@@ -928,7 +931,7 @@ def iq4xs_verify_drafts(probs, tokens, accept_u, draw_u, paths, accepted, next_t
     if tree_mask is not None:
         words = _mask_words(fn, tree_mask, M)
         mask = tree_mask.data_ptr()
-    if (not (dev == probs.get_device() == tokens.get_device() == accept_u.get_device() == draw_u.get_device() ==
+    if (not (dev  == tokens.get_device() == accept_u.get_device() == draw_u.get_device() ==
             paths.get_device() == accepted.get_device() == next_token.get_device()) or
             (draft_probs is not None and draft_probs.get_device() != dev) or
             (tree_mask is not None and tree_mask.get_device() != dev)):
@@ -937,7 +940,7 @@ def iq4xs_verify_drafts(probs, tokens, accept_u, draw_u, paths, accepted, next_t
         pr, dr = V, V if at_d else 0
     args = _VERIFY(probs.data_ptr(), pr, at_d, dr, tokens.data_ptr(), mask, words, accept_u.data_ptr(), draw_u.data_ptr(),
                    M, V, paths.data_ptr(), p_shape[1], accepted.data_ptr(), next_token.data_ptr())
-    rc = (_lib or load()).iq4xs_verify_drafts(args, batch.desc, _stream(stream))
+    rc = (_lib or load()).iq4xs_verify_drafts(args, batch.desc, _stream_on(stream, dev))
     if rc:
         _check(fn, rc)
 

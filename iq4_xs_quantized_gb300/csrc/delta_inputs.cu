@@ -9,6 +9,7 @@
 // sequence alone reads the state's inputs, and writes them anew: its rows are
 // at least the three that need them.  A drafted tree's rows read their
 // ancestors' inputs instead, out of L1 or L2.
+#include "attention.cuh"
 #include "delta.cuh"
 
 namespace iq4xs {
@@ -17,6 +18,7 @@ namespace {
 constexpr int kInputThreads = 128;
 constexpr int kInputCols = 4 * kInputThreads;  // channels of a CTA
 constexpr int kAbreast = 4;                    // rows whose loads are in flight together
+constexpr int kShortRun = 16, kLongRun = 32;   // rows of one CTA
 
 struct InputParams {
     const float* x;
@@ -35,13 +37,24 @@ struct InputParams {
     int mask_words, advance, rows, run, col_parts, key_lanes;
 };
 
-__device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
-__device__ __forceinline__ void tap(float4& y, const float4 (&w)[4], int j, const float4& x) {
-    const float* w0 = reinterpret_cast<const float*>(w);  // [channel][tap]
-    y.x = fmaf(w0[j], x.x, y.x);
-    y.y = fmaf(w0[4 + j], x.y, y.y);
-    y.z = fmaf(w0[8 + j], x.z, y.z);
-    y.w = fmaf(w0[12 + j], x.w, y.w);
+// Four channels, as two pairs for packed arithmetic.
+struct Four {
+    float2 a, b;
+};
+__device__ __forceinline__ Four as_four(const float4& x) { return {make_float2(x.x, x.y), make_float2(x.z, x.w)}; }
+__device__ __forceinline__ void tap(Four& y, const Four& w, const Four& x) {
+    y.a = fma2(w.a, x.a, y.a);
+    y.b = fma2(w.b, x.b, y.b);
+}
+// y / (1 + e^-y): approximations of 2 units in the last place of fp32, behind
+// which a rounding to 16 bits comes.
+__device__ __forceinline__ float2 silu(float2 y) {
+    const float2 z = fma2(y, make_float2(-1.44269504088896340736f, -1.44269504088896340736f), make_float2(-0.f, -0.f));
+    const float2 e = add2(make_float2(fast_exp2(z.x), fast_exp2(z.y)), make_float2(1.f, 1.f));
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+    return fma2(y, r, make_float2(-0.f, -0.f));
 }
 
 template <class T>
@@ -86,82 +99,103 @@ __global__ void __launch_bounds__(kInputThreads) delta_inputs_kernel(const Input
     const int c = part * kInputCols + 4 * threadIdx.x;
     const bool here = c < d.channels;  // (lanes behind the last channel take part in the shuffles)
     const int64_t x_extent = 4 * ((p.rows - 1) * p.x_stride + d.channels);
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const Four zero = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     auto input = [&](int row) {
         const float* from = p.x + row * p.x_stride + c;
-        return here && bc_global(bc, from, 16, p.x, x_extent, kBcDeltaX) ? *reinterpret_cast<const float4*>(from) : zero;
+        return here && bc_global(bc, from, 16, p.x, x_extent, kBcDeltaX) ? as_four(*reinterpret_cast<const float4*>(from)) : zero;
     };
     float* const at_conv = d.conv + p.conv_offset + slot * d.conv_slot_stride;
     auto before = [&](int i) {  // input i of the state's, oldest first
         const float* from = at_conv + (int64_t)i * d.channels + c;
         return here && len > 0 && bc_global(bc, from, 16, d.conv, d.conv_extent, kBcDeltaConv)
-                   ? *reinterpret_cast<const float4*>(from) : zero;
+                   ? as_four(*reinterpret_cast<const float4*>(from)) : zero;
     };
-    float4 w[4];
+    Four w[4];  // of a tap
+    {
+        float4 of[4];  // of a channel
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float* from = p.weight + 4 * (int64_t)(c + i);
-        w[i] = here && bc_global(bc, from, 16, p.weight, 16 * (int64_t)d.channels, kBcDeltaW)
-                   ? *reinterpret_cast<const float4*>(from) : zero;
+        for (int i = 0; i < 4; ++i) {
+            const float* from = p.weight + 4 * (int64_t)(c + i);
+            of[i] = here && bc_global(bc, from, 16, p.weight, 16 * (int64_t)d.channels, kBcDeltaW)
+                        ? *reinterpret_cast<const float4*>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        w[0] = {make_float2(of[0].x, of[1].x), make_float2(of[2].x, of[3].x)};
+        w[1] = {make_float2(of[0].y, of[1].y), make_float2(of[2].y, of[3].y)};
+        w[2] = {make_float2(of[0].z, of[1].z), make_float2(of[2].z, of[3].z)};
+        w[3] = {make_float2(of[0].w, of[1].w), make_float2(of[2].w, of[3].w)};
     }
     const int keys = d.key_heads * d.key_dim, kind = c < keys ? 0 : c < 2 * keys ? 1 : 2;
     const bool unit_norm = part * kInputCols + 4 * (threadIdx.x & ~31) < 2 * keys;
     uint16_t* const base = p.out[kind];
     const int64_t out_stride = p.out_stride[kind];
     const int64_t out_extent = 2 * ((p.rows - 1) * out_stride + (kind < 2 ? keys : d.heads * d.value_dim));
+    uint16_t* to = base + (first + t0) * out_stride + c - kind * keys;  // of the next row finished
     // Four rows side by side: SiLU, unit norm, rounding (rows t .. t1 - 1).
-    auto finish = [&](int t, float4 (&y)[kAbreast]) {
-        float sum[kAbreast];
+    auto finish = [&](int t, Four (&y)[kAbreast]) {
 #pragma unroll
-        for (int i = 0; i < kAbreast; ++i) {
-            y[i] = make_float4(silu(y[i].x), silu(y[i].y), silu(y[i].z), silu(y[i].w));
-            sum[i] = fmaf(y[i].x, y[i].x, fmaf(y[i].y, y[i].y, fmaf(y[i].z, y[i].z, y[i].w * y[i].w)));
-        }
-        if (unit_norm)  // (some lane of the warp has a query's or key's channels)
+        for (int i = 0; i < kAbreast; ++i) y[i] = {silu(y[i].a), silu(y[i].b)};
+        if (unit_norm) {  // (some lane of the warp has a query's or key's channels)
+            float sum[kAbreast];
+#pragma unroll
+            for (int i = 0; i < kAbreast; ++i)
+                sum[i] = fmaf(y[i].a.x, y[i].a.x, fmaf(y[i].a.y, y[i].a.y, fmaf(y[i].b.x, y[i].b.x, y[i].b.y * y[i].b.y)));
             for (int o = p.key_lanes / 2; o > 0; o >>= 1)
 #pragma unroll
                 for (int i = 0; i < kAbreast; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-        uint16_t* to = base + (first + t) * out_stride + c - kind * keys;
 #pragma unroll
-        for (int i = 0; i < kAbreast; ++i, to += out_stride) {
-            const float r = kind < 2 ? rsqrtf(sum[i] + p.eps) : 1.f;
-            if (here && t + i < t1 && bc_global(bc, to, 8, base, out_extent, kBcDeltaQkv))
-                *reinterpret_cast<uint2*>(to) =
-                    make_uint2(T::pack(r * y[i].x, r * y[i].y), T::pack(r * y[i].z, r * y[i].w));
+            for (int i = 0; i < kAbreast; ++i) {
+                const float r = kind < 2 ? rsqrtf(sum[i] + p.eps) : 1.f;
+                const float2 r2 = make_float2(r, r);
+                y[i] = {fma2(y[i].a, r2, make_float2(-0.f, -0.f)), fma2(y[i].b, r2, make_float2(-0.f, -0.f))};
+            }
         }
+#pragma unroll
+        for (int i = 0; i < kAbreast; ++i, to += out_stride)
+            if (here && t + i < t1 && bc_global(bc, to, 8, base, out_extent, kBcDeltaQkv))
+                *reinterpret_cast<uint2*>(to) = make_uint2(T::pack(y[i].a.x, y[i].a.y), T::pack(y[i].b.x, y[i].b.y));
     };
     auto past = [&](int t) { return t >= 0 ? input(first + t) : before(kConvTaps - 1 + t); };
     if (p.tree_mask == nullptr) {
-        float4 x0 = past(t0 - 3), x1 = past(t0 - 2), x2 = past(t0 - 1);
-        float4 new0 = zero, new1 = zero, new2 = zero;
+        Four x0 = past(t0 - 3), x1 = past(t0 - 2), x2 = past(t0 - 1);
+        Four new0 = zero, new1 = zero, new2 = zero;
         const bool moves = p.advance && t0 == 0;
         if (moves) {  // (the state's inputs are read before they are written)
             new0 = past(n - 3);
             new1 = past(n - 2);
             new2 = past(n - 1);
         }
-        for (int t = t0; t < t1; t += kAbreast) {
-            float4 x3[kAbreast], y[kAbreast];
+        Four ahead[kAbreast];
+        const float* from = p.x + (first + t0) * p.x_stride + c;
+        auto ask = [&](int t) {
 #pragma unroll
-            for (int i = 0; i < kAbreast; ++i) x3[i] = t + i < t1 ? input(first + t + i) : zero;
+            for (int i = 0; i < kAbreast; ++i, from += p.x_stride)
+                ahead[i] = here && t + i < t1 && bc_global(bc, from, 16, p.x, x_extent, kBcDeltaX)
+                               ? as_four(*reinterpret_cast<const float4*>(from)) : zero;
+        };
+        ask(t0);
+        for (int t = t0; t < t1; t += kAbreast) {
+            Four y[kAbreast];
 #pragma unroll
             for (int i = 0; i < kAbreast; ++i) {
                 y[i] = zero;
-                tap(y[i], w, 0, x0);
-                tap(y[i], w, 1, x1);
-                tap(y[i], w, 2, x2);
-                tap(y[i], w, 3, x3[i]);
+                tap(y[i], w[0], x0);
+                tap(y[i], w[1], x1);
+                tap(y[i], w[2], x2);
+                tap(y[i], w[3], ahead[i]);
                 x0 = x1;
                 x1 = x2;
-                x2 = x3[i];
+                x2 = ahead[i];
             }
+            ask(t + kAbreast);  // (the next rows' loads are in flight while these are finished)
             finish(t, y);
         }
         if (moves && here && bc_global(bc, at_conv + c, 16, d.conv, d.conv_extent, kBcDeltaConv) &&
-            bc_global(bc, at_conv + 2 * d.channels + c, 16, d.conv, d.conv_extent, kBcDeltaConv)) {
-            *reinterpret_cast<float4*>(at_conv + c) = new0;
-            *reinterpret_cast<float4*>(at_conv + d.channels + c) = new1;
-            *reinterpret_cast<float4*>(at_conv + 2 * (int64_t)d.channels + c) = new2;
+            bc_global(bc, at_conv + 2 * (int64_t)d.channels + c, 16, d.conv, d.conv_extent, kBcDeltaConv)) {
+            const Four moved[3] = {new0, new1, new2};
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                *reinterpret_cast<float4*>(at_conv + (int64_t)i * d.channels + c) =
+                    make_float4(moved[i].a.x, moved[i].a.y, moved[i].b.x, moved[i].b.y);
         }
         return;
     }
@@ -177,20 +211,20 @@ __global__ void __launch_bounds__(kInputThreads) delta_inputs_kernel(const Input
         return -1;
     };
     for (int t = t0; t < t1; t += kAbreast) {
-        float4 y[kAbreast];
+        Four y[kAbreast];
         int from[kAbreast];
 #pragma unroll
         for (int i = 0; i < kAbreast; ++i) {
             from[i] = min(t + i, t1 - 1);
             y[i] = zero;
-            tap(y[i], w, 3, input(first + from[i]));
+            tap(y[i], w[3], input(first + from[i]));
         }
 #pragma unroll
         for (int j = 2; j >= 0; --j)
 #pragma unroll
             for (int i = 0; i < kAbreast; ++i) {
                 from[i] = parent(from[i]);
-                tap(y[i], w, j, past(from[i]));
+                tap(y[i], w[j], past(from[i]));
             }
         finish(t, y);
     }
@@ -226,7 +260,9 @@ cudaError_t launch_delta_inputs(const iq4xs_delta_inputs_args& a, const DeltaVie
     p.rows = (int)a.rows;
     p.key_lanes = d.key_dim / 4;
     p.col_parts = (d.channels + kInputCols - 1) / kInputCols + 1;
-    p.run = 16;  // (at least the three rows that read the state's inputs)
+    // Rows of a run (at least the three that read the state's inputs): longer
+    // ones look their sequence up less often, while the SMs keep several rounds.
+    p.run = a.rows * p.col_parts >= (int64_t)kLongRun * 16 * num_sms ? kLongRun : kShortRun;
     const int64_t blocks = (a.rows / p.run + b.sequences) * p.col_parts;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)blocks);

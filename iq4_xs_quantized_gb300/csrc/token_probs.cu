@@ -14,7 +14,8 @@ namespace {
 
 constexpr int kProbThreads = 512;
 constexpr int kProbWarps = kProbThreads / 32;
-constexpr int kProbUnits = 9;  // of four logits that a thread keeps
+constexpr int kProbUnits = 4;  // of four logits that a thread keeps
+constexpr int kAhead = 4;      // or has in flight
 constexpr int kProbPart = 4 * kProbThreads * kProbUnits;
 constexpr int kProbCluster = 8;
 
@@ -35,7 +36,7 @@ __device__ __forceinline__ float exp2_of(float x) {
     return y;
 }
 
-template <bool kGreedy>
+template <bool kGreedy, bool kHold>
 __device__ __forceinline__ void row_probs(const float* logits, const float* in, int64_t in_extent, float* probs, float* out,
                                           int64_t out_extent, int vocab, float t, int rank, int ranks, const Bc& bc) {
     __shared__ float tops[kProbWarps], sums[kProbWarps];
@@ -49,7 +50,7 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
     const int u0 = rank * each, u1 = min(units, u0 + each);
     auto load = [&](int u, float (&x)[4]) {
         const int i0 = 4 * u - skew;
-        if (i0 >= 0 && i0 + 4 <= vocab) {
+        if (u < u1 && i0 >= 0 && i0 + 4 <= vocab) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (bc_global(bc, in + i0, 16, logits, in_extent, kBcLogits)) v = *reinterpret_cast<const float4*>(in + i0);
             x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
@@ -57,21 +58,16 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 x[e] = -INFINITY;
-                if (i0 + e >= 0 && i0 + e < vocab && bc_global(bc, in + i0 + e, 4, logits, in_extent, kBcLogits))
+                if (u < u1 && i0 + e >= 0 && i0 + e < vocab && bc_global(bc, in + i0 + e, 4, logits, in_extent, kBcLogits))
                     x[e] = in[i0 + e];
             }
         }
     };
-    float x[kProbUnits][4];
+    // (1 / T within fp32's range: equal values then give 1 at any T)
+    const float c = fminf(fmaxf(1.44269504088896340736f / t, 1.17549435e-38f), 3.40282347e38f);
+    float x[kHold ? kProbUnits : 1][4];
     float top = -INFINITY, sum = 0.f;
     int place = INT32_MAX;
-#pragma unroll
-    for (int k = 0; k < kProbUnits; ++k) {
-        const int u = u0 + k * kProbThreads + tid;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[k][e] = -INFINITY;
-        if (u < u1) load(u, x[k]);
-    }
     auto look = [&](const float (&v)[4], int u) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -90,12 +86,35 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
         if (kGreedy && (other > top || (other == top && at < place))) place = at;
         top = fmaxf(top, other);
     };
+    float own = -INFINITY;  // what a thread's weights (or sum) are taken against
+    // e^((l - own) / T)
+    auto weigh = [&](float (&v)[4]) {
+        const float shift = own == -INFINITY ? 0.f : own;
 #pragma unroll
-    for (int k = 0; k < kProbUnits; ++k) look(x[k], u0 + k * kProbThreads + tid);
-    for (int u = u0 + kProbUnits * kProbThreads + tid; u < u1; u += kProbThreads) {  // what registers do not hold
-        float v[4];
-        load(u, v);
-        look(v, u);
+        for (int e = 0; e < 4; ++e) v[e] = exp2_of((v[e] - shift) * c);
+    };
+    if constexpr (kHold) {
+#pragma unroll
+        for (int k = 0; k < kProbUnits; ++k) load(u0 + k * kProbThreads + tid, x[k]);
+#pragma unroll
+        for (int k = 0; k < kProbUnits; ++k) look(x[k], u0 + k * kProbThreads + tid);
+    } else {
+        for (int u = u0 + tid; u < u1; u += kAhead * kProbThreads) {
+            float v[kAhead][4];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) load(u + k * kProbThreads, v[k]);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) look(v[k], u + k * kProbThreads);
+            if (!kGreedy) {  // a running sum
+                sum = top > own && own != -INFINITY ? sum * exp2_of((own - top) * c) : sum;
+                own = top;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    weigh(v[k]);
+                    sum += (v[k][0] + v[k][1]) + (v[k][2] + v[k][3]);
+                }
+            }
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -108,25 +127,18 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
     }
     __syncthreads();
     for (int w = 0; w < kProbWarps; ++w) first_top(tops[w], places[w]);
-    // e^((l - top) / T) against the part's own maximum, in the logits' place; the
-    // row's is made of the parts'.  (1 / T within fp32's range: equal values
-    // then give 1 at any T.)
-    const float c = fminf(fmaxf(1.44269504088896340736f / t, 1.17549435e-38f), 3.40282347e38f);
-    const float own = top, shift = top == -INFINITY ? 0.f : top;
-    auto weigh = [&](float (&v)[4]) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[e] = exp2_of((v[e] - shift) * c);
-            sum += v[e];
-        }
-    };
+    // The part's sum against its own maximum; the row's is made of the parts'.
     if (!kGreedy) {
+        if constexpr (kHold) {  // weights in the logits' place
+            own = top;
 #pragma unroll
-        for (int k = 0; k < kProbUnits; ++k) weigh(x[k]);
-        for (int u = u0 + kProbUnits * kProbThreads + tid; u < u1; u += kProbThreads) {
-            float v[4];
-            load(u, v);
-            weigh(v);
+            for (int k = 0; k < kProbUnits; ++k) {
+                weigh(x[k]);
+                sum += (x[k][0] + x[k][1]) + (x[k][2] + x[k][3]);
+            }
+        } else {
+            sum = own == -INFINITY ? sum : sum * exp2_of((own - top) * c);
+            own = top;
         }
     }
 #pragma unroll
@@ -139,23 +151,19 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
         if (tid == 0) mine = make_uint4(__float_as_uint(top), (uint32_t)place, __float_as_uint(sum), 0);
         cluster_arrive_release();
         cluster_wait();
-        uint4 part[kProbCluster];
-#pragma unroll
-        for (int r = 0; r < kProbCluster; ++r)
-            if (r < ranks) part[r] = ld_rank(&mine, r);
-#pragma unroll
-        for (int r = 0; r < kProbCluster; ++r)
-            if (r < ranks) first_top(__uint_as_float(part[r].x), (int)part[r].y);
+        for (int r = 0; r < ranks; ++r) {
+            const uint4 part = ld_rank(&mine, r);
+            first_top(__uint_as_float(part.x), (int)part.y);
+        }
         sum = 0.f;
-#pragma unroll
-        for (int r = 0; r < kProbCluster; ++r)
-            if (r < ranks) {
-                const float of = __uint_as_float(part[r].z), its = __uint_as_float(part[r].x);
-                sum += kGreedy ? of : its == -INFINITY ? of : of * exp2_of((its - top) * c);
-            }
+        for (int r = 0; r < ranks; ++r) {
+            const uint4 part = ld_rank(&mine, r);
+            const float of = __uint_as_float(part.z), its = __uint_as_float(part.x);
+            sum += kGreedy ? of : its == -INFINITY ? of : of * exp2_of((its - top) * c);
+        }
         cluster_arrive_release();  // (no CTA ends while another reads its part)
     }
-    // a weight times this is the probability (a part without any: zeros, unless the row is NaN)
+    // A weight times this is the probability (a part without any: zeros, unless the row is NaN).
     const float factor = own == -INFINITY ? sum * 0.f : own == top ? 1.f / sum : exp2_of((own - top) * c) / sum;
     auto put = [&](const float (&v)[4], int u) {
         const int i0 = 4 * u - skew;
@@ -165,7 +173,7 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
             y[e] = kGreedy ? (isnan(sum) ? sum : i0 + e == place ? 1.f : 0.f) : v[e] * factor;
         if (same && i0 >= 0 && i0 + 4 <= vocab) {
             if (bc_global(bc, out + i0, 16, probs, out_extent, kBcProbs))
-                *reinterpret_cast<float4*>(out + i0) = make_float4(y[0], y[1], y[2], y[3]);
+                __stcs(reinterpret_cast<float4*>(out + i0), make_float4(y[0], y[1], y[2], y[3]));
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -173,24 +181,33 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
                     out[i0 + e] = y[e];
         }
     };
-    for (int u = u0 + kProbUnits * kProbThreads + tid; u < u1; u += kProbThreads) {
-        float v[4];
-        load(u, v);
-        if (!kGreedy) weigh(v);
-        put(v, u);
-    }
+    if constexpr (kHold) {
 #pragma unroll
-    for (int k = 0; k < kProbUnits; ++k) {
-        const int u = u0 + k * kProbThreads + tid;
-        if (u < u1) put(x[k], u);
+        for (int k = 0; k < kProbUnits; ++k) {
+            const int u = u0 + k * kProbThreads + tid;
+            if (u < u1) put(x[k], u);
+        }
+    } else {
+        for (int u = u0 + tid; u < u1; u += kAhead * kProbThreads) {
+            float v[kAhead][4];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (!kGreedy) load(u + k * kProbThreads, v[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (!kGreedy) weigh(v[k]);
+                if (u + k * kProbThreads < u1) put(v[k], u + k * kProbThreads);
+            }
+        }
     }
     if (ranks > 1) cluster_wait();
 }
 
-__global__ void __launch_bounds__(kProbThreads, 2) token_probs_kernel(const float* logits, int64_t logits_stride,
-                                                                   int64_t rows, int vocab, const float* temperature,
-                                                                   float* probs, int64_t probs_stride, int ranks,
-                                                                   int* err) {
+template <bool kHold>
+__global__ void __launch_bounds__(kProbThreads, kHold ? 2 : 3)
+    token_probs_kernel(const float* logits, int64_t logits_stride, int64_t rows, int vocab, const float* temperature,
+                       float* probs, int64_t probs_stride, int ranks, int* err) {
     griddep_launch_dependents();
     griddep_wait();
     const Bc bc = bc_open(err);
@@ -201,8 +218,8 @@ __global__ void __launch_bounds__(kProbThreads, 2) token_probs_kernel(const floa
     const int64_t in_extent = 4 * ((rows - 1) * logits_stride + vocab), out_extent = 4 * ((rows - 1) * probs_stride + vocab);
     float t = 1.f;
     if (temperature != nullptr && bc_global(bc, temperature + row, 4, temperature, 4 * rows, kBcTemp)) t = temperature[row];
-    if (t > 0.f) row_probs<false>(logits, in, in_extent, probs, out, out_extent, vocab, t, rank, ranks, bc);
-    else row_probs<true>(logits, in, in_extent, probs, out, out_extent, vocab, 1.f, rank, ranks, bc);
+    if (t > 0.f) row_probs<false, kHold>(logits, in, in_extent, probs, out, out_extent, vocab, t, rank, ranks, bc);
+    else row_probs<true, kHold>(logits, in, in_extent, probs, out, out_extent, vocab, 1.f, rank, ranks, bc);
 }
 
 }  // namespace
@@ -215,8 +232,16 @@ cudaError_t launch_token_probs(const float* logits, int64_t logits_stride, int64
     while (ranks < kProbCluster && ((int64_t)ranks * kProbPart < vocab + 3 ||
                                     (2 * ranks * rows <= num_sms && (int64_t)ranks * 4 * kProbThreads < vocab)))
         ranks *= 2;
-    return launch_chained(token_probs_kernel, dim3((unsigned)(rows * ranks)), dim3(kProbThreads), 0, stream, ranks, logits,
-                          logits_stride, rows, (int)vocab, temperature, probs, probs_stride, ranks, err);
+    // In registers where all rows are under way at once so; else read twice, the
+    // second time from L2.
+    const bool hold = (int64_t)ranks * kProbPart >= vocab + 3 && ranks * rows <= 2 * num_sms;
+    if (!hold) {
+        ranks = 1;
+        while (ranks < kProbCluster && 2 * ranks * rows <= 3 * num_sms && (int64_t)ranks * 4 * kProbThreads < vocab) ranks *= 2;
+    }
+    return launch_chained(hold ? token_probs_kernel<true> : token_probs_kernel<false>, dim3((unsigned)(rows * ranks)),
+                          dim3(kProbThreads), 0, stream, ranks, logits, logits_stride, rows, (int)vocab, temperature, probs,
+                          probs_stride, ranks, err);
 }
 
 }  // namespace iq4xs
