@@ -26,7 +26,7 @@ struct CommitParams {
 };
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(kCommitThreads, 4) delta_commit_kernel(const CommitParams p, const DeltaView d,
+__global__ void __launch_bounds__(kCommitThreads, 5) delta_commit_kernel(const CommitParams p, const DeltaView d,
                                                                       const BatchView b, int* err) {
     constexpr int VS = 64, kCols = VS / 4, kGroups = kCommitThreads / kCols, kKeys = DK / kGroups;
     __shared__ __align__(16) float k_at[kPath][DK];

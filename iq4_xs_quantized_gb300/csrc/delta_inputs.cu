@@ -58,7 +58,7 @@ __device__ __forceinline__ float2 silu(float2 y) {
 }
 
 template <class T>
-__global__ void __launch_bounds__(kInputThreads) delta_inputs_kernel(const InputParams p, const DeltaView d,
+__global__ void __launch_bounds__(kInputThreads, 6) delta_inputs_kernel(const InputParams p, const DeltaView d,
                                                                      const BatchView b, int* err) {
     griddep_launch_dependents();
     griddep_wait();

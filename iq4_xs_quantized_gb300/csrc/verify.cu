@@ -10,6 +10,8 @@
 //
 // Few bytes are read (a row or two of probabilities a sequence): what it takes
 // is the chain of launch, tree, probabilities, sums, and the draw's search.
+#include <type_traits>
+
 #include "delta.cuh"
 
 namespace iq4xs {
@@ -56,6 +58,7 @@ struct VerifyShared {
     Order order;
 };
 
+__device__ __forceinline__ float in_unit(float p) { return p > 0.f ? fminf(p, 1.f) : 0.f; }  // (NaN: 0)
 // p in 0..1 as a whole number of 2^-61.
 __device__ __forceinline__ unsigned long long whole(float p) {
     if (!(p > 0.f)) return 0;
@@ -174,7 +177,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             if (p.draft != nullptr) {
                 const unsigned long long q = whole(sh.q[t]);
                 for (int i = 0; i < taken; ++i) r = take_off(r, sh.mass[i], q);
-                if (sh.token[t] >= 0 && u * real(mass) * real(q) < real(r)) {
+                // (at first by the values themselves, whose product 64 bits hold)
+                if (sh.token[t] >= 0 && (taken == 0 ? u * (double)in_unit(sh.q[t]) < (double)in_unit(sh.p[t])
+                                                    : u * real(mass) * real(q) < real(r))) {
                     accept();
                     continue;
                 }
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             }
             if (sh.token[t] < 0) continue;
             if (sh.again[t]) r = 0;
-            if (u * real(mass) < real(r)) {
+            if (gone == 0 ? sh.u[t] < in_unit(sh.p[t]) : u * real(mass) < real(r)) {
                 accept();
                 continue;
             }
@@ -222,42 +227,58 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         cluster_sync();
         const Order o = sh.order;
         if (o.what == kEnd) break;
-        // What is left behind the row of eight values from i0 on, `step` apart (0 behind the part's end).
+        // What is left behind the row of values i0, i0 + step, ... (0 behind the part's end).
         const float* const p_row = p.probs + o.node * p.probs_stride;
         const float* const q_row = p.draft + o.node * p.draft_stride;
-        auto left_at = [&](int i0, int step, unsigned long long (&r)[8]) {
-            float pr[8], qr[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int i = i0 + k * step;
-                pr[k] = i < end && bc_global(bc, p_row + i, 4, p.probs, p_extent, kBcVerifyProbs) ? p_row[i] : 0.f;
+        auto ask = [&](const float* row, const float* base, int64_t extent, int i) {
+            return i < end && bc_global(bc, row + i, 4, base, extent, kBcVerifyProbs) ? row[i] : 0.f;
+        };
+        auto left_of = [&](float pr, float qr) {
+            unsigned long long r = whole(pr);
+            if (o.taken > 0) {  // (the first m is 1)
+                const unsigned long long q = whole(qr);
+                r = r > q ? r - q : 0;
+                for (int x = 1; x < o.taken; ++x) r = take_off(r, sh.mass[x], q);
             }
+            return r;
+        };
+        // Sums of `kRuns` runs from `run` on, their loads in flight together.
+        auto sum_runs = [&](auto runs_tag, int run) {
+            constexpr int kRuns = decltype(runs_tag)::value;
+            float pr[kRuns][8], qr[kRuns][8];
+#pragma unroll
+            for (int y = 0; y < kRuns; ++y)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    pr[y][k] = ask(p_row, p.probs, p_extent, begin + (run + y * kVerifyWarps) * kRun + lane + 32 * k);
             if (o.taken > 0) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int i = i0 + k * step;
-                    qr[k] = i < end && bc_global(bc, q_row + i, 4, p.draft, q_extent, kBcVerifyProbs) ? q_row[i] : 0.f;
-                }
+                for (int y = 0; y < kRuns; ++y)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        qr[y][k] = ask(q_row, p.draft, q_extent, begin + (run + y * kVerifyWarps) * kRun + lane + 32 * k);
+            }
+            unsigned long long sum[kRuns];
+#pragma unroll
+            for (int y = 0; y < kRuns; ++y) {
+                sum[y] = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[y] += left_of(pr[y][k], qr[y][k]);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) r[k] = whole(pr[k]);
-            if (o.taken > 0) {  // (the first m is 1)
+            for (int k = 16; k > 0; k >>= 1)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const unsigned long long q = whole(qr[k]);
-                    r[k] = r[k] > q ? r[k] - q : 0;
-                    for (int x = 1; x < o.taken; ++x) r[k] = take_off(r[k], sh.mass[x], q);
-                }
-            }
+                for (int y = 0; y < kRuns; ++y) sum[y] += __shfl_xor_sync(0xffffffffu, sum[y], k);
+            if (lane == 0)
+#pragma unroll
+                for (int y = 0; y < kRuns; ++y)
+                    if (run + y * kVerifyWarps < runs) sh.runs[run + y * kVerifyWarps] = sum[y];
         };
         if (o.gone >= 0) {
-            for (int run = warp; run < runs; run += kVerifyWarps) {
-                unsigned long long r[8];
-                left_at(begin + run * kRun + lane, 32, r);
-                unsigned long long sum = ((r[0] + r[1]) + (r[2] + r[3])) + ((r[4] + r[5]) + (r[6] + r[7]));
-#pragma unroll
-                for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-                if (lane == 0) sh.runs[run] = sum;
+            if (p.draft != nullptr) {
+                for (int run = warp; run < runs; run += 2 * kVerifyWarps) sum_runs(std::integral_constant<int, 2>{}, run);
+            } else {
+                for (int run = warp; run < runs; run += 4 * kVerifyWarps) sum_runs(std::integral_constant<int, 4>{}, run);
             }
             __syncthreads();
             for (int i = tid; i < o.gone; i += kVerifyThreads) {
@@ -313,7 +334,15 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         // Eight neighbouring values a lane.
         const int i0 = begin + run * kRun + 8 * lane;
         unsigned long long r[8], sum = 0;
-        left_at(i0, 1, r);
+        float pr[8], qr[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) pr[k] = ask(p_row, p.probs, p_extent, i0 + k);
+        if (o.taken > 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) qr[k] = ask(q_row, p.draft, q_extent, i0 + k);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) r[k] = left_of(pr[k], qr[k]);
         for (int k = 0; k < o.gone; ++k)
 #pragma unroll
             for (int x = 0; x < 8; ++x) r[x] = sh.gone[k] == i0 + x ? 0 : r[x];
