@@ -160,12 +160,14 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     int node = 0, t = 1, count = 1, taken = 0, gone = 0;
     bool summed = false;  // what is left behind the node has been summed
     unsigned long long mass = kOne;
+    float near_mass = 1.f;
     auto accept = [&] {
         node = t;
         if (bc_global(bc, path + count, 4, p.paths, path_extent, kBcVerifyOut)) path[count] = t;
         ++count;
         taken = gone = 0;
         mass = kOne;
+        near_mass = 1.f;
         summed = false;
     };
     auto walk = [&]() -> int {
@@ -191,11 +193,15 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             }
             if (sh.token[t] < 0) continue;
             if (sh.again[t]) r = 0;
-            if (gone == 0 ? sh.u[t] < in_unit(sh.p[t]) : u * real(mass) < real(r)) {
+            // (In fp32 where that is far from a tie: its mass is off by 2^-24 a sibling, 1024 of them at most.)
+            const float chance = sh.again[t] ? 0.f : in_unit(sh.p[t]), bar = sh.u[t] * near_mass;
+            const bool far = fabsf(bar - chance) > 0x1p-12f;
+            if (gone == 0 ? sh.u[t] < chance : far ? bar < chance : u * real(mass) < real(r)) {
                 accept();
                 continue;
             }
             mass -= min(mass, r);
+            near_mass = fmaxf(near_mass - chance, 0.f);
             if (!sh.again[t]) sh.gone[gone++] = sh.token[t];
         }
         return kDraw;
@@ -246,18 +252,23 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         auto sum_runs = [&](auto runs_tag, int run) {
             constexpr int kRuns = decltype(runs_tag)::value;
             float pr[kRuns][8], qr[kRuns][8];
+            auto ask_runs = [&](float (&to)[kRuns][8], const float* row, const float* base, int64_t extent) {
+                const int i0 = begin + run * kRun + lane;
+                const float* const from = row + i0;
+                if (!kBoundsCheck && i0 - lane + ((kRuns - 1) * kVerifyWarps + 1) * kRun <= end) {  // (all inside: no test a value)
 #pragma unroll
-            for (int y = 0; y < kRuns; ++y)
+                    for (int y = 0; y < kRuns; ++y)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    pr[y][k] = ask(p_row, p.probs, p_extent, begin + (run + y * kVerifyWarps) * kRun + lane + 32 * k);
-            if (o.taken > 0) {
+                        for (int k = 0; k < 8; ++k) to[y][k] = from[y * kVerifyWarps * kRun + 32 * k];
+                } else {
 #pragma unroll
-                for (int y = 0; y < kRuns; ++y)
+                    for (int y = 0; y < kRuns; ++y)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        qr[y][k] = ask(q_row, p.draft, q_extent, begin + (run + y * kVerifyWarps) * kRun + lane + 32 * k);
-            }
+                        for (int k = 0; k < 8; ++k) to[y][k] = ask(row, base, extent, i0 + y * kVerifyWarps * kRun + 32 * k);
+                }
+            };
+            ask_runs(pr, p_row, p.probs, p_extent);
+            if (o.taken > 0) ask_runs(qr, q_row, p.draft, q_extent);
             unsigned long long sum[kRuns];
 #pragma unroll
             for (int y = 0; y < kRuns; ++y) {
