@@ -443,7 +443,12 @@ int iq4xs_set_pdl(int enable);
  *   0x107 the split-K slices of the other cluster ranks
  *   0x108 a stage of Q8_1 codes  0x109 a stage of activation scales;
  * in the warp-MMA matmul:
- *   0x10B a stage of weights and codes   0x10C a stage slot being freed.
+ *   0x10B a stage of weights and codes   0x10C a stage slot being freed;
+ * in attention:
+ *   0x10D a stage of keys or values   0x10E a stage slot being freed
+ *   0x10F a score or output product;
+ * in the delta rule:
+ *   0x110 a product or a block's operands   0x111 a block's rows or a state.
  * (0x102 is a code stage's MMAs completing, which frees its slot.)
  */
 int iq4xs_last_device_error(int* code_out);
@@ -466,7 +471,8 @@ int iq4xs_last_device_error(int* code_out);
  * split-K tile); 0x40-0x4A the tcgen05 matmul (W box, W box alignment,
  * code box, code box alignment, prepared operand, ds, y, span scales,
  * shared-memory size, split-K slices, grouped row_offsets or an expert's
- * rows).  A TMA box reaching past its tensor
+ * rows); 0x60-0x84 the attention side; 0x90-0x99 the recurrent layers;
+ * 0xA0-0xA5 the probabilities and the verification.  A TMA box reaching past its tensor
  * is recorded but still copied (the copy unit fills the rest); a box origin
  * off the 16-byte grid is recorded and not copied, and that stage's bounded
  * wait then runs out.  Results are those of the normal build whenever
@@ -494,7 +500,10 @@ int iq4xs_test_bounds_margin(int64_t bytes);
  * call's output is then undefined, every CTA still drains its copies (and,
  * on tcgen05, frees its tensor memory), and iq4xs_last_device_error
  * reports IQ4XS_ERR_TIMEOUT with code 0x101 (tcgen05) or 0x10B (warp MMA).
- * -1 disarms.  Host only.
+ * The next iq4xs_tree_attention takes it too (stage `stage` of every CTA: 0x10D),
+ * and iq4xs_delta_rule (block `stage` of 64 rows, or, in blocks of 8 and 16, the
+ * state that a CTA fetches as its `stage`-th: 0x111; that call's states stay as
+ * they are where the wait ran out).  -1 disarms.  Host only.
  */
 int iq4xs_test_skip_w_stage(int64_t stage);
 
@@ -750,7 +759,7 @@ int iq4xs_cache_copy_pages(const iq4xs_kv_cache* cache, const int32_t* src, cons
  * Sequence s of a batch has slot slot_of[s], or s where slot_of is NULL (device
  * memory; slots of one batch are distinct).  A sequence with lens[s] == 0 has
  * an empty state, whatever its slot holds.  Of the batch these calls read
- * row_offsets and lens only.
+ * row_offsets and lens only (its other arrays are to be there all the same).
  */
 typedef struct {
     float* s;
@@ -819,10 +828,11 @@ int iq4xs_delta_inputs(const iq4xs_delta_inputs_args* args, const iq4xs_delta_st
  *   max_rows  no sequence has more rows (one that does is skipped,
  *             IQ4XS_ERR_DATA); 0: not known.
  * Rows of no sequence are not written.  A row has no influence on rows that do
- * not come from it, whatever it holds.  S, sums and products are kept to fp32
- * (long runs of rows in two fp16 parts with a common exponent a column, 2^-22
- * of a value or 2^-38 of the column's largest, whichever is more).  Results are
- * the same from run to run.
+ * not come from it, whatever it holds.  S, sums and statistics are fp32; where
+ * several rows go through the tensor cores, what has more than 16 bits goes in
+ * two parts (2^-22 of a value, or 2^-38 of the largest of its column or row,
+ * whichever is more).  Results are the same from run to run.
+ * Speed: the kernel's form follows rows / sequences and max_rows: give it.
  * 1 <= rows <= 32768.
  */
 typedef struct {

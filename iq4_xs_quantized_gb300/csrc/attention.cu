@@ -7,10 +7,6 @@
 namespace iq4xs {
 namespace {
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 // Where no sequence can be longer than this (the table's width), in tokens:
 // items are not cut; or from kAloneTokens on a cluster shares an item, if the
 // SMs hold all items' clusters.  Measured for one token, 24/4 heads of 256, as

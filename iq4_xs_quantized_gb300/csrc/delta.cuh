@@ -43,6 +43,18 @@ __device__ __forceinline__ void unpack8(bool bf16, const uint4& w, float* x) {
     else unpack8<KvF16>(w, x);
 }
 
+// A value as two parts that tf32 holds: without its last 13 bits, and the remainder.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+// D += A B of a 16 x 8 x 8 tile by the warp-level MMA on tf32.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint2& b) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+}
+
 struct DeltaRule {  // iq4xs_delta_rule_args as its kernels see them
     const uint16_t* q;
     const uint16_t* k;
@@ -57,6 +69,7 @@ struct DeltaRule {  // iq4xs_delta_rule_args as its kernels see them
     int64_t s_offset;  // of the layer
     float scale;
     int mask_words, max_rows, rows, bf16;
+    int skip_block;  // (a test's) copies of this block, or item, of every CTA stay out; -1: none
 };
 
 // The new tokens before t that row row0 + t comes from, as bits (of 64).

@@ -136,6 +136,7 @@ int iq4xs_delta_rule(const iq4xs_delta_rule_args* a, const iq4xs_delta_state* st
     p.scale = (float)a->scale;
     p.rows = (int)a->rows;
     p.bf16 = a->dtype == IQ4XS_KV_BF16;
+    p.skip_block = take_skip_stage();
     // The most rows that a sequence can have; the kernels skip one with more.
     p.max_rows = (int)(a->max_rows > 0 && a->max_rows < a->rows ? a->max_rows : a->rows);
     if (a->u && p.max_rows > kDeltaTreeRows) p.max_rows = kDeltaTreeRows;

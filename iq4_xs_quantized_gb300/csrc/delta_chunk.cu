@@ -220,16 +220,6 @@ __device__ __forceinline__ uint32_t hide(float2 (&x)[16], const Gates& gt, int f
     return bits;
 }
 
-// D += A B of a 16 x 8 x 8 tile by the warp-level MMA on tf32, both sides in two parts.
-__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-    hi = __float_as_uint(x) & 0xffffe000u;
-    lo = __float_as_uint(x - __uint_as_float(hi));
-}
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
 // A tile (16 rows from `rows`, 8 columns from `cols`) of an N x N block below T's
 // diagonal at `at`: pass 0, X = A21 T11; pass 1, T21 = -T22 X.
 template <int N>
@@ -240,13 +230,14 @@ __device__ __forceinline__ void below_tile(const float* A, float* T, float* X, i
     float d[2][4] = {};
 #pragma unroll
     for (int k = 0; k < N; k += 8) {
-        uint32_t a[2][4], b[2][2];
+        uint32_t a[2][4];
+        uint2 b[2];
         split_tf32(left[k], a[0][0], a[1][0]);
         split_tf32(left[k + 8 * kPitch], a[0][1], a[1][1]);
         split_tf32(left[k + 4], a[0][2], a[1][2]);
         split_tf32(left[k + 4 + 8 * kPitch], a[0][3], a[1][3]);
-        split_tf32(right[k * kPitch], b[0][0], b[1][0]);
-        split_tf32(right[(k + 4) * kPitch], b[0][1], b[1][1]);
+        split_tf32(right[k * kPitch], b[0].x, b[1].x);
+        split_tf32(right[(k + 4) * kPitch], b[0].y, b[1].y);
         mma_tf32(d[1], a[1], b[0]);
         mma_tf32(d[1], a[0], b[1]);
         mma_tf32(d[0], a[0], b[0]);
@@ -352,6 +343,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         auto stage = [&](int c) {
             const int buf = c & 1, row = row0 + c * kRows;
             staged = c;
+            if (c == p.skip_block) return;
             mbar_arrive_expect_tx(landed + buf, C::kKqBytes + C::kVBytes);
             uint8_t* const kq = smem + C::kKq + buf * C::kKqBytes;
 #pragma unroll
@@ -915,6 +907,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             }
             tc_fence_before();
         }
+        lost = any_of<5, kMainThreads>(lost);  // one answer: what follows is a warp's work
         if (!lost) take_rows(blocks - 1, odd_last, scale_s, scale_u);
         if (!keep && busy && !lost) {
 #pragma unroll
@@ -933,10 +926,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // Rows of `width` 16-bit values, in boxes of kRows rows by `box`.
 bool encode_rows(void* enc, const uint16_t* base, int64_t width, int64_t rows, int64_t stride, int box, CUtensorMapSwizzle swizzle,

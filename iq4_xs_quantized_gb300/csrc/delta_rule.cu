@@ -197,16 +197,6 @@ struct FewShape {
     static_assert(kBar % 2 == 0, "barrier's alignment");
 };
 
-__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-    hi = __float_as_uint(x) & 0xffffe000u;
-    lo = __float_as_uint(x - __uint_as_float(hi));
-}
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint2& b) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
-}
-
 // x + a u where `with` holds (a selection, not a branch).
 __device__ __forceinline__ float take(bool with, float a, float u, float x) {
     const float y = fmaf(a, u, x);
@@ -257,8 +247,9 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
         it.n = it.len < 0 || it.slot < 0 || n > p.max_rows ? 0 : n;
         return it;
     };
+    int fetched = 0;
     auto fetch = [&](const FewItem& it) {  // by one thread
-        if (it.n == 0 || it.len == 0) return;
+        if (it.n == 0 || it.len == 0 || fetched++ == p.skip_block) return;
         mbar_arrive_expect_tx(landed, DK * VS * 4);
         bc_tma(bc, it.v0, 4, VS, d.value_dim, it.head * DK, (int64_t)d.heads * DK, kBcDeltaS, kBcDeltaS);
 #pragma unroll
@@ -521,9 +512,6 @@ cudaError_t launch_row(const DeltaRule& p, const DeltaView& d, const BatchView& 
     const dim3 grid((unsigned)((int64_t)b.sequences * d.heads * (d.value_dim / VS)));
     return launch_chained(delta_row_kernel<DK, VS>, grid, dim3(kRowThreads), 0, stream, 1, p, d, b, err);
 }
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 template <int DK, int kWarps, int TB>
 cudaError_t launch_few(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err, int num_sms,
