@@ -488,6 +488,8 @@ class KVBatch:
               "row_offsets [B + 1], lens [B], held [B], page_table [B, width]")
         self.row_offsets, self.lens, self.held, self.page_table = row_offsets, lens, held, page_table
         self.sequences = b
+        devices = {t.get_device() for t in (row_offsets, lens, held, page_table)}
+        self.device = devices.pop() if len(devices) == 1 else -1
         width = page_table.shape[1]
         stride = page_table.stride(0) if b > 1 else width
         self.desc = struct.pack("<7q", b, row_offsets.data_ptr(), lens.data_ptr(), held.data_ptr(),
@@ -769,7 +771,7 @@ def iq4xs_delta_inputs(x, conv_weight, a, b, a_log, dt_bias, eps: float, q, k, v
     if tree_mask is not None:
         words = _mask_words(fn, tree_mask, M)
         mask = tree_mask.data_ptr()
-    if (not (dev == st.device == conv_weight.get_device() == a.get_device() == b.get_device() ==
+    if (not (dev == st.device == batch.device == conv_weight.get_device() == a.get_device() == b.get_device() ==
             a_log.get_device() == dt_bias.get_device() == q.get_device() == k.get_device() == v.get_device() ==
             g.get_device() == beta.get_device()) or
             (tree_mask is not None and tree_mask.get_device() != dev)):
@@ -809,7 +811,7 @@ def iq4xs_delta_rule(q, k, v, g, beta, scale: float, out, state: DeltaState, lay
     if tree_mask is not None:
         words = _mask_words(fn, tree_mask, M)
         mask = tree_mask.data_ptr()
-    if (not (dev == st.device == k.get_device() == v.get_device() == g.get_device() == beta.get_device() ==
+    if (not (dev == st.device == batch.device == k.get_device() == v.get_device() == g.get_device() == beta.get_device() ==
             out.get_device()) or
             (u is not None and u.get_device() != dev) or
             (tree_mask is not None and tree_mask.get_device() != dev)):
@@ -860,7 +862,7 @@ def iq4xs_delta_commit(k, g, u, x, state: DeltaState, batch: KVBatch, paths, acc
     if not (len(p_shape) == 2 and p_shape[0] == B and accepted.numel() == B and paths.is_contiguous() and
             accepted.is_contiguous()):
         raise ValueError(f"{fn}: paths [B, width], accepted [B], contiguous")
-    if (not (dev == st.device == g.get_device() == u.get_device() == paths.get_device() ==
+    if (not (dev == st.device == batch.device == g.get_device() == u.get_device() == paths.get_device() ==
             accepted.get_device()) or
             (x is not None and x.get_device() != dev)):
         _wrong_device(fn)
@@ -887,7 +889,7 @@ def iq4xs_token_probs(logits, probs, temperature=None, stream=None) -> None:
         if not (temperature.dtype is f32 and temperature.shape == (M,) and temperature.is_contiguous()):
             raise ValueError(f"{fn}: temperature is contiguous float32 [M]")
         at_t = temperature.data_ptr()
-    if (not (dev  == probs.get_device()) or
+    if (not (dev == probs.get_device()) or
             (temperature is not None and temperature.get_device() != dev)):
         _wrong_device(fn)
     if M == 1:
@@ -931,7 +933,7 @@ def iq4xs_verify_drafts(probs, tokens, accept_u, draw_u, paths, accepted, next_t
     if tree_mask is not None:
         words = _mask_words(fn, tree_mask, M)
         mask = tree_mask.data_ptr()
-    if (not (dev  == tokens.get_device() == accept_u.get_device() == draw_u.get_device() ==
+    if (not (dev == batch.device == tokens.get_device() == accept_u.get_device() == draw_u.get_device() ==
             paths.get_device() == accepted.get_device() == next_token.get_device()) or
             (draft_probs is not None and draft_probs.get_device() != dev) or
             (tree_mask is not None and tree_mask.get_device() != dev)):

@@ -69,6 +69,8 @@ struct DeltaRule {  // iq4xs_delta_rule_args as its kernels see them
     int64_t s_offset;  // of the layer
     float scale;
     int mask_words, max_rows, rows, bf16;
+    int max_given;   // the caller said so
+    int few_rows;    // sequences of more rows go in blocks of 64
     int skip_block;  // (a test's) copies of this block, or item, of every CTA stay out; -1: none
 };
 
@@ -84,7 +86,7 @@ __device__ __forceinline__ uint64_t delta_seen(const uint64_t* mask, int words, 
 
 cudaError_t launch_delta_inputs(const iq4xs_delta_inputs_args& a, const DeltaView& d, const BatchView& b, int* err,
                                 int num_sms, cudaStream_t stream);
-cudaError_t launch_delta_rule(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err, int num_sms,
+cudaError_t launch_delta_rule(DeltaRule p, const DeltaView& d, const BatchView& b, void* encode, int* err, int num_sms,
                               cudaStream_t stream);
 cudaError_t launch_delta_chunk(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err,
                                cudaStream_t stream);
@@ -93,7 +95,7 @@ cudaError_t launch_delta_commit(const iq4xs_delta_commit_args& a, const DeltaVie
 cudaError_t launch_token_probs(const float* logits, int64_t logits_stride, int64_t rows, int64_t vocab,
                                const float* temperature, float* probs, int64_t probs_stride, int* err, int num_sms,
                                cudaStream_t stream);
-cudaError_t launch_verify_drafts(const iq4xs_verify_drafts_args& a, const BatchView& b, int* err,
+cudaError_t launch_verify_drafts(const iq4xs_verify_drafts_args& a, const BatchView& b, int* err, int num_sms,
                                  cudaStream_t stream);
 
 }  // namespace iq4xs

@@ -139,6 +139,8 @@ int iq4xs_delta_rule(const iq4xs_delta_rule_args* a, const iq4xs_delta_state* st
     p.skip_block = take_skip_stage();
     // The most rows that a sequence can have; the kernels skip one with more.
     p.max_rows = (int)(a->max_rows > 0 && a->max_rows < a->rows ? a->max_rows : a->rows);
+    p.max_given = a->max_rows > 0;
+    p.few_rows = 0;
     if (a->u && p.max_rows > kDeltaTreeRows) p.max_rows = kDeltaTreeRows;
     return from_cuda(launch_delta_rule(p, d, b, encode, err, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -205,7 +207,7 @@ int iq4xs_verify_drafts(const iq4xs_verify_drafts_args* a, const iq4xs_kv_batch*
     void* encode;
     if ((rc = device_context(&err, &sms, &encode))) return rc;
     if (b.sequences == 0) return IQ4XS_OK;
-    return from_cuda(launch_verify_drafts(*a, b, err, reinterpret_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_verify_drafts(*a, b, err, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

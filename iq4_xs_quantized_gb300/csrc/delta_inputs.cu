@@ -9,6 +9,12 @@
 // sequence alone reads the state's inputs, and writes them anew: its rows are
 // at least the three that need them.  A drafted tree's rows read their
 // ancestors' inputs instead, out of L1 or L2.
+//
+// Four rows' loads are in flight together and the next four's are asked for
+// before these are worked on (6,147 rows of 16 + 16 + 48 heads of 128: 74 us, 5.1 TB/s of
+// the 6.8 of a copy; two abreast 82, CTAs of 256 threads 84).  At that size the
+// issue slots are 75 % used (packed arithmetic took 5 us off); the smallest calls
+// are a launch and three dependent loads.
 #include "attention.cuh"
 #include "delta.cuh"
 
@@ -18,7 +24,8 @@ namespace {
 constexpr int kInputThreads = 128;
 constexpr int kInputCols = 4 * kInputThreads;  // channels of a CTA
 constexpr int kAbreast = 4;                    // rows whose loads are in flight together
-constexpr int kShortRun = 16, kLongRun = 32;   // rows of one CTA
+constexpr int kLeastRun = 4, kShortRun = 16, kLongRun = 32;  // rows of one CTA
+static_assert(kLeastRun >= kConvTaps - 1, "the first run alone touches the state");
 
 struct InputParams {
     const float* x;
@@ -260,9 +267,15 @@ cudaError_t launch_delta_inputs(const iq4xs_delta_inputs_args& a, const DeltaVie
     p.rows = (int)a.rows;
     p.key_lanes = d.key_dim / 4;
     p.col_parts = (d.channels + kInputCols - 1) / kInputCols + 1;
-    // Rows of a run (at least the three that read the state's inputs): longer
-    // ones look their sequence up less often, while the SMs keep several rounds.
-    p.run = a.rows * p.col_parts >= (int64_t)kLongRun * 16 * num_sms ? kLongRun : kShortRun;
+    // Rows of a run, at least the three that read the state's inputs: few while about
+    // all CTAs are resident at once, for a CTA's rows come one behind the other (48
+    // heads, runs of 4, 8 and 16: 96 rows 5.4, 5.8 and 7.5 us, 300 8.2, 7.1 and 8.8, 1,000
+    // 19.9, 15.2 and 14.1); 32 where SMs keep several rounds all the same, for runs look
+    // their sequence up and read three rows again (of 16 and 32: 2,048 rows 27.1 and 28.4,
+    // 4,000 48.4 and 46.1, 6,147 71.2 and 69.7; of 64 71.4).
+    p.run = kLeastRun;
+    while (p.run < kShortRun && a.rows * p.col_parts > (int64_t)p.run * 7 * num_sms) p.run *= 2;
+    if (a.rows * p.col_parts >= (int64_t)kLongRun * 16 * num_sms) p.run = kLongRun;
     const int64_t blocks = (a.rows / p.run + b.sequences) * p.col_parts;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)blocks);

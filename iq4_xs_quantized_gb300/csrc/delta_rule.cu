@@ -13,7 +13,9 @@
 //
 // A CTA holds a head's S, or a slice of its columns, in registers for all of a
 // sequence's rows: HBM reads it once and, where it moves on, writes it once,
-// which bounds single rows.
+// which bounds single rows (45 sequences of 48 heads of 128 x 128, 283 MB: 45.6 us, 6.2 TB/s, 92 %
+// of a copy; one sequence 3.2 us, of which a launch and three loads that wait for one another
+// are most).
 #include "attention.cuh"
 #include "delta.cuh"
 
@@ -173,7 +175,9 @@ __global__ void __launch_bounds__(kRowThreads, 4) delta_row_kernel(const DeltaRu
 // CTAs stay for several items (a head's columns of a sequence): S comes to shared
 // memory by TMA, goes to registers, and the next item's is on its way meanwhile.
 // (CTAs of one item each load together and then compute together: 16.3 us where
-// this takes @@ for 12 trees of 8.)
+// this takes 12.7 for 12 trees of 8 of 48 heads of 128 x 128, 40 MB: 3.1 TB/s; FFMA instead
+// of the MMA 17.8.)  What bounds it: an item's chain of six steps between barriers,
+// about 2.9 us, two CTAs an SM; S in two parts is a third of its instructions.
 constexpr int kFewPad = 8;  // floats behind a row in shared memory: rows an operand reads together on all banks
 
 template <int DK, int kWarps, int TB>
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
         it.len = batch_len(b, s, err);
         it.slot = delta_slot(d, s, err);
         if (n > p.max_rows && tid == 0) data_error(err, kDataCount);
-        it.n = it.len < 0 || it.slot < 0 || n > p.max_rows ? 0 : n;
+        it.n = it.len < 0 || it.slot < 0 || n > p.max_rows || n > p.few_rows ? 0 : n;
         return it;
     };
     int fetched = 0;
@@ -535,32 +539,55 @@ cudaError_t launch_few(const DeltaRule& p, const DeltaView& d, const BatchView& 
                           C::kSmem, stream, 1, map, p, d, b, (int)items, err);
 }
 
-// Single rows where a sequence has one on average; else blocks of eight, or of
-// 16.  Slices of 32 columns while that many CTAs find an SM of their own.
 template <int DK>
 cudaError_t launch_keys(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err, int num_sms,
-                        cudaStream_t stream) {
-    const int64_t items = (int64_t)b.sequences * d.heads;
-    const bool few = items * (d.value_dim / 32) <= 2 * num_sms;
-    if (p.max_rows == 1 || (p.u == nullptr && p.rows <= b.sequences))
-        return few ? launch_row<DK, 32>(p, d, b, err, stream) : launch_row<DK, 64>(p, d, b, err, stream);
-    if (p.max_rows <= 8 || (p.u == nullptr && p.rows <= 8 * (int64_t)b.sequences))
-        return few                  ? launch_few<DK, 2, 8>(p, d, b, encode, err, num_sms, stream)
-               : d.value_dim == 128 ? launch_few<DK, 8, 8>(p, d, b, encode, err, num_sms, stream)
-                                    : launch_few<DK, 4, 8>(p, d, b, encode, err, num_sms, stream);
+                        bool single, int block, cudaStream_t stream) {
+    if (single) {
+        // 32 columns a CTA while all CTAs are resident at once, else 64 (48 heads:
+        // 1 sequence 3.57 and 3.96 us, 3 4.46 and 5.00; 4 6.38 and 5.96, 16 16.1
+        // and 13.6, 45 58.7 and 47.0).
+        const bool thin = (int64_t)b.sequences * d.heads * (d.value_dim / 32) <= 4 * num_sms;
+        return thin ? launch_row<DK, 32>(p, d, b, err, stream) : launch_row<DK, 64>(p, d, b, err, stream);
+    }
+    // (32 columns a CTA were no faster here, for one sequence either: 6.57 us for
+    // 4.95 for a tree of 8.)
+    if (block == 8)
+        return d.value_dim == 128 ? launch_few<DK, 8, 8>(p, d, b, encode, err, num_sms, stream)
+                                  : launch_few<DK, 4, 8>(p, d, b, encode, err, num_sms, stream);
     return d.value_dim == 128 ? launch_few<DK, 8, 16>(p, d, b, encode, err, num_sms, stream)
                               : launch_few<DK, 4, 16>(p, d, b, encode, err, num_sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_delta_rule(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err, int num_sms,
+// The form follows a sequence's rows (times in us, 48 heads of 128 x 128).
+// Row by row up to two on average: 12 chains of 2 13.4 (blocks of 8: 17.5), of 4
+// 19.1 (17.7); 48 of 2 60.5 (66.0), of 4 83.2 (66.7).
+// Blocks of 8 for chains: 48 of 9 98.6 (blocks of 16: 117), of 16 103 (124), of 32
+// 171 (218).  A tree is one block: of 16 from 9 rows on.
+// Blocks of 64 from there where they win.  They take 13.4 for a wave of the SMs
+// whatever the rows: 3 chains of 16 13.6 (blocks of 8: 13.3), of 20 13.6 (16.9), 1 of 20
+// 13.4 (12.5), of 32 13.3 (15.5); in several waves 12 chains of 32 51.7 (42.9), 48
+// of 32 225 (171), each 8 rows more 8 and 34.
+// A batch whose longest sequence is longer, but not the mean, takes both.
+cudaError_t launch_delta_rule(DeltaRule p, const DeltaView& d, const BatchView& b, void* encode, int* err, int num_sms,
                               cudaStream_t stream) {
-    // A tree is one block; chains of more than 12 rows on average go in blocks of 64.
-    if (p.u != nullptr ? p.max_rows > 16 : p.rows > 12 * (int64_t)b.sequences && p.max_rows > 16)
-        return launch_delta_chunk(p, d, b, encode, err, stream);
-    return d.key_dim == 64 ? launch_keys<64>(p, d, b, encode, err, num_sms, stream)
-                           : launch_keys<128>(p, d, b, encode, err, num_sms, stream);
+    const bool tree = p.u != nullptr;
+    const int64_t sequences = b.sequences;
+    const int few = tree || sequences * d.heads <= num_sms ? 16 : 40;
+    if (p.max_rows > few && p.rows > few * sequences) return launch_delta_chunk(p, d, b, encode, err, stream);
+    const bool both = p.max_rows > few && (tree || p.max_given);
+    if (both) {
+        p.few_rows = few;
+        const cudaError_t e = launch_delta_chunk(p, d, b, encode, err, stream);
+        if (e != cudaSuccess) return e;
+    } else {
+        p.few_rows = p.max_rows;
+    }
+    const bool single = tree ? p.max_rows == 1 : p.rows <= 2 * sequences && (p.max_rows <= 8 || !p.max_given);
+    const int block = tree && p.max_rows > 8 ? 16 : 8;
+    return d.key_dim == 64 ? launch_keys<64>(p, d, b, encode, err, num_sms, single, block, stream)
+                           : launch_keys<128>(p, d, b, encode, err, num_sms, single, block, stream);
 }
 
 }  // namespace iq4xs

@@ -5,6 +5,9 @@
 // or, T not above 0, 1 at the first of the largest logits.  A row is read once,
 // by a cluster of CTAs that keep their parts in registers and exchange maximum
 // and sum through distributed shared memory, and written once: HBM bounds it.
+// 96 rows of 131,073: 18.2 us, 5.5 TB/s of the 6.8 of a copy; start, the clusters'
+// exchange and the end are what is left.  One row of 32,000: 3.9 us, a launch, the
+// loads and the exchange.
 // Rows start at any multiple of four bytes; a part's units of four values lie on
 // 16-byte boundaries of the logits, cut at the row's ends.
 #include "delta.cuh"
@@ -233,7 +236,8 @@ cudaError_t launch_token_probs(const float* logits, int64_t logits_stride, int64
                                     (2 * ranks * rows <= num_sms && (int64_t)ranks * 4 * kProbThreads < vocab)))
         ranks *= 2;
     // In registers where all rows are under way at once so; else read twice, the
-    // second time from L2.
+    // second time from L2 (32,000 logits: 8 rows 4.4 us in registers, 5.0 read twice, 48 5.7
+    // and 9.6; 96 9.4 and 8.1, 192 14.1 and 10.2).
     const bool hold = (int64_t)ranks * kProbPart >= vocab + 3 && ranks * rows <= 2 * num_sms;
     if (!hold) {
         ranks = 1;

@@ -9,7 +9,10 @@
 // changes them: a draw near the border of two tokens always falls alike.
 //
 // Few bytes are read (a row or two of probabilities a sequence): what it takes
-// is the chain of launch, tree, probabilities, sums, and the draw's search.
+// is the chain of launch, tree, probabilities, sums, and the draw's search: 12 trees of 8
+// over 131,073 tokens 11.7 us, a chain of four with a drafter's probabilities over
+// 32,000 10.0.  (CTAs of 256, 512 and 1,024 threads: 13.1, 12.3 and 12.4 before the loads
+// were grouped.)
 #include <type_traits>
 
 #include "delta.cuh"
@@ -393,7 +396,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
 
 }  // namespace
 
-cudaError_t launch_verify_drafts(const iq4xs_verify_drafts_args& a, const BatchView& b, int* err, cudaStream_t stream) {
+cudaError_t launch_verify_drafts(const iq4xs_verify_drafts_args& a, const BatchView& b, int* err, int num_sms,
+                                 cudaStream_t stream) {
     VerifyParams p;
     p.probs = a.probs;
     p.draft = a.draft_probs;
@@ -411,7 +415,14 @@ cudaError_t launch_verify_drafts(const iq4xs_verify_drafts_args& a, const BatchV
     p.vocab = (int)a.vocab;
     p.path_width = (int)a.path_width;
     p.ranks = 1;
-    while (p.ranks < kVerifyCluster && p.ranks * 8 * kRun < p.vocab) p.ranks *= 2;  // (a run for half of a CTA's warps)
+    // A run for half of a CTA's warps, and a CTA an SM: 131,073 tokens, 12 sequences 18.5,
+    // 13.6 and 10.9 us by 2, 4 and 8 CTAs each, 45 18.5, 24.6 and 28.7; 701 tokens
+    // and a drafter's probabilities, 12 sequences 9.4 by one and 10.7 by two.  (At
+    // least as many as the sums' runs need.)
+    while (p.ranks < kVerifyCluster &&
+           (p.vocab > (int64_t)p.ranks * kMaxRuns * kRun ||
+            (p.ranks * 8 * kRun < p.vocab && 2 * (int64_t)p.ranks * b.sequences <= num_sms)))
+        p.ranks *= 2;
     return launch_chained(verify_kernel, dim3((unsigned)(b.sequences * p.ranks)), dim3(kVerifyThreads), 0, stream, p.ranks,
                           p, b, err);
 }

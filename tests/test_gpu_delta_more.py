@@ -34,6 +34,23 @@ def test_rule_mixed_batches(new, dtype):
     D.run_rule(Batch(lens, new, 2, 8, dtype=dtype, seed=len(new)))
 
 
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("hk,hv", [(2, 8), (16, 48)])
+@pytest.mark.parametrize("new", [[1] * 20 + [130], [300, 0, 1, 2, 41, 40, 39], [17] + [0] * 30 + [16, 1], [2] * 9 + [8], [1] * 9 + [9],
+                                 [0, 0, 70, 0, 0, 0, 0, 0, 0]])
+def test_rule_long_among_short(new, hk, hv, dtype):
+    """A longest sequence that is known: long ones in blocks of 64, the others not."""
+    D.run_rule(Batch([0 if i % 3 == 1 else 5 for i in range(len(new))], new, hk, hv, dtype=dtype, seed=len(new)), max_rows=max(new))
+
+
+@pytest.mark.parametrize("known", (True, False))
+@pytest.mark.parametrize("new", [[1] * 9 + [17], [64, 0, 16, 3], [8, 9, 0, 40, 16], [2] * 12 + [64]])
+def test_trees_of_all_sizes(new, known):
+    rng = np.random.default_rng(len(new))
+    parents = [tree_parents(n, rng) if n else [] for n in new]
+    D.run_rule(Batch([4] * len(new), new, 2, 4, seed=2), parents, keep=True, max_rows=max(new) if known else None)
+
+
 @pytest.mark.parametrize("hk,hv,dk,dv", D.DIMS)
 @pytest.mark.parametrize("tree", (3, 8, 13))
 def test_rule_many_trees(hk, hv, dk, dv, tree):
@@ -190,3 +207,32 @@ def test_a_wait_that_runs_out(new, stage):
     assert torch.equal(bt.s[:, hit].view(torch.int32), before[:, hit].view(torch.int32))
     bt.s.copy_(before)
     D.run_rule(bt, ops=ops)
+
+
+@pytest.mark.parametrize("rows,vocab", [(1, 32000), (5, 4097), (96, 33001), (200, 8003), (3, 300001)])
+def test_probs_in_place(rows, vocab):
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    logits = torch.randn(rows, vocab + 5, generator=g, device="cuda")[:, 1:1 + vocab]
+    t = torch.linspace(0, 2, rows, device="cuda")
+    want = torch.empty(rows, vocab, device="cuda")
+    B.iq4xs_token_probs(logits, want, t)
+    V.check_probs(want, logits, t)
+    B.iq4xs_token_probs(logits, logits, t)
+    assert torch.equal(logits, want)
+
+
+def test_a_batch_on_the_host_is_refused():
+    bt = Batch([4], [2], 1, 1)
+    ops = bt.operands()
+    out, u = torch.empty(2, bt.dv, device="cuda"), torch.empty(2, 1, bt.dv, device="cuda")
+    x, ab, heads = bt.randn(2, bt.channels), bt.randn(2, 1), bt.randn(1)
+    there = [i32(v) for v in ([0, 2], [4], [0], [[0]])]
+    probs, tokens, rand = torch.full((2, 8), 0.125, device="cuda"), i32([0, 1]), torch.rand(2, device="cuda")
+    for i in range(4):
+        host = B.KVBatch(*[t.cpu() if j == i else t for j, t in enumerate(there)])
+        for call in (lambda: B.iq4xs_delta_rule(*ops, 0.1, out, bt.state, 0, host),
+                     lambda: B.iq4xs_delta_inputs(x, bt.randn(bt.channels, 4), ab, ab, heads, heads, 1e-6, *ops, bt.state, 0, host),
+                     lambda: B.iq4xs_delta_commit(ops[1][None], ops[3][None], u[None], x[None], bt.state, host, i32([[0]]), i32([1])),
+                     lambda: B.iq4xs_verify_drafts(probs, tokens, rand, rand[:1], i32([[0, 0]]), i32([0]), i32([0]), host)):
+            with pytest.raises(ValueError, match="current CUDA device"):
+                call()
