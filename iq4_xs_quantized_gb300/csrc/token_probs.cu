@@ -21,6 +21,7 @@ constexpr int kProbUnits = 4;  // of four logits that a thread keeps
 constexpr int kAhead = 4;      // or has in flight
 constexpr int kProbPart = 4 * kProbThreads * kProbUnits;
 constexpr int kProbCluster = 8;
+constexpr int kProbMost = 40000;  // logits of a part that is read twice
 
 __device__ __forceinline__ uint32_t rank_addr(const void* p, int rank) {
     uint32_t a;
@@ -230,18 +231,22 @@ __global__ void __launch_bounds__(kProbThreads, kHold ? 2 : 3)
 cudaError_t launch_token_probs(const float* logits, int64_t logits_stride, int64_t rows, int64_t vocab,
                                const float* temperature, float* probs, int64_t probs_stride, int* err, int num_sms,
                                cudaStream_t stream) {
-    // A row's parts: as many as registers want, and more while SMs are free.
+    // In registers where one CTA holds a row, or all rows are under way at once, in as
+    // few parts as hold it (one row of 8,000: 2.8 us by one CTA, 3.4 by four, 32,000
+    // 3.9 by four and 4.1 by eight); else read twice, the second time from L2 (600 rows of
+    // 8,000 6.7 us in registers, 7.1 read twice; of 32,000 8 4.4 and 5.0, 48 5.7 and 9.6, 96 9.4
+    // and 8.1, 192 14.1 and 10.2).
     int ranks = 1;
-    while (ranks < kProbCluster && ((int64_t)ranks * kProbPart < vocab + 3 ||
-                                    (2 * ranks * rows <= num_sms && (int64_t)ranks * 4 * kProbThreads < vocab)))
-        ranks *= 2;
-    // In registers where all rows are under way at once so; else read twice, the
-    // second time from L2 (32,000 logits: 8 rows 4.4 us in registers, 5.0 read twice, 48 5.7
-    // and 9.6; 96 9.4 and 8.1, 192 14.1 and 10.2).
-    const bool hold = (int64_t)ranks * kProbPart >= vocab + 3 && ranks * rows <= 2 * num_sms;
+    while (ranks < kProbCluster && (int64_t)ranks * kProbPart < vocab + 3) ranks *= 2;
+    const bool hold = (int64_t)ranks * kProbPart >= vocab + 3 && (ranks == 1 || ranks * rows <= 2 * num_sms);
+    // Read twice, as many parts as are resident at once (32,000: 96 rows 8.0, 8.8, 8.2 and 15.9 us
+    // by 1, 2, 4 and 8, 200 10.9, 10.3, 14.2, 28.6, 400 14.3, 18.9, 25.1, 52.6; 131,073: one row 20.0, 12.8,
+    // 8.7, 6.8), of at most 40,000 (200 rows of 131,073: 59.3, 51.1, 44.3, 53.7).
     if (!hold) {
         ranks = 1;
-        while (ranks < kProbCluster && 2 * ranks * rows <= 3 * num_sms && (int64_t)ranks * 4 * kProbThreads < vocab) ranks *= 2;
+        while (ranks < kProbCluster && (int64_t)ranks * 4 * kProbThreads < vocab &&
+               (2 * ranks * rows <= 3 * num_sms || (int64_t)ranks * kProbMost < vocab))
+            ranks *= 2;
     }
     return launch_chained(hold ? token_probs_kernel<true> : token_probs_kernel<false>, dim3((unsigned)(rows * ranks)),
                           dim3(kProbThreads), 0, stream, ranks, logits, logits_stride, rows, (int)vocab, temperature, probs,

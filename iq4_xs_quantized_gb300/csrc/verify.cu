@@ -77,6 +77,29 @@ __device__ __forceinline__ unsigned long long take_off(unsigned long long r, uns
     const unsigned long long off = __umul64hi(m << 1, q << 2);
     return r > off ? r - off : 0;
 }
+// What is left of p behind `taken` subtractions of q (the first m is 1).
+__device__ __forceinline__ unsigned long long left_of(float p, float q_at, int taken, const unsigned long long* mass) {
+    const unsigned long long q = whole(q_at);
+    unsigned long long r = whole(p);
+    r = r > q ? r - q : 0;
+#pragma unroll 1
+    for (int x = 1; x < taken; ++x) r = take_off(r, mass[x], q);
+    return r;
+}
+// Sums of eight.  (Out of line: a step calls this kernel once, its instructions
+// come from L2 or HBM, and unrolled for every run they were most of its time.)
+__device__ __noinline__ unsigned long long whole8(float a, float b, float c, float d, float e, float f, float g, float h) {
+    return ((whole(a) + whole(b)) + (whole(c) + whole(d))) + ((whole(e) + whole(f)) + (whole(g) + whole(h)));
+}
+__device__ __noinline__ unsigned long long left8(float a, float b, float c, float d, float e, float f, float g, float h, float qa, float qb,
+                                                 float qc, float qd, float qe, float qf, float qg, float qh, int taken,
+                                                 const unsigned long long* mass) {
+    const float p[8] = {a, b, c, d, e, f, g, h}, q[8] = {qa, qb, qc, qd, qe, qf, qg, qh};
+    unsigned long long sum = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += left_of(p[k], q[k], taken, mass);
+    return sum;
+}
 __device__ __forceinline__ uint32_t at_rank(const void* p, int rank) {
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
@@ -242,15 +265,6 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         auto ask = [&](const float* row, const float* base, int64_t extent, int i) {
             return i < end && bc_global(bc, row + i, 4, base, extent, kBcVerifyProbs) ? row[i] : 0.f;
         };
-        auto left_of = [&](float pr, float qr) {
-            unsigned long long r = whole(pr);
-            if (o.taken > 0) {  // (the first m is 1)
-                const unsigned long long q = whole(qr);
-                r = r > q ? r - q : 0;
-                for (int x = 1; x < o.taken; ++x) r = take_off(r, sh.mass[x], q);
-            }
-            return r;
-        };
         // Sums of `kRuns` runs from `run` on, their loads in flight together.
         auto sum_runs = [&](auto runs_tag, int run) {
             constexpr int kRuns = decltype(runs_tag)::value;
@@ -275,9 +289,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             unsigned long long sum[kRuns];
 #pragma unroll
             for (int y = 0; y < kRuns; ++y) {
-                sum[y] = 0;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) sum[y] += left_of(pr[y][k], qr[y][k]);
+                const float(&a)[8] = pr[y], (&e)[8] = qr[y];
+                sum[y] = o.taken > 0 ? left8(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], e[0], e[1], e[2], e[3], e[4], e[5],
+                                             e[6], e[7], o.taken, sh.mass)
+                                     : whole8(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7]);
             }
 #pragma unroll
             for (int k = 16; k > 0; k >>= 1)
@@ -356,7 +371,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             for (int k = 0; k < 8; ++k) qr[k] = ask(q_row, p.draft, q_extent, i0 + k);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) r[k] = left_of(pr[k], qr[k]);
+        for (int k = 0; k < 8; ++k) r[k] = o.taken > 0 ? left_of(pr[k], qr[k], o.taken, sh.mass) : whole(pr[k]);
         for (int k = 0; k < o.gone; ++k)
 #pragma unroll
             for (int x = 0; x < 8; ++x) r[x] = sh.gone[k] == i0 + x ? 0 : r[x];
