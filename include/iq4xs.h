@@ -832,7 +832,8 @@ int iq4xs_delta_inputs(const iq4xs_delta_inputs_args* args, const iq4xs_delta_st
  * several rows go through the tensor cores, what has more than 16 bits goes in
  * two parts (2^-22 of a value, or 2^-38 of the largest of its column or row,
  * whichever is more).  Results are the same from run to run.
- * Speed: the kernel's form follows rows / sequences and max_rows: give it.
+ * Speed: the kernel's form follows rows / sequences and max_rows: give it (a long
+ * sequence among short ones then goes in a launch of its own).
  * 1 <= rows <= 32768.
  */
 typedef struct {

@@ -15,19 +15,19 @@
 // memory.  Eight more warps prepare the next block meanwhile: K and Q in shared
 // memory, their products [K; Q] K^T, decays (by walking back from every row, so
 // that no difference of long sums enters), A and P; T's diagonal blocks of 16 by
-// substitution, what is below them, -T22 A21 T11, by the warp-level MMA on tf32 (three
-// terms of two parts; substitution throughout took 2,000 cycles more).
+// substitution, what is below them, -T22 A21 T11, by the warp-level MMA on tf32, three
+// terms of two parts (with decays from a scan and rows asked into L2: 231 to 210 us).
 //
 // Measured: 6,147 rows of 3 sequences, 48 heads of 128 x 128: 210 us, floor of the bytes
 // 44; 144 CTAs, 33 blocks of 12,300 cycles in a row, the first behind 8 us.  What bounds
 // it is that chain: preparing a block takes 11,300 cycles (copies landing 1,000,
-// conversion 2,900, the pairs' product 1,900, decays 1,600, substitution 1,500, the rest of T
-// 3,700), the block itself 10,500 (S^T [K; Q] and the last block's out 2,400, r 2,000, u
-// 3,600, S 2,500), of which the tensor core is busy 13 %.  Tried: copies issued
-// by other warps and as soon as the block lets go of K, Q and V (medians of a CTA 196
-// us instead of 198, but the slowest 203 to 233 instead of 201: 213 to 230 in all);
-// polling instead of sleeping waits (216); the gates under the pairs' product, three
-// sums for T's terms, the last two products issued by two warps (no difference).
+// conversion 2,900, the pairs' product 1,900, decays 1,600, substitution 1,500, the rest
+// of T 3,700), the block itself 10,500 (S^T [K; Q] and the last block's out 2,400, r
+// 2,000, u 3,600, S 2,500), the tensor core busy 20 % of the time.  Tried: copies issued by
+// other warps and as soon as the block lets go of K, Q and V (medians of a CTA 196 us
+// instead of 198, but the slowest 203 to 233 instead of 201: 213 to 230 in all); polling
+// instead of sleeping waits (216); the gates under the pairs' product, three sums for T's
+// terms, the last two products issued by two warps (no difference).
 //
 // Precision.  The products take fp16.  K and Q of 16 bits are exact (bf16 rows
 // times a power of two; what is 2^-38 below a row's largest is cut), all else goes

@@ -12,9 +12,9 @@
 //
 // Four rows' loads are in flight together and the next four's are asked for
 // before these are worked on (6,147 rows of 16 + 16 + 48 heads of 128: 74 us, 5.1 TB/s of
-// the 6.8 of a copy; two abreast 82, CTAs of 256 threads 84).  At that size the
-// issue slots are 75 % used (packed arithmetic took 5 us off); the smallest calls
-// are a launch and three dependent loads.
+// the 6.8 of a copy; two abreast 82, CTAs of 256 threads 84).  Half of
+// the issue slots are used then (packed arithmetic took 5 us off) and loads are
+// what warps wait for; the smallest calls are a launch and three dependent loads.
 #include "attention.cuh"
 #include "delta.cuh"
 

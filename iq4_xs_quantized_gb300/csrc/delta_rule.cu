@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) delta_row_kernel(const DeltaRu
 // CTAs stay for several items (a head's columns of a sequence): S comes to shared
 // memory by TMA, goes to registers, and the next item's is on its way meanwhile.
 // (CTAs of one item each load together and then compute together: 16.3 us where
-// this takes 12.7 for 12 trees of 8 of 48 heads of 128 x 128, 40 MB: 3.1 TB/s; FFMA instead
+// this takes 12.7 for 12 trees of 8 of 48 heads of 128 x 128 with the states in L2, 16.4 from
+// HBM, 40 MB: 2.4 TB/s; FFMA instead
 // of the MMA 17.8.)  What bounds it: an item's chain of six steps between barriers,
 // about 2.9 us, two CTAs an SM; S in two parts is a third of its instructions.
 constexpr int kFewPad = 8;  // floats behind a row in shared memory: rows an operand reads together on all banks

@@ -10,8 +10,8 @@
 //
 // Few bytes are read (a row or two of probabilities a sequence): what it takes
 // is the chain of launch, tree, probabilities, sums, and the draw's search: 12 trees of 8
-// over 131,073 tokens 11.7 us, a chain of four with a drafter's probabilities over
-// 32,000 10.0.  (CTAs of 256, 512 and 1,024 threads: 13.1, 12.3 and 12.4 before the loads
+// over 131,073 tokens 11.1 us (19 with cold caches), a chain of four with a drafter's
+// probabilities over 32,000 10.2.  (CTAs of 256, 512 and 1,024 threads: 13.1, 12.3 and 12.4 before the loads
 // were grouped.)
 #include <type_traits>
 

@@ -236,3 +236,40 @@ def test_a_batch_on_the_host_is_refused():
                      lambda: B.iq4xs_verify_drafts(probs, tokens, rand, rand[:1], i32([[0, 0]]), i32([0]), i32([0]), host)):
             with pytest.raises(ValueError, match="current CUDA device"):
                 call()
+
+
+def test_a_graph_follows_the_offsets():
+    """Which sequences are long is read when the kernels run: a captured call with
+    a long one among short ones, replayed after the offsets have changed."""
+    shapes = ([1, 70, 1, 3], [3, 1, 1, 70], [70, 5, 0, 0], [18, 19, 19, 19])
+    for max_rows in (70, None):
+        bt = Batch([4, 4, 4, 0], shapes[0], 2, 40, seed=8)
+        ops, start = bt.operands(), bt.s.clone()
+        out = torch.full((bt.rows, bt.hv * bt.dv), float("nan"), device="cuda")
+
+        def call():
+            B.iq4xs_delta_rule(*ops, 0.1, out, bt.state, 0, bt.batch, max_rows=max_rows)
+
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            call()
+        for new in shapes:
+            bt.batch.row_offsets.copy_(i32(np.concatenate([[0], np.cumsum(new)])))
+            ends = []
+            for run in (call, graph.replay):
+                bt.s.copy_(start)
+                out.fill_(float("nan"))
+                run()
+                torch.cuda.synchronize()
+                ends.append((out.clone(), bt.s.clone()))
+            rows = sum(new)
+            assert torch.isfinite(ends[0][0][:rows]).all()
+            for a, b in zip(*ends):
+                assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+            other = Batch([4, 4, 4, 0], new, 2, 40, seed=8)  # (the same slots)
+            other.s.copy_(start)
+            want = rule_ref(other, *ops, 0.1, chains(new))
+            D.near(ends[0][0][:rows].unflatten(1, (bt.hv, bt.dv)), want[0][:rows], want[1][:rows], "out")
+    assert B.iq4xs_last_device_error() == 0
