@@ -6,7 +6,8 @@
 // by a cluster of CTAs that keep their parts in registers and exchange maximum
 // and sum through distributed shared memory, and written once: HBM bounds it.
 // 96 rows of 131,073: 23.3 us from HBM, 4.3 TB/s of the 6.8 of a copy (18.0 with the logits in
-// L2): all rows are read, then all are written.  One row of 32,000: 3.7 us, a launch, the
+// L2): all rows are read, then all are written (CTAs of 256 threads 24.9 to 34.8, of 1,024
+// 30 and more; two and eight units abreast 24.5 and 29.4).  One row of 32,000: 3.7 us, a launch, the
 // loads and the exchange.
 // Rows start at any multiple of four bytes; a part's units of four values lie on
 // 16-byte boundaries of the logits, cut at the row's ends.
