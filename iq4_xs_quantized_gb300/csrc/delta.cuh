@@ -19,12 +19,21 @@ struct DeltaView {
 constexpr int kConvTaps = 4;
 constexpr int kDeltaTreeRows = 64;  // rows of a sequence whose state stays
 
-// The slot of sequence s; -1 (recorded) where it is out of range.
-__device__ __forceinline__ int delta_slot(const DeltaView& d, int s, int* err) {
-    const int slot = d.slot_of != nullptr ? d.slot_of[s] : s;
-    if (slot >= 0 && slot < d.slots) return slot;
-    data_error(err, kDataSlot);
-    return -1;
+// Sequence s: its rows (n = 0 where the offsets are out of order or of range),
+// its length and slot (-1 where out of range).  All four values are asked for
+// before the first is looked at: a look that may record keeps later loads behind it.
+struct DeltaSequence {
+    int first, n, len, slot;
+};
+__device__ __forceinline__ DeltaSequence delta_sequence(const BatchView& b, const DeltaView& d, int s, int rows, int* err) {
+    const int32_t* const at_slot = d.slot_of != nullptr ? d.slot_of + s : b.lens + s;
+    const int first = b.row_offsets[s], end = b.row_offsets[s + 1], len = b.lens[s], mapped = *at_slot;
+    const int slot = d.slot_of != nullptr ? mapped : s;
+    const bool rows_fit = first >= 0 && end >= first && end <= rows, slot_fits = slot >= 0 && slot < d.slots;
+    if (!rows_fit) data_error(err, kDataOffsets);
+    if (len < 0) data_error(err, kDataLens);
+    if (!slot_fits) data_error(err, kDataSlot);
+    return {first, rows_fit ? end - first : 0, max(len, -1), slot_fits ? slot : -1};
 }
 
 // Eight 16-bit values -> fp32.

@@ -292,9 +292,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     griddep_wait();
     const Bc bc = bc_open(err);
     const int head = blockIdx.x % d.heads, s = blockIdx.x / d.heads;
-    int row0;
-    const int n = batch_rows(b, s, p.rows, &row0, err);
-    const int len = batch_len(b, s, err), slot = delta_slot(d, s, err);
+    const DeltaSequence seq = delta_sequence(b, d, s, p.rows, err);
+    const int row0 = seq.first, n = seq.n, len = seq.len, slot = seq.slot;
     if (n <= p.few_rows || len < 0 || slot < 0) return;
     if (n > p.max_rows) {
         if (tid == 0) data_error(err, kDataCount);

@@ -43,9 +43,9 @@ __global__ void __launch_bounds__(kCommitThreads, 5) delta_commit_kernel(const C
     constexpr int kSlices = DV / VS;
     const int parts = d.heads * kSlices + p.conv_parts, tid = threadIdx.x;
     const int part = blockIdx.x % parts, s = blockIdx.x / parts % b.sequences, layer = blockIdx.x / parts / b.sequences;
-    int row0;
-    const int n = batch_rows(b, s, p.rows, &row0, err);
-    const int len = batch_len(b, s, err), slot = delta_slot(d, s, err), count = p.accepted[s];
+    const int count = p.accepted[s];
+    const DeltaSequence seq = delta_sequence(b, d, s, p.rows, err);
+    const int row0 = seq.first, n = seq.n, len = seq.len, slot = seq.slot;
     if (len < 0 || slot < 0) return;
     if (count < 0 || count > p.path_width || count > n) {
         if (tid == 0) data_error(err, kDataPath);

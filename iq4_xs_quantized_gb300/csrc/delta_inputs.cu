@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(kInputThreads, 6) delta_inputs_kernel(const In
         if (begun != 0xffffffffu) break;
     }
     if (s < 0) return;
-    int first;
-    const int n = batch_rows(b, s, p.rows, &first, err), len = batch_len(b, s, err), slot = delta_slot(d, s, err);
+    const DeltaSequence seq = delta_sequence(b, d, s, p.rows, err);
+    const int first = seq.first, n = seq.n, len = seq.len, slot = seq.slot;
     const int t0 = (at - (first / p.run + s)) * p.run, t1 = min(n, t0 + p.run);
     if (len < 0 || slot < 0 || t0 < 0 || t0 >= n) return;
 

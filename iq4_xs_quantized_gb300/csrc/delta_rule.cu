@@ -50,9 +50,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) delta_row_kernel(const DeltaRu
     const int slice = blockIdx.x % slices, head = blockIdx.x / slices % d.heads, s = blockIdx.x / slices / d.heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int col = tid % kCols * 4, group = tid / kCols;
-    int row0;
-    const int n = batch_rows(b, s, p.rows, &row0, err);
-    const int len = batch_len(b, s, err), slot = delta_slot(d, s, err);
+    const DeltaSequence seq = delta_sequence(b, d, s, p.rows, err);
+    const int row0 = seq.first, n = seq.n, len = seq.len, slot = seq.slot;
     if (n == 0 || len < 0 || slot < 0) return;
     if (n > p.max_rows) {
         if (tid == 0) data_error(err, kDataCount);
@@ -245,9 +244,11 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
         const int s = item / slices / d.heads;
         it.head = item / slices % d.heads;
         it.v0 = item % slices * VS;
-        const int n = batch_rows(b, s, p.rows, &it.row0, err);
-        it.len = batch_len(b, s, err);
-        it.slot = delta_slot(d, s, err);
+        const DeltaSequence seq = delta_sequence(b, d, s, p.rows, err);
+        const int n = seq.n;
+        it.row0 = seq.first;
+        it.len = seq.len;
+        it.slot = seq.slot;
         if (n > p.max_rows && tid == 0) data_error(err, kDataCount);
         it.n = it.len < 0 || it.slot < 0 || n > p.max_rows || n > p.few_rows ? 0 : n;
         return it;
@@ -266,7 +267,6 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
     uint32_t phase = 0;
     bool lost = false;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const FewItem next = look(item + gridDim.x);
         const int n = now.n, row0 = now.row0, len = now.len, slot = now.slot, head = now.head, v0 = now.v0;
         const int key_head = head / (d.heads / d.key_heads);
         // A block's rows: asked for before the next item's state, behind which they would wait.
@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
             }
         };
         ask(0);
+        const FewItem next = look(item + gridDim.x);  // (its loads beside this one's state)
         // Element e of step i: key channel 8 i + 2 t4 + (e & 1), column 16 warp + g + 8 (e >> 1).
         float S[kSteps][4];
         if (n > 0 && len > 0) {
@@ -318,8 +319,19 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
 #pragma unroll
                 for (int e = 0; e < 4; ++e) S[i][e] = 0.f;
         }
-        if (__syncthreads_or(lost)) break;  // (all leave together; S has been read, the last item is done)
-        if (tid == 0) fetch(next);
+        if (__syncthreads_or(lost)) break;  // (all leave together; the last item is done)
+        if (tid == 0) {
+            // The next state: to L2 now, to shared memory once a product has used all of
+            // this one (a barrier alone does not wait for loads on their way to
+            // registers, and the copy does not queue behind them).
+            if (n == 0) fetch(next);
+            else if (next.n > 0 && next.len > 0)
+#pragma unroll
+                for (int i = 0; i < C::kBoxes; ++i)
+                    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(&map_s),
+                                 "r"(next.v0 + 32 * i), "r"(next.head * DK), "r"(next.slot)
+                                 : "memory");
+        }
         if (tid < 3 * TB && next.n > 0) {  // the next item's rows on their way to L2
             const int t = tid / 3, which = tid % 3, nk = next.head / (d.heads / d.key_heads) * DK;
             if (t < next.n) {
@@ -416,6 +428,7 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
                 }
             }
             __syncthreads();
+            if (t0 == 0 && tid == 0) fetch(next);
             // u, a column a thread.  (A row takes the rows that it comes from, and no
             // others: 0 times NaN is none of its.)
             if (tid < VS) {

@@ -273,3 +273,21 @@ def test_a_graph_follows_the_offsets():
             want = rule_ref(other, *ops, 0.1, chains(new))
             D.near(ends[0][0][:rows].unflatten(1, (bt.hv, bt.dv)), want[0][:rows], want[1][:rows], "out")
     assert B.iq4xs_last_device_error() == 0
+
+
+@pytest.mark.parametrize("new,keep", [([2] * 9 + [8], False), ([8] * 10, True), ([12] * 10, True)])
+def test_rule_again_and_again(new, keep):
+    """Several items a CTA, their states in L2, so that a copy follows its order
+    closely: it must not come before the last state has been read."""
+    bt = Batch([5] * len(new), new, 16, 48, dtype=torch.bfloat16, seed=1)
+    ops, start = bt.operands(), bt.s.clone()
+    out = torch.empty(bt.rows, bt.hv * bt.dv, device="cuda")
+    u = torch.empty(bt.rows, bt.hv, bt.dv, device="cuda") if keep else None
+    first = differ = None
+    for _ in range(400):
+        bt.s.copy_(start)
+        B.iq4xs_delta_rule(*ops, 0.1, out, bt.state, 0, bt.batch, u=u, max_rows=max(new))
+        if first is None:
+            first, differ = (out.clone(), bt.s.clone()), torch.zeros((), device="cuda")
+        differ += (out != first[0]).any() | (bt.s.view(torch.int32) != first[1].view(torch.int32)).any()
+    assert differ.item() == 0 and B.iq4xs_last_device_error() == 0
