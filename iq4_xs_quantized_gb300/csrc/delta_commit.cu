@@ -6,10 +6,10 @@
 // path's last three.  The rows' k and u are small beside S, which is read once
 // and written once: HBM bounds it.  A CTA takes 64 columns of one head of one
 // sequence and layer, S in registers; paths of more than kPath rows go in runs.
-// 24 layers x 12 sequences x 48 heads of 128 x 128, paths of 5: 311 us, 6.1 TB/s, 90 % of a
+// 24 layers x 12 sequences x 48 heads of 128 x 128, paths of 5: 306 to 311 us, 6.1 TB/s, 90 % of a
 // copy.  Five CTAs an SM keep enough loads in flight (four: 351 us, three 353; six
 // spill, 367; slices of 32 columns 381 and more: rows of 128 bytes).  One sequence, four
-// layers: 4.9 us, a launch and the chain accepted - path - gates - S.
+// layers: 4.7 us, a launch and the chain accepted - path - gates - S.
 #include "delta.cuh"
 
 namespace iq4xs {

@@ -13,7 +13,7 @@
 //
 // A CTA holds a head's S, or a slice of its columns, in registers for all of a
 // sequence's rows: HBM reads it once and, where it moves on, writes it once,
-// which bounds single rows (45 sequences of 48 heads of 128 x 128, 283 MB: 45.6 us, 6.2 TB/s, 92 %
+// which bounds single rows (45 sequences of 48 heads of 128 x 128, 283 MB: 45.1 us, 6.3 TB/s, 92 %
 // of a copy; one sequence 3.2 us, of which a launch and three loads that wait for one another
 // are most).
 #include "attention.cuh"
@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) delta_row_kernel(const DeltaRu
 // CTAs stay for several items (a head's columns of a sequence): S comes to shared
 // memory by TMA, goes to registers, and the next item's is on its way meanwhile.
 // (CTAs of one item each load together and then compute together: 16.3 us where
-// this takes 12.7 for 12 trees of 8 of 48 heads of 128 x 128 with the states in L2, 16.4 from
-// HBM, 40 MB: 2.4 TB/s; FFMA instead
+// took 15.1 for 12 trees of 8 of 48 heads of 128 x 128 with the states in L2; 12.2 now, 15.8 from
+// HBM, 40 MB: 2.5 TB/s; FFMA instead
 // of the MMA 17.8.)  What bounds it: an item's chain of six steps between barriers,
 // about 2.9 us, two CTAs an SM; S in two parts is a third of its instructions.
 constexpr int kFewPad = 8;  // floats behind a row in shared memory: rows an operand reads together on all banks
