@@ -14,7 +14,7 @@
 // A CTA holds a head's S, or a slice of its columns, in registers for all of a
 // sequence's rows: HBM reads it once and, where it moves on, writes it once,
 // which bounds single rows (45 sequences of 48 heads of 128 x 128, 283 MB: 45.1 us, 6.3 TB/s, 92 %
-// of a copy; one sequence 3.2 us, of which a launch and three loads that wait for one another
+// of a copy; one sequence 3.2 us, of which a launch and two loads that wait for one another
 // are most).
 #include "attention.cuh"
 #include "delta.cuh"
