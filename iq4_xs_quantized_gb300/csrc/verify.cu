@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         }
         if (total == 0 && !plain) {  // nothing is left: from the row itself
             plain = true;
+            cluster_sync();  // (sums of before: no other barrier keeps the next order from overtaking the looks at this one)
             continue;
         }
         if (total == 0) {
