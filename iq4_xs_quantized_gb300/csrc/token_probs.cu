@@ -154,6 +154,7 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
     for (int w = 0; w < kProbWarps; ++w) sum += sums[w];
     if (ranks > 1) {
         if (tid == 0) mine = make_uint4(__float_as_uint(top), (uint32_t)place, __float_as_uint(sum), 0);
+        __syncwarp();  // (the barrier wants warps whole)
         cluster_arrive_release();
         cluster_wait();
         for (int r = 0; r < ranks; ++r) {
@@ -206,7 +207,10 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
             }
         }
     }
-    if (ranks > 1) cluster_wait();
+    if (ranks > 1) {
+        __syncwarp();
+        cluster_wait();
+    }
 }
 
 template <bool kHold>

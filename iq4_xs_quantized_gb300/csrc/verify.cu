@@ -59,6 +59,7 @@ struct VerifyShared {
     unsigned long long parts[kVerifyCluster];      // the CTAs' sums
     unsigned long long runs[kMaxRuns];             // this CTA's, run by run
     Order order;
+    int count;  // rows accepted
 };
 
 __device__ __forceinline__ float in_unit(float p) { return p > 0.f ? fminf(p, 1.f) : 0.f; }  // (NaN: 0)
@@ -114,6 +115,7 @@ __device__ __forceinline__ int ld_rank(const int* p, int rank) {
     return v;
 }
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();  // (the barrier wants warps whole, and threads of their own have been at work)
     cluster_arrive_release();
     cluster_wait();
 }
@@ -240,6 +242,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     float draw = 0.f;
     if (bc_global(bc, p.draw_u + s, 4, p.draw_u, 4 * (int64_t)b.sequences, kBcVerifyRow)) draw = p.draw_u[s];
     bool plain = false;
+    __syncwarp();
     cluster_wait();  // (every CTA has begun: its shared memory may be written)
     for (;;) {
         if (rank == 0 && tid == 0) {
@@ -398,14 +401,14 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     }
     if (rank == 0) {
         if (tid == 0) {
-            sh.order.node = n > 0 ? count : 0;
+            sh.count = n > 0 ? count : 0;
             if (bc_global(bc, p.accepted + s, 4, p.accepted, 4 * (int64_t)b.sequences, kBcVerifyOut))
                 p.accepted[s] = n > 0 ? count : 0;
             if (n > 0 && bc_global(bc, path, 4, p.paths, path_extent, kBcVerifyOut)) path[0] = 0;
             if (n == 0 && bc_global(bc, p.next + s, 4, p.next, 4 * (int64_t)b.sequences, kBcVerifyOut)) p.next[s] = -1;
         }
         __syncthreads();
-        for (int i = sh.order.node + tid; i < p.path_width; i += kVerifyThreads)
+        for (int i = sh.count + tid; i < p.path_width; i += kVerifyThreads)
             if (bc_global(bc, path + i, 4, p.paths, path_extent, kBcVerifyOut)) path[i] = 0;
     }
 }
