@@ -827,11 +827,14 @@ int iq4xs_delta_inputs(const iq4xs_delta_inputs_args* args, const iq4xs_delta_st
  *   u         fp32 [rows][heads][value_dim], 16-byte aligned, or NULL.
  *   max_rows  no sequence has more rows (one that does is skipped,
  *             IQ4XS_ERR_DATA); 0: not known.
- * Rows of no sequence are not written.  A row has no influence on rows that do
- * not come from it, whatever it holds.  S, sums and statistics are fp32; where
- * several rows go through the tensor cores, what has more than 16 bits goes in
- * two parts (2^-22 of a value, or 2^-38 of the largest of its column or row,
- * whichever is more).  Results are the same from run to run.
+ * Rows of no sequence are not written.  NaN, infinities and products beyond
+ * fp32's range reach the rows that come from theirs, which may be NaN, and no
+ * others.  S, sums and statistics are fp32; where several rows go through the
+ * tensor cores, what has more than 16 bits goes in two parts (2^-22 of a value,
+ * or 2^-38 of the largest of its column or row, whichever is more: a sequence of
+ * more than 16 rows goes in blocks of up to 64, whose rows share a column, so that
+ * finite values 2^14 and more times another row's cost it bits).  Results are the
+ * same from run to run.
  * Speed: the kernel's form follows rows / sequences and max_rows: give it (a long
  * sequence among short ones then goes in a launch of its own).
  * 1 <= rows <= 32768.

@@ -38,6 +38,9 @@
 //
 // A row that holds NaN or infinities (or meets them in S) gives zeros to the
 // products and is marked; u and o of rows that come from it are made NaN after them.
+// So is a row whose A or T passes fp32's range (keys of norms whose product is 2^127):
+// T is then made again, column by column over the rows that come from one another
+// alone, for 0 times infinity in a row of another branch is NaN.
 #include <type_traits>
 
 #include "attention.cuh"
@@ -230,6 +233,29 @@ __device__ __forceinline__ uint32_t hide(float2 (&x)[16], const Gates& gt, int f
         if (bits >> (2 * i + 1) & 1) x[i].y = 0.f;
     }
     return bits;
+}
+
+__device__ __forceinline__ float max3_nan(float top, float a, float b) {  // NaN where one is
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return top;
+}
+// A column of T again, from the rows that come from one another alone (and the
+// zeros above the diagonal that the substitution wrote).  What is not finite
+// becomes 0, its row is marked.
+__device__ __noinline__ void careful_column(const float* A, float* T, const unsigned long long* seen, unsigned long long* odd,
+                                            int col) {
+#pragma unroll 1
+    for (int i = col & ~15; i < kRows; ++i) {
+        float x = i == col ? 1.f : 0.f;
+#pragma unroll 1
+        for (int j = col; j < i; ++j)
+            if (seen[i] >> j & 1) x = fmaf(-A[i * kPitch + j], T[j * kPitch + col], x);
+        if (odd_value(x)) {
+            atomicOr(odd, 1ull << i);
+            x = 0.f;
+        }
+        T[i * kPitch + col] = x;
+    }
 }
 
 // A tile (16 rows from `rows`, 8 columns from `cols`) of an N x N block below T's
@@ -593,23 +619,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             prep_sync();
             below_tile<32>(A, Ts, X, 0, tile / 4 * 16, tile % 4 * 8, lane, 1);
             prep_sync();
-            {
-                // A quarter of a row a thread.
+            // T's parts, a quarter of a row a thread; once more where T was not finite.
+            bool stop = false;
+#pragma unroll 1
+            for (bool again = false;; again = true) {
                 const int row = id / 4, quarter = id % 4;
                 float most = 0.f;
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
                     const float4 w = *reinterpret_cast<const float4*>(Ts + row * kPitch + 16 * quarter + j);
-                    most = max3(max3(most, w.x, w.y), w.z, w.w);
+                    most = max3_nan(max3_nan(most, w.x, w.y), w.z, w.w);
                 }
+                const bool odd = odd_value(most);
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
                 const float2 f = fit(most);
                 if (quarter == 0) gt.ct[row] = f.y;
                 put_parts(Ts + row * kPitch, 2 * quarter, 2 * quarter + 2, f.x, base + C::kT + buf * 2 * C::kPartBytes, row);
+                fence_proxy_async_smem();
+                if (!any_of<6, kPrepThreads>(lost || odd) || again) break;
+                stop = any_of<6, kPrepThreads>(lost);
+                if (stop) break;
+                if (id < kRows) careful_column(A, Ts, seen_at, odd_at, id);
+                prep_sync();
+                if (id == 0) gt.odd = *odd_at;
             }
-            fence_proxy_async_smem();
-            if (any_of<6, kPrepThreads>(lost)) break;
+            if (stop) break;
             mbar_arrive(full + buf);
         }
         // Tensor memory is given back only when every product is done.
