@@ -66,8 +66,13 @@ __global__ void __launch_bounds__(kCommitThreads, 5) delta_commit_kernel(const C
             S[i] = __ldcs(reinterpret_cast<const float4*>(at_s + i * DV));
     }
     const int32_t* path = p.paths + (int64_t)s * p.path_width;
+    const int64_t path_extent = 4 * (int64_t)b.sequences * p.path_width;
     bool bad = false;
     for (int i = tid; i < count; i += kCommitThreads) {
+        if (!bc_global(bc, path + i, 4, p.paths, path_extent, kBcDeltaPath)) {
+            bad = true;
+            continue;
+        }
         const int t = path[i];
         bad |= t < 0 || t >= n || (i > 0 && t <= path[i - 1]);
     }

@@ -95,8 +95,11 @@ __global__ void __launch_bounds__(kInputThreads, 6) delta_inputs_kernel(const In
             if (!bc_global(bc, a, 4, p.a, 4 * ((p.rows - 1) * p.a_stride + d.heads), kBcDeltaGate) ||
                 !bc_global(bc, c, 4, p.b, 4 * ((p.rows - 1) * p.b_stride + d.heads), kBcDeltaGate))
                 continue;
-            const float z = *a + p.dt_bias[h];
-            const float g = -expf(p.a_log[h]) * (fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))));
+            float rate = 0.f, bias = 0.f;
+            if (bc_global(bc, p.a_log + h, 4, p.a_log, 4 * (int64_t)d.heads, kBcDeltaGate)) rate = p.a_log[h];
+            if (bc_global(bc, p.dt_bias + h, 4, p.dt_bias, 4 * (int64_t)d.heads, kBcDeltaGate)) bias = p.dt_bias[h];
+            const float z = *a + bias;
+            const float g = -expf(rate) * (fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))));
             const int64_t to = (int64_t)row * d.heads + h;
             if (bc_global(bc, p.g + to, 4, p.g, extent, kBcDeltaGate)) p.g[to] = g;
             if (bc_global(bc, p.beta + to, 4, p.beta, extent, kBcDeltaGate)) p.beta[to] = 1.f / (1.f + expf(-*c));
