@@ -168,12 +168,17 @@ __global__ void __launch_bounds__(kRowThreads, 4) delta_row_kernel(const DeltaRu
 // left operand and lies in the layout that the state's update gives as a result
 // (key channels 2 t and 2 t + 1 of eight stand for the operand's t and t + 4), so
 // it stays where it is.  K and Q of 16 bits are exact in tf32; S and u go in two
-// parts, a value without its last 13 bits and the remainder (22 bits together);
-// sums are joined, and S moved on, by fp32 arithmetic that rounds.
+// parts, a value without its last 13 bits and the remainder, of which the MMA takes
+// 11 (22 bits together); sums are joined, and S moved on, by fp32 arithmetic that
+// rounds.  12 trees of 8 are off by 5.5e-7 of the largest output (4.1e-7 of their norm),
+// fp32 throughout by 2.8e-7 (1.7e-7): most of it is the MMA's cut-off sums over 16
+// steps, a quarter the remainder's last bits.  Two sums in turn and a rounded remainder
+// take it to 2.7e-7 (2.0e-7), at 13.9 us instead of 12.3 (48 chains of 16 111 instead
+// of 103), a sum of each step joined by itself to 3.3e-7 (1.9e-7) at 13.7: not taken.
 //
 // CTAs stay for several items (a head's columns of a sequence): S comes to shared
 // memory by TMA, goes to registers, and the next item's is on its way meanwhile.
-// (CTAs of one item each load together and then compute together: 16.3 us where
+// (CTAs of one item each load together and then compute together: 16.3 us where these
 // took 15.1 for 12 trees of 8 of 48 heads of 128 x 128 with the states in L2; 12.2 now, 15.8 from
 // HBM, 40 MB: 2.5 TB/s; FFMA instead
 // of the MMA 17.8.)  What bounds it: an item's chain of six steps between barriers,
@@ -217,6 +222,7 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
                      const __grid_constant__ DeltaView d, const __grid_constant__ BatchView b, int items, int* err) {
     using C = FewShape<DK, kWarps, TB>;
     constexpr int kSteps = DK / 8, VS = C::VS, kTiles = C::kTiles;
+    constexpr bool kMoves = TB == 8;  // (blocks of 16 are for trees, whose state stays)
     extern __shared__ __align__(1024) float sm[];
     uint32_t* const seen = reinterpret_cast<uint32_t*>(sm + C::kSeen);
     uint64_t* const landed = reinterpret_cast<uint64_t*>(sm + C::kBar);
@@ -481,7 +487,7 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
                     }
                 }
             }
-            if (p.u == nullptr) {
+            if (kMoves && p.u == nullptr) {
                 // S: columns by key channels, the rows between
                 uint32_t hi[kTiles][4], lo[kTiles][4];
 #pragma unroll
@@ -506,8 +512,9 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
                     for (int e = 0; e < 4; ++e) S[i][e] = fmaf(decay, S[i][e], add[e]);
                 }
             }
+            if (!kMoves) break;  // (one block: no loop that S's parts could be kept over)
         }
-        if (n > 0 && p.u == nullptr) {
+        if (kMoves && n > 0 && p.u == nullptr) {
             float* const at_s = d.s + p.s_offset + slot * d.s_slot_stride + ((int64_t)head * DK + 2 * t4) * d.value_dim + v0 + 16 * warp + g;
 #pragma unroll
             for (int i = 0; i < kSteps; ++i)
