@@ -11,6 +11,7 @@
 // loads and the exchange.
 // Rows start at any multiple of four bytes; a part's units of four values lie on
 // 16-byte boundaries of the logits, cut at the row's ends.
+#include "attention.cuh"
 #include "delta.cuh"
 
 namespace iq4xs {
@@ -68,9 +69,20 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
             }
         }
     };
-    // (1 / T within fp32's range: equal values then give 1 at any T)
-    const float c = fminf(fmaxf(1.44269504088896340736f / t, 1.17549435e-38f), 3.40282347e38f);
     float x[kHold ? kProbUnits : 1][4];
+    if constexpr (kHold) {
+#pragma unroll
+        for (int k = 0; k < kProbUnits; ++k) load(u0 + k * kProbThreads + tid, x[k]);
+    }
+    // e^(d / T), d not above 0, with one rounding of the exponent: log2(e) / T, within
+    // fp32's range (equal values then give 1 at any T), as a number 2^-20 below it and
+    // what that lacks, above 0 so that -inf stays -inf.
+    float inverse;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(inverse) : "f"(t));
+    const float rate = 1.4426936f * inverse, c = fminf(fmaxf(rate, 1.17549435e-38f), 3.40282347e38f);
+    const float lack = (fmaf(-c, t, 1.44269502f) + 1.9259630e-8f) * inverse;
+    const float c2 = c == rate && lack > 0.f ? lack : 0x1p-149f;
+    auto power = [&](float d) { return exp2_of(fmaf(d, c, d * c2)); };
     float top = -INFINITY, sum = 0.f;
     int place = INT32_MAX;
     auto look = [&](const float (&v)[4], int u) {
@@ -92,15 +104,17 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
         top = fmaxf(top, other);
     };
     float own = -INFINITY;  // what a thread's weights (or sum) are taken against
-    // e^((l - own) / T)
     auto weigh = [&](float (&v)[4]) {
         const float shift = own == -INFINITY ? 0.f : own;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = exp2_of((v[e] - shift) * c);
+        for (int e = 0; e < 4; e += 2) {
+            const float2 d = add2(make_float2(v[e], v[e + 1]), make_float2(-shift, -shift));
+            const float2 z = fma2(d, make_float2(c, c), fma2(d, make_float2(c2, c2), make_float2(-0.f, -0.f)));
+            v[e] = exp2_of(z.x);
+            v[e + 1] = exp2_of(z.y);
+        }
     };
     if constexpr (kHold) {
-#pragma unroll
-        for (int k = 0; k < kProbUnits; ++k) load(u0 + k * kProbThreads + tid, x[k]);
 #pragma unroll
         for (int k = 0; k < kProbUnits; ++k) look(x[k], u0 + k * kProbThreads + tid);
     } else {
@@ -111,7 +125,7 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) look(v[k], u + k * kProbThreads);
             if (!kGreedy) {  // a running sum
-                sum = top > own && own != -INFINITY ? sum * exp2_of((own - top) * c) : sum;
+                sum = top > own && own != -INFINITY ? sum * power(own - top) : sum;
                 own = top;
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
@@ -142,7 +156,7 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
                 sum += (x[k][0] + x[k][1]) + (x[k][2] + x[k][3]);
             }
         } else {
-            sum = own == -INFINITY ? sum : sum * exp2_of((own - top) * c);
+            sum = own == -INFINITY ? sum : sum * power(own - top);
             own = top;
         }
     }
@@ -165,12 +179,12 @@ __device__ __forceinline__ void row_probs(const float* logits, const float* in, 
         for (int r = 0; r < ranks; ++r) {
             const uint4 part = ld_rank(&mine, r);
             const float of = __uint_as_float(part.z), its = __uint_as_float(part.x);
-            sum += kGreedy ? of : its == -INFINITY ? of : of * exp2_of((its - top) * c);
+            sum += kGreedy ? of : its == -INFINITY ? of : of * power(its - top);
         }
         cluster_arrive_release();  // (no CTA ends while another reads its part)
     }
     // A weight times this is the probability (a part without any: zeros, unless the row is NaN).
-    const float factor = own == -INFINITY ? sum * 0.f : own == top ? 1.f / sum : exp2_of((own - top) * c) / sum;
+    const float factor = own == -INFINITY ? sum * 0.f : own == top ? 1.f / sum : power(own - top) / sum;
     auto put = [&](const float (&v)[4], int u) {
         const int i0 = 4 * u - skew;
         float y[4];
