@@ -833,10 +833,12 @@ int iq4xs_delta_inputs(const iq4xs_delta_inputs_args* args, const iq4xs_delta_st
  * tensor cores, what has more than 16 bits goes in two parts (2^-22 of a value,
  * or 2^-38 of the largest of its column or row, whichever is more: a sequence of
  * more than 16 rows goes in blocks of up to 64, whose rows share a column, so that
- * finite values 2^14 and more times another row's cost it bits).  Results are the
+ * finite values 2^16 and more times another row's cost it bits).  Results are the
  * same from run to run.
- * Speed: the kernel's form follows rows / sequences and max_rows: give it (a long
- * sequence among short ones then goes in a launch of its own).
+ * Speed: the kernel's form follows rows / sequences and max_rows: give it.  Not
+ * known (0), a batch with u is also looked through by a launch for sequences of more
+ * than 16 rows, single rows go in blocks, and a long chain among short ones goes in
+ * blocks of 8 to its end instead of a launch of its own.
  * 1 <= rows <= 32768.
  */
 typedef struct {
@@ -912,15 +914,19 @@ int iq4xs_token_probs(const float* logits, int64_t logits_stride, int64_t rows, 
  * row reached, n, are tried in rising order, r = probs[n] and m = 1 at first:
  *   child c is accepted if accept_u[c] m q(x) < r(x), x = tokens[c], and n = c;
  *   else r <- max(r - m q, 0), m <- sum r.
- * q = draft_probs[n], the distribution that n's children were drawn from; or,
+ * q = draft_probs[n], the distribution that n's children were drawn from, each by
+ * itself (the same token may come twice; children drawn without replacement come
+ * from other distributions, and what is accepted then does not follow probs); or,
  * with draft_probs NULL (drafts that were not drawn), q(i) = [i = x], where the
  * sum is 1 less the tokens rejected.  When no child is left, next[s] is the
  * first i with r_0 + ... + r_i > draw_u[s] sum r (sum r = 0: from probs[n]; that
- * 0 too: -1); the same when the path is full.  Values are taken as exact and sums kept to 2^-61, so that results
- * do not depend on timing.  A probability is taken as within 0..1 (NaN: 0).
+ * 0 too: -1); the same when the path is full.  Values are taken as exact and sums
+ * kept to 2^-61, so that results do not depend on timing.  A probability is taken as
+ * within 0..1 (NaN: 0), and a row's are to sum to less than 4 (a distribution's
+ * sum to about 1): of more, the tokens accepted and drawn mean nothing.
  *   probs, draft_probs  fp32 [rows][vocab], rows probs_stride, draft_stride apart
  *   tokens      int32 [rows]; one outside 0..vocab-1 is never accepted
- *   accept_u    fp32 [rows];  draw_u  fp32 [sequences], in [0, 1)
+ *   accept_u    fp32 [rows];  draw_u  fp32 [sequences]; both in [0, 1)
  *   paths       int32 [sequences][path_width]: the rows accepted, row 0 first, as
  *               iq4xs_cache_commit takes them; zeros behind.  accepted int32
  *               [sequences] their number, at most path_width.

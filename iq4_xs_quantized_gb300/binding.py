@@ -792,7 +792,9 @@ def iq4xs_delta_rule(q, k, v, g, beta, scale: float, out, state: DeltaState, lay
     Without u the rows are chains and the layer's state moves on over them; with
     u (fp32 [M, Hv, Dv], written: what iq4xs_delta_commit takes) the state stays
     and every row starts from its parent's (tree_mask; None: a chain), at most 64
-    rows a sequence.  max_rows: no sequence has more rows (None: not known)."""
+    rows a sequence.  max_rows: no sequence has more rows (None: not known, which
+    costs time: drafted trees then take a second launch, a long chain among short
+    ones blocks of 8 rows)."""
     fn, st = "iq4xs_delta_rule", state
     M = q.shape[0]
     if st.mapped is not None:
@@ -906,7 +908,8 @@ def iq4xs_verify_drafts(probs, tokens, accept_u, draw_u, paths, accepted, next_t
     paths int32 [B, width] and accepted int32 [B] as iq4xs_cache_commit takes
     them, and next_token int32 [B], drawn by draw_u fp32 [B] from what is left.
     draft_probs fp32 [M, V]: row r's distribution that its children were drawn
-    from (None: they were not drawn)."""
+    from, each by itself and with replacement (None: they were not drawn).  Random
+    numbers are in [0, 1), a row's probabilities sum to less than 4."""
     fn, f32, i32, B = "iq4xs_verify_drafts", torch.float32, torch.int32, batch.sequences
     shape = probs.shape
     M, V = shape
