@@ -102,3 +102,24 @@ def test_rule_every_form_keeps_tree_rows_apart():
         clear = [t for t in range(bt.rows) if t % 4 < 2]
         near(out[clear], want[0][clear], want[1][clear], "out")
         assert not torch.isfinite(u[wide[1::2]]).any()
+
+
+@pytest.mark.parametrize("dk,dv", ((128, 128), (64, 64)))
+def test_rule_wide_keys_in_a_chain(dk, dv):
+    """Chains of several blocks whose state moves on: what comes before the block is as ever, what
+    comes from the pair is not finite, the other sequence is untouched, and nothing waits for long."""
+    new = [150, 130]
+    bt = Batch([3, 4], new, 2, 4, dk, dv, torch.bfloat16, seed=dk)
+    q, k, v, g, beta = (x.clone() for x in bt.operands())
+    k[[70, 71]] = (k[70].float() * 2.0**70).to(k.dtype)
+    g[[70, 71]], beta[[70, 71]] = -0.01, 0.5
+    out = torch.empty(bt.rows, bt.hv, bt.dv, device="cuda")
+    want = rule_ref(bt, q, k, v, g, beta, 0.1, [list(range(-1, n - 1)) for n in new])
+    B.iq4xs_delta_rule(q, k, v, g, beta, 0.1, out.flatten(1), bt.state, 0, bt.batch, max_rows=150)
+    assert B.iq4xs_last_device_error() == 0
+    for rows in (slice(0, 64), slice(150, 280)):
+        near(out[rows], want[0][rows], want[1][rows], "out")
+    assert not torch.isfinite(out[71:150]).any()
+    slot = bt.slot_n[1]
+    near(bt.s[0, slot], want[4][slot], want[5][slot], "state")
+    assert not torch.isfinite(bt.s[0, bt.slot_n[0]]).any()
