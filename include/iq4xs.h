@@ -830,7 +830,7 @@ int iq4xs_delta_inputs(const iq4xs_delta_inputs_args* args, const iq4xs_delta_st
  * Rows of no sequence are not written.  NaN, infinities and products beyond
  * fp32's range reach the rows that come from theirs, which may be NaN, and no
  * others.  S, sums and statistics are fp32; where several rows go through the
- * tensor cores, what has more than 16 bits goes in two parts (2^-22 of a value,
+ * tensor cores, what has more than 16 bits goes in two parts (2^-21 of a value,
  * or 2^-38 of the largest of its column or row, whichever is more: a sequence of
  * more than 16 rows goes in blocks of up to 64, whose rows share a column, so that
  * finite values 2^16 and more times another row's cost it bits).  Results are the

@@ -168,13 +168,13 @@ __global__ void __launch_bounds__(kRowThreads, 4) delta_row_kernel(const DeltaRu
 // left operand and lies in the layout that the state's update gives as a result
 // (key channels 2 t and 2 t + 1 of eight stand for the operand's t and t + 4), so
 // it stays where it is.  K and Q of 16 bits are exact in tf32; S and u go in two
-// parts, a value without its last 13 bits and the remainder, of which the MMA takes
-// 11 (22 bits together); sums are joined, and S moved on, by fp32 arithmetic that
-// rounds.  12 trees of 8 are off by 5.5e-7 of the largest output (4.1e-7 of their norm),
-// fp32 throughout by 2.8e-7 (1.7e-7): most of it is the MMA's cut-off sums over 16
-// steps, a quarter the remainder's last bits.  Two sums in turn and a rounded remainder
-// take it to 2.7e-7 (2.0e-7), at 13.9 us instead of 12.3 (48 chains of 16 111 instead
-// of 103), a sum of each step joined by itself to 3.3e-7 (1.9e-7) at 13.7: not taken.
+// parts, a value without its last 13 bits and the remainder, rounded to the 11 bits
+// that the MMA takes of it (2^-22 of a value); the MMA cuts its sums off, so S^T k and
+// S^T q are made of three (the remainders', each half of the channels'), which are
+// joined, and S is moved on, by fp32 arithmetic that rounds.  12 trees of 8 are then off
+// by 2.8e-7 of the largest output and 2.0e-7 of their norm, fp32 throughout by 2.8e-7 and
+// 1.7e-7; with cut remainders and one sum for both halves 5.5e-7 and 4.1e-7 (trees
+// no faster, 48 chains of 16 103 us instead of 107).
 //
 // CTAs stay for several items (a head's columns of a sequence): S comes to shared
 // memory by TMA, goes to registers, and the next item's is on its way meanwhile.
@@ -216,13 +216,12 @@ struct FewItem {
     int row0, n, len, slot, head, v0;  // n = 0: nothing to do
 };
 
-template <int DK, int kWarps, int TB>
+template <int DK, int kWarps, int TB, bool kMoves>
 __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarps)
     delta_few_kernel(const __grid_constant__ CUtensorMap map_s, const __grid_constant__ DeltaRule p,
                      const __grid_constant__ DeltaView d, const __grid_constant__ BatchView b, int items, int* err) {
     using C = FewShape<DK, kWarps, TB>;
     constexpr int kSteps = DK / 8, VS = C::VS, kTiles = C::kTiles;
-    constexpr bool kMoves = TB == 8;  // (blocks of 16 are for trees, whose state stays)
     extern __shared__ __align__(1024) float sm[];
     uint32_t* const seen = reinterpret_cast<uint32_t*>(sm + C::kSeen);
     uint64_t* const landed = reinterpret_cast<uint64_t*>(sm + C::kBar);
@@ -376,25 +375,26 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
             // S^T [K; Q]: columns by rows.  The last warps also [K; Q] K^T: rows by rows,
             // tile y of rows with tile x before or at it.
             {
-                float sk[kTiles][2][4] = {}, sq[kTiles][2][4] = {}, pairs[2][4] = {};
+                float sk[kTiles][3][4] = {}, sq[kTiles][3][4] = {}, pairs[2][4] = {};
                 const int pair = kWarps - 1 - warp;  // tiles (0, 0), (1, 0), (1, 1)
                 const int ty = pair > 0 ? 1 : 0, tx = pair > 1 ? 1 : 0;
                 const bool has_pair = pair < (kTiles == 2 ? 3 : 1);
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
                     uint32_t hi[4], lo[4];
-                    split_tf32(S[i][0], hi[0], lo[0]);
-                    split_tf32(S[i][2], hi[1], lo[1]);
-                    split_tf32(S[i][1], hi[2], lo[2]);
-                    split_tf32(S[i][3], hi[3], lo[3]);
+                    split_tf32_near(S[i][0], hi[0], lo[0]);
+                    split_tf32_near(S[i][2], hi[1], lo[1]);
+                    split_tf32_near(S[i][1], hi[2], lo[2]);
+                    split_tf32_near(S[i][3], hi[3], lo[3]);
+                    const int half = i < kSteps / 2 ? 0 : 2;
 #pragma unroll
                     for (int x = 0; x < kTiles; ++x) {
                         const uint2 k = *reinterpret_cast<const uint2*>(sm + C::kK + (8 * x + g) * C::kPitch + 8 * i + 2 * t4);
                         const uint2 q = *reinterpret_cast<const uint2*>(sm + C::kQ + (8 * x + g) * C::kPitch + 8 * i + 2 * t4);
                         mma_tf32(sk[x][1], lo, k);
                         mma_tf32(sq[x][1], lo, q);
-                        mma_tf32(sk[x][0], hi, k);
-                        mma_tf32(sq[x][0], hi, q);
+                        mma_tf32(sk[x][half], hi, k);
+                        mma_tf32(sq[x][half], hi, q);
                     }
                     if (has_pair) {
                         const uint2 k = *reinterpret_cast<const uint2*>(sm + C::kK + (8 * ty + g) * C::kPitch + 8 * i + 2 * t4);
@@ -408,8 +408,8 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int to = (8 * x + 2 * t4 + (e & 1)) * C::kVPitch + 16 * warp + g + 8 * (e >> 1);
-                        sm[C::kU + to] = sk[x][0][e] + sk[x][1][e];
-                        sm[C::kO + to] = sq[x][0][e] + sq[x][1][e];
+                        sm[C::kU + to] = sk[x][0][e] + (sk[x][1][e] + sk[x][2][e]);
+                        sm[C::kO + to] = sq[x][0][e] + (sq[x][1][e] + sq[x][2][e]);
                     }
                 if (has_pair) {
                     const int t = 8 * ty + g;
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
                 for (int t = 0; t < TB; ++t) {
                     sm[C::kU + t * C::kVPitch + tid] = u[t];
                     float* to = p.u + ((int64_t)(first + t) * d.heads + head) * d.value_dim + v0 + tid;
-                    if (p.u != nullptr && t < m && bc_global(bc, to, 4, p.u, 4 * p.rows * values, kBcDeltaU)) *to = u[t];
+                    if (!kMoves && t < m && bc_global(bc, to, 4, p.u, 4 * p.rows * values, kBcDeltaU)) *to = u[t];
                 }
             }
             __syncthreads();
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
                     }
                 }
             }
-            if (kMoves && p.u == nullptr) {
+            if (kMoves) {
                 // S: columns by key channels, the rows between
                 uint32_t hi[kTiles][4], lo[kTiles][4];
 #pragma unroll
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int t = 8 * x + t4 + 4 * (e >> 1);
-                        split_tf32(sm[C::kGates + 3 * TB + t] * sm[C::kU + t * C::kVPitch + 16 * warp + g + 8 * (e & 1)], hi[x][e], lo[x][e]);
+                        split_tf32_near(sm[C::kGates + 3 * TB + t] * sm[C::kU + t * C::kVPitch + 16 * warp + g + 8 * (e & 1)], hi[x][e], lo[x][e]);
                     }
                 const float decay = sm[C::kGates + 2 * TB + m - 1];
 #pragma unroll
@@ -512,9 +512,9 @@ __global__ void __launch_bounds__(FewShape<DK, kWarps, TB>::kThreads, 16 / kWarp
                     for (int e = 0; e < 4; ++e) S[i][e] = fmaf(decay, S[i][e], add[e]);
                 }
             }
-            if (!kMoves) break;  // (one block: no loop that S's parts could be kept over)
+            if (!kMoves) break;  // (a tree is one block: no loop that S's parts could be kept over)
         }
-        if (kMoves && n > 0 && p.u == nullptr) {
+        if (kMoves && n > 0) {
             float* const at_s = d.s + p.s_offset + slot * d.s_slot_stride + ((int64_t)head * DK + 2 * t4) * d.value_dim + v0 + 16 * warp + g;
 #pragma unroll
             for (int i = 0; i < kSteps; ++i)
@@ -538,7 +538,7 @@ cudaError_t launch_row(const DeltaRule& p, const DeltaView& d, const BatchView& 
     return launch_chained(delta_row_kernel<DK, VS>, grid, dim3(kRowThreads), 0, stream, 1, p, d, b, err);
 }
 
-template <int DK, int kWarps, int TB>
+template <int DK, int kWarps, int TB, bool kMoves>
 cudaError_t launch_few(const DeltaRule& p, const DeltaView& d, const BatchView& b, void* encode, int* err, int num_sms,
                        cudaStream_t stream) {
     using C = FewShape<DK, kWarps, TB>;
@@ -553,10 +553,10 @@ cudaError_t launch_few(const DeltaRule& p, const DeltaView& d, const BatchView& 
                                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    const cudaError_t e = allow_smem<delta_few_kernel<DK, kWarps, TB>>(C::kSmem);
+    const cudaError_t e = allow_smem<delta_few_kernel<DK, kWarps, TB, kMoves>>(C::kSmem);
     if (e != cudaSuccess) return e;
     const int64_t items = (int64_t)b.sequences * d.heads * (d.value_dim / C::VS), most = (int64_t)num_sms * (16 / kWarps);
-    return launch_chained(delta_few_kernel<DK, kWarps, TB>, dim3((unsigned)(items < most ? items : most)), dim3(C::kThreads),
+    return launch_chained(delta_few_kernel<DK, kWarps, TB, kMoves>, dim3((unsigned)(items < most ? items : most)), dim3(C::kThreads),
                           C::kSmem, stream, 1, map, p, d, b, (int)items, err);
 }
 
@@ -572,11 +572,14 @@ cudaError_t launch_keys(const DeltaRule& p, const DeltaView& d, const BatchView&
     }
     // (32 columns a CTA were no faster here, for one sequence either: 6.57 us for
     // 4.95 for a tree of 8.)
+    if (p.u == nullptr)
+        return d.value_dim == 128 ? launch_few<DK, 8, 8, true>(p, d, b, encode, err, num_sms, stream)
+                                  : launch_few<DK, 4, 8, true>(p, d, b, encode, err, num_sms, stream);
     if (block == 8)
-        return d.value_dim == 128 ? launch_few<DK, 8, 8>(p, d, b, encode, err, num_sms, stream)
-                                  : launch_few<DK, 4, 8>(p, d, b, encode, err, num_sms, stream);
-    return d.value_dim == 128 ? launch_few<DK, 8, 16>(p, d, b, encode, err, num_sms, stream)
-                              : launch_few<DK, 4, 16>(p, d, b, encode, err, num_sms, stream);
+        return d.value_dim == 128 ? launch_few<DK, 8, 8, false>(p, d, b, encode, err, num_sms, stream)
+                                  : launch_few<DK, 4, 8, false>(p, d, b, encode, err, num_sms, stream);
+    return d.value_dim == 128 ? launch_few<DK, 8, 16, false>(p, d, b, encode, err, num_sms, stream)
+                              : launch_few<DK, 4, 16, false>(p, d, b, encode, err, num_sms, stream);
 }
 
 }  // namespace
