@@ -18,7 +18,7 @@
 // substitution, what is below them, -T22 A21 T11, by the warp-level MMA on tf32, three
 // terms of two parts (with decays from a scan and rows asked into L2: 231 to 210 us).
 //
-// Measured: 6,147 rows of 3 sequences, 48 heads of 128 x 128: 210 us, floor of the bytes
+// Measured: 6,147 rows of 3 sequences, 48 heads of 128 x 128: 212 us, floor of the bytes
 // 44; 144 CTAs, 33 blocks of 12,300 cycles in a row, the first behind 8 us.  What bounds
 // it is that chain: preparing a block takes 11,300 cycles (copies landing 1,000,
 // conversion 2,900, the pairs' product 1,900, decays 1,600, substitution 1,500, the rest

@@ -53,8 +53,11 @@ __device__ __forceinline__ void tap(Four& y, const Four& w, const Four& x) {
     y.a = fma2(w.a, x.a, y.a);
     y.b = fma2(w.b, x.b, y.b);
 }
-// y / (1 + e^-y): approximations of 2 units in the last place of fp32, behind
-// which a rounding to 16 bits comes.
+// y / (1 + e^-y) by the approximate power and reciprocal.  The exponent is rounded once,
+// and so the result is off by about (8 + 1.2 |y|) 2^-24 of itself for y below 0 (8 2^-24
+// above); below -87.3 the reciprocal is flushed and the result 0 (1e-36 and less).  A
+// rounding to 16 bits comes behind it: fp16 holds nothing of y below -20 (2^-19 there for
+// half a step of 2^-11), bf16 2^-17 at -87 for half a step of 2^-8.
 __device__ __forceinline__ float2 silu(float2 y) {
     const float2 z = fma2(y, make_float2(-1.44269504088896340736f, -1.44269504088896340736f), make_float2(-0.f, -0.f));
     const float2 e = add2(make_float2(fast_exp2(z.x), fast_exp2(z.y)), make_float2(1.f, 1.f));

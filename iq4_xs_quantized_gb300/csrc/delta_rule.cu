@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) delta_row_kernel(const DeltaRu
 // CTAs stay for several items (a head's columns of a sequence): S comes to shared
 // memory by TMA, goes to registers, and the next item's is on its way meanwhile.
 // (CTAs of one item each load together and then compute together: 16.3 us where these
-// took 15.1 for 12 trees of 8 of 48 heads of 128 x 128 with the states in L2; 12.2 now, 15.8 from
-// HBM, 40 MB: 2.5 TB/s; FFMA instead
+// took 15.1 for 12 trees of 8 of 48 heads of 128 x 128 with the states in L2; 11.7 now, 15.0 from
+// HBM, 40 MB: 2.7 TB/s; FFMA instead
 // of the MMA 17.8.)  What bounds it: an item's chain of six steps between barriers,
 // about 2.9 us, two CTAs an SM; S in two parts is a third of its instructions.
 constexpr int kFewPad = 8;  // floats behind a row in shared memory: rows an operand reads together on all banks
@@ -585,15 +585,20 @@ cudaError_t launch_keys(const DeltaRule& p, const DeltaView& d, const BatchView&
 }  // namespace
 
 // The form follows a sequence's rows (times in us, 48 heads of 128 x 128).
-// Row by row up to two on average: 12 chains of 2 13.4 (blocks of 8: 17.5), of 4
-// 19.1 (17.7); 48 of 2 60.5 (66.0), of 4 83.2 (66.7).
-// Blocks of 8 for chains: 48 of 9 98.6 (blocks of 16: 117), of 16 103 (124), of 32
-// 171 (218).  A tree is one block: of 16 from 9 rows on.
-// Blocks of 64 from there where they win.  They take 13.4 for a wave of the SMs
-// whatever the rows: 3 chains of 16 13.6 (blocks of 8: 13.3), of 20 13.6 (16.9), 1 of 20
-// 13.4 (12.5), of 32 13.3 (15.5); in several waves 12 chains of 32 51.7 (42.9), 48
-// of 32 225 (171), each 8 rows more 8 and 34.
+// Row by row up to two on average: 12 chains of 2 13.3 (blocks of 8: 18.1), of 4
+// 18.8 (18.4); 48 of 2 59.8 (69.4), of 4 81.6 (70.4).
+// Blocks of 8 for chains: 48 of 16 107 (blocks of 16, which have no such form any more,
+// 1.2 times as much), of 32 177.  A tree is one block: of 16 from 9 rows on.
+// Blocks of 64 from there where they win.  They take 13.6 for a wave of the SMs
+// whatever the rows: 3 chains of 16 13.7 (blocks of 8: 13.1), of 20 13.6 (16.5), 1 of 20
+// 13.6 (13.0), of 32 13.5 (16.0); in several waves 12 chains of 32 50.8 (44.1), 48
+// of 32 221 (177), each 8 rows more 8 and 34.
 // A batch whose longest sequence is longer, but not the mean, takes both.
+// The same limits for other heads: 48 chains of 16 heads of 128 x 128 of 3 rows 26.7 (row
+// by row 20.8), of 4 26.9 (24.6), of 40 80.2 (blocks of 64: 77.8), of 48 80.3 (blocks of 8:
+// 94.1).  Narrow heads stay in blocks of 8 for too short: 6 of 64 x 64, one chain of 20
+// 10.8 (blocks of 8: 7.1), of 40 10.7 (10.2), 48 of 48 21.2 (16.4), of 64 21.0 (21.1); 16 of
+// 128 x 64, 48 of 48 67.3 (52.4), of 64 67.2 (69.7).
 cudaError_t launch_delta_rule(DeltaRule p, const DeltaView& d, const BatchView& b, void* encode, int* err, int num_sms,
                               cudaStream_t stream) {
     const bool tree = p.u != nullptr;

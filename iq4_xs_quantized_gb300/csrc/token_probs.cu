@@ -2,13 +2,16 @@
 //
 //   p_i = e^((l_i - top) / T) / sum_j e^((l_j - top) / T)
 //
-// or, T not above 0, 1 at the first of the largest logits.  A row is read once,
-// by a cluster of CTAs that keep their parts in registers and exchange maximum
-// and sum through distributed shared memory, and written once: HBM bounds it.
-// 96 rows of 131,073: 23.3 us from HBM, 4.3 TB/s of the 6.8 of a copy (18.0 with the logits in
-// L2): all rows are read, then all are written (CTAs of 256 threads 24.9 to 34.8, of 1,024
-// 30 and more; two and eight units abreast 24.5 and 29.4).  One row of 32,000: 3.7 us, a launch, the
-// loads and the exchange.
+// or, T not above 0, 1 at the first of the largest logits.  A cluster of CTAs shares a
+// row and exchanges maximum and sum through distributed shared memory, in one of
+// two forms.  Where registers hold the rows under way, a row is read once, kept, and
+// written: one row of 32,000 3.8 us, a launch, the loads and the exchange.  Of a
+// batch whose rows they do not hold, each part is read with a running maximum and sum
+// and read again, out of L2, when the row's are known: 96 rows of 131,073 23.7 us from
+// HBM, 4.3 TB/s of the 6.8 of a copy (18.8 with the logits in L2).  All its rows are read
+// before the first is written, which bounds it: HBM is busy for 28 % of the capture's
+// cycles, loads are what warps wait for (CTAs of 256 threads 24.9 to 34.8, of
+// 1,024 30 and more; two and eight units abreast 24.5 and 29.4).
 // Rows start at any multiple of four bytes; a part's units of four values lie on
 // 16-byte boundaries of the logits, cut at the row's ends.
 #include "attention.cuh"

@@ -9,10 +9,12 @@
 // changes them: a draw near the border of two tokens always falls alike.
 //
 // Few bytes are read (a row or two of probabilities a sequence): what it takes
-// is the chain of launch, tree, probabilities, sums, and the draw's search: 12 trees of 8
-// over 131,073 tokens 11.1 us (19 with cold caches), a chain of four with a drafter's
+// is the chain of launch, tree, probabilities, sums, and the draw's search, whose barriers
+// warps wait at (8.0 stalls an issue; for instructions 1.5): 12 trees of 8
+// over 131,073 tokens 11.0 us (17 with cold caches), a chain of four with a drafter's
 // probabilities over 32,000 10.2.  (CTAs of 256, 512 and 1,024 threads: 13.1, 12.3 and 12.4 before the loads
-// were grouped.)
+// were grouped.)  With a drafter's probabilities every rejection sums two rows again: 12
+// chains of 4 over 131,073 16.6 us, 12 trees of 8 34.8, 45 177.8.
 #include <type_traits>
 
 #include "delta.cuh"
